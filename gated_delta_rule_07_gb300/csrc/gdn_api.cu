@@ -583,6 +583,216 @@ gdn_status gdn_backward(const gdn_problem* p, const void* q, const void* k, cons
   return to_status(gdn::backward(a, stream));
 }
 
+// ------------------------------------------------ softmax-attention layers' operators
+
+namespace {
+
+bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
+
+// rows strided in elements: every row starts on a 16-byte boundary
+bool strides_ok(int64_t token, int64_t head, int io) {
+  const int64_t unit = io == GDN_BF16 ? 8 : 4;
+  return token >= 0 && head >= 0 && token % unit == 0 && head % unit == 0;
+}
+
+gdn_status check_rope(const gdn_qk_rope_problem* p) {
+  if (!p) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens < 0 || p->total_tokens > (int64_t)INT32_MAX || p->hq < 1 || p->hkv < 1 ||
+      p->max_positions < 1 || p->rotary_dim < 0 || p->rotary_dim > p->head_dim ||
+      (p->style != 0 && p->style != 1) || !(p->eps >= 0.f))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (!head_dim_ok(p->head_dim) || p->rotary_dim % 16 || p->hq > 65535 || p->hkv > 65535)
+    return GDN_ERR_UNSUPPORTED;
+  if (!strides_ok(p->q_token_stride, p->q_head_stride, p->io_dtype) ||
+      !strides_ok(p->k_token_stride, p->k_head_stride, p->io_dtype))
+    return GDN_ERR_INVALID_ARGUMENT;
+  return GDN_OK;
+}
+
+gdn::QkRopeArgs rope_args(const gdn_qk_rope_problem* p, const void* q, const void* k,
+                          const int32_t* positions, const float* cos_sin, const float* wq,
+                          const float* wk, int32_t* dev_status) {
+  gdn::QkRopeArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = p->total_tokens;
+  a.q_ts = p->q_token_stride; a.q_hs = p->q_head_stride;
+  a.k_ts = p->k_token_stride; a.k_hs = p->k_head_stride;
+  a.hq = p->hq; a.hkv = p->hkv; a.D = p->head_dim; a.R = p->rotary_dim;
+  a.max_pos = p->max_positions;
+  a.bf16 = p->io_dtype == GDN_BF16;
+  a.pairs = p->style == 1;
+  a.eps = p->eps; a.offset = p->weight_offset;
+  a.q = q; a.k = k; a.pos = positions; a.table = cos_sin; a.wq = wq; a.wk = wk;
+  a.status = dev_status;
+  return a;
+}
+
+gdn_status check_kv(const gdn_kv_cache* c, const gdn_kv_problem* p) {
+  if (!c || !p) return GDN_ERR_INVALID_ARGUMENT;
+  if (!c->k_codes || !c->v_codes || !c->k_scale || !c->v_scale || !aligned16(c->k_codes) ||
+      !aligned16(c->v_codes) || c->num_pages < 1 || c->hkv < 1 || p->total_tokens < 0 ||
+      p->total_tokens > (int64_t)INT32_MAX || p->num_seqs < 1 || p->max_pages < 1)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+    return GDN_ERR_UNSUPPORTED;
+  if (c->format != GDN_KV_INT8 && c->format != GDN_KV_E4M3) return GDN_ERR_UNSUPPORTED;
+  if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if (!head_dim_ok(c->head_dim) || c->hkv > 65535) return GDN_ERR_UNSUPPORTED;
+  // positions are 32-bit; slots of touched pages are grid.x
+  if ((int64_t)p->max_pages * c->page_size > (int64_t)INT32_MAX ||
+      p->total_tokens / c->page_size + 2 * (int64_t)p->num_seqs > (int64_t)INT32_MAX)
+    return GDN_ERR_UNSUPPORTED;
+  return GDN_OK;
+}
+
+bool rows_ok(const gdn_kv_problem* p, const int32_t* cu) {
+  return cu != nullptr || p->num_seqs == 1 || p->total_tokens == p->num_seqs;
+}
+
+gdn::KvArgs kv_args(const gdn_kv_cache* c, const gdn_kv_problem* p, const int32_t* table,
+                    const int32_t* pos0, const int32_t* cu, int32_t* dev_status) {
+  gdn::KvArgs a;
+  memset(&a, 0, sizeof(a));
+  a.T = p->total_tokens;
+  a.N = p->num_seqs; a.hq = p->hq; a.hkv = c->hkv; a.D = c->head_dim;
+  a.page = c->page_size; a.num_pages = c->num_pages; a.max_pages = p->max_pages;
+  a.k_ts = p->k_token_stride; a.k_hs = p->k_head_stride;
+  a.v_ts = p->v_token_stride; a.v_hs = p->v_head_stride;
+  a.q_ts = p->q_token_stride; a.q_hs = p->q_head_stride;
+  a.bf16 = p->io_dtype == GDN_BF16;
+  a.e4m3 = c->format == GDN_KV_E4M3;
+  a.table = table; a.pos0 = pos0; a.cu = cu;
+  a.k_codes = static_cast<uint8_t*>(c->k_codes);
+  a.v_codes = static_cast<uint8_t*>(c->v_codes);
+  a.k_scale = c->k_scale; a.v_scale = c->v_scale;
+  a.status = dev_status;
+  return a;
+}
+
+}  // namespace
+
+gdn_status gdn_qk_norm_rope(const gdn_qk_rope_problem* p, const void* q, const void* k,
+                            const int32_t* positions, const float* cos_sin,
+                            const float* q_weight, const float* k_weight, void* q_out,
+                            void* k_out, int32_t* dev_status, cudaStream_t stream) {
+  const gdn_status st = check_rope(p);
+  if (st != GDN_OK) return st;
+  if (p->total_tokens == 0) return GDN_OK;
+  if (!q || !k || !positions || !q_out || !k_out || (!cos_sin && p->rotary_dim))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(cos_sin) || !aligned16(q_weight) || !aligned16(k_weight))
+    return GDN_ERR_INVALID_ARGUMENT;
+  gdn::QkRopeArgs a = rope_args(p, q, k, positions, cos_sin, q_weight, k_weight, dev_status);
+  a.q_out = q_out;
+  a.k_out = k_out;
+  return to_status(gdn::qk_rope(a, false, stream));
+}
+
+size_t gdn_qk_norm_rope_backward_workspace_size(const gdn_qk_rope_problem* p) {
+  return check_rope(p) != GDN_OK ? 0 : (size_t)gdn::kRopeCtas * 2 * p->head_dim * sizeof(float);
+}
+
+gdn_status gdn_qk_norm_rope_backward(const gdn_qk_rope_problem* p, const void* q, const void* k,
+                                     const int32_t* positions, const float* cos_sin,
+                                     const float* q_weight, const float* k_weight,
+                                     const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                     float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  const gdn_status st = check_rope(p);
+  if (st != GDN_OK) return st;
+  if (!dq_weight || !dk_weight) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens == 0) {  // sums over no rows
+    GDN_TRY(cudaMemsetAsync(dq_weight, 0, p->head_dim * sizeof(float), stream));
+    GDN_TRY(cudaMemsetAsync(dk_weight, 0, p->head_dim * sizeof(float), stream));
+    return GDN_OK;
+  }
+  if (!q || !k || !positions || !dq_out || !dk_out || !dq || !dk || (!cos_sin && p->rotary_dim))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(dq_out) || !aligned16(dk_out) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(cos_sin) || !aligned16(q_weight) ||
+      !aligned16(k_weight))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (!workspace || !aligned16(workspace) ||
+      ws_bytes < gdn_qk_norm_rope_backward_workspace_size(p))
+    return GDN_ERR_WORKSPACE;
+  gdn::QkRopeArgs a = rope_args(p, q, k, positions, cos_sin, q_weight, k_weight, dev_status);
+  a.dq_out = dq_out; a.dk_out = dk_out; a.dq = dq; a.dk = dk;
+  a.dwq = dq_weight; a.dwk = dk_weight;
+  a.partial = static_cast<float*>(workspace);
+  return to_status(gdn::qk_rope(a, true, stream));
+}
+
+gdn_status gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_problem* p, const void* k,
+                         const void* v, const int32_t* block_table, const int32_t* ctx_lens,
+                         const int32_t* cu_seqlens, int32_t* dev_status, cudaStream_t stream) {
+  const gdn_status st = check_kv(cache, p);
+  if (st != GDN_OK) return st;
+  if (!strides_ok(p->k_token_stride, p->k_head_stride, p->io_dtype) ||
+      !strides_ok(p->v_token_stride, p->v_head_stride, p->io_dtype) || !rows_ok(p, cu_seqlens))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens == 0) return GDN_OK;
+  if (!k || !v || !block_table || !ctx_lens || !aligned16(k) || !aligned16(v))
+    return GDN_ERR_INVALID_ARGUMENT;
+  gdn::KvArgs a = kv_args(cache, p, block_table, ctx_lens, cu_seqlens, dev_status);
+  a.k = k;
+  a.v = v;
+  return to_status(gdn::kv_append(a, stream));
+}
+
+gdn_status gdn_kv_read(const gdn_kv_cache* cache, const gdn_kv_problem* p,
+                       const int32_t* block_table, const int32_t* start,
+                       const int32_t* cu_seqlens, void* k_out, void* v_out, int32_t* dev_status,
+                       cudaStream_t stream) {
+  const gdn_status st = check_kv(cache, p);
+  if (st != GDN_OK) return st;
+  if (!rows_ok(p, cu_seqlens)) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens == 0) return GDN_OK;
+  if (!block_table || !k_out || !v_out || !aligned16(k_out) || !aligned16(v_out))
+    return GDN_ERR_INVALID_ARGUMENT;
+  gdn::KvArgs a = kv_args(cache, p, block_table, start, cu_seqlens, dev_status);
+  a.k_out = k_out;
+  a.v_out = v_out;
+  return to_status(gdn::kv_read(a, stream));
+}
+
+static gdn_status check_kv_attention(const gdn_kv_cache* cache, const gdn_kv_problem* p) {
+  const gdn_status st = check_kv(cache, p);
+  if (st != GDN_OK) return st;
+  if (p->hq < 1 || p->hq % cache->hkv ||
+      !strides_ok(p->q_token_stride, p->q_head_stride, p->io_dtype))
+    return GDN_ERR_INVALID_ARGUMENT;
+  return p->hq > 65535 ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+size_t gdn_kv_attention_workspace_size(const gdn_kv_cache* cache, const gdn_kv_problem* p) {
+  if (check_kv_attention(cache, p) != GDN_OK) return 0;
+  return gdn::kv_attention_workspace(kv_args(cache, p, nullptr, nullptr, nullptr, nullptr));
+}
+
+gdn_status gdn_kv_attention(const gdn_kv_cache* cache, const gdn_kv_problem* p, const void* q,
+                            const int32_t* block_table, const int32_t* kv_lens,
+                            const int32_t* cu_seqlens, float scale, int32_t window, void* out,
+                            float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                            cudaStream_t stream) {
+  const gdn_status st = check_kv_attention(cache, p);
+  if (st != GDN_OK) return st;
+  if (!rows_ok(p, cu_seqlens) || window < 0) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens == 0) return GDN_OK;
+  if (!q || !block_table || !kv_lens || !out || !aligned16(q) || !aligned16(out))
+    return GDN_ERR_INVALID_ARGUMENT;
+  gdn::KvArgs a = kv_args(cache, p, block_table, kv_lens, cu_seqlens, dev_status);
+  const size_t need = gdn::kv_attention_workspace(a);
+  if (need && (!workspace || !aligned16(workspace) || ws_bytes < need))
+    return GDN_ERR_WORKSPACE;
+  a.q = q; a.out = out; a.lse = lse;
+  a.scale = scale;
+  a.window = window;
+  a.workspace = static_cast<float*>(workspace);
+  return to_status(gdn::kv_attention(a, stream));
+}
+
 gdn_status gdn_device_status(const void* status_word, int reset, cudaStream_t stream) {
   if (!status_word) return GDN_ERR_INVALID_ARGUMENT;
   int32_t host = 0;

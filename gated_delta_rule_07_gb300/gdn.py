@@ -36,7 +36,10 @@ EXPORTED = ("gdn_status_string", "gdn_check_problem", "gdn_workspace_size", "gdn
             "gdn_segment_summary_fused", "gdn_chunk_emit_fused", "gdn_last_error_string",
             "gdn_forward_static_scratch", "gdn_forward_timed", "gdn_forward_with_limits",
             "gdn_check_decode_problem", "gdn_decode_step", "gdn_backward_workspace_size",
-            "gdn_backward", "gdn_prologue")
+            "gdn_backward", "gdn_prologue", "gdn_qk_norm_rope",
+            "gdn_qk_norm_rope_backward_workspace_size", "gdn_qk_norm_rope_backward",
+            "gdn_kv_append", "gdn_kv_read", "gdn_kv_attention_workspace_size",
+            "gdn_kv_attention")
 
 
 class Problem(ctypes.Structure):
@@ -57,6 +60,33 @@ class PrologueProblem(ctypes.Structure):
                 ("hk", ctypes.c_int32), ("hv", ctypes.c_int32), ("k_dim", ctypes.c_int32),
                 ("v_dim", ctypes.c_int32), ("conv_width", ctypes.c_int32),
                 ("activation", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
+
+
+class QkRopeProblem(ctypes.Structure):
+    _fields_ = [("total_tokens", ctypes.c_int64), ("hq", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("style", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("max_positions", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64)]
+
+
+class KvCacheDesc(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("hkv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
+
+
+class KvProblem(ctypes.Structure):
+    _fields_ = [("total_tokens", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("hq", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64)]
 
 
 class GdnError(RuntimeError):
@@ -101,9 +131,23 @@ _lib.gdn_prologue.argtypes = [ctypes.POINTER(PrologueProblem), _vp, _fp, _vp, _v
 _dpp = ctypes.POINTER(DecodeProblem)
 _lib.gdn_check_decode_problem.argtypes = [_dpp]
 _lib.gdn_decode_step.argtypes = [_dpp, _vp, _vp, _vp, _fp, _fp, _ip, _fp, _vp, _ip, _vp]
+_rp = ctypes.POINTER(QkRopeProblem)
+_lib.gdn_qk_norm_rope.argtypes = [_rp, _vp, _vp, _ip, _fp, _fp, _fp, _vp, _vp, _ip, _vp]
+_lib.gdn_qk_norm_rope_backward_workspace_size.restype = ctypes.c_size_t
+_lib.gdn_qk_norm_rope_backward_workspace_size.argtypes = [_rp]
+_lib.gdn_qk_norm_rope_backward.argtypes = [_rp, _vp, _vp, _ip, _fp, _fp, _fp, _vp, _vp, _vp, _vp,
+                                           _fp, _fp, _vp, ctypes.c_size_t, _ip, _vp]
+_cp, _kp = ctypes.POINTER(KvCacheDesc), ctypes.POINTER(KvProblem)
+_lib.gdn_kv_append.argtypes = [_cp, _kp, _vp, _vp, _ip, _ip, _ip, _ip, _vp]
+_lib.gdn_kv_read.argtypes = [_cp, _kp, _ip, _ip, _ip, _vp, _vp, _ip, _vp]
+_lib.gdn_kv_attention_workspace_size.restype = ctypes.c_size_t
+_lib.gdn_kv_attention_workspace_size.argtypes = [_cp, _kp]
+_lib.gdn_kv_attention.argtypes = [_cp, _kp, _vp, _ip, _ip, _ip, ctypes.c_float, ctypes.c_int32,
+                                  _vp, _fp, _vp, ctypes.c_size_t, _ip, _vp]
 for _n in EXPORTED:
     if _n not in ("gdn_status_string", "gdn_workspace_size", "gdn_last_error_string",
-                  "gdn_backward_workspace_size"):
+                  "gdn_backward_workspace_size", "gdn_qk_norm_rope_backward_workspace_size",
+                  "gdn_kv_attention_workspace_size"):
         getattr(_lib, _n).restype = ctypes.c_int
 
 
@@ -339,6 +383,300 @@ def decode(q, k, v, g, beta, slot, state, out=None, check_status=False, stream=N
 def gdn_device_status(status_word, reset=True, stream=None) -> int:
     """Synchronous read of a device status word (a dev_status tensor or a workspace)."""
     return _lib.gdn_device_status(_ptr(status_word), int(bool(reset)), _stream(stream))
+
+
+# ------------------------------------------------- softmax-attention layers' operators
+
+_IO = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+_KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_ROPE_STYLES = {"half": 0, "pairs": 1}
+_GDN_ERR_INVALID_ARGUMENT, _GDN_ERR_UNSUPPORTED = 1, 2
+
+
+def _refuse(where, why, status=_GDN_ERR_INVALID_ARGUMENT):
+    raise GdnError(status, f"{where}: {why}")
+
+
+def _io_of(where, *tensors):
+    dtype = tensors[0].dtype
+    io = _IO.get(dtype)
+    if io is None:
+        _refuse(where, f"dtype {dtype}", _GDN_ERR_UNSUPPORTED)
+    for t in tensors:
+        if t.dtype is not dtype:
+            _refuse(where, f"dtypes {dtype} and {t.dtype} in one call")
+    return io
+
+
+def _packed(where, shape, dtype, **tensors):
+    """Contiguous tensors of one shape and dtype."""
+    for name, t in tensors.items():
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+            _refuse(where, f"{name} is to be a contiguous {dtype} tensor {tuple(shape)}, got "
+                           f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _rows(where, name, t):
+    """Token and head stride of a [T, heads, D] tensor whose last dimension is contiguous."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        _refuse(where, f"{name} is to be [tokens, heads, D] with a contiguous last dimension")
+    return t.stride(0), t.stride(1)
+
+
+def _on_gpu(where, *tensors):
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            _refuse(where, "a tensor is not on the GPU")
+
+
+def _hold(stream, *tensors):
+    """Temporaries and outputs allocated on the current stream and used on `stream`: their memory
+    is not handed out again before the work on `stream` is done."""
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _status_word(check_status, device):
+    return torch.zeros(1, dtype=torch.int32, device=device) if check_status else None
+
+
+def _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, style):
+    io = _io_of(where, q, k)
+    qs, ks = _rows(where, "q", q), _rows(where, "k", k)
+    T, hq, D = q.shape
+    if k.shape[0] != T or k.shape[2] != D:
+        _refuse(where, f"q {tuple(q.shape)} and k {tuple(k.shape)} do not go together")
+    _packed(where, (T,), torch.int32, positions=positions)
+    if cos_sin.dim() != 2:
+        _refuse(where, "cos_sin is to be [positions, R]")
+    _packed(where, cos_sin.shape, torch.float32, cos_sin=cos_sin)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _packed(where, (D,), torch.float32, **{name: w})
+    if style not in _ROPE_STYLES:
+        _refuse(where, f"style {style!r}")
+    _on_gpu(where, q, k, positions, cos_sin, q_weight, k_weight)
+    return QkRopeProblem(T, hq, k.shape[1], D, cos_sin.shape[1], _ROPE_STYLES[style], io,
+                         cos_sin.shape[0], eps, weight_offset, *qs, *ks)
+
+
+def gdn_qk_norm_rope(p, q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out,
+                     dev_status=None, stream=None):
+    _check(_lib.gdn_qk_norm_rope(p, _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin),
+                                 _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out),
+                                 _ptr(dev_status), _stream(stream)), "gdn_qk_norm_rope")
+
+
+def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6,
+                 weight_offset=0.0, style="half", check_status=False, stream=None):
+    """Queries [T, hq, D] and keys [T, hkv, D], normalised per head and rotated by position (see
+    include/gdn.h); q and k may be slices of one projection.  Returns contiguous tensors."""
+    where = "qk_norm_rope"
+    p = _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset,
+                      style)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    st = _status_word(check_status, q.device)
+    _hold(stream, q_out, k_out, st)
+    gdn_qk_norm_rope(p, q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out, st, stream)
+    if check_status:
+        _check(gdn_device_status(st, True, stream), "qk_norm_rope (device status)")
+    return q_out, k_out
+
+
+def gdn_qk_norm_rope_backward_workspace_size(p) -> int:
+    return int(_lib.gdn_qk_norm_rope_backward_workspace_size(p))
+
+
+def gdn_qk_norm_rope_backward(p, q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
+                              dq, dk, dq_weight, dk_weight, workspace, ws_bytes=None,
+                              dev_status=None, stream=None):
+    ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.gdn_qk_norm_rope_backward(
+        p, _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin), _ptr(q_weight), _ptr(k_weight),
+        _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight),
+        _ptr(workspace), int(ws_bytes), _ptr(dev_status), _stream(stream)),
+        "gdn_qk_norm_rope_backward")
+
+
+def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out, eps=1e-6,
+                          weight_offset=0.0, style="half", workspace=None, check_status=False,
+                          stream=None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of <dq_out, q_out> + <dk_out, k_out> through
+    qk_norm_rope on the same inputs."""
+    where = "qk_norm_rope_backward"
+    p = _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset,
+                      style)
+    _packed(where, q.shape, q.dtype, dq_out=dq_out)
+    _packed(where, k.shape, k.dtype, dk_out=dk_out)
+    _on_gpu(where, dq_out, dk_out)
+    dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
+    dw = torch.empty(2, q.shape[2], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(max(gdn_qk_norm_rope_backward_workspace_size(p), 256),
+                                dtype=torch.uint8, device=q.device)
+    st = _status_word(check_status, q.device)
+    _hold(stream, dq, dk, dw, workspace, st)
+    gdn_qk_norm_rope_backward(p, q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
+                              dq, dk, dw[0], dw[1], workspace, None, st, stream)
+    if check_status:
+        _check(gdn_device_status(st, True, stream), "qk_norm_rope_backward (device status)")
+    return dq, dk, dw[0], dw[1]
+
+
+class KVCache:
+    """The buffers of a paged 8-bit key/value cache (layouts of include/gdn.h):
+    k [pages, hkv, page, D] and v [pages, hkv, page // 4, D, 4], both int8 or float8_e4m3fn;
+    k_scale, v_scale [pages, hkv] fp32.  ``KVCache.empty`` allocates them."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        where = "KVCache"
+        if k.dtype not in _KV_FORMATS:
+            _refuse(where, f"dtype {k.dtype}", _GDN_ERR_UNSUPPORTED)
+        if k.dim() != 4:
+            _refuse(where, "k is to be [pages, hkv, page, D]")
+        pages, hkv, page, D = k.shape
+        _packed(where, k.shape, k.dtype, k=k)
+        _packed(where, (pages, hkv, page // 4, D, 4), k.dtype, v=v)
+        _packed(where, (pages, hkv), torch.float32, k_scale=k_scale, v_scale=v_scale)
+        _on_gpu(where, k, v, k_scale, v_scale)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), pages, page, hkv, D, _KV_FORMATS[k.dtype])
+
+    @classmethod
+    def empty(cls, pages, hkv, page, D, dtype=torch.int8, device="cuda"):
+        """A cache of `pages` pages; nothing in it is initialised, or needs to be."""
+        return cls(torch.empty(pages, hkv, page, D, dtype=dtype, device=device),
+                   torch.empty(pages, hkv, page // 4, D, 4, dtype=dtype, device=device),
+                   torch.empty(pages, hkv, dtype=torch.float32, device=device),
+                   torch.empty(pages, hkv, dtype=torch.float32, device=device))
+
+
+def _kv_sequences(where, cache, T, block_table, lens, cu_seqlens):
+    """Checks the tables of a cache call; the number of sequences and pages a table row."""
+    if block_table.dim() != 2:
+        _refuse(where, "block_table is to be [sequences, pages]")
+    N, max_pages = block_table.shape
+    _packed(where, block_table.shape, torch.int32, block_table=block_table)
+    if lens is not None:
+        _packed(where, (N,), torch.int32, lengths=lens)
+    if cu_seqlens is not None:
+        _packed(where, (N + 1,), torch.int32, cu_seqlens=cu_seqlens)
+    elif N != 1 and N != T:
+        _refuse(where, f"{T} rows of {N} sequences need cu_seqlens")
+    _on_gpu(where, block_table, lens, cu_seqlens)
+    return N, max_pages
+
+
+def _kv_heads(where, cache, **tensors):
+    d = cache.desc
+    for name, t in tensors.items():
+        if t.shape[1] != d.hkv or t.shape[2] != d.head_dim:
+            _refuse(where, f"{name} {tuple(t.shape)} for a cache of {d.hkv} heads of "
+                           f"{d.head_dim}")
+
+
+def gdn_kv_append(cache, p, k, v, block_table, ctx_lens, cu_seqlens, dev_status=None,
+                  stream=None):
+    _check(_lib.gdn_kv_append(cache, p, _ptr(k), _ptr(v), _ptr(block_table), _ptr(ctx_lens),
+                              _ptr(cu_seqlens), _ptr(dev_status), _stream(stream)),
+           "gdn_kv_append")
+
+
+def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=False,
+              stream=None):
+    """Quantises new keys and values [T, hkv, D] into the cache's pages, behind the ctx_lens[n]
+    tokens that each sequence already holds.  Without cu_seqlens the rows are one sequence's, or
+    one row each of T sequences."""
+    where = "kv_append"
+    io = _io_of(where, k, v)
+    ks, vs = _rows(where, "k", k), _rows(where, "v", v)
+    if v.shape[0] != k.shape[0]:
+        _refuse(where, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not go together")
+    _kv_heads(where, cache, k=k, v=v)
+    _on_gpu(where, k, v)
+    N, max_pages = _kv_sequences(where, cache, k.shape[0], block_table, ctx_lens, cu_seqlens)
+    p = KvProblem(k.shape[0], N, max_pages, 0, io, *ks, *vs, 0, 0)
+    st = _status_word(check_status, k.device)
+    _hold(stream, st)
+    gdn_kv_append(cache.desc, p, k, v, block_table, ctx_lens, cu_seqlens, st, stream)
+    if check_status:
+        _check(gdn_device_status(st, True, stream), "kv_append (device status)")
+
+
+def gdn_kv_read(cache, p, block_table, start, cu_seqlens, k_out, v_out, dev_status=None,
+                stream=None):
+    _check(_lib.gdn_kv_read(cache, p, _ptr(block_table), _ptr(start), _ptr(cu_seqlens),
+                            _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream)),
+           "gdn_kv_read")
+
+
+def kv_read(cache, block_table, start, cu_seqlens, tokens, dtype=torch.bfloat16,
+            check_status=False, stream=None):
+    """Keys and values [tokens, hkv, D] of the positions start[n] onward (None: from 0) of each
+    sequence, cu_seqlens[n + 1] - cu_seqlens[n] of them, read back from the cache."""
+    where = "kv_read"
+    if dtype not in _IO:
+        _refuse(where, f"dtype {dtype}", _GDN_ERR_UNSUPPORTED)
+    N, max_pages = _kv_sequences(where, cache, tokens, block_table, start, cu_seqlens)
+    d = cache.desc
+    shape = (tokens, d.hkv, d.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=block_table.device)
+    v = torch.empty(shape, dtype=dtype, device=block_table.device)
+    p = KvProblem(tokens, N, max_pages, 0, _IO[dtype], 0, 0, 0, 0, 0, 0)
+    st = _status_word(check_status, block_table.device)
+    _hold(stream, k, v, st)
+    gdn_kv_read(d, p, block_table, start, cu_seqlens, k, v, st, stream)
+    if check_status:
+        _check(gdn_device_status(st, True, stream), "kv_read (device status)")
+    return k, v
+
+
+def gdn_kv_attention_workspace_size(cache, p) -> int:
+    return int(_lib.gdn_kv_attention_workspace_size(cache, p))
+
+
+def gdn_kv_attention(cache, p, q, block_table, kv_lens, cu_seqlens, scale, window, out, lse,
+                     workspace, ws_bytes=None, dev_status=None, stream=None):
+    if ws_bytes is None:
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(_lib.gdn_kv_attention(cache, p, _ptr(q), _ptr(block_table), _ptr(kv_lens),
+                                 _ptr(cu_seqlens), scale, window, _ptr(out), _ptr(lse),
+                                 _ptr(workspace), int(ws_bytes), _ptr(dev_status),
+                                 _stream(stream)), "gdn_kv_attention")
+
+
+def kv_attention(cache, q, block_table, kv_lens, cu_seqlens=None, scale=None, window=0,
+                 workspace=None, check_status=False, stream=None):
+    """out [T, hq, D] and lse [T, hq] of the queries of each sequence's last tokens over the
+    cache's kv_lens[n] tokens (which include them); scale defaults to 1 / sqrt(D).  Without
+    cu_seqlens the rows are one sequence's, or one row each of T sequences."""
+    where = "kv_attention"
+    io = _io_of(where, q)
+    qs = _rows(where, "q", q)
+    T, hq, D = q.shape
+    if D != cache.desc.head_dim:
+        _refuse(where, f"q {tuple(q.shape)} for a cache of heads of {cache.desc.head_dim}")
+    _on_gpu(where, q)
+    N, max_pages = _kv_sequences(where, cache, T, block_table, kv_lens, cu_seqlens)
+    p = KvProblem(T, N, max_pages, hq, io, 0, 0, 0, 0, *qs)
+    out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        need = gdn_kv_attention_workspace_size(cache.desc, p)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    st = _status_word(check_status, q.device)
+    _hold(stream, out, lse, workspace, st)
+    gdn_kv_attention(cache.desc, p, q, block_table, kv_lens, cu_seqlens,
+                     D ** -0.5 if scale is None else scale, window, out, lse, workspace, None,
+                     st, stream)
+    if check_status:
+        _check(gdn_device_status(st, True, stream), "kv_attention (device status)")
+    return out, lse
 
 
 # ------------------------------------------------------------------ convenience API

@@ -345,6 +345,135 @@ gdn_status gdn_decode_step(const gdn_decode_problem* p, const void* q, const voi
                            const int32_t* slot, float* state, void* out, int32_t* dev_status,
                            cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------- */
+/* Softmax-attention layers beside the recurrent ones: query/key norms with the position       */
+/* rotation, a paged 8-bit key/value cache, and attention over it.                             */
+
+typedef struct gdn_qk_rope_problem {
+    int64_t total_tokens;     /* T >= 0                                                     */
+    int32_t hq, hkv;          /* query heads, key heads (>= 1, independent of each other)   */
+    int32_t head_dim;         /* D in {64, 128, 256}                                        */
+    int32_t rotary_dim;       /* R in {0, 16, 32, ... D}: the first R dimensions are turned */
+    int32_t style;            /* pairs: 0 (i, i + R/2), 1 (2i, 2i + 1)                      */
+    int32_t io_dtype;         /* gdn_dtype of q, k and their gradients                      */
+    int32_t max_positions;    /* rows of the table                                          */
+    float eps;                /* added to the mean square                                   */
+    float weight_offset;      /* added to both weights (1 for weights stored around zero)   */
+    int64_t q_token_stride, q_head_stride;  /* elements; multiples of 16 bytes; the last      */
+    int64_t k_token_stride, k_head_stride;  /* dimension is contiguous                        */
+} gdn_qk_rope_problem;
+
+/* Queries and keys normalised per head and rotated by position, in one pass.  Per row x (one
+ * head of one token), r = 1 / sqrt(mean(x^2) + eps):
+ *     y = x r (weight + weight_offset);
+ *     then each pair (a, b) of the first R dimensions becomes (a c - b s, b c + a s), with
+ *     c = cos_sin[pos][i], s = cos_sin[pos][R/2 + i] of pair i.
+ *   q [T, hq, D], k [T, hkv, D] io dtype, strided as the problem says (slices of one projection);
+ *   positions int32 [T], checked on the device (a token outside [0, max_positions) is left
+ *   unwritten and GDN_ERR_DEVICE_INPUT recorded in dev_status);  cos_sin [max_positions, R] fp32
+ *   (may be NULL when R = 0);  q_weight, k_weight [D] fp32, or NULL for 1 (without the offset);
+ *   q_out [T, hq, D], k_out [T, hkv, D] io dtype, contiguous, not overlapping the inputs.
+ * All pointers 16-byte aligned (positions 4-byte).  Statistics fp32, one rounding at the end. */
+gdn_status gdn_qk_norm_rope(const gdn_qk_rope_problem* p, const void* q, const void* k,
+                            const int32_t* positions, const float* cos_sin,
+                            const float* q_weight, const float* k_weight, void* q_out,
+                            void* k_out, int32_t* dev_status, cudaStream_t stream);
+
+/* Bytes of device workspace gdn_qk_norm_rope_backward needs (0 when p is invalid). */
+size_t gdn_qk_norm_rope_backward_workspace_size(const gdn_qk_rope_problem* p);
+
+/* Gradients of <dq_out, q_out> + <dk_out, k_out> with respect to q, k and both weights.
+ *   dq_out, dk_out  [T, hq | hkv, D] io dtype, contiguous
+ *   dq, dk          [T, hq | hkv, D] io dtype, contiguous
+ *   dq_weight, dk_weight  [D] fp32: sums over all tokens and heads, in a fixed order
+ *   workspace       16-byte aligned, need not be initialised
+ * A token whose position is out of range is skipped as in the forward. */
+gdn_status gdn_qk_norm_rope_backward(const gdn_qk_rope_problem* p, const void* q, const void* k,
+                                     const int32_t* positions, const float* cos_sin,
+                                     const float* q_weight, const float* k_weight,
+                                     const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                     float* dq_weight, float* dk_weight, void* workspace,
+                                     size_t ws_bytes, int32_t* dev_status, cudaStream_t stream);
+
+typedef enum gdn_kv_format { GDN_KV_INT8 = 0, GDN_KV_E4M3 = 1 } gdn_kv_format;
+
+/* A paged cache held in 8 bits.  A page holds page_size tokens of every kv head, and has one
+ * scale for the keys and one for the values of each head; value = code * scale.  Layouts:
+ *   k_codes [num_pages, hkv, page_size, D]            one byte each: int8, or e4m3 bits
+ *   v_codes [num_pages, hkv, page_size / 4, D, 4]     (token t of a page: [t / 4][d][t % 4])
+ *   k_scale, v_scale [num_pages, hkv] fp32
+ * Codes pointers 16-byte aligned.  No buffer needs initialising. */
+typedef struct gdn_kv_cache {
+    void* k_codes;
+    void* v_codes;
+    float* k_scale;
+    float* v_scale;
+    int32_t num_pages;        /* >= 1                                                       */
+    int32_t page_size;        /* 16, 32, 64 or 128 tokens                                   */
+    int32_t hkv;              /* kv heads                                                   */
+    int32_t head_dim;         /* D in {64, 128, 256}                                        */
+    int32_t format;           /* gdn_kv_format                                              */
+} gdn_kv_cache;
+
+typedef struct gdn_kv_problem {
+    int64_t total_tokens;     /* T >= 0: packed rows of the call                            */
+    int32_t num_seqs;         /* N >= 1                                                     */
+    int32_t max_pages;        /* entries of a block-table row (>= 1)                        */
+    int32_t hq;               /* query heads (attention only; a multiple of hkv)            */
+    int32_t io_dtype;         /* gdn_dtype of k, v, q and the outputs                       */
+    int64_t k_token_stride, k_head_stride;  /* elements, multiples of 16 bytes (append)     */
+    int64_t v_token_stride, v_head_stride;
+    int64_t q_token_stride, q_head_stride;  /* (attention)                                  */
+} gdn_kv_problem;
+
+/* CONVENTIONS of the three cache calls.  block_table int32 [N, max_pages]: the pages of each
+ * sequence in order; entries past a sequence's length are not read.  cu_seqlens int32 [N+1]: the
+ * packed rows of each sequence (any may be empty), or NULL for one sequence of T rows or, when
+ * T == N, one row each.  Lengths, tables and page ids are checked on the device: a sequence whose
+ * rows or length do not fit, or a page outside the pool, is skipped (left unwritten; such a page's
+ * keys are left out of the attention) and GDN_ERR_DEVICE_INPUT is recorded in dev_status (device
+ * int32, or NULL).  A page that a call writes must belong to one sequence of the call; pages that
+ * are only read may be shared. */
+
+/* Quantises new keys and values into the cache: row i of sequence n becomes the token at position
+ * ctx_lens[n] + i.  For the new tokens of each (page, head), with qmax = 127 (int8) or 448 (e4m3),
+ *     s = max(amax * (1 / qmax), the page's scale if it holds earlier tokens of the sequence),
+ *     code = round_to_nearest_even(x * (1 / s)), within +-qmax,
+ * and where s grew, the page's earlier codes c become round(c * (s_old * (1 / s))).  All of it in
+ * fp32.  A page without earlier tokens ignores the scale it had.  A page whose amax is below 2^-100
+ * is stored as zeros with scale 0.  Values that are not finite are kept out of amax, stored as the
+ * largest code of their sign (a NaN as 0), and recorded as GDN_ERR_DEVICE_RANGE.  Codes depend on
+ * how a sequence was cut into calls (by the scale's growth), not on anything else.
+ *   k, v [T, hkv, D] io dtype, strided;  ctx_lens int32 [N]: tokens already held.
+ * The caller advances its lengths. */
+gdn_status gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_problem* p, const void* k,
+                         const void* v, const int32_t* block_table, const int32_t* ctx_lens,
+                         const int32_t* cu_seqlens, int32_t* dev_status, cudaStream_t stream);
+
+/* Reads tokens back as values: row i of sequence n is the token at position start[n] + i (start
+ * NULL: from 0).  k_out, v_out [T, hkv, D] io dtype, contiguous. */
+gdn_status gdn_kv_read(const gdn_kv_cache* cache, const gdn_kv_problem* p,
+                       const int32_t* block_table, const int32_t* start,
+                       const int32_t* cu_seqlens, void* k_out, void* v_out, int32_t* dev_status,
+                       cudaStream_t stream);
+
+/* Bytes of device workspace gdn_kv_attention needs (0 when the arguments are invalid, or when it
+ * needs none). */
+size_t gdn_kv_attention_workspace_size(const gdn_kv_cache* cache, const gdn_kv_problem* p);
+
+/* Softmax attention of new tokens over the cache: row i of sequence n (of q_n rows) is the token
+ * at position p = kv_lens[n] - q_n + i, whose keys are already in the cache; it sees the keys j
+ * with j <= p, and j > p - window where window > 0.  Query head h reads kv head h / (hq / hkv).
+ *     out = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
+ *   q [T, hq, D] io dtype, strided;  kv_lens int32 [N];  out [T, hq, D] io dtype, contiguous;
+ *   lse [T, hq] fp32, or NULL.  A row without keys (kv_lens 0, or p < 0) gets out = 0, lse = -inf.
+ * Made for one or a few rows per sequence (decode, drafted tokens); any number is computed.  */
+gdn_status gdn_kv_attention(const gdn_kv_cache* cache, const gdn_kv_problem* p, const void* q,
+                            const int32_t* block_table, const int32_t* kv_lens,
+                            const int32_t* cu_seqlens, float scale, int32_t window, void* out,
+                            float* lse, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                            cudaStream_t stream);
+
 /* Text of the last CUDA error that made an entry point return GDN_ERR_CUDA on the calling
  * host thread ("no CUDA error" when there was none).  Static storage. */
 const char* gdn_last_error_string(void);

@@ -1,0 +1,312 @@
+"""GPU: attention over the 8-bit paged cache (gdn_kv_attention) against fp64.
+
+Tolerances, from the arithmetic.  A score is a sum of D exact products accumulated in fp32 (a
+product of the inputs and the code is exact in the operands used; fp32 inputs are split in two):
+rounding errors of at most 2^-23 of the running sum add up like a walk, sqrt(D) 2^-23 sum |q k|
+scale, below 2^-14 for the inputs here (D <= 256, sum |q k| scale < 20).  A weight's relative error
+is that of exp: the score's error plus 2^-21.  bf16: weights are rounded to fp16 (2^-11 each), so
+out is off by at most (2^-11 + 2^-14 + ..) sum p |v| and half an ulp of 8 significant bits,
+2^-8 |out|: the bound is 2^-10 sum p |v| + 2^-8 |out|.  fp32: 2^-13 sum p |v| (twice the score's bound).  lse: the score's
+bound, 2^-13 with the sum's and log's.
+"""
+import math
+
+import pytest
+import torch
+
+import attention_testutil as at
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    from gated_delta_rule_07_gb300 import build
+    build.build()
+    from gated_delta_rule_07_gb300 import gdn as mod
+    assert torch.cuda.is_available()
+    return mod
+
+
+def check(out, lse, ref, io, what=""):
+    o, l, mag = ref
+    out, lse = out.double().cpu(), lse.double().cpu()
+    if io == torch.bfloat16:
+        tol = 2.0 ** -10 * mag + 2.0 ** -8 * o.abs()
+    else:
+        tol = 2.0 ** -13 * mag
+    err = (out - o).abs()
+    assert not torch.isnan(out).any(), what
+    assert bool((err <= tol).all()), (what, float((err - tol).max()), int((err > tol).sum()))
+    empty = torch.isinf(l)
+    assert torch.equal(torch.isinf(lse), empty) and bool((lse[empty] < 0).all()), what
+    assert bool(((lse - l).abs()[~empty] <= 2.0 ** -13 * l.abs().clamp(min=1)[~empty]).all()), what
+
+
+class Problem:
+    def __init__(self, gdn, lens, new, hq, hkv, D, page, fmt, io, seed=0, std_q=1.2, junk=-1):
+        gen = torch.Generator().manual_seed(seed)
+        self.lens, self.new, self.page, self.io = lens, new, page, io
+        self.tables, pages = at.block_tables(lens, page, gen, junk=junk)
+        self.kc, self.ks = at.random_cache(pages, hkv, page, D, fmt, gen)
+        self.vc, self.vs = at.random_cache(pages, hkv, page, D, fmt, gen, 0.4)
+        self.q = (std_q * torch.randn(sum(new), hq, D, generator=gen)).to(io)
+        self.gdn, self.D = gdn, D
+        self.load()
+
+    def load(self):
+        self.cache = self.gdn.KVCache(self.kc.cuda(), at.packed_v(self.vc).cuda(), self.ks.cuda(),
+                                      self.vs.cuda())
+
+    def run(self, window=0, cu="packed", q=None, **kw):
+        cu = at.cumulative(self.new).cuda() if cu == "packed" else cu
+        kw.setdefault("check_status", True)
+        return self.gdn.kv_attention(self.cache, self.q.cuda() if q is None else q,
+                                     self.tables.cuda(),
+                                     torch.tensor(self.lens, dtype=torch.int32).cuda(), cu,
+                                     window=window, **kw)
+
+    def ref(self, window=0, scale=None):
+        return at.attention_ref(self.q, self.kc, self.ks, self.vc, self.vs, self.tables,
+                                self.lens, self.new, self.page,
+                                self.D ** -0.5 if scale is None else scale, window)
+
+
+def edge_lengths(page):
+    return [0, 1, 2, 15, 16, 17, page - 1, page, page + 1, 3 * page + 5, 31, 33, 64, 65, 777]
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("hq,hkv,D,page", [(8, 1, 128, 64), (3, 3, 64, 16), (16, 2, 256, 64),
+                                           (12, 1, 128, 32), (16, 1, 64, 128), (14, 2, 256, 16),
+                                           (20, 1, 128, 16), (40, 1, 256, 32), (10, 2, 64, 32)])
+def test_one_query_per_sequence(gdn, hq, hkv, D, page, fmt, io):
+    lens = edge_lengths(page)
+    p = Problem(gdn, lens, [1] * len(lens), hq, hkv, D, page, fmt, io, seed=hq + D)
+    check(*p.run(), p.ref(), io)
+    check(*p.run(cu=None), p.ref(), io)
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("window", [0, 1, 7, 100])
+@pytest.mark.parametrize("hq,hkv,D,page", [(8, 2, 128, 64), (7, 1, 64, 16), (4, 4, 256, 32)])
+def test_several_queries_and_windows(gdn, hq, hkv, D, page, window, fmt, io):
+    """Drafted tokens: each row has its own last key; rows before the first key (more rows than
+    tokens) are empty; sequences without rows take no part."""
+    lens = [0, 1, 3, 40, 129, 300, 64, 16, 500]
+    new = [2, 3, 3, 5, 1, 9, 0, 16, 33]
+    p = Problem(gdn, lens, new, hq, hkv, D, page, fmt, io, seed=window + D)
+    check(*p.run(window), p.ref(window), io)
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+def test_long_sequences_are_split_and_joined(gdn, io):
+    """One long sequence among short ones: work split over its length and joined."""
+    lens, new = [20011, 5, 3000, 1], [1, 1, 2, 1]
+    for hq, hkv, D, page, fmt in ((8, 1, 128, 64, torch.int8), (4, 2, 64, 16, at.FORMATS[1]),
+                                  (16, 2, 256, 128, torch.int8)):
+        p = Problem(gdn, lens, new, hq, hkv, D, page, fmt, io, seed=D)
+        check(*p.run(), p.ref(), io, (hq, D))
+
+
+def test_many_sequences(gdn):
+    gen = torch.Generator().manual_seed(1)
+    lens = [int(x) for x in torch.randint(0, 90, (700,), generator=gen)]
+    new = [int(x) for x in torch.randint(0, 3, (700,), generator=gen)]
+    lens = [max(a, b) if a else 0 for a, b in zip(lens, new)]
+    p = Problem(gdn, lens, new, 4, 2, 64, 16, torch.int8, torch.bfloat16)
+    check(*p.run(), p.ref(), torch.bfloat16)
+
+
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+def test_bytes_past_the_length_do_not_count(gdn, fmt):
+    """Unused slots of a last page hold every byte there is (e4m3's NaN codes too), unused table
+    entries any number, unused pages' scales NaN: the result does not change by a bit."""
+    lens, new, page = [1, 18, 45, 64, 0], [1, 1, 3, 1, 1], 32
+    p = Problem(gdn, lens, new, 6, 2, 128, page, fmt, torch.bfloat16, seed=4)
+    want = p.run()
+    check(*want, p.ref(), torch.bfloat16)
+    used = set()
+    for n, L in enumerate(lens):
+        for i in range(-(-L // page)):
+            pid = int(p.tables[n, i])
+            used.add(pid)
+            t = min(page, L - i * page)
+            for codes in (p.kc, p.vc):
+                raw = codes.view(torch.uint8)
+                fill = torch.tensor([0x7f, 0xff, 0x80, 0x7e], dtype=torch.uint8).repeat(32)
+                raw[pid, :, t:] = fill[:128]
+    for pid in range(p.ks.shape[0]):
+        if pid not in used:
+            p.ks[pid] = float("nan")
+            p.vs[pid] = float("inf")
+    for junk in (-1, 10 ** 9, -2 ** 31):
+        for n, L in enumerate(lens):
+            p.tables[n, -(-L // page):] = junk
+        p.load()
+        got = p.run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_scales_of_very_different_pages(gdn):
+    """Pages whose value scales differ by up to 2^80 and key scales by 2^6, a page of zeros among
+    them, with the weight on the page of small values: the sum keeps its relative accuracy."""
+    for fmt in at.FORMATS:
+        for io in at.IOS:
+            p = Problem(gdn, [16 * 6], [1], 2, 1, 128, 16, fmt, io, seed=8, std_q=0.3)
+            ids = p.tables[0].long()
+            p.vs[ids, 0] *= torch.tensor([1.0, 2.0 ** -40, 2.0 ** 40, 2.0 ** -14, 0.0, 1.0])
+            p.ks[ids, 0] *= torch.tensor([1.0, 64.0, 0.01, 1.0, 1.0, 0.0])
+            p.load()
+            check(*p.run(), p.ref(), io, (fmt, io))
+    # all the weight on the small page
+    p = Problem(gdn, [32], [1], 1, 1, 64, 16, torch.int8, torch.bfloat16, seed=9)
+    ids = p.tables[0].long()
+    p.kc[ids[0]], p.kc[ids[1]] = 1, -1
+    p.ks[ids] = 40.0 / 64
+    p.q[:] = 1.0
+    p.vs[ids, 0] = torch.tensor([2.0 ** -60, 1.0])
+    p.load()
+    check(*p.run(), p.ref(), torch.bfloat16, "weight on the small page")
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+def test_large_and_small_queries(gdn, io):
+    """Queries far outside the fp16 range (their scores brought back by `scale`), tiny ones and
+    zeros."""
+    p = Problem(gdn, [70, 70, 70], [1, 1, 1], 4, 2, 128, 32, torch.int8, io, seed=10)
+    p.q[0] *= 2.0 ** 60
+    check(*(x[:1] for x in p.run(scale=2.0 ** -62)),
+          tuple(x[:1] for x in p.ref(scale=2.0 ** -62)), io)
+    p.q[0], p.q[1] = 0, p.q[1] * 2.0 ** -40
+    check(*p.run(), p.ref(), io)
+
+
+def test_strided_queries(gdn):
+    """Queries as the first half of each head of a gated projection."""
+    p = Problem(gdn, [100, 33], [1, 2], 8, 2, 128, 64, torch.int8, torch.bfloat16, seed=12)
+    wide = torch.randn(3, 8, 256).bfloat16().cuda()
+    wide[:, :, :128] = p.q.cuda()
+    check(*p.run(q=wide[:, :, :128]), p.ref(), torch.bfloat16)
+
+
+def test_shared_pages(gdn):
+    """Two sequences whose tables share a prefix."""
+    p = Problem(gdn, [100, 120], [1, 1], 4, 2, 64, 16, torch.int8, torch.bfloat16, seed=13)
+    p.tables[1, :6] = p.tables[0, :6]
+    check(*p.run(), p.ref(), torch.bfloat16)
+
+
+def test_bad_lengths_and_pages_are_reported(gdn):
+    p = Problem(gdn, [40, 40, 40], [1, 1, 1], 4, 2, 64, 16, torch.int8, torch.bfloat16, seed=14)
+    ref = p.ref()
+    tables = p.tables.clone()
+    p.lens = [40, 49, 40]          # past the table's 3 pages
+    with pytest.raises(gdn.GdnError) as e:
+        p.run()
+    assert e.value.status == 6
+    got = p.run(check_status=False)
+    for i in (0, 2):
+        check(got[0][i:i + 1], got[1][i:i + 1], tuple(x[i:i + 1] for x in ref), torch.bfloat16)
+    p.lens = [40, 40, 40]
+    p.tables[2, 1] = p.ks.shape[0]  # outside the pool: its keys are left out
+    with pytest.raises(gdn.GdnError) as e:
+        p.run()
+    assert e.value.status == 6
+    got = p.run(check_status=False)
+    p.tables = tables
+    for i in (0, 1):
+        check(got[0][i:i + 1], got[1][i:i + 1], tuple(x[i:i + 1] for x in ref), torch.bfloat16)
+    assert not torch.isnan(got[0]).any()
+
+
+def test_repeats_bit_for_bit_and_on_another_stream(gdn):
+    p = Problem(gdn, [9000, 3, 1200], [2, 1, 1], 16, 2, 128, 64, torch.int8, torch.bfloat16)
+    want = p.run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, {}, {"stream": s}):
+        got = p.run(**kw)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_one_workspace_for_many_calls(gdn):
+    """A workspace kept by the caller, filled with other calls' contents and with junk."""
+    p = Problem(gdn, [5000, 100], [1, 1], 8, 1, 128, 64, torch.int8, torch.bfloat16, seed=20)
+    o = Problem(gdn, [50, 4000], [3, 1], 8, 1, 128, 64, torch.int8, torch.bfloat16, seed=21)
+    want, other = p.run(), o.run()
+    ws = torch.full((64 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(p.run(workspace=ws)[0], want[0])
+        assert torch.equal(o.run(workspace=ws)[0], other[0])
+
+
+def test_offsets_past_32_bits(gdn):
+    """Pages beyond 2^32 bytes of a large cache give what the same pages of a small one give."""
+    page, hkv, D = 128, 8, 256
+    pages = (1 << 32) // (page * hkv * D) + 3
+    p = Problem(gdn, [300], [1], 16, hkv, D, page, torch.int8, torch.bfloat16, seed=22)
+    want = p.run()
+    ids = p.tables[0].long()
+    big = gdn.KVCache.empty(pages, hkv, page, D)
+    far = torch.tensor([pages - 1, 0, pages - 2])
+    big.k[far.cuda()], big.v[far.cuda()] = p.cache.k[ids.cuda()], p.cache.v[ids.cuda()]
+    big.k_scale[far.cuda()] = p.cache.k_scale[ids.cuda()]
+    big.v_scale[far.cuda()] = p.cache.v_scale[ids.cuda()]
+    p.cache, p.tables = big, far.int()[None]
+    got = p.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_graph_capture(gdn):
+    """A captured call replays on new contents of the same buffers."""
+    p = Problem(gdn, [600, 40], [1, 1], 8, 2, 128, 64, torch.int8, torch.bfloat16, seed=23)
+    q, tables = p.q.cuda(), p.tables.cuda()
+    lens = torch.tensor(p.lens, dtype=torch.int32).cuda()
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    gdn.kv_attention(p.cache, q, tables, lens, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = gdn.kv_attention(p.cache, q, tables, lens, workspace=ws)
+    for new_lens in ([600, 40], [1, 33], [311, 0]):
+        lens.copy_(torch.tensor(new_lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        p.lens = new_lens
+        check(out, lse, p.ref(), torch.bfloat16, new_lens)
+
+
+def test_append_then_attend_matches_unquantised(gdn):
+    """The whole path: appended prompts and single tokens, then attention, against fp64 attention
+    over what the cache reads back."""
+    gen = torch.Generator().manual_seed(30)
+    hq, hkv, D, page = 8, 2, 128, 32
+    lens = [70, 5]
+    cache = gdn.KVCache.empty(8, hkv, page, D)
+    tables = torch.tensor([[3, 1, 7], [2, 0, 5]], dtype=torch.int32).cuda()
+    k, v = [torch.randn(75, hkv, D, generator=gen).bfloat16().cuda() for _ in range(2)]
+    gdn.kv_append(cache, k, v, tables, torch.zeros(2, dtype=torch.int32).cuda(),
+                  at.cumulative(lens).cuda(), check_status=True)
+    for step in range(3):
+        held = torch.tensor(lens, dtype=torch.int32).cuda()
+        k, v = [torch.randn(2, hkv, D, generator=gen).bfloat16().cuda() for _ in range(2)]
+        q = torch.randn(2, hq, D, generator=gen).bfloat16().cuda()
+        gdn.kv_append(cache, k, v, tables, held, check_status=True)
+        out, lse = gdn.kv_attention(cache, q, tables, held + 1, check_status=True)
+        lens = [n + 1 for n in lens]
+        kk, vv = gdn.kv_read(cache, tables, None, at.cumulative(lens).cuda(), sum(lens),
+                             torch.float32)
+        at0 = 0
+        for n, L in enumerate(lens):
+            kn, vn = kk[at0:at0 + L].double().cpu(), vv[at0:at0 + L].double().cpu()
+            at0 += L
+            x = torch.einsum("hgd,jhd->hgj", q[n].double().cpu().view(hkv, hq // hkv, D), kn)
+            w = torch.softmax(x / math.sqrt(D), -1)
+            want = torch.einsum("hgj,jhd->hgd", w, vn).reshape(hq, D)
+            mag = torch.einsum("hgj,jhd->hgd", w, vn.abs()).reshape(hq, D)
+            err = (out[n].double().cpu() - want).abs()
+            assert bool((err <= 2.0 ** -10 * mag + 2.0 ** -8 * want.abs()).all())
