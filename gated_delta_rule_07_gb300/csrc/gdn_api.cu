@@ -5,6 +5,7 @@
 #include <string.h>
 
 #include "gdn.h"
+#include "gdn_attention.h"
 #include "gdn_internal.h"
 
 namespace {

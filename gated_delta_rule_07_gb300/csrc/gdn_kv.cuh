@@ -14,8 +14,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "gdn_attention.h"
 #include "gdn_common.cuh"
-#include "gdn_internal.h"
 
 namespace gdn {
 
