@@ -6,6 +6,30 @@
 // within the window):
 //     x_j = scale q . k_j,   o = sum_j softmax(x)_j v_j,   lse = log sum_j exp(x_j),
 // kv head h / (hq / hkv).  A row that no key is left for gets o = 0 and lse = -inf.
+//
+// Bound by HBM: with g query heads a kv head and m rows, 2 D bytes of codes feed 4 g m D flops.
+// The kernel streams the codes once, straight into registers:
+//   * Products.  Rows (query tokens x the heads of a kv head) are the N = 8 side of
+//     mma.m16n8k16 (fp16 operands, fp32 sums); keys are the M side of S^T = K Q^T and the channels
+//     the M side of O^T = V^T P^T.  Every code is then needed by one lane of one warp: no shared
+//     memory, no barrier, no copy in the way.  Which of a product's contraction indices a lane
+//     holds is free as long as both operands agree, so a lane's 16 contiguous bytes of a key row
+//     are its operands of four products (the queries are laid out to match), and the value
+//     layout's words of four tokens are those of the second product; the weights get from the
+//     first's result layout to the second's operand layout by an 8 x 8 transpose (movmatrix).
+//   * Codes are exact in fp16: int8 by way of 1024 + u in an fp16's mantissa, e4m3 by moving its
+//     bits (times 2^-8; no code becomes a NaN, so bytes past a length are harmless under a weight
+//     of 0).  Queries are scaled by a power of two per row into fp16's range: exact for bf16; fp32
+//     ones are split into two fp16 parts, and the weights too, for fp32 accuracy.
+//   * Softmax, one pass: the running maximum is of y = x log2 e + log2(value scale), so that the
+//     weights w = 2^(y - M) already carry their page's value scale and stay in fp16's range
+//     whatever the scales are; the sum takes w / value scale.  The maximum only moves (and the
+//     sums are only rescaled) when a tile exceeds it by 2^6: weights stay below 2^6.
+//   * Work.  Units of 16 keys, of all sequences, kv heads and row tiles in one line, cut into
+//     equal runs, one a CTA: ragged lengths balance, one long sequence fills the GPU.  A CTA's
+//     warps take its run's units in turn and join at the end of each item; items cut between CTAs
+//     leave partial sums (M, sum, unnormalised o), joined in order by a second small kernel.
+#include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include "gdn_kv.cuh"
@@ -13,112 +37,611 @@
 namespace gdn {
 namespace {
 
-constexpr int kAttThreads = 128;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kTile = 16;      // keys of a unit
+constexpr int kMinUnits = 8;   // units of a CTA at least
+constexpr int kMaxCtas = 608;  // CTAs at most (the workspace holds two partial results of each)
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 6.f;  // the maximum moves when exceeded by this (log2)
 
-template <typename IO, int D, bool E4M3>
-__global__ void __launch_bounds__(kAttThreads) kv_attention_simple(KvArgs a) {
-  constexpr int kWarps = kAttThreads / 32, C = D / 32;
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int64_t t = blockIdx.x;
-  const int h = blockIdx.y, kh = h / (a.hq / a.hkv);
-  int n = 0;
-  int64_t b = 0, e = a.T;
-  if (a.cu) {
-    int lo = 0, hi = a.N - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    n = lo;
-    if (!seq_bounds(a.cu, n, a.T, a.status, b, e) || t < b || t >= e) return;
-  } else if (a.N > 1) {
-    n = (int)t;
-    b = t;
-    e = t + 1;
+// ------------------------------------------------------------------------------ the work plan
+
+struct Item {          // what a sequence asks for
+  int64_t row0;        // its first packed row
+  int m, len;          // query rows (tokens), keys
+  int tile0, tiles;    // units of 16 keys that some row sees
+  int row_tiles;       // tiles of the m * group rows of a kv head
+};
+
+template <int ROWS>
+__device__ __forceinline__ bool item_of(const KvArgs& a, int n, Item& it) {
+  int64_t b, e;
+  if (a.cu == nullptr && a.N > 1) {
+    b = n;
+    e = n + 1;
+  } else if (!seq_bounds(a.cu, n, a.T, a.status, b, e)) {
+    return false;
   }
+  if (e <= b) return false;
   const int len = a.pos0[n];
   if (len < 0 || len > (int64_t)a.max_pages * a.page) {
-    if (threadIdx.x == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
-    return;
+    set_status(a.status, GDN_ERR_DEVICE_INPUT);
+    return false;
   }
-  const int64_t at = len - (e - b) + (t - b);
-  const int64_t j0 = a.window > 0 && at - a.window + 1 > 0 ? at - a.window + 1 : 0;
-  const IO* qp = static_cast<const IO*>(a.q) + t * a.q_ts + h * a.q_hs;
-  float q[C], o[C], m = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-  for (int i = 0; i < C; ++i) {
-    q[i] = to_f32(qp[32 * i + lane]);
-    o[i] = 0.f;
-  }
-  for (int64_t j = j0 + warp; j <= at; j += kWarps) {
-    const int pid = kv_page_id(a, n, (int)(j / a.page));
-    if (pid < 0) continue;
-    const int64_t block = (int64_t)pid * a.hkv + kh;
-    const int s = (int)(j % a.page);
-    const uint8_t* kp = a.k_codes + (block * a.page + s) * D;
-    const uint8_t* vp = a.v_codes + (block * a.page + (s & ~3)) * D + (s & 3);
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) x = fmaf(q[i], kv_value<E4M3>(kp[32 * i + lane]), x);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    x *= a.scale * a.k_scale[block];
-    const float mn = fmaxf(m, x), f = __expf(m - mn), p = __expf(x - mn), vs = a.v_scale[block];
-    l = l * f + p;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-      o[i] = fmaf(p * vs, kv_value<E4M3>(vp[4 * (32 * i + lane)]), o[i] * f);
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < C; ++i) so[warp][32 * i + lane] = o[i];
-  __syncthreads();
-  float M = -CUDART_INF_F, L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-  float f[kWarps];
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = M > -CUDART_INF_F ? __expf(sm[w] - M) : 0.f;
-    L += sl[w] * f[w];
-  }
-  IO* out = static_cast<IO*>(a.out) + (t * a.hq + h) * D;
-  for (int d = threadIdx.x; d < D; d += kAttThreads) {
-    float x = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) x = fmaf(so[w][d], f[w], x);
-    out[d] = from_f32<IO>(L > 0.f ? x / L : 0.f);
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[t * a.hq + h] = M + logf(L);
+  it.row0 = b;
+  it.m = (int)(e - b);
+  it.len = len;
+  const int64_t lo = a.window > 0 ? (int64_t)len - it.m - a.window + 1 : 0;
+  it.tile0 = lo > 0 ? (int)(lo / kTile) : 0;
+  it.tiles = (len + kTile - 1) / kTile - it.tile0;
+  if (it.tiles < 1) it.tiles = 1;  // no key at all: a unit that sees nothing writes the zeros
+  it.row_tiles = (int)(((int64_t)it.m * (a.hq / a.hkv) + ROWS - 1) / ROWS);
+  return true;
+}
+__device__ __forceinline__ int64_t units_of(const KvArgs& a, const Item& it) {
+  return (int64_t)it.tiles * it.row_tiles * a.hkv;
 }
 
-template <typename IO, int D>
-cudaError_t launch_att(const KvArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)a.T, (unsigned)a.hq);
-  if (a.e4m3) kv_attention_simple<IO, D, true><<<grid, kAttThreads, 0, s>>>(a);
-  else kv_attention_simple<IO, D, false><<<grid, kAttThreads, 0, s>>>(a);
-  return cudaGetLastError();
+struct Desc {  // an item that ends in CTA c and began in CTA `first` < c
+  int n, head, row_tile, first;
+};
+
+// ---------------------------------------------------------------------------------- operands
+
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
 }
-template <typename IO>
-cudaError_t launch_att_io(const KvArgs& a, cudaStream_t s) {
+
+// four codes to two registers of fp16 pairs (int8: the codes; e4m3: the values times 2^-8)
+template <bool E4M3>
+__device__ __forceinline__ void open_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (E4M3) {
+    const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);
+    lo = (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
+    hi = (y & 0x80008000u) | ((y >> 1) & 0x3f803f80u);
+  } else {
+    const uint32_t u = w ^ 0x80808080u;  // code + 128; 0x6400 | u is 1024 + u
+    const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x64806480u));
+  }
+}
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 open_half(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ------------------------------------------------------------------------------------ kernel
+
+// NT: tiles of 8 rows that a warp carries.  SPLIT (fp32 I/O): queries and weights in two parts.
+template <int D, int NT, bool SPLIT> struct Shape {
+  static constexpr int rows = 8 * NT, parts = SPLIT ? 2 : 1;
+  // queries stay in registers where they are few, else each product reads them from shared memory
+  static constexpr bool q_regs = !SPLIT && D * NT <= 128;
+  static constexpr int q_bytes = parts * rows * D * 2;
+  static constexpr int pad = D + 4;  // floats of a row of partial sums (conflict-free)
+  static constexpr int o_bytes = kWarps * rows * pad * 4;
+  static constexpr int smem = q_bytes > o_bytes ? q_bytes : o_bytes;
+  // registers decide the resident CTAs: the sums alone are D NT / 4 of them
+  static constexpr int ctas = D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;
+};
+
+template <typename IO, int D, int NT, bool E4M3>
+__global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(IO) == 4>::ctas))
+kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
+  constexpr bool SPLIT = sizeof(IO) == 4;
+  using S = Shape<D, NT, SPLIT>;
+  constexpr int ROWS = S::rows, KC = D / 64, VC = D / 32, STEPS = D / 16;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ int64_t scan[kWarps];
+  __shared__ int64_t start_off;
+  __shared__ int start_n;
+  __shared__ float q_scale[ROWS];
+  __shared__ float2 warp_ml[kWarps][ROWS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  const int r = lane >> 2, c = lane & 3;
+
+  // the plan: all units, this CTA's run [u0, u1) of them, the sequence that u0 falls into
+  int64_t total = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t u0 = blockIdx.x * (per > kMinUnits ? per : kMinUnits);
+    int64_t before = 0;
+    for (int n0 = 0; n0 < a.N; n0 += kThreads) {
+      Item it;
+      const int n = n0 + tid;
+      const int64_t w = n < a.N && item_of<ROWS>(a, n, it) ? units_of(a, it) : 0;
+      int64_t s = w;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += y;
+      }
+      if (lane == 31) scan[warp] = s;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) s += scan[i];
+        all += scan[i];
+      }
+      s += before;  // units up to and with sequence n
+      if (pass && u0 < s && u0 >= s - w) {
+        start_n = n;
+        start_off = u0 - (s - w);
+      }
+      before += all;
+      __syncthreads();
+    }
+    if (pass == 0) total = before;
+  }
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  per = per > kMinUnits ? per : kMinUnits;
+  int64_t u = blockIdx.x * per;
+  const int64_t u1 = u + per < total ? u + per : total;
+  if (tid == 0) descs[blockIdx.x].n = -1;
+  if (u >= u1) return;
+
+  const int group = a.hq / a.hkv;
+  int n = start_n;
+  int64_t off = start_off;
+  while (u < u1 && n < a.N) {
+    Item it;
+    if (!item_of<ROWS>(a, n, it) || off >= units_of(a, it)) {
+      ++n;
+      off = 0;
+      continue;
+    }
+    // one item: kv head, row tile, and this CTA's units [ta, tb) of it
+    const int which = (int)(off / it.tiles), ta = (int)(off - (int64_t)which * it.tiles);
+    const int head = which / it.row_tiles, rt = which - head * it.row_tiles;
+    const int tb = (int)(it.tiles < ta + (u1 - u) ? it.tiles : ta + (u1 - u));
+    const int row_base = rt * ROWS, row_end = it.m * group;
+
+    // queries: scaled by a power of two into [1, 2), fp16, in the order the products take them
+    for (int row = warp; row < ROWS; row += kWarps) {
+      const int rr = row_base + row;
+      float f[D / 32 < 4 ? 4 : D / 32];
+      const bool live = rr < row_end;
+      const IO* q = static_cast<const IO*>(a.q) + (it.row0 + (live ? rr / group : 0)) * a.q_ts +
+                    (head * group + (live ? rr % group : 0)) * a.q_hs;
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < (D + 127) / 128; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int d = 128 * i + 4 * lane + e;
+          f[4 * i + e] = live && d < D ? to_f32(q[d]) : 0.f;
+          amax = fmaxf(amax, fabsf(f[4 * i + e]));
+        }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      int ex = (int)((__float_as_uint(amax) >> 23) & 0xff);
+      ex = ex == 0 ? 127 : min(max(ex, 2), 252);
+      const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+      if (lane == 0) q_scale[row] = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+      for (int i = 0; i < (D + 127) / 128; ++i) {
+        const int d = 128 * i + 4 * lane;
+        if (d < D) {
+          // dims 64 j + 16 cc + 4 w + {0..3}: lane (row % 8, cc), product 4 j + w
+          const int step = 4 * (d / 64) + (d % 16) / 4, cc = (d % 64) / 16;
+          const int at = (((row / 8) * (STEPS / 2) + step / 2) * 32 + 4 * (row % 8) + cc) * 16 +
+                         (step & 1) * 8;
+          uint2 hi;
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = f[4 * i + e] * down;
+          hi.x = pack_half(x[0], x[1]);
+          hi.y = pack_half(x[2], x[3]);
+          *reinterpret_cast<uint2*>(smem + at) = hi;
+          if constexpr (SPLIT) {
+            const float2 p = open_half(hi.x), s = open_half(hi.y);
+            *reinterpret_cast<uint2*>(smem + ROWS * D * 2 + at) =
+                make_uint2(pack_half(x[0] - p.x, x[1] - p.y), pack_half(x[2] - s.x, x[3] - s.y));
+          }
+        }
+      }
+    }
+    __syncthreads();
+    uint4 qr[S::q_regs ? NT : 1][S::q_regs ? STEPS / 2 : 1];
+    if constexpr (S::q_regs) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int s = 0; s < STEPS / 2; ++s)
+          qr[t][s] = reinterpret_cast<const uint4*>(smem)[(t * (STEPS / 2) + s) * 32 + lane];
+    }
+    // this lane's columns: rows 8 t + 2 c + e, the last key each sees, its scale
+    int last[NT][2];
+    float qs[NT][2], M[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * t + 2 * c + e;
+        last[t][e] = row_base + row < row_end ? it.len - it.m + (row_base + row) / group : -1;
+        qs[t][e] = q_scale[row] * a.scale * kLog2e;
+        M[t][e] = -CUDART_INF_F;
+        l[t][e] = 0.f;
+      }
+    const int last_row = min(row_base + ROWS, row_end) - 1;
+    // keys that every live row sees: [all_lo, all_hi]
+    const int all_hi = row_base + ROWS <= row_end ? it.len - it.m + row_base / group : -1;
+    const int64_t all_lo = a.window > 0
+        ? (int64_t)it.len - it.m + last_row / group - a.window + 1 : INT64_MIN;
+    float acc[NT][2 * VC][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 2 * VC; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][i][e] = 0.f;
+
+    const int* table = a.table + (int64_t)n * a.max_pages;
+    auto page_of = [&](int tile) {  // a tile's page id (-1: none; its keys are left out)
+      const int key = (it.tile0 + tile) * kTile;
+      if (tile >= tb || key >= it.len) return -1;
+      const int pid = __ldg(table + key / a.page);
+      if (pid >= 0 && pid < a.num_pages) return pid;
+      if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
+      return -1;
+    };
+    uint4 kb[2][KC], vb[VC];
+    float ks = 0.f, vs = 0.f;
+    // key rows of the lane: tokens 4 (r / 2) + r % 2 and two on, so that the first product's
+    // result rows are the tokens whose weights the second's operand words hold
+    const int tok = 4 * (r >> 1) + (r & 1);
+    auto load_k = [&](int pid, int tile) {
+      if (pid < 0) return;
+      const int64_t block = (int64_t)pid * a.hkv + head;
+      const int slot = (it.tile0 + tile) * kTile % a.page;
+      const uint8_t* p = a.k_codes + (block * a.page + slot + tok) * D + 16 * c;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        kb[0][j] = ld_stream(p + 64 * j);
+        kb[1][j] = ld_stream(p + 2 * D + 64 * j);
+      }
+    };
+    auto load_v = [&](int pid, int tile) {
+      if (pid < 0) return;
+      const int64_t block = (int64_t)pid * a.hkv + head;
+      const int slot = (it.tile0 + tile) * kTile % a.page;
+      const uint8_t* p = a.v_codes + (block * a.page + slot + 4 * c) * D + 16 * r;
+#pragma unroll
+      for (int j = 0; j < VC; ++j) vb[j] = ld_stream(p + 128 * j);
+    };
+    auto load_scales = [&](int pid) {
+      if (pid < 0) return;
+      const int64_t block = (int64_t)pid * a.hkv + head;
+      ks = __ldg(a.k_scale + block);
+      vs = __ldg(a.v_scale + block);
+    };
+    int tile = ta + warp, pid = page_of(tile), pid_next = page_of(tile + kWarps);
+#pragma unroll
+    for (int j = 0; j < KC; ++j) kb[0][j] = kb[1][j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < VC; ++j) vb[j] = make_uint4(0, 0, 0, 0);
+    load_k(pid, tile);
+    load_v(pid, tile);
+    load_scales(pid);
+    for (; tile < tb; tile += kWarps) {
+      const int pid_after = page_of(tile + 2 * kWarps);
+      float s[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&kb[0][j]);
+        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&kb[1][j]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // two products of the four in 16 bytes
+          uint32_t x[2][4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            open_codes<E4M3>(w0[2 * h + i], x[i][0], x[i][2]);
+            open_codes<E4M3>(w1[2 * h + i], x[i][1], x[i][3]);
+          }
+#pragma unroll
+          for (int part = 0; part < S::parts; ++part)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              uint4 q;
+              if constexpr (S::q_regs)
+                q = qr[t][2 * j + h];
+              else
+                q = reinterpret_cast<const uint4*>(smem + part * ROWS * D * 2)
+                    [(t * (STEPS / 2) + 2 * j + h) * 32 + lane];
+              mma16816(s[t], x[0][0], x[0][1], x[0][2], x[0][3], q.x, q.y);
+              mma16816(s[t], x[1][0], x[1][1], x[1][2], x[1][3], q.z, q.w);
+            }
+        }
+      }
+      const float k_now = ks * (E4M3 ? 256.f : 1.f), v_now = vs * (E4M3 ? 256.f : 1.f);
+      load_k(pid_next, tile + kWarps);
+      load_scales(pid_next);
+
+      // scores in log2, with the page's value scale; a page of zero values weighs as 2^-100
+      const float lv = v_now > 0.f ? __log2f(v_now) : -100.f;
+      const float rv = exp2_fast(-lv);
+      const int key = (it.tile0 + tile) * kTile + tok;
+      const int first = (it.tile0 + tile) * kTile;
+      const bool open = pid >= 0 && first + kTile - 1 <= all_hi && first >= all_lo;
+      bool moves = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y = fmaf(s[t][e], k_now * qs[t][e & 1], lv);
+          if (!open) {
+            const int kk = key + (e & 2), la = last[t][e & 1];
+            const bool seen = pid >= 0 && kk <= la && (a.window == 0 || (int64_t)kk > (int64_t)la - a.window);
+            y = seen ? y : -CUDART_INF_F;
+          }
+          s[t][e] = y;
+          moves |= y > M[t][e & 1] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(s[t][e], s[t][e + 2]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            m = fmaxf(m, M[t][e]);
+            const float f = m > -CUDART_INF_F ? exp2_fast(M[t][e] - m) : 1.f;
+            M[t][e] = m;
+            l[t][e] *= f;
+#pragma unroll
+            for (int i = 0; i < 2 * VC; ++i) {
+              acc[t][i][e] *= f;
+              acc[t][i][e + 2] *= f;
+            }
+          }
+      }
+      uint32_t p[NT][S::parts][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float m = M[t][e & 1];
+          w[e] = exp2_fast(s[t][e] - (m > -CUDART_INF_F ? m : 0.f));
+          l[t][e & 1] = fmaf(w[e], rv, l[t][e & 1]);
+        }
+        const uint32_t h0 = pack_half(w[0], w[1]), h1 = pack_half(w[2], w[3]);
+        p[t][0][0] = transpose8x8(h0);
+        p[t][0][1] = transpose8x8(h1);
+        if constexpr (SPLIT) {
+          const float2 x = open_half(h0), y = open_half(h1);
+          p[t][1][0] = transpose8x8(pack_half(w[0] - x.x, w[1] - x.y));
+          p[t][1][1] = transpose8x8(pack_half(w[2] - y.x, w[3] - y.y));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < VC; ++j) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&vb[j]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[4];
+          open_codes<E4M3>(w[2 * h], x[0], x[2]);
+          open_codes<E4M3>(w[2 * h + 1], x[1], x[3]);
+#pragma unroll
+          for (int part = 0; part < S::parts; ++part)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+              mma16816(acc[t][2 * j + h], x[0], x[1], x[2], x[3], p[t][part][0], p[t][part][1]);
+        }
+      }
+      load_v(pid_next, tile + kWarps);
+      pid = pid_next;
+      pid_next = pid_after;
+    }
+
+    // join the warps: each leaves its maxima and sums, then its o, on the common maximum
+    __syncthreads();  // (queries in shared memory are no longer needed)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[t][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (r == 0) warp_ml[warp][8 * t + 2 * c + e] = make_float2(M[t][e], x);
+      }
+    float* so = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < VC; ++j)
+          *reinterpret_cast<float4*>(so + (warp * ROWS + 8 * t + 2 * c + e) * S::pad + 32 * j +
+                                     4 * r) =
+              make_float4(acc[t][2 * j][e], acc[t][2 * j][e + 2], acc[t][2 * j + 1][e],
+                          acc[t][2 * j + 1][e + 2]);
+    __syncthreads();
+    const bool begins = ta == 0, ends = tb == it.tiles;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
+    for (int i = tid; i < ROWS * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = row_base + row;
+      if (rr >= row_end) continue;
+      float m = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][row].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m > -CUDART_INF_F) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = exp2_fast(warp_ml[w][row].x - m);
+          const float4 x = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * S::pad + d);
+          L = fmaf(warp_ml[w][row].y, f, L);
+          o.x = fmaf(x.x, f, o.x);
+          o.y = fmaf(x.y, f, o.y);
+          o.z = fmaf(x.z, f, o.z);
+          o.w = fmaf(x.w, f, o.w);
+        }
+      }
+      if (begins && ends) {
+        const int64_t at = (it.row0 + rr / group) * a.hq + head * group + rr % group;
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        IO* out = static_cast<IO*>(a.out) + at * D + d;
+        out[0] = from_f32<IO>(o.x * inv);
+        out[1] = from_f32<IO>(o.y * inv);
+        out[2] = from_f32<IO>(o.z * inv);
+        out[3] = from_f32<IO>(o.w * inv);
+        if (a.lse && d == 0) a.lse[at] = (m + log2f(L)) * kLn2;
+      } else {
+        *reinterpret_cast<float4*>(part_o + (slot * ROWS + row) * D + d) = o;
+        if (d == 0) part_ml[slot * ROWS + row] = make_float2(m, L);
+      }
+    }
+    if (ends && !begins && tid == 0)
+      descs[blockIdx.x] = Desc{n, head, rt, (int)((u - ta) / per)};
+    __syncthreads();
+    u += tb - ta;
+    off += tb - ta;
+  }
+}
+
+// Joins the partial results of the item that ended in CTA blockIdx.x and began in an earlier one:
+// a warp a row, lanes along D, partials in CTA order.
+template <typename IO, int D, int NT>
+__global__ void __launch_bounds__(256) kv_attention_join(KvArgs a, const float* part_o,
+                                                         const float2* part_ml,
+                                                         const Desc* descs) {
+  constexpr int ROWS = 8 * NT, C = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Desc d = descs[blockIdx.x];
+  if (d.n < 0) return;
+  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + threadIdx.x / 32;
+  Item it;
+  if (!item_of<ROWS>(a, d.n, it)) return;
+  const int group = a.hq / a.hkv, rr = d.row_tile * ROWS + row;
+  if (row >= ROWS || rr >= it.m * group) return;
+  const int count = (int)blockIdx.x - d.first + 1;
+  float m = -CUDART_INF_F;
+  for (int i = lane; i < count; i += 32)
+    m = fmaxf(m, part_ml[(2 * (int64_t)(d.first + i) + (i == 0)) * ROWS + row].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float L = 0.f, o[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = 0.f;
+  if (m > -CUDART_INF_F) {
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const int64_t slot = (2 * (int64_t)(d.first + i) + (i == 0)) * ROWS + row;
+      const float2 ml = part_ml[slot];
+      const float f = exp2_fast(ml.x - m);
+      L = fmaf(ml.y, f, L);
+#pragma unroll
+      for (int j = 0; j < C; ++j) o[j] = fmaf(part_o[slot * D + 32 * j + lane], f, o[j]);
+    }
+  }
+  const int64_t at = (it.row0 + rr / group) * a.hq + d.head * group + rr % group;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  IO* out = static_cast<IO*>(a.out) + at * D;
+#pragma unroll
+  for (int j = 0; j < C; ++j) out[32 * j + lane] = from_f32<IO>(o[j] * inv);
+  if (a.lse && lane == 0) a.lse[at] = (m + log2f(L)) * kLn2;
+}
+
+// --------------------------------------------------------------------------------- launching
+
+// Tiles of 8 rows a warp carries: as many as the average sequence's rows of a kv head fill (a row
+// tile more reads the cache once more), within the registers (D NT <= 512).
+int row_tiles(const KvArgs& a) {
+  const int64_t rows = (a.T + a.N - 1) / a.N * (a.hq / a.hkv);
+  return rows <= 8 ? 1 : rows <= 16 || a.D == 256 ? 2 : 4;
+}
+
+template <typename IO, int D, int NT, bool E4M3>
+cudaError_t launch(const KvArgs& a, cudaStream_t s) {
+  using S = Shape<D, NT, sizeof(IO) == 4>;
+  const auto kern = kv_attention_kernel<IO, D, NT, E4M3>;
+  static const cudaError_t ready =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
+  if (ready != cudaSuccess) return ready;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int ctas = sms * S::ctas < kMaxCtas ? sms * S::ctas : kMaxCtas;
+  float* part_o = a.workspace;
+  float2* part_ml = reinterpret_cast<float2*>(part_o + (int64_t)2 * kMaxCtas * S::rows * D);
+  Desc* descs = reinterpret_cast<Desc*>(part_ml + (int64_t)2 * kMaxCtas * S::rows);
+  kern<<<ctas, kThreads, S::smem, s>>>(a, part_o, part_ml, descs);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // launched while the first kernel drains; it waits for its end before it reads anything
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(ctas, NT);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attention_join<IO, D, NT>, a, (const float*)part_o,
+                            (const float2*)part_ml, (const Desc*)descs);
+}
+
+template <typename IO, int D, bool E4M3>
+cudaError_t launch_rows(const KvArgs& a, cudaStream_t s) {
+  switch (row_tiles(a)) {
+    case 1: return launch<IO, D, 1, E4M3>(a, s);
+    case 2: return launch<IO, D, 2, E4M3>(a, s);
+    default:
+      if constexpr (D <= 128) return launch<IO, D, 4, E4M3>(a, s);
+      else return launch<IO, D, 2, E4M3>(a, s);
+  }
+}
+template <typename IO, bool E4M3>
+cudaError_t launch_d(const KvArgs& a, cudaStream_t s) {
   switch (a.D) {
-    case 64: return launch_att<IO, 64>(a, s);
-    case 128: return launch_att<IO, 128>(a, s);
-    default: return launch_att<IO, 256>(a, s);
+    case 64: return launch_rows<IO, 64, E4M3>(a, s);
+    case 128: return launch_rows<IO, 128, E4M3>(a, s);
+    default: return launch_rows<IO, 256, E4M3>(a, s);
   }
 }
 
 }  // namespace
 
-size_t kv_attention_workspace(const KvArgs&) { return 0; }
+size_t kv_attention_workspace(const KvArgs& a) {
+  const size_t rows = (size_t)2 * kMaxCtas * 8 * row_tiles(a);
+  return rows * a.D * sizeof(float) + rows * sizeof(float2) + kMaxCtas * sizeof(Desc);
+}
 
 cudaError_t kv_attention(const KvArgs& a, cudaStream_t s) {
-  return a.bf16 ? launch_att_io<__nv_bfloat16>(a, s) : launch_att_io<float>(a, s);
+  if (a.bf16) return a.e4m3 ? launch_d<__nv_bfloat16, true>(a, s) : launch_d<__nv_bfloat16, false>(a, s);
+  return a.e4m3 ? launch_d<float, true>(a, s) : launch_d<float, false>(a, s);
 }
 
 }  // namespace gdn
