@@ -657,7 +657,9 @@ gdn::KvArgs kv_args(const gdn_kv_cache* c, const gdn_kv_problem* p, const int32_
   memset(&a, 0, sizeof(a));
   a.T = p->total_tokens;
   a.N = p->num_seqs; a.hq = p->hq; a.hkv = c->hkv; a.D = c->head_dim;
-  a.page = c->page_size; a.num_pages = c->num_pages; a.max_pages = p->max_pages;
+  a.page = c->page_size;
+  while ((1 << a.page_shift) < a.page) ++a.page_shift;
+  a.num_pages = c->num_pages; a.max_pages = p->max_pages;
   a.k_ts = p->k_token_stride; a.k_hs = p->k_head_stride;
   a.v_ts = p->v_token_stride; a.v_hs = p->v_head_stride;
   a.q_ts = p->q_token_stride; a.q_hs = p->q_head_stride;

@@ -31,7 +31,7 @@ cudaError_t qk_rope(const QkRopeArgs& a, bool backward, cudaStream_t s);
 // already held (append), first position (read), whole length (attention) of each sequence.
 struct KvArgs {
   int64_t T, k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;
-  int N, hq, hkv, D, page, num_pages, max_pages, window;
+  int N, hq, hkv, D, page, page_shift, num_pages, max_pages, window;  // page = 1 << page_shift
   bool bf16, e4m3;
   float scale;
   const void *k, *v, *q;

@@ -39,10 +39,12 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16;      // keys of a unit
-constexpr int kMinUnits = 8;   // units of a CTA at least
+constexpr int kMinUnits = 16;  // units of a CTA at least
+constexpr int kItemUnits = 8;  // units that starting an item is worth (queries, joining warps)
 constexpr int kMaxCtas = 608;  // CTAs at most (the workspace holds two partial results of each)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 6.f;  // the maximum moves when exceeded by this (log2)
+constexpr float kNone = -1e30f;  // the maximum before any key
 
 // ------------------------------------------------------------------------------ the work plan
 
@@ -78,8 +80,12 @@ __device__ __forceinline__ bool item_of(const KvArgs& a, int n, Item& it) {
   it.row_tiles = (int)(((int64_t)it.m * (a.hq / a.hkv) + ROWS - 1) / ROWS);
   return true;
 }
+// its units: an item (a kv head and row tile of it) is kItemUnits idle ones, then its tiles
 __device__ __forceinline__ int64_t units_of(const KvArgs& a, const Item& it) {
-  return (int64_t)it.tiles * it.row_tiles * a.hkv;
+  return (int64_t)(it.tiles + kItemUnits) * it.row_tiles * a.hkv;
+}
+__device__ __forceinline__ int64_t div_up(int64_t x, uint32_t y) {  // x >= 0
+  return x < 0xffffffffLL - y ? (uint32_t)(x + y - 1) / y : (x + y - 1) / y;
 }
 
 struct Desc {  // an item that ends in CTA c and began in CTA `first` < c
@@ -110,6 +116,22 @@ __device__ __forceinline__ void open_codes(uint32_t w, uint32_t& lo, uint32_t& h
   }
 }
 
+__device__ __forceinline__ void load4(const float* p, float* f) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* f) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                            *reinterpret_cast<const uint32_t*>(&y));
+}
+
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -131,7 +153,13 @@ __device__ __forceinline__ float2 open_half(uint32_t x) {
 }
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -165,11 +193,10 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const int r = lane >> 2, c = lane & 3;
 
-  // the plan: all units, this CTA's run [u0, u1) of them, the sequence that u0 falls into
-  int64_t total = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t u0 = blockIdx.x * (per > kMinUnits ? per : kMinUnits);
+  // the plan: all units, this CTA's run [u, u1) of them, the sequence that u falls into (sequences
+  // beyond a CTA's threads are walked twice: once for the total, once to find the run's start)
+  int64_t total = 0, per = 0, u = 0;
+  for (int pass = a.N <= kThreads; pass < 2; ++pass) {
     int64_t before = 0;
     for (int n0 = 0; n0 < a.N; n0 += kThreads) {
       Item it;
@@ -190,20 +217,25 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         all += scan[i];
       }
       s += before;  // units up to and with sequence n
-      if (pass && u0 < s && u0 >= s - w) {
-        start_n = n;
-        start_off = u0 - (s - w);
-      }
       before += all;
+      if (n0 + kThreads >= a.N) total = before;
+      if (pass) {
+        if (per == 0) {
+          per = div_up(total, gridDim.x);
+          per = per > kMinUnits ? per : kMinUnits;
+          u = blockIdx.x * per;
+        }
+        if (u < s && u >= s - w) {
+          start_n = n;
+          start_off = u - (s - w);
+        }
+      }
       __syncthreads();
     }
-    if (pass == 0) total = before;
   }
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  per = per > kMinUnits ? per : kMinUnits;
-  int64_t u = blockIdx.x * per;
   const int64_t u1 = u + per < total ? u + per : total;
   if (tid == 0) descs[blockIdx.x].n = -1;
+  asm volatile("griddepcontrol.launch_dependents;");
   if (u >= u1) return;
 
   const int group = a.hq / a.hkv;
@@ -216,11 +248,65 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       off = 0;
       continue;
     }
-    // one item: kv head, row tile, and this CTA's units [ta, tb) of it
-    const int which = (int)(off / it.tiles), ta = (int)(off - (int64_t)which * it.tiles);
+    // one item: kv head, row tile, and this CTA's tiles [ta, tb) of it
+    const int span = it.tiles + kItemUnits;
+    const int which = off < 0x7fffffff ? (int)((uint32_t)off / (uint32_t)span) : (int)(off / span);
+    const int at0 = (int)(off - (int64_t)which * span);  // place in the item, idle units first
+    const int at1 = (int)(span < at0 + (u1 - u) ? span : at0 + (u1 - u));
+    const int64_t item_u = u - at0;
+    u += at1 - at0;
+    off += at1 - at0;
+    const int ta = max(at0 - kItemUnits, 0), tb = max(at1 - kItemUnits, 0);
+    if (ta >= tb) continue;
     const int head = which / it.row_tiles, rt = which - head * it.row_tiles;
-    const int tb = (int)(it.tiles < ta + (u1 - u) ? it.tiles : ta + (u1 - u));
     const int row_base = rt * ROWS, row_end = it.m * group;
+
+    // the first tiles are on their way before the queries are
+    const int* table = a.table + (int64_t)n * a.max_pages;
+    auto page_of = [&](int tile) {  // a tile's page id (-1: none; its keys are left out)
+      const int key = (it.tile0 + tile) * kTile;
+      if (tile >= tb || key >= it.len) return -1;
+      const int pid = __ldg(table + (key >> a.page_shift));
+      if (pid >= 0 && pid < a.num_pages) return pid;
+      if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
+      return -1;
+    };
+    uint4 kb[2][KC], vb[VC];
+    float ks = 0.f, vs = 0.f;
+    // key rows of the lane: tokens 4 (r / 2) + r % 2 and two on, so that the first product's
+    // result rows are the tokens whose weights the second's operand words hold
+    const int tok = 4 * (r >> 1) + (r & 1);
+    const uint8_t* const kp = a.k_codes + tok * D + 16 * c;
+    const uint8_t* const vp = a.v_codes + 4 * c * D + 16 * r;
+    auto bytes_of = [&](int pid, int tile) {  // where the tile's keys and its values begin
+      const int slot = ((it.tile0 + tile) * kTile) & (a.page - 1);
+      return ((int64_t)pid * a.hkv + head) * (a.page * D) + slot * D;
+    };
+    auto load_k = [&](int pid, int tile) {
+      if (pid < 0) return;
+      const uint8_t* p = kp + bytes_of(pid, tile);
+#pragma unroll
+      for (int j = 0; j < KC; ++j) {
+        kb[0][j] = ld_stream(p + 64 * j);
+        kb[1][j] = ld_stream(p + 2 * D + 64 * j);
+      }
+      const int64_t block = (int64_t)pid * a.hkv + head;
+      ks = __ldg(a.k_scale + block);
+      vs = __ldg(a.v_scale + block);
+    };
+    auto load_v = [&](int pid, int tile) {
+      if (pid < 0) return;
+      const uint8_t* p = vp + bytes_of(pid, tile);
+#pragma unroll
+      for (int j = 0; j < VC; ++j) vb[j] = ld_stream(p + 128 * j);
+    };
+#pragma unroll
+    for (int j = 0; j < KC; ++j) kb[0][j] = kb[1][j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < VC; ++j) vb[j] = make_uint4(0, 0, 0, 0);
+    int tile = ta + warp, pid = page_of(tile), pid_next = page_of(tile + kWarps);
+    load_k(pid, tile);
+    load_v(pid, tile);
 
     // queries: scaled by a power of two into [1, 2), fp16, in the order the products take them
     for (int row = warp; row < ROWS; row += kWarps) {
@@ -232,11 +318,12 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       float amax = 0.f;
 #pragma unroll
       for (int i = 0; i < (D + 127) / 128; ++i)
+        {
+          const int d = 128 * i + 4 * lane;
+          f[4 * i] = f[4 * i + 1] = f[4 * i + 2] = f[4 * i + 3] = 0.f;
+          if (live && d < D) load4(q + d, f + 4 * i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int d = 128 * i + 4 * lane + e;
-          f[4 * i + e] = live && d < D ? to_f32(q[d]) : 0.f;
-          amax = fmaxf(amax, fabsf(f[4 * i + e]));
+          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(f[4 * i + e]));
         }
 #pragma unroll
       for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -286,7 +373,7 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         const int row = 8 * t + 2 * c + e;
         last[t][e] = row_base + row < row_end ? it.len - it.m + (row_base + row) / group : -1;
         qs[t][e] = q_scale[row] * a.scale * kLog2e;
-        M[t][e] = -CUDART_INF_F;
+        M[t][e] = kNone;
         l[t][e] = 0.f;
       }
     const int last_row = min(row_base + ROWS, row_end) - 1;
@@ -302,53 +389,6 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][i][e] = 0.f;
 
-    const int* table = a.table + (int64_t)n * a.max_pages;
-    auto page_of = [&](int tile) {  // a tile's page id (-1: none; its keys are left out)
-      const int key = (it.tile0 + tile) * kTile;
-      if (tile >= tb || key >= it.len) return -1;
-      const int pid = __ldg(table + key / a.page);
-      if (pid >= 0 && pid < a.num_pages) return pid;
-      if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
-      return -1;
-    };
-    uint4 kb[2][KC], vb[VC];
-    float ks = 0.f, vs = 0.f;
-    // key rows of the lane: tokens 4 (r / 2) + r % 2 and two on, so that the first product's
-    // result rows are the tokens whose weights the second's operand words hold
-    const int tok = 4 * (r >> 1) + (r & 1);
-    auto load_k = [&](int pid, int tile) {
-      if (pid < 0) return;
-      const int64_t block = (int64_t)pid * a.hkv + head;
-      const int slot = (it.tile0 + tile) * kTile % a.page;
-      const uint8_t* p = a.k_codes + (block * a.page + slot + tok) * D + 16 * c;
-#pragma unroll
-      for (int j = 0; j < KC; ++j) {
-        kb[0][j] = ld_stream(p + 64 * j);
-        kb[1][j] = ld_stream(p + 2 * D + 64 * j);
-      }
-    };
-    auto load_v = [&](int pid, int tile) {
-      if (pid < 0) return;
-      const int64_t block = (int64_t)pid * a.hkv + head;
-      const int slot = (it.tile0 + tile) * kTile % a.page;
-      const uint8_t* p = a.v_codes + (block * a.page + slot + 4 * c) * D + 16 * r;
-#pragma unroll
-      for (int j = 0; j < VC; ++j) vb[j] = ld_stream(p + 128 * j);
-    };
-    auto load_scales = [&](int pid) {
-      if (pid < 0) return;
-      const int64_t block = (int64_t)pid * a.hkv + head;
-      ks = __ldg(a.k_scale + block);
-      vs = __ldg(a.v_scale + block);
-    };
-    int tile = ta + warp, pid = page_of(tile), pid_next = page_of(tile + kWarps);
-#pragma unroll
-    for (int j = 0; j < KC; ++j) kb[0][j] = kb[1][j] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int j = 0; j < VC; ++j) vb[j] = make_uint4(0, 0, 0, 0);
-    load_k(pid, tile);
-    load_v(pid, tile);
-    load_scales(pid);
     for (; tile < tb; tile += kWarps) {
       const int pid_after = page_of(tile + 2 * kWarps);
       float s[NT][4];
@@ -383,10 +423,9 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       }
       const float k_now = ks * (E4M3 ? 256.f : 1.f), v_now = vs * (E4M3 ? 256.f : 1.f);
       load_k(pid_next, tile + kWarps);
-      load_scales(pid_next);
 
       // scores in log2, with the page's value scale; a page of zero values weighs as 2^-100
-      const float lv = v_now > 0.f ? __log2f(v_now) : -100.f;
+      const float lv = v_now > 0.f ? log2_fast(v_now) : -100.f;
       const float rv = exp2_fast(-lv);
       const int key = (it.tile0 + tile) * kTile + tok;
       const int first = (it.tile0 + tile) * kTile;
@@ -403,8 +442,11 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             y = seen ? y : -CUDART_INF_F;
           }
           s[t][e] = y;
-          moves |= y > M[t][e & 1] + kSlack;
         }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) moves |= fmaxf(s[t][e], s[t][e + 2]) > M[t][e] + kSlack;
       if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -414,7 +456,7 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             m = fmaxf(m, M[t][e]);
-            const float f = m > -CUDART_INF_F ? exp2_fast(M[t][e] - m) : 1.f;
+            const float f = exp2_fast(M[t][e] - m);
             M[t][e] = m;
             l[t][e] *= f;
 #pragma unroll
@@ -430,8 +472,7 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         float w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float m = M[t][e & 1];
-          w[e] = exp2_fast(s[t][e] - (m > -CUDART_INF_F ? m : 0.f));
+          w[e] = exp2_fast(s[t][e] - M[t][e & 1]);
           l[t][e & 1] = fmaf(w[e], rv, l[t][e & 1]);
         }
         const uint32_t h0 = pack_half(w[0], w[1]), h1 = pack_half(w[2], w[3]);
@@ -491,30 +532,25 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     for (int i = tid; i < ROWS * (D / 4); i += kThreads) {
       const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = row_base + row;
       if (rr >= row_end) continue;
-      float m = -CUDART_INF_F, L = 0.f;
+      float m = kNone, L = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][row].x);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m > -CUDART_INF_F) {
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = exp2_fast(warp_ml[w][row].x - m);
-          const float4 x = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * S::pad + d);
-          L = fmaf(warp_ml[w][row].y, f, L);
-          o.x = fmaf(x.x, f, o.x);
-          o.y = fmaf(x.y, f, o.y);
-          o.z = fmaf(x.z, f, o.z);
-          o.w = fmaf(x.w, f, o.w);
-        }
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_fast(warp_ml[w][row].x - m);
+        const float4 x = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * S::pad + d);
+        L = fmaf(warp_ml[w][row].y, f, L);
+        o.x = fmaf(x.x, f, o.x);
+        o.y = fmaf(x.y, f, o.y);
+        o.z = fmaf(x.z, f, o.z);
+        o.w = fmaf(x.w, f, o.w);
       }
       if (begins && ends) {
         const int64_t at = (it.row0 + rr / group) * a.hq + head * group + rr % group;
         const float inv = L > 0.f ? 1.f / L : 0.f;
         IO* out = static_cast<IO*>(a.out) + at * D + d;
-        out[0] = from_f32<IO>(o.x * inv);
-        out[1] = from_f32<IO>(o.y * inv);
-        out[2] = from_f32<IO>(o.z * inv);
-        out[3] = from_f32<IO>(o.w * inv);
+        store4(out, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         if (a.lse && d == 0) a.lse[at] = (m + log2f(L)) * kLn2;
       } else {
         *reinterpret_cast<float4*>(part_o + (slot * ROWS + row) * D + d) = o;
@@ -522,54 +558,76 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       }
     }
     if (ends && !begins && tid == 0)
-      descs[blockIdx.x] = Desc{n, head, rt, (int)((u - ta) / per)};
+      descs[blockIdx.x] = Desc{n, head, rt, (int)((item_u + kItemUnits) / per)};
     __syncthreads();
-    u += tb - ta;
-    off += tb - ta;
   }
 }
 
-// Joins the partial results of the item that ended in CTA blockIdx.x and began in an earlier one:
-// a warp a row, lanes along D, partials in CTA order.
+// Joins the partial results of the item that ended in CTA blockIdx.x and began in an earlier one.
+// A thread takes four channels of a row and every `groups`-th partial, in CTA order; the groups
+// join in shared memory, in order.  Columns (rows x D / 4) are spread over blockIdx.y.
+constexpr int kJoinThreads = 256;
 template <typename IO, int D, int NT>
-__global__ void __launch_bounds__(256) kv_attention_join(KvArgs a, const float* part_o,
-                                                         const float2* part_ml,
-                                                         const Desc* descs) {
-  constexpr int ROWS = 8 * NT, C = D / 32;
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, const float* part_o,
+                                                                  const float2* part_ml,
+                                                                  const Desc* descs, int groups) {
+  constexpr int ROWS = 8 * NT;
+  __shared__ float4 so[kJoinThreads];
+  __shared__ float2 sml[kJoinThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Desc d = descs[blockIdx.x];
   if (d.n < 0) return;
-  const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + threadIdx.x / 32;
   Item it;
   if (!item_of<ROWS>(a, d.n, it)) return;
-  const int group = a.hq / a.hkv, rr = d.row_tile * ROWS + row;
-  if (row >= ROWS || rr >= it.m * group) return;
-  const int count = (int)blockIdx.x - d.first + 1;
-  float m = -CUDART_INF_F;
-  for (int i = lane; i < count; i += 32)
-    m = fmaxf(m, part_ml[(2 * (int64_t)(d.first + i) + (i == 0)) * ROWS + row].x);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float L = 0.f, o[C];
-#pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = 0.f;
-  if (m > -CUDART_INF_F) {
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {
-      const int64_t slot = (2 * (int64_t)(d.first + i) + (i == 0)) * ROWS + row;
-      const float2 ml = part_ml[slot];
+  const int cols = kJoinThreads / groups, g = threadIdx.x / cols;
+  const int col = blockIdx.y * cols + threadIdx.x % cols, row = col / (D / 4);
+  const int dim = 4 * (col % (D / 4)), group = a.hq / a.hkv, rr = d.row_tile * ROWS + row;
+  const bool live = rr < it.m * group;
+  const int count = live ? (int)blockIdx.x - d.first + 1 : 0;
+  // CTA first + i left its part in its second slot where the item began there, else in its first
+  const int64_t slot0 = 2 * (int64_t)d.first * ROWS + row;
+  float m = kNone, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = g; i < count; i += groups)
+    m = fmaxf(m, part_ml[slot0 + (2 * i + (i == 0)) * ROWS].x);
+#pragma unroll 8
+  for (int i = g; i < count; i += groups) {
+    const int64_t slot = slot0 + (2 * i + (i == 0)) * ROWS;
+    const float2 ml = part_ml[slot];
+    const float4 x = *reinterpret_cast<const float4*>(part_o + slot * D + dim);
+    const float f = exp2_fast(ml.x - m);
+    L = fmaf(ml.y, f, L);
+    o.x = fmaf(x.x, f, o.x);
+    o.y = fmaf(x.y, f, o.y);
+    o.z = fmaf(x.z, f, o.z);
+    o.w = fmaf(x.w, f, o.w);
+  }
+  if (groups > 1) {
+    so[threadIdx.x] = o;
+    sml[threadIdx.x] = make_float2(m, L);
+    __syncthreads();
+    if (g) return;
+    for (int i = 1; i < groups; ++i) m = fmaxf(m, sml[i * cols + threadIdx.x].x);
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    L = 0.f;
+    for (int i = 0; i < groups; ++i) {
+      const float2 ml = sml[i * cols + threadIdx.x];
+      const float4 x = so[i * cols + threadIdx.x];
       const float f = exp2_fast(ml.x - m);
       L = fmaf(ml.y, f, L);
-#pragma unroll
-      for (int j = 0; j < C; ++j) o[j] = fmaf(part_o[slot * D + 32 * j + lane], f, o[j]);
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z);
+      o.w = fmaf(x.w, f, o.w);
     }
   }
+  if (!live) return;
   const int64_t at = (it.row0 + rr / group) * a.hq + d.head * group + rr % group;
   const float inv = L > 0.f ? 1.f / L : 0.f;
-  IO* out = static_cast<IO*>(a.out) + at * D;
-#pragma unroll
-  for (int j = 0; j < C; ++j) out[32 * j + lane] = from_f32<IO>(o[j] * inv);
-  if (a.lse && lane == 0) a.lse[at] = (m + log2f(L)) * kLn2;
+  store4(static_cast<IO*>(a.out) + at * D + dim,
+         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (a.lse && dim == 0) a.lse[at] = (m + log2f(L)) * kLn2;
 }
 
 // --------------------------------------------------------------------------------- launching
@@ -604,13 +662,18 @@ cudaError_t launch(const KvArgs& a, cudaStream_t s) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(ctas, NT);
-  cfg.blockDim = dim3(256);
+  // partials of an item, if the sequences are alike: a thread takes about eight of them
+  const int64_t parts = ctas / ((int64_t)a.N * a.hkv);
+  constexpr int all_cols = S::rows * (D / 4);
+  int groups = all_cols < kJoinThreads ? kJoinThreads / all_cols : 1;
+  while (groups < 16 && 8 * groups < parts) groups *= 2;
+  cfg.gridDim = dim3(ctas, all_cols * groups / kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kv_attention_join<IO, D, NT>, a, (const float*)part_o,
-                            (const float2*)part_ml, (const Desc*)descs);
+                            (const float2*)part_ml, (const Desc*)descs, groups);
 }
 
 template <typename IO, int D, bool E4M3>
