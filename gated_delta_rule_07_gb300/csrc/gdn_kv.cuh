@@ -61,48 +61,25 @@ struct KvSpan {
   int64_t row;    // the packed row of token lo
 };
 
-// Finds slot's span; false where there is none.  One warp's lanes search together.
-__device__ __forceinline__ bool kv_span(const KvArgs& a, int64_t slot, KvSpan& s) {
-  int n = 0;
-  int64_t b, e, k;
-  if (a.cu == nullptr && a.N > 1) {  // one row a sequence, one page each
-    n = (int)slot;
-    b = n;
-    e = n + 1;
-    k = 0;
-  } else {
-    if (a.cu) {  // the largest n with cu[n] / page + 2 n <= slot: 32 probes a step
-      const int lane = threadIdx.x & 31;
-      int lo = 0, hi = a.N - 1;  // the answer is in [lo, hi]
-      while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + (lane + 1) * step;
-        bool below = false;
-        if (at <= hi) {
-          const int c = a.cu[at];
-          below = (int64_t)(c < 0 ? 0 : c) / a.page + 2 * (int64_t)at <= slot;
-        }
-        // (a table that is not sorted may send this anywhere in [0, N): it is checked below)
-        const int got = __popc(__ballot_sync(0xffffffffu, below));
-        const int next = lo + got * step;
-        hi = min(hi, next + step - 1);
-        lo = min(next, hi);
-        if (step == 1) break;
-      }
-      n = lo;
-    }
-    if (!seq_bounds(a.cu, n, a.T, a.status, b, e)) return false;
-    k = slot - (b / a.page + 2 * (int64_t)n);
-  }
+// The page's id, or -1 (and the status word set) where the block table names none of the pool.
+__device__ __forceinline__ int kv_page_id(const KvArgs& a, int n, int page_i) {
+  const int pid = a.table[(int64_t)n * a.max_pages + page_i];
+  if (pid >= 0 && pid < a.num_pages) return pid;
+  set_status(a.status, GDN_ERR_DEVICE_INPUT);
+  return -1;
+}
+
+// Sequence n's span in its k-th slot; false where it has none (or does not fit).
+__device__ __forceinline__ bool kv_span_of(const KvArgs& a, int n, int64_t b, int64_t e, int64_t p0,
+                                           int64_t k, KvSpan& s) {
   if (k < 0 || e <= b) return false;
-  const int64_t p0 = a.pos0 ? a.pos0[n] : 0, p1 = p0 + (e - b);
-  if (p0 < 0 || p1 > (int64_t)a.max_pages * a.page) {
+  const int64_t p1 = p0 + (e - b);
+  if (p0 < 0 || p1 > (int64_t)a.max_pages << a.page_shift) {
     set_status(a.status, GDN_ERR_DEVICE_INPUT);
     return false;
   }
-  const int64_t pi = p0 / a.page + k;
-  if (pi * a.page >= p1) return false;
-  const int64_t first = pi * a.page;
+  const int64_t pi = (p0 >> a.page_shift) + k, first = pi << a.page_shift;
+  if (first >= p1) return false;
   s.n = n;
   s.page_i = (int)pi;
   s.lo = (int)(p0 > first ? p0 - first : 0);
@@ -111,12 +88,73 @@ __device__ __forceinline__ bool kv_span(const KvArgs& a, int64_t slot, KvSpan& s
   return true;
 }
 
-// The page's id, or -1 (and the status word set) where the block table names none of the pool.
-__device__ __forceinline__ int kv_page_id(const KvArgs& a, int n, int page_i) {
-  const int pid = a.table[(int64_t)n * a.max_pages + page_i];
-  if (pid >= 0 && pid < a.num_pages) return pid;
-  set_status(a.status, GDN_ERR_DEVICE_INPUT);
-  return -1;
+// A CTA's span and page id (-1: nothing to do), found together by its threads.  Up to a thread a
+// sequence: each looks at its own (one step of loads, and the owner reads the block table), else a
+// search by 32 probes a step.
+struct KvFound {
+  KvSpan span;
+  int pid, owner;
+};
+__device__ __forceinline__ void kv_find(const KvArgs& a, int64_t slot, KvFound& shared) {
+  const int tid = threadIdx.x;
+  if (a.N <= (int)blockDim.x && (a.cu || a.N == 1)) {
+    if (tid == 0) {
+      shared.pid = -1;
+      shared.owner = a.N;
+    }
+    __syncthreads();
+    KvSpan s;
+    bool mine = false;
+    if (tid < a.N) {
+      const int64_t b = a.cu ? a.cu[tid] : 0, e = a.cu ? a.cu[tid + 1] : a.T;
+      const int64_t p0 = a.pos0 ? a.pos0[tid] : 0;
+      const int64_t k = slot - ((b >> a.page_shift) + 2 * (int64_t)tid);
+      if (b < 0 || e < b || e > a.T)
+        set_status(a.status, GDN_ERR_DEVICE_INPUT);
+      else
+        mine = k < (e >> a.page_shift) - (b >> a.page_shift) + 2 &&
+               kv_span_of(a, tid, b, e, p0, k, s);
+      // (of a table that does not ascend, several sequences may claim a slot: the first has it)
+      if (mine) atomicMin(&shared.owner, tid);
+    }
+    __syncthreads();
+    if (mine && shared.owner == tid) {
+      shared.span = s;
+      shared.pid = kv_page_id(a, s.n, s.page_i);
+    }
+    __syncthreads();
+    return;
+  }
+  if (tid < 32) {
+    int n = (int)slot;  // (without cu: one row a sequence, one page each)
+    int64_t b = n, e = n + 1, k = 0;
+    bool ok = true;
+    if (a.cu) {  // the largest n with cu[n] / page + 2 n <= slot is in [lo, hi]
+      int lo = 0, hi = a.N - 1;
+      while (lo < hi) {
+        const int step = (hi - lo + 31) / 32, at = lo + (tid + 1) * step;
+        bool below = false;
+        if (at <= hi) {
+          const int c = a.cu[at];
+          below = (int64_t)((c < 0 ? 0 : c) >> a.page_shift) + 2 * (int64_t)at <= slot;
+        }
+        // (a table that does not ascend may send this anywhere in [0, N): it is checked below)
+        const int next = lo + __popc(__ballot_sync(0xffffffffu, below)) * step;
+        hi = min(hi, next + step - 1);
+        lo = min(next, hi);
+      }
+      n = lo;
+      ok = seq_bounds(a.cu, n, a.T, a.status, b, e);
+      k = slot - ((b >> a.page_shift) + 2 * (int64_t)n);
+    }
+    KvSpan s;
+    ok = ok && kv_span_of(a, n, b, e, a.pos0 ? a.pos0[n] : 0, k, s);
+    if (tid == 0) {
+      shared.pid = ok ? kv_page_id(a, s.n, s.page_i) : -1;
+      if (ok) shared.span = s;
+    }
+  }
+  __syncthreads();
 }
 
 }  // namespace gdn

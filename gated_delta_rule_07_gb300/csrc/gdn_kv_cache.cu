@@ -8,8 +8,14 @@
 // starts takes its scale from its new tokens alone, whatever its last owner left.
 //
 // One CTA per (touched page, head, keys or values): it needs the page's whole amax before it can
-// write the first code, and pages are independent.  Bound by HBM for prompts (each new element
-// is read once and written as one byte), by latency for single tokens.
+// write the first code, and pages are independent.  The page's new values are read once and wait
+// in registers for the amax (the number of registers is a template parameter: page x D / 256
+// values a thread).  Keys: a thread takes 8 channels of a token (16 bytes of bf16 in, 8 out);
+// values: 4 tokens of 4 channels, one 16-byte piece of the value layout.  Heads are the fastest
+// grid index, so that CTAs running together read whole token rows.  Bound by HBM for prompts, by
+// latency for single tokens.
+#include <cuda_fp16.h>
+
 #include "gdn_kv.cuh"
 
 namespace gdn {
@@ -17,98 +23,379 @@ namespace {
 
 constexpr int kKvThreads = 256;
 
+// ------------------------------------------------------------------------- elements and codes
+
+template <typename IO> struct Quad;  // four consecutive elements as loaded
+template <> struct Quad<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void open(float* f) const {
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+  }
+};
+template <> struct Quad<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = __ldg(reinterpret_cast<const uint2*>(p));
+  }
+  __device__ __forceinline__ void clear() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void open(float* f) const {  // a bf16 is the top half of an fp32
+    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+// eight: one 16-byte load of bf16, two of fp32
 template <typename IO>
-__device__ __forceinline__ float kv_ld(const IO* p) { return to_f32(*p); }
+__device__ __forceinline__ void load8(Quad<IO>* q, const IO* p) {
+  if constexpr (sizeof(IO) == 2) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    q[0].v = make_uint2(v.x, v.y);
+    q[1].v = make_uint2(v.z, v.w);
+  } else {
+    q[0].load(p);
+    q[1].load(p + 4);
+  }
+}
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-// the byte of token t, channel d in a (page, head) block
-template <int D, bool VALUES> __device__ __forceinline__ int64_t code_at(int t, int d) {
-  return VALUES ? (int64_t)(t & ~3) * D + 4 * d + (t & 3) : (int64_t)t * D + d;
-}
-
-template <typename IO, int D, bool E4M3, bool VALUES>
-__device__ void append_block(const KvArgs& a, const KvSpan& s, int pid) {
-  __shared__ float red[kKvThreads / 32];
-  const int h = blockIdx.y, tid = threadIdx.x;
-  const int64_t block = (int64_t)pid * a.hkv + h;
-  uint8_t* codes = (VALUES ? a.v_codes : a.k_codes) + block * a.page * D;
-  float* scale = (VALUES ? a.v_scale : a.k_scale) + block;
-  const int64_t ts = VALUES ? a.v_ts : a.k_ts;
-  const IO* x = static_cast<const IO*>(VALUES ? a.v : a.k) + s.row * ts +
-                h * (VALUES ? a.v_hs : a.k_hs);
-  const int n = (s.hi - s.lo) * D;
-  float amax = 0.f;
-  bool bad = false;
-  for (int e = tid; e < n; e += kKvThreads) {
-    const float v = kv_ld(x + (e / D) * ts + e % D);
-    if (finite(v)) amax = fmaxf(amax, fabsf(v));
+// largest finite magnitude so far; `bad` where an element is not finite
+__device__ __forceinline__ void take_amax(const float* f, float& amax, bool& bad) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float m = fabsf(f[i]);
+    if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
     else bad = true;
   }
-  if (bad) set_status(a.status, GDN_ERR_DEVICE_RANGE);
+}
+
+// The codes of four elements, the first in the low byte.  `bad`: some element of the thread's is
+// not finite (those take the careful way; a NaN becomes 0, an infinity the largest code, or 0
+// where the page has no scale).
+template <bool E4M3>
+__device__ __forceinline__ uint32_t encode4(const float* f, float inv, bool bad) {
+  if (bad) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w |= kv_code<E4M3>(finite(f[i]) ? f[i] * inv : (inv > 0.f ? f[i] : 0.f)) << (8 * i);
+    return w;
+  }
+  if constexpr (E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1] * inv), "f"(f[0] * inv));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3] * inv), "f"(f[2] * inv));
+    return lo | ((uint32_t)hi << 16);
+  } else {
+    // |x inv| <= 127 (1 + 2^-22): adding 1.5 2^23 leaves the rounded integer in the low byte
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(__fadd_rn(__fmul_rn(f[i], inv), 12582912.f));
+    return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+  }
+}
+
+// four codes on a new scale
+template <bool E4M3> __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r |= kv_code<E4M3>(kv_value<E4M3>((w >> (8 * i)) & 0xffu) * ratio) << (8 * i);
+  return r;
+}
+
+// ------------------------------------------------------------------------------------- append
+
+// The page's new scale: its amax joined over the CTA, against the scale it holds.
+struct NewScale {
+  float held, now, inv;
+};
+template <bool E4M3>
+__device__ __forceinline__ NewScale new_scale(float amax, bool bad, float held, float* red,
+                                              int32_t* status) {
+  const int tid = threadIdx.x;
+  if (bad) set_status(status, GDN_ERR_DEVICE_RANGE);
 #pragma unroll
   for (int off = 16; off; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   if (tid % 32 == 0) red[tid / 32] = amax;
-  const float held = s.lo > 0 ? *scale : 0.f;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kKvThreads / 32; ++i) amax = fmaxf(amax, red[i]);
-  const float now = fmaxf(held, amax >= kKvTiny ? amax * (float)(1.0 / kv_qmax<E4M3>()) : 0.f);
-  const float inv = now > 0.f ? 1.f / now : 0.f;
-  if (now > held && held > 0.f) {  // the page's earlier codes on the new scale
-    const float ratio = held * inv;
-    for (int e = tid; e < s.lo * D; e += kKvThreads) {
-      uint8_t* c = codes + code_at<D, VALUES>(e / D, e % D);
-      *c = (uint8_t)kv_code<E4M3>(kv_value<E4M3>(*c) * ratio);
-    }
-  }
-  for (int e = tid; e < n; e += kKvThreads) {
-    const float v = kv_ld(x + (e / D) * ts + e % D);
-    const float y = finite(v) ? v * inv : (now > 0.f ? v : 0.f);
-    codes[code_at<D, VALUES>(s.lo + e / D, e % D)] = (uint8_t)kv_code<E4M3>(y);
-  }
-  if (tid == 0) *scale = now;
+  NewScale s;
+  s.held = held;
+  s.now = fmaxf(held, amax >= kKvTiny ? amax * (float)(1.0 / kv_qmax<E4M3>()) : 0.f);
+  s.inv = s.now > 0.f ? 1.f / s.now : 0.f;
+  return s;
 }
 
-template <typename IO, int D, bool E4M3>
-__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvArgs a) {
-  KvSpan s;
-  if (!kv_span(a, blockIdx.x, s)) return;
-  const int pid = kv_page_id(a, s.n, s.page_i);
-  if (pid < 0) return;
-  if (blockIdx.z) append_block<IO, D, E4M3, true>(a, s, pid);
-  else append_block<IO, D, E4M3, false>(a, s, pid);
+// keys: IT pieces of 8 channels a thread
+template <typename IO, int D, bool E4M3, int IT>
+__device__ __forceinline__ void append_keys(const KvArgs& a, const KvSpan& s, int pid, int h,
+                                            float* red) {
+  const int tid = threadIdx.x, pieces = (s.hi - s.lo) * (D / 8);
+  const int64_t block = (int64_t)pid * a.hkv + h;
+  uint8_t* codes = a.k_codes + block * a.page * D;
+  const IO* x = static_cast<const IO*>(a.k) + s.row * a.k_ts + h * a.k_hs;
+  Quad<IO> q[IT][2];
+  const float held = s.lo > 0 ? a.k_scale[block] : 0.f;
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int e = tid + i * kKvThreads;
+    q[i][0].clear();
+    q[i][1].clear();
+    if (e < pieces) load8(q[i], x + (e / (D / 8)) * a.k_ts + 8 * (e % (D / 8)));
+  }
+  float amax = 0.f, f[4];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      q[i][j].open(f);
+      take_amax(f, amax, bad);
+    }
+  const NewScale n = new_scale<E4M3>(amax, bad, held, red, a.status);
+  if (n.now > n.held && n.held > 0.f) {  // the page's earlier codes on the new scale
+    uint32_t* w = reinterpret_cast<uint32_t*>(codes);
+    for (int e = tid; e < s.lo * (D / 4); e += kKvThreads)
+      w[e] = rescale4<E4M3>(w[e], n.held * n.inv);
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int e = tid + i * kKvThreads;
+    if (e < pieces) {
+      uint2 w;
+      q[i][0].open(f);
+      w.x = encode4<E4M3>(f, n.inv, bad);
+      q[i][1].open(f);
+      w.y = encode4<E4M3>(f, n.inv, bad);
+      *reinterpret_cast<uint2*>(codes + s.lo * D + 8 * e) = w;
+    }
+  }
+  if (tid == 0) a.k_scale[block] = n.now;
 }
+
+// values: IT pieces of 4 tokens x 4 channels a thread (a piece at an end of the span may hold
+// earlier tokens' codes, or none yet)
+template <typename IO, int D, bool E4M3, int IT>
+__device__ __forceinline__ void append_values(const KvArgs& a, const KvSpan& s, int pid, int h,
+                                              float* red) {
+  const int tid = threadIdx.x, g0 = s.lo / 4;
+  const int pieces = ((s.hi + 3) / 4 - g0) * (D / 4);
+  const int64_t block = (int64_t)pid * a.hkv + h;
+  uint8_t* codes = a.v_codes + block * a.page * D;
+  const IO* x = static_cast<const IO*>(a.v) + s.row * a.v_ts + h * a.v_hs;
+  Quad<IO> q[IT][4];
+  uint4 old = make_uint4(0u, 0u, 0u, 0u);  // codes beside the new ones in the first piece
+  const float held = s.lo > 0 ? a.v_scale[block] : 0.f;
+  if (s.lo % 4 && tid < D / 4)
+    old = *reinterpret_cast<const uint4*>(codes + (int64_t)g0 * 4 * D + 16 * tid);
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int e = tid + i * kKvThreads, t0 = 4 * (g0 + e / (D / 4)), d = 4 * (e % (D / 4));
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      q[i][t].clear();
+      if (e < pieces && t0 + t >= s.lo && t0 + t < s.hi)
+        q[i][t].load(x + (t0 + t - s.lo) * a.v_ts + d);
+    }
+  }
+  float amax = 0.f, f[4];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < IT; ++i)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      q[i][t].open(f);
+      take_amax(f, amax, bad);
+    }
+  const NewScale n = new_scale<E4M3>(amax, bad, held, red, a.status);
+  const bool grew = n.now > n.held && n.held > 0.f;
+  if (grew) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(codes);
+    for (int e = tid; e < g0 * D; e += kKvThreads) w[e] = rescale4<E4M3>(w[e], n.held * n.inv);
+  }
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int e = tid + i * kKvThreads;
+    if (e < pieces) {
+      uint32_t w[4], o[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {  // w[t]: token t's codes of the four channels
+        q[i][t].open(f);
+        w[t] = encode4<E4M3>(f, n.inv, bad);
+      }
+      // transpose 4 x 4 bytes: a word of four tokens for each channel
+      const uint32_t a01 = __byte_perm(w[0], w[1], 0x5140), b01 = __byte_perm(w[0], w[1], 0x7362);
+      const uint32_t a23 = __byte_perm(w[2], w[3], 0x5140), b23 = __byte_perm(w[2], w[3], 0x7362);
+      o[0] = __byte_perm(a01, a23, 0x5410);
+      o[1] = __byte_perm(a01, a23, 0x7632);
+      o[2] = __byte_perm(b01, b23, 0x5410);
+      o[3] = __byte_perm(b01, b23, 0x7632);
+      if (i == 0 && s.lo % 4 && tid < D / 4) {  // earlier tokens in the first piece
+        const uint32_t keep = (1u << (8 * (s.lo % 4))) - 1u;
+        const uint32_t was[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          o[c] = (o[c] & ~keep) |
+                 ((grew ? rescale4<E4M3>(was[c], n.held * n.inv) : was[c]) & keep);
+      }
+      *reinterpret_cast<uint4*>(codes + (int64_t)g0 * 4 * D + 16 * e) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if (tid == 0) a.v_scale[block] = n.now;
+}
+
+// IT: pages of at most 4096 IT new values
+template <typename IO, int D, bool E4M3, int IT>
+__global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvArgs a) {
+  __shared__ KvFound found;
+  __shared__ float red[kKvThreads / 32];
+  const int which = blockIdx.x % (2 * a.hkv);
+  kv_find(a, blockIdx.x / (2 * a.hkv), found);
+  if (found.pid < 0) return;
+  const KvSpan s = found.span;
+  if (which & 1) append_values<IO, D, E4M3, IT>(a, s, found.pid, which / 2, red);
+  else append_keys<IO, D, E4M3, 2 * IT>(a, s, found.pid, which / 2, red);
+}
+
+// --------------------------------------------------------------------------------------- read
+
+// four values of a word's codes
+template <bool E4M3>
+__device__ __forceinline__ void decode4(uint32_t w, float scale, float* f) {
+  if constexpr (E4M3) {  // (kv_value's bits for two codes at a time)
+    const uint32_t x = __byte_perm(w, 0, 0x1404), y = __byte_perm(w, 0, 0x3424);
+    const uint32_t lo = (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u);
+    const uint32_t hi = (y & 0x80008000u) | ((y >> 1) & 0x3f803f80u);
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    f[0] = p.x * 256.f * scale; f[1] = p.y * 256.f * scale;
+    f[2] = q.x * 256.f * scale; f[3] = q.y * 256.f * scale;
+  } else {  // 2^23 + (code + 128) in an fp32's mantissa
+    const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)) - 8388736.f) * scale;
+  }
+}
+__device__ __forceinline__ void put4(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ uint2 bf16x4(const float* f) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const float* f) {
+  *reinterpret_cast<uint2*>(p) = bf16x4(f);
+}
+
+constexpr int kReadUnroll = 4;  // loads a thread has in flight
 
 template <typename IO, int D, bool E4M3>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvArgs a) {
-  KvSpan s;
-  if (!kv_span(a, blockIdx.x, s)) return;
-  const int pid = kv_page_id(a, s.n, s.page_i);
-  if (pid < 0) return;
-  const int h = blockIdx.y;
-  const int64_t block = (int64_t)pid * a.hkv + h;
-  const bool values = blockIdx.z;
-  const uint8_t* codes = (values ? a.v_codes : a.k_codes) + block * a.page * D;
-  const float scale = (values ? a.v_scale : a.k_scale)[block];
-  IO* out = static_cast<IO*>(values ? a.v_out : a.k_out) + (s.row * a.hkv + h) * D;
-  for (int e = threadIdx.x; e < (s.hi - s.lo) * D; e += kKvThreads) {
-    const int t = s.lo + e / D, d = e % D;
-    const uint32_t c = codes[values ? code_at<D, true>(t, d) : code_at<D, false>(t, d)];
-    out[(int64_t)(e / D) * a.hkv * D + d] = from_f32<IO>(kv_value<E4M3>(c) * scale);
+  __shared__ KvFound found;
+  const int which = blockIdx.x % (2 * a.hkv), h = which / 2, tid = threadIdx.x;
+  kv_find(a, blockIdx.x / (2 * a.hkv), found);
+  if (found.pid < 0) return;
+  const KvSpan s = found.span;
+  const int64_t block = (int64_t)found.pid * a.hkv + h;
+  const int64_t ts = (int64_t)a.hkv * D;
+  if (which & 1) {  // values: 4 tokens x 4 channels
+    const uint8_t* codes = a.v_codes + block * a.page * D;
+    const float scale = a.v_scale[block];
+    const int g0 = s.lo / 4, pieces = ((s.hi + 3) / 4 - g0) * (D / 4);
+    IO* out = static_cast<IO*>(a.v_out) + (s.row * a.hkv + h) * D;
+    for (int e0 = tid; e0 < pieces; e0 += kReadUnroll * kKvThreads) {
+      uint4 w[kReadUnroll];
+#pragma unroll
+      for (int i = 0; i < kReadUnroll; ++i) {
+        const int e = e0 + i * kKvThreads;
+        if (e < pieces)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(codes + (int64_t)g0 * 4 * D + 16 * e));
+      }
+#pragma unroll
+      for (int i = 0; i < kReadUnroll; ++i) {
+        const int e = e0 + i * kKvThreads;
+        if (e >= pieces) break;
+        const int t0 = 4 * (g0 + e / (D / 4)), d = 4 * (e % (D / 4));
+        float f[4][4];
+        decode4<E4M3>(w[i].x, scale, f[0]);
+        decode4<E4M3>(w[i].y, scale, f[1]);
+        decode4<E4M3>(w[i].z, scale, f[2]);
+        decode4<E4M3>(w[i].w, scale, f[3]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (t0 + t >= s.lo && t0 + t < s.hi) {
+            const float g[4] = {f[0][t], f[1][t], f[2][t], f[3][t]};
+            put4(out + (t0 + t - s.lo) * ts + d, g);
+          }
+      }
+    }
+  } else {  // keys: 16 bytes of output a thread
+    constexpr int E = 16 / sizeof(IO);
+    const uint8_t* codes = a.k_codes + block * a.page * D + s.lo * D;
+    const float scale = a.k_scale[block];
+    const int pieces = (s.hi - s.lo) * (D / E);
+    IO* out = static_cast<IO*>(a.k_out) + (s.row * a.hkv + h) * D;
+    for (int e0 = tid; e0 < pieces; e0 += kReadUnroll * kKvThreads) {
+      uint32_t w[kReadUnroll][E / 4];
+#pragma unroll
+      for (int i = 0; i < kReadUnroll; ++i) {
+        const int e = e0 + i * kKvThreads;
+        if (e < pieces) {
+          if constexpr (E == 8) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(codes + E * e));
+            w[i][0] = v.x;
+            w[i][1] = v.y;
+          } else {
+            w[i][0] = __ldg(reinterpret_cast<const uint32_t*>(codes + E * e));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kReadUnroll; ++i) {
+        const int e = e0 + i * kKvThreads;
+        if (e >= pieces) break;
+        IO* dst = out + (e / (D / E)) * ts + E * (e % (D / E));
+        float f[4];
+        decode4<E4M3>(w[i][0], scale, f);
+        if constexpr (E == 8) {
+          const uint2 x = bf16x4(f);
+          decode4<E4M3>(w[i][1], scale, f);
+          const uint2 y = bf16x4(f);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(x.x, x.y, y.x, y.y);
+        } else {
+          put4(dst, f);
+        }
+      }
+    }
   }
 }
 
-template <typename IO, int D>
+// ---------------------------------------------------------------------------------- launching
+
+template <typename IO, int D, bool E4M3>
 cudaError_t launch_kv(const KvArgs& a, bool append, cudaStream_t s) {
-  const int64_t slots = a.cu == nullptr && a.N > 1 ? a.N : a.T / a.page + 2 * (int64_t)a.N;
-  const dim3 grid((unsigned)slots, (unsigned)a.hkv, 2);
-  if (append) {
-    if (a.e4m3) kv_append_kernel<IO, D, true><<<grid, kKvThreads, 0, s>>>(a);
-    else kv_append_kernel<IO, D, false><<<grid, kKvThreads, 0, s>>>(a);
+  const int64_t slots =
+      a.cu == nullptr && a.N > 1 ? a.N : (a.T >> a.page_shift) + 2 * (int64_t)a.N;
+  const int64_t ctas = slots * 2 * a.hkv;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)ctas;
+  // registers for the values that a page can add: one row a sequence needs one piece
+  const int values = a.cu == nullptr && a.N > 1 ? D : a.page * D;
+  if (!append) {
+    kv_read_kernel<IO, D, E4M3><<<grid, kKvThreads, 0, s>>>(a);
+  } else if (values <= 4096) {
+    kv_append_kernel<IO, D, E4M3, 1><<<grid, kKvThreads, 0, s>>>(a);
+  } else if (values <= 8192) {
+    kv_append_kernel<IO, D, E4M3, 2><<<grid, kKvThreads, 0, s>>>(a);
+  } else if (values <= 16384) {  // (pages of 128 tokens at most: D / 32 pieces)
+    if constexpr (D >= 128) kv_append_kernel<IO, D, E4M3, 4><<<grid, kKvThreads, 0, s>>>(a);
   } else {
-    if (a.e4m3) kv_read_kernel<IO, D, true><<<grid, kKvThreads, 0, s>>>(a);
-    else kv_read_kernel<IO, D, false><<<grid, kKvThreads, 0, s>>>(a);
+    if constexpr (D >= 256) kv_append_kernel<IO, D, E4M3, 8><<<grid, kKvThreads, 0, s>>>(a);
   }
   return cudaGetLastError();
 }
@@ -116,9 +403,9 @@ cudaError_t launch_kv(const KvArgs& a, bool append, cudaStream_t s) {
 template <typename IO>
 cudaError_t launch_kv_io(const KvArgs& a, bool append, cudaStream_t s) {
   switch (a.D) {
-    case 64: return launch_kv<IO, 64>(a, append, s);
-    case 128: return launch_kv<IO, 128>(a, append, s);
-    default: return launch_kv<IO, 256>(a, append, s);
+    case 64: return a.e4m3 ? launch_kv<IO, 64, true>(a, append, s) : launch_kv<IO, 64, false>(a, append, s);
+    case 128: return a.e4m3 ? launch_kv<IO, 128, true>(a, append, s) : launch_kv<IO, 128, false>(a, append, s);
+    default: return a.e4m3 ? launch_kv<IO, 256, true>(a, append, s) : launch_kv<IO, 256, false>(a, append, s);
   }
 }
 

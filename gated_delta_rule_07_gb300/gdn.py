@@ -168,8 +168,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # (what torch.cuda.current_stream().cuda_stream gives, without its object)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -386,100 +386,105 @@ def gdn_device_status(status_word, reset=True, stream=None) -> int:
 
 
 # ------------------------------------------------- softmax-attention layers' operators
+#
+# These calls are short on the GPU (a decode step's take a few microseconds), so the host's part
+# is kept lean: each tensor is looked at once, in the order that costs least, and messages are
+# only built for a refusal.
 
 _IO = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _ROPE_STYLES = {"half": 0, "pairs": 1}
 _GDN_ERR_INVALID_ARGUMENT, _GDN_ERR_UNSUPPORTED = 1, 2
+_F32, _I32 = torch.float32, torch.int32
 
 
 def _refuse(where, why, status=_GDN_ERR_INVALID_ARGUMENT):
     raise GdnError(status, f"{where}: {why}")
 
 
-def _io_of(where, *tensors):
-    dtype = tensors[0].dtype
-    io = _IO.get(dtype)
+def _io_of(where, t):
+    io = _IO.get(t.dtype)
     if io is None:
-        _refuse(where, f"dtype {dtype}", _GDN_ERR_UNSUPPORTED)
-    for t in tensors:
-        if t.dtype is not dtype:
-            _refuse(where, f"dtypes {dtype} and {t.dtype} in one call")
+        _refuse(where, f"dtype {t.dtype}", _GDN_ERR_UNSUPPORTED)
     return io
 
 
-def _packed(where, shape, dtype, **tensors):
-    """Contiguous tensors of one shape and dtype."""
-    for name, t in tensors.items():
-        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
-            _refuse(where, f"{name} is to be a contiguous {dtype} tensor {tuple(shape)}, got "
-                           f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+def _packed(where, name, t, shape, dtype):
+    """t is a contiguous GPU tensor of this shape and dtype."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
+        _refuse(where, f"{name} is to be a contiguous {dtype} tensor {tuple(shape)} on the GPU, "
+                       f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
 
-def _rows(where, name, t):
-    """Token and head stride of a [T, heads, D] tensor whose last dimension is contiguous."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        _refuse(where, f"{name} is to be [tokens, heads, D] with a contiguous last dimension")
-    return t.stride(0), t.stride(1)
-
-
-def _on_gpu(where, *tensors):
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            _refuse(where, "a tensor is not on the GPU")
+def _rows(where, name, t, dtype):
+    """Shape, token and head stride of a [T, heads, D] GPU tensor whose last dimension is
+    contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
+        _refuse(where, f"{name} is to be [tokens, heads, D] with a contiguous last dimension, "
+                       f"got {tuple(shape)} with strides {stride}")
+    if t.dtype is not dtype:
+        _refuse(where, f"{name} is {t.dtype}, the call's dtype is {dtype}")
+    if not t.is_cuda:
+        _refuse(where, f"{name} is not on the GPU")
+    return shape, stride[0], stride[1]
 
 
 def _hold(stream, *tensors):
     """Temporaries and outputs allocated on the current stream and used on `stream`: their memory
     is not handed out again before the work on `stream` is done."""
-    if stream is not None and hasattr(stream, "cuda_stream"):
+    if hasattr(stream, "cuda_stream"):
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
 
 
-def _status_word(check_status, device):
-    return torch.zeros(1, dtype=torch.int32, device=device) if check_status else None
+def _opt(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, style):
-    io = _io_of(where, q, k)
-    qs, ks = _rows(where, "q", q), _rows(where, "k", k)
-    T, hq, D = q.shape
-    if k.shape[0] != T or k.shape[2] != D:
-        _refuse(where, f"q {tuple(q.shape)} and k {tuple(k.shape)} do not go together")
-    _packed(where, (T,), torch.int32, positions=positions)
-    if cos_sin.dim() != 2:
+    io, dtype = _io_of(where, q), q.dtype
+    (T, hq, D), qt, qh = _rows(where, "q", q, dtype)
+    kshape, kt, kh = _rows(where, "k", k, dtype)
+    if kshape[0] != T or kshape[2] != D:
+        _refuse(where, f"q {tuple(q.shape)} and k {tuple(kshape)} do not go together")
+    _packed(where, "positions", positions, (T,), _I32)
+    tshape = cos_sin.shape
+    if len(tshape) != 2:
         _refuse(where, "cos_sin is to be [positions, R]")
-    _packed(where, cos_sin.shape, torch.float32, cos_sin=cos_sin)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _packed(where, (D,), torch.float32, **{name: w})
-    if style not in _ROPE_STYLES:
+    _packed(where, "cos_sin", cos_sin, tshape, _F32)
+    if q_weight is not None:
+        _packed(where, "q_weight", q_weight, (D,), _F32)
+    if k_weight is not None:
+        _packed(where, "k_weight", k_weight, (D,), _F32)
+    which = _ROPE_STYLES.get(style)
+    if which is None:
         _refuse(where, f"style {style!r}")
-    _on_gpu(where, q, k, positions, cos_sin, q_weight, k_weight)
-    return QkRopeProblem(T, hq, k.shape[1], D, cos_sin.shape[1], _ROPE_STYLES[style], io,
-                         cos_sin.shape[0], eps, weight_offset, *qs, *ks)
+    return QkRopeProblem(T, hq, kshape[1], D, tshape[1], which, io, tshape[0], eps,
+                         weight_offset, qt, qh, kt, kh)
 
 
 def gdn_qk_norm_rope(p, q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out,
                      dev_status=None, stream=None):
-    _check(_lib.gdn_qk_norm_rope(p, _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin),
-                                 _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out),
-                                 _ptr(dev_status), _stream(stream)), "gdn_qk_norm_rope")
+    _check(_lib.gdn_qk_norm_rope(p, q.data_ptr(), k.data_ptr(), positions.data_ptr(),
+                                 cos_sin.data_ptr(), _opt(q_weight), _opt(k_weight),
+                                 q_out.data_ptr(), k_out.data_ptr(), _opt(dev_status),
+                                 _stream(stream)), "gdn_qk_norm_rope")
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6,
                  weight_offset=0.0, style="half", check_status=False, stream=None):
     """Queries [T, hq, D] and keys [T, hkv, D], normalised per head and rotated by position (see
     include/gdn.h); q and k may be slices of one projection.  Returns contiguous tensors."""
-    where = "qk_norm_rope"
-    p = _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset,
-                      style)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    st = _status_word(check_status, q.device)
-    _hold(stream, q_out, k_out, st)
+    p = _rope_problem("qk_norm_rope", q, k, positions, cos_sin, q_weight, k_weight, eps,
+                      weight_offset, style)
+    device, dtype = q.device, q.dtype
+    q_out = torch.empty(q.shape, dtype=dtype, device=device)
+    k_out = torch.empty(k.shape, dtype=dtype, device=device)
+    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
+    if stream is not None:
+        _hold(stream, q_out, k_out, st)
     gdn_qk_norm_rope(p, q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out, st, stream)
     if check_status:
         _check(gdn_device_status(st, True, stream), "qk_norm_rope (device status)")
@@ -487,7 +492,7 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-
 
 
 def gdn_qk_norm_rope_backward_workspace_size(p) -> int:
-    return int(_lib.gdn_qk_norm_rope_backward_workspace_size(p))
+    return _lib.gdn_qk_norm_rope_backward_workspace_size(p)
 
 
 def gdn_qk_norm_rope_backward(p, q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
@@ -495,10 +500,10 @@ def gdn_qk_norm_rope_backward(p, q, k, positions, cos_sin, q_weight, k_weight, d
                               dev_status=None, stream=None):
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
     _check(_lib.gdn_qk_norm_rope_backward(
-        p, _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin), _ptr(q_weight), _ptr(k_weight),
-        _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight),
-        _ptr(workspace), int(ws_bytes), _ptr(dev_status), _stream(stream)),
-        "gdn_qk_norm_rope_backward")
+        p, q.data_ptr(), k.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), _opt(q_weight),
+        _opt(k_weight), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+        dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), ws_bytes,
+        _opt(dev_status), _stream(stream)), "gdn_qk_norm_rope_backward")
 
 
 def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out, eps=1e-6,
@@ -509,21 +514,23 @@ def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, 
     where = "qk_norm_rope_backward"
     p = _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset,
                       style)
-    _packed(where, q.shape, q.dtype, dq_out=dq_out)
-    _packed(where, k.shape, k.dtype, dk_out=dk_out)
-    _on_gpu(where, dq_out, dk_out)
+    device, D = q.device, p.head_dim
+    _packed(where, "dq_out", dq_out, q.shape, q.dtype)
+    _packed(where, "dk_out", dk_out, k.shape, q.dtype)
     dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
-    dw = torch.empty(2, q.shape[2], dtype=torch.float32, device=q.device)
+    dqw = torch.empty(D, dtype=_F32, device=device)
+    dkw = torch.empty(D, dtype=_F32, device=device)
     if workspace is None:
-        workspace = torch.empty(max(gdn_qk_norm_rope_backward_workspace_size(p), 256),
-                                dtype=torch.uint8, device=q.device)
-    st = _status_word(check_status, q.device)
-    _hold(stream, dq, dk, dw, workspace, st)
+        workspace = torch.empty(gdn_qk_norm_rope_backward_workspace_size(p), dtype=torch.uint8,
+                                device=device)
+    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
+    if stream is not None:
+        _hold(stream, dq, dk, dqw, dkw, workspace, st)
     gdn_qk_norm_rope_backward(p, q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
-                              dq, dk, dw[0], dw[1], workspace, None, st, stream)
+                              dq, dk, dqw, dkw, workspace, None, st, stream)
     if check_status:
         _check(gdn_device_status(st, True, stream), "qk_norm_rope_backward (device status)")
-    return dq, dk, dw[0], dw[1]
+    return dq, dk, dqw, dkw
 
 
 class KVCache:
@@ -538,11 +545,12 @@ class KVCache:
         if k.dim() != 4:
             _refuse(where, "k is to be [pages, hkv, page, D]")
         pages, hkv, page, D = k.shape
-        _packed(where, k.shape, k.dtype, k=k)
-        _packed(where, (pages, hkv, page // 4, D, 4), k.dtype, v=v)
-        _packed(where, (pages, hkv), torch.float32, k_scale=k_scale, v_scale=v_scale)
-        _on_gpu(where, k, v, k_scale, v_scale)
+        _packed(where, "k", k, k.shape, k.dtype)
+        _packed(where, "v", v, (pages, hkv, page // 4, D, 4), k.dtype)
+        _packed(where, "k_scale", k_scale, (pages, hkv), _F32)
+        _packed(where, "v_scale", v_scale, (pages, hkv), _F32)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.heads, self.head_dim = hkv, D
         self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                 v_scale.data_ptr(), pages, page, hkv, D, _KV_FORMATS[k.dtype])
 
@@ -551,39 +559,31 @@ class KVCache:
         """A cache of `pages` pages; nothing in it is initialised, or needs to be."""
         return cls(torch.empty(pages, hkv, page, D, dtype=dtype, device=device),
                    torch.empty(pages, hkv, page // 4, D, 4, dtype=dtype, device=device),
-                   torch.empty(pages, hkv, dtype=torch.float32, device=device),
-                   torch.empty(pages, hkv, dtype=torch.float32, device=device))
+                   torch.empty(pages, hkv, dtype=_F32, device=device),
+                   torch.empty(pages, hkv, dtype=_F32, device=device))
 
 
-def _kv_sequences(where, cache, T, block_table, lens, cu_seqlens):
-    """Checks the tables of a cache call; the number of sequences and pages a table row."""
-    if block_table.dim() != 2:
+def _kv_sequences(where, T, block_table, lens, cu_seqlens):
+    """Checks the tables of a cache call; the number of sequences and of pages in a table row."""
+    shape = block_table.shape
+    if len(shape) != 2:
         _refuse(where, "block_table is to be [sequences, pages]")
-    N, max_pages = block_table.shape
-    _packed(where, block_table.shape, torch.int32, block_table=block_table)
+    _packed(where, "block_table", block_table, shape, _I32)
+    N = shape[0]
     if lens is not None:
-        _packed(where, (N,), torch.int32, lengths=lens)
+        _packed(where, "lengths", lens, (N,), _I32)
     if cu_seqlens is not None:
-        _packed(where, (N + 1,), torch.int32, cu_seqlens=cu_seqlens)
+        _packed(where, "cu_seqlens", cu_seqlens, (N + 1,), _I32)
     elif N != 1 and N != T:
         _refuse(where, f"{T} rows of {N} sequences need cu_seqlens")
-    _on_gpu(where, block_table, lens, cu_seqlens)
-    return N, max_pages
-
-
-def _kv_heads(where, cache, **tensors):
-    d = cache.desc
-    for name, t in tensors.items():
-        if t.shape[1] != d.hkv or t.shape[2] != d.head_dim:
-            _refuse(where, f"{name} {tuple(t.shape)} for a cache of {d.hkv} heads of "
-                           f"{d.head_dim}")
+    return N, shape[1]
 
 
 def gdn_kv_append(cache, p, k, v, block_table, ctx_lens, cu_seqlens, dev_status=None,
                   stream=None):
-    _check(_lib.gdn_kv_append(cache, p, _ptr(k), _ptr(v), _ptr(block_table), _ptr(ctx_lens),
-                              _ptr(cu_seqlens), _ptr(dev_status), _stream(stream)),
-           "gdn_kv_append")
+    _check(_lib.gdn_kv_append(cache, p, k.data_ptr(), v.data_ptr(), block_table.data_ptr(),
+                              ctx_lens.data_ptr(), _opt(cu_seqlens), _opt(dev_status),
+                              _stream(stream)), "gdn_kv_append")
 
 
 def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=False,
@@ -592,16 +592,18 @@ def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=
     tokens that each sequence already holds.  Without cu_seqlens the rows are one sequence's, or
     one row each of T sequences."""
     where = "kv_append"
-    io = _io_of(where, k, v)
-    ks, vs = _rows(where, "k", k), _rows(where, "v", v)
-    if v.shape[0] != k.shape[0]:
-        _refuse(where, f"k {tuple(k.shape)} and v {tuple(v.shape)} do not go together")
-    _kv_heads(where, cache, k=k, v=v)
-    _on_gpu(where, k, v)
-    N, max_pages = _kv_sequences(where, cache, k.shape[0], block_table, ctx_lens, cu_seqlens)
-    p = KvProblem(k.shape[0], N, max_pages, 0, io, *ks, *vs, 0, 0)
-    st = _status_word(check_status, k.device)
-    _hold(stream, st)
+    io, dtype = _io_of(where, k), k.dtype
+    shape, kt, kh = _rows(where, "k", k, dtype)
+    vshape, vt, vh = _rows(where, "v", v, dtype)
+    T, h, D = shape
+    if vshape != shape or h != cache.heads or D != cache.head_dim:
+        _refuse(where, f"k {tuple(shape)} and v {tuple(vshape)} for a cache of {cache.heads} "
+                       f"heads of {cache.head_dim}")
+    N, max_pages = _kv_sequences(where, T, block_table, ctx_lens, cu_seqlens)
+    p = KvProblem(T, N, max_pages, 0, io, kt, kh, vt, vh, 0, 0)
+    st = torch.zeros(1, dtype=_I32, device=k.device) if check_status else None
+    if stream is not None:
+        _hold(stream, st)
     gdn_kv_append(cache.desc, p, k, v, block_table, ctx_lens, cu_seqlens, st, stream)
     if check_status:
         _check(gdn_device_status(st, True, stream), "kv_append (device status)")
@@ -609,9 +611,9 @@ def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=
 
 def gdn_kv_read(cache, p, block_table, start, cu_seqlens, k_out, v_out, dev_status=None,
                 stream=None):
-    _check(_lib.gdn_kv_read(cache, p, _ptr(block_table), _ptr(start), _ptr(cu_seqlens),
-                            _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream)),
-           "gdn_kv_read")
+    _check(_lib.gdn_kv_read(cache, p, block_table.data_ptr(), _opt(start), _opt(cu_seqlens),
+                            k_out.data_ptr(), v_out.data_ptr(), _opt(dev_status),
+                            _stream(stream)), "gdn_kv_read")
 
 
 def kv_read(cache, block_table, start, cu_seqlens, tokens, dtype=torch.bfloat16,
@@ -619,34 +621,34 @@ def kv_read(cache, block_table, start, cu_seqlens, tokens, dtype=torch.bfloat16,
     """Keys and values [tokens, hkv, D] of the positions start[n] onward (None: from 0) of each
     sequence, cu_seqlens[n + 1] - cu_seqlens[n] of them, read back from the cache."""
     where = "kv_read"
-    if dtype not in _IO:
+    io = _IO.get(dtype)
+    if io is None:
         _refuse(where, f"dtype {dtype}", _GDN_ERR_UNSUPPORTED)
-    N, max_pages = _kv_sequences(where, cache, tokens, block_table, start, cu_seqlens)
-    d = cache.desc
-    shape = (tokens, d.hkv, d.head_dim)
-    k = torch.empty(shape, dtype=dtype, device=block_table.device)
-    v = torch.empty(shape, dtype=dtype, device=block_table.device)
-    p = KvProblem(tokens, N, max_pages, 0, _IO[dtype], 0, 0, 0, 0, 0, 0)
-    st = _status_word(check_status, block_table.device)
-    _hold(stream, k, v, st)
-    gdn_kv_read(d, p, block_table, start, cu_seqlens, k, v, st, stream)
+    N, max_pages = _kv_sequences(where, tokens, block_table, start, cu_seqlens)
+    shape, device = (tokens, cache.heads, cache.head_dim), block_table.device
+    k = torch.empty(shape, dtype=dtype, device=device)
+    v = torch.empty(shape, dtype=dtype, device=device)
+    p = KvProblem(tokens, N, max_pages, 0, io, 0, 0, 0, 0, 0, 0)
+    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
+    if stream is not None:
+        _hold(stream, k, v, st)
+    gdn_kv_read(cache.desc, p, block_table, start, cu_seqlens, k, v, st, stream)
     if check_status:
         _check(gdn_device_status(st, True, stream), "kv_read (device status)")
     return k, v
 
 
 def gdn_kv_attention_workspace_size(cache, p) -> int:
-    return int(_lib.gdn_kv_attention_workspace_size(cache, p))
+    return _lib.gdn_kv_attention_workspace_size(cache, p)
 
 
 def gdn_kv_attention(cache, p, q, block_table, kv_lens, cu_seqlens, scale, window, out, lse,
                      workspace, ws_bytes=None, dev_status=None, stream=None):
-    if ws_bytes is None:
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(_lib.gdn_kv_attention(cache, p, _ptr(q), _ptr(block_table), _ptr(kv_lens),
-                                 _ptr(cu_seqlens), scale, window, _ptr(out), _ptr(lse),
-                                 _ptr(workspace), int(ws_bytes), _ptr(dev_status),
-                                 _stream(stream)), "gdn_kv_attention")
+    ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.gdn_kv_attention(cache, p, q.data_ptr(), block_table.data_ptr(),
+                                 kv_lens.data_ptr(), _opt(cu_seqlens), scale, window,
+                                 out.data_ptr(), _opt(lse), workspace.data_ptr(), ws_bytes,
+                                 _opt(dev_status), _stream(stream)), "gdn_kv_attention")
 
 
 def kv_attention(cache, q, block_table, kv_lens, cu_seqlens=None, scale=None, window=0,
@@ -655,22 +657,21 @@ def kv_attention(cache, q, block_table, kv_lens, cu_seqlens=None, scale=None, wi
     cache's kv_lens[n] tokens (which include them); scale defaults to 1 / sqrt(D).  Without
     cu_seqlens the rows are one sequence's, or one row each of T sequences."""
     where = "kv_attention"
-    io = _io_of(where, q)
-    qs = _rows(where, "q", q)
-    T, hq, D = q.shape
-    if D != cache.desc.head_dim:
-        _refuse(where, f"q {tuple(q.shape)} for a cache of heads of {cache.desc.head_dim}")
-    _on_gpu(where, q)
-    N, max_pages = _kv_sequences(where, cache, T, block_table, kv_lens, cu_seqlens)
-    p = KvProblem(T, N, max_pages, hq, io, 0, 0, 0, 0, *qs)
-    out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+    io, dtype, device = _io_of(where, q), q.dtype, q.device
+    shape, qt, qh = _rows(where, "q", q, dtype)
+    T, hq, D = shape
+    if D != cache.head_dim:
+        _refuse(where, f"q {tuple(shape)} for a cache of heads of {cache.head_dim}")
+    N, max_pages = _kv_sequences(where, T, block_table, kv_lens, cu_seqlens)
+    p = KvProblem(T, N, max_pages, hq, io, 0, 0, 0, 0, qt, qh)
+    out = torch.empty(shape, dtype=dtype, device=device)
+    lse = torch.empty((T, hq), dtype=_F32, device=device)
     if workspace is None:
-        need = gdn_kv_attention_workspace_size(cache.desc, p)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    st = _status_word(check_status, q.device)
-    _hold(stream, out, lse, workspace, st)
+        workspace = torch.empty(gdn_kv_attention_workspace_size(cache.desc, p),
+                                dtype=torch.uint8, device=device)
+    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
+    if stream is not None:
+        _hold(stream, out, lse, workspace, st)
     gdn_kv_attention(cache.desc, p, q, block_table, kv_lens, cu_seqlens,
                      D ** -0.5 if scale is None else scale, window, out, lse, workspace, None,
                      st, stream)
