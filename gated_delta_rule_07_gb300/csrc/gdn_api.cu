@@ -694,7 +694,7 @@ gdn_status gdn_qk_norm_rope(const gdn_qk_rope_problem* p, const void* q, const v
 }
 
 size_t gdn_qk_norm_rope_backward_workspace_size(const gdn_qk_rope_problem* p) {
-  return check_rope(p) != GDN_OK ? 0 : (size_t)gdn::kRopeCtas * 2 * p->head_dim * sizeof(float);
+  return check_rope(p) != GDN_OK ? 0 : (size_t)gdn::kRopeCtas * p->head_dim * sizeof(float);
 }
 
 gdn_status gdn_qk_norm_rope_backward(const gdn_qk_rope_problem* p, const void* q, const void* k,

@@ -12,7 +12,7 @@ namespace gdn {
 
 // Query/key norms and rotation, forward and gradients (gdn_qk_norm_rope and its backward).
 // Row strides are in elements; outputs and output gradients are contiguous.
-constexpr int kRopeCtas = 608;  // CTAs of the gradient kernel at most: its partial weight sums
+constexpr int kRopeCtas = 456;  // CTAs of the gradient kernel at most, one partial weight sum each
 struct QkRopeArgs {
   int64_t T, q_ts, q_hs, k_ts, k_hs;
   int hq, hkv, D, R, max_pos;
@@ -22,7 +22,7 @@ struct QkRopeArgs {
   const int32_t* pos;
   const float *table, *wq, *wk;
   void *q_out, *k_out, *dq, *dk;
-  float *dwq, *dwk, *partial;  // partial [CTAs, 2, D]
+  float *dwq, *dwk, *partial;  // partial [CTAs, D]: query rows' CTAs first
   int32_t* status;
 };
 cudaError_t qk_rope(const QkRopeArgs& a, bool backward, cudaStream_t s);

@@ -10,9 +10,10 @@
 //     dw_d = sum over rows of dy_d n_d,   dn = dy (w + offset),   dx = r (dn - n mean(dn n)).
 //
 // Bound by HBM: every element is read once and written once (the gradient reads two and writes
-// one).  A row is held by D / 8 lanes, eight consecutive elements each (16 bytes of bf16), so a
-// row's mean is a shuffle over those lanes and its rotation partner's elements are one lane's
-// registers away; nothing goes through shared memory.  Statistics are fp32.
+// one).  A row is held by D / 8 lanes, two groups of four elements each: the two halves of four
+// pairs ("half": d = 4 l and R/2 + 4 l; eight neighbours for "pairs" and past R), so that a pair
+// is within one lane, a row's mean is a shuffle over its lanes, and nothing goes through shared
+// memory.  Statistics are fp32.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -26,115 +27,98 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kVec = 8;  // elements a lane holds of a row
 
-// eight elements as loaded
-template <typename IO> struct Pack8;
-template <> struct Pack8<__nv_bfloat16> { uint4 u; };
-template <> struct Pack8<float> { float4 a, b; };
-
-__device__ __forceinline__ void load8(Pack8<__nv_bfloat16>& p, const __nv_bfloat16* s) {
-  p.u = __ldg(reinterpret_cast<const uint4*>(s));
-}
-__device__ __forceinline__ void load8(Pack8<float>& p, const float* s) {
-  p.a = __ldg(reinterpret_cast<const float4*>(s));
-  p.b = __ldg(reinterpret_cast<const float4*>(s) + 1);
-}
-__device__ __forceinline__ void open8(const Pack8<__nv_bfloat16>& p, float* f) {
-  const uint32_t u[4] = {p.u.x, p.u.y, p.u.z, p.u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {  // a bf16 is the top half of an fp32
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// four consecutive elements as loaded
+template <typename IO> struct Quad;
+template <> struct Quad<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void open(float* f) const {
+    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
   }
-}
-__device__ __forceinline__ void open8(const Pack8<float>& p, float* f) {
-  f[0] = p.a.x; f[1] = p.a.y; f[2] = p.a.z; f[3] = p.a.w;
-  f[4] = p.b.x; f[5] = p.b.y; f[6] = p.b.z; f[7] = p.b.w;
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* d, const float* f) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  *reinterpret_cast<uint4*>(d) = make_uint4(u[0], u[1], u[2], u[3]);
-}
-__device__ __forceinline__ void store8(float* d, const float* f) {
-  reinterpret_cast<float4*>(d)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(d)[1] = make_float4(f[4], f[5], f[6], f[7]);
-}
-__device__ __forceinline__ Pack8<__nv_bfloat16> shfl8(const Pack8<__nv_bfloat16>& p, int src) {
-  Pack8<__nv_bfloat16> r;
-  r.u.x = __shfl_sync(0xffffffffu, p.u.x, src);
-  r.u.y = __shfl_sync(0xffffffffu, p.u.y, src);
-  r.u.z = __shfl_sync(0xffffffffu, p.u.z, src);
-  r.u.w = __shfl_sync(0xffffffffu, p.u.w, src);
-  return r;
-}
-__device__ __forceinline__ Pack8<float> shfl8(const Pack8<float>& p, int src) {
-  Pack8<float> r;
-  r.a.x = __shfl_sync(0xffffffffu, p.a.x, src);
-  r.a.y = __shfl_sync(0xffffffffu, p.a.y, src);
-  r.a.z = __shfl_sync(0xffffffffu, p.a.z, src);
-  r.a.w = __shfl_sync(0xffffffffu, p.a.w, src);
-  r.b.x = __shfl_sync(0xffffffffu, p.b.x, src);
-  r.b.y = __shfl_sync(0xffffffffu, p.b.y, src);
-  r.b.z = __shfl_sync(0xffffffffu, p.b.z, src);
-  r.b.w = __shfl_sync(0xffffffffu, p.b.w, src);
-  return r;
-}
-
-// eight floats of a 16-byte aligned row, or all `otherwise` where there is none
-__device__ __forceinline__ void floats8(const float* s, float otherwise, float* f) {
-  if (s) {
-    Pack8<float> p;
-    load8(p, s);
-    open8(p, f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) f[i] = otherwise;
-  }
-}
-
-// A lane's part in the rotation: its cosines and signed sines, and the lane that holds the other
-// element of each of its pairs.  out_i = y_i cs_i + other_i sn_i, where `other` is the partner
-// lane's element i ("half") or this lane's element i ^ 1 ("pairs"); lanes past R turn nothing.
-struct Turn {
-  float cs[kVec], sn[kVec];
-  int partner;
 };
-template <int LPR>
-__device__ __forceinline__ Turn make_turn(const float* row, int R, bool pairs, int lane,
-                                          float sign) {
-  Turn t;
-  const int l = lane % LPR, d0 = kVec * l;
-  t.partner = lane;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    t.cs[i] = 1.f;
-    t.sn[i] = 0.f;
+template <> struct Quad<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v = __ldg(reinterpret_cast<const uint2*>(p));
   }
-  if (d0 >= R) return t;
-  if (pairs) {
-    const float4 c = __ldg(reinterpret_cast<const float4*>(row + d0 / 2));
-    const float4 s = __ldg(reinterpret_cast<const float4*>(row + R / 2 + d0 / 2));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+  __device__ __forceinline__ void clear() { v = make_uint2(0u, 0u); }
+  __device__ __forceinline__ void open(float* f) const {  // a bf16 is the top half of an fp32
+    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+};
+__device__ __forceinline__ void put4(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ uint2 bf16x4(const float* f) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+}
+__device__ __forceinline__ void put4(__nv_bfloat16* p, const float* f) {
+  *reinterpret_cast<uint2*>(p) = bf16x4(f);
+}
+__device__ __forceinline__ void put8(float* p, const float* f) {
+  put4(p, f);
+  put4(p + 4, f + 4);
+}
+__device__ __forceinline__ void put8(__nv_bfloat16* p, const float* f) {
+  const uint2 x = bf16x4(f), y = bf16x4(f + 4);
+  *reinterpret_cast<uint4*>(p) = make_uint4(x.x, x.y, y.x, y.y);
+}
+
+// A lane's place in a row of the forward: where its two groups of four begin.
+struct Place {
+  int d0, d1;
+  bool turned;
+};
+template <bool PAIRS>
+__device__ __forceinline__ Place place_of(int l, int R) {
+  Place p;
+  p.turned = kVec * l < R;
+  const bool halves = !PAIRS && p.turned;
+  p.d0 = halves ? 4 * l : kVec * l;
+  p.d1 = halves ? R / 2 + 4 * l : kVec * l + 4;
+  return p;
+}
+
+// A lane's eight elements as four pairs: a[i], b[i] turn together.
+template <bool PAIRS, typename IO>
+__device__ __forceinline__ void open_pairs(const Quad<IO>* q, float* a, float* b) {
+  if constexpr (PAIRS) {
+    float f[kVec];
+    q[0].open(f);
+    q[1].open(f + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      t.cs[2 * i] = t.cs[2 * i + 1] = cc[i];
-      t.sn[2 * i] = -sign * ss[i];
-      t.sn[2 * i + 1] = sign * ss[i];
+      a[i] = f[2 * i];
+      b[i] = f[2 * i + 1];
     }
   } else {
-    const bool low = d0 < R / 2;
-    t.partner = low ? lane + R / (2 * kVec) : lane - R / (2 * kVec);
-    const int at = low ? d0 : d0 - R / 2;
-    floats8(row + at, 1.f, t.cs);
-    floats8(row + R / 2 + at, 0.f, t.sn);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) t.sn[i] *= low ? -sign : sign;
+    q[0].open(a);
+    q[1].open(b);
   }
-  return t;
+}
+template <bool PAIRS, typename IO>
+__device__ __forceinline__ void put_pairs(IO* row, const Place& p, const float* a, const float* b) {
+  if constexpr (PAIRS) {  // (d1 follows d0)
+    const float f[kVec] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3]};
+    put4(row + p.d0, f);
+    put4(row + p.d1, f + 4);
+  } else {
+    put4(row + p.d0, a);
+    put4(row + p.d1, b);
+  }
+}
+// four elements of a weight (plus the offset), or ones
+__device__ __forceinline__ void weight4(const float* w, int d, float offset, float* f) {
+  if (w) {
+    Quad<float> q;
+    q.load(w + d);
+    q.open(f);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = w ? f[i] + offset : 1.f;
 }
 
 template <int LPR>
@@ -144,224 +128,340 @@ __device__ __forceinline__ float row_sum(float s) {
   return s;
 }
 
-// A warp takes `U` steps of 32 / LPR heads of one token.  Units: token x head group, token major.
-template <typename IO, int D, int U>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_kernel(QkRopeArgs a) {
+// Work: a unit is a token's run of `steps` x 32 / LPR query heads, or key heads.  A warp takes one
+// unit: the rotation's and the weight's factors are the same for all its rows and are formed once.
+struct RopeUnits {
+  int steps;         // row steps of a unit
+  int per_q, per_k;  // units of a token's query heads, key heads
+};
+
+template <typename IO, int D, bool PAIRS, int U>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(IO) == 2 ? 4 : 2)
+qk_rope_kernel(QkRopeArgs a, RopeUnits un) {
   constexpr int LPR = D / kVec, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const int H = a.hq + a.hkv, groups = (H + RPW * U - 1) / (RPW * U);
-  const int64_t units = a.T * groups;
-  const int64_t step = (int64_t)gridDim.x * (kRopeThreads / 32);
-  for (int64_t u = (int64_t)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32; u < units;
-       u += step) {
-    const int64_t t = u / groups;
-    const int h0 = (int)(u - t * groups) * RPW * U + sub;
-    Pack8<IO> x[U];
+  const int64_t u = (int64_t)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32;
+  const int per_token = un.per_q + un.per_k;
+  const int64_t t = u < 0x7fffffff ? (uint32_t)u / (uint32_t)per_token : u / per_token;
+  if (t >= a.T) return;
+  int first = (int)(u - t * per_token);
+  const bool isq = first < un.per_q;
+  if (!isq) first -= un.per_q;
+  const int heads = isq ? a.hq : a.hkv;
+  const int h1 = min(heads, (first + 1) * un.steps * RPW);
+  const Place p = place_of<PAIRS>(l, a.R);
+  int h = first * un.steps * RPW + sub;
+  const int64_t hs = isq ? a.q_hs : a.k_hs;
+  // the next row to load, its second group's distance, the distance of a step's row
+  const IO* src = static_cast<const IO*>(isq ? a.q : a.k) + t * (isq ? a.q_ts : a.k_ts) + h * hs +
+                  p.d0;
+  const int dd = p.d1 - p.d0;
+  const int64_t rs = RPW * hs;
+  IO* dst = static_cast<IO*>(isq ? a.q_out : a.k_out) + (t * heads + h) * D;
+  Quad<IO> x[U][2];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    x[i][0].clear();
+    x[i][1].clear();
+    if (h + i * RPW < h1) {
+      x[i][0].load(src);
+      x[i][1].load(src + dd);
+    }
+    src += rs;
+  }
+  const int pos = a.pos[t];
+  float w[kVec], wa[4], wb[4], c[4], s[4];
+  weight4(isq ? a.wq : a.wk, p.d0, a.offset, w);
+  weight4(isq ? a.wq : a.wk, p.d1, a.offset, w + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    wa[i] = PAIRS ? w[2 * i] : w[i];
+    wb[i] = PAIRS ? w[2 * i + 1] : w[4 + i];
+    c[i] = 1.f;
+    s[i] = 0.f;
+  }
+  if (pos < 0 || pos >= a.max_pos) {  // (the same for the whole warp)
+    if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
+    return;
+  }
+  if (p.turned) {
+    const float* row = a.table + (int64_t)pos * a.R + 4 * l;
+    Quad<float> q;
+    q.load(row);
+    q.open(c);
+    q.load(row + a.R / 2);
+    q.open(s);
+  }
+  // out_a = r (a wa c - b wb s), out_b = r (b wb c + a wa s)
+  float aa[4], ab[4], ba[4], bb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    aa[i] = wa[i] * c[i];
+    ab[i] = wb[i] * -s[i];
+    bb[i] = wb[i] * c[i];
+    ba[i] = wa[i] * s[i];
+  }
+  const int rounds = (h1 - (h - sub) + U * RPW - 1) / (U * RPW);
+  for (int round = 0; round < rounds; ++round) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * RPW;
-      const IO* p = h < a.hq ? static_cast<const IO*>(a.q) + t * a.q_ts + h * a.q_hs
-                             : static_cast<const IO*>(a.k) + t * a.k_ts + (h - a.hq) * a.k_hs;
-      if (h < H) load8(x[i], p + kVec * l);
-      else x[i] = Pack8<IO>{};
-    }
-    const int pos = a.pos[t];
-    if (pos < 0 || pos >= a.max_pos) {  // (the same for the whole warp)
-      if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
-      continue;
-    }
-    const Turn turn = make_turn<LPR>(a.table + (int64_t)pos * a.R, a.R, a.pairs, lane, 1.f);
-    const int pl = turn.partner % LPR;
+      float f[4], g[4], o[4], s2 = 0.f;
+      open_pairs<PAIRS>(x[i], f, g);
+      if (h + (i + U) * RPW < h1) {  // the next round's row
+        x[i][0].load(src);
+        x[i][1].load(src + dd);
+      }
+      src += rs;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * RPW;
-      float f[kVec], w[kVec], o[kVec], s2 = 0.f;
-      open8(x[i], f);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) s2 = fmaf(f[j], f[j], s2);
+      for (int j = 0; j < 4; ++j) s2 = fmaf(f[j], f[j], fmaf(g[j], g[j], s2));
       const float r = rsqrtf(row_sum<LPR>(s2) * (1.f / D) + a.eps);
-      const float* wt = h < a.hq ? a.wq : a.wk;
-      floats8(wt ? wt + kVec * l : nullptr, 1.f - a.offset, w);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) f[j] *= r * (w[j] + a.offset);
-      if (a.pairs) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) o[j] = fmaf(f[j], turn.cs[j], f[j ^ 1] * turn.sn[j]);
-      } else {
-        float g[kVec];
-        open8(shfl8(x[i], turn.partner), g);
-        floats8(wt ? wt + kVec * pl : nullptr, 1.f - a.offset, w);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-          o[j] = fmaf(f[j], turn.cs[j], g[j] * (r * (w[j] + a.offset)) * turn.sn[j]);
+      for (int j = 0; j < 4; ++j) {
+        o[j] = r * fmaf(f[j], aa[j], g[j] * ab[j]);
+        g[j] = r * fmaf(g[j], bb[j], f[j] * ba[j]);
       }
-      if (h < H) {
-        IO* dst = h < a.hq ? static_cast<IO*>(a.q_out) + (t * a.hq + h) * D
-                           : static_cast<IO*>(a.k_out) + (t * a.hkv + h - a.hq) * D;
-        store8(dst + kVec * l, o);
-      }
+      if (h + i * RPW < h1) put_pairs<PAIRS>(dst + i * RPW * D, p, o, g);
     }
+    h += U * RPW;
+    dst += U * RPW * D;
   }
 }
 
-// Gradients.  Each warp walks its units in a fixed order and keeps its share of both weights'
-// gradients in registers; a CTA's warps join theirs in shared memory and write one partial sum
-// per CTA, which qk_rope_dw_kernel adds up in CTA order: the same bits on every run.
-template <typename IO, int D, int U>
-__global__ void __launch_bounds__(kRopeThreads) qk_rope_backward_kernel(QkRopeArgs a) {
+// Gradients.  A CTA has query rows or key rows, a warp walks tokens in a fixed order and keeps its
+// share of the weight's gradient in registers; a CTA's warps join theirs in shared memory and
+// write one partial sum per CTA, which qk_rope_dw_kernel adds up in a fixed order: the same bits
+// on every run.  A thread's rows come through a ring of its own in shared memory (cp.async), so
+// that kRopeRing - 1 of them are on their way without holding registers.
+constexpr int kRopeRing = 4;
+template <typename IO> constexpr int rope_ring_bytes() {
+  return kRopeRing * 4 * kRopeThreads * 4 * (int)sizeof(IO);
+}
+template <int BYTES>
+__device__ __forceinline__ void ring_copy(uint32_t dst, const void* src, bool ok) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(ok ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(ok ? 8 : 0) : "memory");
+}
+
+template <typename IO, int D, bool PAIRS>
+__global__ void __launch_bounds__(kRopeThreads, sizeof(IO) == 2 ? 3 : 2)
+qk_rope_backward_kernel(QkRopeArgs a, int ctas_q) {
   constexpr int LPR = D / kVec, RPW = 32 / LPR, kWarps = kRopeThreads / 32;
-  __shared__ float part[kWarps][2][D];
+  constexpr int QB = 4 * sizeof(IO);  // bytes of a group of four
+  __shared__ __align__(16) float part[kWarps][D];
+  extern __shared__ __align__(16) char ring[];  // [slot][x0, x1, g0, g1][thread]
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR, warp = threadIdx.x / 32;
-  const int H = a.hq + a.hkv, groups = (H + RPW * U - 1) / (RPW * U);
-  const int64_t units = a.T * groups;
-  const int64_t step = (int64_t)gridDim.x * kWarps;
-  float dw[2][kVec];
+  const bool isq = (int)blockIdx.x < ctas_q;
+  const int heads = isq ? a.hq : a.hkv, T = (int)a.T;  // (T fits 31 bits)
+  const int64_t rs = RPW * (isq ? a.q_hs : a.k_hs), ts = isq ? a.q_ts : a.k_ts;
+  const Place p = place_of<PAIRS>(l, a.R);
+  const int dd = p.d1 - p.d0;
+  const IO* const xs = static_cast<const IO*>(isq ? a.q : a.k) + sub * (isq ? a.q_hs : a.k_hs) + p.d0;
+  const IO* const gs = static_cast<const IO*>(isq ? a.dq_out : a.dk_out) + sub * D + p.d0;
+  IO* const dst = static_cast<IO*>(isq ? a.dq : a.dk) + sub * D;
+  float w[kVec], wa[4], wb[4], dwa[4], dwb[4];
+  weight4(isq ? a.wq : a.wk, p.d0, a.offset, w);
+  weight4(isq ? a.wq : a.wk, p.d1, a.offset, w + 4);
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) dw[0][j] = dw[1][j] = 0.f;
-  for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += step) {
-    const int64_t t = u / groups;
-    const int h0 = (int)(u - t * groups) * RPW * U + sub;
-    Pack8<IO> x[U], g[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * RPW;
-      const bool isq = h < a.hq;
-      const IO* p = isq ? static_cast<const IO*>(a.q) + t * a.q_ts + h * a.q_hs
-                        : static_cast<const IO*>(a.k) + t * a.k_ts + (h - a.hq) * a.k_hs;
-      const IO* d = isq ? static_cast<const IO*>(a.dq_out) + (t * a.hq + h) * D
-                        : static_cast<const IO*>(a.dk_out) + (t * a.hkv + h - a.hq) * D;
-      if (h < H) {
-        load8(x[i], p + kVec * l);
-        load8(g[i], d + kVec * l);
-      } else {
-        x[i] = Pack8<IO>{};
-        g[i] = Pack8<IO>{};
-      }
+  for (int j = 0; j < 4; ++j) {
+    wa[j] = PAIRS ? w[2 * j] : w[j];
+    wb[j] = PAIRS ? w[2 * j + 1] : w[4 + j];
+    dwa[j] = dwb[j] = 0.f;
+  }
+  const int stride = (int)(isq ? ctas_q : gridDim.x - ctas_q) * kWarps;
+  int t = (int)(isq ? blockIdx.x : blockIdx.x - ctas_q) * kWarps + warp;
+  auto after = [&](int tt) { return tt < T - stride ? tt + stride : T; };
+
+  // the copies walk the rows of the warp's tokens ahead of the sums
+  int ft = t, fh = sub, fslot = 0;
+  const IO *xp = xs + (int64_t)(t < T ? t : 0) * ts, *gp = gs + (int64_t)(t < T ? t : 0) * heads * D;
+  const uint32_t ring0 = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * QB;
+  auto fetch = [&] {
+    const bool ok = ft < T && fh < heads;
+    const uint32_t at = ring0 + fslot * (4 * kRopeThreads * QB);
+    // (a copy that reads nothing still names an address inside the tensor)
+    ring_copy<QB>(at, ok ? xp : xs - sub * (isq ? a.q_hs : a.k_hs), ok);
+    ring_copy<QB>(at + kRopeThreads * QB, ok ? xp + dd : xs - sub * (isq ? a.q_hs : a.k_hs), ok);
+    ring_copy<QB>(at + 2 * kRopeThreads * QB, ok ? gp : gs - sub * D, ok);
+    ring_copy<QB>(at + 3 * kRopeThreads * QB, ok ? gp + dd : gs - sub * D, ok);
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+    fslot = fslot == kRopeRing - 1 ? 0 : fslot + 1;
+    fh += RPW;
+    xp += rs;
+    gp += RPW * D;
+    if (fh - sub >= heads && ft < T) {  // the warp's next token (the same step for all its lanes)
+      ft = after(ft);
+      fh = sub;
+      const int64_t tt = ft < T ? ft : 0;
+      xp = xs + tt * ts;
+      gp = gs + tt * heads * D;
     }
-    const int pos = a.pos[t];
-    if (pos < 0 || pos >= a.max_pos) {
-      if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
-      continue;
+  };
+#pragma unroll
+  for (int i = 0; i < kRopeRing - 1; ++i) fetch();
+  int slot = 0, pos = t < T ? a.pos[t] : 0;
+  while (t < T) {
+    const int next = after(t);
+    const bool good = pos >= 0 && pos < a.max_pos;
+    if (!good && lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
+    float c[4], s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      c[j] = 1.f;
+      s[j] = 0.f;
     }
-    const Turn turn = make_turn<LPR>(a.table + (int64_t)pos * a.R, a.R, a.pairs, lane, -1.f);
+    if (p.turned) {
+      const float* row = a.table + (int64_t)(good ? pos : 0) * a.R + 4 * l;
+      Quad<float> q;
+      q.load(row);
+      q.open(c);
+      q.load(row + a.R / 2);
+      q.open(s);
+    }
+    if (next < T) pos = a.pos[next];
+    IO* out = dst + (int64_t)t * heads * D;
+    for (int h = sub; h - sub < heads; h += RPW) {
+      fetch();
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(kRopeRing - 1) : "memory");
+      Quad<IO> q[2];
+      float xa[4], xb[4], ya[4], yb[4], s2 = 0.f, dot = 0.f;
+      const char* at = ring + slot * (4 * kRopeThreads * QB) + threadIdx.x * QB;
+      q[0].v = *reinterpret_cast<const decltype(q[0].v)*>(at);
+      q[1].v = *reinterpret_cast<const decltype(q[0].v)*>(at + kRopeThreads * QB);
+      open_pairs<PAIRS>(q, xa, xb);
+      q[0].v = *reinterpret_cast<const decltype(q[0].v)*>(at + 2 * kRopeThreads * QB);
+      q[1].v = *reinterpret_cast<const decltype(q[0].v)*>(at + 3 * kRopeThreads * QB);
+      open_pairs<PAIRS>(q, ya, yb);
+      slot = slot == kRopeRing - 1 ? 0 : slot + 1;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * RPW;
-      const bool isq = h < a.hq;
-      float f[kVec], d[kVec], dy[kVec], w[kVec], s2 = 0.f, dot = 0.f;
-      open8(x[i], f);
-      open8(g[i], d);
-      if (a.pairs) {
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) dy[j] = fmaf(d[j], turn.cs[j], d[j ^ 1] * turn.sn[j]);
-      } else {
-        float e[kVec];
-        open8(shfl8(g[i], turn.partner), e);
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) dy[j] = fmaf(d[j], turn.cs[j], e[j] * turn.sn[j]);
-      }
-      const float* wt = isq ? a.wq : a.wk;
-      floats8(wt ? wt + kVec * l : nullptr, 1.f - a.offset, w);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        s2 = fmaf(f[j], f[j], s2);
-        w[j] = dy[j] * (w[j] + a.offset);  // dn
-        dot = fmaf(w[j], f[j], dot);
+      for (int j = 0; j < 4; ++j) {  // dy: turned back
+        const float da = ya[j];
+        ya[j] = fmaf(da, c[j], yb[j] * s[j]);
+        yb[j] = fmaf(yb[j], c[j], -da * s[j]);
+        s2 = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], s2));
+        dot = fmaf(ya[j] * wa[j], xa[j], fmaf(yb[j] * wb[j], xb[j], dot));
       }
       const float r = rsqrtf(row_sum<LPR>(s2) * (1.f / D) + a.eps);
       const float m = row_sum<LPR>(dot) * (1.f / D) * r;  // mean(dn n)
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const float n = f[j] * r;
-        const float c = dy[j] * n;
-        dw[0][j] += isq ? c : 0.f;
-        dw[1][j] += isq ? 0.f : c;
-        f[j] = r * (w[j] - n * m);
+      for (int j = 0; j < 4; ++j) {
+        const float na = xa[j] * r, nb = xb[j] * r;
+        if (good) {
+          dwa[j] = fmaf(ya[j], na, dwa[j]);
+          dwb[j] = fmaf(yb[j], nb, dwb[j]);
+        }
+        xa[j] = r * fmaf(ya[j], wa[j], -na * m);
+        xb[j] = r * fmaf(yb[j], wb[j], -nb * m);
       }
-      if (h < H) {
-        IO* dst = isq ? static_cast<IO*>(a.dq) + (t * a.hq + h) * D
-                      : static_cast<IO*>(a.dk) + (t * a.hkv + h - a.hq) * D;
-        store8(dst + kVec * l, f);
-      }
+      if (good && h < heads) put_pairs<PAIRS>(out, p, xa, xb);
+      out += RPW * D;
     }
+    t = next;
   }
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
   // a warp's rows (lanes with the same l), then the CTA's warps
 #pragma unroll
-  for (int which = 0; which < 2; ++which)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      float s = dw[which][j];
-#pragma unroll
-      for (int off = LPR; off < 32; off <<= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      if (sub == 0) part[warp][which][kVec * l + j] = s;
+    for (int off = LPR; off < 32; off <<= 1) {
+      dwa[j] += __shfl_xor_sync(0xffffffffu, dwa[j], off);
+      dwb[j] += __shfl_xor_sync(0xffffffffu, dwb[j], off);
     }
+  if (sub == 0) put_pairs<PAIRS>(part[warp], p, dwa, dwb);
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * D; c += kRopeThreads) {
-    float s = 0.f;
+  for (int d = threadIdx.x; d < D; d += kRopeThreads) {
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += part[i][c / D][c % D];
-    a.partial[(int64_t)blockIdx.x * 2 * D + c] = s;
+    for (int i = 0; i < kWarps; ++i) sum += part[i][d];
+    a.partial[(int64_t)blockIdx.x * D + d] = sum;
   }
 }
 
-// dw[c] = sum over CTAs of partial[cta][c]: a warp per 32 columns takes every eighth CTA
-__global__ void __launch_bounds__(256) qk_rope_dw_kernel(QkRopeArgs a, int ctas) {
-  __shared__ float part[8][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
+// dw = the sum of the query CTAs' (key CTAs') partial sums: a block has 32 columns of one of them,
+// its 32 warps every 32nd CTA
+__global__ void __launch_bounds__(1024) qk_rope_dw_kernel(QkRopeArgs a, int ctas_q, int ctas) {
+  __shared__ float part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  const int blocks = a.D / 32;
+  const bool isq = (int)blockIdx.x < blocks;
+  const int c = (isq ? blockIdx.x : blockIdx.x - blocks) * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < ctas; i += 8) s += a.partial[(int64_t)i * 2 * a.D + c];
+#pragma unroll 8
+  for (int i = (isq ? 0 : ctas_q) + warp; i < (isq ? ctas_q : ctas); i += 32)
+    s += a.partial[(int64_t)i * a.D + c];
   part[warp][lane] = s;
   __syncthreads();
-  if (warp) return;
-  s = 0.f;
+  s = part[lane][warp];  // warp w joins column w
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += part[i][lane];
-  if (c < a.D) a.dwq[c] = s;
-  else a.dwk[c - a.D] = s;
+  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+  if (lane == 0) (isq ? a.dwq : a.dwk)[c - lane + warp] = s;
 }
 
-// A warp takes four steps of heads a unit where there are units enough to fill the GPU's warps
-// several times over, one step where there are few.
-bool many(const QkRopeArgs& a) {
-  const int rpw = 32 * kVec / a.D;
-  return a.T * ((a.hq + a.hkv + 4 * rpw - 1) / (4 * rpw)) >= 4 * kRopeCtas * (kRopeThreads / 32);
-}
+int div_up(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
 
-template <typename IO, int D, int U>
-int rope_ctas(const QkRopeArgs& a) {
-  constexpr int RPW = 32 * kVec / D;
-  const int64_t units = a.T * ((a.hq + a.hkv + RPW * U - 1) / (RPW * U));
-  const int64_t c = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-  return (int)(c < kRopeCtas ? c : kRopeCtas);
-}
-
-template <typename IO, int D, int U>
-cudaError_t launch_rope(const QkRopeArgs& a, bool backward, cudaStream_t s) {
-  const int ctas = rope_ctas<IO, D, U>(a);
-  if (!backward) {
-    // forward: no per-CTA state, so every unit gets a warp of its own
-    constexpr int RPW = 32 * kVec / D;
-    const int64_t units = a.T * ((a.hq + a.hkv + RPW * U - 1) / (RPW * U));
-    const int64_t c = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
-    qk_rope_kernel<IO, D, U><<<(unsigned)(c < 0x7fffffff ? c : 0x7fffffff), kRopeThreads, 0, s>>>(a);
-    return cudaGetLastError();
-  }
-  qk_rope_backward_kernel<IO, D, U><<<ctas, kRopeThreads, 0, s>>>(a);
-  qk_rope_dw_kernel<<<2 * D / 32, 256, 0, s>>>(a, ctas);
+template <typename IO, int D, bool PAIRS, int U>
+cudaError_t launch_forward(const QkRopeArgs& a, RopeUnits un, cudaStream_t s) {
+  const int64_t units = a.T * (un.per_q + un.per_k);
+  const int64_t ctas = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  qk_rope_kernel<IO, D, PAIRS, U><<<(unsigned)ctas, kRopeThreads, 0, s>>>(a, un);
   return cudaGetLastError();
 }
 
+template <typename IO, int D, bool PAIRS>
+cudaError_t launch_rope(const QkRopeArgs& a, bool backward, cudaStream_t s) {
+  constexpr int RPW = 32 * kVec / D, kWarps = kRopeThreads / 32;
+  if (!backward) {
+    // as many heads a unit as leave two units for each of the GPU's 32 x 152 warps, sixteen steps
+    // at most; a single step where tokens are few
+    RopeUnits un;
+    for (un.steps = 16;; un.steps /= 4) {
+      un.per_q = div_up(a.hq, un.steps * RPW);
+      un.per_k = div_up(a.hkv, un.steps * RPW);
+      if (un.steps == 1 || a.T * (un.per_q + un.per_k) >= 2 * 32 * 152) break;
+    }
+    return un.steps == 1 ? launch_forward<IO, D, PAIRS, 1>(a, un, s)
+                         : launch_forward<IO, D, PAIRS, 4>(a, un, s);
+  }
+  // three CTAs an SM at most, shared between query and key rows by their number; a warp a token
+  const int most = div_up(a.T, kWarps);
+  int64_t ctas_q = (int64_t)kRopeCtas * a.hq / (a.hq + a.hkv);
+  ctas_q = ctas_q < 1 ? 1 : ctas_q > kRopeCtas - 1 ? kRopeCtas - 1 : ctas_q;
+  int64_t ctas_k = kRopeCtas - ctas_q;
+  if (ctas_q > most) ctas_q = most;
+  if (ctas_k > most) ctas_k = most;
+  const auto kern = qk_rope_backward_kernel<IO, D, PAIRS>;
+  constexpr int smem = rope_ring_bytes<IO>();
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)(ctas_q + ctas_k), kRopeThreads, smem, s>>>(a, (int)ctas_q);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_rope_dw_kernel, a, (int)ctas_q, (int)(ctas_q + ctas_k));
+}
 template <typename IO, int D>
-cudaError_t launch_rope_u(const QkRopeArgs& a, bool backward, cudaStream_t s) {
-  return many(a) ? launch_rope<IO, D, 4>(a, backward, s) : launch_rope<IO, D, 1>(a, backward, s);
+cudaError_t launch_rope_style(const QkRopeArgs& a, bool backward, cudaStream_t s) {
+  return a.pairs ? launch_rope<IO, D, true>(a, backward, s) : launch_rope<IO, D, false>(a, backward, s);
 }
 template <typename IO>
 cudaError_t launch_rope_io(const QkRopeArgs& a, bool backward, cudaStream_t s) {
   switch (a.D) {
-    case 64: return launch_rope_u<IO, 64>(a, backward, s);
-    case 128: return launch_rope_u<IO, 128>(a, backward, s);
-    default: return launch_rope_u<IO, 256>(a, backward, s);
+    case 64: return launch_rope_style<IO, 64>(a, backward, s);
+    case 128: return launch_rope_style<IO, 128>(a, backward, s);
+    default: return launch_rope_style<IO, 256>(a, backward, s);
   }
 }
 
