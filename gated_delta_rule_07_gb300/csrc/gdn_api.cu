@@ -657,6 +657,8 @@ gdn::KvArgs kv_args(const gdn_kv_cache* c, const gdn_kv_problem* p, const int32_
   memset(&a, 0, sizeof(a));
   a.T = p->total_tokens;
   a.N = p->num_seqs; a.hq = p->hq; a.hkv = c->hkv; a.D = c->head_dim;
+  a.group = p->hq / c->hkv;
+  if (a.group > 1) a.group_mul = (uint32_t)((0xffffffffu / (uint32_t)a.group) + 1);
   a.page = c->page_size;
   while ((1 << a.page_shift) < a.page) ++a.page_shift;
   a.num_pages = c->num_pages; a.max_pages = p->max_pages;
@@ -766,7 +768,7 @@ static gdn_status check_kv_attention(const gdn_kv_cache* cache, const gdn_kv_pro
   if (p->hq < 1 || p->hq % cache->hkv ||
       !strides_ok(p->q_token_stride, p->q_head_stride, p->io_dtype))
     return GDN_ERR_INVALID_ARGUMENT;
-  return p->hq > 65535 ? GDN_ERR_UNSUPPORTED : GDN_OK;
+  return p->hq > 32768 ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
 size_t gdn_kv_attention_workspace_size(const gdn_kv_cache* cache, const gdn_kv_problem* p) {

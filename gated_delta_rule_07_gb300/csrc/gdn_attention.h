@@ -32,6 +32,8 @@ cudaError_t qk_rope(const QkRopeArgs& a, bool backward, cudaStream_t s);
 struct KvArgs {
   int64_t T, k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;
   int N, hq, hkv, D, page, page_shift, num_pages, max_pages, window;  // page = 1 << page_shift
+  int group;           // query heads of a kv head; 2^32 / group, rounded up
+  uint32_t group_mul;
   bool bf16, e4m3;
   float scale;
   const void *k, *v, *q;

@@ -77,19 +77,31 @@ __device__ __forceinline__ bool item_of(const KvArgs& a, int n, Item& it) {
   it.tile0 = lo > 0 ? (int)(lo / kTile) : 0;
   it.tiles = (len + kTile - 1) / kTile - it.tile0;
   if (it.tiles < 1) it.tiles = 1;  // no key at all: a unit that sees nothing writes the zeros
-  it.row_tiles = (int)(((int64_t)it.m * (a.hq / a.hkv) + ROWS - 1) / ROWS);
+  it.row_tiles = (int)(((int64_t)it.m * a.group + ROWS - 1) / ROWS);
   return true;
 }
 // its units: an item (a kv head and row tile of it) is kItemUnits idle ones, then its tiles
 __device__ __forceinline__ int64_t units_of(const KvArgs& a, const Item& it) {
   return (int64_t)(it.tiles + kItemUnits) * it.row_tiles * a.hkv;
 }
-__device__ __forceinline__ int64_t div_up(int64_t x, uint32_t y) {  // x >= 0
-  return x < 0xffffffffLL - y ? (uint32_t)(x + y - 1) / y : (x + y - 1) / y;
+// x / y for x >= 0, y > 0 (a quotient that fits an int)
+__device__ __forceinline__ int quotient(int64_t x, int64_t y) {
+  int q = (int)__fdividef((float)x, (float)y);
+  while ((int64_t)q * y > x) --q;
+  while ((int64_t)(q + 1) * y <= x) ++q;
+  return q;
+}
+// x / group for the small x of a row tile (group_mul = 2^32 / group, rounded up)
+__device__ __forceinline__ int over_group(const KvArgs& a, int x) {
+  return a.group == 1 ? x : (int)__umulhi((uint32_t)x, a.group_mul);
 }
 
-struct Desc {  // an item that ends in CTA c and began in CTA `first` < c
-  int n, head, row_tile, first;
+// An item that ends in this CTA and began in CTA `first` before it (first < 0: there is none).
+struct Desc {
+  int64_t row0;                 // the sequence's first packed row
+  int first, head, rows;        // kv head, live rows of the row tile
+  int token0, rem;              // row r of the tile: token token0 + (rem + r) / group
+  int unused;
 };
 
 // ---------------------------------------------------------------------------------- operands
@@ -116,14 +128,24 @@ __device__ __forceinline__ void open_codes(uint32_t w, uint32_t& lo, uint32_t& h
   }
 }
 
-__device__ __forceinline__ void load4(const float* p, float* f) {
-  const float4 v = *reinterpret_cast<const float4*>(p);
-  f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+__device__ __forceinline__ void load16(const float* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+    f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+  }
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float* f) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-  f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[8 * i + 2 * e] = __uint_as_float(u[e] << 16);
+      f[8 * i + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+  }
 }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
@@ -221,7 +243,8 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       if (n0 + kThreads >= a.N) total = before;
       if (pass) {
         if (per == 0) {
-          per = div_up(total, gridDim.x);
+          // (a run may be a little longer than its share: the same in every CTA)
+          per = (int64_t)((float)total * (1.000002f / (float)gridDim.x)) + 1;
           per = per > kMinUnits ? per : kMinUnits;
           u = blockIdx.x * per;
         }
@@ -234,11 +257,10 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     }
   }
   const int64_t u1 = u + per < total ? u + per : total;
-  if (tid == 0) descs[blockIdx.x].n = -1;
+  if (tid == 0) descs[blockIdx.x].first = -1;
   asm volatile("griddepcontrol.launch_dependents;");
   if (u >= u1) return;
 
-  const int group = a.hq / a.hkv;
   int n = start_n;
   int64_t off = start_off;
   while (u < u1 && n < a.N) {
@@ -250,7 +272,7 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     }
     // one item: kv head, row tile, and this CTA's tiles [ta, tb) of it
     const int span = it.tiles + kItemUnits;
-    const int which = off < 0x7fffffff ? (int)((uint32_t)off / (uint32_t)span) : (int)(off / span);
+    const int which = quotient(off, span);
     const int at0 = (int)(off - (int64_t)which * span);  // place in the item, idle units first
     const int at1 = (int)(span < at0 + (u1 - u) ? span : at0 + (u1 - u));
     const int64_t item_u = u - at0;
@@ -258,8 +280,11 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     off += at1 - at0;
     const int ta = max(at0 - kItemUnits, 0), tb = max(at1 - kItemUnits, 0);
     if (ta >= tb) continue;
-    const int head = which / it.row_tiles, rt = which - head * it.row_tiles;
-    const int row_base = rt * ROWS, row_end = it.m * group;
+    const int head = (uint32_t)which / (uint32_t)it.row_tiles;
+    const int row_base = (which - head * it.row_tiles) * ROWS;
+    const int rows = min(ROWS, it.m * a.group - row_base);  // live rows of the tile
+    // row r of the tile is token token0 + (rem + r) / group, query head head group + the remainder
+    const int token0 = (uint32_t)row_base / (uint32_t)a.group, rem = row_base - token0 * a.group;
 
     // the first tiles are on their way before the queries are
     const int* table = a.table + (int64_t)n * a.max_pages;
@@ -308,50 +333,45 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     load_k(pid, tile);
     load_v(pid, tile);
 
-    // queries: scaled by a power of two into [1, 2), fp16, in the order the products take them
-    for (int row = warp; row < ROWS; row += kWarps) {
-      const int rr = row_base + row;
-      float f[D / 32 < 4 ? 4 : D / 32];
-      const bool live = rr < row_end;
-      const IO* q = static_cast<const IO*>(a.q) + (it.row0 + (live ? rr / group : 0)) * a.q_ts +
-                    (head * group + (live ? rr % group : 0)) * a.q_hs;
-      float amax = 0.f;
+    // queries: scaled by a power of two into [1, 2), fp16, in the order the products take them.  A
+    // thread has 16 dims of a row, 64 j + 16 cc on: lane (row % 8, cc)'s share of products 4 j ..
+    // 4 j + 3
+#pragma unroll 1
+    for (int i = tid; i < ROWS * STEPS; i += kThreads) {
+      const int row = i / STEPS, chunk = i % STEPS;
+      const int tk = over_group(a, rem + row), gq = rem + row - tk * a.group;
+      const bool live = row < rows;
+      const IO* q = static_cast<const IO*>(a.q) + (it.row0 + (live ? token0 + tk : 0)) * a.q_ts +
+                    (int64_t)(head * a.group + (live ? gq : 0)) * a.q_hs + 16 * chunk;
+      float f[16], amax = 0.f;
+      load16(q, f);
 #pragma unroll
-      for (int i = 0; i < (D + 127) / 128; ++i)
-        {
-          const int d = 128 * i + 4 * lane;
-          f[4 * i] = f[4 * i + 1] = f[4 * i + 2] = f[4 * i + 3] = 0.f;
-          if (live && d < D) load4(q + d, f + 4 * i);
+      for (int e = 0; e < 16; ++e) {
+        f[e] = live ? f[e] : 0.f;
+        amax = fmaxf(amax, fabsf(f[e]));
+      }
+      // (the row's threads are neighbours; whole warps run here: ROWS STEPS is a multiple of 32)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(f[4 * i + e]));
-        }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int o = 1; o < STEPS; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       int ex = (int)((__float_as_uint(amax) >> 23) & 0xff);
       ex = ex == 0 ? 127 : min(max(ex, 2), 252);
       const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-      if (lane == 0) q_scale[row] = __uint_as_float((uint32_t)ex << 23);
+      if (chunk == 0) q_scale[row] = __uint_as_float((uint32_t)ex << 23) * (a.scale * kLog2e);
+      uint4* at = reinterpret_cast<uint4*>(smem) +
+                  ((row / 8) * (STEPS / 2) + 2 * (chunk / 4)) * 32 + 4 * (row % 8) + chunk % 4;
 #pragma unroll
-      for (int i = 0; i < (D + 127) / 128; ++i) {
-        const int d = 128 * i + 4 * lane;
-        if (d < D) {
-          // dims 64 j + 16 cc + 4 w + {0..3}: lane (row % 8, cc), product 4 j + w
-          const int step = 4 * (d / 64) + (d % 16) / 4, cc = (d % 64) / 16;
-          const int at = (((row / 8) * (STEPS / 2) + step / 2) * 32 + 4 * (row % 8) + cc) * 16 +
-                         (step & 1) * 8;
-          uint2 hi;
-          float x[4];
+      for (int h = 0; h < 2; ++h) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = f[4 * i + e] * down;
-          hi.x = pack_half(x[0], x[1]);
-          hi.y = pack_half(x[2], x[3]);
-          *reinterpret_cast<uint2*>(smem + at) = hi;
-          if constexpr (SPLIT) {
-            const float2 p = open_half(hi.x), s = open_half(hi.y);
-            *reinterpret_cast<uint2*>(smem + ROWS * D * 2 + at) =
-                make_uint2(pack_half(x[0] - p.x, x[1] - p.y), pack_half(x[2] - s.x, x[3] - s.y));
-          }
+        for (int e = 0; e < 4; ++e) {
+          const float x = f[8 * h + 2 * e] * down, y = f[8 * h + 2 * e + 1] * down;
+          hi[e] = pack_half(x, y);
+          const float2 z = open_half(hi[e]);
+          lo[e] = pack_half(x - z.x, y - z.y);
         }
+        at[32 * h] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (SPLIT)
+          at[ROWS * D / 8 + 32 * h] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
     __syncthreads();
@@ -371,16 +391,16 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int row = 8 * t + 2 * c + e;
-        last[t][e] = row_base + row < row_end ? it.len - it.m + (row_base + row) / group : -1;
-        qs[t][e] = q_scale[row] * a.scale * kLog2e;
+        last[t][e] = row < rows ? it.len - it.m + token0 + over_group(a, rem + row) : -1;
+        qs[t][e] = q_scale[row];
         M[t][e] = kNone;
         l[t][e] = 0.f;
       }
-    const int last_row = min(row_base + ROWS, row_end) - 1;
-    // keys that every live row sees: [all_lo, all_hi]
-    const int all_hi = row_base + ROWS <= row_end ? it.len - it.m + row_base / group : -1;
-    const int64_t all_lo = a.window > 0
-        ? (int64_t)it.len - it.m + last_row / group - a.window + 1 : INT64_MIN;
+    // keys that every row sees: [all_lo, all_hi] (none where some row is not live)
+    const int all_hi = rows == ROWS ? it.len - it.m + token0 : -1;
+    const int64_t all_lo = a.window > 0 ? (int64_t)it.len - it.m + token0 +
+                                              over_group(a, rem + rows - 1) - a.window + 1
+                                        : INT64_MIN;
     float acc[NT][2 * VC][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -504,8 +524,7 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       pid_next = pid_after;
     }
 
-    // join the warps: each leaves its maxima and sums, then its o, on the common maximum
-    __syncthreads();  // (queries in shared memory are no longer needed)
+    // join the warps: each leaves its maxima and sums, then its o on the common maximum
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -515,50 +534,76 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (r == 0) warp_ml[warp][8 * t + 2 * c + e] = make_float2(M[t][e], x);
       }
+    __syncthreads();  // (the queries in shared memory are no longer needed either)
     float* so = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 2; ++e) {
+        const int row = 8 * t + 2 * c + e;
+        float m = M[t][e];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][row].x);
+        const float f = exp2_fast(M[t][e] - m);
 #pragma unroll
         for (int j = 0; j < VC; ++j)
-          *reinterpret_cast<float4*>(so + (warp * ROWS + 8 * t + 2 * c + e) * S::pad + 32 * j +
-                                     4 * r) =
-              make_float4(acc[t][2 * j][e], acc[t][2 * j][e + 2], acc[t][2 * j + 1][e],
-                          acc[t][2 * j + 1][e + 2]);
-    __syncthreads();
-    const bool begins = ta == 0, ends = tb == it.tiles;
+          *reinterpret_cast<float4*>(so + (warp * ROWS + row) * S::pad + 32 * j + 4 * r) =
+              make_float4(acc[t][2 * j][e] * f, acc[t][2 * j][e + 2] * f,
+                          acc[t][2 * j + 1][e] * f, acc[t][2 * j + 1][e + 2] * f);
+      }
+    const bool begins = ta == 0, ends = tb == it.tiles, whole = begins && ends;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
-    for (int i = tid; i < ROWS * (D / 4); i += kThreads) {
-      const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = row_base + row;
-      if (rr >= row_end) continue;
+    if (tid < rows) {  // the rows' sums
       float m = kNone, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][row].x);
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][tid].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w)
+        L = fmaf(warp_ml[w][tid].y, exp2_fast(warp_ml[w][tid].x - m), L);
+      q_scale[tid] = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+      if (!whole) {
+        part_ml[slot * ROWS + tid] = make_float2(m, L);
+      } else if (a.lse) {
+        const int tk = over_group(a, rem + tid);
+        a.lse[(it.row0 + token0 + tk) * a.hq + head * a.group + rem + tid - tk * a.group] =
+            (m + log2f(L)) * kLn2;
+      }
+    }
+    if (ends && !begins && tid == 0) {
+      Desc d;
+      d.row0 = it.row0;
+      d.first = quotient(item_u + kItemUnits, per);
+      d.head = head;
+      d.rows = rows;
+      d.token0 = token0;
+      d.rem = rem;
+      d.unused = 0;
+      descs[blockIdx.x] = d;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < rows * (D / 4); i += kThreads) {
+      const int row = i / (D / 4), d = 4 * (i % (D / 4));
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_fast(warp_ml[w][row].x - m);
         const float4 x = *reinterpret_cast<const float4*>(so + (w * ROWS + row) * S::pad + d);
-        L = fmaf(warp_ml[w][row].y, f, L);
-        o.x = fmaf(x.x, f, o.x);
-        o.y = fmaf(x.y, f, o.y);
-        o.z = fmaf(x.z, f, o.z);
-        o.w = fmaf(x.w, f, o.w);
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
       }
-      if (begins && ends) {
-        const int64_t at = (it.row0 + rr / group) * a.hq + head * group + rr % group;
-        const float inv = L > 0.f ? 1.f / L : 0.f;
-        IO* out = static_cast<IO*>(a.out) + at * D + d;
-        store4(out, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (a.lse && d == 0) a.lse[at] = (m + log2f(L)) * kLn2;
+      const float inv = q_scale[row];
+      o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      if (whole) {
+        const int tk = over_group(a, rem + row);
+        const int64_t at =
+            (it.row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group;
+        store4(static_cast<IO*>(a.out) + at * D + d, o);
       } else {
         *reinterpret_cast<float4*>(part_o + (slot * ROWS + row) * D + d) = o;
-        if (d == 0) part_ml[slot * ROWS + row] = make_float2(m, L);
       }
     }
-    if (ends && !begins && tid == 0)
-      descs[blockIdx.x] = Desc{n, head, rt, (int)((item_u + kItemUnits) / per)};
     __syncthreads();
   }
 }
@@ -576,32 +621,28 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, cons
   __shared__ float2 sml[kJoinThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Desc d = descs[blockIdx.x];
-  if (d.n < 0) return;
-  Item it;
-  if (!item_of<ROWS>(a, d.n, it)) return;
+  if (d.first < 0) return;
   const int cols = kJoinThreads / groups, g = threadIdx.x / cols;
   const int col = blockIdx.y * cols + threadIdx.x % cols, row = col / (D / 4);
-  const int dim = 4 * (col % (D / 4)), group = a.hq / a.hkv, rr = d.row_tile * ROWS + row;
-  const bool live = rr < it.m * group;
+  const int dim = 4 * (col % (D / 4));
+  const bool live = row < d.rows;
   const int count = live ? (int)blockIdx.x - d.first + 1 : 0;
   // CTA first + i left its part in its second slot where the item began there, else in its first
   const int64_t slot0 = 2 * (int64_t)d.first * ROWS + row;
   float m = kNone, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = g; i < count; i += groups)
-    m = fmaxf(m, part_ml[slot0 + (2 * i + (i == 0)) * ROWS].x);
-#pragma unroll 8
+#pragma unroll 4
   for (int i = g; i < count; i += groups) {
     const int64_t slot = slot0 + (2 * i + (i == 0)) * ROWS;
     const float2 ml = part_ml[slot];
     const float4 x = *reinterpret_cast<const float4*>(part_o + slot * D + dim);
-    const float f = exp2_fast(ml.x - m);
-    L = fmaf(ml.y, f, L);
-    o.x = fmaf(x.x, f, o.x);
-    o.y = fmaf(x.y, f, o.y);
-    o.z = fmaf(x.z, f, o.z);
-    o.w = fmaf(x.w, f, o.w);
+    const float now = fmaxf(m, ml.x), f = exp2_fast(ml.x - now), k = exp2_fast(m - now);
+    m = now;
+    L = fmaf(ml.y, f, L * k);
+    o.x = fmaf(x.x, f, o.x * k);
+    o.y = fmaf(x.y, f, o.y * k);
+    o.z = fmaf(x.z, f, o.z * k);
+    o.w = fmaf(x.w, f, o.w * k);
   }
   if (groups > 1) {
     so[threadIdx.x] = o;
@@ -623,7 +664,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, cons
     }
   }
   if (!live) return;
-  const int64_t at = (it.row0 + rr / group) * a.hq + d.head * group + rr % group;
+  const int tk = over_group(a, d.rem + row);
+  const int64_t at =
+      (d.row0 + d.token0 + tk) * a.hq + d.head * a.group + d.rem + row - tk * a.group;
   const float inv = L > 0.f ? 1.f / L : 0.f;
   store4(static_cast<IO*>(a.out) + at * D + dim,
          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
@@ -635,7 +678,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, cons
 // Tiles of 8 rows a warp carries: as many as the average sequence's rows of a kv head fill (a row
 // tile more reads the cache once more), within the registers (D NT <= 512).
 int row_tiles(const KvArgs& a) {
-  const int64_t rows = (a.T + a.N - 1) / a.N * (a.hq / a.hkv);
+  const int64_t rows = (a.T + a.N - 1) / a.N * a.group;
   return rows <= 8 ? 1 : rows <= 16 || a.D == 256 ? 2 : 4;
 }
 
@@ -650,7 +693,12 @@ cudaError_t launch(const KvArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int ctas = sms * S::ctas < kMaxCtas ? sms * S::ctas : kMaxCtas;
+  // as many CTAs as run together, or as the block table's width can give kMinUnits units
+  const int64_t rows = (a.T + a.N - 1) / a.N * a.group / S::rows + 1;
+  const int64_t most = (((int64_t)a.max_pages << a.page_shift) / kTile + kItemUnits) * a.hkv * a.N *
+                       rows / kMinUnits + 1;
+  int ctas = sms * S::ctas < kMaxCtas ? sms * S::ctas : kMaxCtas;
+  if (ctas > most) ctas = (int)most;
   float* part_o = a.workspace;
   float2* part_ml = reinterpret_cast<float2*>(part_o + (int64_t)2 * kMaxCtas * S::rows * D);
   Desc* descs = reinterpret_cast<Desc*>(part_ml + (int64_t)2 * kMaxCtas * S::rows);
