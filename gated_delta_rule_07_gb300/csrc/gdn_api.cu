@@ -640,8 +640,8 @@ gdn_status check_kv(const gdn_kv_cache* c, const gdn_kv_problem* p) {
   if (c->format != GDN_KV_INT8 && c->format != GDN_KV_E4M3) return GDN_ERR_UNSUPPORTED;
   if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
   if (!head_dim_ok(c->head_dim) || c->hkv > 65535) return GDN_ERR_UNSUPPORTED;
-  // positions are 32-bit; slots of touched pages are grid.x
-  if ((int64_t)p->max_pages * c->page_size > (int64_t)INT32_MAX ||
+  // positions are 32-bit (with room for a tile past the end); slots of touched pages are grid.x
+  if ((int64_t)p->max_pages * c->page_size > (int64_t)1 << 30 ||
       p->total_tokens / c->page_size + 2 * (int64_t)p->num_seqs > (int64_t)INT32_MAX)
     return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
@@ -768,7 +768,9 @@ static gdn_status check_kv_attention(const gdn_kv_cache* cache, const gdn_kv_pro
   if (p->hq < 1 || p->hq % cache->hkv ||
       !strides_ok(p->q_token_stride, p->q_head_stride, p->io_dtype))
     return GDN_ERR_INVALID_ARGUMENT;
-  return p->hq > 32768 ? GDN_ERR_UNSUPPORTED : GDN_OK;
+  // rows (tokens x query heads) are 32-bit
+  return p->hq > 32768 || p->total_tokens * p->hq > (int64_t)INT32_MAX ? GDN_ERR_UNSUPPORTED
+                                                                     : GDN_OK;
 }
 
 size_t gdn_kv_attention_workspace_size(const gdn_kv_cache* cache, const gdn_kv_problem* p) {

@@ -1,0 +1,330 @@
+// gdn_kv_attention.cuh -- what the attention kernels over the 8-bit cache share: the work plan, the
+// codes as fp16, and the join of partial results.
+//
+// Work: units of UNIT keys, of all sequences, kv heads and row tiles in one line, cut into equal
+// runs, one a CTA: ragged lengths balance, and one long sequence fills the GPU.  Items cut between
+// CTAs leave partial sums (M, sum, unnormalised o), joined in order by a second small kernel.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "gdn_kv.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kAttWarps = 4, kAttThreads = 32 * kAttWarps;
+constexpr int kMaxCtas = 608;  // CTAs at most (the workspace holds two partial results of each)
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// The reference M of a row's weights 2^(y - M) stands kHead below the largest score where it was
+// last moved, and moves when a score exceeds it by kSlack (log2): weights stay within fp16's range,
+// and one 2^-22 of the largest still has all of fp16's bits.
+constexpr float kHead = 8.f, kSlack = 15.f;
+constexpr float kNone = -1e30f;  // the reference before any key
+
+// ------------------------------------------------------------------------------ the work plan
+
+struct Item {          // what a sequence asks for
+  int64_t row0;        // its first packed row
+  int m, len;          // query rows (tokens), keys
+  int tile0, tiles;    // tiles of UNIT keys that some row sees
+  int row_tiles;       // tiles of ROWS of the m * group rows of a kv head
+};
+
+// An item is a kv head and row tile of a sequence.  Its units: IDLE ones for its start (queries,
+// joining warps), then its tiles of UNIT keys.
+template <int ROWS, int UNIT, int IDLE> struct Work {
+  static constexpr int unit = UNIT, idle = IDLE, rows = ROWS;
+static __device__ __forceinline__ bool item_of(const KvArgs& a, int n, Item& it) {
+  int64_t b, e;
+  if (a.cu == nullptr && a.N > 1) {
+    b = n;
+    e = n + 1;
+  } else if (!seq_bounds(a.cu, n, a.T, a.status, b, e)) {
+    return false;
+  }
+  if (e <= b) return false;
+  const int len = a.pos0[n];
+  if (len < 0 || len > (int64_t)a.max_pages * a.page) {
+    set_status(a.status, GDN_ERR_DEVICE_INPUT);
+    return false;
+  }
+  it.row0 = b;
+  it.m = (int)(e - b);
+  it.len = len;
+  const int64_t lo = a.window > 0 ? (int64_t)len - it.m - a.window + 1 : 0;
+  it.tile0 = lo > 0 ? (int)(lo / UNIT) : 0;
+  it.tiles = (len + UNIT - 1) / UNIT - it.tile0;
+  if (it.tiles < 1) it.tiles = 1;  // no key at all: a unit that sees nothing writes the zeros
+  it.row_tiles = (int)(((int64_t)it.m * a.group + ROWS - 1) / ROWS);
+  return true;
+}
+static __device__ __forceinline__ int64_t units_of(const KvArgs& a, const Item& it) {
+  return (int64_t)(it.tiles + IDLE) * it.row_tiles * a.hkv;
+}
+};
+// x / y for x >= 0, y > 0 (a quotient that fits an int)
+__device__ __forceinline__ int quotient(int64_t x, int64_t y) {
+  int q = (int)__fdividef((float)x, (float)y);
+  while ((int64_t)q * y > x) --q;
+  while ((int64_t)(q + 1) * y <= x) ++q;
+  return q;
+}
+// x / group for the small x of a row tile (group_mul = 2^32 / group, rounded up)
+__device__ __forceinline__ int over_group(const KvArgs& a, int x) {
+  return a.group == 1 ? x : (int)__umulhi((uint32_t)x, a.group_mul);
+}
+
+// An item that ends in this CTA and began in CTA `first` before it (first < 0: there is none).
+struct Desc {
+  int64_t row0;                 // the sequence's first packed row
+  int first, head, rows;        // kv head, live rows of the row tile
+  int token0, rem;              // row r of the tile: token token0 + (rem + r) / group
+  int unused;
+};
+
+// A CTA's run of units: [u, u1) of the line, `per` a CTA, beginning `off` units into sequence n.
+struct Run {
+  int64_t per, u, u1, off;
+  int n;
+};
+
+// Finds this CTA's run (false: it has none) and clears its descriptor.  Sequences beyond a CTA's
+// threads are walked twice: once for the total, once to find the run's start.
+template <typename W>
+__device__ __forceinline__ bool plan_run(const KvArgs& a, int min_units, Desc* descs, Run& run) {
+  __shared__ int64_t scan[kAttWarps];
+  __shared__ int64_t start_off;
+  __shared__ int start_n;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  int64_t total = 0, per = 0, u = 0;
+  for (int pass = a.N <= kAttThreads; pass < 2; ++pass) {
+    int64_t before = 0;
+    for (int n0 = 0; n0 < a.N; n0 += kAttThreads) {
+      Item it;
+      const int n = n0 + tid;
+      const int64_t w = n < a.N && W::item_of(a, n, it) ? W::units_of(a, it) : 0;
+      int64_t s = w;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += y;
+      }
+      if (lane == 31) scan[warp] = s;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int i = 0; i < kAttWarps; ++i) {
+        if (i < warp) s += scan[i];
+        all += scan[i];
+      }
+      s += before;  // units up to and with sequence n
+      before += all;
+      if (n0 + kAttThreads >= a.N) total = before;
+      if (pass) {
+        if (per == 0) {
+          // (a run may be a little longer than its share: the same in every CTA)
+          per = (int64_t)((float)total * (1.000002f / (float)gridDim.x)) + 1;
+          per = per > min_units ? per : min_units;
+          u = blockIdx.x * per;
+        }
+        if (u < s && u >= s - w) {
+          start_n = n;
+          start_off = u - (s - w);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  const int64_t u1 = u + per < total ? u + per : total;
+  if (tid == 0) descs[blockIdx.x].first = -1;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (u >= u1) return false;
+  run = Run{per, u, u1, start_off, start_n};
+  return true;
+}
+
+// ---------------------------------------------------------------------------------- operands
+
+__device__ __forceinline__ uint4 ld_stream(const uint8_t* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// four codes to two registers of fp16 pairs
+template <bool E4M3>
+__device__ __forceinline__ void open_codes(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (E4M3) {
+    asm("{.reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; "
+        "cvt.rn.f16x2.e4m3x2 %1, b;}" : "=r"(lo), "=r"(hi) : "r"(w));
+  } else {
+    const uint32_t u = w ^ 0x80808080u;  // code + 128; 0x6400 | u is 1024 + u
+    const uint32_t x = __byte_perm(u, 0x64646464u, 0x4140), y = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(x), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(y), "r"(0x64806480u));
+  }
+}
+
+__device__ __forceinline__ void load16(const float* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+    f[4 * i] = v.x; f[4 * i + 1] = v.y; f[4 * i + 2] = v.z; f[4 * i + 3] = v.w;
+  }
+}
+__device__ __forceinline__ void load16(const __nv_bfloat16* p, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[8 * i + 2 * e] = __uint_as_float(u[e] << 16);
+      f[8 * i + 2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+    }
+  }
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                            *reinterpret_cast<const uint32_t*>(&y));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 open_half(uint32_t x) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float log2_fast(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ---------------------------------------------------------------------------------- the join
+
+// Joins the partial results of the item that ended in CTA blockIdx.x and began in an earlier one.
+// A thread takes four channels of a row and every `groups`-th partial, in CTA order; the groups
+// join in shared memory, in order.  Columns (rows x D / 4) are spread over blockIdx.y.
+constexpr int kJoinThreads = 256;
+template <typename IO, int D, int ROWS>
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, const float* part_o,
+                                                                  const float2* part_ml,
+                                                                  const Desc* descs, int groups) {
+  __shared__ float4 so[kJoinThreads];
+  __shared__ float2 sml[kJoinThreads];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Desc d = descs[blockIdx.x];
+  if (d.first < 0) return;
+  const int cols = kJoinThreads / groups, g = threadIdx.x / cols;
+  const int col = blockIdx.y * cols + threadIdx.x % cols, row = col / (D / 4);
+  const int dim = 4 * (col % (D / 4));
+  const bool live = row < d.rows;
+  const int count = live ? (int)blockIdx.x - d.first + 1 : 0;
+  // CTA first + i left its part in its second slot where the item began there, else in its first
+  const int64_t slot0 = 2 * (int64_t)d.first * ROWS + row;
+  float m = kNone, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = g; i < count; i += groups) {
+    const int64_t slot = slot0 + (2 * i + (i == 0)) * ROWS;
+    const float2 ml = part_ml[slot];
+    const float4 x = *reinterpret_cast<const float4*>(part_o + slot * D + dim);
+    const float now = fmaxf(m, ml.x), f = exp2_fast(ml.x - now), k = exp2_fast(m - now);
+    m = now;
+    L = fmaf(ml.y, f, L * k);
+    o.x = fmaf(x.x, f, o.x * k);
+    o.y = fmaf(x.y, f, o.y * k);
+    o.z = fmaf(x.z, f, o.z * k);
+    o.w = fmaf(x.w, f, o.w * k);
+  }
+  if (groups > 1) {
+    so[threadIdx.x] = o;
+    sml[threadIdx.x] = make_float2(m, L);
+    __syncthreads();
+    if (g) return;
+    for (int i = 1; i < groups; ++i) m = fmaxf(m, sml[i * cols + threadIdx.x].x);
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+    L = 0.f;
+    for (int i = 0; i < groups; ++i) {
+      const float2 ml = sml[i * cols + threadIdx.x];
+      const float4 x = so[i * cols + threadIdx.x];
+      const float f = exp2_fast(ml.x - m);
+      L = fmaf(ml.y, f, L);
+      o.x = fmaf(x.x, f, o.x);
+      o.y = fmaf(x.y, f, o.y);
+      o.z = fmaf(x.z, f, o.z);
+      o.w = fmaf(x.w, f, o.w);
+    }
+  }
+  if (!live) return;
+  const int tk = over_group(a, d.rem + row);
+  const int64_t at =
+      (d.row0 + d.token0 + tk) * a.hq + d.head * a.group + d.rem + row - tk * a.group;
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  store4(static_cast<IO*>(a.out) + at * D + dim,
+         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+  if (a.lse && dim == 0) a.lse[at] = (m + log2f(L)) * kLn2;
+}
+
+// --------------------------------------------------------------------------------- launching
+
+struct Workspace {  // two partial results of each CTA, a descriptor of each
+  float* part_o;
+  float2* part_ml;
+  Desc* descs;
+  Workspace(const KvArgs& a, int rows) {
+    part_o = a.workspace;
+    part_ml = reinterpret_cast<float2*>(part_o + (int64_t)2 * kMaxCtas * rows * a.D);
+    descs = reinterpret_cast<Desc*>(part_ml + (int64_t)2 * kMaxCtas * rows);
+  }
+  static size_t bytes(const KvArgs& a, int rows) {
+    const size_t r = (size_t)2 * kMaxCtas * rows;
+    return r * a.D * sizeof(float) + r * sizeof(float2) + kMaxCtas * sizeof(Desc);
+  }
+};
+
+// as many CTAs as run together, or as the block table's width can give min_units units
+template <typename W> int grid_ctas(const KvArgs& a, int resident, int min_units) {
+  const int64_t row_tiles = (a.T + a.N - 1) / a.N * a.group / W::rows + 1;
+  const int64_t most = (((int64_t)a.max_pages << a.page_shift) / W::unit + 1 + W::idle) * a.hkv *
+                       a.N * row_tiles / min_units + 1;
+  const int ctas = resident < kMaxCtas ? resident : kMaxCtas;
+  return ctas < most ? ctas : (int)most;
+}
+
+// The join is launched while the first kernel drains; it waits for its end before it reads.
+template <typename IO, int D, int ROWS>
+cudaError_t launch_join(const KvArgs& a, const Workspace& ws, int ctas, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  // partials of an item, if the sequences are alike: a thread takes about eight of them
+  const int64_t parts = ctas / ((int64_t)a.N * a.hkv);
+  constexpr int all_cols = ROWS * (D / 4);
+  int groups = all_cols < kJoinThreads ? kJoinThreads / all_cols : 1;
+  while (groups < 16 && 8 * groups < parts) groups *= 2;
+  cfg.gridDim = dim3(ctas, all_cols * groups / kJoinThreads);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_attention_join<IO, D, ROWS>, a, (const float*)ws.part_o,
+                            (const float2*)ws.part_ml, (const Desc*)ws.descs, groups);
+}
+
+}  // namespace
+}  // namespace gdn

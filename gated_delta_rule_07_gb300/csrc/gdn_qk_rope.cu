@@ -58,14 +58,6 @@ __device__ __forceinline__ uint2 bf16x4(const float* f) {
 __device__ __forceinline__ void put4(__nv_bfloat16* p, const float* f) {
   *reinterpret_cast<uint2*>(p) = bf16x4(f);
 }
-__device__ __forceinline__ void put8(float* p, const float* f) {
-  put4(p, f);
-  put4(p + 4, f + 4);
-}
-__device__ __forceinline__ void put8(__nv_bfloat16* p, const float* f) {
-  const uint2 x = bf16x4(f), y = bf16x4(f + 4);
-  *reinterpret_cast<uint4*>(p) = make_uint4(x.x, x.y, y.x, y.y);
-}
 
 // A lane's place in a row of the forward: where its two groups of four begin.
 struct Place {
@@ -101,7 +93,7 @@ __device__ __forceinline__ void open_pairs(const Quad<IO>* q, float* a, float* b
 }
 template <bool PAIRS, typename IO>
 __device__ __forceinline__ void put_pairs(IO* row, const Place& p, const float* a, const float* b) {
-  if constexpr (PAIRS) {  // (d1 follows d0)
+  if constexpr (PAIRS) {
     const float f[kVec] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3]};
     put4(row + p.d0, f);
     put4(row + p.d1, f + 4);

@@ -6,9 +6,12 @@ rounding errors of at most 2^-23 of the running sum add up like a walk, sqrt(D) 
 scale, below 2^-14 for the inputs here (D <= 256, sum |q k| scale < 20).  A weight's relative error
 is that of exp: the score's error plus 2^-21.  bf16: weights are rounded to fp16 (2^-11 each), so
 out is off by at most (2^-11 + 2^-14 + ..) sum p |v| and half an ulp of 8 significant bits,
-2^-8 |out|: the bound is 2^-10 sum p |v| + 2^-8 |out|.  fp32: 2^-13 sum p |v| (twice the score's bound).  lse: the score's
+2^-8 |out|; fp16's smallest step,
+2^-24, is 2^-32 of a row's largest weight, so every key may add half that of the largest value: the
+bound is 2^-10 sum p |v| + 2^-8 |out| + 2^-33 keys max |v|.  fp32: 2^-13 sum p |v| (twice the score's bound).  lse: the score's
 bound, 2^-13 with the sum's and log's.
 """
+import itertools
 import math
 
 import pytest
@@ -28,11 +31,11 @@ def gdn():
     return mod
 
 
-def check(out, lse, ref, io, what=""):
+def check(out, lse, ref, io, what="", floor=0.0):
     o, l, mag = ref
     out, lse = out.double().cpu(), lse.double().cpu()
     if io == torch.bfloat16:
-        tol = 2.0 ** -10 * mag + 2.0 ** -8 * o.abs()
+        tol = 2.0 ** -10 * mag + 2.0 ** -8 * o.abs() + floor
     else:
         tol = 2.0 ** -13 * mag
     err = (out - o).abs()
@@ -106,7 +109,8 @@ def test_long_sequences_are_split_and_joined(gdn, io):
     """One long sequence among short ones: work split over its length and joined."""
     lens, new = [20011, 5, 3000, 1], [1, 1, 2, 1]
     for hq, hkv, D, page, fmt in ((8, 1, 128, 64, torch.int8), (4, 2, 64, 16, at.FORMATS[1]),
-                                  (16, 2, 256, 128, torch.int8)):
+                                  (16, 2, 256, 128, torch.int8), (12, 1, 128, 32, at.FORMATS[1]),
+                                  (40, 2, 64, 64, torch.int8), (64, 1, 128, 16, torch.int8)):
         p = Problem(gdn, lens, new, hq, hkv, D, page, fmt, io, seed=D)
         check(*p.run(), p.ref(), io, (hq, D))
 
@@ -120,12 +124,13 @@ def test_many_sequences(gdn):
     check(*p.run(), p.ref(), torch.bfloat16)
 
 
+@pytest.mark.parametrize("hq", [6, 32])  # few rows, and many (another kernel)
 @pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
-def test_bytes_past_the_length_do_not_count(gdn, fmt):
+def test_bytes_past_the_length_do_not_count(gdn, fmt, hq):
     """Unused slots of a last page hold every byte there is (e4m3's NaN codes too), unused table
     entries any number, unused pages' scales NaN: the result does not change by a bit."""
     lens, new, page = [1, 18, 45, 64, 0], [1, 1, 3, 1, 1], 32
-    p = Problem(gdn, lens, new, 6, 2, 128, page, fmt, torch.bfloat16, seed=4)
+    p = Problem(gdn, lens, new, hq, 2, 128, page, fmt, torch.bfloat16, seed=4)
     want = p.run()
     check(*want, p.ref(), torch.bfloat16)
     used = set()
@@ -150,17 +155,33 @@ def test_bytes_past_the_length_do_not_count(gdn, fmt):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_many_rows(gdn):
+    """More rows than one row tile holds, of one sequence and of several; the maximum of a row
+    moves late (large keys at the end) and early; odd counts."""
+    for hq, hkv, D, page, new, lens in ((64, 1, 128, 32, [3, 1], [700, 129]),
+                                        (24, 2, 64, 16, [11, 40], [300, 77]),
+                                        (7, 1, 128, 128, [100], [515]),
+                                        (10, 1, 64, 64, [64, 0, 1], [64, 10, 2])):
+        for fmt in at.FORMATS:
+            for window in (0, 50):
+                p = Problem(gdn, lens, new, hq, hkv, D, page, fmt, torch.bfloat16, seed=hq)
+                late = p.tables[0, (lens[0] - 1) // page]
+                p.ks[late] *= 8
+                p.load()
+                floor = 2.0 ** -33 * max(lens) * float(p.vs.max()) * at.QMAX[fmt]
+                check(*p.run(window), p.ref(window), torch.bfloat16, (hq, D, fmt, window), floor)
+
+
 def test_scales_of_very_different_pages(gdn):
     """Pages whose value scales differ by up to 2^80 and key scales by 2^6, a page of zeros among
     them, with the weight on the page of small values: the sum keeps its relative accuracy."""
-    for fmt in at.FORMATS:
-        for io in at.IOS:
-            p = Problem(gdn, [16 * 6], [1], 2, 1, 128, 16, fmt, io, seed=8, std_q=0.3)
-            ids = p.tables[0].long()
-            p.vs[ids, 0] *= torch.tensor([1.0, 2.0 ** -40, 2.0 ** 40, 2.0 ** -14, 0.0, 1.0])
-            p.ks[ids, 0] *= torch.tensor([1.0, 64.0, 0.01, 1.0, 1.0, 0.0])
-            p.load()
-            check(*p.run(), p.ref(), io, (fmt, io))
+    for fmt, io, hq in itertools.product(at.FORMATS, at.IOS, (2, 12)):
+        p = Problem(gdn, [16 * 6], [1], hq, 1, 128, 16, fmt, io, seed=8, std_q=0.3)
+        ids = p.tables[0].long()
+        p.vs[ids, 0] *= torch.tensor([1.0, 2.0 ** -40, 2.0 ** 40, 2.0 ** -14, 0.0, 1.0])
+        p.ks[ids, 0] *= torch.tensor([1.0, 64.0, 0.01, 1.0, 1.0, 0.0])
+        p.load()
+        check(*p.run(), p.ref(), io, (fmt, io))
     # all the weight on the small page
     p = Problem(gdn, [32], [1], 1, 1, 64, 16, torch.int8, torch.bfloat16, seed=9)
     ids = p.tables[0].long()
