@@ -113,11 +113,13 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 
     // the first tiles are on their way before the queries are
     const int* table = a.table + (int64_t)n * a.max_pages;
-    auto page_of = [&](int tile) {  // a tile's page id (-1: none; its keys are left out)
-      const int key = (it.tile0 + tile) * kTile;
-      if (tile >= tb || key >= it.len) return -1;
-      const int pid = __ldg(table + (key >> a.page_shift));
-      if (pid >= 0 && pid < a.num_pages) return pid;
+    auto has_page = [&](int tile) { return tile < tb && (it.tile0 + tile) * kTile < it.len; };
+    auto entry_of = [&](int tile) {  // the table's entry, loaded a tile before it is looked at
+      return has_page(tile) ? __ldg(table + ((it.tile0 + tile) * kTile >> a.page_shift)) : -1;
+    };
+    auto page_of = [&](int entry, int tile) {  // a tile's page id (-1: none; its keys are left out)
+      if (!has_page(tile)) return -1;
+      if (entry >= 0 && entry < a.num_pages) return entry;
       if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
       return -1;
     };
@@ -154,7 +156,9 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     for (int j = 0; j < KC; ++j) kb[0][j] = kb[1][j] = make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < VC; ++j) vb[j] = make_uint4(0, 0, 0, 0);
-    int tile = ta + warp, pid = page_of(tile), pid_next = page_of(tile + kWarps);
+    int tile = ta + warp;
+    const int entry0 = entry_of(tile);
+    int entry = entry_of(tile + kWarps), pid = page_of(entry0, tile);
     load_k(pid, tile);
     load_v(pid, tile);
 
@@ -235,7 +239,6 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         for (int e = 0; e < 4; ++e) acc[t][i][e] = 0.f;
 
     for (; tile < tb; tile += kWarps) {
-      const int pid_after = page_of(tile + 2 * kWarps);
       float s[NT][4];
 #pragma unroll
       for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
@@ -267,7 +270,9 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         }
       }
       const float k_now = ks, v_now = vs;
+      const int pid_next = page_of(entry, tile + kWarps);
       load_k(pid_next, tile + kWarps);
+      entry = entry_of(tile + 2 * kWarps);
 
       // scores in log2, with the page's value scale; a page of zero values weighs as 2^-100
       const float lv = v_now > 0.f ? log2_fast(v_now) : -100.f;
@@ -357,7 +362,6 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       }
       load_v(pid_next, tile + kWarps);
       pid = pid_next;
-      pid_next = pid_after;
     }
 
     // join the warps: each leaves its maxima and sums, then its o on the common maximum

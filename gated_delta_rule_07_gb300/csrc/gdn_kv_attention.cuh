@@ -92,16 +92,16 @@ struct Run {
 
 // Finds this CTA's run (false: it has none) and clears its descriptor.  Sequences beyond a CTA's
 // threads are walked twice: once for the total, once to find the run's start.
-template <typename W>
+template <typename W, int THREADS = kAttThreads>
 __device__ __forceinline__ bool plan_run(const KvArgs& a, int min_units, Desc* descs, Run& run) {
-  __shared__ int64_t scan[kAttWarps];
+  __shared__ int64_t scan[THREADS / 32];
   __shared__ int64_t start_off;
   __shared__ int start_n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   int64_t total = 0, per = 0, u = 0;
-  for (int pass = a.N <= kAttThreads; pass < 2; ++pass) {
+  for (int pass = a.N <= THREADS; pass < 2; ++pass) {
     int64_t before = 0;
-    for (int n0 = 0; n0 < a.N; n0 += kAttThreads) {
+    for (int n0 = 0; n0 < a.N; n0 += THREADS) {
       Item it;
       const int n = n0 + tid;
       const int64_t w = n < a.N && W::item_of(a, n, it) ? W::units_of(a, it) : 0;
@@ -115,13 +115,13 @@ __device__ __forceinline__ bool plan_run(const KvArgs& a, int min_units, Desc* d
       __syncthreads();
       int64_t all = 0;
 #pragma unroll
-      for (int i = 0; i < kAttWarps; ++i) {
+      for (int i = 0; i < THREADS / 32; ++i) {
         if (i < warp) s += scan[i];
         all += scan[i];
       }
       s += before;  // units up to and with sequence n
       before += all;
-      if (n0 + kAttThreads >= a.N) total = before;
+      if (n0 + THREADS >= a.N) total = before;
       if (pass) {
         if (per == 0) {
           // (a run may be a little longer than its share: the same in every CTA)
