@@ -15,7 +15,8 @@
 //     rescaled.  The sums of the weights stay in the threads' registers until the item ends.
 //   * One CTA an SM, its warps in three parts that hand steps to each other by mbarriers, each
 //     buffer twice: eight warps load codes (a step ahead, in registers) and open them; eight turn
-//     scores into weights; one thread issues the products, S^T of a step before O^T of the last.
+//     scores into weights; a thread of the first part issues the products, S^T of a step before
+//     O^T of the last (a warp of its own would leave each thread 96 registers, not 128).
 //     So opening, softmax and products of different steps run side by side.  (All in one part, two
 //     CTAs an SM, took 2.5 times as long: each step's chain of waits in a row.)
 // Work is cut as in the other kernel, in units of 128 keys.
@@ -27,8 +28,8 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kOpenWarps = 8, kSoftWarps = 8;  // then the warp that issues the products
-constexpr int kTcThreads = 32 * (kOpenWarps + kSoftWarps + 1);
+constexpr int kOpenWarps = 8, kSoftWarps = 8;
+constexpr int kTcThreads = 32 * (kOpenWarps + kSoftWarps);
 constexpr int kRows = 64;        // query rows of an item: columns of S^T and O^T
 constexpr int kKeys = 128;       // keys of a step, lanes of S^T
 constexpr int kTcMinUnits = 2;   // steps of a CTA at least
@@ -239,6 +240,37 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       const int v_chunk = 2 * (warp & 3) + g, v_row = 4 * (x & 1);
       const uint8_t* const kp = a.k_codes + r * D + 16 * c4;
       const uint8_t* const vp = a.v_codes + 8 * g * D + 16 * x;
+      // The products, issued by one thread (of warp 0): S^T of a step, and O^T, begun or added to.
+      auto issue_scores = [&](uint32_t step) {
+        if (lane == 0) {
+          wait_one(bar(kKeysIn, step), parity(step), failed);
+          if (step >= 2) wait_one(bar(kScoresRead, step), parity(step - 2), failed);
+          fence_after_sync();
+          const uint32_t k = base + TcSmem::K + (step & 1) * TcSmem::tile;
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s)
+            mma_ss(tm + 64 * (step & 1), sdesc(k + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
+                   sdesc(base + TcSmem::Q + (s >> 2) * (kRows * 128) + (s & 3) * 32, 16, 1024),
+                   idesc_f16(128, 64, 0, 0), s > 0);
+          mma_commit(bar(kScoresDone, step));
+        }
+        __syncwarp();
+      };
+      auto issue_sum = [&](uint32_t step, bool begin) {
+        if (lane == 0) {
+          wait_one(bar(kValuesIn, step), parity(step), failed);
+          wait_one(bar(kWeightsIn, step), parity(step), failed);
+          fence_after_sync();
+          const uint32_t v = base + TcSmem::V + (step & 1) * TcSmem::tile;
+          const uint32_t p = base + TcSmem::P + (step & 1) * TcSmem::p_tile;
+#pragma unroll
+          for (int s = 0; s < kKeys / 16; ++s)
+            mma_ss(tm + 128, sdesc(v + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
+                   sdesc(p + s * 2048, 128 * 128, 1024), idesc_f16(128, 64, 0, 1), !begin || s > 0);
+          mma_commit(bar(kSumDone, step));
+        }
+        __syncwarp();
+      };
       uint4 kb[2][KC], vb[VC][2];
       int64_t from = 0;  // where the warp's keys, and its values, begin
       auto load_k = [&](int pid, int tile) {
@@ -290,6 +322,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kKeysIn, step));
         load_k(pid, tile + 1);
+        if (warp == 0) issue_scores(step);
         if (E4M3 && first + kKeys > it.len) {  // bytes past the length: no NaN under weights of 0
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -329,8 +362,10 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kValuesIn, step));
         load_v(pid);
+        if (warp == 0 && tile > ta) issue_sum(step - 1, tile == ta + 1);
       }
-    } else if (warp < kOpenWarps + kSoftWarps) {
+      if (warp == 0) issue_sum(step - 1, tb == ta + 1);
+    } else {
       // ------------------------------------------------------------------ scores to weights
       // Tensor Memory: lanes (keys, channels) 32 quarter + lane; columns (rows) 32 i + 16 half
       // + 0 .. 15
@@ -527,41 +562,8 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         __syncwarp();
       }
       fence_before_sync();
-    } else if (lane == 0) {
-      // ------------------------------------------------------------------ the products
-      const uint32_t id = idesc_f16(128, 64, 0, 0), id_pv = idesc_f16(128, 64, 0, 1);
-      const int steps = tb - ta;
-      for (int i = 0; i <= steps; ++i) {
-        const uint32_t step = step0 + i;
-        if (i < steps) {  // S^T of this step
-          wait_one(bar(kKeysIn, step), parity(step), failed);
-          if (step >= 2) wait_one(bar(kScoresRead, step), parity(step - 2), failed);
-          fence_after_sync();
-          const uint32_t k = base + TcSmem::K + (step & 1) * TcSmem::tile;
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_ss(tm + 64 * (step & 1), sdesc(k + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
-                   sdesc(base + TcSmem::Q + (s >> 2) * (kRows * 128) + (s & 3) * 32, 16, 1024), id,
-                   s > 0);
-          mma_commit(bar(kScoresDone, step));
-        }
-        if (i > 0) {  // O^T of the last
-          const uint32_t prev = step - 1;
-          wait_one(bar(kValuesIn, prev), parity(prev), failed);
-          wait_one(bar(kWeightsIn, prev), parity(prev), failed);
-          fence_after_sync();
-          const uint32_t v = base + TcSmem::V + (prev & 1) * TcSmem::tile;
-          const uint32_t p = base + TcSmem::P + (prev & 1) * TcSmem::p_tile;
-#pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            mma_ss(tm + 128, sdesc(v + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
-                   sdesc(p + s * 2048, 128 * 128, 1024), id_pv, i > 1 || s > 0);
-          mma_commit(bar(kSumDone, prev));
-        }
-      }
     }
     step0 += tb - ta;
-    __syncwarp();  // (the warp of the one thread that issues)
     __syncthreads();
     fence_after_sync();
   }
