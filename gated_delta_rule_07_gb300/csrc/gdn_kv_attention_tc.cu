@@ -15,10 +15,10 @@
 //     rescaled.  The sums of the weights stay in the threads' registers until the item ends.
 //   * One CTA an SM, its warps in three parts that hand steps to each other by mbarriers, each
 //     buffer twice: eight warps load codes (a step ahead, in registers) and open them; eight turn
-//     scores into weights; a thread of the first part issues the products, S^T of a step before
-//     O^T of the last (a warp of its own would leave each thread 96 registers, not 128).
-//     So opening, softmax and products of different steps run side by side.  (All in one part, two
-//     CTAs an SM, took 2.5 times as long: each step's chain of waits in a row.)
+//     scores into weights; one thread issues the products, S^T of a step before O^T of the last;
+//     one warp looks pages and scales up, a few steps ahead, for all of them.  So opening, softmax
+//     and products of different steps run side by side, and each part's chain of instructions a
+//     step, which is what bounds the kernel, is short.
 // Work is cut as in the other kernel, in units of 128 keys.
 #include "gdn_kv_attention.cuh"
 #include "gdn_sm100.cuh"
@@ -28,8 +28,9 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kOpenWarps = 8, kSoftWarps = 8;
-constexpr int kTcThreads = 32 * (kOpenWarps + kSoftWarps);
+constexpr int kOpenWarps = 8, kSoftWarps = 8;  // then one that issues, one that looks pages up
+constexpr int kTcThreads = 32 * (kOpenWarps + kSoftWarps + 2);
+constexpr int kAhead = 4;        // steps whose pages are known at a time
 constexpr int kRows = 64;        // query rows of an item: columns of S^T and O^T
 constexpr int kKeys = 128;       // keys of a step, lanes of S^T
 constexpr int kTcMinUnits = 2;   // steps of a CTA at least
@@ -44,20 +45,37 @@ struct TcSmem {  // byte offsets, each operand tile on a 1024-byte boundary
   static constexpr int P = V + 2 * tile;      // 2 x [128 keys][64 rows]
   static constexpr int p_tile = 128 * 64 * 2;
   static constexpr int Q = P + 2 * p_tile;    // [64 rows][D], 64-channel blocks
-  static constexpr int row_c = Q + 64 * 128 * 2;     // float2 {score scale, reference} of a row
-  static constexpr int row_f = row_c + 64 * 8;       // float: rescaling of a row
-  static constexpr int row_d = row_f + 64 * 4;       // float: a row's reference before its last move
+  // float4 {a0, a1, b0, b1} of a pair of rows: score scale, minus the reference
+  static constexpr int row_ab = Q + 64 * 128 * 2;
+  static constexpr int row_f = row_ab + 64 * 8;      // float: rescaling of a row
+  static constexpr int row_d = row_f + 64 * 4;       // float: minus a row's reference before it moved
   static constexpr int row_last = row_d + 64 * 4;    // int: the last key a row sees
   static constexpr int wmax = row_last + 64 * 4;     // float [4 quarters][64]
-  static constexpr int bars = wmax + 4 * 64 * 4;     // mbarriers, two of each of the six below
-  static constexpr int tmem = bars + 12 * 8;
+  static constexpr int runs = wmax + 4 * 64 * 4;     // PageRun [kAhead][8]
+  static constexpr int bars = runs + kAhead * 8 * 32;  // mbarriers, see below
+  static constexpr int tmem = bars + (10 + 2 * kAhead) * 8;
   static constexpr int failed = tmem + 4;
-  static constexpr int bytes = failed + 4 + 1024;    // (the base is rounded up to 1024)
+  static constexpr int item = failed + 4;            // ItemState
+  static constexpr int bytes = item + 64 + 1024;     // (the base is rounded up to 1024)
   static constexpr int sums = K;  // float [64][129], at the end of an item
 };
-// The mbarriers of a buffer: its keys (values, weights) are in place; S^T is done, so the key tile
-// is free again; O^T is done, so the value and weight tiles are; S^T has been read.
-enum { kKeysIn = 0, kValuesIn = 2, kWeightsIn = 4, kScoresDone = 6, kSumDone = 8, kScoresRead = 10 };
+// A step's run of 16 keys, all within a page: where its codes begin (< 0: it has no page), its key
+// scale, log2 of its value scale, and that scale's inverse.
+struct alignas(16) PageRun {
+  int64_t from, unused;
+  float ks, lv, rv, unused2;
+};
+// What the item loop needs again after an item (kept out of the registers in between).
+struct ItemState {
+  int64_t u, off, per, u1, row0, first_u;
+  int n;
+};
+static_assert(sizeof(PageRun) == 32 && sizeof(ItemState) <= 64, "TcSmem");
+// The mbarriers.  Two of each, for the steps that use a buffer in turn: its keys, values, weights
+// are in place; S^T is done, so the key tile is free again; O^T is done, so the value and weight
+// tiles are.  kAhead of each: S^T has been read (and the step's runs); the step's runs are in place.
+enum { kKeysIn = 0, kValuesIn = 2, kWeightsIn = 4, kScoresDone = 6, kSumDone = 8 };
+constexpr int kScoresRead = 10, kPagesIn = kScoresRead + kAhead;
 
 __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
@@ -66,9 +84,39 @@ __device__ __forceinline__ void sts16(uint32_t a, uint32_t x, uint32_t y, uint32
 
 // sixteen columns of this warp's lanes, loaded and waited for
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  uint32_t none[16] = {};
-  tmem_ld16_nw(taddr, r);
-  tmem_wait_ld16x2(r, none);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// two fp32 in a 64-bit register: one instruction for both
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 // Bounded wait: sleeps in hardware; gives up after about a second, or when another thread has.
 __device__ __forceinline__ void wait_one(uint32_t bar, uint32_t parity, volatile int* failed) {
@@ -101,23 +149,43 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   constexpr int KC = D / 64, VC = D / 64;
   extern __shared__ char smem_raw[];
-  Run run;
-  if (!plan_run<TcWork, kTcThreads>(a, kTcMinUnits, descs, run)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   char* const sm = smem_raw + (base - raw);
-  float2* const row_c = reinterpret_cast<float2*>(sm + TcSmem::row_c);
+  float4* const row_ab = reinterpret_cast<float4*>(sm + TcSmem::row_ab);
   float* const row_f = reinterpret_cast<float*>(sm + TcSmem::row_f);
   float* const row_d = reinterpret_cast<float*>(sm + TcSmem::row_d);
   int* const row_last = reinterpret_cast<int*>(sm + TcSmem::row_last);
   float* const wmax = reinterpret_cast<float*>(sm + TcSmem::wmax);
+  PageRun* const runs = reinterpret_cast<PageRun*>(sm + TcSmem::runs);
+  volatile ItemState* const state = reinterpret_cast<volatile ItemState*>(sm + TcSmem::item);
   volatile int* const failed = reinterpret_cast<volatile int*>(sm + TcSmem::failed);
   const uint32_t bars = base + TcSmem::bars;
+  auto score_scale = [&](int row) -> float& {
+    return reinterpret_cast<float*>(row_ab)[4 * (row >> 1) + (row & 1)];
+  };
+  auto minus_ref = [&](int row) -> float& {
+    return reinterpret_cast<float*>(row_ab)[4 * (row >> 1) + 2 + (row & 1)];
+  };
   auto bar = [&](int which, uint32_t step) { return bars + 8 * (which + (step & 1)); };
+  auto read_bar = [&](uint32_t step) { return bars + 8 * (kScoresRead + step % kAhead); };
+  auto pages_bar = [&](uint32_t step) { return bars + 8 * (kPagesIn + step % kAhead); };
   // a step's buffers are used every other step: the parity of its own use of a barrier
   auto parity = [](uint32_t step) { return (step >> 1) & 1; };
+  auto parity4 = [](uint32_t step) { return (step / kAhead) & 1; };
 
+  {
+    Run run;
+    if (!plan_run<TcWork, kTcThreads>(a, kTcMinUnits, descs, run)) return;
+    if (tid == 0) {
+      state->u = run.u;
+      state->off = run.off;
+      state->per = run.per;
+      state->u1 = run.u1;
+      state->n = run.n;
+    }
+  }
   if (warp == 0) {
     tmem_alloc(base + TcSmem::tmem, 256);
     tmem_relinquish();
@@ -129,7 +197,10 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       mbar_init(bars + 8 * (kWeightsIn + b), kSoftWarps);
       mbar_init(bars + 8 * (kScoresDone + b), 1);
       mbar_init(bars + 8 * (kSumDone + b), 1);
+    }
+    for (int b = 0; b < kAhead; ++b) {
       mbar_init(bars + 8 * (kScoresRead + b), kSoftWarps);
+      mbar_init(bars + 8 * (kPagesIn + b), 1);
     }
     *failed = 0;
   }
@@ -141,51 +212,39 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + TcSmem::tmem);  // S^T, S^T, O^T
 
   uint32_t step0 = 0;  // steps of the items before this one
-  int n = run.n;
-  int64_t u = run.u, off = run.off;
-  while (u < run.u1 && n < a.N && !*failed) {
+  while (!*failed) {
+    const int64_t u = state->u, off = state->off, u1 = state->u1;
+    const int n = state->n;
+    if (u >= u1 || n >= a.N) break;
+    __syncthreads();  // (the state is read before it moves on)
     Item it;
     if (!TcWork::item_of(a, n, it) || off >= TcWork::units_of(a, it)) {
-      ++n;
-      off = 0;
+      if (tid == 0) {
+        state->n = n + 1;
+        state->off = 0;
+      }
+      __syncthreads();
       continue;
     }
     const int span = it.tiles + kTcItemUnits;
     const int which = quotient(off, span);
     const int at0 = (int)(off - (int64_t)which * span);
-    const int at1 = (int)(span < at0 + (run.u1 - u) ? span : at0 + (run.u1 - u));
-    const int64_t item_u = u - at0;
-    u += at1 - at0;
-    off += at1 - at0;
+    const int at1 = (int)(span < at0 + (u1 - u) ? span : at0 + (u1 - u));
     const int ta = max(at0 - kTcItemUnits, 0), tb = max(at1 - kTcItemUnits, 0);
-    if (ta >= tb) continue;
+    if (tid == 0) {
+      state->u = u + at1 - at0;
+      state->off = off + at1 - at0;
+      state->row0 = it.row0;
+      state->first_u = u - at0 + kTcItemUnits;
+    }
+    if (ta >= tb) {
+      __syncthreads();
+      continue;
+    }
     const int head = (uint32_t)which / (uint32_t)it.row_tiles;
     const int row_base = (which - head * it.row_tiles) * kRows;
     const int rows = min(kRows, it.m * a.group - row_base);
     const int token0 = (uint32_t)row_base / (uint32_t)a.group, rem = row_base - token0 * a.group;
-
-    // Page ids of a step's run of 16 keys.  The table's entry is loaded a step before it is looked
-    // at.
-    const int* table = a.table + (int64_t)n * a.max_pages;
-    auto has_page = [&](int tile, int run16) {
-      return tile < tb && (it.tile0 + tile) * kKeys + 16 * run16 < it.len;
-    };
-    auto entry_of = [&](int tile, int run16) {
-      const int key = (it.tile0 + tile) * kKeys + 16 * run16;
-      return has_page(tile, run16) ? __ldg(table + (key >> a.page_shift)) : -1;
-    };
-    auto page_of = [&](int entry, int tile, int run16) {  // -1: none
-      if (!has_page(tile, run16)) return -1;
-      if (entry >= 0 && entry < a.num_pages) return entry;
-      if (lane == 0) set_status(a.status, GDN_ERR_DEVICE_INPUT);
-      return -1;
-    };
-    // keys that every live row sees: [all_lo, all_hi]
-    const int all_hi = it.len - it.m + token0;
-    const int64_t all_lo = a.window > 0 ? (int64_t)it.len - it.m + token0 +
-                                              over_group(a, rem + rows - 1) - a.window + 1
-                                        : INT64_MIN;
-    const bool begins = ta == 0, ends = tb == it.tiles, whole = begins && ends;
 
     // queries: scaled by a power of two into [1, 2), fp16; a thread has 16 channels of a row
 #pragma unroll 1
@@ -209,8 +268,8 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
       if (chunk == 0) {
         // (a row that is not live has a reference that nothing exceeds: weights 0)
-        row_c[row] = make_float2(__uint_as_float((uint32_t)ex << 23) * (a.scale * kLog2e),
-                                 live ? kNone : -kNone);
+        score_scale(row) = __uint_as_float((uint32_t)ex << 23) * (a.scale * kLog2e);
+        minus_ref(row) = live ? -kNone : kNone;
         row_last[row] = live ? it.len - it.m + token0 + tk : -1;
       }
       const uint32_t at = base + TcSmem::Q + (chunk / 4) * (kRows * 128) + row * 128;
@@ -240,68 +299,34 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       const int v_chunk = 2 * (warp & 3) + g, v_row = 4 * (x & 1);
       const uint8_t* const kp = a.k_codes + r * D + 16 * c4;
       const uint8_t* const vp = a.v_codes + 8 * g * D + 16 * x;
-      // The products, issued by one thread (of warp 0): S^T of a step, and O^T, begun or added to.
-      auto issue_scores = [&](uint32_t step) {
-        if (lane == 0) {
-          wait_one(bar(kKeysIn, step), parity(step), failed);
-          if (step >= 2) wait_one(bar(kScoresRead, step), parity(step - 2), failed);
-          fence_after_sync();
-          const uint32_t k = base + TcSmem::K + (step & 1) * TcSmem::tile;
-#pragma unroll
-          for (int s = 0; s < D / 16; ++s)
-            mma_ss(tm + 64 * (step & 1), sdesc(k + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
-                   sdesc(base + TcSmem::Q + (s >> 2) * (kRows * 128) + (s & 3) * 32, 16, 1024),
-                   idesc_f16(128, 64, 0, 0), s > 0);
-          mma_commit(bar(kScoresDone, step));
-        }
-        __syncwarp();
-      };
-      auto issue_sum = [&](uint32_t step, bool begin) {
-        if (lane == 0) {
-          wait_one(bar(kValuesIn, step), parity(step), failed);
-          wait_one(bar(kWeightsIn, step), parity(step), failed);
-          fence_after_sync();
-          const uint32_t v = base + TcSmem::V + (step & 1) * TcSmem::tile;
-          const uint32_t p = base + TcSmem::P + (step & 1) * TcSmem::p_tile;
-#pragma unroll
-          for (int s = 0; s < kKeys / 16; ++s)
-            mma_ss(tm + 128, sdesc(v + (s >> 2) * 16384 + (s & 3) * 32, 16, 1024),
-                   sdesc(p + s * 2048, 128 * 128, 1024), idesc_f16(128, 64, 0, 1), !begin || s > 0);
-          mma_commit(bar(kSumDone, step));
-        }
-        __syncwarp();
-      };
       uint4 kb[2][KC], vb[VC][2];
-      int64_t from = 0;  // where the warp's keys, and its values, begin
-      auto load_k = [&](int pid, int tile) {
-        const int slot = ((it.tile0 + tile) * kKeys + 16 * warp) & (a.page - 1);
-        from = ((int64_t)pid * a.hkv + head) * (a.page * D) + slot * D;
+      auto load_k = [&](int64_t from) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int h = 0; h < KC; ++h)
-            kb[j][h] = pid >= 0 ? ld_stream(kp + from + 8 * D * j + 64 * h)
-                                : make_uint4(0u, 0u, 0u, 0u);
+            kb[j][h] = from >= 0 ? ld_stream(kp + from + 8 * D * j + 64 * h)
+                                 : make_uint4(0u, 0u, 0u, 0u);
       };
-      auto load_v = [&](int pid) {
+      auto load_v = [&](int64_t from) {
 #pragma unroll
         for (int i = 0; i < VC; ++i)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            vb[i][t] = pid >= 0 ? ld_stream(vp + from + 256 * i + 4 * D * t)
-                                : make_uint4(0u, 0u, 0u, 0u);
+            vb[i][t] = from >= 0 ? ld_stream(vp + from + 256 * i + 4 * D * t)
+                                 : make_uint4(0u, 0u, 0u, 0u);
       };
+      auto from_of = [&](uint32_t step) {  // (once its pages are in)
+        return *reinterpret_cast<volatile int64_t*>(&runs[step % kAhead * 8 + warp].from);
+      };
+      wait_bar(pages_bar(step0), parity4(step0), failed);
       {
-        const int pid = page_of(entry_of(ta, warp), ta, warp);
-        load_k(pid, ta);
-        load_v(pid);
+        const int64_t from = from_of(step0);
+        load_k(from);
+        load_v(from);
       }
-      int entry = entry_of(ta + 1, warp);
       uint32_t step = step0;
       for (int tile = ta; tile < tb; ++tile, ++step) {
-        const int first = (it.tile0 + tile) * kKeys;
-        const int pid = page_of(entry, tile + 1, warp);
-        entry = entry_of(tile + 2, warp);
         const uint32_t at = (step & 1) * TcSmem::tile;
         if (step >= 2) wait_bar(bar(kScoresDone, step), parity(step - 2), failed);
 #pragma unroll
@@ -321,12 +346,17 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kKeysIn, step));
-        load_k(pid, tile + 1);
-        if (warp == 0) issue_scores(step);
-        if (E4M3 && first + kKeys > it.len) {  // bytes past the length: no NaN under weights of 0
+        int64_t from = -1;
+        if (tile + 1 < tb) {
+          wait_bar(pages_bar(step + 1), parity4(step + 1), failed);
+          from = from_of(step + 1);
+        }
+        load_k(from);
+        const int left = it.len - (it.tile0 + tile) * kKeys - 16 * warp;  // keys up to the length
+        if (E4M3 && left < 16) {  // bytes past the length: no NaN under their weights of 0
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const int keep = min(max(it.len - first - 16 * warp - 8 * g - 4 * t, 0), 4);
+            const int keep = min(max(left - 8 * g - 4 * t, 0), 4);
             const uint32_t mask = keep == 4 ? 0xffffffffu : (1u << (8 * keep)) - 1u;
 #pragma unroll
             for (int i = 0; i < VC; ++i) {
@@ -361,45 +391,37 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kValuesIn, step));
-        load_v(pid);
-        if (warp == 0 && tile > ta) issue_sum(step - 1, tile == ta + 1);
+        load_v(from);
       }
-      if (warp == 0) issue_sum(step - 1, tb == ta + 1);
-    } else {
+    } else if (warp < kOpenWarps + kSoftWarps) {
       // ------------------------------------------------------------------ scores to weights
       // Tensor Memory: lanes (keys, channels) 32 quarter + lane; columns (rows) 32 i + 16 half
       // + 0 .. 15
       const int sw = warp - kOpenWarps, quarter = sw & 3, half = sw >> 2;
       const int tm_lane = 32 * quarter + lane, own = 2 * quarter + (lane >> 4), st = 32 * sw + lane;
       const uint32_t tm_q = tm + ((uint32_t)(quarter * 32) << 16), tm_o = tm_q + 128;
-      float l[kRows / 2];  // sums of the weights of this thread's key and rows
+      // keys that every live row sees: [all_lo, all_hi]
+      const int all_hi = it.len - it.m + token0;
+      const int64_t lo = (int64_t)all_hi + over_group(a, rem + rows - 1) - a.window + 1;
+      const int all_lo = a.window > 0 && lo > 0 ? (int)lo : 0;
+      uint64_t l[kRows / 4];  // sums of the weights of this thread's key, two rows a register
 #pragma unroll
-      for (int i = 0; i < kRows / 2; ++i) l[i] = 0.f;
-      float ks = 0.f, vs = 0.f;  // this thread's key: its scales (vs < 0: it has no page)
-      auto load_scales = [&](int pid) {
-        const int64_t block = (int64_t)pid * a.hkv + head;
-        ks = pid >= 0 ? __ldg(a.k_scale + block) : 0.f;
-        vs = pid >= 0 ? __ldg(a.v_scale + block) : -1.f;
-      };
-      load_scales(page_of(entry_of(ta, own), ta, own));
-      int entry = entry_of(ta + 1, own);
+      for (int i = 0; i < kRows / 4; ++i) l[i] = 0;
       uint32_t step = step0;
       for (int tile = ta; tile < tb; ++tile, ++step) {
         const int first = (it.tile0 + tile) * kKeys, key = first + tm_lane;
         const bool open = first + kKeys - 1 <= all_hi && first >= all_lo;
         const uint32_t tm_s = tm_q + 64 * (step & 1);
         const uint32_t p_at = base + TcSmem::P + (step & 1) * TcSmem::p_tile + tm_lane * 128;
-        // a page of zero values weighs as 2^-100; keys without a page not at all
-        const float k_now = ks;
-        const float lv = vs > 0.f ? log2_fast(vs) : vs < 0.f ? -CUDART_INF_F : -100.f;
-        const float rv = vs < 0.f ? 0.f : exp2_fast(-lv);
-        load_scales(page_of(entry, tile + 1, own));
-        entry = entry_of(tile + 2, own);
-        if (step >= 2) wait_bar(bar(kSumDone, step), parity(step - 2), failed);  // (the weight tile)
+        // S^T of this step is done, so is O^T of the one before the last (issued before it): the
+        // weight tile is free.  The keys were in place before S^T was begun, so the pages were.
         wait_bar(bar(kScoresDone, step), parity(step), failed);
         fence_after_sync();
+        const float4 run = *reinterpret_cast<const float4*>(&runs[step % kAhead * 8 + own].ks);
+        const float ks = run.x, lv = run.y, rv = run.z;
+        const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), rv2 = pair(rv, rv);
         auto seen = [&](int la) {
-          return key <= la && (a.window == 0 || (int64_t)key > (int64_t)la - a.window);
+          return key <= la && (a.window == 0 || key > la - a.window);
         };
         // A score above its row's reference by more than kSlack counts as kSlack here; if there is
         // one, its part is taken out of the sums again, the references move, and the weights are
@@ -414,9 +436,11 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             tmem_ld16(tm_s + 16 * c, s);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              const float4 rc = *reinterpret_cast<const float4*>(row_c + 16 * c + i);
-              float y0 = fmaf(__uint_as_float(s[i]), k_now * rc.x, lv - rc.y);
-              float y1 = fmaf(__uint_as_float(s[i + 1]), k_now * rc.z, lv - rc.w);
+              const ulonglong2 ab = *reinterpret_cast<const ulonglong2*>(row_ab + 8 * c + i / 2);
+              const uint64_t s2 = pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+              const uint64_t a2 = mul2(ks2, ab.x);
+              float y0, y1;
+              unpair(fma2(s2, a2, add2(lv2, ab.y)), y0, y1);
               if (!open) {
                 const int2 la = *reinterpret_cast<const int2*>(row_last + 16 * c + i);
                 y0 = seen(la.x) ? y0 : -CUDART_INF_F;
@@ -424,17 +448,16 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
               }
               top = fmaxf(top, fmaxf(y0, y1));
               const float w0 = exp2_fast(fminf(y0, kSlack)), w1 = exp2_fast(fminf(y1, kSlack));
-              float &l0 = l[16 * cc + i], &l1 = l[16 * cc + i + 1];
+              uint64_t& l2 = l[8 * cc + i / 2];
               if (again) {
                 // (the very comparison of the first time, against the reference of then)
-                const float2 was = *reinterpret_cast<const float2*>(row_d + 16 * c + i);
-                const float z0 = fmaf(__uint_as_float(s[i]), k_now * rc.x, lv - was.x);
-                const float z1 = fmaf(__uint_as_float(s[i + 1]), k_now * rc.z, lv - was.y);
-                l0 = y0 > -CUDART_INF_F && z0 > kSlack ? fmaf(w0, rv, l0) : l0;
-                l1 = y1 > -CUDART_INF_F && z1 > kSlack ? fmaf(w1, rv, l1) : l1;
+                const uint64_t was = *reinterpret_cast<const uint64_t*>(row_d + 16 * c + i);
+                float z0, z1;
+                unpair(fma2(s2, a2, add2(lv2, was)), z0, z1);
+                l2 = fma2(pair(y0 > -CUDART_INF_F && z0 > kSlack ? w0 : 0.f,
+                               y1 > -CUDART_INF_F && z1 > kSlack ? w1 : 0.f), rv2, l2);
               } else {
-                l0 = fmaf(w0, rv, l0);
-                l1 = fmaf(w1, rv, l1);
+                l2 = fma2(pair(w0, w1), rv2, l2);
               }
               p[i / 2] = pack_half(w0, w1);
             }
@@ -455,26 +478,40 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             uint32_t s[16];
             tmem_ld16(tm_s + 16 * c, s);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 rc = row_c[16 * c + i];
-              const bool in = seen(row_last[16 * c + i]);
-              const float z = fmaf(__uint_as_float(s[i]), k_now * rc.x, lv - rc.y);
-              if (in && z > kSlack) l[16 * cc + i] = fmaf(-exp2_fast(kSlack), rv, l[16 * cc + i]);
-              float y = in ? fmaf(__uint_as_float(s[i]), k_now * rc.x, lv) : -CUDART_INF_F;
+            for (int i = 0; i < 16; i += 2) {
+              const ulonglong2 ab = *reinterpret_cast<const ulonglong2*>(row_ab + 8 * c + i / 2);
+              const int2 la = *reinterpret_cast<const int2*>(row_last + 16 * c + i);
+              const uint64_t s2 = pair(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+              const uint64_t a2 = mul2(ks2, ab.x);
+              float y0, y1, z0, z1;
+              unpair(fma2(s2, a2, add2(lv2, ab.y)), z0, z1);
+              unpair(fma2(s2, a2, lv2), y0, y1);
+              const bool in0 = seen(la.x), in1 = seen(la.y);
+              const float over = -exp2_fast(kSlack);
+              l[8 * cc + i / 2] = fma2(pair(in0 && z0 > kSlack ? over : 0.f,
+                                            in1 && z1 > kSlack ? over : 0.f), rv2, l[8 * cc + i / 2]);
+              y0 = in0 ? y0 : -CUDART_INF_F;
+              y1 = in1 ? y1 : -CUDART_INF_F;
 #pragma unroll
-              for (int o = 16; o; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-              if (lane == 0) wmax[quarter * kRows + 16 * c + i] = y;
+              for (int o = 16; o; o >>= 1) {
+                y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
+                y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
+              }
+              if (lane == 0) {
+                wmax[quarter * kRows + 16 * c + i] = y0;
+                wmax[quarter * kRows + 16 * c + i + 1] = y1;
+              }
             }
           }
           soft_or(false);
           if (st < rows) {
-            const float was = row_c[st].y;
+            const float was = -minus_ref(st);
             float m = was;
 #pragma unroll
             for (int q = 0; q < 4; ++q) m = fmaxf(m, wmax[q * kRows + st] - kHead);
             row_f[st] = exp2_fast(was - m);
-            row_d[st] = was;
-            row_c[st].y = m;
+            row_d[st] = -was;
+            minus_ref(st) = -m;
           }
           soft_or(false);
 #pragma unroll
@@ -484,10 +521,14 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             uint32_t s[16];
             if (tile > ta) tmem_ld16(tm_o + 16 * c, s);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float f = 16 * c + i < rows ? row_f[16 * c + i] : 1.f;
-              l[16 * cc + i] *= f;
-              if (tile > ta) s[i] = __float_as_uint(__uint_as_float(s[i]) * f);
+            for (int i = 0; i < 16; i += 2) {
+              const float f0 = 16 * c + i < rows ? row_f[16 * c + i] : 1.f;
+              const float f1 = 16 * c + i + 1 < rows ? row_f[16 * c + i + 1] : 1.f;
+              l[8 * cc + i / 2] = mul2(l[8 * cc + i / 2], pair(f0, f1));
+              if (tile > ta) {
+                s[i] = __float_as_uint(__uint_as_float(s[i]) * f0);
+                s[i + 1] = __float_as_uint(__uint_as_float(s[i + 1]) * f1);
+              }
             }
             if (tile > ta) tmem_st16(tm_o + 16 * c, s);
           }
@@ -498,39 +539,45 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(bar(kWeightsIn, step));
-          mbar_arrive(bar(kScoresRead, step));
+          mbar_arrive(read_bar(step));
         }
       }
       // the item's end: sums over the keys (threads), then o
+      const bool begins = ta == 0, ends = tb == it.tiles, whole = begins && ends;
+      const int64_t row0 = state->row0;
       wait_bar(bar(kSumDone, step - 1), parity(step - 1), failed);
       fence_after_sync();
       float* const sums = reinterpret_cast<float*>(sm + TcSmem::sums);
 #pragma unroll
       for (int cc = 0; cc < kRows / 32; ++cc)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (32 * cc + 16 * half + i < rows)
-            sums[(32 * cc + 16 * half + i) * 129 + tm_lane] = l[16 * cc + i];
+        for (int i = 0; i < 16; i += 2) {
+          const int row = 32 * cc + 16 * half + i;
+          float l0, l1;
+          unpair(l[8 * cc + i / 2], l0, l1);
+          if (row < rows) sums[row * 129 + tm_lane] = l0;
+          if (row + 1 < rows) sums[(row + 1) * 129 + tm_lane] = l1;
+        }
       soft_or(false);
       const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
       if (st < rows) {
         float L = 0.f;
 #pragma unroll 8
         for (int i = 0; i < kKeys; ++i) L += sums[st * 129 + i];
-        const float m = row_c[st].y;
+        const float m = -minus_ref(st);
         row_f[st] = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
         if (!whole) {
           part_ml[slot * kRows + st] = make_float2(m, L);
         } else if (a.lse) {
           const int tk = over_group(a, rem + st);
-          a.lse[(it.row0 + token0 + tk) * a.hq + head * a.group + rem + st - tk * a.group] =
+          a.lse[(row0 + token0 + tk) * a.hq + head * a.group + rem + st - tk * a.group] =
               (m + log2f(L)) * kLn2;
         }
       }
       if (ends && !begins && st == 0) {
         Desc d;
-        d.row0 = it.row0;
-        d.first = quotient(item_u + kTcItemUnits, run.per);
+        d.row0 = row0;
+        d.first = quotient(state->first_u, state->per);
         d.head = head;
         d.rows = rows;
         d.token0 = token0;
@@ -552,7 +599,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             if (whole) {
               const int tk = over_group(a, rem + row);
               const int64_t at =
-                  (it.row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group;
+                  (row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group;
               static_cast<__nv_bfloat16*>(a.out)[at * D + tm_lane] = __float2bfloat16_rn(o);
             } else {
               part_o[(slot * kRows + row) * D + tm_lane] = o;
@@ -562,6 +609,85 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         __syncwarp();
       }
       fence_before_sync();
+    } else if (warp == kOpenWarps + kSoftWarps) {
+      // ------------------------------------------------------------------ the products
+      if (lane == 0) {
+        const uint32_t id = idesc_f16(128, 64, 0, 0), id_pv = idesc_f16(128, 64, 0, 1);
+        const uint64_t dk = sdesc(base + TcSmem::K, 16, 1024), dq = sdesc(base + TcSmem::Q, 16, 1024);
+        const uint64_t dv = sdesc(base + TcSmem::V, 16, 1024);
+        const uint64_t dp = sdesc(base + TcSmem::P, 128 * 128, 1024);
+        const int steps = tb - ta;
+        for (int i = 0; i <= steps; ++i) {
+          const uint32_t step = step0 + i;
+          if (i < steps) {  // S^T of this step
+            wait_one(bar(kKeysIn, step), parity(step), failed);
+            if (step >= 2) wait_one(read_bar(step - 2), parity4(step - 2), failed);
+            fence_after_sync();
+            const uint64_t k = dk + (step & 1) * (TcSmem::tile >> 4);
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              mma_ss(tm + 64 * (step & 1), k + (((s >> 2) * 16384 + (s & 3) * 32) >> 4),
+                     dq + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4), id, s > 0);
+            mma_commit(bar(kScoresDone, step));
+          }
+          if (i > 0) {  // O^T of the last
+            const uint32_t prev = step - 1;
+            wait_one(bar(kValuesIn, prev), parity(prev), failed);
+            wait_one(bar(kWeightsIn, prev), parity(prev), failed);
+            fence_after_sync();
+            const uint64_t v = dv + (prev & 1) * (TcSmem::tile >> 4);
+            const uint64_t p = dp + (prev & 1) * (TcSmem::p_tile >> 4);
+#pragma unroll
+            for (int s = 0; s < kKeys / 16; ++s)
+              mma_ss(tm + 128, v + (((s >> 2) * 16384 + (s & 3) * 32) >> 4), p + ((s * 2048) >> 4),
+                     id_pv, i > 1 || s > 0);
+            mma_commit(bar(kSumDone, prev));
+          }
+        }
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ pages and scales
+      // lanes 0 .. 7: a run of 16 keys each; the table's entry two steps ahead of its scales' use
+      const int* table = a.table + (int64_t)n * a.max_pages;
+      auto has_page = [&](int tile) {
+        return lane < 8 && tile < tb && (it.tile0 + tile) * kKeys + 16 * lane < it.len;
+      };
+      auto entry_of = [&](int tile) {
+        const int key = (it.tile0 + tile) * kKeys + 16 * lane;
+        return has_page(tile) ? __ldg(table + (key >> a.page_shift)) : -1;
+      };
+      int entry = entry_of(ta);
+      uint32_t step = step0;
+      for (int tile = ta; tile < tb; ++tile, ++step) {
+        const int next = entry_of(tile + 1);
+        PageRun run;
+        run.from = -1;
+        run.unused = 0;
+        // keys without a page weigh nothing, a page of zero values as 2^-100
+        run.ks = 0.f;
+        run.lv = -CUDART_INF_F;
+        run.rv = run.unused2 = 0.f;
+        if (has_page(tile)) {
+          if (entry >= 0 && entry < a.num_pages) {
+            const int64_t block = (int64_t)entry * a.hkv + head;
+            const int slot = ((it.tile0 + tile) * kKeys + 16 * lane) & (a.page - 1);
+            const float vs = __ldg(a.v_scale + block);
+            run.from = block * (a.page * D) + slot * D;
+            run.ks = __ldg(a.k_scale + block);
+            run.lv = vs > 0.f ? log2_fast(vs) : -100.f;
+            run.rv = exp2_fast(-run.lv);
+          } else {
+            set_status(a.status, GDN_ERR_DEVICE_INPUT);
+          }
+        }
+        entry = next;
+        // the slot's last user: the softmax of kAhead steps before
+        if (step >= kAhead) wait_bar(read_bar(step), parity4(step - kAhead), failed);
+        if (lane < 8) runs[step % kAhead * 8 + lane] = run;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pages_bar(step));
+      }
     }
     step0 += tb - ta;
     __syncthreads();
