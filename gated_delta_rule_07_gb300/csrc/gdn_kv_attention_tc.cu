@@ -31,12 +31,11 @@ using namespace sm100;
 constexpr int kOpenWarps = 8, kSoftWarps = 8;  // then one that issues, one that looks pages up
 constexpr int kTcThreads = 32 * (kOpenWarps + kSoftWarps + 2);
 constexpr int kAhead = 4;        // steps whose pages are known at a time
-constexpr int kRows = 64;        // query rows of an item: columns of S^T and O^T
+constexpr int kCols = 64;        // columns of S^T and O^T: an item's query rows, at most
 constexpr int kKeys = 128;       // keys of a step, lanes of S^T
 constexpr int kTcMinUnits = 2;   // steps of a CTA at least
 constexpr int kTcItemUnits = 3;  // steps that starting an item is worth
 constexpr long long kWaitCycles = 2000000000LL;  // limit of a bounded wait: about a second
-using TcWork = Work<kRows, kKeys, kTcItemUnits>;
 
 struct TcSmem {  // byte offsets, each operand tile on a 1024-byte boundary
   static constexpr int tile = 128 * 128 * 2;
@@ -144,9 +143,10 @@ __device__ __forceinline__ bool soft_or(bool v) {
   return r != 0;
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int ROWS>
 __global__ void __launch_bounds__(kTcThreads, 1)
 kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
+  using TcWork = Work<ROWS, kKeys, kTcItemUnits>;
   constexpr int KC = D / 64, VC = D / 64;
   extern __shared__ char smem_raw[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
@@ -242,13 +242,13 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       continue;
     }
     const int head = (uint32_t)which / (uint32_t)it.row_tiles;
-    const int row_base = (which - head * it.row_tiles) * kRows;
-    const int rows = min(kRows, it.m * a.group - row_base);
+    const int row_base = (which - head * it.row_tiles) * ROWS;
+    const int rows = min(ROWS, it.m * a.group - row_base);
     const int token0 = (uint32_t)row_base / (uint32_t)a.group, rem = row_base - token0 * a.group;
 
     // queries: scaled by a power of two into [1, 2), fp16; a thread has 16 channels of a row
 #pragma unroll 1
-    for (int i = tid; i < kRows * (D / 16); i += kTcThreads) {
+    for (int i = tid; i < ROWS * (D / 16); i += kTcThreads) {
       const int row = i / (D / 16), chunk = i % (D / 16);
       const int tk = over_group(a, rem + row), gq = rem + row - tk * a.group;
       const bool live = row < rows;
@@ -272,7 +272,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         minus_ref(row) = live ? -kNone : kNone;
         row_last[row] = live ? it.len - it.m + token0 + tk : -1;
       }
-      const uint32_t at = base + TcSmem::Q + (chunk / 4) * (kRows * 128) + row * 128;
+      const uint32_t at = base + TcSmem::Q + (chunk / 4) * (kCols * 128) + row * 128;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t y[4];
@@ -404,9 +404,9 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       const int all_hi = it.len - it.m + token0;
       const int64_t lo = (int64_t)all_hi + over_group(a, rem + rows - 1) - a.window + 1;
       const int all_lo = a.window > 0 && lo > 0 ? (int)lo : 0;
-      uint64_t l[kRows / 4];  // sums of the weights of this thread's key, two rows a register
+      uint64_t l[ROWS / 4];  // sums of the weights of this thread's key, two rows a register
 #pragma unroll
-      for (int i = 0; i < kRows / 4; ++i) l[i] = 0;
+      for (int i = 0; i < ROWS / 4; ++i) l[i] = 0;
       uint32_t step = step0;
       for (int tile = ta; tile < tb; ++tile, ++step) {
         const int first = (it.tile0 + tile) * kKeys, key = first + tm_lane;
@@ -429,7 +429,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         float top = 0.f;  // the largest score above its row's reference
         auto weights = [&](bool again) {
 #pragma unroll
-          for (int cc = 0; cc < kRows / 32; ++cc) {
+          for (int cc = 0; cc < ROWS / 32; ++cc) {
             const int c = 2 * cc + half;
             if (16 * c >= rows) break;
             uint32_t s[16], p[8];
@@ -472,7 +472,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
           if (tile > ta) wait_bar(bar(kSumDone, step - 1), parity(step - 1), failed);
           fence_after_sync();
 #pragma unroll
-          for (int cc = 0; cc < kRows / 32; ++cc) {
+          for (int cc = 0; cc < ROWS / 32; ++cc) {
             const int c = 2 * cc + half;
             if (16 * c >= rows) break;
             uint32_t s[16];
@@ -498,8 +498,8 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
                 y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
               }
               if (lane == 0) {
-                wmax[quarter * kRows + 16 * c + i] = y0;
-                wmax[quarter * kRows + 16 * c + i + 1] = y1;
+                wmax[quarter * ROWS + 16 * c + i] = y0;
+                wmax[quarter * ROWS + 16 * c + i + 1] = y1;
               }
             }
           }
@@ -508,14 +508,14 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             const float was = -minus_ref(st);
             float m = was;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) m = fmaxf(m, wmax[q * kRows + st] - kHead);
+            for (int q = 0; q < 4; ++q) m = fmaxf(m, wmax[q * ROWS + st] - kHead);
             row_f[st] = exp2_fast(was - m);
             row_d[st] = -was;
             minus_ref(st) = -m;
           }
           soft_or(false);
 #pragma unroll
-          for (int cc = 0; cc < kRows / 32; ++cc) {
+          for (int cc = 0; cc < ROWS / 32; ++cc) {
             const int c = 2 * cc + half;
             if (16 * c >= rows) break;
             uint32_t s[16];
@@ -549,7 +549,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       fence_after_sync();
       float* const sums = reinterpret_cast<float*>(sm + TcSmem::sums);
 #pragma unroll
-      for (int cc = 0; cc < kRows / 32; ++cc)
+      for (int cc = 0; cc < ROWS / 32; ++cc)
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           const int row = 32 * cc + 16 * half + i;
@@ -567,7 +567,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         const float m = -minus_ref(st);
         row_f[st] = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
         if (!whole) {
-          part_ml[slot * kRows + st] = make_float2(m, L);
+          part_ml[slot * ROWS + st] = make_float2(m, L);
         } else if (a.lse) {
           const int tk = over_group(a, rem + st);
           a.lse[(row0 + token0 + tk) * a.hq + head * a.group + rem + st - tk * a.group] =
@@ -602,7 +602,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
                   (row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group;
               static_cast<__nv_bfloat16*>(a.out)[at * D + tm_lane] = __float2bfloat16_rn(o);
             } else {
-              part_o[(slot * kRows + row) * D + tm_lane] = o;
+              part_o[(slot * ROWS + row) * D + tm_lane] = o;
             }
           }
         }
@@ -627,7 +627,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)
               mma_ss(tm + 64 * (step & 1), k + (((s >> 2) * 16384 + (s & 3) * 32) >> 4),
-                     dq + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4), id, s > 0);
+                     dq + (((s >> 2) * (kCols * 128) + (s & 3) * 32) >> 4), id, s > 0);
             mma_commit(bar(kScoresDone, step));
           }
           if (i > 0) {  // O^T of the last
@@ -699,9 +699,10 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   if (warp == 0) tmem_dealloc(tm, 256);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int ROWS>
 cudaError_t launch_tc(const KvArgs& a, cudaStream_t s) {
-  const auto kern = kv_attention_tc_kernel<D, E4M3>;
+  using TcWork = Work<ROWS, kKeys, kTcItemUnits>;
+  const auto kern = kv_attention_tc_kernel<D, E4M3, ROWS>;
   static const cudaError_t ready =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem::bytes);
   if (ready != cudaSuccess) return ready;
@@ -710,20 +711,29 @@ cudaError_t launch_tc(const KvArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = grid_ctas<TcWork>(a, sms, kTcMinUnits);
-  const Workspace ws(a, kRows);
+  const Workspace ws(a, ROWS);
   kern<<<ctas, kTcThreads, TcSmem::bytes, s>>>(a, ws.part_o, ws.part_ml, ws.descs);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_join<__nv_bfloat16, D, kRows>(a, ws, ctas, s);
+  return launch_join<__nv_bfloat16, D, ROWS>(a, ws, ctas, s);
+}
+
+// Rows of an item: 32 where the average sequence's rows of a kv head fit, which leaves the softmax's
+// threads half the sums to hold; else 64 (a row tile more reads and opens the codes once more).
+int item_rows(const KvArgs& a) { return (a.T + a.N - 1) / a.N * a.group <= 32 ? 32 : 64; }
+
+template <int D, bool E4M3>
+cudaError_t launch_tc_rows(const KvArgs& a, cudaStream_t s) {
+  return item_rows(a) == 32 ? launch_tc<D, E4M3, 32>(a, s) : launch_tc<D, E4M3, 64>(a, s);
 }
 
 }  // namespace
 
-size_t kv_attention_tc_workspace(const KvArgs& a) { return Workspace::bytes(a, kRows); }
+size_t kv_attention_tc_workspace(const KvArgs& a) { return Workspace::bytes(a, item_rows(a)); }
 
 cudaError_t kv_attention_tc(const KvArgs& a, cudaStream_t s) {
-  if (a.D == 64) return a.e4m3 ? launch_tc<64, true>(a, s) : launch_tc<64, false>(a, s);
-  return a.e4m3 ? launch_tc<128, true>(a, s) : launch_tc<128, false>(a, s);
+  if (a.D == 64) return a.e4m3 ? launch_tc_rows<64, true>(a, s) : launch_tc_rows<64, false>(a, s);
+  return a.e4m3 ? launch_tc_rows<128, true>(a, s) : launch_tc_rows<128, false>(a, s);
 }
 
 }  // namespace gdn
