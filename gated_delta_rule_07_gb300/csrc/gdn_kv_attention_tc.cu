@@ -93,6 +93,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr)
       : "memory");
 }
+// true in one thread of a converged warp
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 // two fp32 in a 64-bit register: one instruction for both
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t r;
@@ -611,7 +617,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       fence_before_sync();
     } else if (warp == kOpenWarps + kSoftWarps) {
       // ------------------------------------------------------------------ the products
-      if (lane == 0) {
+      {
         const uint32_t id = idesc_f16(128, 64, 0, 0), id_pv = idesc_f16(128, 64, 0, 1);
         const uint64_t dk = sdesc(base + TcSmem::K, 16, 1024), dq = sdesc(base + TcSmem::Q, 16, 1024);
         const uint64_t dv = sdesc(base + TcSmem::V, 16, 1024);
@@ -620,28 +626,34 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         for (int i = 0; i <= steps; ++i) {
           const uint32_t step = step0 + i;
           if (i < steps) {  // S^T of this step
-            wait_one(bar(kKeysIn, step), parity(step), failed);
-            if (step >= 2) wait_one(read_bar(step - 2), parity4(step - 2), failed);
+            wait_bar(bar(kKeysIn, step), parity(step), failed);
+            if (step >= 2) wait_bar(read_bar(step - 2), parity4(step - 2), failed);
             fence_after_sync();
             const uint64_t k = dk + (step & 1) * (TcSmem::tile >> 4);
+            if (elected()) {
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)
               mma_ss(tm + 64 * (step & 1), k + (((s >> 2) * 16384 + (s & 3) * 32) >> 4),
                      dq + (((s >> 2) * (kCols * 128) + (s & 3) * 32) >> 4), id, s > 0);
             mma_commit(bar(kScoresDone, step));
+            }
+            __syncwarp();
           }
           if (i > 0) {  // O^T of the last
             const uint32_t prev = step - 1;
-            wait_one(bar(kValuesIn, prev), parity(prev), failed);
-            wait_one(bar(kWeightsIn, prev), parity(prev), failed);
+            wait_bar(bar(kValuesIn, prev), parity(prev), failed);
+            wait_bar(bar(kWeightsIn, prev), parity(prev), failed);
             fence_after_sync();
             const uint64_t v = dv + (prev & 1) * (TcSmem::tile >> 4);
             const uint64_t p = dp + (prev & 1) * (TcSmem::p_tile >> 4);
+            if (elected()) {
 #pragma unroll
             for (int s = 0; s < kKeys / 16; ++s)
               mma_ss(tm + 128, v + (((s >> 2) * 16384 + (s & 3) * 32) >> 4), p + ((s * 2048) >> 4),
                      id_pv, i > 1 || s > 0);
             mma_commit(bar(kSumDone, prev));
+            }
+            __syncwarp();
           }
         }
       }
