@@ -1,4 +1,6 @@
-"""Builds libgdn.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libgdn.so (the C-ABI library) in-tree with nvcc for sm_103a, and the torch binding of
+the calls that are short enough for Python to matter (``_gdn_torch.so``, g++ against torch's
+headers; it calls libgdn.so).
 
 Each .cu file is compiled in parallel to an object, then linked into
 ``gated_delta_rule_07_gb300/_build/libgdn.so``.  Rebuilds only when a source or header is
@@ -7,10 +9,12 @@ newer than the library.  Usage: ``python -m gated_delta_rule_07_gb300.build [--f
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
+TORCH_SRC = os.path.join(CSRC, "gdn_torch.cpp")
+TORCH_LIB = os.path.join(BUILD, "_gdn_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -42,12 +48,30 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(TORCH_LIB):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
+    deps = [TORCH_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
         os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def torch_binding_command(out: str) -> list:
+    """The g++ command that compiles gdn_torch.cpp (linked against libgdn.so beside it; torch's own
+    libraries are in the process that imports it)."""
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    inc += [d for d in (os.path.join(cuda, "include"),
+                        os.path.join(cuda, "targets", "sbsa-linux", "include"),
+                        os.path.join(cuda, "targets", "x86_64-linux", "include"))
+            if os.path.isdir(d)]
+    lib = os.path.join(torch_dir, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            *[f"-I{d}" for d in inc], TORCH_SRC, "-o", out, f"-L{lib}", "-ltorch_python",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False, extra: tuple = ()) -> str:
@@ -60,6 +84,11 @@ def build(force: bool = False, verbose: bool = False, extra: tuple = ()) -> str:
     if verbose:
         common += ["-Xptxas", "-v"]
     procs, objs = [], []
+    binding = TORCH_LIB + f".tmp{os.getpid()}"
+    # (its references to libgdn.so are resolved when it is loaded, after that library)
+    procs.append((TORCH_SRC, subprocess.Popen(torch_binding_command(binding),
+                                              stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                              text=True)))
     for src in sources():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
@@ -80,6 +109,7 @@ def build(force: bool = False, verbose: bool = False, extra: tuple = ()) -> str:
     subprocess.run([cc, "-shared", *ARCH, "-cudart", "shared", "-o", tmp, *objs,
                     f"-L{libdir}", f"-Xlinker", f"-rpath={libdir}"], check=True)
     os.replace(tmp, LIB)
+    os.replace(binding, TORCH_LIB)
     return LIB
 
 

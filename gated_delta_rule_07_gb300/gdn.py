@@ -11,6 +11,8 @@ Importing this module loads the library and raises ImportError when it has not b
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -23,7 +25,22 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"libgdn.so is not built ({LIB_PATH}); run "
                       "`python -m gated_delta_rule_07_gb300.build` (needs nvcc)")
 
-_lib = ctypes.CDLL(LIB_PATH)
+# (global: the torch binding's references to the C entry points are resolved against it)
+_lib = ctypes.CDLL(LIB_PATH, mode=ctypes.RTLD_GLOBAL)
+
+
+def _load_torch_binding():
+    path = _build.TORCH_LIB
+    if not os.path.exists(path):
+        raise ImportError(f"_gdn_torch.so is not built ({path}); run "
+                          "`python -m gated_delta_rule_07_gb300.build`")
+    loader = importlib.machinery.ExtensionFileLoader("_gdn_torch", path)
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_gdn_torch", loader))
+    loader.exec_module(mod)
+    return mod
+
+
+_native = _load_torch_binding()
 
 GDN_OK = 0
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
@@ -387,108 +404,71 @@ def gdn_device_status(status_word, reset=True, stream=None) -> int:
 
 # ------------------------------------------------- softmax-attention layers' operators
 #
-# These calls are short on the GPU (a decode step's take a few microseconds), so the host's part
-# is kept lean: each tensor is looked at once, in the order that costs least, and messages are
-# only built for a refusal.
+# The functions named after the C entry points are the ctypes form, as above.  The others go
+# through the torch binding (csrc/gdn_torch.cpp): a decode step's kernels take a few microseconds,
+# so its checks and allocations are made there.  What they refuse raises GdnError before any CUDA
+# work.
 
+_native.set_error(GdnError)
 _IO = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _ROPE_STYLES = {"half": 0, "pairs": 1}
-_GDN_ERR_INVALID_ARGUMENT, _GDN_ERR_UNSUPPORTED = 1, 2
-_F32, _I32 = torch.float32, torch.int32
 
 
-def _refuse(where, why, status=_GDN_ERR_INVALID_ARGUMENT):
+def _refuse(where, why, status=1):
     raise GdnError(status, f"{where}: {why}")
 
 
-def _io_of(where, t):
-    io = _IO.get(t.dtype)
-    if io is None:
-        _refuse(where, f"dtype {t.dtype}", _GDN_ERR_UNSUPPORTED)
-    return io
-
-
-def _packed(where, name, t, shape, dtype):
-    """t is a contiguous GPU tensor of this shape and dtype."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
-        _refuse(where, f"{name} is to be a contiguous {dtype} tensor {tuple(shape)} on the GPU, "
-                       f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-
-
-def _rows(where, name, t, dtype):
-    """Shape, token and head stride of a [T, heads, D] GPU tensor whose last dimension is
-    contiguous."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or (stride[2] != 1 and shape[2] > 1):
-        _refuse(where, f"{name} is to be [tokens, heads, D] with a contiguous last dimension, "
-                       f"got {tuple(shape)} with strides {stride}")
-    if t.dtype is not dtype:
-        _refuse(where, f"{name} is {t.dtype}, the call's dtype is {dtype}")
-    if not t.is_cuda:
-        _refuse(where, f"{name} is not on the GPU")
-    return shape, stride[0], stride[1]
+def _style(where, style):
+    code = _ROPE_STYLES.get(style)
+    if code is None:
+        _refuse(where, f"style {style!r}")
+    return code
 
 
 def _hold(stream, *tensors):
-    """Temporaries and outputs allocated on the current stream and used on `stream`: their memory
+    """Outputs and temporaries allocated on the current stream and used on `stream`: their memory
     is not handed out again before the work on `stream` is done."""
     if hasattr(stream, "cuda_stream"):
         for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+            t.record_stream(stream)
 
 
-def _opt(t):
-    return None if t is None else t.data_ptr()
+def _handle(stream):
+    return stream if stream is None else _stream(stream)
 
 
-def _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, style):
-    io, dtype = _io_of(where, q), q.dtype
-    (T, hq, D), qt, qh = _rows(where, "q", q, dtype)
-    kshape, kt, kh = _rows(where, "k", k, dtype)
-    if kshape[0] != T or kshape[2] != D:
-        _refuse(where, f"q {tuple(q.shape)} and k {tuple(kshape)} do not go together")
-    _packed(where, "positions", positions, (T,), _I32)
-    tshape = cos_sin.shape
-    if len(tshape) != 2:
-        _refuse(where, "cos_sin is to be [positions, R]")
-    _packed(where, "cos_sin", cos_sin, tshape, _F32)
-    if q_weight is not None:
-        _packed(where, "q_weight", q_weight, (D,), _F32)
-    if k_weight is not None:
-        _packed(where, "k_weight", k_weight, (D,), _F32)
-    which = _ROPE_STYLES.get(style)
-    if which is None:
-        _refuse(where, f"style {style!r}")
-    return QkRopeProblem(T, hq, kshape[1], D, tshape[1], which, io, tshape[0], eps,
-                         weight_offset, qt, qh, kt, kh)
+def _checked(check_status, device, stream, where, call):
+    """call(status word or None), with the word read back afterwards where asked for."""
+    if not check_status:
+        return call(None)
+    st = torch.zeros(1, dtype=torch.int32, device=device)
+    _hold(stream, st)
+    result = call(st)
+    _check(gdn_device_status(st, True, stream), f"{where} (device status)")
+    return result
 
 
 def gdn_qk_norm_rope(p, q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out,
                      dev_status=None, stream=None):
-    _check(_lib.gdn_qk_norm_rope(p, q.data_ptr(), k.data_ptr(), positions.data_ptr(),
-                                 cos_sin.data_ptr(), _opt(q_weight), _opt(k_weight),
-                                 q_out.data_ptr(), k_out.data_ptr(), _opt(dev_status),
-                                 _stream(stream)), "gdn_qk_norm_rope")
+    _check(_lib.gdn_qk_norm_rope(p, _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin),
+                                 _ptr(q_weight), _ptr(k_weight), _ptr(q_out), _ptr(k_out),
+                                 _ptr(dev_status), _stream(stream)), "gdn_qk_norm_rope")
 
 
 def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-6,
                  weight_offset=0.0, style="half", check_status=False, stream=None):
     """Queries [T, hq, D] and keys [T, hkv, D], normalised per head and rotated by position (see
     include/gdn.h); q and k may be slices of one projection.  Returns contiguous tensors."""
-    p = _rope_problem("qk_norm_rope", q, k, positions, cos_sin, q_weight, k_weight, eps,
-                      weight_offset, style)
-    device, dtype = q.device, q.dtype
-    q_out = torch.empty(q.shape, dtype=dtype, device=device)
-    k_out = torch.empty(k.shape, dtype=dtype, device=device)
-    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
-    if stream is not None:
-        _hold(stream, q_out, k_out, st)
-    gdn_qk_norm_rope(p, q, k, positions, cos_sin, q_weight, k_weight, q_out, k_out, st, stream)
-    if check_status:
-        _check(gdn_device_status(st, True, stream), "qk_norm_rope (device status)")
-    return q_out, k_out
+    code = _style("qk_norm_rope", style)
+    if stream is None and not check_status:
+        return _native.qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps,
+                                    weight_offset, code, None, None)
+    out = _checked(check_status, q.device, stream, "qk_norm_rope", lambda st: _native.qk_norm_rope(
+        q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, code, st,
+        _handle(stream)))
+    _hold(stream, *out)
+    return out
 
 
 def gdn_qk_norm_rope_backward_workspace_size(p) -> int:
@@ -500,10 +480,10 @@ def gdn_qk_norm_rope_backward(p, q, k, positions, cos_sin, q_weight, k_weight, d
                               dev_status=None, stream=None):
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
     _check(_lib.gdn_qk_norm_rope_backward(
-        p, q.data_ptr(), k.data_ptr(), positions.data_ptr(), cos_sin.data_ptr(), _opt(q_weight),
-        _opt(k_weight), dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-        dq_weight.data_ptr(), dk_weight.data_ptr(), workspace.data_ptr(), ws_bytes,
-        _opt(dev_status), _stream(stream)), "gdn_qk_norm_rope_backward")
+        p, _ptr(q), _ptr(k), _ptr(positions), _ptr(cos_sin), _ptr(q_weight), _ptr(k_weight),
+        _ptr(dq_out), _ptr(dk_out), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight),
+        _ptr(workspace), int(ws_bytes), _ptr(dev_status), _stream(stream)),
+        "gdn_qk_norm_rope_backward")
 
 
 def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out, eps=1e-6,
@@ -512,25 +492,20 @@ def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, 
     """Gradients (dq, dk, dq_weight, dk_weight) of <dq_out, q_out> + <dk_out, k_out> through
     qk_norm_rope on the same inputs."""
     where = "qk_norm_rope_backward"
-    p = _rope_problem(where, q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset,
-                      style)
-    device, D = q.device, p.head_dim
-    _packed(where, "dq_out", dq_out, q.shape, q.dtype)
-    _packed(where, "dk_out", dk_out, k.shape, q.dtype)
-    dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
-    dqw = torch.empty(D, dtype=_F32, device=device)
-    dkw = torch.empty(D, dtype=_F32, device=device)
-    if workspace is None:
+    code = _style(where, style)
+    if workspace is None and stream is not None:
+        (T, hq, D), (rows, R) = q.shape, cos_sin.shape
+        p = QkRopeProblem(T, hq, k.shape[1], D, R, code, _IO.get(q.dtype, -1), rows, eps,
+                          weight_offset, *q.stride()[:2], *k.stride()[:2])
         workspace = torch.empty(gdn_qk_norm_rope_backward_workspace_size(p), dtype=torch.uint8,
-                                device=device)
-    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
+                                device=q.device)
+        _hold(stream, workspace)
+    grads = _checked(check_status, q.device, stream, where, lambda st: (
+        _native.qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
+                                      eps, weight_offset, code, workspace, st, _handle(stream))))
     if stream is not None:
-        _hold(stream, dq, dk, dqw, dkw, workspace, st)
-    gdn_qk_norm_rope_backward(p, q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
-                              dq, dk, dqw, dkw, workspace, None, st, stream)
-    if check_status:
-        _check(gdn_device_status(st, True, stream), "qk_norm_rope_backward (device status)")
-    return dq, dk, dqw, dkw
+        _hold(stream, *grads)
+    return grads
 
 
 class KVCache:
@@ -539,51 +514,38 @@ class KVCache:
     k_scale, v_scale [pages, hkv] fp32.  ``KVCache.empty`` allocates them."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        where = "KVCache"
-        if k.dtype not in _KV_FORMATS:
-            _refuse(where, f"dtype {k.dtype}", _GDN_ERR_UNSUPPORTED)
+        fmt = _KV_FORMATS.get(k.dtype)
+        if fmt is None:
+            _refuse("KVCache", f"dtype {k.dtype}", 2)
         if k.dim() != 4:
-            _refuse(where, "k is to be [pages, hkv, page, D]")
+            _refuse("KVCache", "k is to be [pages, hkv, page, D]")
         pages, hkv, page, D = k.shape
-        _packed(where, "k", k, k.shape, k.dtype)
-        _packed(where, "v", v, (pages, hkv, page // 4, D, 4), k.dtype)
-        _packed(where, "k_scale", k_scale, (pages, hkv), _F32)
-        _packed(where, "v_scale", v_scale, (pages, hkv), _F32)
+        for name, t, shape, dtype in (("k", k, k.shape, k.dtype),
+                                      ("v", v, (pages, hkv, page // 4, D, 4), k.dtype),
+                                      ("k_scale", k_scale, (pages, hkv), torch.float32),
+                                      ("v_scale", v_scale, (pages, hkv), torch.float32)):
+            if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
+                _refuse("KVCache", f"{name} is to be a contiguous {dtype} tensor {tuple(shape)} on "
+                                   f"the GPU, got {t.dtype} {tuple(t.shape)} on {t.device}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.heads, self.head_dim = hkv, D
         self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
-                                v_scale.data_ptr(), pages, page, hkv, D, _KV_FORMATS[k.dtype])
+                                v_scale.data_ptr(), pages, page, hkv, D, fmt)
+        self._address = ctypes.addressof(self.desc)
 
     @classmethod
     def empty(cls, pages, hkv, page, D, dtype=torch.int8, device="cuda"):
         """A cache of `pages` pages; nothing in it is initialised, or needs to be."""
         return cls(torch.empty(pages, hkv, page, D, dtype=dtype, device=device),
                    torch.empty(pages, hkv, page // 4, D, 4, dtype=dtype, device=device),
-                   torch.empty(pages, hkv, dtype=_F32, device=device),
-                   torch.empty(pages, hkv, dtype=_F32, device=device))
-
-
-def _kv_sequences(where, T, block_table, lens, cu_seqlens):
-    """Checks the tables of a cache call; the number of sequences and of pages in a table row."""
-    shape = block_table.shape
-    if len(shape) != 2:
-        _refuse(where, "block_table is to be [sequences, pages]")
-    _packed(where, "block_table", block_table, shape, _I32)
-    N = shape[0]
-    if lens is not None:
-        _packed(where, "lengths", lens, (N,), _I32)
-    if cu_seqlens is not None:
-        _packed(where, "cu_seqlens", cu_seqlens, (N + 1,), _I32)
-    elif N != 1 and N != T:
-        _refuse(where, f"{T} rows of {N} sequences need cu_seqlens")
-    return N, shape[1]
+                   torch.empty(pages, hkv, dtype=torch.float32, device=device),
+                   torch.empty(pages, hkv, dtype=torch.float32, device=device))
 
 
 def gdn_kv_append(cache, p, k, v, block_table, ctx_lens, cu_seqlens, dev_status=None,
                   stream=None):
-    _check(_lib.gdn_kv_append(cache, p, k.data_ptr(), v.data_ptr(), block_table.data_ptr(),
-                              ctx_lens.data_ptr(), _opt(cu_seqlens), _opt(dev_status),
-                              _stream(stream)), "gdn_kv_append")
+    _check(_lib.gdn_kv_append(cache, p, _ptr(k), _ptr(v), _ptr(block_table), _ptr(ctx_lens),
+                              _ptr(cu_seqlens), _ptr(dev_status), _stream(stream)),
+           "gdn_kv_append")
 
 
 def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=False,
@@ -591,51 +553,29 @@ def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=
     """Quantises new keys and values [T, hkv, D] into the cache's pages, behind the ctx_lens[n]
     tokens that each sequence already holds.  Without cu_seqlens the rows are one sequence's, or
     one row each of T sequences."""
-    where = "kv_append"
-    io, dtype = _io_of(where, k), k.dtype
-    shape, kt, kh = _rows(where, "k", k, dtype)
-    vshape, vt, vh = _rows(where, "v", v, dtype)
-    T, h, D = shape
-    if vshape != shape or h != cache.heads or D != cache.head_dim:
-        _refuse(where, f"k {tuple(shape)} and v {tuple(vshape)} for a cache of {cache.heads} "
-                       f"heads of {cache.head_dim}")
-    N, max_pages = _kv_sequences(where, T, block_table, ctx_lens, cu_seqlens)
-    p = KvProblem(T, N, max_pages, 0, io, kt, kh, vt, vh, 0, 0)
-    st = torch.zeros(1, dtype=_I32, device=k.device) if check_status else None
-    if stream is not None:
-        _hold(stream, st)
-    gdn_kv_append(cache.desc, p, k, v, block_table, ctx_lens, cu_seqlens, st, stream)
-    if check_status:
-        _check(gdn_device_status(st, True, stream), "kv_append (device status)")
+    _checked(check_status, k.device, stream, "kv_append", lambda st: _native.kv_append(
+        cache._address, k, v, block_table, ctx_lens, cu_seqlens, st, _handle(stream)))
 
 
 def gdn_kv_read(cache, p, block_table, start, cu_seqlens, k_out, v_out, dev_status=None,
                 stream=None):
-    _check(_lib.gdn_kv_read(cache, p, block_table.data_ptr(), _opt(start), _opt(cu_seqlens),
-                            k_out.data_ptr(), v_out.data_ptr(), _opt(dev_status),
-                            _stream(stream)), "gdn_kv_read")
+    _check(_lib.gdn_kv_read(cache, p, _ptr(block_table), _ptr(start), _ptr(cu_seqlens),
+                            _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream)),
+           "gdn_kv_read")
 
 
 def kv_read(cache, block_table, start, cu_seqlens, tokens, dtype=torch.bfloat16,
             check_status=False, stream=None):
     """Keys and values [tokens, hkv, D] of the positions start[n] onward (None: from 0) of each
     sequence, cu_seqlens[n + 1] - cu_seqlens[n] of them, read back from the cache."""
-    where = "kv_read"
     io = _IO.get(dtype)
     if io is None:
-        _refuse(where, f"dtype {dtype}", _GDN_ERR_UNSUPPORTED)
-    N, max_pages = _kv_sequences(where, tokens, block_table, start, cu_seqlens)
-    shape, device = (tokens, cache.heads, cache.head_dim), block_table.device
-    k = torch.empty(shape, dtype=dtype, device=device)
-    v = torch.empty(shape, dtype=dtype, device=device)
-    p = KvProblem(tokens, N, max_pages, 0, io, 0, 0, 0, 0, 0, 0)
-    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
+        _refuse("kv_read", f"dtype {dtype}", 2)
+    out = _checked(check_status, block_table.device, stream, "kv_read", lambda st: _native.kv_read(
+        cache._address, block_table, start, cu_seqlens, tokens, io, st, _handle(stream)))
     if stream is not None:
-        _hold(stream, k, v, st)
-    gdn_kv_read(cache.desc, p, block_table, start, cu_seqlens, k, v, st, stream)
-    if check_status:
-        _check(gdn_device_status(st, True, stream), "kv_read (device status)")
-    return k, v
+        _hold(stream, *out)
+    return out
 
 
 def gdn_kv_attention_workspace_size(cache, p) -> int:
@@ -645,10 +585,19 @@ def gdn_kv_attention_workspace_size(cache, p) -> int:
 def gdn_kv_attention(cache, p, q, block_table, kv_lens, cu_seqlens, scale, window, out, lse,
                      workspace, ws_bytes=None, dev_status=None, stream=None):
     ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
-    _check(_lib.gdn_kv_attention(cache, p, q.data_ptr(), block_table.data_ptr(),
-                                 kv_lens.data_ptr(), _opt(cu_seqlens), scale, window,
-                                 out.data_ptr(), _opt(lse), workspace.data_ptr(), ws_bytes,
-                                 _opt(dev_status), _stream(stream)), "gdn_kv_attention")
+    _check(_lib.gdn_kv_attention(cache, p, _ptr(q), _ptr(block_table), _ptr(kv_lens),
+                                 _ptr(cu_seqlens), scale, window, _ptr(out), _ptr(lse),
+                                 _ptr(workspace), int(ws_bytes), _ptr(dev_status),
+                                 _stream(stream)), "gdn_kv_attention")
+
+
+def kv_attention_workspace(cache, q, block_table):
+    """A workspace for kv_attention calls of these shapes."""
+    T, hq, _ = q.shape
+    p = KvProblem(T, block_table.shape[0], block_table.shape[1], hq, _IO[q.dtype], 0, 0, 0, 0,
+                  q.stride(0), q.stride(1))
+    return torch.empty(gdn_kv_attention_workspace_size(cache.desc, p), dtype=torch.uint8,
+                       device=q.device)
 
 
 def kv_attention(cache, q, block_table, kv_lens, cu_seqlens=None, scale=None, window=0,
@@ -656,28 +605,17 @@ def kv_attention(cache, q, block_table, kv_lens, cu_seqlens=None, scale=None, wi
     """out [T, hq, D] and lse [T, hq] of the queries of each sequence's last tokens over the
     cache's kv_lens[n] tokens (which include them); scale defaults to 1 / sqrt(D).  Without
     cu_seqlens the rows are one sequence's, or one row each of T sequences."""
-    where = "kv_attention"
-    io, dtype, device = _io_of(where, q), q.dtype, q.device
-    shape, qt, qh = _rows(where, "q", q, dtype)
-    T, hq, D = shape
-    if D != cache.head_dim:
-        _refuse(where, f"q {tuple(shape)} for a cache of heads of {cache.head_dim}")
-    N, max_pages = _kv_sequences(where, T, block_table, kv_lens, cu_seqlens)
-    p = KvProblem(T, N, max_pages, hq, io, 0, 0, 0, 0, qt, qh)
-    out = torch.empty(shape, dtype=dtype, device=device)
-    lse = torch.empty((T, hq), dtype=_F32, device=device)
+    if stream is None and not check_status:
+        return _native.kv_attention(cache._address, q, block_table, kv_lens, cu_seqlens, scale,
+                                    window, workspace, None, None)
     if workspace is None:
-        workspace = torch.empty(gdn_kv_attention_workspace_size(cache.desc, p),
-                                dtype=torch.uint8, device=device)
-    st = torch.zeros(1, dtype=_I32, device=device) if check_status else None
-    if stream is not None:
-        _hold(stream, out, lse, workspace, st)
-    gdn_kv_attention(cache.desc, p, q, block_table, kv_lens, cu_seqlens,
-                     D ** -0.5 if scale is None else scale, window, out, lse, workspace, None,
-                     st, stream)
-    if check_status:
-        _check(gdn_device_status(st, True, stream), "kv_attention (device status)")
-    return out, lse
+        workspace = kv_attention_workspace(cache, q, block_table)
+        _hold(stream, workspace)
+    out = _checked(check_status, q.device, stream, "kv_attention", lambda st: _native.kv_attention(
+        cache._address, q, block_table, kv_lens, cu_seqlens, scale, window, workspace, st,
+        _handle(stream)))
+    _hold(stream, *out)
+    return out
 
 
 # ------------------------------------------------------------------ convenience API

@@ -104,7 +104,8 @@ def test_bad_positions_are_reported_and_skipped(gdn):
     pos[2], pos[5] = 100, -1
     gq, gk = on_gpu(proj, q, k)
     args = (gq, gk, pos.cuda(), tab.cuda(), wq.cuda(), wk.cuda())
-    p = gdn._rope_problem("test", *args, 1e-6, 0.0, "half")
+    p = gdn.QkRopeProblem(8, 2, 1, 128, 64, 0, gdn.GDN_BF16, 100, 1e-6, 0.0, *gq.stride()[:2],
+                          *gk.stride()[:2])
     qo, ko = torch.full_like(dqo.cuda(), 7.0), torch.full_like(dko.cuda(), 7.0)
     st = torch.zeros(1, dtype=torch.int32, device="cuda")
     gdn.gdn_qk_norm_rope(p, *args, qo, ko, st)
@@ -147,5 +148,11 @@ def test_on_another_stream(gdn):
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     got = gdn.qk_norm_rope(*args, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    do = (torch.randn_like(want[0]), torch.randn_like(want[1]))
+    want = gdn.qk_norm_rope_backward(*args, *do)
+    s.wait_stream(torch.cuda.current_stream())
+    got = gdn.qk_norm_rope_backward(*args, *do, stream=s)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
