@@ -16,6 +16,7 @@
 
 #include "gdn_attention.h"
 #include "gdn_common.cuh"
+#include "gdn_stream_order.cuh"
 
 namespace gdn {
 

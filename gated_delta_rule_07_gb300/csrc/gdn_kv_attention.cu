@@ -468,17 +468,15 @@ cudaError_t launch(const KvArgs& a, cudaStream_t s) {
   using S = Shape<D, NT, sizeof(IO) == 4>;
   using W = Work<S::rows, kTile, kItemUnits>;
   const auto kern = kv_attention_kernel<IO, D, NT, E4M3>;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem);
-  if (ready != cudaSuccess) return ready;
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, S::smem, ready);
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = grid_ctas<W>(a, sms * S::ctas, kMinUnits);
   const Workspace ws(a, S::rows);
-  kern<<<ctas, kThreads, S::smem, s>>>(a, ws.part_o, ws.part_ml, ws.descs);
-  e = cudaGetLastError();
+  e = launch_ordered(kern, dim3(ctas), kThreads, S::smem, s, a, ws.part_o, ws.part_ml, ws.descs);
   if (e != cudaSuccess) return e;
   return launch_join<IO, D, S::rows>(a, ws, ctas, s);
 }

@@ -98,6 +98,7 @@ __device__ __forceinline__ bool plan_run(const KvArgs& a, int min_units, Desc* d
   __shared__ int64_t start_off;
   __shared__ int start_n;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
+  stream_order();
   int64_t total = 0, per = 0, u = 0;
   for (int pass = a.N <= THREADS; pass < 2; ++pass) {
     int64_t before = 0;
@@ -139,7 +140,6 @@ __device__ __forceinline__ bool plan_run(const KvArgs& a, int min_units, Desc* d
   }
   const int64_t u1 = u + per < total ? u + per : total;
   if (tid == 0) descs[blockIdx.x].first = -1;
-  asm volatile("griddepcontrol.launch_dependents;");
   if (u >= u1) return false;
   run = Run{per, u, u1, start_off, start_n};
   return true;
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, cons
                                                                   const Desc* descs, int groups) {
   __shared__ float4 so[kJoinThreads];
   __shared__ float2 sml[kJoinThreads];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  stream_order();
   const Desc d = descs[blockIdx.x];
   if (d.first < 0) return;
   const int cols = kJoinThreads / groups, g = threadIdx.x / cols;
@@ -305,25 +305,16 @@ template <typename W> int grid_ctas(const KvArgs& a, int resident, int min_units
   return ctas < most ? ctas : (int)most;
 }
 
-// The join is launched while the first kernel drains; it waits for its end before it reads.
 template <typename IO, int D, int ROWS>
 cudaError_t launch_join(const KvArgs& a, const Workspace& ws, int ctas, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
   // partials of an item, if the sequences are alike: a thread takes about eight of them
   const int64_t parts = ctas / ((int64_t)a.N * a.hkv);
   constexpr int all_cols = ROWS * (D / 4);
   int groups = all_cols < kJoinThreads ? kJoinThreads / all_cols : 1;
   while (groups < 16 && 8 * groups < parts) groups *= 2;
-  cfg.gridDim = dim3(ctas, all_cols * groups / kJoinThreads);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_attention_join<IO, D, ROWS>, a, (const float*)ws.part_o,
-                            (const float2*)ws.part_ml, (const Desc*)ws.descs, groups);
+  return launch_ordered(kv_attention_join<IO, D, ROWS>, dim3(ctas, all_cols * groups / kJoinThreads),
+                        kJoinThreads, 0, s, a, (const float*)ws.part_o, (const float2*)ws.part_ml,
+                        (const Desc*)ws.descs, groups);
 }
 
 }  // namespace

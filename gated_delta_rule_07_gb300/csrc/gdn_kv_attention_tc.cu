@@ -715,17 +715,16 @@ template <int D, bool E4M3, int ROWS>
 cudaError_t launch_tc(const KvArgs& a, cudaStream_t s) {
   using TcWork = Work<ROWS, kKeys, kTcItemUnits>;
   const auto kern = kv_attention_tc_kernel<D, E4M3, ROWS>;
-  static const cudaError_t ready =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TcSmem::bytes);
-  if (ready != cudaSuccess) return ready;
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, TcSmem::bytes, ready);
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = grid_ctas<TcWork>(a, sms, kTcMinUnits);
   const Workspace ws(a, ROWS);
-  kern<<<ctas, kTcThreads, TcSmem::bytes, s>>>(a, ws.part_o, ws.part_ml, ws.descs);
-  e = cudaGetLastError();
+  e = launch_ordered(kern, dim3(ctas), kTcThreads, TcSmem::bytes, s, a, ws.part_o, ws.part_ml,
+                     ws.descs);
   if (e != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, D, ROWS>(a, ws, ctas, s);
 }

@@ -251,9 +251,10 @@ __device__ __forceinline__ void append_values(const KvArgs& a, const KvSpan& s, 
 // IT: pages of at most 4096 IT new values
 template <typename IO, int D, bool E4M3, int IT>
 __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(KvArgs a) {
-  __shared__ KvFound found;
   __shared__ float red[kKvThreads / 32];
   const int which = blockIdx.x % (2 * a.hkv);
+  stream_order();
+  __shared__ KvFound found;
   kv_find(a, blockIdx.x / (2 * a.hkv), found);
   if (found.pid < 0) return;
   const KvSpan s = found.span;
@@ -296,8 +297,9 @@ constexpr int kReadUnroll = 4;  // loads a thread has in flight
 
 template <typename IO, int D, bool E4M3>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(KvArgs a) {
-  __shared__ KvFound found;
   const int which = blockIdx.x % (2 * a.hkv), h = which / 2, tid = threadIdx.x;
+  stream_order();
+  __shared__ KvFound found;
   kv_find(a, blockIdx.x / (2 * a.hkv), found);
   if (found.pid < 0) return;
   const KvSpan s = found.span;
@@ -386,18 +388,15 @@ cudaError_t launch_kv(const KvArgs& a, bool append, cudaStream_t s) {
   const unsigned grid = (unsigned)ctas;
   // registers for the values that a page can add: one row a sequence needs one piece
   const int values = a.cu == nullptr && a.N > 1 ? D : a.page * D;
-  if (!append) {
-    kv_read_kernel<IO, D, E4M3><<<grid, kKvThreads, 0, s>>>(a);
-  } else if (values <= 4096) {
-    kv_append_kernel<IO, D, E4M3, 1><<<grid, kKvThreads, 0, s>>>(a);
-  } else if (values <= 8192) {
-    kv_append_kernel<IO, D, E4M3, 2><<<grid, kKvThreads, 0, s>>>(a);
-  } else if (values <= 16384) {  // (pages of 128 tokens at most: D / 32 pieces)
-    if constexpr (D >= 128) kv_append_kernel<IO, D, E4M3, 4><<<grid, kKvThreads, 0, s>>>(a);
-  } else {
-    if constexpr (D >= 256) kv_append_kernel<IO, D, E4M3, 8><<<grid, kKvThreads, 0, s>>>(a);
+  auto go = [&](void (*kern)(KvArgs)) { return launch_ordered(kern, dim3(grid), kKvThreads, 0, s, a); };
+  if (!append) return go(kv_read_kernel<IO, D, E4M3>);
+  if (values <= 4096) return go(kv_append_kernel<IO, D, E4M3, 1>);
+  if (values <= 8192) return go(kv_append_kernel<IO, D, E4M3, 2>);
+  if constexpr (D >= 128) {  // (pages of 128 tokens at most: D / 32 pieces)
+    if (values <= 16384) return go(kv_append_kernel<IO, D, E4M3, 4>);
   }
-  return cudaGetLastError();
+  if constexpr (D >= 256) return go(kv_append_kernel<IO, D, E4M3, 8>);
+  return cudaErrorInvalidConfiguration;
 }
 
 template <typename IO>

@@ -20,6 +20,7 @@
 
 #include "gdn_attention.h"
 #include "gdn_common.cuh"
+#include "gdn_stream_order.cuh"
 
 namespace gdn {
 namespace {
@@ -131,6 +132,7 @@ template <typename IO, int D, bool PAIRS, int U>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(IO) == 2 ? 4 : 2)
 qk_rope_kernel(QkRopeArgs a, RopeUnits un) {
   constexpr int LPR = D / kVec, RPW = 32 / LPR;
+  stream_order();
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const int64_t u = (int64_t)blockIdx.x * (kRopeThreads / 32) + threadIdx.x / 32;
   const int per_token = un.per_q + un.per_k;
@@ -245,6 +247,7 @@ qk_rope_backward_kernel(QkRopeArgs a, int ctas_q) {
   constexpr int QB = 4 * sizeof(IO);  // bytes of a group of four
   __shared__ __align__(16) float part[kWarps][D];
   extern __shared__ __align__(16) char ring[];  // [slot][x0, x1, g0, g1][thread]
+  stream_order();
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR, warp = threadIdx.x / 32;
   const bool isq = (int)blockIdx.x < ctas_q;
   const int heads = isq ? a.hq : a.hkv, T = (int)a.T;  // (T fits 31 bits)
@@ -380,7 +383,7 @@ __global__ void __launch_bounds__(1024) qk_rope_dw_kernel(QkRopeArgs a, int ctas
   const int blocks = a.D / 32;
   const bool isq = (int)blockIdx.x < blocks;
   const int c = (isq ? blockIdx.x : blockIdx.x - blocks) * 32 + lane;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  stream_order();
   float s = 0.f;
 #pragma unroll 8
   for (int i = (isq ? 0 : ctas_q) + warp; i < (isq ? ctas_q : ctas); i += 32)
@@ -400,8 +403,8 @@ cudaError_t launch_forward(const QkRopeArgs& a, RopeUnits un, cudaStream_t s) {
   const int64_t units = a.T * (un.per_q + un.per_k);
   const int64_t ctas = (units + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  qk_rope_kernel<IO, D, PAIRS, U><<<(unsigned)ctas, kRopeThreads, 0, s>>>(a, un);
-  return cudaGetLastError();
+  return launch_ordered(qk_rope_kernel<IO, D, PAIRS, U>, dim3((unsigned)ctas), kRopeThreads, 0, s, a,
+                        un);
 }
 
 template <typename IO, int D, bool PAIRS>
@@ -428,21 +431,13 @@ cudaError_t launch_rope(const QkRopeArgs& a, bool backward, cudaStream_t s) {
   if (ctas_k > most) ctas_k = most;
   const auto kern = qk_rope_backward_kernel<IO, D, PAIRS>;
   constexpr int smem = rope_ring_bytes<IO>();
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> ready{0};
+  cudaError_t e = allow_smem(kern, smem, ready);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)(ctas_q + ctas_k), kRopeThreads, smem, s>>>(a, (int)ctas_q);
-  e = cudaGetLastError();
+  e = launch_ordered(kern, dim3((unsigned)(ctas_q + ctas_k)), kRopeThreads, smem, s, a, (int)ctas_q);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(2 * D / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, qk_rope_dw_kernel, a, (int)ctas_q, (int)(ctas_q + ctas_k));
+  return launch_ordered(qk_rope_dw_kernel, dim3(2 * D / 32), 1024, 0, s, a, (int)ctas_q,
+                        (int)(ctas_q + ctas_k));
 }
 template <typename IO, int D>
 cudaError_t launch_rope_style(const QkRopeArgs& a, bool backward, cudaStream_t s) {
