@@ -71,7 +71,7 @@ def torch_binding_command(out: str) -> list:
     lib = os.path.join(torch_dir, "lib")
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
             *[f"-I{d}" for d in inc], TORCH_SRC, "-o", out, f"-L{lib}", "-ltorch_python",
-            "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+            "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False, extra: tuple = ()) -> str:

@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -115,6 +115,12 @@ class Args {
   const gdn_kv_cache* cache(int i) const {
     return static_cast<const gdn_kv_cache*>(PyLong_AsVoidPtr(v_[i]));
   }
+  const at::Tensor& workspace(int i) const {
+    const at::Tensor& t = tensor(i, "workspace");
+    if (!t.is_cuda() || !t.is_contiguous())
+      refuse(at("workspace is to be a contiguous tensor on the GPU, got ") + shown(t));
+    return t;
+  }
   // the status word: an int32 tensor, or None
   int32_t* status(int i) const {
     return static_cast<int32_t*>(const_cast<void*>(packed_or_null(i, "dev_status", at::kInt, {1})));
@@ -133,8 +139,9 @@ class Args {
 
 const float* f32(const void* p) { return static_cast<const float*>(p); }
 const int32_t* i32(const void* p) { return static_cast<const int32_t*>(p); }
+// (torch.empty without the operator's way through the dispatcher, which costs as much again)
 at::Tensor empty(at::IntArrayRef shape, const at::Tensor& like, at::ScalarType dtype) {
-  return at::empty(shape, like.options().dtype(dtype));
+  return at::Tensor(at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt));
 }
 PyObject* tuple_of(std::initializer_list<at::Tensor> tensors) {
   PyObject* t = PyTuple_New((Py_ssize_t)tensors.size());
@@ -201,7 +208,7 @@ PyObject* qk_norm_rope_backward(const Args& a) {
   at::Tensor dq = empty(r.q.sizes(), r.q, dtype), dk = empty(r.k.sizes(), r.k, dtype);
   at::Tensor dqw = empty({D}, r.q, at::kFloat), dkw = empty({D}, r.q, at::kFloat);
   const size_t need = gdn_qk_norm_rope_backward_workspace_size(&r.p);
-  at::Tensor ws = a.none(11) ? empty({(int64_t)need}, r.q, at::kByte) : a.tensor(11, "workspace");
+  at::Tensor ws = a.none(11) ? empty({(int64_t)need}, r.q, at::kByte) : a.workspace(11);
   check(gdn_qk_norm_rope_backward(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.pos, r.table, r.qw, r.kw,
                                   dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                   dqw.data_ptr<float>(), dkw.data_ptr<float>(), ws.data_ptr(),
@@ -290,7 +297,7 @@ PyObject* kv_attention(const Args& a) {
   at::Tensor out = empty(q.sizes(), q, q.scalar_type()), lse = empty({T, q.size(1)}, q, at::kFloat);
   at::Tensor ws = a.none(7)
       ? empty({(int64_t)gdn_kv_attention_workspace_size(c, &p)}, q, at::kByte)
-      : a.tensor(7, "workspace");
+      : a.workspace(7);
   check(gdn_kv_attention(c, &p, q.data_ptr(), i32(t.table.data_ptr()), t.lens, t.cu, scale,
                          (int32_t)window, out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(),
                          ws.nbytes(), a.status(8), a.stream(9)),
