@@ -37,6 +37,8 @@ constexpr int kTcMinUnits = 2;   // steps of a CTA at least
 constexpr int kTcItemUnits = 3;  // steps that starting an item is worth
 constexpr long long kWaitCycles = 2000000000LL;  // limit of a bounded wait: about a second
 
+constexpr int kSumPad = 136;     // floats between rows of key sums (conflict-free)
+
 struct TcSmem {  // byte offsets, each operand tile on a 1024-byte boundary
   static constexpr int tile = 128 * 128 * 2;
   static constexpr int K = 0;                 // 2 x [128 keys][D], 64-channel blocks
@@ -56,7 +58,7 @@ struct TcSmem {  // byte offsets, each operand tile on a 1024-byte boundary
   static constexpr int failed = tmem + 4;
   static constexpr int item = failed + 4;            // ItemState
   static constexpr int bytes = item + 64 + 1024;     // (the base is rounded up to 1024)
-  static constexpr int sums = K;  // float [64][129], at the end of an item
+  static constexpr int sums = K;  // float [rows][kSumPad], then [rows][D], at the end of an item
 };
 // A step's run of 16 keys, all within a page: where its codes begin (< 0: it has no page), its key
 // scale, log2 of its value scale, and that scale's inverse.
@@ -149,6 +151,16 @@ __device__ __forceinline__ bool soft_or(bool v) {
   return r != 0;
 }
 
+// the queries are in place: the softmax warps to the one that issues the products
+__device__ __forceinline__ void queries_in() {
+  asm volatile("barrier.cta.sync 2, %0;" ::"n"(32 * (kSoftWarps + 1)) : "memory");
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 template <int D, bool E4M3, int ROWS>
 __global__ void __launch_bounds__(kTcThreads, 1)
 kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
@@ -181,18 +193,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   auto parity = [](uint32_t step) { return (step >> 1) & 1; };
   auto parity4 = [](uint32_t step) { return (step / kAhead) & 1; };
 
-  {
-    Run run;
-    if (!plan_run<TcWork, kTcThreads>(a, kTcMinUnits, descs, run)) return;
-    if (tid == 0) {
-      state->u = run.u;
-      state->off = run.off;
-      state->per = run.per;
-      state->u1 = run.u1;
-      state->n = run.n;
-    }
-  }
-  if (warp == 0) {
+  if (warp == kOpenWarps + kSoftWarps) {
     tmem_alloc(base + TcSmem::tmem, 256);
     tmem_relinquish();
   }
@@ -213,6 +214,17 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   // (what the tiles hold past D or past the live rows only reaches lanes and columns of the products
   // that nobody reads)
   fence_before_sync();
+  {
+    Run run = {};
+    const bool any = plan_run<TcWork, kTcThreads>(a, kTcMinUnits, descs, run);
+    if (tid == 0) {
+      state->u = run.u;
+      state->off = run.off;
+      state->per = run.per;
+      state->u1 = any ? run.u1 : run.u;  // (no units: nothing to do)
+      state->n = run.n;
+    }
+  }
   __syncthreads();
   fence_after_sync();
   const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + TcSmem::tmem);  // S^T, S^T, O^T
@@ -237,7 +249,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     const int at0 = (int)(off - (int64_t)which * span);
     const int at1 = (int)(span < at0 + (u1 - u) ? span : at0 + (u1 - u));
     const int ta = max(at0 - kTcItemUnits, 0), tb = max(at1 - kTcItemUnits, 0);
-    if (tid == 0) {
+    if (tid == 32 * kOpenWarps) {  // (a softmax warp: those read it at the item's end)
       state->u = u + at1 - at0;
       state->off = off + at1 - at0;
       state->row0 = it.row0;
@@ -251,45 +263,6 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     const int row_base = (which - head * it.row_tiles) * ROWS;
     const int rows = min(ROWS, it.m * a.group - row_base);
     const int token0 = (uint32_t)row_base / (uint32_t)a.group, rem = row_base - token0 * a.group;
-
-    // queries: scaled by a power of two into [1, 2), fp16; a thread has 16 channels of a row
-#pragma unroll 1
-    for (int i = tid; i < ROWS * (D / 16); i += kTcThreads) {
-      const int row = i / (D / 16), chunk = i % (D / 16);
-      const int tk = over_group(a, rem + row), gq = rem + row - tk * a.group;
-      const bool live = row < rows;
-      float f[16], amax = 0.f;
-      load16(static_cast<const __nv_bfloat16*>(a.q) + (it.row0 + (live ? token0 + tk : 0)) * a.q_ts +
-                 (int64_t)(head * a.group + (live ? gq : 0)) * a.q_hs + 16 * chunk, f);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        f[e] = live ? f[e] : 0.f;
-        amax = fmaxf(amax, fabsf(f[e]));
-      }
-#pragma unroll
-      for (int o = 1; o < D / 16; o <<= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      int ex = (int)((__float_as_uint(amax) >> 23) & 0xff);
-      ex = ex == 0 ? 127 : min(max(ex, 2), 252);
-      const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-      if (chunk == 0) {
-        // (a row that is not live has a reference that nothing exceeds: weights 0)
-        score_scale(row) = __uint_as_float((uint32_t)ex << 23) * (a.scale * kLog2e);
-        minus_ref(row) = live ? -kNone : kNone;
-        row_last[row] = live ? it.len - it.m + token0 + tk : -1;
-      }
-      const uint32_t at = base + TcSmem::Q + (chunk / 4) * (kCols * 128) + row * 128;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[e] = pack_half(f[8 * h + 2 * e] * down, f[8 * h + 2 * e + 1] * down);
-        sts16(at + (((2 * (chunk % 4) + h) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
-      }
-    }
-    fence_async_smem();
-    __syncthreads();
 
     if (warp < kOpenWarps) {
       // ------------------------------------------------------------------ opening the codes
@@ -406,6 +379,44 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       const int sw = warp - kOpenWarps, quarter = sw & 3, half = sw >> 2;
       const int tm_lane = 32 * quarter + lane, own = 2 * quarter + (lane >> 4), st = 32 * sw + lane;
       const uint32_t tm_q = tm + ((uint32_t)(quarter * 32) << 16), tm_o = tm_q + 128;
+      // queries: scaled by a power of two into [1, 2), fp16; a thread has 16 channels of a row
+#pragma unroll 1
+      for (int i = st; i < ROWS * (D / 16); i += 32 * kSoftWarps) {
+        const int row = i / (D / 16), chunk = i % (D / 16);
+        const int tk = over_group(a, rem + row), gq = rem + row - tk * a.group;
+        const bool live = row < rows;
+        float f[16], amax = 0.f;
+        load16(static_cast<const __nv_bfloat16*>(a.q) + (it.row0 + (live ? token0 + tk : 0)) * a.q_ts +
+                   (int64_t)(head * a.group + (live ? gq : 0)) * a.q_hs + 16 * chunk, f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          f[e] = live ? f[e] : 0.f;
+          amax = fmaxf(amax, fabsf(f[e]));
+        }
+#pragma unroll
+        for (int o = 1; o < D / 16; o <<= 1)
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        int ex = (int)((__float_as_uint(amax) >> 23) & 0xff);
+        ex = ex == 0 ? 127 : min(max(ex, 2), 252);
+        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+        if (chunk == 0) {
+          // (a row that is not live has a reference that nothing exceeds: weights 0)
+          score_scale(row) = __uint_as_float((uint32_t)ex << 23) * (a.scale * kLog2e);
+          minus_ref(row) = live ? -kNone : kNone;
+          row_last[row] = live ? it.len - it.m + token0 + tk : -1;
+        }
+        const uint32_t at = base + TcSmem::Q + (chunk / 4) * (kCols * 128) + row * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = pack_half(f[8 * h + 2 * e] * down, f[8 * h + 2 * e + 1] * down);
+          sts16(at + (((2 * (chunk % 4) + h) ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
+        }
+      }
+      fence_async_smem();
+      queries_in();
       // keys that every live row sees: [all_lo, all_hi]
       const int all_hi = it.len - it.m + token0;
       const int64_t lo = (int64_t)all_hi + over_group(a, rem + rows - 1) - a.window + 1;
@@ -471,11 +482,13 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             sts16(p_at + (((2 * c + 1) ^ (lane & 7)) << 4), p[4], p[5], p[6], p[7]);
           }
         };
-        weights(false);
-        if (soft_or(top > kSlack)) {
+        // (an item's first step has no reference yet: it goes straight there)
+        const bool starts = tile == ta;
+        if (!starts) weights(false);
+        if (starts || soft_or(top > kSlack)) {
           // the rows' references move to this step's maxima; O^T of the last step has to be done
           // (that of this one waits for the weights)
-          if (tile > ta) wait_bar(bar(kSumDone, step - 1), parity(step - 1), failed);
+          if (!starts) wait_bar(bar(kSumDone, step - 1), parity(step - 1), failed);
           fence_after_sync();
 #pragma unroll
           for (int cc = 0; cc < ROWS / 32; ++cc) {
@@ -493,16 +506,13 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
               unpair(fma2(s2, a2, add2(lv2, ab.y)), z0, z1);
               unpair(fma2(s2, a2, lv2), y0, y1);
               const bool in0 = seen(la.x), in1 = seen(la.y);
-              const float over = -exp2_fast(kSlack);
+              const float over = starts ? 0.f : -exp2_fast(kSlack);
               l[8 * cc + i / 2] = fma2(pair(in0 && z0 > kSlack ? over : 0.f,
                                             in1 && z1 > kSlack ? over : 0.f), rv2, l[8 * cc + i / 2]);
               y0 = in0 ? y0 : -CUDART_INF_F;
               y1 = in1 ? y1 : -CUDART_INF_F;
-#pragma unroll
-              for (int o = 16; o; o >>= 1) {
-                y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, o));
-                y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, o));
-              }
+              y0 = warp_max(y0);
+              y1 = warp_max(y1);
               if (lane == 0) {
                 wmax[quarter * ROWS + 16 * c + i] = y0;
                 wmax[quarter * ROWS + 16 * c + i + 1] = y1;
@@ -525,20 +535,20 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             const int c = 2 * cc + half;
             if (16 * c >= rows) break;
             uint32_t s[16];
-            if (tile > ta) tmem_ld16(tm_o + 16 * c, s);
+            if (!starts) tmem_ld16(tm_o + 16 * c, s);
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
               const float f0 = 16 * c + i < rows ? row_f[16 * c + i] : 1.f;
               const float f1 = 16 * c + i + 1 < rows ? row_f[16 * c + i + 1] : 1.f;
               l[8 * cc + i / 2] = mul2(l[8 * cc + i / 2], pair(f0, f1));
-              if (tile > ta) {
+              if (!starts) {
                 s[i] = __float_as_uint(__uint_as_float(s[i]) * f0);
                 s[i + 1] = __float_as_uint(__uint_as_float(s[i + 1]) * f1);
               }
             }
-            if (tile > ta) tmem_st16(tm_o + 16 * c, s);
+            if (!starts) tmem_st16(tm_o + 16 * c, s);
           }
-          weights(true);
+          weights(!starts);
         }
         fence_async_smem();
         fence_before_sync();
@@ -561,23 +571,28 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
           const int row = 32 * cc + 16 * half + i;
           float l0, l1;
           unpair(l[8 * cc + i / 2], l0, l1);
-          if (row < rows) sums[row * 129 + tm_lane] = l0;
-          if (row + 1 < rows) sums[(row + 1) * 129 + tm_lane] = l1;
+          if (row < rows) sums[row * kSumPad + tm_lane] = l0;
+          if (row + 1 < rows) sums[(row + 1) * kSumPad + tm_lane] = l1;
         }
       soft_or(false);
       const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
-      if (st < rows) {
+#pragma unroll 1
+      for (int row = st >> 3; row < ROWS; row += 4 * kSoftWarps) {  // eight threads a row
         float L = 0.f;
-#pragma unroll 8
-        for (int i = 0; i < kKeys; ++i) L += sums[st * 129 + i];
-        const float m = -minus_ref(st);
-        row_f[st] = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
-        if (!whole) {
-          part_ml[slot * ROWS + st] = make_float2(m, L);
-        } else if (a.lse) {
-          const int tk = over_group(a, rem + st);
-          a.lse[(row0 + token0 + tk) * a.hq + head * a.group + rem + st - tk * a.group] =
-              (m + log2f(L)) * kLn2;
+#pragma unroll
+        for (int i = 0; i < kKeys / 8; ++i) L += sums[row * kSumPad + 8 * i + (st & 7)];
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (row < rows && (st & 7) == 0) {
+          const float m = -minus_ref(row);
+          row_f[row] = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+          if (!whole) {
+            part_ml[slot * ROWS + row] = make_float2(m, L);
+          } else if (a.lse) {
+            const int tk = over_group(a, rem + row);
+            a.lse[(row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group] =
+                (m + log2f(L)) * kLn2;
+          }
         }
       }
       if (ends && !begins && st == 0) {
@@ -591,32 +606,37 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         d.unused = 0;
         descs[blockIdx.x] = d;
       }
-      soft_or(false);
+      float* const o_at = sums + ROWS * kSumPad;  // [ROWS][D]
 #pragma unroll 1
       for (int c = half; 16 * c < rows; c += 2) {  // this thread's channel, sixteen rows at a time
         uint32_t s[16];
         tmem_ld16(tm_o + 16 * c, s);
         if (tm_lane < D) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int row = 16 * c + i;
-            if (row >= rows) break;
-            const float o = __uint_as_float(s[i]) * row_f[row];
-            if (whole) {
-              const int tk = over_group(a, rem + row);
-              const int64_t at =
-                  (row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group;
-              static_cast<__nv_bfloat16*>(a.out)[at * D + tm_lane] = __float2bfloat16_rn(o);
-            } else {
-              part_o[(slot * ROWS + row) * D + tm_lane] = o;
-            }
-          }
+          for (int i = 0; i < 16; ++i) o_at[(16 * c + i) * D + tm_lane] = __uint_as_float(s[i]);
         }
         __syncwarp();
+      }
+      soft_or(false);
+#pragma unroll 1
+      for (int i = st; i < rows * (D / 4); i += 32 * kSoftWarps) {
+        const int row = i / (D / 4), d = 4 * (i % (D / 4));
+        float4 o = *reinterpret_cast<const float4*>(o_at + row * D + d);
+        const float inv = row_f[row];
+        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (whole) {
+          const int tk = over_group(a, rem + row);
+          const int64_t at =
+              (row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group;
+          store4(static_cast<__nv_bfloat16*>(a.out) + at * D + d, o);
+        } else {
+          *reinterpret_cast<float4*>(part_o + (slot * ROWS + row) * D + d) = o;
+        }
       }
       fence_before_sync();
     } else if (warp == kOpenWarps + kSoftWarps) {
       // ------------------------------------------------------------------ the products
+      queries_in();
       {
         const uint32_t id = idesc_f16(128, 64, 0, 0), id_pv = idesc_f16(128, 64, 0, 1);
         const uint64_t dk = sdesc(base + TcSmem::K, 16, 1024), dq = sdesc(base + TcSmem::Q, 16, 1024);
@@ -708,7 +728,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   if (tid == 0 && *failed) set_status(a.status, GDN_ERR_DEVICE_TIMEOUT);
   fence_before_sync();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tm, 256);
+  if (warp == kOpenWarps + kSoftWarps) tmem_dealloc(tm, 256);
 }
 
 template <int D, bool E4M3, int ROWS>
