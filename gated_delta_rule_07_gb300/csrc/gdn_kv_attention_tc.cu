@@ -34,7 +34,7 @@ constexpr int kAhead = 4;        // steps whose pages are known at a time
 constexpr int kCols = 64;        // columns of S^T and O^T: an item's query rows, at most
 constexpr int kKeys = 128;       // keys of a step, lanes of S^T
 constexpr int kTcMinUnits = 2;   // steps of a CTA at least
-constexpr int kTcItemUnits = 3;  // steps that starting an item is worth
+constexpr int kTcItemUnits = 5;  // steps that starting an item is worth
 constexpr long long kWaitCycles = 2000000000LL;  // limit of a bounded wait: about a second
 
 constexpr int kSumPad = 136;     // floats between rows of key sums (conflict-free)
