@@ -38,7 +38,7 @@ namespace {
 
 constexpr int kWarps = kAttWarps, kThreads = kAttThreads;
 constexpr int kTile = 16;      // keys of a unit
-constexpr int kMinUnits = 16;  // units of a CTA at least
+constexpr int kMinUnits = 8;   // units of a CTA at least
 constexpr int kItemUnits = 8;  // units that starting an item is worth (queries, joining warps)
 
 // ---------------------------------------------------------------------------------- operands

@@ -215,24 +215,19 @@ __device__ __forceinline__ float log2_fast(float x) {
 
 // ---------------------------------------------------------------------------------- the join
 
-// Joins the partial results of the item that ended in CTA blockIdx.x and began in an earlier one.
+// Joins the partial results of the item that ended in CTA `cta` and began in CTA d.first before it.
 // A thread takes four channels of a row and every `groups`-th partial, in CTA order; the groups
 // join in shared memory, in order.  Columns (rows x D / 4) are spread over blockIdx.y.
 constexpr int kJoinThreads = 256;
 template <typename IO, int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, const float* part_o,
-                                                                  const float2* part_ml,
-                                                                  const Desc* descs, int groups) {
-  __shared__ float4 so[kJoinThreads];
-  __shared__ float2 sml[kJoinThreads];
-  stream_order();
-  const Desc d = descs[blockIdx.x];
-  if (d.first < 0) return;
+__device__ __forceinline__ void join_item(const KvArgs& a, const float* part_o,
+                                          const float2* part_ml, int cta, const Desc& d, int groups,
+                                          float4* so, float2* sml) {
   const int cols = kJoinThreads / groups, g = threadIdx.x / cols;
   const int col = blockIdx.y * cols + threadIdx.x % cols, row = col / (D / 4);
   const int dim = 4 * (col % (D / 4));
   const bool live = row < d.rows;
-  const int count = live ? (int)blockIdx.x - d.first + 1 : 0;
+  const int count = live ? cta - d.first + 1 : 0;
   // CTA first + i left its part in its second slot where the item began there, else in its first
   const int64_t slot0 = 2 * (int64_t)d.first * ROWS + row;
   float m = kNone, L = 0.f;
@@ -279,6 +274,36 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, cons
   if (a.lse && dim == 0) a.lse[at] = (m + log2f(L)) * kLn2;
 }
 
+// SEVERAL: block blockIdx.x joins the items that ended in the CTAs blockIdx.x, + gridDim.x, ..;
+// else the one that ended in CTA blockIdx.x, if any did.
+template <typename IO, int D, int ROWS, bool SEVERAL>
+__global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, const float* part_o,
+                                                                  const float2* part_ml,
+                                                                  const Desc* descs, int ctas,
+                                                                  int groups) {
+  __shared__ float4 so[kJoinThreads];
+  __shared__ float2 sml[kJoinThreads];
+  stream_order();
+  if constexpr (SEVERAL) {
+    __shared__ int ending[kMaxCtas], items;
+    if (threadIdx.x == 0) items = 0;
+    __syncthreads();
+    // (in any order: items do not depend on each other)
+    for (int c = blockIdx.x + threadIdx.x * gridDim.x; c < ctas; c += kJoinThreads * gridDim.x)
+      if (descs[c].first >= 0) ending[atomicAdd(&items, 1)] = c;
+    __syncthreads();
+    for (int i = 0; i < items; ++i) {
+      const Desc d = descs[ending[i]];
+      join_item<IO, D, ROWS>(a, part_o, part_ml, ending[i], d, groups, so, sml);
+      __syncthreads();
+    }
+  } else {
+    const Desc d = descs[blockIdx.x];
+    if (d.first >= 0)
+      join_item<IO, D, ROWS>(a, part_o, part_ml, (int)blockIdx.x, d, groups, so, sml);
+  }
+}
+
 // --------------------------------------------------------------------------------- launching
 
 struct Workspace {  // two partial results of each CTA, a descriptor of each
@@ -307,18 +332,27 @@ template <typename W> int grid_ctas(const KvArgs& a, int resident, int min_units
 
 template <typename IO, int D, int ROWS>
 cudaError_t launch_join(const KvArgs& a, const Workspace& ws, int ctas, cudaStream_t s) {
+  // Few long items: a block for each CTA would mostly find nothing to join, and setting those up
+  // takes time (one sequence of 60000 keys, 2 kv heads: 26.2 us with a block a CTA, 19.7 with four
+  // an item; 32 sequences of up to 8192 keys, 8 kv heads: 18.9 with a block a CTA, 20.2 with one
+  // an item).
+  const int64_t items = (int64_t)a.N * a.hkv, parts = ctas / items;
+  const bool few = 4 * items < ctas;
   // An item has about `parts` partials where the sequences are alike, several times as many where
   // some are longer: four groups of threads for each and more from 16 partials on, so that a thread
-  // takes a few.  32 sequences of up to 8192 keys take 18.8 us so, 21.9 with one group, 19.6 with
-  // groups for every partial.  Where most items have none (256 sequences of up to 500 keys) more
-  // groups only cost blocks: 19.2 us with four, 18.3 with one.
-  const int64_t parts = ctas / ((int64_t)a.N * a.hkv);
+  // takes a few.  Those 32 sequences take 18.9 us so, 21.9 with one group, 19.6 with groups for
+  // every partial.  Where most items have none (256 sequences of up to 500 keys) more groups only
+  // cost blocks: 19.2 us with four, 18.3 with one.
   constexpr int all_cols = ROWS * (D / 4);
   int groups = all_cols < kJoinThreads ? kJoinThreads / all_cols : 1;
-  while (groups < 16 && ((parts > 0 && groups < 4) || 4 * groups < parts)) groups *= 2;
-  return launch_ordered(kv_attention_join<IO, D, ROWS>, dim3(ctas, all_cols * groups / kJoinThreads),
-                        kJoinThreads, 0, s, a, (const float*)ws.part_o, (const float2*)ws.part_ml,
-                        (const Desc*)ws.descs, groups);
+  while (groups < (few ? 64 : 16) && ((parts > 0 && groups < 4) || 4 * groups < parts)) groups *= 2;
+  const auto go = [&](auto kern, int blocks) {
+    return launch_ordered(kern, dim3(blocks, all_cols * groups / kJoinThreads), kJoinThreads, 0, s, a,
+                          (const float*)ws.part_o, (const float2*)ws.part_ml,
+                          (const Desc*)ws.descs, ctas, groups);
+  };
+  if (few) return go(kv_attention_join<IO, D, ROWS, true>, (int)(4 * items));
+  return go(kv_attention_join<IO, D, ROWS, false>, ctas);
 }
 
 }  // namespace

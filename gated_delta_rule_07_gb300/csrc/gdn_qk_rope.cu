@@ -375,25 +375,29 @@ qk_rope_backward_kernel(QkRopeArgs a, int ctas_q) {
   }
 }
 
-// dw = the sum of the query CTAs' (key CTAs') partial sums: a block has 32 columns of one of them,
-// its 32 warps every 32nd CTA
+// dw = the sum of the query CTAs' (key CTAs') partial sums.  A block has eight columns of one of
+// them, its threads every 128th CTA each: few dependent steps, in a fixed order.
 __global__ void __launch_bounds__(1024) qk_rope_dw_kernel(QkRopeArgs a, int ctas_q, int ctas) {
-  __shared__ float part[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-  const int blocks = a.D / 32;
+  __shared__ float part[32][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, sub = lane / 8;
+  const int blocks = a.D / 8;
   const bool isq = (int)blockIdx.x < blocks;
-  const int c = (isq ? blockIdx.x : blockIdx.x - blocks) * 32 + lane;
+  const int c = (isq ? blockIdx.x : blockIdx.x - blocks) * 8 + lane % 8;
   stream_order();
   float s = 0.f;
-#pragma unroll 8
-  for (int i = (isq ? 0 : ctas_q) + warp; i < (isq ? ctas_q : ctas); i += 32)
+#pragma unroll 4
+  for (int i = (isq ? 0 : ctas_q) + 4 * warp + sub; i < (isq ? ctas_q : ctas); i += 128)
     s += a.partial[(int64_t)i * a.D + c];
-  part[warp][lane] = s;
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  if (sub == 0) part[warp][lane] = s;
   __syncthreads();
-  s = part[lane][warp];  // warp w joins column w
+  if (threadIdx.x < 8) {
+    float sum = 0.f;
 #pragma unroll
-  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (lane == 0) (isq ? a.dwq : a.dwk)[c - lane + warp] = s;
+    for (int i = 0; i < 32; ++i) sum += part[i][lane];
+    (isq ? a.dwq : a.dwk)[c] = sum;
+  }
 }
 
 int div_up(int64_t x, int64_t y) { return (int)((x + y - 1) / y); }
@@ -436,7 +440,7 @@ cudaError_t launch_rope(const QkRopeArgs& a, bool backward, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_ordered(kern, dim3((unsigned)(ctas_q + ctas_k)), kRopeThreads, smem, s, a, (int)ctas_q);
   if (e != cudaSuccess) return e;
-  return launch_ordered(qk_rope_dw_kernel, dim3(2 * D / 32), 1024, 0, s, a, (int)ctas_q,
+  return launch_ordered(qk_rope_dw_kernel, dim3(2 * D / 8), 1024, 0, s, a, (int)ctas_q,
                         (int)(ctas_q + ctas_k));
 }
 template <typename IO, int D>
