@@ -453,11 +453,16 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 // rows of a kv head in the average sequence
 int64_t average_rows(const KvArgs& a) { return (a.T + a.N - 1) / a.N * a.group; }
 
-// More than eight rows: the tcgen05 kernel, where it is built.
-bool use_tc(const KvArgs& a) { return a.bf16 && a.D <= 128 && average_rows(a) > 8; }
+// More than sixteen rows: the tcgen05 kernel, where it is built.  int8, 4 kv heads of 128: 24
+// sequences of 20000 keys with 8 .. 40 rows take 131 us there and 203 here, with 8 .. 64 rows 154 and
+// 273, but with 8 or 16 rows 117 and 107; 16 x 20000 keys with 16 rows 78 and 69; one sequence of
+// 1500 keys with 16 rows 12.6 and 8.8; 64 x 65536 with 8 rows 912 and 579.
+bool use_tc(const KvArgs& a) { return a.bf16 && a.D <= 128 && average_rows(a) > 16; }
 
 // Tiles of 8 rows a warp carries: as many as the average sequence's rows fill (a row tile more
-// reads the cache once more), within the registers (D NT <= 512).
+// reads the cache once more), within the registers (D NT <= 512).  16 x 30000 keys, 4 kv heads of
+// 128, fp32: 8 rows take 84 us with one tile (two: 118); 16 rows 112 with two (one: 154, four: 206);
+// 32 rows 189 with four (two: 211).
 int row_tiles(const KvArgs& a) {
   const int64_t rows = average_rows(a);
   return rows <= 8 ? 1 : rows <= 16 || a.D == 256 ? 2 : 4;
@@ -486,8 +491,8 @@ cudaError_t launch_rows(const KvArgs& a, cudaStream_t s) {
   const int tiles = row_tiles(a);
   if (tiles == 1) return launch<IO, D, 1, E4M3>(a, s);
   if constexpr (D == 256) return launch<IO, D, 2, E4M3>(a, s);
-  // (bf16 with more rows and smaller heads runs on tcgen05)
-  else if constexpr (sizeof(IO) == 2) return cudaErrorInvalidConfiguration;
+  // (bf16 with more rows of smaller heads runs on tcgen05)
+  else if constexpr (sizeof(IO) == 2) return launch<IO, D, 2, E4M3>(a, s);
   else return tiles == 2 ? launch<IO, D, 2, E4M3>(a, s) : launch<IO, D, 4, E4M3>(a, s);
 }
 template <typename IO, bool E4M3>

@@ -225,8 +225,9 @@ qk_rope_kernel(QkRopeArgs a, RopeUnits un) {
 // share of the weight's gradient in registers; a CTA's warps join theirs in shared memory and
 // write one partial sum per CTA, which qk_rope_dw_kernel adds up in a fixed order: the same bits
 // on every run.  A thread's rows come through a ring of its own in shared memory (cp.async), so
-// that kRopeRing - 1 of them are on their way without holding registers.
-constexpr int kRopeRing = 4;
+// that the next is on its way without holding registers.  8192 tokens of 18 heads of 256 take 42.8 us
+// with two slots, 45.0 with three, 45.7 with four (the L1 cache gets what the ring leaves).
+constexpr int kRopeRing = 2;
 template <typename IO> constexpr int rope_ring_bytes() {
   return kRopeRing * 4 * kRopeThreads * 4 * (int)sizeof(IO);
 }
@@ -415,19 +416,22 @@ template <typename IO, int D, bool PAIRS>
 cudaError_t launch_rope(const QkRopeArgs& a, bool backward, cudaStream_t s) {
   constexpr int RPW = 32 * kVec / D, kWarps = kRopeThreads / 32;
   if (!backward) {
-    // as many heads a unit as leave two units for each of the GPU's 32 x 152 warps, sixteen steps
-    // at most; a single step where tokens are few
+    // Heads of a unit: sixteen steps, four, or one, the most that leaves 4096 units (27 warps an SM).
+    // 16384 tokens of 40 heads of 128 take 59.4 us with sixteen, 62.1 with four, 121.5 with one;
+    // 1024 such tokens 5.4, 5.2 and 7.3; 256 tokens of 18 heads of 256 take 5.2, 3.0 and 2.7.
     RopeUnits un;
     for (un.steps = 16;; un.steps /= 4) {
       un.per_q = div_up(a.hq, un.steps * RPW);
       un.per_k = div_up(a.hkv, un.steps * RPW);
-      if (un.steps == 1 || a.T * (un.per_q + un.per_k) >= 2 * 32 * 152) break;
+      if (un.steps == 1 || a.T * (un.per_q + un.per_k) >= 4096) break;
     }
     return un.steps == 1 ? launch_forward<IO, D, PAIRS, 1>(a, un, s)
                          : launch_forward<IO, D, PAIRS, 4>(a, un, s);
   }
-  // three CTAs an SM at most, shared between query and key rows by their number; a warp a token
-  const int most = div_up(a.T, kWarps);
+  // Three CTAs an SM at most, shared between query and key rows by their number (8192 tokens of 18
+  // heads of 256: 42.8 us; two an SM 48.6, four 53.2); where tokens are few, a warp two of them
+  // (1531 tokens of 9 heads of 64, fp32: 6.5 us; one 7.1, four 7.9).
+  const int most = div_up(a.T, 2 * kWarps);
   int64_t ctas_q = (int64_t)kRopeCtas * a.hq / (a.hq + a.hkv);
   ctas_q = ctas_q < 1 ? 1 : ctas_q > kRopeCtas - 1 ? kRopeCtas - 1 : ctas_q;
   int64_t ctas_k = kRopeCtas - ctas_q;
