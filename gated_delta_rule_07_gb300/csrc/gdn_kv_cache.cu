@@ -65,14 +65,26 @@ __device__ __forceinline__ void load8(Quad<IO>* q, const IO* p) {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-// largest finite magnitude so far; `bad` where an element is not finite
-__device__ __forceinline__ void take_amax(const float* f, float& amax, bool& bad) {
+// The largest magnitude so far, as bits without the sign: their order is that of the magnitudes, with
+// infinities and NaN above the finite ones.  bf16: of the even and of the odd elements.
+__device__ __forceinline__ void take_bits(const Quad<float>& q, uint32_t& m) {
+  m = max(max(m, __float_as_uint(q.v.x) & 0x7fffffffu), __float_as_uint(q.v.y) & 0x7fffffffu);
+  m = max(max(m, __float_as_uint(q.v.z) & 0x7fffffffu), __float_as_uint(q.v.w) & 0x7fffffffu);
+}
+__device__ __forceinline__ void take_bits(const Quad<__nv_bfloat16>& q, uint32_t& m) {
+  m = __vmaxu2(__vmaxu2(m, q.v.x & 0x7fff7fffu), q.v.y & 0x7fff7fffu);
+}
+template <typename IO> __device__ __forceinline__ float bits_value(uint32_t m) {
+  if constexpr (sizeof(IO) == 4) return __uint_as_float(m);
+  else return __uint_as_float(max(m & 0xffff0000u, m << 16));
+}
+// the largest finite magnitude
+template <typename IO> __device__ __forceinline__ void take_finite(const Quad<IO>& q, float& amax) {
+  float f[4];
+  q.open(f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float m = fabsf(f[i]);
-    if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
-    else bad = true;
-  }
+  for (int i = 0; i < 4; ++i)
+    if (finite(f[i])) amax = fmaxf(amax, fabsf(f[i]));
 }
 
 // Elements that are not finite, once the page's scale is known: a NaN becomes 0, an infinity the
@@ -159,16 +171,22 @@ template <typename IO, int D, bool E4M3, int IT> struct NewKeys {
   __device__ __forceinline__ void store(const KvArgs& a, const KvSpan& s, int64_t block, float* red) {
     const int tid = threadIdx.x, pieces = (s.hi - s.lo) * (D / 8);
     uint8_t* codes = a.k_codes + block * a.page * D;
-    float amax = 0.f, f[4];
-    bool bad = false;
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       if (i && i * kKvThreads >= pieces) break;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        q[i][j].open(f);
-        take_amax(f, amax, bad);
-      }
+      for (int j = 0; j < 2; ++j) take_bits(q[i][j], top);
+    }
+    float amax = bits_value<IO>(top), f[4];
+    const bool bad = !finite(amax);
+    if (bad) {
+      amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (!i || i * kKvThreads < pieces) take_finite(q[i][j], amax);
     }
     const NewScale n = new_scale<E4M3>(amax, bad, held, red, a.status);
     if (n.now > n.held && n.held > 0.f) {  // the page's earlier codes on the new scale
@@ -232,16 +250,22 @@ template <typename IO, int D, bool E4M3, int IT> struct NewValues {
     const int tid = threadIdx.x, g0 = s.lo / 4;
     const int pieces = ((s.hi + 3) / 4 - g0) * (D / 4);
     uint8_t* codes = a.v_codes + block * a.page * D;
-    float amax = 0.f, f[4];
-    bool bad = false;
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
       if (i && i * kKvThreads >= pieces) break;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        q[i][t].open(f);
-        take_amax(f, amax, bad);
-      }
+      for (int t = 0; t < 4; ++t) take_bits(q[i][t], top);
+    }
+    float amax = bits_value<IO>(top), f[4];
+    const bool bad = !finite(amax);
+    if (bad) {
+      amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < IT; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (!i || i * kKvThreads < pieces) take_finite(q[i][t], amax);
     }
     const NewScale n = new_scale<E4M3>(amax, bad, held, red, a.status);
     const bool grew = n.now > n.held && n.held > 0.f;
