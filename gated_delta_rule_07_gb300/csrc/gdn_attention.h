@@ -48,7 +48,7 @@ cudaError_t kv_append(const KvArgs& a, cudaStream_t s);
 cudaError_t kv_read(const KvArgs& a, cudaStream_t s);
 cudaError_t kv_attention(const KvArgs& a, cudaStream_t s);
 size_t kv_attention_workspace(const KvArgs& a);
-// its form on tcgen05, for more than eight rows a kv head (bf16, D <= 128)
+// its form on tcgen05, for more than sixteen rows a kv head (bf16, D <= 128)
 cudaError_t kv_attention_tc(const KvArgs& a, cudaStream_t s);
 size_t kv_attention_tc_workspace(const KvArgs& a);
 

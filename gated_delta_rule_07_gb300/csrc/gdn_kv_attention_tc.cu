@@ -1,4 +1,4 @@
-// gdn_kv_attention_tc.cu -- attention over the paged 8-bit cache where a kv head has more than eight
+// gdn_kv_attention_tc.cu -- attention over the paged 8-bit cache where a kv head has more than sixteen
 // query rows a sequence (large groups, drafted tokens): bf16 I/O, D <= 128, on tcgen05.
 //
 // With few rows, opening a code costs more than using it, so here each code is opened once for up
@@ -13,13 +13,21 @@
 //     writes its weights as part of one operand row.  As in the kernel for few rows the reference
 //     of the weights only moves when a step exceeds it; only then is the sum in Tensor Memory
 //     rescaled.  The sums of the weights stay in the threads' registers until the item ends.
-//   * One CTA an SM, its warps in three parts that hand steps to each other by mbarriers, each
+//   * One CTA an SM, its warps in four parts that hand steps to each other by mbarriers, each
 //     buffer twice: eight warps load codes (a step ahead, in registers) and open them; eight turn
 //     scores into weights; one thread issues the products, S^T of a step before O^T of the last;
 //     one warp looks pages and scales up, a few steps ahead, for all of them.  So opening, softmax
 //     and products of different steps run side by side, and each part's chain of instructions a
 //     step, which is what bounds the kernel, is short.
 // Work is cut as in the other kernel, in units of 128 keys.
+//
+// A step of 128 keys of 128 channels moves 32 KB of codes from HBM (1220 cycles at the SM's share of
+// a copy's rate) and about 170 KB through shared memory (the opened tiles written and read again by
+// the products, weights, queries: about 1350 cycles).  It takes about 2200: the two chains a step,
+// codes loaded and opened, and scores read, weighed and written, each wait on the products once.
+// Measured (GB300): 24 sequences of up to 20000 keys, 4 kv heads of 128, 8 .. 40 rows: 131 us (48% of
+// the copy's rate; tensor pipe 20% busy); 8 .. 64 rows 154 us.  Items of 32 keep half the sums in the
+// softmax's 96 registers.
 #include "gdn_kv_attention.cuh"
 #include "gdn_sm100.cuh"
 
@@ -33,8 +41,10 @@ constexpr int kTcThreads = 32 * (kOpenWarps + kSoftWarps + 2);
 constexpr int kAhead = 4;        // steps whose pages are known at a time
 constexpr int kCols = 64;        // columns of S^T and O^T: an item's query rows, at most
 constexpr int kKeys = 128;       // keys of a step, lanes of S^T
-constexpr int kTcMinUnits = 2;   // steps of a CTA at least
-constexpr int kTcItemUnits = 5;  // steps that starting an item is worth
+constexpr int kTcMinUnits = 2;   // steps of a CTA at least (4 x 9000 keys: 1 to 4 within 5%)
+// Steps that starting an item is worth: 40 ragged sequences of up to 9000 keys, 24 rows, take 28.6 us
+// with 5, 30.6 with 4, 39.3 with 2; 24 x 20000 keys 131 us with any of them.
+constexpr int kTcItemUnits = 5;
 constexpr long long kWaitCycles = 2000000000LL;  // limit of a bounded wait: about a second
 
 constexpr int kSumPad = 136;     // floats between rows of key sums (conflict-free)
@@ -652,10 +662,10 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             const uint64_t k = dk + (step & 1) * (TcSmem::tile >> 4);
             if (elected()) {
 #pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              mma_ss(tm + 64 * (step & 1), k + (((s >> 2) * 16384 + (s & 3) * 32) >> 4),
-                     dq + (((s >> 2) * (kCols * 128) + (s & 3) * 32) >> 4), id, s > 0);
-            mma_commit(bar(kScoresDone, step));
+              for (int s = 0; s < D / 16; ++s)
+                mma_ss(tm + 64 * (step & 1), k + (((s >> 2) * 16384 + (s & 3) * 32) >> 4),
+                       dq + (((s >> 2) * (kCols * 128) + (s & 3) * 32) >> 4), id, s > 0);
+              mma_commit(bar(kScoresDone, step));
             }
             __syncwarp();
           }
@@ -668,10 +678,10 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             const uint64_t p = dp + (prev & 1) * (TcSmem::p_tile >> 4);
             if (elected()) {
 #pragma unroll
-            for (int s = 0; s < kKeys / 16; ++s)
-              mma_ss(tm + 128, v + (((s >> 2) * 16384 + (s & 3) * 32) >> 4), p + ((s * 2048) >> 4),
-                     id_pv, i > 1 || s > 0);
-            mma_commit(bar(kSumDone, prev));
+              for (int s = 0; s < kKeys / 16; ++s)
+                mma_ss(tm + 128, v + (((s >> 2) * 16384 + (s & 3) * 32) >> 4), p + ((s * 2048) >> 4),
+                       id_pv, i > 1 || s > 0);
+              mma_commit(bar(kSumDone, prev));
             }
             __syncwarp();
           }
@@ -751,6 +761,8 @@ cudaError_t launch_tc(const KvArgs& a, cudaStream_t s) {
 
 // Rows of an item: 32 where the average sequence's rows of a kv head fit, which leaves the softmax's
 // threads half the sums to hold; else 64 (a row tile more reads and opens the codes once more).
+// 24 x 20000 keys with 22 rows on average take 131 us with 32 (146 with 64), with 36 rows 154 us with
+// 64 (172 with 32).
 int item_rows(const KvArgs& a) { return (a.T + a.N - 1) / a.N * a.group <= 32 ? 32 : 64; }
 
 template <int D, bool E4M3>

@@ -467,7 +467,13 @@ size_t gdn_kv_attention_workspace_size(const gdn_kv_cache* cache, const gdn_kv_p
  *     out = sum_j softmax_j(scale q . k_j) v_j,   lse = log sum_j exp(scale q . k_j)
  *   q [T, hq, D] io dtype, strided;  kv_lens int32 [N];  out [T, hq, D] io dtype, contiguous;
  *   lse [T, hq] fp32, or NULL.  A row without keys (kv_lens 0, or p < 0) gets out = 0, lse = -inf.
- * Made for one or a few rows per sequence (decode, drafted tokens); any number is computed.  */
+ * Made for one or a few rows per sequence (decode, drafted tokens); any number is computed.
+ * hq <= 32768, T hq < 2^31, max_pages page_size <= 2^30 (lengths fit 30 bits; byte offsets into the
+ * pool are 64-bit).  dev_status records GDN_ERR_DEVICE_INPUT as above, and GDN_ERR_DEVICE_TIMEOUT if
+ * a wait inside the kernel ran out (about a second; outputs are then undefined).  The same inputs
+ * give the same bits.  Products take fp16 operands with fp32 sums: codes are exact in fp16; bf16
+ * queries are too, after a power of two per row; fp32 queries, and for them the weights, are split
+ * into two fp16 parts. */
 gdn_status gdn_kv_attention(const gdn_kv_cache* cache, const gdn_kv_problem* p, const void* q,
                             const int32_t* block_table, const int32_t* kv_lens,
                             const int32_t* cu_seqlens, float scale, int32_t window, void* out,
