@@ -419,13 +419,6 @@ def _refuse(where, why, status=1):
     raise GdnError(status, f"{where}: {why}")
 
 
-def _style(where, style):
-    code = _ROPE_STYLES.get(style)
-    if code is None:
-        _refuse(where, f"style {style!r}")
-    return code
-
-
 def _hold(stream, *tensors):
     """Outputs and temporaries allocated on the current stream and used on `stream`: their memory
     is not handed out again before the work on `stream` is done."""
@@ -460,7 +453,9 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-
                  weight_offset=0.0, style="half", check_status=False, stream=None):
     """Queries [T, hq, D] and keys [T, hkv, D], normalised per head and rotated by position (see
     include/gdn.h); q and k may be slices of one projection.  Returns contiguous tensors."""
-    code = _style("qk_norm_rope", style)
+    code = _ROPE_STYLES.get(style)
+    if code is None:
+        _refuse("qk_norm_rope", f"style {style!r}")
     if stream is None and not check_status:
         return _native.qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps,
                                     weight_offset, code, None, None)
@@ -492,7 +487,13 @@ def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, 
     """Gradients (dq, dk, dq_weight, dk_weight) of <dq_out, q_out> + <dk_out, k_out> through
     qk_norm_rope on the same inputs."""
     where = "qk_norm_rope_backward"
-    code = _style(where, style)
+    code = _ROPE_STYLES.get(style)
+    if code is None:
+        _refuse(where, f"style {style!r}")
+    if stream is None and not check_status:
+        return _native.qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out,
+                                             dk_out, eps, weight_offset, code, workspace, None,
+                                             None)
     if workspace is None and stream is not None:
         (T, hq, D), (rows, R) = q.shape, cos_sin.shape
         p = QkRopeProblem(T, hq, k.shape[1], D, R, code, _IO.get(q.dtype, -1), rows, eps,
@@ -553,6 +554,9 @@ def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=
     """Quantises new keys and values [T, hkv, D] into the cache's pages, behind the ctx_lens[n]
     tokens that each sequence already holds.  Without cu_seqlens the rows are one sequence's, or
     one row each of T sequences."""
+    if stream is None and not check_status:
+        _native.kv_append(cache._address, k, v, block_table, ctx_lens, cu_seqlens, None, None)
+        return
     _checked(check_status, k.device, stream, "kv_append", lambda st: _native.kv_append(
         cache._address, k, v, block_table, ctx_lens, cu_seqlens, st, _handle(stream)))
 
@@ -571,6 +575,9 @@ def kv_read(cache, block_table, start, cu_seqlens, tokens, dtype=torch.bfloat16,
     io = _IO.get(dtype)
     if io is None:
         _refuse("kv_read", f"dtype {dtype}", 2)
+    if stream is None and not check_status:
+        return _native.kv_read(cache._address, block_table, start, cu_seqlens, tokens, io, None,
+                               None)
     out = _checked(check_status, block_table.device, stream, "kv_read", lambda st: _native.kv_read(
         cache._address, block_table, start, cu_seqlens, tokens, io, st, _handle(stream)))
     if stream is not None:
