@@ -289,21 +289,12 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       const uint8_t* const kp = a.k_codes + r * D + 16 * c4;
       const uint8_t* const vp = a.v_codes + 8 * g * D + 16 * x;
       uint4 kb[2][KC], vb[VC][2];
-      auto load_k = [&](int64_t from) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int h = 0; h < KC; ++h)
-            kb[j][h] = from >= 0 ? ld_stream(kp + from + 8 * D * j + 64 * h)
-                                 : make_uint4(0u, 0u, 0u, 0u);
+      auto load_k = [&](int64_t from, int j, int h) {
+        kb[j][h] = from >= 0 ? ld_stream(kp + from + 8 * D * j + 64 * h) : make_uint4(0u, 0u, 0u, 0u);
       };
-      auto load_v = [&](int64_t from) {
-#pragma unroll
-        for (int i = 0; i < VC; ++i)
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-            vb[i][t] = from >= 0 ? ld_stream(vp + from + 256 * i + 4 * D * t)
-                                 : make_uint4(0u, 0u, 0u, 0u);
+      auto load_v = [&](int64_t from, int i, int t) {
+        vb[i][t] =
+            from >= 0 ? ld_stream(vp + from + 256 * i + 4 * D * t) : make_uint4(0u, 0u, 0u, 0u);
       };
       auto from_of = [&](uint32_t step) {  // (once its pages are in)
         return *reinterpret_cast<volatile int64_t*>(&runs[step % kAhead * 8 + warp].from);
@@ -311,9 +302,22 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       wait_bar(pages_bar(step0), parity4(step0), failed);
       {
         const int64_t from = from_of(step0);
-        load_k(from);
-        load_v(from);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int h = 0; h < KC; ++h) load_k(from, j, h);
+#pragma unroll
+        for (int i = 0; i < VC; ++i)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) load_v(from, i, t);
       }
+      // A register's codes of the next step are asked for as soon as this step's are taken.
+      auto next_from = [&](int tile, uint32_t step) -> int64_t {
+        if (tile >= tb) return -1;
+        wait_bar(pages_bar(step), parity4(step), failed);
+        return from_of(step);
+      };
+      int64_t from = next_from(ta + 1, step0 + 1);
       uint32_t step = step0;
       for (int tile = ta; tile < tb; ++tile, ++step) {
         const uint32_t at = (step & 1) * TcSmem::tile;
@@ -328,6 +332,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             open_codes<E4M3>(w.y, y[2], y[3]);
             open_codes<E4M3>(w.z, y[4], y[5]);
             open_codes<E4M3>(w.w, y[6], y[7]);
+            load_k(from, j, h);
             const uint32_t to = k_at + at + h * 16384 + j * 1024;
             sts16(to + k_c0, y[0], y[1], y[2], y[3]);
             sts16(to + k_c1, y[4], y[5], y[6], y[7]);
@@ -335,12 +340,6 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kKeysIn, step));
-        int64_t from = -1;
-        if (tile + 1 < tb) {
-          wait_bar(pages_bar(step + 1), parity4(step + 1), failed);
-          from = from_of(step + 1);
-        }
-        load_k(from);
         const int left = it.len - (it.tile0 + tile) * kKeys - 16 * warp;  // keys up to the length
         if (E4M3 && left < 16) {  // bytes past the length: no NaN under their weights of 0
 #pragma unroll
@@ -366,6 +365,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             w[t][1] = turn ? vb[i][t].w : vb[i][t].y;
             w[t][2] = turn ? vb[i][t].x : vb[i][t].z;
             w[t][3] = turn ? vb[i][t].y : vb[i][t].w;
+            load_v(from, i, t);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -380,7 +380,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kValuesIn, step));
-        load_v(from);
+        from = next_from(tile + 2, step + 2);
       }
     } else if (warp < kOpenWarps + kSoftWarps) {
       // ------------------------------------------------------------------ scores to weights
