@@ -38,7 +38,7 @@ using namespace sm100;
 
 constexpr int kOpenWarps = 8, kSoftWarps = 8;  // then one that issues, one that looks pages up
 constexpr int kTcThreads = 32 * (kOpenWarps + kSoftWarps + 2);
-constexpr int kAhead = 4;        // steps whose pages are known at a time
+constexpr int kAhead = 8;        // steps whose pages are known at a time
 constexpr int kCols = 64;        // columns of S^T and O^T: an item's query rows, at most
 constexpr int kKeys = 128;       // keys of a step, lanes of S^T
 constexpr int kTcMinUnits = 2;   // steps of a CTA at least (4 x 9000 keys: 1 to 4 within 5%)
@@ -201,7 +201,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
   auto pages_bar = [&](uint32_t step) { return bars + 8 * (kPagesIn + step % kAhead); };
   // a step's buffers are used every other step: the parity of its own use of a barrier
   auto parity = [](uint32_t step) { return (step >> 1) & 1; };
-  auto parity4 = [](uint32_t step) { return (step / kAhead) & 1; };
+  auto parity_ahead = [](uint32_t step) { return (step / kAhead) & 1; };
 
   if (warp == kOpenWarps + kSoftWarps) {
     tmem_alloc(base + TcSmem::tmem, 256);
@@ -299,7 +299,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       auto from_of = [&](uint32_t step) {  // (once its pages are in)
         return *reinterpret_cast<volatile int64_t*>(&runs[step % kAhead * 8 + warp].from);
       };
-      wait_bar(pages_bar(step0), parity4(step0), failed);
+      wait_bar(pages_bar(step0), parity_ahead(step0), failed);
       {
         const int64_t from = from_of(step0);
 #pragma unroll
@@ -314,7 +314,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       // A register's codes of the next step are asked for as soon as this step's are taken.
       auto next_from = [&](int tile, uint32_t step) -> int64_t {
         if (tile >= tb) return -1;
-        wait_bar(pages_bar(step), parity4(step), failed);
+        wait_bar(pages_bar(step), parity_ahead(step), failed);
         return from_of(step);
       };
       int64_t from = next_from(ta + 1, step0 + 1);
@@ -657,7 +657,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
           const uint32_t step = step0 + i;
           if (i < steps) {  // S^T of this step
             wait_bar(bar(kKeysIn, step), parity(step), failed);
-            if (step >= 2) wait_bar(read_bar(step - 2), parity4(step - 2), failed);
+            if (step >= 2) wait_bar(read_bar(step - 2), parity_ahead(step - 2), failed);
             fence_after_sync();
             const uint64_t k = dk + (step & 1) * (TcSmem::tile >> 4);
             if (elected()) {
@@ -690,19 +690,21 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       __syncwarp();
     } else {
       // ------------------------------------------------------------------ pages and scales
-      // lanes 0 .. 7: a run of 16 keys each; the table's entry two steps ahead of its scales' use
+      // Four steps at a time, eight lanes each, a lane a run of 16 keys; the table's entries four
+      // steps ahead of their scales' use.  (One step at a time, the loads' latency each step held the
+      // whole kernel back: 131 us for 24 x 20000 keys.)
+      constexpr int kBatch = 4;
       const int* table = a.table + (int64_t)n * a.max_pages;
-      auto has_page = [&](int tile) {
-        return lane < 8 && tile < tb && (it.tile0 + tile) * kKeys + 16 * lane < it.len;
-      };
+      const int mine = lane >> 3, at = 16 * (lane & 7);
+      auto has_page = [&](int tile) { return tile < tb && (it.tile0 + tile) * kKeys + at < it.len; };
       auto entry_of = [&](int tile) {
-        const int key = (it.tile0 + tile) * kKeys + 16 * lane;
+        const int key = (it.tile0 + tile) * kKeys + at;
         return has_page(tile) ? __ldg(table + (key >> a.page_shift)) : -1;
       };
-      int entry = entry_of(ta);
+      int entry = entry_of(ta + mine);
       uint32_t step = step0;
-      for (int tile = ta; tile < tb; ++tile, ++step) {
-        const int next = entry_of(tile + 1);
+      for (int tile = ta; tile < tb; tile += kBatch, step += kBatch) {
+        const int next = entry_of(tile + kBatch + mine);
         PageRun run;
         run.from = -1;
         run.unused = 0;
@@ -710,10 +712,10 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         run.ks = 0.f;
         run.lv = -CUDART_INF_F;
         run.rv = run.unused2 = 0.f;
-        if (has_page(tile)) {
+        if (has_page(tile + mine)) {
           if (entry >= 0 && entry < a.num_pages) {
             const int64_t block = (int64_t)entry * a.hkv + head;
-            const int slot = ((it.tile0 + tile) * kKeys + 16 * lane) & (a.page - 1);
+            const int slot = ((it.tile0 + tile + mine) * kKeys + at) & (a.page - 1);
             const float vs = __ldg(a.v_scale + block);
             run.from = block * (a.page * D) + slot * D;
             run.ks = __ldg(a.k_scale + block);
@@ -724,11 +726,13 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
           }
         }
         entry = next;
-        // the slot's last user: the softmax of kAhead steps before
-        if (step >= kAhead) wait_bar(read_bar(step), parity4(step - kAhead), failed);
-        if (lane < 8) runs[step % kAhead * 8 + lane] = run;
+        // the slots' last users: the softmax of kAhead steps before
+        const int steps = min(kBatch, tb - tile);
+        for (int i = 0; i < steps; ++i)
+          if (step + i >= kAhead) wait_bar(read_bar(step + i), parity_ahead(step + i - kAhead), failed);
+        if (mine < steps) runs[(step + mine) % kAhead * 8 + (lane & 7)] = run;
         __syncwarp();
-        if (lane == 0) mbar_arrive(pages_bar(step));
+        if (lane < steps) mbar_arrive(pages_bar(step + lane));
       }
     }
     step0 += tb - ta;
