@@ -161,6 +161,13 @@ __device__ __forceinline__ bool soft_or(bool v) {
   return r != 0;
 }
 
+// sixteen streamed bytes where `ok`, else zeros (without a branch, or a copy that would wait)
+__device__ __forceinline__ void ld_stream_or_zero(uint4& v, const uint8_t* p, bool ok) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.u32 p, %5, 0;\nmov.b32 %0, 0;\nmov.b32 %1, 0;\nmov.b32 %2, 0;\n"
+      "mov.b32 %3, 0;\n@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"((uint32_t)ok));
+}
 // the queries are in place: the softmax warps to the one that issues the products
 __device__ __forceinline__ void queries_in() {
   asm volatile("barrier.cta.sync 2, %0;" ::"n"(32 * (kSoftWarps + 1)) : "memory");
@@ -290,11 +297,10 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       const uint8_t* const vp = a.v_codes + 8 * g * D + 16 * x;
       uint4 kb[2][KC], vb[VC][2];
       auto load_k = [&](int64_t from, int j, int h) {
-        kb[j][h] = from >= 0 ? ld_stream(kp + from + 8 * D * j + 64 * h) : make_uint4(0u, 0u, 0u, 0u);
+        ld_stream_or_zero(kb[j][h], kp + from + 8 * D * j + 64 * h, from >= 0);
       };
       auto load_v = [&](int64_t from, int i, int t) {
-        vb[i][t] =
-            from >= 0 ? ld_stream(vp + from + 256 * i + 4 * D * t) : make_uint4(0u, 0u, 0u, 0u);
+        ld_stream_or_zero(vb[i][t], vp + from + 256 * i + 4 * D * t, from >= 0);
       };
       auto from_of = [&](uint32_t step) {  // (once its pages are in)
         return *reinterpret_cast<volatile int64_t*>(&runs[step % kAhead * 8 + warp].from);
