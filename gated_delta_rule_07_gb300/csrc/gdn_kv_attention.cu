@@ -468,9 +468,9 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 int64_t average_rows(const KvArgs& a) { return (a.T + a.N - 1) / a.N * a.group; }
 
 // More than sixteen rows: the tcgen05 kernel, where it is built.  int8, 4 kv heads of 128: 24
-// sequences of 20000 keys with 8 .. 40 rows take 131 us there and 203 here, with 8 .. 64 rows 154 and
-// 273, but with 8 or 16 rows 117 and 107; 16 x 20000 keys with 16 rows 78 and 69; one sequence of
-// 1500 keys with 16 rows 12.6 and 8.8; 64 x 65536 with 8 rows 912 and 579.
+// sequences of 20000 keys with 8 .. 40 rows take 123 us there and 158 here, with 8 .. 64 rows 152 and
+// 248, but with 8 or 16 rows 109 and 107; 16 x 20000 keys with 16 rows 74 and 69; one sequence of
+// 1500 keys with 16 rows 12.6 and 8.9.
 bool use_tc(const KvArgs& a) { return a.bf16 && a.D <= 128 && average_rows(a) > 16; }
 
 // Tiles of 8 rows a warp carries: as many as the average sequence's rows fill (a row tile more
