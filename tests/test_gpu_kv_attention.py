@@ -104,6 +104,16 @@ def test_several_queries_and_windows(gdn, hq, hkv, D, page, window, fmt, io):
     check(*p.run(window), p.ref(window), io)
 
 
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("group,D", [(4, 128), (5, 64), (4, 256)])
+def test_some_sequences_with_many_rows(gdn, group, D, fmt):
+    """Few rows on average (so the few-rows kernel), many in some sequences: several row tiles."""
+    new = [1, 9, 1, 1, 2, 17, 1, 1, 1]
+    lens = [700, 33, 1, 0, 64, 2000, 128, 16, 15]
+    p = Problem(gdn, lens, new, 2 * group, 2, D, 32, fmt, torch.bfloat16, seed=group + D)
+    check(*p.run(), p.ref(), torch.bfloat16)
+
+
 @pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
 def test_long_sequences_are_split_and_joined(gdn, io):
     """One long sequence among short ones: work split over its length and joined."""

@@ -75,6 +75,33 @@ def test_append_matches_plain_form(gdn, hkv, D, page, fmt, io):
     pool.check(tables, lens)
 
 
+@pytest.mark.parametrize("hkv", [22, 41])
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+def test_many_heads_and_pages(gdn, hkv, fmt):
+    """Enough pages and heads that a CTA takes several heads of a page (22: two for the append; 41:
+    four, and two for the read back), the last of them fewer; one value in some heads is not
+    finite."""
+    gen = torch.Generator().manual_seed(hkv)
+    page, D = 16, 64
+    ctx, new = [3, 0, 40], [700, 1, 1400]
+    lens = [a + b for a, b in zip(ctx, new)]
+    tables, pages = at.block_tables(lens, page, gen)
+    pool = Pool(gdn, pages, hkv, page, D, fmt, gen)
+    k, v = draws(gen, sum(new), hkv, D, torch.bfloat16)
+    k[100, 1, 5], k[1500, hkv - 1, 63], v[700, 2, 0] = float("inf"), float("nan"), -float("inf")
+    pool.append(gdn, k, v, tables, ctx, new)
+    pool.check(tables, lens)
+    got = gdn.kv_read(pool.cache, tables.cuda(), None, at.cumulative(lens).cuda(), sum(lens),
+                      torch.float32)
+    for out, codes, scales in zip(got, (pool.kc, pool.vc), (pool.ks, pool.vs)):
+        values = at.values(codes).float()
+        for n, first in enumerate(at.cumulative(lens)[:-1].tolist()):
+            pos = torch.arange(lens[n])
+            pid = tables[n].long()[pos // page]
+            want = values[pid, :, pos % page] * scales[pid][:, :, None]
+            assert torch.equal(out[first:first + lens[n]].cpu(), want)
+
+
 @pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
 def test_token_by_token(gdn, fmt):
     """Seventy single tokens of growing size for each of five sequences, without cu_seqlens: pages
