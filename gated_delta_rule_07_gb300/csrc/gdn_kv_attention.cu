@@ -36,8 +36,8 @@
 // heads of 128, 8 rows: int8 579 us (95%), e4m3 553 us (the conversion is one instruction; opened
 // by shifts it was 726); 16 x 32768 keys 79 us (84%); fp32 I/O, 16 x 30000 keys, 84 us (71%: twice
 // the products); 16 x 30000 keys, heads of 256, 8 rows 71 us (83%), 16 rows 53 us for half the bytes
-// (56%: registers leave two CTAs an SM); heads of 64 in pages of 16, 102 us (58%: a warp's tile of
-// 16 keys is 2 KB, so the softmax's instructions weigh twice as much a byte).  One sequence of 1500 keys takes 9.3 us and 32
+// (56%: registers leave two CTAs an SM); heads of 64 in pages of 16, 16 x 60000 keys, 93 us (64%: a
+// warp's tile of 16 keys is 2 KB, so the softmax's instructions weigh twice as much a byte).  One sequence of 1500 keys takes 9.3 us and 32
 // ragged ones of up to 8192 18.7 us: launch, plan, an item's start and end, and the join are about
 // 9 us of either.  A deeper ring of tiles in shared memory was slower (64 x 65536: 825 us, at any
 // depth): its copies take more issue than the loads here.
@@ -80,8 +80,12 @@ template <int D, int NT, bool SPLIT> struct Shape {
   static constexpr int pad = D + 4;  // floats of a row of partial sums (conflict-free)
   static constexpr int o_bytes = kWarps * rows * pad * 4;
   static constexpr int smem = q_bytes > o_bytes ? q_bytes : o_bytes;
-  // registers decide the resident CTAs: the sums alone are D NT / 4 of them
-  static constexpr int ctas = D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;
+  // Registers decide the resident CTAs: the sums alone are D NT / 4 of them.  Heads of 64 have small
+  // tiles and need more warps for as many bytes on their way: 16 x 60000 keys, bf16, 92.8 us with
+  // six CTAs an SM (75 registers), 99.1 with five, 102.7 with four; fp32 (with spills at six), 16 x
+  // 30000: 58.5, 57.6, 59.9.  Heads of 128 spill with five: 64 x 65536 keys 759 us, 583 with four.
+  static constexpr int ctas =
+      D * NT <= 64 ? (SPLIT ? 5 : 6) : D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;
 };
 
 template <typename IO, int D, int NT, bool E4M3>

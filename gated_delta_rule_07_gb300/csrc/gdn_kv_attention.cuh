@@ -15,7 +15,7 @@ namespace gdn {
 namespace {
 
 constexpr int kAttWarps = 4, kAttThreads = 32 * kAttWarps;
-constexpr int kMaxCtas = 608;  // CTAs at most, four an SM (the workspace holds two parts of each)
+constexpr int kMaxCtas = 912;  // CTAs at most, six an SM (the workspace holds two parts of each)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // The reference M of a row's weights 2^(y - M) stands kHead below the largest score where it was
 // last moved, and moves when a score exceeds it by kSlack (log2): weights stay within fp16's range,
