@@ -48,8 +48,8 @@ namespace {
 
 constexpr int kWarps = kAttWarps, kThreads = kAttThreads;
 constexpr int kTile = 16;      // keys of a unit
-// Units of a CTA at least: one sequence of 1500 keys takes 9.4 us with 8, 11.4 with 16, 15.7 with 32;
-// with 4 one of 8000 keys takes 24.7 us against 11.8 (too many parts to join).
+// Units of a CTA at least: one sequence of 1500 keys takes 9.3 us with 8, 11.4 with 16, 15.7 with 32;
+// with 4 it takes 8.5, but one of 8000 keys 14.1 us against 11.7 (more parts to join).
 constexpr int kMinUnits = 8;
 // Units that starting an item is worth (queries, joining warps): 32 ragged sequences of up to 8192
 // keys take 18.7 us with 8, 19.7 with 16, 41.3 with 1.
