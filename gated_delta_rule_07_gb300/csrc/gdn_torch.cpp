@@ -125,11 +125,8 @@ class Args {
   int32_t* status(int i) const {
     return static_cast<int32_t*>(const_cast<void*>(packed_or_null(i, "dev_status", at::kInt, {1})));
   }
-  // the stream: a handle, or None for torch's current one
-  cudaStream_t stream(int i) const {
-    if (v_[i] == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-    return static_cast<cudaStream_t>(PyLong_AsVoidPtr(v_[i]));
-  }
+  // torch's current stream (gdn.py makes the stream that a user names the current one)
+  static cudaStream_t stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
   std::string at(const char* what) const { return std::string(name_) + ": " + what; }
 
  private:
@@ -187,18 +184,18 @@ Rope rope_of(const Args& a, int e) {
               f32(a.packed_or_null(5, "k_weight", at::kFloat, {D}))};
 }
 
-// q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, style, status, stream
+// q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, style, status
 PyObject* qk_norm_rope(const Args& a) {
   const Rope r = rope_of(a, 6);
   at::Tensor q_out = empty(r.q.sizes(), r.q, r.q.scalar_type());
   at::Tensor k_out = empty(r.k.sizes(), r.k, r.q.scalar_type());
   check(gdn_qk_norm_rope(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.pos, r.table, r.qw, r.kw,
-                         q_out.data_ptr(), k_out.data_ptr(), a.status(9), a.stream(10)),
+                         q_out.data_ptr(), k_out.data_ptr(), a.status(9), a.stream()),
         "qk_norm_rope");
   return tuple_of({q_out, k_out});
 }
 
-// .., dq_out, dk_out, eps, weight_offset, style, workspace, status, stream
+// .., dq_out, dk_out, eps, weight_offset, style, workspace, status
 PyObject* qk_norm_rope_backward(const Args& a) {
   const Rope r = rope_of(a, 8);
   const at::ScalarType dtype = r.q.scalar_type();
@@ -212,7 +209,7 @@ PyObject* qk_norm_rope_backward(const Args& a) {
   check(gdn_qk_norm_rope_backward(&r.p, r.q.data_ptr(), r.k.data_ptr(), r.pos, r.table, r.qw, r.kw,
                                   dqo.data_ptr(), dko.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                   dqw.data_ptr<float>(), dkw.data_ptr<float>(), ws.data_ptr(),
-                                  ws.nbytes(), a.status(12), a.stream(13)),
+                                  ws.nbytes(), a.status(12), a.stream()),
         "qk_norm_rope_backward");
   return tuple_of({dq, dk, dqw, dkw});
 }
@@ -238,7 +235,7 @@ void heads_of(const Args& a, const at::Tensor& t, const char* what, const gdn_kv
            std::to_string(c->head_dim) + ": " + shown(t));
 }
 
-// cache, k, v, block_table, ctx_lens, cu_seqlens, status, stream
+// cache, k, v, block_table, ctx_lens, cu_seqlens, status
 PyObject* kv_append(const Args& a) {
   const gdn_kv_cache* c = a.cache(0);
   gdn_kv_problem p = {};
@@ -255,12 +252,12 @@ PyObject* kv_append(const Args& a) {
   p.v_token_stride = v.stride(0);
   p.v_head_stride = v.stride(1);
   check(gdn_kv_append(c, &p, k.data_ptr(), v.data_ptr(), i32(t.table.data_ptr()), t.lens, t.cu,
-                      a.status(6), a.stream(7)),
+                      a.status(6), a.stream()),
         "kv_append");
   Py_RETURN_NONE;
 }
 
-// cache, block_table, start, cu_seqlens, tokens, io dtype, status, stream
+// cache, block_table, start, cu_seqlens, tokens, io dtype, status
 PyObject* kv_read(const Args& a) {
   const gdn_kv_cache* c = a.cache(0);
   gdn_kv_problem p = {};
@@ -272,12 +269,12 @@ PyObject* kv_read(const Args& a) {
   const std::vector<int64_t> shape = {T, c->hkv, c->head_dim};
   at::Tensor k = empty(shape, t.table, dtype), v = empty(shape, t.table, dtype);
   check(gdn_kv_read(c, &p, i32(t.table.data_ptr()), t.lens, t.cu, k.data_ptr(), v.data_ptr(),
-                    a.status(6), a.stream(7)),
+                    a.status(6), a.stream()),
         "kv_read");
   return tuple_of({k, v});
 }
 
-// cache, q, block_table, kv_lens, cu_seqlens, scale (or None), window, workspace, status, stream
+// cache, q, block_table, kv_lens, cu_seqlens, scale (or None), window, workspace, status
 PyObject* kv_attention(const Args& a) {
   const gdn_kv_cache* c = a.cache(0);
   gdn_kv_problem p = {};
@@ -300,7 +297,7 @@ PyObject* kv_attention(const Args& a) {
       : a.workspace(7);
   check(gdn_kv_attention(c, &p, q.data_ptr(), i32(t.table.data_ptr()), t.lens, t.cu, scale,
                          (int32_t)window, out.data_ptr(), lse.data_ptr<float>(), ws.data_ptr(),
-                         ws.nbytes(), a.status(8), a.stream(9)),
+                         ws.nbytes(), a.status(8), a.stream()),
         "kv_attention");
   return tuple_of({out, lse});
 }
@@ -339,11 +336,11 @@ template <PyObject* (*F)(const Args&), int N> PyMethodDef method(const char* nam
           METH_FASTCALL, nullptr};
 }
 PyMethodDef methods[] = {
-    method<qk_norm_rope, 11>("qk_norm_rope"),
-    method<qk_norm_rope_backward, 14>("qk_norm_rope_backward"),
-    method<kv_append, 8>("kv_append"),
-    method<kv_read, 8>("kv_read"),
-    method<kv_attention, 10>("kv_attention"),
+    method<qk_norm_rope, 10>("qk_norm_rope"),
+    method<qk_norm_rope_backward, 13>("qk_norm_rope_backward"),
+    method<kv_append, 7>("kv_append"),
+    method<kv_read, 7>("kv_read"),
+    method<kv_attention, 9>("kv_attention"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

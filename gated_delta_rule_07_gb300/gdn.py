@@ -419,26 +419,41 @@ def _refuse(where, why, status=1):
     raise GdnError(status, f"{where}: {why}")
 
 
-def _hold(stream, *tensors):
-    """Outputs and temporaries allocated on the current stream and used on `stream`: their memory
-    is not handed out again before the work on `stream` is done."""
+def _side_stream(stream):
+    """A torch stream for what a call was given: one of torch's, or an integer handle."""
     if hasattr(stream, "cuda_stream"):
-        for t in tensors:
-            t.record_stream(stream)
+        return stream
+    # (0 and 1 are CUDA's names of the legacy default stream)
+    return torch.cuda.default_stream() if int(stream) in (0, 1) else torch.cuda.ExternalStream(
+        int(stream))
 
 
-def _handle(stream):
-    return stream if stream is None else _stream(stream)
+def _on(stream, call, *inputs):
+    """call() with `stream` as torch's current one, so that everything it allocates, clears and
+    launches is ordered on it.  The allocator learns that the inputs are used there and that the
+    outputs will be used on the caller's stream: no memory is handed out again before the work that
+    uses it is done.  Ordering the streams themselves (inputs written, outputs read) is the caller's."""
+    side = _side_stream(stream)
+    with torch.cuda.stream(side):
+        result = call()
+    here = torch.cuda.current_stream(side.device)
+    if here != side:
+        for t in inputs:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(side)
+        for t in result if isinstance(result, tuple) else (result,):
+            if t is not None:
+                t.record_stream(here)
+    return result
 
 
-def _checked(check_status, device, stream, where, call):
+def _checked(check_status, device, where, call):
     """call(status word or None), with the word read back afterwards where asked for."""
     if not check_status:
         return call(None)
     st = torch.zeros(1, dtype=torch.int32, device=device)
-    _hold(stream, st)
     result = call(st)
-    _check(gdn_device_status(st, True, stream), f"{where} (device status)")
+    _check(gdn_device_status(st), f"{where} (device status)")
     return result
 
 
@@ -453,17 +468,18 @@ def qk_norm_rope(q, k, positions, cos_sin, q_weight=None, k_weight=None, eps=1e-
                  weight_offset=0.0, style="half", check_status=False, stream=None):
     """Queries [T, hq, D] and keys [T, hkv, D], normalised per head and rotated by position (see
     include/gdn.h); q and k may be slices of one projection.  Returns contiguous tensors."""
+    if stream is not None:
+        return _on(stream, lambda: qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps,
+                                                weight_offset, style, check_status),
+                   q, k, positions, cos_sin, q_weight, k_weight)
     code = _ROPE_STYLES.get(style)
     if code is None:
         _refuse("qk_norm_rope", f"style {style!r}")
-    if stream is None and not check_status:
+    if not check_status:
         return _native.qk_norm_rope(q, k, positions, cos_sin, q_weight, k_weight, eps,
-                                    weight_offset, code, None, None)
-    out = _checked(check_status, q.device, stream, "qk_norm_rope", lambda st: _native.qk_norm_rope(
-        q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, code, st,
-        _handle(stream)))
-    _hold(stream, *out)
-    return out
+                                    weight_offset, code, None)
+    return _checked(True, q.device, "qk_norm_rope", lambda st: _native.qk_norm_rope(
+        q, k, positions, cos_sin, q_weight, k_weight, eps, weight_offset, code, st))
 
 
 def gdn_qk_norm_rope_backward_workspace_size(p) -> int:
@@ -487,26 +503,20 @@ def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, 
     """Gradients (dq, dk, dq_weight, dk_weight) of <dq_out, q_out> + <dk_out, k_out> through
     qk_norm_rope on the same inputs."""
     where = "qk_norm_rope_backward"
+    if stream is not None:
+        return _on(stream, lambda: qk_norm_rope_backward(
+            q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out, eps, weight_offset, style,
+            workspace, check_status), q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
+            workspace)
     code = _ROPE_STYLES.get(style)
     if code is None:
         _refuse(where, f"style {style!r}")
-    if stream is None and not check_status:
+    if not check_status:
         return _native.qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out,
-                                             dk_out, eps, weight_offset, code, workspace, None,
-                                             None)
-    if workspace is None and stream is not None:
-        (T, hq, D), (rows, R) = q.shape, cos_sin.shape
-        p = QkRopeProblem(T, hq, k.shape[1], D, R, code, _IO.get(q.dtype, -1), rows, eps,
-                          weight_offset, *q.stride()[:2], *k.stride()[:2])
-        workspace = torch.empty(gdn_qk_norm_rope_backward_workspace_size(p), dtype=torch.uint8,
-                                device=q.device)
-        _hold(stream, workspace)
-    grads = _checked(check_status, q.device, stream, where, lambda st: (
-        _native.qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out,
-                                      eps, weight_offset, code, workspace, st, _handle(stream))))
-    if stream is not None:
-        _hold(stream, *grads)
-    return grads
+                                             dk_out, eps, weight_offset, code, workspace, None)
+    return _checked(True, q.device, where, lambda st: _native.qk_norm_rope_backward(
+        q, k, positions, cos_sin, q_weight, k_weight, dq_out, dk_out, eps, weight_offset, code,
+        workspace, st))
 
 
 class KVCache:
@@ -533,6 +543,10 @@ class KVCache:
                                 v_scale.data_ptr(), pages, page, hkv, D, fmt)
         self._address = ctypes.addressof(self.desc)
 
+    @property
+    def buffers(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
     @classmethod
     def empty(cls, pages, hkv, page, D, dtype=torch.int8, device="cuda"):
         """A cache of `pages` pages; nothing in it is initialised, or needs to be."""
@@ -554,11 +568,15 @@ def kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens=None, check_status=
     """Quantises new keys and values [T, hkv, D] into the cache's pages, behind the ctx_lens[n]
     tokens that each sequence already holds.  Without cu_seqlens the rows are one sequence's, or
     one row each of T sequences."""
-    if stream is None and not check_status:
-        _native.kv_append(cache._address, k, v, block_table, ctx_lens, cu_seqlens, None, None)
+    if stream is not None:
+        return _on(stream, lambda: kv_append(cache, k, v, block_table, ctx_lens, cu_seqlens,
+                                             check_status),
+                   k, v, block_table, ctx_lens, cu_seqlens, *cache.buffers)
+    if not check_status:
+        _native.kv_append(cache._address, k, v, block_table, ctx_lens, cu_seqlens, None)
         return
-    _checked(check_status, k.device, stream, "kv_append", lambda st: _native.kv_append(
-        cache._address, k, v, block_table, ctx_lens, cu_seqlens, st, _handle(stream)))
+    _checked(True, k.device, "kv_append", lambda st: _native.kv_append(
+        cache._address, k, v, block_table, ctx_lens, cu_seqlens, st))
 
 
 def gdn_kv_read(cache, p, block_table, start, cu_seqlens, k_out, v_out, dev_status=None,
@@ -572,17 +590,17 @@ def kv_read(cache, block_table, start, cu_seqlens, tokens, dtype=torch.bfloat16,
             check_status=False, stream=None):
     """Keys and values [tokens, hkv, D] of the positions start[n] onward (None: from 0) of each
     sequence, cu_seqlens[n + 1] - cu_seqlens[n] of them, read back from the cache."""
+    if stream is not None:
+        return _on(stream, lambda: kv_read(cache, block_table, start, cu_seqlens, tokens, dtype,
+                                           check_status),
+                   block_table, start, cu_seqlens, *cache.buffers)
     io = _IO.get(dtype)
     if io is None:
         _refuse("kv_read", f"dtype {dtype}", 2)
-    if stream is None and not check_status:
-        return _native.kv_read(cache._address, block_table, start, cu_seqlens, tokens, io, None,
-                               None)
-    out = _checked(check_status, block_table.device, stream, "kv_read", lambda st: _native.kv_read(
-        cache._address, block_table, start, cu_seqlens, tokens, io, st, _handle(stream)))
-    if stream is not None:
-        _hold(stream, *out)
-    return out
+    if not check_status:
+        return _native.kv_read(cache._address, block_table, start, cu_seqlens, tokens, io, None)
+    return _checked(True, block_table.device, "kv_read", lambda st: _native.kv_read(
+        cache._address, block_table, start, cu_seqlens, tokens, io, st))
 
 
 def gdn_kv_attention_workspace_size(cache, p) -> int:
@@ -612,17 +630,15 @@ def kv_attention(cache, q, block_table, kv_lens, cu_seqlens=None, scale=None, wi
     """out [T, hq, D] and lse [T, hq] of the queries of each sequence's last tokens over the
     cache's kv_lens[n] tokens (which include them); scale defaults to 1 / sqrt(D).  Without
     cu_seqlens the rows are one sequence's, or one row each of T sequences."""
-    if stream is None and not check_status:
+    if stream is not None:
+        return _on(stream, lambda: kv_attention(cache, q, block_table, kv_lens, cu_seqlens, scale,
+                                                window, workspace, check_status),
+                   q, block_table, kv_lens, cu_seqlens, workspace, *cache.buffers)
+    if not check_status:
         return _native.kv_attention(cache._address, q, block_table, kv_lens, cu_seqlens, scale,
-                                    window, workspace, None, None)
-    if workspace is None:
-        workspace = kv_attention_workspace(cache, q, block_table)
-        _hold(stream, workspace)
-    out = _checked(check_status, q.device, stream, "kv_attention", lambda st: _native.kv_attention(
-        cache._address, q, block_table, kv_lens, cu_seqlens, scale, window, workspace, st,
-        _handle(stream)))
-    _hold(stream, *out)
-    return out
+                                    window, workspace, None)
+    return _checked(True, q.device, "kv_attention", lambda st: _native.kv_attention(
+        cache._address, q, block_table, kv_lens, cu_seqlens, scale, window, workspace, st))
 
 
 # ------------------------------------------------------------------ convenience API
