@@ -618,6 +618,10 @@ def gdn_kv_attention(cache, p, q, block_table, kv_lens, cu_seqlens, scale, windo
 
 def kv_attention_workspace(cache, q, block_table):
     """A workspace for kv_attention calls of these shapes."""
+    if q.dim() != 3 or block_table.dim() != 2:
+        _refuse("kv_attention_workspace", "q is to be [tokens, heads, D], block_table [N, pages]")
+    if q.dtype not in _IO:
+        _refuse("kv_attention_workspace", f"dtype {q.dtype}", 2)
     T, hq, _ = q.shape
     p = KvProblem(T, block_table.shape[0], block_table.shape[1], hq, _IO[q.dtype], 0, 0, 0, 0,
                   q.stride(0), q.stride(1))

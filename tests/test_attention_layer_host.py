@@ -187,3 +187,16 @@ def test_values_layout_roundtrip():
     assert v.shape == (3, 2, 8, 64, 4) and v.is_contiguous()
     assert int(v[1, 1, 5, 7, 2]) == int(codes[1, 1, 5 * 4 + 2, 7])
     assert torch.equal(at.unpacked_v(v), codes)
+
+
+def test_workspace_for_refuses(gdn):
+    """kv_attention_workspace refuses as the call itself does."""
+    class Cache:
+        desc = cache_desc(gdn)
+    table = torch.zeros(2, 2, dtype=torch.int32)
+    for q, t, status in ((torch.zeros(8, 4, 128, dtype=torch.float16), table, 2),
+                         (torch.zeros(8, 512, dtype=torch.bfloat16), table, 1),
+                         (torch.zeros(8, 4, 128, dtype=torch.bfloat16), table[0], 1)):
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.kv_attention_workspace(Cache, q, t)
+        assert e.value.status == status
