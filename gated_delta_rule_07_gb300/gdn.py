@@ -190,6 +190,34 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _side_stream(stream):
+    """A torch stream for what a call was given: one of torch's, or an integer handle."""
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    # (0 and 1 are CUDA's names of the legacy default stream)
+    return torch.cuda.default_stream() if int(stream) in (0, 1) else torch.cuda.ExternalStream(
+        int(stream))
+
+
+def _on(stream, call, *inputs):
+    """call() with `stream` as torch's current one, so that everything it allocates, clears and
+    launches is ordered on it.  The allocator learns that the inputs are used there and that the
+    outputs will be used on the caller's stream: no memory is handed out again before the work that
+    uses it is done.  Ordering the streams themselves (inputs written, outputs read) is the caller's."""
+    side = _side_stream(stream)
+    with torch.cuda.stream(side):
+        result = call()
+    here = torch.cuda.current_stream(side.device)
+    if here != side:
+        for t in inputs:
+            if isinstance(t, torch.Tensor):
+                t.record_stream(side)
+        for t in result if isinstance(result, tuple) else (result,):
+            if t is not None:
+                t.record_stream(here)
+    return result
+
+
 def _check(status, where):
     if status != GDN_OK:
         raise GdnError(status, where)
@@ -316,6 +344,10 @@ def backward(q, k, v, g, beta, dout, h0=None, dh_final=None, cu_seqlens=None, wo
              check_status=False, stream=None):
     """Gradients (dq, dk, dv, dg, dbeta, dh0) of <dout, out> + <dh_final, h_final> through the
     forward on the same inputs; allocates the outputs (and the workspace unless given)."""
+    if stream is not None:
+        return _on(stream, lambda: backward(q, k, v, g, beta, dout, h0, dh_final, cu_seqlens,
+                                            workspace, check_status),
+                   q, k, v, g, beta, dout, h0, dh_final, cu_seqlens, workspace)
     p = problem_for(q, v, cu_seqlens)
     N = p.num_seqs
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -325,9 +357,9 @@ def backward(q, k, v, g, beta, dout, h0=None, dh_final=None, cu_seqlens=None, wo
         workspace = torch.empty(max(gdn_backward_workspace_size(p), 256), dtype=torch.uint8,
                                 device=q.device)
     gdn_backward(p, q, k, v, g, beta, h0, cu_seqlens, dout, dh_final, dq, dk, dv, dg, dbeta,
-                 dh0, workspace, stream=stream)
+                 dh0, workspace)
     if check_status:
-        _check(gdn_device_status(workspace, True, stream), "gdn_backward (device status)")
+        _check(gdn_device_status(workspace), "gdn_backward (device status)")
     return dq, dk, dv, dg, dbeta, dh0
 
 
@@ -342,6 +374,10 @@ def gdn_prologue(p, x, conv_w, conv_state_in, a, b, A_log, dt_bias, cu_seqlens, 
 def prologue(x, conv_w, a, b, A_log, dt_bias, hk, hv, K, V, conv_state=None, cu_seqlens=None,
              activation="none", check_status=False, stream=None):
     """q, k, v, g, beta, new conv state from the projections (layouts of include/gdn.h)."""
+    if stream is not None:
+        return _on(stream, lambda: prologue(x, conv_w, a, b, A_log, dt_bias, hk, hv, K, V,
+                                            conv_state, cu_seqlens, activation, check_status),
+                   x, conv_w, a, b, A_log, dt_bias, conv_state, cu_seqlens)
     T = x.shape[0]
     N = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
     W = conv_w.shape[1]
@@ -356,9 +392,9 @@ def prologue(x, conv_w, a, b, A_log, dt_bias, hk, hv, K, V, conv_state=None, cu_
     new_state = torch.empty(N, x.shape[1], max(W - 1, 0), dtype=x.dtype, device=dev)
     st = torch.zeros(1, dtype=torch.int32, device=dev) if check_status else None
     gdn_prologue(p, x, conv_w, conv_state, a, b, A_log, dt_bias, cu_seqlens, q, k, v, g, beta,
-                 new_state if W > 1 else None, st, stream)
+                 new_state if W > 1 else None, st)
     if check_status:
-        _check(gdn_device_status(st, True, stream), "gdn_prologue (device status)")
+        _check(gdn_device_status(st), "gdn_prologue (device status)")
     return q, k, v, g, beta, new_state
 
 
@@ -387,13 +423,16 @@ def gdn_decode_step(p, q, k, v, g, beta, slot, state, out, dev_status=None, stre
 def decode(q, k, v, g, beta, slot, state, out=None, check_status=False, stream=None):
     """One decode step: row b continues the request held in state[slot[b]] (updated in place).
     Returns out [B, hv, V]; with check_status, waits and raises on a device-side error."""
+    if stream is not None:
+        return _on(stream, lambda: decode(q, k, v, g, beta, slot, state, out, check_status),
+                   q, k, v, g, beta, slot, state, out)
     p = decode_problem_for(q, v, state)
     if out is None:
         out = torch.empty_like(v)
     st = torch.zeros(1, dtype=torch.int32, device=q.device) if check_status else None
-    gdn_decode_step(p, q, k, v, g, beta, slot, state, out, st, stream)
+    gdn_decode_step(p, q, k, v, g, beta, slot, state, out, st)
     if check_status:
-        _check(gdn_device_status(st, reset=True, stream=stream), "gdn_decode_step (device status)")
+        _check(gdn_device_status(st), "gdn_decode_step (device status)")
     return out
 
 
@@ -417,34 +456,6 @@ _ROPE_STYLES = {"half": 0, "pairs": 1}
 
 def _refuse(where, why, status=1):
     raise GdnError(status, f"{where}: {why}")
-
-
-def _side_stream(stream):
-    """A torch stream for what a call was given: one of torch's, or an integer handle."""
-    if hasattr(stream, "cuda_stream"):
-        return stream
-    # (0 and 1 are CUDA's names of the legacy default stream)
-    return torch.cuda.default_stream() if int(stream) in (0, 1) else torch.cuda.ExternalStream(
-        int(stream))
-
-
-def _on(stream, call, *inputs):
-    """call() with `stream` as torch's current one, so that everything it allocates, clears and
-    launches is ordered on it.  The allocator learns that the inputs are used there and that the
-    outputs will be used on the caller's stream: no memory is handed out again before the work that
-    uses it is done.  Ordering the streams themselves (inputs written, outputs read) is the caller's."""
-    side = _side_stream(stream)
-    with torch.cuda.stream(side):
-        result = call()
-    here = torch.cuda.current_stream(side.device)
-    if here != side:
-        for t in inputs:
-            if isinstance(t, torch.Tensor):
-                t.record_stream(side)
-        for t in result if isinstance(result, tuple) else (result,):
-            if t is not None:
-                t.record_stream(here)
-    return result
 
 
 def _checked(check_status, device, where, call):
@@ -657,6 +668,10 @@ def forward(q, k, v, g, beta, h0=None, cu_seqlens=None, P=1, out=None,
 
     ``cu_seqlens`` is an int32 CUDA tensor [N+1] or None (one sequence).  With
     ``check_status`` the device status word is read back (a synchronisation)."""
+    if stream is not None:
+        return _on(stream, lambda: forward(q, k, v, g, beta, h0, cu_seqlens, P, out, h_final,
+                                           workspace, want_final, check_status),
+                   q, k, v, g, beta, h0, cu_seqlens, out, h_final, workspace)
     p = problem_for(q, v, cu_seqlens, P)
     N = p.num_seqs
     if out is None:
@@ -665,8 +680,8 @@ def forward(q, k, v, g, beta, h0=None, cu_seqlens=None, P=1, out=None,
         h_final = torch.empty(N, p.hv, p.k_dim, p.v_dim, dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = workspace_for(p, q.device)
-    gdn_forward(p, q, k, v, g, beta, h0, cu_seqlens, out, h_final, workspace, stream=stream)
+    gdn_forward(p, q, k, v, g, beta, h0, cu_seqlens, out, h_final, workspace)
     if check_status:
-        st = gdn_device_status(workspace, True, stream)
+        st = gdn_device_status(workspace)
         _check(st, "gdn_forward (device status)")
     return out, h_final

@@ -70,7 +70,59 @@ class Layer:
             self.cache.k, self.cache.v, self.cache.k_scale, self.cache.v_scale)]
 
 
+class Recurrent:
+    """The same for the recurrent layers' calls."""
+
+    def __init__(self, gdn, seed=0):
+        gen = torch.Generator().manual_seed(seed)
+        T, hk, hv, D, N = 200, 2, 4, 128, 3
+        rand = lambda *n: torch.randn(*n, generator=gen).bfloat16().cuda()  # noqa: E731
+        self.gdn, self.heads = gdn, (hk, hv, D, D)
+        self.q, self.v, self.do = rand(T, hk, D) / 11, rand(T, hv, D), rand(T, hv, D)
+        self.k = rand(T, hk, D)
+        self.k = (self.k.float() / self.k.float().norm(dim=-1, keepdim=True)).bfloat16()
+        self.g = -torch.rand(T, hv, generator=gen).cuda()
+        self.beta = torch.rand(T, hv, generator=gen).cuda()
+        self.cu = at.cumulative([70, 1, 129]).cuda()
+        self.x = rand(T, 2 * hk * D + hv * D)
+        self.conv, self.ab = torch.randn(self.x.shape[1], 4, generator=gen).cuda(), rand(T, hv)
+        self.log, self.bias = torch.zeros(hv).cuda(), torch.zeros(hv).cuda()
+        self.h0 = torch.randn(N, hv, D, D, generator=gen).cuda()
+        self.slot = torch.tensor([2, -1, 0], dtype=torch.int32).cuda()
+        self.fresh()
+        torch.cuda.synchronize()
+
+    def fresh(self):
+        self.state = self.h0.clone()
+
+    def calls(self):
+        g = self.gdn
+        rows = self.q[:3], self.k[:3], self.v[:3], self.g[:3], self.beta[:3]
+        return {
+            "forward": lambda q=None, **kw: g.forward(
+                self.q if q is None else q, self.k, self.v, self.g, self.beta, self.h0, self.cu,
+                P=2, **kw),
+            "backward": lambda q=None, **kw: g.backward(
+                self.q if q is None else q, self.k, self.v, self.g, self.beta, self.do,
+                cu_seqlens=self.cu, **kw),
+            "prologue": lambda q=None, **kw: g.prologue(
+                self.x, self.conv, self.ab, self.ab, self.log, self.bias, *self.heads, None,
+                self.cu, **kw),
+            "decode": lambda q=None, **kw: (g.decode(
+                rows[0] if q is None else q[:3], *rows[1:], self.slot, self.state, **kw),
+                self.state),
+        }
+
+    def results(self, out):
+        return [t.clone() for t in out]
+
+
 NAMES = ["qk_norm_rope", "qk_norm_rope_backward", "kv_append", "kv_read", "kv_attention"]
+MORE = ["forward", "backward", "prologue", "decode"]
+
+
+def layer_of(gdn, name):
+    return Recurrent(gdn) if name in MORE else Layer(gdn)
 
 
 def same(got, want):
@@ -87,10 +139,10 @@ def small_junk():
     del held
 
 
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", NAMES + MORE)
 def test_status_word_with_work_pending(gdn, name):
     """The status word is cleared on the call's stream, not behind the current one's work."""
-    layer = Layer(gdn)
+    layer = layer_of(gdn, name)
     want = layer.results(layer.calls()[name]())
     torch.cuda.synchronize()
     layer.fresh()
@@ -101,7 +153,7 @@ def test_status_word_with_work_pending(gdn, name):
         torch.cuda._sleep(SPIN)
         out = layer.calls()[name](check_status=True, stream=stream)
         torch.cuda.synchronize()
-        if name != "kv_append" or stream is s:  # (a second append re-rounds what the first wrote)
+        if name not in ("kv_append", "decode") or stream is s:  # (those change what they read)
             same(layer.results(out), want)
 
 
@@ -120,11 +172,12 @@ def test_recorded_error_is_not_wiped(gdn):
         torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("name", [n for n in NAMES if n != "kv_append"])
+@pytest.mark.parametrize("name", [n for n in NAMES + MORE if n != "kv_append"])
 def test_outputs_do_not_take_memory_in_use(gdn, name):
     """Memory that the current stream will still write, freed before the call, is not its output."""
-    layer = Layer(gdn)
+    layer = layer_of(gdn, name)
     want = layer.results(layer.calls()[name]())
+    layer.fresh()
     s = torch.cuda.Stream()
     torch.cuda.synchronize()
     torch.cuda._sleep(SPIN)
@@ -138,11 +191,11 @@ def test_outputs_do_not_take_memory_in_use(gdn, name):
 
 
 @pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
-@pytest.mark.parametrize("name", NAMES)
+@pytest.mark.parametrize("name", NAMES + MORE)
 def test_memory_is_held_until_the_call_is_done(gdn, name, handle):
     """Inputs and temporaries that the host lets go of while the call still waits for its turn are
     not filled by later tensors of the current stream."""
-    layer = Layer(gdn)
+    layer = layer_of(gdn, name)
     want = layer.results(layer.calls()[name]())
     layer.fresh()
     s = torch.cuda.Stream()
@@ -155,8 +208,10 @@ def test_memory_is_held_until_the_call_is_done(gdn, name, handle):
     out = layer.calls()[name](q=q, stream=s.cuda_stream if handle else s)
     del q
     later = []
-    for n in (layer.q.numel() * 2, 1 << 20, 2 << 20, 4 << 20):  # (workspaces are a few MB)
+    for n in (layer.q.numel() * 2, 1 << 20, 2 << 20, 4 << 20):  # (workspaces: a few MB, some more)
         later += [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for n in (16 << 20, 64 << 20, 160 << 20):
+        later.append(torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
     same(layer.results(out), want)
     assert torch.cuda.memory_reserved() - before < 1 << 30
