@@ -10,11 +10,13 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
 #include <exception>
+#include <optional>
 #include <sstream>
 #include <string>
 #include <vector>
@@ -45,12 +47,24 @@ std::string shown(const at::Tensor& t) {
 
 // ------------------------------------------------------------------------------- arguments
 
+// A cache as gdn.KVCache keeps it: the C ABI's description and the GPU that the buffers are on.
+struct Cache {
+  gdn_kv_cache desc;
+  int32_t device;
+};
+
 class Args {
  public:
   Args(const char* name, PyObject* const* v, Py_ssize_t n, Py_ssize_t want) : name_(name), v_(v) {
     if (n != want) refuse(std::string(name) + ": wrong number of arguments");
   }
-  // a tensor on the GPU
+  // The call's GPU is that of its cache or first tensor: all the others are to be on it.
+  void on(int device, const char* what) const {
+    if (device_ < 0) device_ = device;
+    if (device != device_)
+      refuse(at(what) + " is on cuda:" + std::to_string(device) + ", what comes before it on cuda:" +
+             std::to_string(device_));
+  }
   const at::Tensor& tensor(int i, const char* what) const {
     const at::Tensor* t = optional(i, what);
     if (!t) refuse(at(what) + " is to be a tensor");
@@ -79,6 +93,7 @@ class Args {
       o << "] on the GPU, got " << shown(t);
       refuse(o.str());
     }
+    on(t.get_device(), what);
     return t;
   }
   const void* packed_or_null(int i, const char* what, at::ScalarType dtype,
@@ -92,7 +107,8 @@ class Args {
       refuse(at(what) + " is to be [tokens, heads, D] with a contiguous last dimension, got " +
              shown(t));
     if (t.scalar_type() != dtype || !t.is_cuda())
-      refuse(at(what) + " has another dtype or device than the call: " + shown(t));
+      refuse(at(what) + " is not on the GPU, or has another dtype than the call: " + shown(t));
+    on(t.get_device(), what);
     return t;
   }
   int io(int i, const char* what) const {
@@ -113,25 +129,35 @@ class Args {
   }
   bool none(int i) const { return v_[i] == Py_None; }
   const gdn_kv_cache* cache(int i) const {
-    return static_cast<const gdn_kv_cache*>(PyLong_AsVoidPtr(v_[i]));
+    const Cache* c = static_cast<const Cache*>(PyLong_AsVoidPtr(v_[i]));
+    on(c->device, "cache");
+    return &c->desc;
   }
   const at::Tensor& workspace(int i) const {
     const at::Tensor& t = tensor(i, "workspace");
     if (!t.is_cuda() || !t.is_contiguous())
       refuse(at("workspace is to be a contiguous tensor on the GPU, got ") + shown(t));
+    on(t.get_device(), "workspace");
     return t;
   }
   // the status word: an int32 tensor, or None
   int32_t* status(int i) const {
     return static_cast<int32_t*>(const_cast<void*>(packed_or_null(i, "dev_status", at::kInt, {1})));
   }
-  // torch's current stream (gdn.py makes the stream that a user names the current one)
-  static cudaStream_t stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
+  // torch's current stream on the call's GPU, which becomes the current one until the call's end
+  // (gdn.py makes the stream that a user names the current one)
+  cudaStream_t stream() const {
+    const auto d = static_cast<c10::DeviceIndex>(device_);
+    if (d != c10::cuda::current_device()) guard_.emplace(d);
+    return c10::cuda::getCurrentCUDAStream(d).stream();
+  }
   std::string at(const char* what) const { return std::string(name_) + ": " + what; }
 
  private:
   const char* name_;
   PyObject* const* v_;
+  mutable int device_ = -1;
+  mutable std::optional<c10::cuda::CUDAGuard> guard_;
 };
 
 const float* f32(const void* p) { return static_cast<const float*>(p); }

@@ -530,6 +530,11 @@ def qk_norm_rope_backward(q, k, positions, cos_sin, q_weight, k_weight, dq_out, 
         workspace, st))
 
 
+class _CacheHandle(ctypes.Structure):
+    """What the torch binding reads of a cache: its description and the GPU that it is on."""
+    _fields_ = [("desc", KvCacheDesc), ("device", ctypes.c_int32)]
+
+
 class KVCache:
     """The buffers of a paged 8-bit key/value cache (layouts of include/gdn.h):
     k [pages, hkv, page, D] and v [pages, hkv, page // 4, D, 4], both int8 or float8_e4m3fn;
@@ -549,10 +554,14 @@ class KVCache:
             if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or not t.is_cuda:
                 _refuse("KVCache", f"{name} is to be a contiguous {dtype} tensor {tuple(shape)} on "
                                    f"the GPU, got {t.dtype} {tuple(t.shape)} on {t.device}")
+            if t.device != k.device:
+                _refuse("KVCache", f"{name} is on {t.device}, k on {k.device}")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.desc = KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
-                                v_scale.data_ptr(), pages, page, hkv, D, fmt)
-        self._address = ctypes.addressof(self.desc)
+        self._handle = _CacheHandle(KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+                                                v_scale.data_ptr(), pages, page, hkv, D, fmt),
+                                    k.device.index)
+        self.desc = self._handle.desc  # (a view of it)
+        self._address = ctypes.addressof(self._handle)
 
     @property
     def buffers(self):

@@ -200,3 +200,33 @@ def test_workspace_for_refuses(gdn):
         with pytest.raises(gdn.GdnError) as e:
             gdn.kv_attention_workspace(Cache, q, t)
         assert e.value.status == status
+
+
+class OnGpu:
+    """Looks like a tensor on some GPU; there is nothing behind it."""
+
+    def __init__(self, shape, dtype, index):
+        self.shape, self.dtype, self.device = shape, dtype, torch.device("cuda", index)
+        self.is_cuda = True
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return FAKE
+
+
+def test_cache_buffers_on_one_gpu(gdn):
+    def cache(*index):
+        return gdn.KVCache(*(OnGpu(s, d, i) for s, d, i in zip(
+            ((2, 1, 16, 64), (2, 1, 4, 64, 4), (2, 1), (2, 1)),
+            (torch.int8, torch.int8, torch.float32, torch.float32), index)))
+    c = cache(1, 1, 1, 1)
+    assert c._handle.device == 1 and c.desc.num_pages == 2 and c.desc.k_codes == FAKE
+    for index in ((0, 1, 0, 0), (0, 0, 1, 0), (0, 0, 0, 1), (1, 0, 0, 0)):
+        with pytest.raises(gdn.GdnError) as e:
+            cache(*index)
+        assert e.value.status == 1 and "cuda:1" in str(e.value)
