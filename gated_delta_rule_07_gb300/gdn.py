@@ -538,7 +538,8 @@ class _CacheHandle(ctypes.Structure):
 class KVCache:
     """The buffers of a paged 8-bit key/value cache (layouts of include/gdn.h):
     k [pages, hkv, page, D] and v [pages, hkv, page // 4, D, 4], both int8 or float8_e4m3fn;
-    k_scale, v_scale [pages, hkv] fp32.  ``KVCache.empty`` allocates them."""
+    k_scale, v_scale [pages, hkv] fp32.  ``KVCache.empty`` allocates them.  The buffers of a cache
+    stay the ones that it was made of (its calls keep their addresses); their contents are free."""
 
     def __init__(self, k, v, k_scale, v_scale):
         fmt = _KV_FORMATS.get(k.dtype)
@@ -556,16 +557,18 @@ class KVCache:
                                    f"the GPU, got {t.dtype} {tuple(t.shape)} on {t.device}")
             if t.device != k.device:
                 _refuse("KVCache", f"{name} is on {t.device}, k on {k.device}")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._buffers = k, v, k_scale, v_scale
         self._handle = _CacheHandle(KvCacheDesc(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
                                                 v_scale.data_ptr(), pages, page, hkv, D, fmt),
                                     k.device.index)
         self.desc = self._handle.desc  # (a view of it)
         self._address = ctypes.addressof(self._handle)
 
-    @property
-    def buffers(self):
-        return self.k, self.v, self.k_scale, self.v_scale
+    buffers = property(lambda self: self._buffers)
+    k = property(lambda self: self._buffers[0])
+    v = property(lambda self: self._buffers[1])
+    k_scale = property(lambda self: self._buffers[2])
+    v_scale = property(lambda self: self._buffers[3])
 
     @classmethod
     def empty(cls, pages, hkv, page, D, dtype=torch.int8, device="cuda"):

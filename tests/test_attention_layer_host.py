@@ -230,3 +230,14 @@ def test_cache_buffers_on_one_gpu(gdn):
         with pytest.raises(gdn.GdnError) as e:
             cache(*index)
         assert e.value.status == 1 and "cuda:1" in str(e.value)
+
+
+def test_cache_keeps_its_buffers(gdn):
+    """The calls go by the buffers' addresses: assigning another tensor is refused."""
+    c = gdn.KVCache(*(OnGpu(s, d, 0) for s, d in (
+        ((2, 1, 16, 64), torch.int8), ((2, 1, 4, 64, 4), torch.int8), ((2, 1), torch.float32),
+        ((2, 1), torch.float32))))
+    for name in ("k", "v", "k_scale", "v_scale", "buffers"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, None)
+    assert c.buffers == (c.k, c.v, c.k_scale, c.v_scale)
