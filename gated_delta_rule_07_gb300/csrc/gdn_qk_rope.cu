@@ -348,17 +348,19 @@ qk_rope_backward_kernel(QkRopeArgs a, int ctas_q) {
       }
       const float r = rsqrtf(row_sum<LPR>(s2) * (1.f / D) + a.eps);
       const float m = row_sum<LPR>(dot) * (1.f / D) * r;  // mean(dn n)
+      // (past the last head there is no row: zeros, whose n is not a number where eps is 0)
+      const bool live = good && h < heads;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float na = xa[j] * r, nb = xb[j] * r;
-        if (good) {
+        if (live) {
           dwa[j] = fmaf(ya[j], na, dwa[j]);
           dwb[j] = fmaf(yb[j], nb, dwb[j]);
         }
         xa[j] = r * fmaf(ya[j], wa[j], -na * m);
         xb[j] = r * fmaf(yb[j], wb[j], -nb * m);
       }
-      if (good && h < heads) put_pairs<PAIRS>(out, p, xa, xb);
+      if (live) put_pairs<PAIRS>(out, p, xa, xb);
       out += RPW * D;
     }
     t = next;

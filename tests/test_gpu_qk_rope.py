@@ -156,3 +156,21 @@ def test_on_another_stream(gdn):
     got = gdn.qk_norm_rope_backward(*args, *do, stream=s)
     s.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("hq,hkv,D", [(3, 1, 64), (5, 6, 64), (3, 1, 128), (2, 1, 256)])
+def test_no_eps(gdn, hq, hkv, D, io):
+    """eps = 0 with numbers of heads that do not fill a warp's rows."""
+    proj, q, k, pos, tab, wq, wk, dqo, dko = make(70, hq, hkv, D, 32, io, seed=D + hq)
+    gq, gk = on_gpu(proj, q, k)
+    args = (gq, gk, pos.cuda(), tab.cuda(), wq.cuda(), wk.cuda())
+    outs = gdn.qk_norm_rope(*args, eps=0.0, check_status=True)
+    grads = gdn.qk_norm_rope_backward(*args, dqo.cuda(), dko.cuda(), eps=0.0, check_status=True)
+    for i, (x, w, do) in enumerate(((q, wq, dqo), (k, wk, dko))):
+        ref, mag = at.rope(x, pos, tab, w, 0.0, 0.0, "half")
+        close(outs[i], ref, mag, 2.0 ** -19, io, ("out", i))
+        dx, dw, dx_mag, dw_mag = at.rope_grad(x, pos, tab, w, 0.0, 0.0, "half", do)
+        assert torch.isfinite(grads[i].float()).all() and torch.isfinite(grads[2 + i]).all()
+        close(grads[i], dx, dx_mag, 2.0 ** -18, io, ("dx", i))
+        close(grads[2 + i], dw, dw_mag, 2.0 ** -14, torch.float32, ("dw", i))
