@@ -590,9 +590,14 @@ namespace {
 
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 
+// a dimension's stride; that of a single row means nothing
+int64_t stride_of(int64_t stride, int64_t rows) { return rows > 1 ? stride : 0; }
+
 // rows strided in elements: every row starts on a 16-byte boundary
-bool strides_ok(int64_t token, int64_t head, int io) {
+bool strides_ok(int64_t token, int64_t tokens, int64_t head, int64_t heads, int io) {
   const int64_t unit = io == GDN_BF16 ? 8 : 4;
+  token = stride_of(token, tokens);
+  head = stride_of(head, heads);
   return token >= 0 && head >= 0 && token % unit == 0 && head % unit == 0;
 }
 
@@ -605,8 +610,8 @@ gdn_status check_rope(const gdn_qk_rope_problem* p) {
   if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
   if (!head_dim_ok(p->head_dim) || p->rotary_dim % 16 || p->hq > 65535 || p->hkv > 65535)
     return GDN_ERR_UNSUPPORTED;
-  if (!strides_ok(p->q_token_stride, p->q_head_stride, p->io_dtype) ||
-      !strides_ok(p->k_token_stride, p->k_head_stride, p->io_dtype))
+  if (!strides_ok(p->q_token_stride, p->total_tokens, p->q_head_stride, p->hq, p->io_dtype) ||
+      !strides_ok(p->k_token_stride, p->total_tokens, p->k_head_stride, p->hkv, p->io_dtype))
     return GDN_ERR_INVALID_ARGUMENT;
   return GDN_OK;
 }
@@ -617,8 +622,10 @@ gdn::QkRopeArgs rope_args(const gdn_qk_rope_problem* p, const void* q, const voi
   gdn::QkRopeArgs a;
   memset(&a, 0, sizeof(a));
   a.T = p->total_tokens;
-  a.q_ts = p->q_token_stride; a.q_hs = p->q_head_stride;
-  a.k_ts = p->k_token_stride; a.k_hs = p->k_head_stride;
+  a.q_ts = stride_of(p->q_token_stride, p->total_tokens);
+  a.q_hs = stride_of(p->q_head_stride, p->hq);
+  a.k_ts = stride_of(p->k_token_stride, p->total_tokens);
+  a.k_hs = stride_of(p->k_head_stride, p->hkv);
   a.hq = p->hq; a.hkv = p->hkv; a.D = p->head_dim; a.R = p->rotary_dim;
   a.max_pos = p->max_positions;
   a.bf16 = p->io_dtype == GDN_BF16;
@@ -662,9 +669,12 @@ gdn::KvArgs kv_args(const gdn_kv_cache* c, const gdn_kv_problem* p, const int32_
   a.page = c->page_size;
   while ((1 << a.page_shift) < a.page) ++a.page_shift;
   a.num_pages = c->num_pages; a.max_pages = p->max_pages;
-  a.k_ts = p->k_token_stride; a.k_hs = p->k_head_stride;
-  a.v_ts = p->v_token_stride; a.v_hs = p->v_head_stride;
-  a.q_ts = p->q_token_stride; a.q_hs = p->q_head_stride;
+  a.k_ts = stride_of(p->k_token_stride, p->total_tokens);
+  a.k_hs = stride_of(p->k_head_stride, c->hkv);
+  a.v_ts = stride_of(p->v_token_stride, p->total_tokens);
+  a.v_hs = stride_of(p->v_head_stride, c->hkv);
+  a.q_ts = stride_of(p->q_token_stride, p->total_tokens);
+  a.q_hs = stride_of(p->q_head_stride, p->hq);
   a.bf16 = p->io_dtype == GDN_BF16;
   a.e4m3 = c->format == GDN_KV_E4M3;
   a.table = table; a.pos0 = pos0; a.cu = cu;
@@ -734,8 +744,9 @@ gdn_status gdn_kv_append(const gdn_kv_cache* cache, const gdn_kv_problem* p, con
                          const int32_t* cu_seqlens, int32_t* dev_status, cudaStream_t stream) {
   const gdn_status st = check_kv(cache, p);
   if (st != GDN_OK) return st;
-  if (!strides_ok(p->k_token_stride, p->k_head_stride, p->io_dtype) ||
-      !strides_ok(p->v_token_stride, p->v_head_stride, p->io_dtype) || !rows_ok(p, cu_seqlens))
+  if (!strides_ok(p->k_token_stride, p->total_tokens, p->k_head_stride, cache->hkv, p->io_dtype) ||
+      !strides_ok(p->v_token_stride, p->total_tokens, p->v_head_stride, cache->hkv, p->io_dtype) ||
+      !rows_ok(p, cu_seqlens))
     return GDN_ERR_INVALID_ARGUMENT;
   if (p->total_tokens == 0) return GDN_OK;
   if (!k || !v || !block_table || !ctx_lens || !aligned16(k) || !aligned16(v))
@@ -766,7 +777,7 @@ static gdn_status check_kv_attention(const gdn_kv_cache* cache, const gdn_kv_pro
   const gdn_status st = check_kv(cache, p);
   if (st != GDN_OK) return st;
   if (p->hq < 1 || p->hq % cache->hkv ||
-      !strides_ok(p->q_token_stride, p->q_head_stride, p->io_dtype))
+      !strides_ok(p->q_token_stride, p->total_tokens, p->q_head_stride, p->hq, p->io_dtype))
     return GDN_ERR_INVALID_ARGUMENT;
   // rows (tokens x query heads) are 32-bit
   return p->hq > 32768 || p->total_tokens * p->hq > (int64_t)INT32_MAX ? GDN_ERR_UNSUPPORTED

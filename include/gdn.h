@@ -359,8 +359,9 @@ typedef struct gdn_qk_rope_problem {
     int32_t max_positions;    /* rows of the table                                          */
     float eps;                /* added to the mean square                                   */
     float weight_offset;      /* added to both weights (1 for weights stored around zero)   */
-    int64_t q_token_stride, q_head_stride;  /* elements; multiples of 16 bytes; the last      */
-    int64_t k_token_stride, k_head_stride;  /* dimension is contiguous                        */
+    int64_t q_token_stride, q_head_stride;  /* elements; multiples of 16 bytes (that of one   */
+    int64_t k_token_stride, k_head_stride;  /* token or head is ignored); the last dimension  */
+                                            /* is contiguous                                  */
 } gdn_qk_rope_problem;
 
 /* Queries and keys normalised per head and rotated by position, in one pass.  Per row x (one
@@ -421,8 +422,8 @@ typedef struct gdn_kv_problem {
     int32_t max_pages;        /* entries of a block-table row (>= 1)                        */
     int32_t hq;               /* query heads (attention only; a multiple of hkv)            */
     int32_t io_dtype;         /* gdn_dtype of k, v, q and the outputs                       */
-    int64_t k_token_stride, k_head_stride;  /* elements, multiples of 16 bytes (append)     */
-    int64_t v_token_stride, v_head_stride;
+    int64_t k_token_stride, k_head_stride;  /* elements, multiples of 16 bytes (append);    */
+    int64_t v_token_stride, v_head_stride;  /* that of one token or head is ignored         */
     int64_t q_token_stride, q_head_stride;  /* (attention)                                  */
 } gdn_kv_problem;
 

@@ -241,3 +241,20 @@ def test_cache_keeps_its_buffers(gdn):
         with pytest.raises(AttributeError):
             setattr(c, name, None)
     assert c.buffers == (c.k, c.v, c.k_scale, c.v_scale)
+
+
+def test_strides_of_single_rows_do_not_count(gdn):
+    """The stride of a dimension of one row says nothing, so it is not held to 16 bytes."""
+    for kw, ok in ((dict(total_tokens=1, q_token_stride=1001, k_token_stride=-3), True),
+                   (dict(total_tokens=0, q_token_stride=1001), True),
+                   (dict(hq=1, q_head_stride=7), True), (dict(hkv=1, k_head_stride=7), True),
+                   (dict(total_tokens=2, q_token_stride=1001), False),
+                   (dict(hq=1, k_head_stride=7), False)):
+        got = gdn.gdn_qk_norm_rope_backward_workspace_size(rope_problem(gdn, **kw))
+        assert (got > 0) == ok, kw
+    for c, kw, ok in (({}, dict(total_tokens=1, q_token_stride=1001), True),
+                      (dict(hkv=1), dict(hq=1, q_head_stride=7), True),
+                      ({}, dict(total_tokens=2, q_token_stride=1001), False),
+                      (dict(hkv=1), dict(hq=2, q_head_stride=7), False)):
+        got = gdn.gdn_kv_attention_workspace_size(cache_desc(gdn, **c), kv_problem(gdn, **kw))
+        assert (got > 0) == ok, kw

@@ -54,3 +54,33 @@ def test_tensors_of_another_gpu(gdn):
     cache._handle.device = cache.k.device.index + 1
     for name, kw in kv_calls(gdn, cache).items():
         refused(gdn, getattr(gdn, name), kw, 1, "cuda:0", "cuda:1")
+
+
+def odd(t):
+    """The same rows with strides that no 16-byte load could follow where a dimension is one."""
+    wide = torch.zeros(t.numel() + 4096, dtype=t.dtype, device=t.device)
+    strides = [1001 if n == 1 else s for n, s in zip(t.shape[:2], t.stride())] + [1]
+    got = wide.as_strided(t.shape, strides)
+    return got.copy_(t)
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("T,heads", [(1, 4), (5, 1), (1, 1)])
+def test_single_rows_of_any_stride(gdn, T, heads, io):
+    """One token, or one head: the results are those of contiguous tensors."""
+    gen = torch.Generator("cuda").manual_seed(T + heads)
+    q, k, v, dq, dk = (torch.randn(T, heads, 64, device="cuda", generator=gen).to(io)
+                       for _ in range(5))
+    pos, tab, w = torch.arange(T, device="cuda").int(), at.table(16, 32).cuda(), torch.ones(64).cuda()
+    for call, more in ((gdn.qk_norm_rope, ()), (gdn.qk_norm_rope_backward, (dq, dk))):
+        want = call(q, k, pos, tab, w, w, *more)
+        got = call(odd(q), odd(k), pos, tab, w, w, *more)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    table, held = ints(1, 1), ints(1)
+    outs = []
+    for f in (lambda t: t, odd):
+        cache = gdn.KVCache.empty(1, heads, 16, 64)
+        gdn.kv_append(cache, f(k), f(v), table, held, check_status=True)
+        outs.append([*gdn.kv_read(cache, table, None, None, T),
+                     *gdn.kv_attention(cache, f(q), table, held + T, check_status=True)])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
