@@ -24,9 +24,9 @@
 //     weights too, for fp32 accuracy.
 //   * Softmax, one pass: the running maximum is of y = x log2 e + log2(value scale), so that the
 //     weights w = 2^(y - M) already carry their page's value scale and stay in fp16's range
-//     whatever the scales are; the sum takes w / value scale.  The reference M follows the
-//     running maximum and only moves (and the sums are only rescaled) when a tile exceeds it by
-//     2^15: weights stay below that, fp16's range.
+//     whatever the scales are; the sum takes w / value scale, on a reference of its own.  The
+//     reference M follows the running maximum and only moves (and the sums are only rescaled) when
+//     a tile exceeds it by 2^15: weights stay below that, fp16's range.
 //   * Work.  Units of 16 keys, of all sequences, kv heads and row tiles in one line, cut into
 //     equal runs, one a CTA: ragged lengths balance, one long sequence fills the GPU.  A CTA's
 //     warps take its run's units in turn and join at the end of each item; items cut between CTAs
@@ -90,14 +90,15 @@ template <int D, int NT, bool SPLIT> struct Shape {
 
 template <typename IO, int D, int NT, bool E4M3>
 __global__ void __launch_bounds__(kThreads, (Shape<D, NT, sizeof(IO) == 4>::ctas))
-kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
+kv_attention_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
   constexpr bool SPLIT = sizeof(IO) == 4;
   using S = Shape<D, NT, SPLIT>;
   using W = Work<S::rows, kTile, kItemUnits>;
   constexpr int ROWS = S::rows, KC = D / 64, VC = D / 32, STEPS = D / 16;
   extern __shared__ __align__(16) char smem[];
-  __shared__ float q_scale[ROWS];
-  __shared__ float2 warp_ml[kWarps][ROWS];
+  __shared__ float q_scale[ROWS], row_up[ROWS];
+  __shared__ float2 warp_mx[kWarps][ROWS];
+  __shared__ float warp_sum[kWarps][ROWS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid / 32;
   const int r = lane >> 2, c = lane & 3;
 
@@ -256,6 +257,8 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[t][i][e] = 0.f;
 
+    // B, and the value scale below which it moves: any at first, until a page of values is met
+    float base = 0.f, low = CUDART_INF_F;
     for (; tile < tb; tile += kWarps) {
       float s[NT][4];
 #pragma unroll
@@ -292,9 +295,25 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       load_k(pid_next, tile + kWarps);
       entry = entry_of(tile + 2 * kWarps);
 
-      // scores in log2, with the page's value scale; a page of zero values weighs as 2^-100
-      const float lv = v_now > 0.f ? log2_fast(v_now) : -100.f;
-      const float rv = exp2_fast(-lv);
+      // scores in log2, with the page's value scale (the same for the whole warp)
+      float lv = log2_fast(v_now);
+      if (v_now < low) {
+        if (v_now < kLeastScale) {
+          lv = base - kZero;
+        } else {
+          const float f = exp2_fast(lv - base);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (low < CUDART_INF_F) l[t][e] *= f;
+              else M[t][e] += lv;
+            }
+          base = lv;
+          low = fmaxf(v_now * exp2_fast(-kBelow), kLeastScale);
+        }
+      }
+      const float rv = exp2_fast(base - lv);
       const int key = (it.tile0 + tile) * kTile + tok;
       const int first = (it.tile0 + tile) * kTile;
       const bool open = pid >= 0 && first + kTile - 1 <= all_hi && first >= all_lo;
@@ -382,7 +401,7 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       pid = pid_next;
     }
 
-    // join the warps: each leaves its maxima and sums, then its o on the common maximum
+    // join the warps: each leaves its references and sums, then its o on the common reference
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -390,7 +409,12 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         float x = l[t][e];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        if (r == 0) warp_ml[warp][8 * t + 2 * c + e] = make_float2(M[t][e], x);
+        const float mx = M[t][e] - base;
+        if (!(low < CUDART_INF_F)) M[t][e] = kNone;  // no values: o does not count
+        if (r == 0) {
+          warp_mx[warp][8 * t + 2 * c + e] = make_float2(M[t][e], mx);
+          warp_sum[warp][8 * t + 2 * c + e] = x;
+        }
       }
     __syncthreads();  // (the queries in shared memory are no longer needed either)
     float* so = reinterpret_cast<float*>(smem);
@@ -401,7 +425,7 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         const int row = 8 * t + 2 * c + e;
         float m = M[t][e];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][row].x);
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_mx[w][row].x);
         const float f = exp2_fast(M[t][e] - m);
 #pragma unroll
         for (int j = 0; j < VC; ++j)
@@ -412,19 +436,23 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
     const bool begins = ta == 0, ends = tb == it.tiles, whole = begins && ends;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (begins ? 1 : 0);
     if (tid < rows) {  // the rows' sums
-      float m = kNone, L = 0.f;
+      float m = kNone, mx = kNone, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, warp_ml[w][tid].x);
+      for (int w = 0; w < kWarps; ++w) {
+        m = fmaxf(m, warp_mx[w][tid].x);
+        mx = fmaxf(mx, warp_mx[w][tid].y);
+      }
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
-        L = fmaf(warp_ml[w][tid].y, exp2_fast(warp_ml[w][tid].x - m), L);
+        L = fmaf(warp_sum[w][tid], exp2_fast(warp_mx[w][tid].y - mx), L);
       q_scale[tid] = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
+      row_up[tid] = whole ? value_scale(m, mx) : 1.f;
       if (!whole) {
-        part_ml[slot * ROWS + tid] = make_float2(m, L);
+        parts[slot * ROWS + tid] = Part{m, mx, L, 0.f};
       } else if (a.lse) {
         const int tk = over_group(a, rem + tid);
         a.lse[(it.row0 + token0 + tk) * a.hq + head * a.group + rem + tid - tk * a.group] =
-            (m + log2f(L)) * kLn2;
+            (mx + log2f(L)) * kLn2;
       }
     }
     if (ends && !begins && tid == 0) {
@@ -451,8 +479,8 @@ kv_attention_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         o.z += x.z;
         o.w += x.w;
       }
-      const float inv = q_scale[row];
-      o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      const float inv = q_scale[row], up = row_up[row];
+      o = make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
       if (whole) {
         const int tk = over_group(a, rem + row);
         const int64_t at =
@@ -499,7 +527,7 @@ cudaError_t launch(const KvArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int ctas = grid_ctas<W>(a, sms * S::ctas, kMinUnits);
   const Workspace ws(a, S::rows);
-  e = launch_ordered(kern, dim3(ctas), kThreads, S::smem, s, a, ws.part_o, ws.part_ml, ws.descs);
+  e = launch_ordered(kern, dim3(ctas), kThreads, S::smem, s, a, ws.part_o, ws.parts, ws.descs);
   if (e != cudaSuccess) return e;
   return launch_join<IO, D, S::rows>(a, ws, ctas, s);
 }

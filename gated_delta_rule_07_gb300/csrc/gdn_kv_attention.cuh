@@ -3,7 +3,16 @@
 //
 // Work: units of UNIT keys, of all sequences, kv heads and row tiles in one line, cut into equal
 // runs, one a CTA: ragged lengths balance, and one long sequence fills the GPU.  Items cut between
-// CTAs leave partial sums (M, sum, unnormalised o), joined in order by a second small kernel.
+// CTAs leave partial sums (M, X, sum, unnormalised o), joined in order by a second small kernel.
+//
+// Range.  The weights of o are 2^(y - M), y = x + log2(value scale) (x: scores in log2), and reach
+// o whatever the scales are.  The sum is of 2^(x - X) and has a reference of its own, X = M - B: B is
+// the smallest log2 of a value scale met so far (within kBelow), so that a term is a weight times
+// 2^(B - log2(value scale)) <= 2^kBelow and neither small scales nor many keys overflow it.  A page of
+// scale 0 weighs as one of 2^(B - kZero), whose codes (zeros, where an append wrote them) weigh less
+// than fp32 tells beside any other page's; before the first other page B is 0, and then moves M
+// instead of the sum.  Terms are lost only below 2^-126: value scales of one sequence and head may
+// differ by 2^100 (beside pages of scale 0, by 2^70).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -22,6 +31,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // and one 2^-22 of the largest still has all of fp16's bits.
 constexpr float kHead = 8.f, kSlack = 15.f;
 constexpr float kNone = -1e30f;  // the reference before any key
+constexpr float kBelow = 8.f;    // how far a value scale may lie below 2^B before B follows
+constexpr float kZero = 40.f;    // how far below 2^B a value scale of 0 stands
+constexpr float kLeastScale = 1.17549435e-38f;  // value scales below it count as 0
 
 // ------------------------------------------------------------------------------ the work plan
 
@@ -219,10 +231,17 @@ __device__ __forceinline__ float log2_fast(float x) {
 // A thread takes four channels of a row and every `groups`-th partial, in CTA order; the groups
 // join in shared memory, in order.  Columns (rows x D / 4) are spread over blockIdx.y.
 constexpr int kJoinThreads = 256;
+// A partial result's references and sum (o beside it).
+struct alignas(16) Part {
+  float m, x, sum, unused;
+};
+// 2^(M - X), what an o over its sum still lacks (an o of zeros may have any M)
+__device__ __forceinline__ float value_scale(float m, float x) { return exp2_fast(fminf(m - x, 127.f)); }
+
 template <typename IO, int D, int ROWS>
 __device__ __forceinline__ void join_item(const KvArgs& a, const float* part_o,
-                                          const float2* part_ml, int cta, const Desc& d, int groups,
-                                          float4* so, float2* sml) {
+                                          const Part* parts, int cta, const Desc& d, int groups,
+                                          float4* so, Part* sml) {
   const int cols = kJoinThreads / groups, g = threadIdx.x / cols;
   const int col = blockIdx.y * cols + threadIdx.x % cols, row = col / (D / 4);
   const int dim = 4 * (col % (D / 4));
@@ -230,16 +249,18 @@ __device__ __forceinline__ void join_item(const KvArgs& a, const float* part_o,
   const int count = live ? cta - d.first + 1 : 0;
   // CTA first + i left its part in its second slot where the item began there, else in its first
   const int64_t slot0 = 2 * (int64_t)d.first * ROWS + row;
-  float m = kNone, L = 0.f;
+  float m = kNone, mx = kNone, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
   for (int i = g; i < count; i += groups) {
     const int64_t slot = slot0 + (2 * i + (i == 0)) * ROWS;
-    const float2 ml = part_ml[slot];
+    const Part ml = parts[slot];
     const float4 x = *reinterpret_cast<const float4*>(part_o + slot * D + dim);
-    const float now = fmaxf(m, ml.x), f = exp2_fast(ml.x - now), k = exp2_fast(m - now);
+    const float now = fmaxf(m, ml.m), f = exp2_fast(ml.m - now), k = exp2_fast(m - now);
+    const float now_x = fmaxf(mx, ml.x);
     m = now;
-    L = fmaf(ml.y, f, L * k);
+    L = fmaf(ml.sum, exp2_fast(ml.x - now_x), L * exp2_fast(mx - now_x));
+    mx = now_x;
     o.x = fmaf(x.x, f, o.x * k);
     o.y = fmaf(x.y, f, o.y * k);
     o.z = fmaf(x.z, f, o.z * k);
@@ -247,17 +268,20 @@ __device__ __forceinline__ void join_item(const KvArgs& a, const float* part_o,
   }
   if (groups > 1) {
     so[threadIdx.x] = o;
-    sml[threadIdx.x] = make_float2(m, L);
+    sml[threadIdx.x] = Part{m, mx, L, 0.f};
     __syncthreads();
     if (g) return;
-    for (int i = 1; i < groups; ++i) m = fmaxf(m, sml[i * cols + threadIdx.x].x);
+    for (int i = 1; i < groups; ++i) {
+      m = fmaxf(m, sml[i * cols + threadIdx.x].m);
+      mx = fmaxf(mx, sml[i * cols + threadIdx.x].x);
+    }
     o = make_float4(0.f, 0.f, 0.f, 0.f);
     L = 0.f;
     for (int i = 0; i < groups; ++i) {
-      const float2 ml = sml[i * cols + threadIdx.x];
+      const Part ml = sml[i * cols + threadIdx.x];
       const float4 x = so[i * cols + threadIdx.x];
-      const float f = exp2_fast(ml.x - m);
-      L = fmaf(ml.y, f, L);
+      const float f = exp2_fast(ml.m - m);
+      L = fmaf(ml.sum, exp2_fast(ml.x - mx), L);
       o.x = fmaf(x.x, f, o.x);
       o.y = fmaf(x.y, f, o.y);
       o.z = fmaf(x.z, f, o.z);
@@ -268,21 +292,21 @@ __device__ __forceinline__ void join_item(const KvArgs& a, const float* part_o,
   const int tk = over_group(a, d.rem + row);
   const int64_t at =
       (d.row0 + d.token0 + tk) * a.hq + d.head * a.group + d.rem + row - tk * a.group;
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L > 0.f ? 1.f / L : 0.f, up = value_scale(m, mx);
   store4(static_cast<IO*>(a.out) + at * D + dim,
-         make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-  if (a.lse && dim == 0) a.lse[at] = (m + log2f(L)) * kLn2;
+         make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up));
+  if (a.lse && dim == 0) a.lse[at] = (mx + log2f(L)) * kLn2;
 }
 
 // SEVERAL: block blockIdx.x joins the items that ended in the CTAs blockIdx.x, + gridDim.x, ..;
 // else the one that ended in CTA blockIdx.x, if any did.
 template <typename IO, int D, int ROWS, bool SEVERAL>
 __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, const float* part_o,
-                                                                  const float2* part_ml,
+                                                                  const Part* parts,
                                                                   const Desc* descs, int ctas,
                                                                   int groups) {
   __shared__ float4 so[kJoinThreads];
-  __shared__ float2 sml[kJoinThreads];
+  __shared__ Part sml[kJoinThreads];
   stream_order();
   if constexpr (SEVERAL) {
     __shared__ int ending[kMaxCtas], items;
@@ -294,13 +318,13 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, cons
     __syncthreads();
     for (int i = 0; i < items; ++i) {
       const Desc d = descs[ending[i]];
-      join_item<IO, D, ROWS>(a, part_o, part_ml, ending[i], d, groups, so, sml);
+      join_item<IO, D, ROWS>(a, part_o, parts, ending[i], d, groups, so, sml);
       __syncthreads();
     }
   } else {
     const Desc d = descs[blockIdx.x];
     if (d.first >= 0)
-      join_item<IO, D, ROWS>(a, part_o, part_ml, (int)blockIdx.x, d, groups, so, sml);
+      join_item<IO, D, ROWS>(a, part_o, parts, (int)blockIdx.x, d, groups, so, sml);
   }
 }
 
@@ -308,16 +332,16 @@ __global__ void __launch_bounds__(kJoinThreads) kv_attention_join(KvArgs a, cons
 
 struct Workspace {  // two partial results of each CTA, a descriptor of each
   float* part_o;
-  float2* part_ml;
+  Part* parts;
   Desc* descs;
   Workspace(const KvArgs& a, int rows) {
     part_o = a.workspace;
-    part_ml = reinterpret_cast<float2*>(part_o + (int64_t)2 * kMaxCtas * rows * a.D);
-    descs = reinterpret_cast<Desc*>(part_ml + (int64_t)2 * kMaxCtas * rows);
+    parts = reinterpret_cast<Part*>(part_o + (int64_t)2 * kMaxCtas * rows * a.D);
+    descs = reinterpret_cast<Desc*>(parts + (int64_t)2 * kMaxCtas * rows);
   }
   static size_t bytes(const KvArgs& a, int rows) {
     const size_t r = (size_t)2 * kMaxCtas * rows;
-    return r * a.D * sizeof(float) + r * sizeof(float2) + kMaxCtas * sizeof(Desc);
+    return r * a.D * sizeof(float) + r * sizeof(Part) + kMaxCtas * sizeof(Desc);
   }
 };
 
@@ -348,7 +372,7 @@ cudaError_t launch_join(const KvArgs& a, const Workspace& ws, int ctas, cudaStre
   while (groups < (few ? 64 : 16) && ((parts > 0 && groups < 4) || 4 * groups < parts)) groups *= 2;
   const auto go = [&](auto kern, int blocks) {
     return launch_ordered(kern, dim3(blocks, all_cols * groups / kJoinThreads), kJoinThreads, 0, s, a,
-                          (const float*)ws.part_o, (const float2*)ws.part_ml,
+                          (const float*)ws.part_o, (const Part*)ws.parts,
                           (const Desc*)ws.descs, ctas, groups);
   };
   if (few) return go(kv_attention_join<IO, D, ROWS, true>, (int)(4 * items));

@@ -72,10 +72,15 @@ struct TcSmem {  // byte offsets, each operand tile on a 1024-byte boundary
   static constexpr int sums = K;  // float [rows][kSumPad], then [rows][D], at the end of an item
 };
 // A step's run of 16 keys, all within a page: where its codes begin (< 0: it has no page), its key
-// scale, log2 of its value scale, and that scale's inverse.
+// scale, log2 of its value scale, 2^B over that scale.  And the same for all runs of the step: B,
+// whether a page of values has been met, and 1, or where B moved (rare) what the sums so far are
+// multiplied by (0: B is the first, and moves the references); 2^B over the scale is then given as 0,
+// so that the step's weights reach the sums only when those have moved.
 struct alignas(16) PageRun {
-  int64_t from, unused;
-  float ks, lv, rv, unused2;
+  int64_t from;
+  float base;
+  int valued;
+  float ks, lv, rv, again;
 };
 // What the item loop needs again after an item (kept out of the registers in between).
 struct ItemState {
@@ -181,7 +186,7 @@ __device__ __forceinline__ float warp_max(float x) {
 
 template <int D, bool E4M3, int ROWS>
 __global__ void __launch_bounds__(kTcThreads, 1)
-kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
+kv_attention_tc_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
   using TcWork = Work<ROWS, kKeys, kTcItemUnits>;
   constexpr int KC = D / 64, VC = D / 64;
   extern __shared__ char smem_raw[];
@@ -453,7 +458,8 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         fence_after_sync();
         const float4 run = *reinterpret_cast<const float4*>(&runs[step % kAhead * 8 + own].ks);
         const float ks = run.x, lv = run.y, rv = run.z;
-        const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv), rv2 = pair(rv, rv);
+        const uint64_t ks2 = pair(ks, ks), lv2 = pair(lv, lv);
+        uint64_t rv2 = pair(rv, rv);
         auto seen = [&](int la) {
           return key <= la && (a.window == 0 || key > la - a.window);
         };
@@ -502,9 +508,22 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         // (an item's first step has no reference yet: it goes straight there)
         const bool starts = tile == ta;
         if (!starts) weights(false);
-        if (starts || soft_or(top > kSlack)) {
+        if (starts || soft_or(top > kSlack || run.w != 1.f)) {
           // the rows' references move to this step's maxima; O^T of the last step has to be done
           // (that of this one waits for the weights)
+          float first_base = 0.f;
+          if (run.w != 1.f) {  // B has moved (not in an item's first step)
+            const float base = runs[step % kAhead * 8].base;
+            if (run.w > 0.f) {
+#pragma unroll
+              for (int i = 0; i < ROWS / 4; ++i) l[i] = mul2(l[i], pair(run.w, run.w));
+            } else {
+              first_base = base;
+            }
+            const float x = lv > -CUDART_INF_F ? exp2_fast(base - lv) : 0.f;
+            rv2 = pair(x, x);
+          }
+          const bool fresh = starts || run.w != 1.f;  // no weight of the step is in the sums
           if (!starts) wait_bar(bar(kSumDone, step - 1), parity(step - 1), failed);
           fence_after_sync();
 #pragma unroll
@@ -523,7 +542,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
               unpair(fma2(s2, a2, add2(lv2, ab.y)), z0, z1);
               unpair(fma2(s2, a2, lv2), y0, y1);
               const bool in0 = seen(la.x), in1 = seen(la.y);
-              const float over = starts ? 0.f : -exp2_fast(kSlack);
+              const float over = fresh ? 0.f : -exp2_fast(kSlack);
               l[8 * cc + i / 2] = fma2(pair(in0 && z0 > kSlack ? over : 0.f,
                                             in1 && z1 > kSlack ? over : 0.f), rv2, l[8 * cc + i / 2]);
               y0 = in0 ? y0 : -CUDART_INF_F;
@@ -538,7 +557,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
           }
           soft_or(false);
           if (st < rows) {
-            const float was = -minus_ref(st);
+            const float was = -minus_ref(st) + first_base;
             float m = was;
 #pragma unroll
             for (int q = 0; q < 4; ++q) m = fmaxf(m, wmax[q * ROWS + st] - kHead);
@@ -565,7 +584,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
             }
             if (!starts) tmem_st16(tm_o + 16 * c, s);
           }
-          weights(!starts);
+          weights(!fresh);
         }
         fence_async_smem();
         fence_before_sync();
@@ -578,6 +597,8 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
       // the item's end: sums over the keys (threads), then o
       const bool begins = ta == 0, ends = tb == it.tiles, whole = begins && ends;
       const int64_t row0 = state->row0;
+      const float base_now = runs[(step - 1) % kAhead * 8].base;
+      const bool valued = runs[(step - 1) % kAhead * 8].valued;
       wait_bar(bar(kSumDone, step - 1), parity(step - 1), failed);
       fence_after_sync();
       float* const sums = reinterpret_cast<float*>(sm + TcSmem::sums);
@@ -601,14 +622,14 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         if (row < rows && (st & 7) == 0) {
-          const float m = -minus_ref(row);
+          const float m = -minus_ref(row), mx = m - base_now;
           row_f[row] = whole ? (L > 0.f ? 1.f / L : 0.f) : 1.f;
           if (!whole) {
-            part_ml[slot * ROWS + row] = make_float2(m, L);
+            parts[slot * ROWS + row] = Part{valued ? m : kNone, mx, L, 0.f};
           } else if (a.lse) {
             const int tk = over_group(a, rem + row);
             a.lse[(row0 + token0 + tk) * a.hq + head * a.group + rem + row - tk * a.group] =
-                (m + log2f(L)) * kLn2;
+                (mx + log2f(L)) * kLn2;
           }
         }
       }
@@ -635,12 +656,13 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         __syncwarp();
       }
       soft_or(false);
+      const float up = !whole ? 1.f : valued ? exp2_fast(base_now) : 0.f;
 #pragma unroll 1
       for (int i = st; i < rows * (D / 4); i += 32 * kSoftWarps) {
         const int row = i / (D / 4), d = 4 * (i % (D / 4));
         float4 o = *reinterpret_cast<const float4*>(o_at + row * D + d);
         const float inv = row_f[row];
-        o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        o = make_float4(o.x * inv * up, o.y * inv * up, o.z * inv * up, o.w * inv * up);
         if (whole) {
           const int tk = over_group(a, rem + row);
           const int64_t at =
@@ -709,30 +731,60 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, float2* part_ml, Desc* descs) {
         return has_page(tile) ? __ldg(table + (key >> a.page_shift)) : -1;
       };
       int entry = entry_of(ta + mine);
+      // B, and the value scale below which it moves: any at first, until a page of values is met
+      float base = 0.f, low = CUDART_INF_F;
       uint32_t step = step0;
       for (int tile = ta; tile < tb; tile += kBatch, step += kBatch) {
         const int next = entry_of(tile + kBatch + mine);
         PageRun run;
         run.from = -1;
-        run.unused = 0;
-        // keys without a page weigh nothing, a page of zero values as 2^-100
         run.ks = 0.f;
-        run.lv = -CUDART_INF_F;
-        run.rv = run.unused2 = 0.f;
+        float vs = 0.f;
         if (has_page(tile + mine)) {
           if (entry >= 0 && entry < a.num_pages) {
             const int64_t block = (int64_t)entry * a.hkv + head;
             const int slot = ((it.tile0 + tile + mine) * kKeys + at) & (a.page - 1);
-            const float vs = __ldg(a.v_scale + block);
+            vs = __ldg(a.v_scale + block);
             run.from = block * (a.page * D) + slot * D;
             run.ks = __ldg(a.k_scale + block);
-            run.lv = vs > 0.f ? log2_fast(vs) : -100.f;
-            run.rv = exp2_fast(-run.lv);
           } else {
             set_status(a.status, GDN_ERR_DEVICE_INPUT);
           }
         }
         entry = next;
+        const bool zeros = !(vs >= kLeastScale);
+        run.again = 1.f;
+        run.base = base;
+        run.valued = low < CUDART_INF_F;
+        if (__any_sync(0xffffffffu, !zeros && vs < low)) {  // B, step by step
+          float least = zeros ? CUDART_INF_F : vs;  // of the step's eight runs
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1)
+            least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const float x = __shfl_sync(0xffffffffu, least, 8 * i);
+            float again = 1.f;
+            if (x < low) {
+              const float lx = log2_fast(x);
+              if (tile + i > ta)
+                again = low < CUDART_INF_F ? fmaxf(exp2_fast(lx - base), kLeastScale) : 0.f;
+              base = lx;
+              low = fmaxf(x * exp2_fast(-kBelow), kLeastScale);
+            }
+            if (mine == i) {
+              run.again = again;
+              run.base = base;
+              run.valued = low < CUDART_INF_F;
+            }
+          }
+        }
+        run.lv = zeros ? run.base - kZero : log2_fast(vs);
+        run.rv = run.again == 1.f ? exp2_fast(run.base - run.lv) : 0.f;
+        if (run.from < 0) {  // keys without a page weigh nothing
+          run.lv = -CUDART_INF_F;
+          run.rv = 0.f;
+        }
         // the slots' last users: the softmax of kAhead steps before
         const int steps = min(kBatch, tb - tile);
         for (int i = 0; i < steps; ++i)
@@ -764,7 +816,7 @@ cudaError_t launch_tc(const KvArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int ctas = grid_ctas<TcWork>(a, sms, kTcMinUnits);
   const Workspace ws(a, ROWS);
-  e = launch_ordered(kern, dim3(ctas), kTcThreads, TcSmem::bytes, s, a, ws.part_o, ws.part_ml,
+  e = launch_ordered(kern, dim3(ctas), kTcThreads, TcSmem::bytes, s, a, ws.part_o, ws.parts,
                      ws.descs);
   if (e != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, D, ROWS>(a, ws, ctas, s);

@@ -472,7 +472,9 @@ size_t gdn_kv_attention_workspace_size(const gdn_kv_cache* cache, const gdn_kv_p
  * hq <= 32768, T hq < 2^31, max_pages page_size <= 2^30 (lengths fit 30 bits; byte offsets into the
  * pool are 64-bit).  dev_status records GDN_ERR_DEVICE_INPUT as above, and GDN_ERR_DEVICE_TIMEOUT if
  * a wait inside the kernel ran out (about a second; outputs are then undefined).  The same inputs
- * give the same bits.  Products take fp16 operands with fp32 sums: codes are exact in fp16; bf16
+ * give the same bits.  Value scales may be as small or as large as an append writes them; those of
+ * the pages that one row sees may differ by 2^100 (by 2^70 beside pages of scale 0, whose values are
+ * zeros; scales below 2^-126 count as 0).  Products take fp16 operands with fp32 sums: codes are exact in fp16; bf16
  * queries are too, after a power of two per row; fp32 queries, and for them the weights, are split
  * into two fp16 parts. */
 gdn_status gdn_kv_attention(const gdn_kv_cache* cache, const gdn_kv_problem* p, const void* q,

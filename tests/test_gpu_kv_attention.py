@@ -341,3 +341,83 @@ def test_append_then_attend_matches_unquantised(gdn):
             mag = torch.einsum("hgj,jhd->hgd", w, vn.abs()).reshape(hq, D)
             err = (out[n].double().cpu() - want).abs()
             assert bool((err <= 2.0 ** -10 * mag + 2.0 ** -8 * want.abs()).all())
+
+
+# Rows a kv head of the two kernels for bf16 and D <= 128 (more than sixteen: the one on tcgen05, with
+# items of 32 or 64 rows); fp32 has one.
+ROWS = [2, 24, 40]
+
+
+def check_range(out, lse, ref, io, lens, p, fmt, what=""):
+    """As `check`, with the floor that fp16's smallest step leaves: a weight off by 2^-25 where the
+    row's largest (page scales included) is 2^8 at least, so 2^-33 of the largest value a key."""
+    floor = 2.0 ** -33 * max(lens) * float(p.vs.max()) * at.QMAX[fmt]
+    o, l, mag = ref
+    check(out, lse, (o, l, mag + 2.0 ** 13 * floor if io == torch.float32 else mag), io, what, floor)
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("rows", ROWS)
+def test_many_keys_of_any_value_scale(gdn, rows, fmt, io):
+    """Twenty thousand keys of nearly the same score, with value scales from the smallest that an
+    append writes (2^-100 over the largest code) to large ones, and all of them zero."""
+    least = 2.0 ** -100 / at.QMAX[fmt]
+    p = Problem(gdn, [20000], [1], rows, 1, 64, 128, fmt, io, seed=40 + rows, std_q=0.01)
+    for scale in (least, 2.0 ** -60, 2.0 ** 60, 2.0 ** 110, 0.0):
+        p.vs[:] = scale
+        p.load()
+        check_range(*p.run(), p.ref(), io, p.lens, p, fmt, scale)
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("rows", ROWS)
+def test_small_scales_and_late_scores(gdn, rows, fmt, io):
+    """The smallest value scales, and scores that rise by 2^6, where the reference stays."""
+    p = Problem(gdn, [1200], [1], rows, 1, 64, 16, fmt, io, seed=50 + rows)
+    ids = p.tables[0].long()
+    p.q[:] = 1.0
+    p.kc.view(torch.uint8)[:] = at.encode(torch.ones(1), fmt).view(torch.uint8)
+    p.ks[ids, 0] = 0.0
+    p.ks[ids[8:], 0] = 4.2 / 64 ** 0.5  # 64 products of 1 and 1, scaled by 64^-1/2: 4.2 = 6 ln 2
+    p.vs[:] = 2.0 ** -100 / at.QMAX[fmt]
+    p.load()
+    check_range(*p.run(), p.ref(), io, p.lens, p, fmt)
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("rows", ROWS)
+def test_pages_of_zeros_among_others(gdn, rows, fmt, io):
+    """Pages of value scale 0 (their codes are not zeros here) first, last, and among pages of large
+    and of small scales: they take their share of the weights and give nothing."""
+    for lens in ([1000, 30], [5000, 16]):
+        p = Problem(gdn, lens, [1, 1], rows, 1, 64, 16, fmt, io, seed=60 + rows, std_q=0.3)
+        drawn = p.vs.clone()
+        for scale in (2.0 ** 60, 1.0, 2.0 ** -60):
+            for zeros in (slice(0, 20), slice(20, None), slice(0, None, 2), slice(1, None, 2)):
+                p.vs[:] = drawn * scale
+                p.vs[p.tables[0].long()[zeros]] = 0.0
+                p.load()
+                check_range(*p.run(), p.ref(), io, p.lens, p, fmt, (lens, scale, zeros))
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("rows", ROWS)
+def test_value_scales_far_apart(gdn, rows, fmt, io):
+    """Page scales spread over 2^90, in random, falling and rising order: the largest pages make the
+    output, every page its part of the sum."""
+    gen = torch.Generator().manual_seed(rows)
+    p = Problem(gdn, [9000, 700], [1, 1], rows, 1, 64, 32, fmt, io, seed=70 + rows)
+    drawn = p.vs.clone()
+    exponents = 90 * torch.rand(p.vs.shape, generator=gen) - 45
+    ids = p.tables[0].long()
+    for order in (None, True, False):
+        e = exponents.clone()
+        if order is not None:
+            e[ids] = exponents[ids].sort(0, descending=order).values
+        p.vs = drawn * torch.exp2(e)
+        p.load()
+        check_range(*p.run(), p.ref(), io, p.lens, p, fmt, order)
