@@ -20,8 +20,9 @@
 //   * Codes are exact in fp16: int8 by way of 1024 + u in an fp16's mantissa, e4m3 by the
 //     conversion instruction (its NaN codes, which only bytes past a length can hold, are taken out
 //     of the values there; a weight of 0 would not hide them).  Queries are scaled by a power of two
-//     per row into fp16's range: exact for bf16; fp32 ones are split into two fp16 parts, and the
-//     weights too, for fp32 accuracy.
+//     per row to the top of fp16's range (row_scale).  Weights are rounded to fp16, 2^-11 each, an
+//     eighth of what the output's rounding to bf16 costs; the weights' sum, which lse is made of,
+//     takes them in fp32.  fp32 queries and weights are split into two fp16 parts, 22 bits.
 //   * Softmax, one pass: the running maximum is of y = x log2 e + log2(value scale), so that the
 //     weights w = 2^(y - M) already carry their page's value scale and stay in fp16's range
 //     whatever the scales are; the sum takes w / value scale, on a reference of its own.  The
@@ -181,9 +182,8 @@ kv_attention_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
     load_k(pid, tile);
     load_v(pid, tile);
 
-    // queries: scaled by a power of two into [1, 2), fp16, in the order the products take them.  A
-    // thread has 16 dims of a row, 64 j + 16 cc on: lane (row % 8, cc)'s share of products 4 j ..
-    // 4 j + 3
+    // queries: scaled by a power of two, fp16, in the order the products take them.  A thread has 16
+    // dims of a row, 64 j + 16 cc on: lane (row % 8, cc)'s share of products 4 j .. 4 j + 3
 #pragma unroll 1
     for (int i = tid; i < ROWS * STEPS; i += kThreads) {
       const int row = i / STEPS, chunk = i % STEPS;
@@ -201,10 +201,9 @@ kv_attention_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
       // (the row's threads are neighbours; whole warps run here: ROWS STEPS is a multiple of 32)
 #pragma unroll
       for (int o = 1; o < STEPS; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      int ex = (int)((__float_as_uint(amax) >> 23) & 0xff);
-      ex = ex == 0 ? 127 : min(max(ex, 2), 252);
-      const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
-      if (chunk == 0) q_scale[row] = __uint_as_float((uint32_t)ex << 23) * (a.scale * kLog2e);
+      const RowScale rs = row_scale(amax);
+      const float down = rs.down;
+      if (chunk == 0) q_scale[row] = rs.up * (a.scale * kLog2e);
       uint4* at = reinterpret_cast<uint4*>(smem) +
                   ((row / 8) * (STEPS / 2) + 2 * (chunk / 4)) * 32 + 4 * (row % 8) + chunk % 4;
 #pragma unroll

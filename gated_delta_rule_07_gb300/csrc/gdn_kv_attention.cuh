@@ -206,6 +206,20 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
                                             *reinterpret_cast<const uint32_t*>(&y));
 }
 
+// A row of queries as fp16: times the power of two `down` that brings its largest magnitude into
+// [2^14, 2^15), and `up` = 1 / down.  fp16's smallest step is then 2^-38 of that magnitude: bf16
+// elements down to 2^-31 of it are exact, and smaller ones (or the second part of an fp32 one) are
+// off by 2^-39 of it at most.
+struct RowScale {
+  float down, up;
+};
+__device__ __forceinline__ RowScale row_scale(float amax) {
+  int ex = (int)((__float_as_uint(amax) >> 23) & 0xff);
+  ex = ex == 0 ? 127 : min(max(ex, 16), 254);  // (both factors normal numbers)
+  return RowScale{__uint_as_float((uint32_t)(254 + 14 - ex) << 23),
+                  __uint_as_float((uint32_t)(ex - 14) << 23)};
+}
+
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);

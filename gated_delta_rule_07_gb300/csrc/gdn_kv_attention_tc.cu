@@ -401,7 +401,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
       const int sw = warp - kOpenWarps, quarter = sw & 3, half = sw >> 2;
       const int tm_lane = 32 * quarter + lane, own = 2 * quarter + (lane >> 4), st = 32 * sw + lane;
       const uint32_t tm_q = tm + ((uint32_t)(quarter * 32) << 16), tm_o = tm_q + 128;
-      // queries: scaled by a power of two into [1, 2), fp16; a thread has 16 channels of a row
+      // queries: scaled by a power of two, fp16; a thread has 16 channels of a row
 #pragma unroll 1
       for (int i = st; i < ROWS * (D / 16); i += 32 * kSoftWarps) {
         const int row = i / (D / 16), chunk = i % (D / 16);
@@ -418,12 +418,11 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
 #pragma unroll
         for (int o = 1; o < D / 16; o <<= 1)
           amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        int ex = (int)((__float_as_uint(amax) >> 23) & 0xff);
-        ex = ex == 0 ? 127 : min(max(ex, 2), 252);
-        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);
+        const RowScale rs = row_scale(amax);
+        const float down = rs.down;
         if (chunk == 0) {
           // (a row that is not live has a reference that nothing exceeds: weights 0)
-          score_scale(row) = __uint_as_float((uint32_t)ex << 23) * (a.scale * kLog2e);
+          score_scale(row) = rs.up * (a.scale * kLog2e);
           minus_ref(row) = live ? -kNone : kNone;
           row_last[row] = live ? it.len - it.m + token0 + tk : -1;
         }

@@ -474,9 +474,12 @@ size_t gdn_kv_attention_workspace_size(const gdn_kv_cache* cache, const gdn_kv_p
  * a wait inside the kernel ran out (about a second; outputs are then undefined).  The same inputs
  * give the same bits.  Value scales may be as small or as large as an append writes them; those of
  * the pages that one row sees may differ by 2^100 (by 2^70 beside pages of scale 0, whose values are
- * zeros; scales below 2^-126 count as 0).  Products take fp16 operands with fp32 sums: codes are exact in fp16; bf16
- * queries are too, after a power of two per row; fp32 queries, and for them the weights, are split
- * into two fp16 parts. */
+ * zeros; scales below 2^-126 count as 0).  Products take fp16
+ * operands with fp32 sums.  Codes are exact in fp16.  Queries are scaled by a power of two per row:
+ * bf16 ones are exact down to 2^-31 of the row's largest magnitude, smaller ones off by at most 2^-39
+ * of it.  For bf16 the softmax's weights are rounded to fp16 for the product with the values (2^-11
+ * each; below 2^-22 of the row's largest weight, 2^-33 of that), not for their sum and lse.  For fp32
+ * queries and weights are split into two fp16 parts (22 bits, with the same least steps). */
 gdn_status gdn_kv_attention(const gdn_kv_cache* cache, const gdn_kv_problem* p, const void* q,
                             const int32_t* block_table, const int32_t* kv_lens,
                             const int32_t* cu_seqlens, float scale, int32_t window, void* out,

@@ -421,3 +421,17 @@ def test_value_scales_far_apart(gdn, rows, fmt, io):
         p.vs = drawn * torch.exp2(e)
         p.load()
         check_range(*p.run(), p.ref(), io, p.lens, p, fmt, order)
+
+
+@pytest.mark.parametrize("io", at.IOS, ids=at.IO_IDS)
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("rows", ROWS)
+def test_one_large_query_element(gdn, rows, fmt, io):
+    """A channel of the queries 2^20 times as large as the others, where the keys are zero: the
+    scores come from the others alone.  (An element off by 2^-39 of the largest is off by 2^-19 of
+    its own size here, below the score's rounding in the bounds above.)"""
+    p = Problem(gdn, [300, 17], [1, 1], rows, 1, 128, 32, fmt, io, seed=80 + rows)
+    p.q[:, :, 5] = 2.0 ** 20
+    p.kc.view(torch.uint8)[..., 5] = 0
+    p.load()
+    check(*p.run(), p.ref(), io)
