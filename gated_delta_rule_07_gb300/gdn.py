@@ -6,7 +6,9 @@ data pointers and the current torch stream, and raise ``GdnError`` on a non-OK s
 ``forward()`` is the convenience call that allocates the outputs and the workspace.
 
 Importing this module loads the library and raises ImportError when it has not been built
-(``python -m gated_delta_rule_07_gb300.build``); there is no fallback implementation.
+(``python -m gated_delta_rule_07_gb300.build``).  The softmax-attention layers' calls also need
+the torch binding beside it, which their first use loads, with the same ImportError; the recurrent
+calls do without.  There is no fallback implementation.
 """
 from __future__ import annotations
 
@@ -40,7 +42,17 @@ def _load_torch_binding():
     return mod
 
 
-_native = _load_torch_binding()
+class _Unloaded:
+    """Stands for the torch binding until a call of it is looked up."""
+
+    def __getattr__(self, name):
+        global _native
+        _native = _load_torch_binding()
+        _native.set_error(GdnError)
+        return getattr(_native, name)
+
+
+_native = _Unloaded()
 
 GDN_OK = 0
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
@@ -448,7 +460,6 @@ def gdn_device_status(status_word, reset=True, stream=None) -> int:
 # so its checks and allocations are made there.  What they refuse raises GdnError before any CUDA
 # work.
 
-_native.set_error(GdnError)
 _IO = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
 _KV_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
 _ROPE_STYLES = {"half": 0, "pairs": 1}

@@ -1,6 +1,10 @@
 """The softmax-attention layers' operators on the host: what they refuse (before any CUDA work, so
 without a GPU), and the fp64 forms that the GPU tests compare with."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -258,3 +262,24 @@ def test_strides_of_single_rows_do_not_count(gdn):
                       (dict(hkv=1), dict(hq=2, q_head_stride=7), False)):
         got = gdn.gdn_kv_attention_workspace_size(cache_desc(gdn, **c), kv_problem(gdn, **kw))
         assert (got > 0) == ok, kw
+
+
+def test_recurrent_calls_do_without_the_binding(gdn):
+    """A missing (or unloadable) torch binding leaves the module's other calls usable; the attention
+    layer's calls say what is missing."""
+    code = """
+import torch
+from gated_delta_rule_07_gb300 import build
+build.TORCH_LIB = {path!r}
+from gated_delta_rule_07_gb300 import gdn
+assert gdn.gdn_workspace_size(gdn.make_problem(64, 1, 1, 1, 128, 128)) > 0
+for _ in range(2):
+    try:
+        gdn.qk_norm_rope(torch.zeros(1, 1, 64), torch.zeros(1, 1, 64), None, None)
+        raise SystemExit("loaded")
+    except ImportError as e:
+        assert build.TORCH_LIB in str(e), e
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    for path in ("/nowhere/_gdn_torch.so", os.path.abspath(__file__)):
+        subprocess.run([sys.executable, "-c", code.format(path=path)], check=True, cwd=root)
