@@ -4,7 +4,8 @@ headers; it calls libgdn.so).
 
 Each .cu file is compiled in parallel to an object, then linked into
 ``gated_delta_rule_07_gb300/_build/libgdn.so``.  Rebuilds only when a source or header is
-newer than the library.  Usage: ``python -m gated_delta_rule_07_gb300.build [--force]``.
+newer than what was built of it, and the binding also when it was built for another torch or
+Python.  Usage: ``python -m gated_delta_rule_07_gb300.build [--force]``.
 """
 from __future__ import annotations
 
@@ -24,6 +25,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn.so")
 TORCH_SRC = os.path.join(CSRC, "gdn_torch.cpp")
 TORCH_LIB = os.path.join(BUILD, "_gdn_torch.so")
+TORCH_FOR = TORCH_LIB + ".for"  # the torch and Python that it was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,13 +49,32 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(TORCH_LIB):
+def _newer(built: str, deps: list) -> bool:
+    if not os.path.exists(built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
-    deps = [TORCH_SRC] + sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
-        os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    t = os.path.getmtime(built)
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _library_stale() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+        os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def torch_build() -> str:
+    """Which torch and Python a binding built now is for (torch itself is not imported)."""
+    where = os.path.dirname(importlib.util.find_spec("torch").origin)
+    with open(os.path.join(where, "version.py")) as f:
+        return f"{sysconfig.get_config_var('EXT_SUFFIX')}\n{where}\n{f.read()}"
+
+
+def _binding_stale() -> bool:
+    if _newer(TORCH_LIB, [TORCH_SRC, os.path.join(INCLUDE, "gdn.h")]):
+        return True
+    if not os.path.exists(TORCH_FOR):
+        return True
+    with open(TORCH_FOR) as f:
+        return f.read() != torch_build()
 
 
 def torch_binding_command(out: str) -> list:
@@ -75,7 +96,8 @@ def torch_binding_command(out: str) -> list:
 
 
 def build(force: bool = False, verbose: bool = False, extra: tuple = ()) -> str:
-    if not force and not _stale():
+    library, binding_too = force or _library_stale(), force or _binding_stale()
+    if not library and not binding_too:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -86,10 +108,11 @@ def build(force: bool = False, verbose: bool = False, extra: tuple = ()) -> str:
     procs, objs = [], []
     binding = TORCH_LIB + f".tmp{os.getpid()}"
     # (its references to libgdn.so are resolved when it is loaded, after that library)
-    procs.append((TORCH_SRC, subprocess.Popen(torch_binding_command(binding),
-                                              stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
-                                              text=True)))
-    for src in sources():
+    if binding_too:
+        procs.append((TORCH_SRC, subprocess.Popen(torch_binding_command(binding),
+                                                  stdout=subprocess.PIPE, stderr=subprocess.STDOUT,
+                                                  text=True)))
+    for src in sources() if library else ():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
         objs.append(obj)
         procs.append((src, subprocess.Popen([cc, *common, "-c", src, "-o", obj],
@@ -103,13 +126,18 @@ def build(force: bool = False, verbose: bool = False, extra: tuple = ()) -> str:
         if p.returncode:
             errors.append(src)
     if errors:
-        raise RuntimeError(f"nvcc failed for {errors}")
+        raise RuntimeError(f"compiling failed for {errors}")
+    if binding_too:
+        os.replace(binding, TORCH_LIB)
+        with open(TORCH_FOR, "w") as f:
+            f.write(torch_build())
+    if not library:
+        return LIB
     tmp = LIB + f".tmp{os.getpid()}"
     libdir = cuda_lib_dir()
     subprocess.run([cc, "-shared", *ARCH, "-cudart", "shared", "-o", tmp, *objs,
                     f"-L{libdir}", f"-Xlinker", f"-rpath={libdir}"], check=True)
     os.replace(tmp, LIB)
-    os.replace(binding, TORCH_LIB)
     return LIB
 
 

@@ -283,3 +283,17 @@ for _ in range(2):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     for path in ("/nowhere/_gdn_torch.so", os.path.abspath(__file__)):
         subprocess.run([sys.executable, "-c", code.format(path=path)], check=True, cwd=root)
+
+
+def test_binding_of_another_torch_is_stale(gdn, monkeypatch, tmp_path):
+    """A binding is built again for another torch or Python, whatever the sources' times."""
+    from gated_delta_rule_07_gb300 import build
+    assert not build._binding_stale() and not build._library_stale()
+    with open(build.TORCH_FOR) as f:
+        assert f.read() == build.torch_build() and torch.__version__ in build.torch_build()
+    other = tmp_path / "for"
+    other.write_text(build.torch_build().replace(torch.__version__, "1.0"))
+    monkeypatch.setattr(build, "TORCH_FOR", str(other))
+    assert build._binding_stale() and not build._library_stale()
+    monkeypatch.setattr(build, "TORCH_FOR", str(tmp_path / "none"))
+    assert build._binding_stale()
