@@ -84,3 +84,113 @@ def test_single_rows_of_any_stride(gdn, T, heads, io):
         outs.append([*gdn.kv_read(cache, table, None, None, T),
                      *gdn.kv_attention(cache, f(q), table, held + T, check_status=True)])
     assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def rope_args():
+    T, D = 5, 64
+    return dict(q=zeros(T, 4, D), k=zeros(T, 2, D), positions=ints(T),
+                cos_sin=zeros(8, 32, dtype=torch.float32),
+                q_weight=zeros(D, dtype=torch.float32), k_weight=zeros(D, dtype=torch.float32))
+
+
+def skewed(t):
+    """The same values with another order of strides."""
+    return t.transpose(0, -1).contiguous().transpose(0, -1)
+
+
+ROPE_CHANGES = [
+    ("q", lambda t: t.float(), 1, "k is"), ("q", lambda t: t.half(), 2, "dtype"),
+    ("q", lambda t: t[0], 1, "q is"), ("q", skewed, 1, "last dimension"),
+    ("q", lambda t: t[:4], 1, "go together"), ("q", lambda t: t.cpu(), 1, "q is"),
+    ("k", lambda t: t.float(), 1, "k is"), ("k", lambda t: t[:4], 1, "go together"),
+    ("k", lambda t: t[..., :32], 1, "go together"), ("k", lambda t: t.cpu(), 1, "k is"),
+    ("k", lambda t: None, 1, "k is to be a tensor"),
+    ("positions", lambda t: t.long(), 1, "positions"), ("positions", lambda t: t[:4], 1, "positions"),
+    ("positions", lambda t: t.cpu(), 1, "positions"),
+    ("positions", lambda t: ints(10)[::2], 1, "positions"),
+    ("cos_sin", lambda t: t.double(), 1, "cos_sin"), ("cos_sin", lambda t: t[0], 1, "cos_sin"),
+    ("cos_sin", skewed, 1, "cos_sin"), ("cos_sin", lambda t: t.cpu(), 1, "cos_sin"),
+    ("q_weight", lambda t: t[:32], 1, "q_weight"), ("k_weight", lambda t: t.bfloat16(), 1, "k_weight"),
+    ("k_weight", lambda t: t.cpu(), 1, "k_weight"),
+]
+
+
+@pytest.mark.parametrize("name,change,status,word", ROPE_CHANGES)
+def test_norms_refuse(gdn, name, change, status, word):
+    kw = rope_args()
+    kw[name] = change(kw[name])
+    refused(gdn, gdn.qk_norm_rope, kw, status, word)
+    kw.update(dq_out=zeros(5, 4, 64), dk_out=zeros(5, 2, 64))
+    refused(gdn, gdn.qk_norm_rope_backward, kw, status, word)
+
+
+@pytest.mark.parametrize("name,change,status,word", [
+    ("dq_out", lambda t: t.float(), 1, "dq_out"), ("dq_out", lambda t: t[:4], 1, "dq_out"),
+    ("dk_out", lambda t: zeros(5, 4, 64), 1, "dk_out"), ("dk_out", skewed, 1, "dk_out"),
+    ("dk_out", lambda t: t.cpu(), 1, "dk_out"),
+    ("dq_out", lambda t: t[:, :1].expand(5, 4, 64), 1, "dq_out"),
+    ("workspace", lambda t: zeros(16), 3, "qk_norm_rope_backward"),
+    ("workspace", lambda t: torch.zeros(1 << 20), 1, "workspace"),
+    ("workspace", lambda t: zeros(1 << 20, 2)[:, 0], 1, "workspace")])
+def test_gradients_refuse(gdn, name, change, status, word):
+    kw = dict(rope_args(), dq_out=zeros(5, 4, 64), dk_out=zeros(5, 2, 64))
+    kw[name] = change(kw.get(name))
+    refused(gdn, gdn.qk_norm_rope_backward, kw, status, word)
+
+
+KV_CHANGES = [
+    ("kv_append", "k", lambda t: t.half(), 2, "dtype"), ("kv_append", "k", lambda t: t.float(), 1, "v is"),
+    ("kv_append", "k", lambda t: t[:, :1], 1, "k does not fit"),
+    ("kv_append", "v", lambda t: t[..., :32], 1, "v does not fit"),
+    ("kv_append", "v", lambda t: t[:3], 1, "numbers of tokens"),
+    ("kv_append", "v", lambda t: t.cpu(), 1, "v is"), ("kv_append", "v", lambda t: t.float(), 1, "v is"),
+    ("kv_append", "ctx_lens", lambda t: t.long(), 1, "lengths"),
+    ("kv_append", "ctx_lens", lambda t: ints(3), 1, "lengths"),
+    ("kv_append", "ctx_lens", lambda t: None, 1, "kv_append"),
+    ("kv_append", "cu_seqlens", lambda t: ints(2), 1, "cu_seqlens"),
+    ("kv_append", "cu_seqlens", lambda t: None, 1, "kv_append"),   # four rows of two sequences
+    ("kv_append", "block_table", skewed, 1, "block_table"),
+    ("kv_append", "block_table", lambda t: t[0], 1, "block_table"),
+    ("kv_read", "block_table", lambda t: t.long(), 1, "block_table"),
+    ("kv_read", "block_table", lambda t: t.cpu(), 1, "block_table"),
+    ("kv_read", "start", lambda t: ints(1), 1, "lengths"),
+    ("kv_read", "cu_seqlens", lambda t: t.cpu(), 1, "cu_seqlens"),
+    ("kv_read", "tokens", lambda t: -1, 1, "kv_read"),
+    ("kv_attention", "q", lambda t: t[..., :32], 1, "q does not fit"),
+    ("kv_attention", "q", lambda t: t[:, :5], 1, "kv_attention"),      # five heads over two
+    ("kv_attention", "q", lambda t: t.half(), 2, "dtype"), ("kv_attention", "q", skewed, 1, "q is"),
+    ("kv_attention", "q", lambda t: t.cpu(), 1, "q is"),
+    ("kv_attention", "kv_lens", lambda t: t.float(), 1, "lengths"),
+    ("kv_attention", "kv_lens", lambda t: ints(1), 1, "lengths"),
+    ("kv_attention", "kv_lens", lambda t: None, 1, "kv_attention"),
+    ("kv_attention", "cu_seqlens", lambda t: ints(4), 1, "cu_seqlens"),
+    ("kv_attention", "block_table", lambda t: ints(2, 6)[:, ::2], 1, "block_table"),
+    ("kv_attention", "window", lambda t: -1, 1, "window"),
+    ("kv_attention", "window", lambda t: 1 << 31, 1, "window"),
+    ("kv_attention", "workspace", lambda t: zeros(16), 3, "kv_attention"),
+    ("kv_attention", "workspace", lambda t: torch.zeros(1 << 26), 1, "workspace"),
+]
+
+
+@pytest.mark.parametrize("call,name,change,status,word", KV_CHANGES)
+def test_cache_calls_refuse(gdn, call, name, change, status, word):
+    kw = kv_calls(gdn, gdn.KVCache.empty(4, 2, 16, 64))[call]
+    kw[name] = change(kw.get(name))
+    refused(gdn, getattr(gdn, call), kw, status, word)
+
+
+@pytest.mark.parametrize("i,change,status,word", [
+    (0, lambda t: t.to(torch.uint8), 2, "dtype"), (0, lambda t: t[0], 1, "k is to be"),
+    (0, lambda t: zeros(2, 1, 16, 128, dtype=torch.int8)[..., ::2], 1, "k is"),
+    (1, lambda t: t.view(2, 1, 16, 64), 1, "v is"),
+    (1, lambda t: t.view(torch.float8_e4m3fn), 1, "v is"), (1, lambda t: t.cpu(), 1, "v is"),
+    (2, lambda t: t.double(), 1, "k_scale"), (2, lambda t: t[:1], 1, "k_scale"),
+    (3, lambda t: t[0], 1, "v_scale"), (3, lambda t: t.cpu(), 1, "v_scale")])
+def test_cache_buffers_refused(gdn, i, change, status, word):
+    buffers = [zeros(2, 1, 16, 64, dtype=torch.int8), zeros(2, 1, 4, 64, 4, dtype=torch.int8),
+               zeros(2, 1, dtype=torch.float32), zeros(2, 1, dtype=torch.float32)]
+    gdn.KVCache(*buffers)
+    buffers[i] = change(buffers[i])
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.KVCache(*buffers)
+    assert e.value.status == status and word in str(e.value)
