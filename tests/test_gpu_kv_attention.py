@@ -435,3 +435,163 @@ def test_one_large_query_element(gdn, rows, fmt, io):
     p.kc.view(torch.uint8)[..., 5] = 0
     p.load()
     check(*p.run(), p.ref(), io)
+
+
+# The many-row kernel's own code for what the tests above show of the other: MANY are rows of a kv
+# head that take it, with items of 32 and of 64 rows.
+MANY = ROWS[1:]
+
+
+def kernels_of(call):
+    """Names of the kernels that call() launches."""
+    act = torch.profiler.ProfilerActivity
+    names = []
+    for _ in range(2):  # (the first profile of a process may come back empty)
+        with torch.profiler.profile(activities=[act.CPU, act.CUDA]) as prof:
+            call()
+            torch.cuda.synchronize()
+        names = [e.name for e in prof.events()]
+    return names
+
+
+def test_which_kernel_runs(gdn):
+    """ROWS reach the kernels that their comment says."""
+    for io in at.IOS:
+        for rows in ROWS:
+            p = Problem(gdn, [100], [1], rows, 1, 128, 32, torch.int8, io)
+            names = " ".join(kernels_of(p.run))
+            many = io == torch.bfloat16 and rows in MANY
+            assert ("kv_attention_tc_kernel" in names) == many, (io, rows, names)
+            assert ("kv_attention_kernel" in names) == (not many), (io, rows, names)
+            if many:
+                size = {24: "32>", 40: "64>"}[rows]
+                assert f"kv_attention_tc_kernel<128, false, {size}" in names, names
+
+
+@pytest.mark.parametrize("fmt", at.FORMATS, ids=at.FORMAT_IDS)
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows_scales_of_very_different_pages(gdn, rows, fmt):
+    """As test_scales_of_very_different_pages, for the many-row kernel."""
+    p = Problem(gdn, [16 * 6, 16 * 9 + 3], [1, 1], rows, 1, 128, 16, fmt, torch.bfloat16, seed=8,
+                std_q=0.3)
+    for n in (0, 1):
+        ids = p.tables[n].long()
+        p.vs[ids[:6], 0] *= torch.tensor([1.0, 2.0 ** -40, 2.0 ** 40, 2.0 ** -14, 0.0, 1.0])
+        p.ks[ids[:6], 0] *= torch.tensor([1.0, 64.0, 0.01, 1.0, 1.0, 0.0])
+    p.load()
+    check_range(*p.run(), p.ref(), torch.bfloat16, p.lens, p, fmt)
+
+
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows_repeat_bit_for_bit(gdn, rows):
+    """Items cut between CTAs and several items a CTA, again and on another stream."""
+    for lens in ([9000, 3, 1200], [70, 300, 5] * 100):
+        p = Problem(gdn, lens, [1] * len(lens), 2 * rows, 2, 128, 64, torch.int8, torch.bfloat16)
+        want = p.run()
+        check(*want, p.ref(), torch.bfloat16)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        for kw in ({}, {}, {"stream": s}):
+            got = p.run(**kw)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows_of_many_sequences(gdn, rows):
+    """More sequences than the many-row kernel has threads, some without rows, some without keys."""
+    gen = torch.Generator().manual_seed(rows)
+    lens = [int(x) for x in torch.randint(0, 200, (1300,), generator=gen)]
+    new = [int(x) for x in torch.randint(0, 3, (1300,), generator=gen)]
+    new[0] = 5
+    p = Problem(gdn, lens, new, rows, 1, 64, 16, torch.int8, torch.bfloat16, seed=rows)
+    check(*p.run(), p.ref(), torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows_bad_lengths_and_pages(gdn, rows):
+    """As test_bad_lengths_and_pages_are_reported, for the many-row kernel: the keys of a page outside
+    the pool are left out, the row's other keys count."""
+    p = Problem(gdn, [40, 340, 40], [1, 1, 1], rows, 1, 64, 16, torch.int8, torch.bfloat16, seed=14)
+    ref = p.ref()
+    p.lens = [40, 401, 40]          # past the table's 22 pages
+    with pytest.raises(gdn.GdnError) as e:
+        p.run()
+    assert e.value.status == 6
+    got = p.run(check_status=False)
+    for i in (0, 2):
+        check(got[0][i:i + 1], got[1][i:i + 1], tuple(x[i:i + 1] for x in ref), torch.bfloat16)
+    p.lens = [40, 340, 40]
+    for bad in (p.ks.shape[0], -7, 2 ** 31 - 1):
+        tables = p.tables.clone()
+        p.tables[1, 3] = bad
+        with pytest.raises(gdn.GdnError) as e:
+            p.run()
+        assert e.value.status == 6
+        got = p.run(check_status=False)
+        p.tables = tables
+        for i in (0, 2):
+            check(got[0][i:i + 1], got[1][i:i + 1], tuple(x[i:i + 1] for x in ref), torch.bfloat16)
+        # the same sequence without the sixteen keys of that page
+        less = Problem(gdn, [324], [1], rows, 1, 64, 16, torch.int8, torch.bfloat16)
+        less.tables = torch.cat([tables[1, :3], tables[1, 4:]])[None]
+        less.q, less.kc, less.ks, less.vc, less.vs = p.q[1:2], p.kc, p.ks, p.vc, p.vs
+        check(got[0][1:2], got[1][1:2], less.ref(), torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows_large_and_small_queries(gdn, rows):
+    p = Problem(gdn, [70, 300, 70], [1, 1, 1], rows, 1, 128, 32, torch.int8, torch.bfloat16, seed=10)
+    p.q[0] *= 2.0 ** 60
+    check(*(x[:1] for x in p.run(scale=2.0 ** -62)),
+          tuple(x[:1] for x in p.ref(scale=2.0 ** -62)), torch.bfloat16)
+    p.q[0], p.q[1] = 0, p.q[1] * 2.0 ** -40
+    check(*p.run(), p.ref(), torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows_one_workspace_for_many_calls(gdn, rows):
+    p = Problem(gdn, [5000, 100], [1, 1], rows, 1, 128, 64, torch.int8, torch.bfloat16, seed=20)
+    o = Problem(gdn, [50, 4000], [1, 1], rows, 1, 128, 64, torch.int8, torch.bfloat16, seed=21)
+    want, other = p.run(), o.run()
+    check(*want, p.ref(), torch.bfloat16)
+    ws = torch.full((128 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        assert torch.equal(p.run(workspace=ws)[0], want[0])
+        assert torch.equal(o.run(workspace=ws)[0], other[0])
+
+
+def test_many_rows_offsets_past_32_bits(gdn):
+    page, hkv, D = 128, 8, 128
+    pages = (1 << 32) // (page * hkv * D) + 3
+    p = Problem(gdn, [300], [1], 24 * hkv, hkv, D, page, torch.int8, torch.bfloat16, seed=22)
+    want = p.run()
+    check(*want, p.ref(), torch.bfloat16)
+    ids = p.tables[0].long()
+    big = gdn.KVCache.empty(pages, hkv, page, D)
+    far = torch.tensor([pages - 1, 0, pages - 2])
+    big.k[far.cuda()], big.v[far.cuda()] = p.cache.k[ids.cuda()], p.cache.v[ids.cuda()]
+    big.k_scale[far.cuda()] = p.cache.k_scale[ids.cuda()]
+    big.v_scale[far.cuda()] = p.cache.v_scale[ids.cuda()]
+    p.cache, p.tables = big, far.int()[None]
+    got = p.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("rows", MANY)
+def test_many_rows_graph_capture(gdn, rows):
+    p = Problem(gdn, [600, 40], [1, 1], rows, 1, 128, 64, torch.int8, torch.bfloat16, seed=23)
+    q, tables = p.q.cuda(), p.tables.cuda()
+    lens = torch.tensor(p.lens, dtype=torch.int32).cuda()
+    ws = gdn.kv_attention_workspace(p.cache, q, tables)
+    gdn.kv_attention(p.cache, q, tables, lens, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = gdn.kv_attention(p.cache, q, tables, lens, workspace=ws)
+    for new_lens in ([600, 40], [1, 33], [311, 0]):
+        lens.copy_(torch.tensor(new_lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        p.lens = new_lens
+        check(out, lse, p.ref(), torch.bfloat16, new_lens)
