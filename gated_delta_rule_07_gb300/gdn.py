@@ -202,13 +202,17 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _side_stream(stream):
-    """A torch stream for what a call was given: one of torch's, or an integer handle."""
-    if hasattr(stream, "cuda_stream"):
-        return stream
-    # (0 and 1 are CUDA's names of the legacy default stream)
-    return torch.cuda.default_stream() if int(stream) in (0, 1) else torch.cuda.ExternalStream(
-        int(stream))
+def _side_stream(stream, inputs):
+    """A torch stream for what a call was given (one of torch's, or an integer handle), on the GPU of
+    the call's tensors."""
+    gpu = next((t.device for t in inputs if getattr(t, "is_cuda", False)), None)
+    if not hasattr(stream, "cuda_stream"):
+        # (0 and 1 are CUDA's names of the legacy default stream)
+        return torch.cuda.default_stream(gpu) if int(stream) in (0, 1) else (
+            torch.cuda.ExternalStream(int(stream), device=gpu))
+    if gpu is not None and stream.device != gpu:
+        raise GdnError(1, f"the stream is on {stream.device}, the tensors on {gpu}")
+    return stream
 
 
 def _on(stream, call, *inputs):
@@ -216,7 +220,7 @@ def _on(stream, call, *inputs):
     launches is ordered on it.  The allocator learns that the inputs are used there and that the
     outputs will be used on the caller's stream: no memory is handed out again before the work that
     uses it is done.  Ordering the streams themselves (inputs written, outputs read) is the caller's."""
-    side = _side_stream(stream)
+    side = _side_stream(stream, inputs)
     with torch.cuda.stream(side):
         result = call()
     here = torch.cuda.current_stream(side.device)

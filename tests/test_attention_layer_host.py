@@ -297,3 +297,14 @@ def test_binding_of_another_torch_is_stale(gdn, monkeypatch, tmp_path):
     assert build._binding_stale() and not build._library_stale()
     monkeypatch.setattr(build, "TORCH_FOR", str(tmp_path / "none"))
     assert build._binding_stale()
+
+
+def test_stream_of_another_gpu_is_refused(gdn):
+    """A stream that torch would leave aside, because the tensors are on another GPU."""
+    class Stream:
+        cuda_stream, device = FAKE, torch.device("cuda", 1)
+    on = OnGpu((2, 2), torch.float32, 1)
+    assert gdn._side_stream(Stream, (None, on)) is Stream
+    with pytest.raises(gdn.GdnError) as e:
+        gdn._side_stream(Stream, (None, OnGpu((2, 2), torch.float32, 0), on))
+    assert e.value.status == 1 and "cuda:1" in str(e.value) and "cuda:0" in str(e.value)
