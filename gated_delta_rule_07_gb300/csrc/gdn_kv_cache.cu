@@ -22,6 +22,7 @@
 // of 256, in 4.8 us, their last pages read back in 5.9 us.
 #include <cuda_fp16.h>
 
+#include "gdn_elements.cuh"
 #include "gdn_kv.cuh"
 
 namespace gdn {
@@ -31,31 +32,6 @@ constexpr int kKvThreads = 256;
 
 // ------------------------------------------------------------------------- elements and codes
 
-template <typename IO> struct Quad;  // four consecutive elements as loaded
-template <> struct Quad<float> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
-  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void open(float* f) const {
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-  }
-  __device__ __forceinline__ void close(const float* f) { v = make_float4(f[0], f[1], f[2], f[3]); }
-};
-template <> struct Quad<__nv_bfloat16> {
-  uint2 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    v = __ldg(reinterpret_cast<const uint2*>(p));
-  }
-  __device__ __forceinline__ void clear() { v = make_uint2(0u, 0u); }
-  __device__ __forceinline__ void open(float* f) const {  // a bf16 is the top half of an fp32
-    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
-  __device__ __forceinline__ void close(const float* f) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-    v = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  }
-};
 // eight: one 16-byte load of bf16, two of fp32
 template <typename IO>
 __device__ __forceinline__ void load8(Quad<IO>* q, const IO* p) {
@@ -386,17 +362,6 @@ __device__ __forceinline__ void decode4(uint32_t w, float scale, float* f) {
       f[i] = (__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7440 + i)) - 8388736.f) * scale;
   }
 }
-__device__ __forceinline__ void put4(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ uint2 bf16x4(const float* f) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-}
-__device__ __forceinline__ void put4(__nv_bfloat16* p, const float* f) {
-  *reinterpret_cast<uint2*>(p) = bf16x4(f);
-}
-
 constexpr int kReadUnroll = 4;  // loads a thread has in flight
 
 // Blocks: (slot, group of `per` heads).  The group's keys and values are cut into runs of

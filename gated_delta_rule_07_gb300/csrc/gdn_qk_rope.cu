@@ -26,6 +26,7 @@
 
 #include "gdn_attention.h"
 #include "gdn_common.cuh"
+#include "gdn_elements.cuh"
 #include "gdn_stream_order.cuh"
 
 namespace gdn {
@@ -33,38 +34,6 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kVec = 8;  // elements a lane holds of a row
-
-// four consecutive elements as loaded
-template <typename IO> struct Quad;
-template <> struct Quad<float> {
-  float4 v;
-  __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
-  __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void open(float* f) const {
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
-  }
-};
-template <> struct Quad<__nv_bfloat16> {
-  uint2 v;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    v = __ldg(reinterpret_cast<const uint2*>(p));
-  }
-  __device__ __forceinline__ void clear() { v = make_uint2(0u, 0u); }
-  __device__ __forceinline__ void open(float* f) const {  // a bf16 is the top half of an fp32
-    f[0] = __uint_as_float(v.x << 16); f[1] = __uint_as_float(v.x & 0xffff0000u);
-    f[2] = __uint_as_float(v.y << 16); f[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
-};
-__device__ __forceinline__ void put4(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ uint2 bf16x4(const float* f) {
-  const __nv_bfloat162 x = __floats2bfloat162_rn(f[0], f[1]), y = __floats2bfloat162_rn(f[2], f[3]);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-}
-__device__ __forceinline__ void put4(__nv_bfloat16* p, const float* f) {
-  *reinterpret_cast<uint2*>(p) = bf16x4(f);
-}
 
 // A lane's place in a row of the forward: where its two groups of four begin.
 struct Place {
