@@ -33,15 +33,17 @@
 //     warps take its run's units in turn and join at the end of each item; items cut between CTAs
 //     leave partial sums (M, sum, unnormalised o), joined in order by a second small kernel.
 //
-// Measured (GB300, device time; share of a copy's 6.80 TB/s): 64 sequences of up to 65536 keys, 4 kv
-// heads of 128, 8 rows: int8 579 us (95%), e4m3 553 us (the conversion is one instruction; opened
-// by shifts it was 726); 16 x 32768 keys 79 us (84%); fp32 I/O, 16 x 30000 keys, 84 us (71%: twice
-// the products); 16 x 30000 keys, heads of 256, 8 rows 71 us (83%), 16 rows 53 us for half the bytes
-// (56%: registers leave two CTAs an SM); heads of 64 in pages of 16, 16 x 60000 keys, 93 us (64%: a
-// warp's tile of 16 keys is 2 KB, so the softmax's instructions weigh twice as much a byte).  One sequence of 1500 keys takes 9.3 us and 32
-// ragged ones of up to 8192 18.7 us: launch, plan, an item's start and end, and the join are about
-// 9 us of either.  A deeper ring of tiles in shared memory was slower (64 x 65536: 825 us, at any
-// depth): its copies take more issue than the loads here.
+// Measured (GB300, device time; share of a copy's 6.80 TB/s), eight query heads a kv head unless said
+// otherwise: 64 sequences of up to 65536 keys, 4 kv heads of 128: int8 585 us (94%), e4m3 563 us (98%:
+// the conversion is one instruction; opened by shifts it was 726); 16 x 32768 keys 79 us (83%); fp32
+// I/O, 16 x 30000 keys, 80 us (74%: twice the products, tensor pipe 29% busy, and 125 registers leave
+// sixteen warps an SM to wait for the loads); 16 x 30000 keys, heads of 256, 8 rows 72 us (83%), 16
+// rows 54 us for half the bytes (55%: registers leave two CTAs an SM); heads of 64 in pages of 16, 16 x
+// 60000 keys, 82 us (72%: a warp's tile of 16 keys is 2 KB, so the softmax's instructions weigh twice
+// as much a byte).  One sequence of 1500 keys takes 9.5 us and 32 ragged ones of up to 8192 19.1 us:
+// launch, plan, an item's start and end, and the join are about 9 us of either.  A deeper ring of tiles
+// in shared memory was slower (64 x 65536: 825 us, at any depth): its copies take more issue than the
+// loads here.
 #include "gdn_kv_attention.cuh"
 
 namespace gdn {
@@ -49,11 +51,11 @@ namespace {
 
 constexpr int kWarps = kAttWarps, kThreads = kAttThreads;
 constexpr int kTile = 16;      // keys of a unit
-// Units of a CTA at least: one sequence of 1500 keys takes 9.3 us with 8, 11.4 with 16, 15.7 with 32;
-// with 4 it takes 8.5, but one of 8000 keys 14.1 us against 11.7 (more parts to join).
+// Units of a CTA at least: one sequence of 1500 keys takes 9.5 us with 8, 11.9 with 16, 16.3 with 32;
+// with 4 it takes 8.7, but one of 8000 keys 12.7 us against 11.0 (more parts to join).
 constexpr int kMinUnits = 8;
 // Units that starting an item is worth (queries, joining warps): 32 ragged sequences of up to 8192
-// keys take 18.7 us with 8, 19.7 with 16, 41.3 with 1.
+// keys take 19.2 us with 8, 19.9 with 16, 42.6 with 1.
 constexpr int kItemUnits = 8;
 
 // ---------------------------------------------------------------------------------- operands
@@ -82,9 +84,9 @@ template <int D, int NT, bool SPLIT> struct Shape {
   static constexpr int o_bytes = kWarps * rows * pad * 4;
   static constexpr int smem = q_bytes > o_bytes ? q_bytes : o_bytes;
   // Registers decide the resident CTAs: the sums alone are D NT / 4 of them.  Heads of 64 have small
-  // tiles and need more warps for as many bytes on their way: 16 x 60000 keys, bf16, 92.8 us with
-  // six CTAs an SM (75 registers), 99.1 with five, 102.7 with four; fp32 (with spills at six), 16 x
-  // 30000: 58.5, 57.6, 59.9.  Heads of 128 spill with five: 64 x 65536 keys 759 us, 583 with four.
+  // tiles and need more warps for as many bytes on their way: 16 x 60000 keys, bf16, 82.6 us with
+  // six CTAs an SM, 90.4 with five or four; fp32 (with spills at six), 16 x 30000: 54.1, 53.5, 56.5.
+  // Heads of 128 spill with five: 64 x 65536 keys 782 us, 585 with four.
   static constexpr int ctas =
       D * NT <= 64 ? (SPLIT ? 5 : 6) : D * NT <= 128 ? 4 : D * NT <= 256 ? 3 : 2;
 };
@@ -499,15 +501,16 @@ kv_attention_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
 int64_t average_rows(const KvArgs& a) { return (a.T + a.N - 1) / a.N * a.group; }
 
 // More than sixteen rows: the tcgen05 kernel, where it is built.  int8, 4 kv heads of 128: 24
-// sequences of 20000 keys with 8 .. 40 rows take 123 us there and 158 here, with 8 .. 64 rows 152 and
-// 248, but with 8 or 16 rows 109 and 107; 16 x 20000 keys with 16 rows 74 and 69; one sequence of
-// 1500 keys with 16 rows 12.6 and 8.9.
+// sequences of 20000 keys with 8 .. 40 rows take 124 us there and 160 here, with 8 .. 64 rows 153 and
+// 250, but with 8 or 16 rows 111 and 108; 16 x 20000 keys with 16 rows 75 and 69; one sequence of
+// 1500 keys with 16 rows 13.0 and 9.4.  Heads of 64 gain less: 24 x 20000 keys with 8 .. 40 rows take 99
+// us there and 106 here, 40 ragged sequences of up to 9000 keys with 8 .. 24 rows 29 and 23.
 bool use_tc(const KvArgs& a) { return a.bf16 && a.D <= 128 && average_rows(a) > 16; }
 
 // Tiles of 8 rows a warp carries: as many as the average sequence's rows fill (a row tile more
 // reads the cache once more), within the registers (D NT <= 512).  16 x 30000 keys, 4 kv heads of
-// 128, fp32: 8 rows take 84 us with one tile (two: 118); 16 rows 112 with two (one: 154, four: 206);
-// 32 rows 189 with four (two: 211).
+// 128, fp32: 8 rows take 80 us with one tile (two: 121); 16 rows 115 with two (one: 147, four: 210);
+// 32 rows 194 with four (two: 216).
 int row_tiles(const KvArgs& a) {
   const int64_t rows = average_rows(a);
   return rows <= 8 ? 1 : rows <= 16 || a.D == 256 ? 2 : 4;

@@ -372,16 +372,16 @@ template <typename W> int grid_ctas(const KvArgs& a, int resident, int min_units
 template <typename IO, int D, int ROWS>
 cudaError_t launch_join(const KvArgs& a, const Workspace& ws, int ctas, cudaStream_t s) {
   // Few long items: a block for each CTA would mostly find nothing to join, and setting those up
-  // takes time (one sequence of 60000 keys, 2 kv heads: 26.2 us with a block a CTA, 19.7 with four
-  // an item; 32 sequences of up to 8192 keys, 8 kv heads: 18.9 with a block a CTA, 20.2 with one
-  // an item).
+  // takes time (one sequence of 60000 keys, 2 kv heads: 27.1 us with a block a CTA, 19.8 with four
+  // an item; 32 sequences of up to 8192 keys, 8 kv heads: 19.1 with a block a CTA, 20.7 with four an
+  // item).
   const int64_t items = (int64_t)a.N * a.hkv, parts = ctas / items;
   const bool few = 4 * items < ctas;
   // An item has about `parts` partials where the sequences are alike, several times as many where
   // some are longer: four groups of threads for each and more from 16 partials on, so that a thread
-  // takes a few.  Those 32 sequences take 18.9 us so, 21.9 with one group, 19.6 with groups for
-  // every partial.  Where most items have none (256 sequences of up to 500 keys) more groups only
-  // cost blocks: 19.2 us with four, 18.3 with one.
+  // takes a few.  Those 32 sequences take 19.1 us so, 21.8 with one group; four of 9000 keys and 24
+  // rows 17.9, and 21.5 with groups for every partial.  Where most items have none (256 sequences of up
+  // to 500 keys) more groups only cost blocks: 28.5 us with four, 27.6 with one.
   constexpr int all_cols = ROWS * (D / 4);
   int groups = all_cols < kJoinThreads ? kJoinThreads / all_cols : 1;
   while (groups < (few ? 64 : 16) && ((parts > 0 && groups < 4) || 4 * groups < parts)) groups *= 2;

@@ -26,9 +26,9 @@
 // the products, weights, queries: about 1350 cycles).  It takes about 2100: the opening warps wait
 // some 650 of them for codes that were asked for a step ahead (a second step ahead does not fit 96
 // registers a thread), and the products' issue takes 950, mostly for shared memory.
-// Measured (GB300): 24 sequences of up to 20000 keys, 4 kv heads of 128, 8 .. 40 rows: 123 us (51% of
-// the copy's rate; tensor pipe 20% busy); 8 .. 64 rows 152 us; heads of 64, 98 us.  Bringing codes to
-// L2 four steps ahead made these 119, 166 and 101 us: left out.
+// Measured (GB300): 24 sequences of up to 20000 keys, 4 kv heads of 128, 8 .. 40 rows: 124 us (51% of
+// the copy's rate; tensor pipe 21% busy; e4m3 122); 8 .. 64 rows 153 us; heads of 64, 99 us.  Bringing
+// codes to L2 four steps ahead made 123, 152 and 98 us of an earlier form 119, 166 and 101: left out.
 #include "gdn_kv_attention.cuh"
 #include "gdn_sm100.cuh"
 
@@ -43,8 +43,8 @@ constexpr int kAhead = 8;        // steps whose pages are known at a time
 constexpr int kCols = 64;        // columns of S^T and O^T: an item's query rows, at most
 constexpr int kKeys = 128;       // keys of a step, lanes of S^T
 constexpr int kTcMinUnits = 2;   // steps of a CTA at least (4 x 9000 keys: 1 to 4 within 5%)
-// Steps that starting an item is worth: 40 ragged sequences of up to 9000 keys, 24 rows, take 28.3 us
-// with 5, 33.8 with 3, 29.6 with 7; 24 x 20000 keys 123 to 124 us with any of them.
+// Steps that starting an item is worth: 40 ragged sequences of up to 9000 keys, 8 .. 24 rows, heads
+// of 64, take 29.5 us with 5, 35.5 with 3, 29.8 with 7; 24 x 20000 keys 124 us with any of them.
 constexpr int kTcItemUnits = 5;
 constexpr long long kWaitCycles = 2000000000LL;  // limit of a bounded wait: about a second
 
@@ -720,7 +720,7 @@ kv_attention_tc_kernel(KvArgs a, float* part_o, Part* parts, Desc* descs) {
       // ------------------------------------------------------------------ pages and scales
       // Four steps at a time, eight lanes each, a lane a run of 16 keys; the table's entries four
       // steps ahead of their scales' use.  (One step at a time the loads' latency is the warp's pace:
-      // 132 us for 24 x 20000 keys, 128 four at a time.)
+      // 132 us for 24 x 20000 keys when it was tried, 128 four at a time.)
       constexpr int kBatch = 4;
       const int* table = a.table + (int64_t)n * a.max_pages;
       const int mine = lane >> 3, at = 16 * (lane & 7);
@@ -823,7 +823,7 @@ cudaError_t launch_tc(const KvArgs& a, cudaStream_t s) {
 
 // Rows of an item: 32 where the average sequence's rows of a kv head fit, which leaves the softmax's
 // threads half the sums to hold; else 64 (a row tile more reads and opens the codes once more).
-// 24 x 20000 keys with 22 rows on average take 123 us with 32 (144 with 64), with 36 rows 152 us with
+// 24 x 20000 keys with 22 rows on average take 124 us with 32 (145 with 64), with 36 rows 153 us with
 // 64 (161 with 32).
 int item_rows(const KvArgs& a) { return (a.T + a.N - 1) / a.N * a.group <= 32 ? 32 : 64; }
 

@@ -304,8 +304,8 @@ template <typename IO, int D, bool E4M3, int IT> struct NewValues {
   }
 };
 
-// Heads [h0, h1) of a page.  (Two heads in flight at a time cost more registers than they hid:
-// prompts 80 us so, 73 one at a time.)
+// Heads [h0, h1) of a page.  (Two heads in flight at a time cost more registers than they
+// hid: prompts took a tenth longer.)
 template <typename New>
 __device__ __forceinline__ void append_heads(const KvArgs& a, const KvSpan& s, int pid, int h0,
                                              int h1, float (*red)[kKvThreads / 32]) {
@@ -318,8 +318,8 @@ __device__ __forceinline__ void append_heads(const KvArgs& a, const KvSpan& s, i
   }
 }
 
-// CTAs an SM holds at least: 64 registers a thread where the waiting values leave room (a cache step
-// of 96 rows takes 8.6 us with the compiler's own 101 registers, 4.8 with 64; prompts 130 and 73).
+// CTAs an SM holds at least: 64 registers a thread where the waiting values leave room (prompts of 7 x
+// 8192 rows take 116 us with the read back with the compiler's own number, 109 so).
 template <typename IO, int IT> constexpr int append_resident() {
   constexpr int words = IT * sizeof(IO);  // x 4: registers of waiting values
   return words <= 8 ? 4 : words <= 16 ? 2 : 1;
@@ -460,9 +460,9 @@ cudaError_t launch_kv(const KvArgs& a, bool append, cudaStream_t s) {
   const int values = a.cu == nullptr && a.N > 1 ? D : a.page * D;
   // A CTA takes several heads of its page, one after the other, where that leaves the GPU four
   // rounds of CTAs (of the 608 that its 152 SMs hold): the page is looked up once for them.
-  // Prompts of 7 x 8192 rows, 8 heads of 128: append 85 us with one head a CTA, 76 with two, 73
-  // with four; read 54 us with one, 48 with two, 51 with four.  A step of 96 rows, 2 heads of 256,
-  // is quicker with one: append 4.8 us against 5.4, read 5.9 against 7.6.
+  // Prompts of 7 x 8192 rows, 8 heads of 128: append 80 us with one head a CTA, 68 with two, 64
+  // with four; read 53 us with one, 47 with two.  A step of 96 rows, 2 heads of 256, is quicker with
+  // one: 10.6 us for both, 12.5 with all heads in a CTA.
   const int64_t single = slots * (append ? 2 : 1) * a.hkv, many = single / (4 * 608);
   const int most = append ? 4 : 2, per = many < 1 ? 1 : many < most ? (int)many : most;
   const int64_t ctas = slots * (append ? 2 : 1) * ((a.hkv + per - 1) / per);
@@ -472,8 +472,8 @@ cudaError_t launch_kv(const KvArgs& a, bool append, cudaStream_t s) {
   };
   if (!append) return go(kv_read_kernel<IO, D, E4M3>);
   // (pages of 128 tokens at most: D / 32 pieces.  Small pages, 5 sequences of 700 rows, 3 heads of 64
-  // in pages of 16: 8.6 us with the read back, 9.4 with room for more.  Between 8192 and 16384 values
-  // the room costs nothing: prompts of pages of 8192 take 118 us with room for 16384, 121 without.)
+  // in pages of 16: 8.6 us with the read back, 8.9 with room for more.  Between 8192 and 16384 values
+  // the room costs nothing: prompts of pages of 8192 take 109 us with room for 16384, 112 without.)
   if (values <= 4096) return go(kv_append_kernel<IO, D, E4M3, 1>);
   if constexpr (D == 256) {
     if (values > 16384) return go(kv_append_kernel<IO, D, E4M3, 8>);

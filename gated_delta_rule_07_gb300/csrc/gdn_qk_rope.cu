@@ -16,10 +16,11 @@
 // through shared memory.  Statistics are fp32.
 //
 // Measured (GB300, whose copies reach 6.80 TB/s), bf16: forward of 16384 tokens of 32 + 8 heads of
-// 128, 59.4 us, 5.79 TB/s of algorithmic bytes (85% of the copies); of 24 tokens of 16 + 2 heads of
-// 256, 1.8 us in a graph, a launch's time.  Gradients of 8192 tokens of 16 + 2 heads of 256 in
-// 42.5 us, 5.38 TB/s (79%): 71% of the issue slots are used, the sums of the weights' gradients and
-// the copies into the ring on top of the forward's work.
+// 128, 59.4 us, 5.79 TB/s of algorithmic bytes (85% of the copies; fp32 107 us, 94%); of 24 tokens of
+// 16 + 2 heads of 256, 1.8 us in a graph, a launch's time.  Gradients of 8192 tokens of 16 + 2 heads of
+// 256 in 42.5 us, 5.38 TB/s (79%; 16384 tokens of 40 heads of 128 in fp32 167 us, 90%): 71% of the issue
+// slots are used, the sums of the weights' gradients and the copies into the ring on top of the
+// forward's work.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

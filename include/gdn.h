@@ -433,8 +433,8 @@ typedef struct gdn_kv_problem {
  * T == N, one row each.  Lengths, tables and page ids are checked on the device: a sequence whose
  * rows or length do not fit, or a page outside the pool, is skipped (left unwritten; such a page's
  * keys are left out of the attention) and GDN_ERR_DEVICE_INPUT is recorded in dev_status (device
- * int32, or NULL).  A page that a call writes must belong to one sequence of the call; pages that
- * are only read may be shared. */
+ * int32, or NULL).  Rows that cu_seqlens gives to no sequence are left unwritten.  A page that a call
+ * writes must belong to one sequence of the call; pages that are only read may be shared. */
 
 /* Quantises new keys and values into the cache: row i of sequence n becomes the token at position
  * ctx_lens[n] + i.  For the new tokens of each (page, head), with qmax = 127 (int8) or 448 (e4m3),
