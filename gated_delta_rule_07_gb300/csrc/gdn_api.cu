@@ -7,6 +7,7 @@
 #include "gdn.h"
 #include "gdn_attention.h"
 #include "gdn_internal.h"
+#include "gdn_linear.h"
 
 namespace {
 
@@ -809,6 +810,247 @@ gdn_status gdn_kv_attention(const gdn_kv_cache* cache, const gdn_kv_problem* p, 
   a.window = window;
   a.workspace = static_cast<float*>(workspace);
   return to_status(gdn::kv_attention(a, stream));
+}
+
+// ------------------------------------------------ linear attention with a decay for each head
+
+namespace {
+
+gdn_status check_linear(const gdn_linear_problem* p) {
+  if (!p) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens < 0 || p->total_tokens > (int64_t)INT32_MAX || p->num_seqs < 1 ||
+      p->hk < 1 || p->hv < 1 || p->k_dim < 1 || p->v_dim < 1 || p->hv % p->hk != 0)
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (p->io_dtype != GDN_BF16 && p->io_dtype != GDN_F32) return GDN_ERR_UNSUPPORTED;
+  if ((p->k_dim != 64 && p->k_dim != 128) || (p->v_dim != 64 && p->v_dim != 128))
+    return GDN_ERR_UNSUPPORTED;
+  if (p->hv > 65535) return GDN_ERR_UNSUPPORTED;  // grid.y
+  // segments are grid.x, of at least 64 tokens each but the last of a sequence
+  if (p->total_tokens / 64 + p->num_seqs > (int64_t)INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  if (!strides_ok(p->q_token_stride, p->total_tokens, p->q_head_stride, p->hk, p->io_dtype) ||
+      !strides_ok(p->k_token_stride, p->total_tokens, p->k_head_stride, p->hk, p->io_dtype) ||
+      !strides_ok(p->v_token_stride, p->total_tokens, p->v_head_stride, p->hv, p->io_dtype))
+    return GDN_ERR_INVALID_ARGUMENT;
+  return GDN_OK;
+}
+
+// A segment's tokens: so many that the segments of all heads fill the SMs a few times over, in whole
+// chunks, within bounds that keep a segment's own state (K V values written and read twice) small
+// beside its rows at the top and its walk short at the bottom.
+int linear_segment(const gdn_linear_problem* p) {
+  const int64_t even = (p->total_tokens * p->hv / (152 * 2) + 63) / 64 * 64;
+  return (int)(even < 64 ? 64 : even > 1024 ? 1024 : even);
+}
+
+gdn::LinearShape linear_shape(const gdn_linear_problem* p, const float* log_decay,
+                              const int32_t* cu, int32_t* dev_status) {
+  gdn::LinearShape s;
+  memset(&s, 0, sizeof(s));
+  s.T = p->total_tokens;
+  s.N = p->num_seqs; s.hk = p->hk; s.hv = p->hv; s.K = p->k_dim; s.V = p->v_dim;
+  s.seg = linear_segment(p);
+  s.slots = s.T / s.seg + s.N;
+  s.bf16 = p->io_dtype == GDN_BF16;
+  s.log_decay = log_decay; s.cu = cu; s.status = dev_status;
+  return s;
+}
+
+gdn::LinearRows linear_rows(const void* x, int64_t ts, int64_t hs, int64_t T, int heads, int hv) {
+  return gdn::LinearRows{x, stride_of(ts, T), stride_of(hs, heads), hv / heads};
+}
+
+size_t linear_states_bytes(const gdn::LinearShape& s) {
+  return align_up((size_t)s.slots * s.hv * s.K * s.V * sizeof(float));
+}
+
+struct LinearBwdLayout {
+  size_t h, d, partial, q, k, v, total;
+};
+LinearBwdLayout linear_bwd_layout(const gdn::LinearShape& s, bool saved) {
+  LinearBwdLayout L;
+  const size_t e = s.bf16 ? 2 : 4, keys = (size_t)s.T * s.hk * s.K, values = (size_t)s.T * s.hv * s.V;
+  L.h = 0;
+  L.d = L.h + linear_states_bytes(s);
+  L.partial = L.d + linear_states_bytes(s);
+  L.q = L.partial + (s.bf16 && s.hv > s.hk ? align_up(keys * sizeof(float)) : 0);
+  L.k = L.q + (saved ? align_up(keys * e) : 0);
+  L.v = L.k + (saved ? align_up(keys * e) : 0);
+  L.total = L.v + (saved ? align_up(values * e) : 0);
+  return L;
+}
+
+gdn_status checkpoint_args(const gdn_checkpoint* t, int count, int format,
+                           gdn::CheckpointArgs& a) {
+  if (!t || count < 1) return GDN_ERR_INVALID_ARGUMENT;
+  if (count > gdn::kCheckpoints || (format != GDN_KV_INT8 && format != GDN_KV_E4M3))
+    return GDN_ERR_UNSUPPORTED;
+  memset(&a, 0, sizeof(a));
+  a.count = count;
+  a.e4m3 = format == GDN_KV_E4M3;
+  int64_t blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    const gdn_checkpoint& c = t[i];
+    if (c.total_tokens < 0 || c.total_tokens > (int64_t)INT32_MAX || c.heads < 1 || c.head_dim < 1)
+      return GDN_ERR_INVALID_ARGUMENT;
+    if ((c.io_dtype != GDN_BF16 && c.io_dtype != GDN_F32) || !head_dim_ok(c.head_dim) ||
+        c.total_tokens * c.heads > (int64_t)INT32_MAX)
+      return GDN_ERR_UNSUPPORTED;
+    if (!strides_ok(c.token_stride, c.total_tokens, c.head_stride, c.heads, c.io_dtype))
+      return GDN_ERR_INVALID_ARGUMENT;
+    if (c.total_tokens > 0 && (!c.x || !c.codes || !c.scale)) return GDN_ERR_INVALID_ARGUMENT;
+    if (!aligned16(c.x) || !aligned16(c.codes) || !aligned16(c.scale))
+      return GDN_ERR_INVALID_ARGUMENT;
+    a.t[i] = {c.x, static_cast<uint8_t*>(c.codes), c.scale, c.total_tokens * c.heads,
+              stride_of(c.token_stride, c.total_tokens), stride_of(c.head_stride, c.heads),
+              c.heads, c.head_dim, c.io_dtype == GDN_BF16};
+    blocks += a.t[i].rows / 32 + 1;  // (a block has 32 rows at least)
+  }
+  return blocks > (int64_t)INT32_MAX ? GDN_ERR_UNSUPPORTED : GDN_OK;
+}
+
+}  // namespace
+
+gdn_status gdn_check_linear_problem(const gdn_linear_problem* p) { return check_linear(p); }
+
+size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p) {
+  if (check_linear(p) != GDN_OK) return 0;
+  return linear_states_bytes(linear_shape(p, nullptr, nullptr, nullptr));
+}
+
+gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, const void* k,
+                                const void* v, const float* log_decay, const float* h0,
+                                const int32_t* cu_seqlens, void* out, float* h_final,
+                                void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                cudaStream_t stream) {
+  const gdn_status st = check_linear(p);
+  if (st != GDN_OK) return st;
+  if (!log_decay || (!cu_seqlens && p->num_seqs != 1)) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens > 0 && (!q || !k || !v || !out)) return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(h0) ||
+      !aligned16(h_final))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const gdn::LinearShape s = linear_shape(p, log_decay, cu_seqlens, dev_status);
+  if (!workspace || !aligned16(workspace) || ws_bytes < linear_states_bytes(s))
+    return GDN_ERR_WORKSPACE;
+  float* states = static_cast<float*>(workspace);
+  const int64_t T = s.T;
+  const gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
+                        kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
+                        vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);
+  if (T > 0) GDN_TRY(gdn::linear_state_simt({s, kr, vr, false, states}, stream));
+  GDN_TRY(gdn::linear_scan({s, false, states, h0, h_final}, stream));
+  if (T > 0)
+    GDN_TRY(gdn::linear_pass_simt({s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr},
+                                  stream));
+  return GDN_OK;
+}
+
+size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p, int saved) {
+  if (check_linear(p) != GDN_OK) return 0;
+  return linear_bwd_layout(linear_shape(p, nullptr, nullptr, nullptr), saved != 0).total;
+}
+
+gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void* q,
+                                         const void* k, const void* v,
+                                         const gdn_linear_saved* saved, const float* log_decay,
+                                         const float* h0, const int32_t* cu_seqlens,
+                                         const void* dout, const float* dh_final, void* dq,
+                                         void* dk, void* dv, float* dh0, void* workspace,
+                                         size_t ws_bytes, int32_t* dev_status,
+                                         cudaStream_t stream) {
+  const gdn_status st = check_linear(p);
+  if (st != GDN_OK) return st;
+  if (!log_decay || (!cu_seqlens && p->num_seqs != 1)) return GDN_ERR_INVALID_ARGUMENT;
+  if (saved && (q || k || v)) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens > 0 && (!dout || !dq || !dk || !dv || (!saved && (!q || !k || !v))))
+    return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv) || !aligned16(h0) || !aligned16(dh_final) ||
+      !aligned16(dh0))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const gdn::LinearShape s = linear_shape(p, log_decay, cu_seqlens, dev_status);
+  const LinearBwdLayout L = linear_bwd_layout(s, saved != nullptr);
+  if (!workspace || !aligned16(workspace) || ws_bytes < L.total) return GDN_ERR_WORKSPACE;
+  char* ws = static_cast<char*>(workspace);
+  float* h = reinterpret_cast<float*>(ws + L.h);
+  float* d = reinterpret_cast<float*>(ws + L.d);
+  const int64_t T = s.T;
+  const int share = s.hv / s.hk;
+  gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
+                  kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
+                  vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);
+  if (saved) {  // opened into the workspace, packed
+    const int64_t keys = (int64_t)s.hk * s.K, values = (int64_t)s.hv * s.V;
+    const gdn_checkpoint t[3] = {
+        {ws + L.q, const_cast<void*>(saved->q_codes), const_cast<float*>(saved->q_scale), T, keys,
+         s.K, s.hk, s.K, p->io_dtype},
+        {ws + L.k, const_cast<void*>(saved->k_codes), const_cast<float*>(saved->k_scale), T, keys,
+         s.K, s.hk, s.K, p->io_dtype},
+        {ws + L.v, const_cast<void*>(saved->v_codes), const_cast<float*>(saved->v_scale), T, values,
+         s.V, s.hv, s.V, p->io_dtype}};
+    gdn::CheckpointArgs ca;
+    const gdn_status cs = checkpoint_args(t, 3, saved->format, ca);
+    if (cs != GDN_OK) return cs;
+    GDN_TRY(gdn::checkpoint_open(ca, stream));
+    qr = linear_rows(ws + L.q, keys, s.K, T, s.hk, s.hv);
+    kr = linear_rows(ws + L.k, keys, s.K, T, s.hk, s.hv);
+    vr = linear_rows(ws + L.v, values, s.V, T, s.hv, s.hv);
+  }
+  const gdn::LinearRows gr =
+      linear_rows(dout, (int64_t)s.hv * s.V, s.V, T, s.hv, s.hv);
+  if (T > 0) {
+    GDN_TRY(gdn::linear_state_simt({s, kr, vr, false, h}, stream));
+    GDN_TRY(gdn::linear_state_simt({s, qr, gr, true, d}, stream));
+    GDN_TRY(gdn::linear_scan({s, false, h, h0, nullptr}, stream));
+  }
+  GDN_TRY(gdn::linear_scan({s, true, d, dh_final, dh0}, stream));
+  if (T > 0) {
+    float* partial = reinterpret_cast<float*>(ws + L.partial);
+    GDN_TRY(gdn::linear_pass_simt({s, gr, vr, kr, s.V, s.K, false, true, h, dq, share, partial},
+                                  stream));
+    GDN_TRY(gdn::linear_pass_simt({s, vr, gr, qr, s.V, s.K, true, true, d, dk, share, partial},
+                                  stream));
+    GDN_TRY(gdn::linear_pass_simt({s, kr, qr, gr, s.K, s.V, true, false, d, dv, 1, nullptr},
+                                  stream));
+  }
+  return GDN_OK;
+}
+
+gdn_status gdn_linear_attention_decode(const gdn_linear_problem* p, int32_t slots, const void* q,
+                                       const void* k, const void* v, const float* log_decay,
+                                       const int32_t* slot, float* state, void* out,
+                                       int32_t* dev_status, cudaStream_t stream) {
+  const gdn_status st = check_linear(p);
+  if (st != GDN_OK) return st;
+  if (slots < 1) return GDN_ERR_INVALID_ARGUMENT;
+  if (p->total_tokens == 0) return GDN_OK;
+  if (!q || !k || !v || !log_decay || !slot || !state || !out) return GDN_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(state) || !aligned16(out))
+    return GDN_ERR_INVALID_ARGUMENT;
+  const int64_t B = p->total_tokens;
+  const gdn::LinearDecode a = {
+      (int)B, slots, p->hk, p->hv, p->k_dim, p->v_dim, p->io_dtype == GDN_BF16,
+      linear_rows(q, p->q_token_stride, p->q_head_stride, B, p->hk, p->hv),
+      linear_rows(k, p->k_token_stride, p->k_head_stride, B, p->hk, p->hv),
+      linear_rows(v, p->v_token_stride, p->v_head_stride, B, p->hv, p->hv), log_decay, slot, state,
+      out, dev_status};
+  return to_status(gdn::linear_decode(a, stream));
+}
+
+gdn_status gdn_checkpoint_pack(const gdn_checkpoint* tensors, int32_t count, int32_t format,
+                               int32_t* dev_status, cudaStream_t stream) {
+  gdn::CheckpointArgs a;
+  const gdn_status st = checkpoint_args(tensors, count, format, a);
+  if (st != GDN_OK) return st;
+  a.status = dev_status;
+  return to_status(gdn::checkpoint_pack(a, stream));
+}
+
+gdn_status gdn_checkpoint_open(const gdn_checkpoint* tensors, int32_t count, int32_t format,
+                               cudaStream_t stream) {
+  gdn::CheckpointArgs a;
+  const gdn_status st = checkpoint_args(tensors, count, format, a);
+  return st != GDN_OK ? st : to_status(gdn::checkpoint_open(a, stream));
 }
 
 gdn_status gdn_device_status(const void* status_word, int reset, cudaStream_t stream) {

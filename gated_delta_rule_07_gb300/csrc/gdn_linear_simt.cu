@@ -1,0 +1,329 @@
+// gdn_linear_simt.cu -- linear attention with a decay for each head (gdn_linear.h) in fp32 on the CUDA
+// cores, for fp32 I/O and the head sizes that the tensor-core kernels do not take; and the scan over a
+// sequence's segments, which both families use.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gdn_elements.cuh"
+#include "gdn_linear.cuh"
+#include "gdn_stream_order.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int C = 64;        // tokens of a chunk
+constexpr int kTile = 32;    // tokens that the state kernel stages at a time
+
+template <typename IO>
+__device__ __forceinline__ const IO* head_rows(const LinearRows& r, int head) {
+  return static_cast<const IO*>(r.p) + (int64_t)(head / r.share) * r.hs;
+}
+
+// Rows t0 .. t0 + n of D elements into dst (rows of `stride` floats), zeros behind them; row i times
+// its weight a^{|w0 + w1 i|}.
+template <int ROWS, int D, typename IO, bool WEIGHTED>
+__device__ __forceinline__ void stage(float* dst, int stride, const IO* src, int64_t ts, int64_t t0,
+                                      int n, float log2a, int w0, int w1) {
+  for (int i = threadIdx.x; i < ROWS * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = i % (D / 4) * 4;
+    Quad<IO> q;
+    float f[4];
+    if (r < n)
+      q.load(src + (t0 + r) * ts + c);
+    else
+      q.clear();
+    q.open(f);
+    if (WEIGHTED) {
+      const float w = r < n ? linear::power(log2a, w0 + w1 * r) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] *= w;
+    }
+    put4(dst + r * stride + c, f);
+  }
+}
+
+// ------------------------------------------------------------------ a segment's own state
+
+// One block a (slot, value head): the K x V sums in registers, 32 tokens staged at a time.
+template <int K, int V, typename IO>
+__global__ void __launch_bounds__(kThreads) linear_state_kernel(LinearState a) {
+  constexpr int MK = K / 16, MV = V / 16;
+  __shared__ __align__(16) float xs[kTile][K], ys[kTile][V];
+  stream_order();
+  if (!linear::usable(a.s)) return;
+  int n;
+  int64_t t0, t1;
+  const int64_t slot = blockIdx.x;
+  const int head = blockIdx.y;
+  if (!linear::slot_tokens(a.s, slot, n, t0, t1)) return;
+  const float log2a = linear::log2_decay(a.s, head);
+  const IO* x = head_rows<IO>(a.x, head);
+  const IO* y = head_rows<IO>(a.y, head);
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  float acc[MK][MV] = {};
+  for (int64_t t = t0; t < t1; t += kTile) {
+    const int m = (int)(t1 - t < kTile ? t1 - t : kTile);
+    // forward: a token decays on its way to the segment's last; backward: to before the first
+    const int w0 = a.reverse ? (int)(t - t0) + 1 : (int)(t1 - 1 - t), w1 = a.reverse ? 1 : -1;
+    stage<kTile, K, IO, false>(&xs[0][0], K, x, a.x.ts, t, m, 0.f, 0, 0);
+    stage<kTile, V, IO, true>(&ys[0][0], V, y, a.y.ts, t, m, log2a, w0, w1);
+    __syncthreads();
+#pragma unroll 4
+    for (int r = 0; r < kTile; ++r) {
+      float u[MK], w[MV];
+#pragma unroll
+      for (int i = 0; i < MK; i += 4) *reinterpret_cast<float4*>(&u[i]) =
+          *reinterpret_cast<const float4*>(&xs[r][ty * MK + i]);
+#pragma unroll
+      for (int i = 0; i < MV; i += 4) *reinterpret_cast<float4*>(&w[i]) =
+          *reinterpret_cast<const float4*>(&ys[r][16 * i + 4 * tx]);
+#pragma unroll
+      for (int i = 0; i < MK; ++i)
+#pragma unroll
+        for (int j = 0; j < MV; ++j) acc[i][j] = fmaf(u[i], w[j], acc[i][j]);
+    }
+    __syncthreads();
+  }
+  float* u = a.states + (slot * a.s.hv + head) * K * V;
+#pragma unroll
+  for (int i = 0; i < MK; ++i)
+#pragma unroll
+    for (int j = 0; j < MV; j += 4) put4(u + (ty * MK + i) * V + 16 * j + 4 * tx, &acc[i][j]);
+}
+
+// ------------------------------------------------------------------ the scan over segments
+
+// One thread carries four elements of a state through its sequence's segments; the segments' sums are
+// read eight ahead, for each step waits for the one before only in registers.
+constexpr int kAhead = 8;
+__global__ void __launch_bounds__(kThreads) linear_scan_kernel(LinearScan a) {
+  stream_order();
+  if (!linear::usable(a.s)) return;
+  const int n = blockIdx.x, head = blockIdx.y;
+  const int64_t size = (int64_t)a.s.K * a.s.V;
+  const int64_t at = ((int64_t)blockIdx.z * kThreads + threadIdx.x) * 4;
+  if (at >= size) return;
+  const int64_t b = a.s.cu ? a.s.cu[n] : 0, e = a.s.cu ? a.s.cu[n + 1] : a.s.T;
+  const int count = (int)((e - b + a.s.seg - 1) / a.s.seg);
+  const int64_t slot0 = b / a.s.seg + n;
+  const float log2a = linear::log2_decay(a.s, head);
+  const float whole = linear::power(log2a, a.s.seg);
+  const float rest = linear::power(log2a, (int)(e - b) - (count - 1) * a.s.seg);  // the last segment's
+  const int64_t mine = ((int64_t)n * a.s.hv + head) * size + at;
+  float4 h = a.first ? *reinterpret_cast<const float4*>(a.first + mine) : make_float4(0, 0, 0, 0);
+  float* u = a.states + (slot0 * a.s.hv + head) * size + at;
+  const int64_t step = (int64_t)a.s.hv * size;
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    float4 add[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = a.reverse ? count - 1 - (i0 + k) : i0 + k;
+      if (i0 + k < count) add[k] = *reinterpret_cast<const float4*>(u + i * step);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = a.reverse ? count - 1 - (i0 + k) : i0 + k;
+      if (i0 + k < count) {
+        *reinterpret_cast<float4*>(u + i * step) = h;
+        const float w = i == count - 1 ? rest : whole;
+        h.x = fmaf(w, h.x, add[k].x);
+        h.y = fmaf(w, h.y, add[k].y);
+        h.z = fmaf(w, h.z, add[k].z);
+        h.w = fmaf(w, h.w, add[k].w);
+      }
+    }
+  }
+  if (a.last) *reinterpret_cast<float4*>(a.last + mine) = h;
+}
+
+// ------------------------------------------------------------------ the pass
+
+// One block a (slot, output head, 64 output columns) walks the segment's chunks of 64 tokens with S in
+// shared memory.  Output heads that several value heads add to are walked once for each, the running
+// sum kept in fp32 (in the output where that is fp32): always in the same order.
+constexpr int BW = 64;
+template <int A> constexpr int pass_smem() {
+  return (2 * C * (A + 4) + C * (BW + 4) + A * (BW + 4) + C * (C + 4)) * 4;
+}
+template <int A, typename IO>
+__global__ void __launch_bounds__(kThreads) linear_pass_kernel(LinearPass a) {
+  extern __shared__ __align__(16) float smem[];
+  float* zs = smem;                    // [C][A + 4]
+  float* xs = zs + C * (A + 4);        // [C][A + 4]
+  float* ys = xs + C * (A + 4);        // [C][BW + 4]
+  float* S = ys + C * (BW + 4);        // [A][BW + 4]
+  float* P = S + A * (BW + 4);         // [C][C + 4]
+  stream_order();
+  if (!linear::usable(a.s)) return;
+  int n;
+  int64_t t0, t1;
+  const int64_t slot = blockIdx.x;
+  if (!linear::slot_tokens(a.s, slot, n, t0, t1)) return;
+  const int oh = blockIdx.y, c0 = blockIdx.z * BW;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int chunks = (int)((t1 - t0 + C - 1) / C);
+  const int64_t ots = (int64_t)(a.s.hv / a.out_share) * a.B;
+  IO* out = static_cast<IO*>(a.out) + (int64_t)oh * a.B + c0 + 4 * tx;
+  float* sum = sizeof(IO) == 4 ? reinterpret_cast<float*>(out)
+                               : a.partial + (int64_t)oh * a.B + c0 + 4 * tx;
+
+  for (int g = 0; g < a.out_share; ++g) {
+    const int head = oh * a.out_share + g;
+    const float log2a = linear::log2_decay(a.s, head);
+    const IO* z = head_rows<IO>(a.z, head);
+    const IO* x = head_rows<IO>(a.x, head);
+    const IO* y = head_rows<IO>(a.y, head) + c0;
+    const float* st = a.states + (slot * a.s.hv + head) * a.A * a.B;
+    const float enter = a.reverse ? 1.f : linear::power(log2a, 1);
+    for (int i = threadIdx.x; i < A * BW; i += kThreads) {
+      // (the faster index along the stored rows)
+      const int r = a.transposed ? i % A : i / BW, c = a.transposed ? i / A : i % BW;
+      const float v = a.transposed ? st[(int64_t)(c0 + c) * a.A + r] : st[(int64_t)r * a.B + c0 + c];
+      S[r * (BW + 4) + c] = v * enter;
+    }
+    for (int ci = 0; ci < chunks; ++ci) {
+      const int64_t t = t0 + (int64_t)(a.reverse ? chunks - 1 - ci : ci) * C;
+      const int m = (int)(t1 - t < C ? t1 - t : C);
+      stage<C, A, IO, false>(zs, A + 4, z, a.z.ts, t, m, 0.f, 0, 0);
+      stage<C, A, IO, false>(xs, A + 4, x, a.x.ts, t, m, 0.f, 0, 0);
+      stage<C, BW, IO, false>(ys, BW + 4, y, a.y.ts, t, m, 0.f, 0, 0);
+      __syncthreads();
+      {  // P[i][j] = a^{|i - j|} z_i . x_j where j is at or before i
+        float p[4][4] = {};
+#pragma unroll 4
+        for (int k = 0; k < A; k += 4) {
+          float4 u[4], w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            u[i] = *reinterpret_cast<const float4*>(zs + (4 * ty + i) * (A + 4) + k);
+            w[i] = *reinterpret_cast<const float4*>(xs + (tx + 16 * i) * (A + 4) + k);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              p[i][j] = fmaf(u[i].x, w[j].x, fmaf(u[i].y, w[j].y,
+                        fmaf(u[i].z, w[j].z, fmaf(u[i].w, w[j].w, p[i][j]))));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int r = 4 * ty + i, c = tx + 16 * j, gap = a.reverse ? c - r : r - c;
+            P[r * (C + 4) + c] = gap >= 0 && c < m ? p[i][j] * linear::power(log2a, gap) : 0.f;
+          }
+      }
+      __syncthreads();
+      float o[4][4] = {};
+#pragma unroll 4
+      for (int k = 0; k < A; ++k) {
+        const float4 w = *reinterpret_cast<const float4*>(S + k * (BW + 4) + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = zs[(4 * ty + i) * (A + 4) + k];
+          o[i][0] = fmaf(u, w.x, o[i][0]);
+          o[i][1] = fmaf(u, w.y, o[i][1]);
+          o[i][2] = fmaf(u, w.z, o[i][2]);
+          o[i][3] = fmaf(u, w.w, o[i][3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        const float w = linear::power(log2a, a.reverse ? (r < m ? m - 1 - r : 0) : r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= w;
+      }
+#pragma unroll 4
+      for (int k = 0; k < C; ++k) {
+        const float4 w = *reinterpret_cast<const float4*>(ys + k * (BW + 4) + 4 * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = P[(4 * ty + i) * (C + 4) + k];
+          o[i][0] = fmaf(u, w.x, o[i][0]);
+          o[i][1] = fmaf(u, w.y, o[i][1]);
+          o[i][2] = fmaf(u, w.z, o[i][2]);
+          o[i][3] = fmaf(u, w.w, o[i][3]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (r >= m) continue;
+        const int64_t row = (t + r) * ots;
+        if (g > 0) {
+          const float4 before = *reinterpret_cast<const float4*>(sum + row);
+          o[i][0] += before.x; o[i][1] += before.y; o[i][2] += before.z; o[i][3] += before.w;
+        }
+        if (g + 1 < a.out_share)
+          put4(sum + row, o[i]);
+        else
+          put4(out + row, o[i]);
+      }
+      __syncthreads();
+      {  // S <- a^m S + sum_j a^{steps to the chunk's end} x_j y_j^T
+        constexpr int MA = A / 16;
+        const float w = linear::power(log2a, m);
+        float acc[MA][4];
+#pragma unroll
+        for (int i = 0; i < MA; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = w * S[(ty * MA + i) * (BW + 4) + 4 * tx + j];
+#pragma unroll 2
+        for (int k = 0; k < m; ++k) {
+          const float wk = linear::power(log2a, a.reverse ? k + 1 : m - k);
+          const float4 yk = *reinterpret_cast<const float4*>(ys + k * (BW + 4) + 4 * tx);
+#pragma unroll
+          for (int i = 0; i < MA; ++i) {
+            const float u = wk * xs[k * (A + 4) + ty * MA + i];
+            acc[i][0] = fmaf(u, yk.x, acc[i][0]);
+            acc[i][1] = fmaf(u, yk.y, acc[i][1]);
+            acc[i][2] = fmaf(u, yk.z, acc[i][2]);
+            acc[i][3] = fmaf(u, yk.w, acc[i][3]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < MA; ++i) put4(S + (ty * MA + i) * (BW + 4) + 4 * tx, acc[i]);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+template <int K, int V>
+cudaError_t launch_state(const LinearState& a, cudaStream_t s) {
+  const dim3 grid((unsigned)a.s.slots, (unsigned)a.s.hv);
+  return a.s.bf16 ? launch_ordered(linear_state_kernel<K, V, __nv_bfloat16>, grid, kThreads, 0, s, a)
+                  : launch_ordered(linear_state_kernel<K, V, float>, grid, kThreads, 0, s, a);
+}
+
+template <int A, typename IO> cudaError_t launch_pass(const LinearPass& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(linear_pass_kernel<A, IO>, pass_smem<A>(), done);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)a.s.slots, (unsigned)(a.s.hv / a.out_share), (unsigned)(a.B / BW));
+  return launch_ordered(linear_pass_kernel<A, IO>, grid, kThreads, pass_smem<A>(), s, a);
+}
+
+}  // namespace
+
+cudaError_t linear_state_simt(const LinearState& a, cudaStream_t s) {
+  if (a.s.K == 128) return a.s.V == 128 ? launch_state<128, 128>(a, s) : launch_state<128, 64>(a, s);
+  return a.s.V == 128 ? launch_state<64, 128>(a, s) : launch_state<64, 64>(a, s);
+}
+
+cudaError_t linear_scan(const LinearScan& a, cudaStream_t s) {
+  const dim3 grid((unsigned)a.s.N, (unsigned)a.s.hv,
+                  (unsigned)((a.s.K * a.s.V / 4 + kThreads - 1) / kThreads));
+  return launch_ordered(linear_scan_kernel, grid, kThreads, 0, s, a);
+}
+
+cudaError_t linear_pass_simt(const LinearPass& a, cudaStream_t s) {
+  if (a.A == 128)
+    return a.s.bf16 ? launch_pass<128, __nv_bfloat16>(a, s) : launch_pass<128, float>(a, s);
+  return a.s.bf16 ? launch_pass<64, __nv_bfloat16>(a, s) : launch_pass<64, float>(a, s);
+}
+
+}  // namespace gdn

@@ -1,5 +1,5 @@
-// gdn_torch.cpp -- Python's way to the softmax-attention layers' calls: checks torch tensors,
-// allocates the outputs and calls the C ABI (gdn.h).
+// gdn_torch.cpp -- Python's way to the calls of the softmax-attention layers, of linear attention and
+// of the 8-bit checkpoints: checks torch tensors, allocates the outputs and calls the C ABI (gdn.h).
 //
 // A decode step's kernels take a few microseconds, and so would each look at a tensor from Python;
 // here a look is a load.  Functions take positional arguments only (gdn.py has the signatures that
@@ -56,8 +56,11 @@ struct Cache {
 class Args {
  public:
   Args(const char* name, PyObject* const* v, Py_ssize_t n, Py_ssize_t want) : name_(name), v_(v) {
-    if (n != want) refuse(std::string(name) + ": wrong number of arguments");
+    if (want >= 0 ? n != want : n < -want)  // (negative: so many or more)
+      refuse(std::string(name) + ": wrong number of arguments");
+    count_ = n;
   }
+  Py_ssize_t count() const { return count_; }
   // The call's GPU is that of its cache or first tensor: all the others are to be on it.
   void on(int device, const char* what) const {
     if (device_ < 0) device_ = device;
@@ -156,6 +159,7 @@ class Args {
  private:
   const char* name_;
   PyObject* const* v_;
+  Py_ssize_t count_ = 0;
   mutable int device_ = -1;
   mutable std::optional<c10::cuda::CUDAGuard> guard_;
 };
@@ -328,14 +332,234 @@ PyObject* kv_attention(const Args& a) {
   return tuple_of({out, lse});
 }
 
+// ------------------------------------------------ linear attention and the 8-bit checkpoints
+
+at::ScalarType io_type(int io) { return io == GDN_BF16 ? at::kBFloat16 : at::kFloat; }
+float* f32_out(const at::Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; }
+
+void strides_of(const at::Tensor& t, int64_t& token, int64_t& head) {
+  token = t.stride(0);
+  head = t.stride(1);
+}
+// q, k [T, hk, K] and v [T, hv, V], as they go together; strides are the caller's
+gdn_linear_problem linear_of(const Args& a, const at::Tensor& q, const at::Tensor& k,
+                             const at::Tensor& v, int io) {
+  const int64_t T = q.size(0), most = INT32_MAX;
+  if (k.sizes() != q.sizes() || v.size(0) != T)
+    refuse(a.at("q, k and v do not go together: ") + shown(q) + ", " + shown(k) + ", " + shown(v));
+  gdn_linear_problem p = {};
+  p.total_tokens = T;
+  p.num_seqs = 1;
+  p.hk = (int32_t)std::min(q.size(1), most);
+  p.hv = (int32_t)std::min(v.size(1), most);
+  p.k_dim = (int32_t)std::min(q.size(2), most);
+  p.v_dim = (int32_t)std::min(v.size(2), most);
+  p.io_dtype = io;
+  return p;
+}
+// cu_seqlens (or None) at i: how many sequences
+const int32_t* sequences(const Args& a, int i, gdn_linear_problem& p) {
+  if (a.none(i)) return nullptr;
+  const at::Tensor& cu = a.packed(i, "cu_seqlens", at::kInt, {-1});
+  if (cu.size(0) < 2) refuse(a.at("cu_seqlens is to have an entry a sequence and one more"));
+  p.num_seqs = (int32_t)std::min(cu.size(0) - 1, (int64_t)INT32_MAX);
+  return i32(cu.data_ptr());
+}
+at::Tensor workspace_of(const Args& a, int i, size_t need, const at::Tensor& like) {
+  return a.none(i) ? empty({(int64_t)need}, like, at::kByte) : a.workspace(i);
+}
+
+// q, k, v, log_decay, h0, cu_seqlens, workspace, status
+PyObject* linear_attention(const Args& a) {
+  const int io = a.io(0, "q");
+  const at::Tensor& q = a.rows(0, "q", io_type(io));
+  const at::Tensor& k = a.rows(1, "k", io_type(io));
+  const at::Tensor& v = a.rows(2, "v", io_type(io));
+  gdn_linear_problem p = linear_of(a, q, k, v, io);
+  strides_of(q, p.q_token_stride, p.q_head_stride);
+  strides_of(k, p.k_token_stride, p.k_head_stride);
+  strides_of(v, p.v_token_stride, p.v_head_stride);
+  const at::Tensor& decay = a.packed(3, "log_decay", at::kFloat, {v.size(1)});
+  const int32_t* cu = sequences(a, 5, p);
+  const std::vector<int64_t> states = {p.num_seqs, v.size(1), q.size(2), v.size(2)};
+  const float* h0 = f32(a.packed_or_null(4, "h0", at::kFloat,
+                                         {states[0], states[1], states[2], states[3]}));
+  check(gdn_check_linear_problem(&p), "linear_attention");
+  at::Tensor out = empty(v.sizes(), v, v.scalar_type()), last = empty(states, v, at::kFloat);
+  at::Tensor ws = workspace_of(a, 6, gdn_linear_attention_workspace_size(&p), q);
+  check(gdn_linear_attention(&p, q.data_ptr(), k.data_ptr(), v.data_ptr(), f32(decay.data_ptr()), h0,
+                             cu, out.data_ptr(), f32_out(last), ws.data_ptr(), ws.nbytes(),
+                             a.status(7), a.stream()),
+        "linear_attention");
+  return tuple_of({out, last});
+}
+
+// q, k, v (or their codes), q_scale, k_scale, v_scale (or None each), io dtype (of codes), log_decay,
+// dout, h0, dh_final, cu_seqlens, workspace, status
+PyObject* linear_attention_backward(const Args& a) {
+  const bool held = !a.none(3);
+  const int io = held ? (int)a.whole(6) : a.io(0, "q");
+  at::ScalarType type = io_type(io);
+  if (held) {
+    type = a.tensor(0, "q").scalar_type();
+    if (type != at::kChar && type != at::kFloat8_e4m3fn)
+      refuse(a.at("the checkpoints' codes are ") + shown(a.tensor(0, "q")), GDN_ERR_UNSUPPORTED);
+  }
+  const at::Tensor& q = a.rows(0, "q", type);
+  const at::Tensor& k = a.rows(1, "k", type);
+  const at::Tensor& v = a.rows(2, "v", type);
+  gdn_linear_problem p = linear_of(a, q, k, v, io);
+  const int64_t T = q.size(0), hk = q.size(1), hv = v.size(1), K = q.size(2), V = v.size(2);
+  gdn_linear_saved saved = {};
+  if (held) {
+    const char* names[] = {"q", "k", "v"};
+    const float** scales[] = {&saved.q_scale, &saved.k_scale, &saved.v_scale};
+    for (int i = 0; i < 3; ++i) {
+      const at::Tensor& c = i == 0 ? q : i == 1 ? k : v;
+      if (!c.is_contiguous()) refuse(a.at(names[i]) + "'s codes are to be contiguous: " + shown(c));
+      *scales[i] = f32(a.packed(3 + i, "scale", at::kFloat, {T, i < 2 ? hk : hv}).data_ptr());
+    }
+    saved.q_codes = q.data_ptr();
+    saved.k_codes = k.data_ptr();
+    saved.v_codes = v.data_ptr();
+    saved.format = type == at::kChar ? GDN_KV_INT8 : GDN_KV_E4M3;
+  } else {
+    strides_of(q, p.q_token_stride, p.q_head_stride);
+    strides_of(k, p.k_token_stride, p.k_head_stride);
+    strides_of(v, p.v_token_stride, p.v_head_stride);
+  }
+  const at::Tensor& decay = a.packed(7, "log_decay", at::kFloat, {hv});
+  const at::Tensor& dout = a.packed(8, "dout", io_type(io), {T, hv, V});
+  const int32_t* cu = sequences(a, 11, p);
+  const std::vector<int64_t> states = {p.num_seqs, hv, K, V};
+  const float* h0 = f32(a.packed_or_null(9, "h0", at::kFloat, {states[0], hv, K, V}));
+  const float* dh = f32(a.packed_or_null(10, "dh_final", at::kFloat, {states[0], hv, K, V}));
+  check(gdn_check_linear_problem(&p), "linear_attention_backward");
+  at::Tensor dq = empty(q.sizes(), q, io_type(io)), dk = empty(k.sizes(), q, io_type(io));
+  at::Tensor dv = empty(v.sizes(), q, io_type(io)), dh0 = empty(states, q, at::kFloat);
+  at::Tensor ws =
+      workspace_of(a, 12, gdn_linear_attention_backward_workspace_size(&p, held), q);
+  check(gdn_linear_attention_backward(
+            &p, held ? nullptr : q.data_ptr(), held ? nullptr : k.data_ptr(),
+            held ? nullptr : v.data_ptr(), held ? &saved : nullptr, f32(decay.data_ptr()), h0, cu,
+            dout.data_ptr(), dh, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), f32_out(dh0),
+            ws.data_ptr(), ws.nbytes(), a.status(13), a.stream()),
+        "linear_attention_backward");
+  return tuple_of({dq, dk, dv, dh0});
+}
+
+// q, k, v, log_decay, slot, state, status
+PyObject* linear_attention_decode(const Args& a) {
+  const int io = a.io(0, "q");
+  const at::Tensor& q = a.rows(0, "q", io_type(io));
+  const at::Tensor& k = a.rows(1, "k", io_type(io));
+  const at::Tensor& v = a.rows(2, "v", io_type(io));
+  gdn_linear_problem p = linear_of(a, q, k, v, io);
+  strides_of(q, p.q_token_stride, p.q_head_stride);
+  strides_of(k, p.k_token_stride, p.k_head_stride);
+  strides_of(v, p.v_token_stride, p.v_head_stride);
+  const at::Tensor& decay = a.packed(3, "log_decay", at::kFloat, {v.size(1)});
+  const at::Tensor& slot = a.packed(4, "slot", at::kInt, {q.size(0)});
+  const at::Tensor& state = a.packed(5, "state", at::kFloat, {-1, v.size(1), q.size(2), v.size(2)});
+  check(gdn_check_linear_problem(&p), "linear_attention_decode");
+  at::Tensor out = empty(v.sizes(), v, v.scalar_type());
+  check(gdn_linear_attention_decode(&p, (int32_t)std::min(state.size(0), (int64_t)INT32_MAX),
+                                    q.data_ptr(), k.data_ptr(), v.data_ptr(), f32(decay.data_ptr()),
+                                    i32(slot.data_ptr()), state.data_ptr<float>(), out.data_ptr(),
+                                    a.status(6), a.stream()),
+        "linear_attention_decode");
+  return tuple_of({out});
+}
+
+gdn_checkpoint checkpoint_of(const at::Tensor& x, const at::Tensor& codes, const at::Tensor& scale,
+                             int io) {
+  const int64_t most = INT32_MAX;
+  return {x.data_ptr(), codes.data_ptr(), scale.data_ptr<float>(), x.size(0), x.stride(0), x.stride(1),
+          (int32_t)std::min(x.size(1), most), (int32_t)std::min(x.size(2), most), io};
+}
+constexpr Py_ssize_t kCheckpoints = 8;  // tensors of one C call
+PyObject* tuple_of(const std::vector<at::Tensor>& tensors) {
+  PyObject* t = PyTuple_New((Py_ssize_t)tensors.size());
+  if (!t) throw std::exception();
+  for (size_t i = 0; i < tensors.size(); ++i) {
+    PyObject* o = THPVariable_Wrap(tensors[i]);
+    if (!o) {
+      Py_DECREF(t);
+      throw std::exception();
+    }
+    PyTuple_SET_ITEM(t, (Py_ssize_t)i, o);
+  }
+  return t;
+}
+
+// status, format, tensors: (codes, scale) of each
+PyObject* checkpoint_pack(const Args& a) {
+  const int64_t format = a.whole(1);
+  const Py_ssize_t n = a.count() - 2;
+  if (n > kCheckpoints) refuse(a.at("at most 8 tensors a call"));
+  std::vector<at::Tensor> made;
+  gdn_checkpoint t[kCheckpoints];
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    const int io = a.io(2 + (int)i, "tensor");
+    const at::Tensor& x = a.rows(2 + (int)i, "tensor", io_type(io));
+    if (x.size(1) == 0 || x.size(2) == 0) refuse(a.at("a tensor without heads: ") + shown(x));
+    made.push_back(empty(x.sizes(), x, format == GDN_KV_INT8 ? at::kChar : at::kFloat8_e4m3fn));
+    made.push_back(empty({x.size(0), x.size(1)}, x, at::kFloat));
+    t[i] = checkpoint_of(x, made[2 * i], made[2 * i + 1], io);
+  }
+  check(gdn_checkpoint_pack(t, (int32_t)n, (int32_t)format, a.status(0), a.stream()),
+        "checkpoint_pack");
+  return tuple_of(made);
+}
+
+// then codes, scale and io dtype of each: the tensors
+PyObject* checkpoint_open(const Args& a) {
+  const Py_ssize_t n = a.count() / 3;
+  if (a.count() % 3 || n > kCheckpoints) refuse(a.at("at most 8 checkpoints a call"));
+  std::vector<at::Tensor> made;
+  gdn_checkpoint t[kCheckpoints];
+  const at::ScalarType type = a.tensor(0, "codes").scalar_type();
+  if (type != at::kChar && type != at::kFloat8_e4m3fn)
+    refuse(a.at("codes are ") + shown(a.tensor(0, "codes")), GDN_ERR_UNSUPPORTED);
+  for (int i = 0; i < (int)n; ++i) {
+    const at::Tensor& codes = a.packed(3 * i, "codes", type, {-1, -1, -1});
+    const at::Tensor& scale =
+        a.packed(3 * i + 1, "scale", at::kFloat, {codes.size(0), codes.size(1)});
+    const int io = (int)a.whole(3 * i + 2);
+    made.push_back(empty(codes.sizes(), codes, io_type(io)));
+    t[i] = checkpoint_of(made.back(), codes, scale, io);
+  }
+  check(gdn_checkpoint_open(t, (int32_t)n, type == at::kChar ? GDN_KV_INT8 : GDN_KV_E4M3,
+                            a.stream()),
+        "checkpoint_open");
+  return tuple_of(made);
+}
+
 // ------------------------------------------------------------------------------- the module
+
+struct Call {
+  PyObject* (*f)(const Args&);
+  const char* name;
+};
+constexpr Call kCalls[] = {{kv_append, "kv_append"},
+                           {kv_read, "kv_read"},
+                           {kv_attention, "kv_attention"},
+                           {qk_norm_rope, "qk_norm_rope"},
+                           {qk_norm_rope_backward, "qk_norm_rope_backward"},
+                           {linear_attention, "linear_attention"},
+                           {linear_attention_backward, "linear_attention_backward"},
+                           {linear_attention_decode, "linear_attention_decode"},
+                           {checkpoint_pack, "checkpoint_pack"},
+                           {checkpoint_open, "checkpoint_open"}};
+template <PyObject* (*F)(const Args&)> constexpr const char* name_of() {
+  for (const Call& c : kCalls)
+    if (c.f == F) return c.name;
+  return "";
+}
 
 template <PyObject* (*F)(const Args&), int N>
 PyObject* entry(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  static constexpr const char* names[] = {"kv_append", "kv_read", "kv_attention", "qk_norm_rope",
-                                          "qk_norm_rope_backward"};
-  const char* name = F == kv_append ? names[0] : F == kv_read ? names[1]
-                     : F == kv_attention ? names[2] : F == qk_norm_rope ? names[3] : names[4];
+  static constexpr const char* name = name_of<F>();
   try {
     return F(Args(name, v, n, N));
   } catch (const Refusal& r) {
@@ -367,6 +591,11 @@ PyMethodDef methods[] = {
     method<kv_append, 7>("kv_append"),
     method<kv_read, 7>("kv_read"),
     method<kv_attention, 9>("kv_attention"),
+    method<linear_attention, 8>("linear_attention"),
+    method<linear_attention_backward, 14>("linear_attention_backward"),
+    method<linear_attention_decode, 7>("linear_attention_decode"),
+    method<checkpoint_pack, -3>("checkpoint_pack"),
+    method<checkpoint_open, -3>("checkpoint_open"),
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -68,7 +68,10 @@ EXPORTED = ("gdn_status_string", "gdn_check_problem", "gdn_workspace_size", "gdn
             "gdn_backward", "gdn_prologue", "gdn_qk_norm_rope",
             "gdn_qk_norm_rope_backward_workspace_size", "gdn_qk_norm_rope_backward",
             "gdn_kv_append", "gdn_kv_read", "gdn_kv_attention_workspace_size",
-            "gdn_kv_attention")
+            "gdn_kv_attention", "gdn_check_linear_problem", "gdn_linear_attention_workspace_size",
+            "gdn_linear_attention", "gdn_linear_attention_backward_workspace_size",
+            "gdn_linear_attention_backward", "gdn_linear_attention_decode", "gdn_checkpoint_pack",
+            "gdn_checkpoint_open")
 
 
 class Problem(ctypes.Structure):
@@ -116,6 +119,29 @@ class KvProblem(ctypes.Structure):
                 ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
                 ("v_head_stride", ctypes.c_int64), ("q_token_stride", ctypes.c_int64),
                 ("q_head_stride", ctypes.c_int64)]
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [("total_tokens", ctypes.c_int64), ("num_seqs", ctypes.c_int32),
+                ("hk", ctypes.c_int32), ("hv", ctypes.c_int32), ("k_dim", ctypes.c_int32),
+                ("v_dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("q_token_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64)]
+
+
+class LinearSaved(ctypes.Structure):
+    _fields_ = [("q_codes", ctypes.c_void_p), ("k_codes", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("q_scale", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("format", ctypes.c_int32)]
+
+
+class CheckpointDesc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("total_tokens", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32)]
 
 
 class GdnError(RuntimeError):
@@ -173,10 +199,28 @@ _lib.gdn_kv_attention_workspace_size.restype = ctypes.c_size_t
 _lib.gdn_kv_attention_workspace_size.argtypes = [_cp, _kp]
 _lib.gdn_kv_attention.argtypes = [_cp, _kp, _vp, _ip, _ip, _ip, ctypes.c_float, ctypes.c_int32,
                                   _vp, _fp, _vp, ctypes.c_size_t, _ip, _vp]
+_lp = ctypes.POINTER(LinearProblem)
+_lib.gdn_check_linear_problem.argtypes = [_lp]
+_lib.gdn_linear_attention_workspace_size.restype = ctypes.c_size_t
+_lib.gdn_linear_attention_workspace_size.argtypes = [_lp]
+_lib.gdn_linear_attention.argtypes = [_lp, _vp, _vp, _vp, _fp, _fp, _ip, _vp, _fp, _vp,
+                                      ctypes.c_size_t, _ip, _vp]
+_lib.gdn_linear_attention_backward_workspace_size.restype = ctypes.c_size_t
+_lib.gdn_linear_attention_backward_workspace_size.argtypes = [_lp, ctypes.c_int]
+_lib.gdn_linear_attention_backward.argtypes = [_lp, _vp, _vp, _vp, ctypes.POINTER(LinearSaved), _fp,
+                                               _fp, _ip, _vp, _fp, _vp, _vp, _vp, _fp, _vp,
+                                               ctypes.c_size_t, _ip, _vp]
+_lib.gdn_linear_attention_decode.argtypes = [_lp, ctypes.c_int32, _vp, _vp, _vp, _fp, _ip, _fp, _vp,
+                                             _ip, _vp]
+_lib.gdn_checkpoint_pack.argtypes = [ctypes.POINTER(CheckpointDesc), ctypes.c_int32, ctypes.c_int32,
+                                     _ip, _vp]
+_lib.gdn_checkpoint_open.argtypes = [ctypes.POINTER(CheckpointDesc), ctypes.c_int32, ctypes.c_int32,
+                                     _vp]
 for _n in EXPORTED:
     if _n not in ("gdn_status_string", "gdn_workspace_size", "gdn_last_error_string",
                   "gdn_backward_workspace_size", "gdn_qk_norm_rope_backward_workspace_size",
-                  "gdn_kv_attention_workspace_size"):
+                  "gdn_kv_attention_workspace_size", "gdn_linear_attention_workspace_size",
+                  "gdn_linear_attention_backward_workspace_size"):
         getattr(_lib, _n).restype = ctypes.c_int
 
 
@@ -359,11 +403,15 @@ def gdn_backward(p, q, k, v, g, beta, h0, cu_seqlens, dout, dh_final, dq, dk, dv
 def backward(q, k, v, g, beta, dout, h0=None, dh_final=None, cu_seqlens=None, workspace=None,
              check_status=False, stream=None):
     """Gradients (dq, dk, dv, dg, dbeta, dh0) of <dout, out> + <dh_final, h_final> through the
-    forward on the same inputs; allocates the outputs (and the workspace unless given)."""
+    forward on the same inputs; allocates the outputs (and the workspace unless given).  q, k and v
+    are the tensors or their Checkpoints."""
     if stream is not None:
+        held = [t for x in (q, k, v) for t in
+                ((x.codes, x.scale) if isinstance(x, Checkpoint) else (x,))]
         return _on(stream, lambda: backward(q, k, v, g, beta, dout, h0, dh_final, cu_seqlens,
                                             workspace, check_status),
-                   q, k, v, g, beta, dout, h0, dh_final, cu_seqlens, workspace)
+                   *held, g, beta, dout, h0, dh_final, cu_seqlens, workspace)
+    q, k, v = (checkpoint_open(x)[0] if isinstance(x, Checkpoint) else x for x in (q, k, v))
     p = problem_for(q, v, cu_seqlens)
     N = p.num_seqs
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
@@ -681,6 +729,172 @@ def kv_attention(cache, q, block_table, kv_lens, cu_seqlens=None, scale=None, wi
                                     window, workspace, None)
     return _checked(True, q.device, "kv_attention", lambda st: _native.kv_attention(
         cache._address, q, block_table, kv_lens, cu_seqlens, scale, window, workspace, st))
+
+
+# ------------------------------------------------- linear attention with a decay for each head
+
+def gdn_check_linear_problem(p) -> int:
+    return _lib.gdn_check_linear_problem(p)
+
+
+def gdn_linear_attention_workspace_size(p) -> int:
+    return _lib.gdn_linear_attention_workspace_size(p)
+
+
+def gdn_linear_attention(p, q, k, v, log_decay, h0, cu_seqlens, out, h_final, workspace,
+                         ws_bytes=None, dev_status=None, stream=None):
+    ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.gdn_linear_attention(p, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0),
+                                     _ptr(cu_seqlens), _ptr(out), _ptr(h_final), _ptr(workspace),
+                                     int(ws_bytes), _ptr(dev_status), _stream(stream)),
+           "gdn_linear_attention")
+
+
+def linear_attention(q, k, v, log_decay, h0=None, cu_seqlens=None, workspace=None,
+                     check_status=False, stream=None):
+    """out [T, hv, V] and the final states [N, hv, K, V] of h_t = exp(log_decay) h_{t-1} + k_t v_t^T,
+    out_t = h_t^T q_t over packed sequences (see include/gdn.h): q, k [T, hk, K] and v [T, hv, V]
+    may be slices of one projection, log_decay [hv] <= 0 belongs to the layer."""
+    if stream is not None:
+        return _on(stream, lambda: linear_attention(q, k, v, log_decay, h0, cu_seqlens, workspace,
+                                                    check_status),
+                   q, k, v, log_decay, h0, cu_seqlens, workspace)
+    if not check_status:
+        return _native.linear_attention(q, k, v, log_decay, h0, cu_seqlens, workspace, None)
+    return _checked(True, q.device, "linear_attention", lambda st: _native.linear_attention(
+        q, k, v, log_decay, h0, cu_seqlens, workspace, st))
+
+
+def gdn_linear_attention_backward_workspace_size(p, saved=False) -> int:
+    return _lib.gdn_linear_attention_backward_workspace_size(p, int(bool(saved)))
+
+
+def gdn_linear_attention_backward(p, q, k, v, saved, log_decay, h0, cu_seqlens, dout, dh_final, dq,
+                                  dk, dv, dh0, workspace, ws_bytes=None, dev_status=None,
+                                  stream=None):
+    ws_bytes = workspace.numel() * workspace.element_size() if ws_bytes is None else ws_bytes
+    _check(_lib.gdn_linear_attention_backward(
+        p, _ptr(q), _ptr(k), _ptr(v), saved, _ptr(log_decay), _ptr(h0), _ptr(cu_seqlens),
+        _ptr(dout), _ptr(dh_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dh0), _ptr(workspace),
+        int(ws_bytes), _ptr(dev_status), _stream(stream)), "gdn_linear_attention_backward")
+
+
+def linear_attention_backward(q, k, v, log_decay, dout, h0=None, dh_final=None, cu_seqlens=None,
+                              workspace=None, check_status=False, stream=None):
+    """Gradients (dq, dk, dv, dh0) of <dout, out> + <dh_final, h_final> through linear_attention on
+    the same inputs.  q, k and v are the tensors, or all three their Checkpoints."""
+    where = "linear_attention_backward"
+    held = [isinstance(x, Checkpoint) for x in (q, k, v)]
+    if any(held) and not all(held):
+        _refuse(where, "q, k and v are to be tensors, or all of them checkpoints")
+    if all(held):
+        if not q.dtype == k.dtype == v.dtype:
+            _refuse(where, "the checkpoints' dtypes differ")
+        acts = (q.codes, k.codes, v.codes, q.scale, k.scale, v.scale, _IO[q.dtype])
+    else:
+        acts = (q, k, v, None, None, None, None)
+    if stream is not None:
+        return _on(stream, lambda: linear_attention_backward(q, k, v, log_decay, dout, h0, dh_final,
+                                                             cu_seqlens, workspace, check_status),
+                   *acts[:6], log_decay, dout, h0, dh_final, cu_seqlens, workspace)
+    if not check_status:
+        return _native.linear_attention_backward(*acts, log_decay, dout, h0, dh_final, cu_seqlens,
+                                                 workspace, None)
+    return _checked(True, dout.device, where, lambda st: _native.linear_attention_backward(
+        *acts, log_decay, dout, h0, dh_final, cu_seqlens, workspace, st))
+
+
+def gdn_linear_attention_decode(p, slots, q, k, v, log_decay, slot, state, out, dev_status=None,
+                                stream=None):
+    _check(_lib.gdn_linear_attention_decode(p, int(slots), _ptr(q), _ptr(k), _ptr(v),
+                                            _ptr(log_decay), _ptr(slot), _ptr(state), _ptr(out),
+                                            _ptr(dev_status), _stream(stream)),
+           "gdn_linear_attention_decode")
+
+
+def linear_attention_decode(q, k, v, log_decay, slot, state, check_status=False, stream=None):
+    """One token of each request: row b continues the request held in state[slot[b]] (updated in
+    place; state [slots, hv, K, V] fp32, slot int32 [B], negative for padding rows).  Returns
+    out [B, hv, V]."""
+    if stream is not None:
+        return _on(stream, lambda: linear_attention_decode(q, k, v, log_decay, slot, state,
+                                                           check_status),
+                   q, k, v, log_decay, slot, state)
+    if not check_status:
+        return _native.linear_attention_decode(q, k, v, log_decay, slot, state, None)[0]
+    return _checked(True, q.device, "linear_attention_decode",
+                    lambda st: _native.linear_attention_decode(q, k, v, log_decay, slot, state,
+                                                               st))[0]
+
+
+# ------------------------------------------------- activations held in 8 bits
+
+class Checkpoint:
+    """Rows [T, heads, D] held in 8 bits (layouts of include/gdn.h): codes [T, heads, D] int8 or
+    float8_e4m3fn, scale [T, heads] fp32, and the dtype that they open to.  checkpoint_pack makes
+    them."""
+
+    __slots__ = ("codes", "scale", "dtype")
+
+    def __init__(self, codes, scale, dtype=torch.bfloat16):
+        if codes.dtype not in _KV_FORMATS or dtype not in _IO:
+            _refuse("Checkpoint", f"codes of dtype {codes.dtype} for {dtype}", 2)
+        for name, t, shape in (("codes", codes, codes.shape), ("scale", scale, codes.shape[:2])):
+            if codes.dim() != 3 or t.shape != shape or not t.is_contiguous() or not t.is_cuda or \
+                    t.device != codes.device or (t is scale and t.dtype is not torch.float32):
+                _refuse("Checkpoint", f"{name} of {t.dtype} {tuple(t.shape)} on {t.device}")
+        self.codes, self.scale, self.dtype = codes, scale, dtype
+
+    shape = property(lambda self: self.codes.shape)
+
+    def __repr__(self):
+        return f"Checkpoint({tuple(self.shape)}, {self.codes.dtype} for {self.dtype})"
+
+
+def gdn_checkpoint_pack(tensors, count, format, dev_status=None, stream=None):
+    _check(_lib.gdn_checkpoint_pack(tensors, int(count), int(format), _ptr(dev_status),
+                                    _stream(stream)), "gdn_checkpoint_pack")
+
+
+def checkpoint_pack(*tensors, dtype=torch.int8, check_status=False, stream=None):
+    """Checkpoints of up to 8 tensors [T, heads, D] (slices of one projection are fine), one scale for
+    each row of D elements, int8 or float8_e4m3fn.  With check_status, raises where a value was not
+    finite."""
+    if stream is not None:
+        side = _side_stream(stream, tensors)
+        made = _on(side, lambda: tuple(x for c in checkpoint_pack(
+            *tensors, dtype=dtype, check_status=check_status) for x in (c.codes, c.scale)), *tensors)
+    else:
+        fmt = _KV_FORMATS.get(dtype)
+        if fmt is None:
+            _refuse("checkpoint_pack", f"dtype {dtype}", 2)
+        if not tensors:
+            _refuse("checkpoint_pack", "nothing to hold")
+        made = _checked(check_status, tensors[0].device, "checkpoint_pack",
+                        lambda st: _native.checkpoint_pack(st, fmt, *tensors))
+    return tuple(_checkpoint(made[2 * i], made[2 * i + 1], x.dtype) for i, x in enumerate(tensors))
+
+
+def _checkpoint(codes, scale, dtype):
+    c = Checkpoint.__new__(Checkpoint)  # (what the library has made needs no checks)
+    c.codes, c.scale, c.dtype = codes, scale, dtype
+    return c
+
+
+def gdn_checkpoint_open(tensors, count, format, stream=None):
+    _check(_lib.gdn_checkpoint_open(tensors, int(count), int(format), _stream(stream)),
+           "gdn_checkpoint_open")
+
+
+def checkpoint_open(*checkpoints, stream=None):
+    """The tensors that checkpoints stand for, contiguous and in their dtypes."""
+    if stream is not None:
+        return _on(stream, lambda: checkpoint_open(*checkpoints),
+                   *(t for c in checkpoints for t in (c.codes, c.scale)))
+    if not checkpoints:
+        _refuse("checkpoint_open", "nothing to open")
+    return _native.checkpoint_open(*(x for c in checkpoints
+                                     for x in (c.codes, c.scale, _IO[c.dtype])))
 
 
 # ------------------------------------------------------------------ convenience API

@@ -346,6 +346,123 @@ gdn_status gdn_decode_step(const gdn_decode_problem* p, const void* q, const voi
                            cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------------- */
+/* Linear attention with a decay for each head: the layers whose state decays by a constant of    */
+/* the head, without gates and without the correction of what a key held before.                  */
+
+typedef struct gdn_linear_problem {
+    int64_t total_tokens;     /* T >= 0: tokens of the packed stream                        */
+    int32_t num_seqs;         /* N >= 1                                                     */
+    int32_t hk, hv;           /* key heads, value heads (hv % hk == 0)                      */
+    int32_t k_dim, v_dim;     /* K, V in {64, 128}                                          */
+    int32_t io_dtype;         /* gdn_dtype of q, k, v, the output and the gradients         */
+    int64_t q_token_stride, q_head_stride;  /* elements, multiples of 16 bytes (that of one   */
+    int64_t k_token_stride, k_head_stride;  /* token or head is ignored); the last dimension  */
+    int64_t v_token_stride, v_head_stride;  /* is contiguous                                  */
+} gdn_linear_problem;
+
+/* Checks a problem description on the host (no device work). */
+gdn_status gdn_check_linear_problem(const gdn_linear_problem* p);
+
+/* Bytes of device workspace gdn_linear_attention needs for problem p (0 when p is invalid): one
+ * K x V fp32 state for each value head of each segment of the sequences. */
+size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p);
+
+/* Linear attention over packed sequences.  Per value head j (key head j / (hv / hk)), with
+ * a = exp(log_decay[j]):
+ *     h_t = a h_{t-1} + k_t v_t^T,     out_t = h_t^T q_t
+ * (the caller folds any scale into q).
+ *   q, k        [T, hk, K], v [T, hv, V] io dtype, strided as the problem says
+ *   log_decay   [hv] fp32, each <= 0 (a constant of the layer; -inf forgets at every token)
+ *   h0          initial states [N, hv, K, V] fp32, or NULL for zeros
+ *   cu_seqlens  device int32 [N+1] with cu[0] = 0, non-decreasing, cu[N] <= T (sequences may be
+ *               empty; rows behind the last are left unwritten); NULL only when N == 1 (then [0, T])
+ *   out         [T, hv, V] io dtype, contiguous
+ *   h_final     [N, hv, K, V] fp32, or NULL to skip; may be h0 itself
+ *   workspace   ws_bytes >= gdn_linear_attention_workspace_size(p), 16-byte aligned, need not be
+ *               initialised; a call's own until its work is done
+ *   dev_status  device int32 status word, or NULL
+ * All tensor pointers 16-byte aligned.  The table and the decays are checked on the device: with a
+ * bad table, or a decay that is NaN or positive, nothing is written and GDN_ERR_DEVICE_INPUT is
+ * recorded.  The same inputs give the same bits.  A value of a sequence that is not finite makes
+ * that sequence's outputs and final state undefined from up to 127 tokens before it on (in the
+ * head that reads it), and no other's.
+ * Precision: states are carried and h_final is formed to fp32 accuracy.  bf16 I/O with K = V = 128
+ * runs on the tensor cores, elsewhere everything is fp32 arithmetic. */
+gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, const void* k,
+                                const void* v, const float* log_decay, const float* h0,
+                                const int32_t* cu_seqlens, void* out, float* h_final,
+                                void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                cudaStream_t stream);
+
+/* 8-bit activations as gdn_checkpoint_pack leaves them: codes [T, heads, D], scale [T, heads]. */
+typedef struct gdn_linear_saved {
+    const void *q_codes, *k_codes, *v_codes;
+    const float *q_scale, *k_scale, *v_scale;
+    int32_t format;           /* gdn_kv_format of all three                                  */
+} gdn_linear_saved;
+
+/* Bytes of device workspace gdn_linear_attention_backward needs (0 when p is invalid); `saved`
+ * != 0 for a call that is given 8-bit activations. */
+size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p, int saved);
+
+/* Gradients of <dout, out> + <dh_final, h_final> through gdn_linear_attention on the same inputs.
+ *   q, k, v     as in the forward; or all three NULL and `saved` their 8-bit checkpoints, whose
+ *               values are those that gdn_checkpoint_open gives in the io dtype
+ *   dout        [T, hv, V] io dtype, contiguous      dh_final  [N, hv, K, V] fp32, or NULL (zeros)
+ *   dq, dk      [T, hk, K] io dtype (a key head's gradient sums over the value heads reading it, in
+ *               fp32 and in a fixed order),  dv [T, hv, V] io dtype, contiguous
+ *   dh0         [N, hv, K, V] fp32, or NULL to skip; may be dh_final itself
+ * The decays are constants of the layer: they get no gradient.  Checks, unwritten rows, workspace,
+ * precision and errors as in the forward; dh0 is formed to fp32 accuracy. */
+gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void* q,
+                                         const void* k, const void* v,
+                                         const gdn_linear_saved* saved, const float* log_decay,
+                                         const float* h0, const int32_t* cu_seqlens,
+                                         const void* dout, const float* dh_final, void* dq,
+                                         void* dk, void* dv, float* dh0, void* workspace,
+                                         size_t ws_bytes, int32_t* dev_status,
+                                         cudaStream_t stream);
+
+/* One token of each of B = p->total_tokens requests (num_seqs is not used), over a pool of states as
+ * gdn_decode_step's: row b's state is state[slot[b]], updated in place, and
+ *     h <- a h + k v^T,     out = h^T q.
+ *   q, k [B, hk, K], v [B, hv, V] io dtype, strided;  slot device int32 [B];
+ *   state [slots, hv, K, V] fp32;  out [B, hv, V] io dtype, contiguous
+ * A negative slot marks a padding row: its out row is set to 0 and no state is touched.  A row
+ * whose slot is >= slots, or is named by another row too, is skipped (state and out row left as they
+ * were), as are the heads whose decay is NaN or positive; GDN_ERR_DEVICE_INPUT is recorded.  fp32
+ * arithmetic. */
+gdn_status gdn_linear_attention_decode(const gdn_linear_problem* p, int32_t slots, const void* q,
+                                       const void* k, const void* v, const float* log_decay,
+                                       const int32_t* slot, float* state, void* out,
+                                       int32_t* dev_status, cudaStream_t stream);
+
+/* A tensor of a checkpoint call: rows x [T, heads, D] of io dtype, strided; codes [T, heads, D] one
+ * byte each and scale [T, heads] fp32, contiguous. */
+typedef struct gdn_checkpoint {
+    void* x;
+    void* codes;
+    float* scale;
+    int64_t total_tokens;     /* T >= 0                                                     */
+    int64_t token_stride, head_stride;  /* of x: elements, multiples of 16 bytes               */
+    int32_t heads, head_dim;  /* D in {64, 128, 256}                                        */
+    int32_t io_dtype;         /* gdn_dtype of x                                             */
+} gdn_checkpoint;
+
+/* Holds up to 8 tensors in 8 bits, one scale for each row (a head of a token), with
+ * qmax = 127 (int8) or 448 (e4m3), in fp32:
+ *     s = amax * (1 / qmax),   code = round_to_nearest_even(x * (1 / s)), within +-qmax.
+ * A row whose amax is below 2^-100 is held as zeros with scale 0.  Values that are not finite are
+ * kept out of amax, held as the largest code of their sign (a NaN as 0), and recorded as
+ * GDN_ERR_DEVICE_RANGE.  format: a gdn_kv_format (0 int8, 1 e4m3), the same for all tensors. */
+gdn_status gdn_checkpoint_pack(const gdn_checkpoint* tensors, int32_t count, int32_t format,
+                               int32_t* dev_status, cudaStream_t stream);
+
+/* Opens them again: x = code * s, rounded once to x's dtype. */
+gdn_status gdn_checkpoint_open(const gdn_checkpoint* tensors, int32_t count, int32_t format,
+                               cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------- */
 /* Softmax-attention layers beside the recurrent ones: query/key norms with the position       */
 /* rotation, a paged 8-bit key/value cache, and attention over it.                             */
 
