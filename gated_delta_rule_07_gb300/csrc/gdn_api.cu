@@ -834,12 +834,38 @@ gdn_status check_linear(const gdn_linear_problem* p) {
   return GDN_OK;
 }
 
+// The problem of a call that is given 8-bit activations: they are opened to packed rows.
+gdn_linear_problem linear_opened(const gdn_linear_problem* p) {
+  gdn_linear_problem o = *p;
+  o.q_token_stride = o.k_token_stride = (int64_t)p->hk * p->k_dim;
+  o.v_token_stride = (int64_t)p->hv * p->v_dim;
+  o.q_head_stride = o.k_head_stride = p->k_dim;
+  o.v_head_stride = p->v_dim;
+  return o;
+}
+
+// Whether the tensor-core kernels take a problem.  (They read rows through tensor maps, which have no
+// way to say that a row is all tokens' or heads': broadcast rows go to the CUDA cores.)
+bool linear_on_tc(const gdn_linear_problem* p) {
+  const int64_t T = p->total_tokens;
+  auto mapped = [T](int64_t ts, int64_t hs, int heads) {
+    return (T == 1 || (ts > 0 && ts < (int64_t)1 << 38)) &&
+           (heads == 1 || (hs > 0 && hs < (int64_t)1 << 38));
+  };
+  return p->io_dtype == GDN_BF16 && p->k_dim == 128 && p->v_dim == 128 &&
+         mapped(p->q_token_stride, p->q_head_stride, p->hk) &&
+         mapped(p->k_token_stride, p->k_head_stride, p->hk) &&
+         mapped(p->v_token_stride, p->v_head_stride, p->hv);
+}
+
 // A segment's tokens: so many that the segments of all heads fill the SMs a few times over, in whole
 // chunks, within bounds that keep a segment's own state (K V values written and read twice) small
 // beside its rows at the top and its walk short at the bottom.
 int linear_segment(const gdn_linear_problem* p) {
-  const int64_t even = (p->total_tokens * p->hv / (152 * 2) + 63) / 64 * 64;
-  return (int)(even < 64 ? 64 : even > 1024 ? 1024 : even);
+  const bool tc = linear_on_tc(p);
+  const int64_t chunk = tc ? 128 : 64, most = tc ? 2048 : 1024;
+  const int64_t even = (p->total_tokens * p->hv / (152 * (tc ? 1 : 2)) + chunk - 1) / chunk * chunk;
+  return (int)(even < chunk ? chunk : even > most ? most : even);
 }
 
 gdn::LinearShape linear_shape(const gdn_linear_problem* p, const float* log_decay,
@@ -861,6 +887,13 @@ gdn::LinearRows linear_rows(const void* x, int64_t ts, int64_t hs, int64_t T, in
 
 size_t linear_states_bytes(const gdn::LinearShape& s) {
   return align_up((size_t)s.slots * s.hv * s.K * s.V * sizeof(float));
+}
+
+cudaError_t linear_state(const gdn_linear_problem* p, const gdn::LinearState& a, cudaStream_t s) {
+  return linear_on_tc(p) ? gdn::linear_state_tc(a, s) : gdn::linear_state_simt(a, s);
+}
+cudaError_t linear_pass(const gdn_linear_problem* p, const gdn::LinearPass& a, cudaStream_t s) {
+  return linear_on_tc(p) ? gdn::linear_pass_tc(a, s) : gdn::linear_pass_simt(a, s);
 }
 
 struct LinearBwdLayout {
@@ -937,17 +970,18 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
   const gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
                         kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
                         vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);
-  if (T > 0) GDN_TRY(gdn::linear_state_simt({s, kr, vr, false, states}, stream));
+  if (T > 0) GDN_TRY(linear_state(p, {s, kr, vr, false, states}, stream));
   GDN_TRY(gdn::linear_scan({s, false, states, h0, h_final}, stream));
   if (T > 0)
-    GDN_TRY(gdn::linear_pass_simt({s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr},
+    GDN_TRY(linear_pass(p, {s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr},
                                   stream));
   return GDN_OK;
 }
 
 size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p, int saved) {
   if (check_linear(p) != GDN_OK) return 0;
-  return linear_bwd_layout(linear_shape(p, nullptr, nullptr, nullptr), saved != 0).total;
+  const gdn_linear_problem o = saved ? linear_opened(p) : *p;
+  return linear_bwd_layout(linear_shape(&o, nullptr, nullptr, nullptr), saved != 0).total;
 }
 
 gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void* q,
@@ -968,6 +1002,8 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
       !aligned16(dk) || !aligned16(dv) || !aligned16(h0) || !aligned16(dh_final) ||
       !aligned16(dh0))
     return GDN_ERR_INVALID_ARGUMENT;
+  const gdn_linear_problem opened = linear_opened(p);
+  if (saved) p = &opened;
   const gdn::LinearShape s = linear_shape(p, log_decay, cu_seqlens, dev_status);
   const LinearBwdLayout L = linear_bwd_layout(s, saved != nullptr);
   if (!workspace || !aligned16(workspace) || ws_bytes < L.total) return GDN_ERR_WORKSPACE;
@@ -976,41 +1012,41 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
   float* d = reinterpret_cast<float*>(ws + L.d);
   const int64_t T = s.T;
   const int share = s.hv / s.hk;
-  gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
-                  kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
-                  vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);
-  if (saved) {  // opened into the workspace, packed
-    const int64_t keys = (int64_t)s.hk * s.K, values = (int64_t)s.hv * s.V;
-    const gdn_checkpoint t[3] = {
-        {ws + L.q, const_cast<void*>(saved->q_codes), const_cast<float*>(saved->q_scale), T, keys,
-         s.K, s.hk, s.K, p->io_dtype},
-        {ws + L.k, const_cast<void*>(saved->k_codes), const_cast<float*>(saved->k_scale), T, keys,
-         s.K, s.hk, s.K, p->io_dtype},
-        {ws + L.v, const_cast<void*>(saved->v_codes), const_cast<float*>(saved->v_scale), T, values,
-         s.V, s.hv, s.V, p->io_dtype}};
+  if (saved) {
+    q = ws + L.q;
+    k = ws + L.k;
+    v = ws + L.v;
+    auto held = [&](const void* to, const void* codes, const float* scale, int heads, int d) {
+      return gdn_checkpoint{const_cast<void*>(to), const_cast<void*>(codes),
+                            const_cast<float*>(scale), T, (int64_t)heads * d, d, heads, d,
+                            p->io_dtype};
+    };
+    const gdn_checkpoint t[3] = {held(q, saved->q_codes, saved->q_scale, s.hk, s.K),
+                                 held(k, saved->k_codes, saved->k_scale, s.hk, s.K),
+                                 held(v, saved->v_codes, saved->v_scale, s.hv, s.V)};
     gdn::CheckpointArgs ca;
     const gdn_status cs = checkpoint_args(t, 3, saved->format, ca);
     if (cs != GDN_OK) return cs;
     GDN_TRY(gdn::checkpoint_open(ca, stream));
-    qr = linear_rows(ws + L.q, keys, s.K, T, s.hk, s.hv);
-    kr = linear_rows(ws + L.k, keys, s.K, T, s.hk, s.hv);
-    vr = linear_rows(ws + L.v, values, s.V, T, s.hv, s.hv);
   }
+  const gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
+                        kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
+                        vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);
   const gdn::LinearRows gr =
       linear_rows(dout, (int64_t)s.hv * s.V, s.V, T, s.hv, s.hv);
   if (T > 0) {
-    GDN_TRY(gdn::linear_state_simt({s, kr, vr, false, h}, stream));
-    GDN_TRY(gdn::linear_state_simt({s, qr, gr, true, d}, stream));
+    GDN_TRY(linear_state(p, {s, kr, vr, false, h}, stream));
+    GDN_TRY(linear_state(p, {s, qr, gr, true, d}, stream));
     GDN_TRY(gdn::linear_scan({s, false, h, h0, nullptr}, stream));
   }
   GDN_TRY(gdn::linear_scan({s, true, d, dh_final, dh0}, stream));
   if (T > 0) {
     float* partial = reinterpret_cast<float*>(ws + L.partial);
-    GDN_TRY(gdn::linear_pass_simt({s, gr, vr, kr, s.V, s.K, false, true, h, dq, share, partial},
+    GDN_TRY(linear_pass(p, {s, gr, vr, kr, s.V, s.K, false, true, h, dq, share, partial},
                                   stream));
-    GDN_TRY(gdn::linear_pass_simt({s, vr, gr, qr, s.V, s.K, true, true, d, dk, share, partial},
+    GDN_TRY(linear_pass(p, {s, vr, gr, qr, s.V, s.K, true, true, d, dk, share, partial},
                                   stream));
-    GDN_TRY(gdn::linear_pass_simt({s, kr, qr, gr, s.K, s.V, true, false, d, dv, 1, nullptr},
+    GDN_TRY(linear_pass(p, {s, kr, qr, gr, s.K, s.V, true, false, d, dv, 1, nullptr},
                                   stream));
   }
   return GDN_OK;

@@ -74,6 +74,11 @@ cudaError_t linear_state_simt(const LinearState& a, cudaStream_t s);
 cudaError_t linear_pass_simt(const LinearPass& a, cudaStream_t s);
 cudaError_t linear_scan(const LinearScan& a, cudaStream_t s);
 
+// The same on the tensor cores: bf16, K = V = 128, segments of whole chunks of 128 tokens, T > 0, rows
+// that are strided by 16 bytes or more.
+cudaError_t linear_state_tc(const LinearState& a, cudaStream_t s);
+cudaError_t linear_pass_tc(const LinearPass& a, cudaStream_t s);
+
 struct LinearDecode {
   int batch, slots, hk, hv, K, V;
   bool bf16;

@@ -99,6 +99,15 @@ def test_gradients(gdn, lens, hk, hv, io, K, V):
     c.check_backward(c.backward(gdn))
 
 
+@pytest.mark.parametrize("hk,hv", [(4, 12), (12, 12)])
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_walks_of_several_chunks(gdn, io, hk, hv):
+    """So many tokens and heads that a segment is several chunks, and its last one a part of one."""
+    c = Case([4000, 33, 2111], hk, hv, 128, 128, io, seed=hk)
+    c.check_forward(c.forward(gdn))
+    c.check_backward(c.backward(gdn))
+
+
 @pytest.mark.parametrize("io", [BF16, F32])
 def test_slices_of_one_projection(gdn, io):
     c = Case([130, 61], 2, 4, 128, 128, io, wide=True, seed=3)
