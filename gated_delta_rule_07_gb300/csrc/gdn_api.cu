@@ -885,8 +885,15 @@ gdn::LinearRows linear_rows(const void* x, int64_t ts, int64_t hs, int64_t T, in
   return gdn::LinearRows{x, stride_of(ts, T), stride_of(hs, heads), hv / heads};
 }
 
-size_t linear_states_bytes(const gdn::LinearShape& s) {
+// The segments' states, and behind them their rows' exponents.
+size_t linear_tops_at(const gdn::LinearShape& s) {
   return align_up((size_t)s.slots * s.hv * s.K * s.V * sizeof(float));
+}
+size_t linear_states_bytes(const gdn::LinearShape& s) {
+  return linear_tops_at(s) + align_up((size_t)s.slots * s.hv * 2 * sizeof(int));
+}
+int* linear_tops(const gdn::LinearShape& s, float* states) {
+  return reinterpret_cast<int*>(reinterpret_cast<char*>(states) + linear_tops_at(s));
 }
 
 cudaError_t linear_state(const gdn_linear_problem* p, const gdn::LinearState& a, cudaStream_t s) {
@@ -970,11 +977,12 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
   const gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
                         kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
                         vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);
-  if (T > 0) GDN_TRY(linear_state(p, {s, kr, vr, false, states}, stream));
+  int* tops = linear_tops(s, states);  // of k, and of v
+  if (T > 0) GDN_TRY(linear_state(p, {s, kr, vr, false, states, tops}, stream));
   GDN_TRY(gdn::linear_scan({s, false, states, h0, h_final}, stream));
   if (T > 0)
-    GDN_TRY(linear_pass(p, {s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr},
-                                  stream));
+    GDN_TRY(linear_pass(p, {s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr, tops,
+                            tops + 1, nullptr}, stream));
   return GDN_OK;
 }
 
@@ -1035,19 +1043,20 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
   const gdn::LinearRows gr =
       linear_rows(dout, (int64_t)s.hv * s.V, s.V, T, s.hv, s.hv);
   if (T > 0) {
-    GDN_TRY(linear_state(p, {s, kr, vr, false, h}, stream));
-    GDN_TRY(linear_state(p, {s, qr, gr, true, d}, stream));
+    GDN_TRY(linear_state(p, {s, kr, vr, false, h, linear_tops(s, h)}, stream));
+    GDN_TRY(linear_state(p, {s, qr, gr, true, d, linear_tops(s, d)}, stream));
     GDN_TRY(gdn::linear_scan({s, false, h, h0, nullptr}, stream));
   }
   GDN_TRY(gdn::linear_scan({s, true, d, dh_final, dh0}, stream));
   if (T > 0) {
     float* partial = reinterpret_cast<float*>(ws + L.partial);
-    GDN_TRY(linear_pass(p, {s, gr, vr, kr, s.V, s.K, false, true, h, dq, share, partial},
-                                  stream));
-    GDN_TRY(linear_pass(p, {s, vr, gr, qr, s.V, s.K, true, true, d, dk, share, partial},
-                                  stream));
-    GDN_TRY(linear_pass(p, {s, kr, qr, gr, s.K, s.V, true, false, d, dv, 1, nullptr},
-                                  stream));
+    const int *tk = linear_tops(s, h), *tv = tk + 1, *tq = linear_tops(s, d), *tg = tq + 1;
+    GDN_TRY(linear_pass(p, {s, gr, vr, kr, s.V, s.K, false, true, h, dq, share, partial, tv, tk, tg},
+                        stream));
+    GDN_TRY(linear_pass(p, {s, vr, gr, qr, s.V, s.K, true, true, d, dk, share, partial, tg, tq, tv},
+                        stream));
+    GDN_TRY(linear_pass(p, {s, kr, qr, gr, s.K, s.V, true, false, d, dv, 1, nullptr, tq, tg, tk},
+                        stream));
   }
   return GDN_OK;
 }

@@ -48,6 +48,7 @@ struct LinearState {
   LinearRows x, y;
   bool reverse;
   float* states;            // [slots, hv, K, V]
+  int* tops;                // tensor cores: [slots, hv, 2], 2^e above all of x's magnitudes, and y's
 };
 // The states that the segments start from, in place of U; the walk starts from `first` (null: 0) and
 // its end goes to `last` (null: nowhere), [N, hv, K, V] each.
@@ -66,7 +67,9 @@ struct LinearPass {
   const float* states;
   void* out;                // [T, hv / out_share, B]
   int out_share;            // value heads summed into one output head
-  float* partial;           // bf16 with out_share > 1: their running sum, [T, hv / out_share, B]
+  float* partial;           // bf16 with out_share > 1: their running sum, T hv / out_share B values
+  // tensor cores: entry 2 (slot hv + head) bounds these rows (see LinearState); z_top may be null
+  const int *x_top, *y_top, *z_top;
 };
 
 // fp32 arithmetic on the CUDA cores: every dtype and head size.

@@ -26,16 +26,24 @@ __device__ __forceinline__ bool elected() {
   return r != 0;
 }
 // Bounded wait of a warp: sleeps in hardware; gives up after about a second, or when another has.
+__device__ __forceinline__ void wait_longer(uint32_t bar, uint32_t parity, volatile int* failed) {
+  const long long began = clock64();
+  while (!*failed && !mbar_try(bar, parity))
+    if (clock64() - began > kWaitCycles) *failed = 1;
+}
+__device__ __forceinline__ void wait_one(uint32_t bar, uint32_t parity, volatile int* failed) {
+  if (!mbar_try(bar, parity)) wait_longer(bar, parity, failed);
+}
 __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile int* failed) {
-  bool done = mbar_try(bar, parity);
-  if (!done) {
-    const long long began = clock64();
-    while (!done && !*failed) {
-      done = mbar_try(bar, parity);
-      if (!done && clock64() - began > kWaitCycles) *failed = 1;
-    }
-  }
+  wait_one(bar, parity, failed);
   __syncwarp();
+}
+// A warpgroup's registers a thread, from now on (of the block's, which the groups share).
+template <int N> __device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void leave_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
 }
 // Bounded wait for work of one's own that is in flight, after another wait has given up.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity) {
@@ -68,6 +76,19 @@ __device__ __forceinline__ float two_to(int e) {
   return __uint_as_float((uint32_t)max(0, min(e, 127) + 127) << 23);
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+// packed bf16: the larger magnitudes, of the even and of the odd elements
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// e with |v| < 2^e for these magnitudes; of zeros the least
+__device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
+  const uint32_t m = max(packed_max & 0x7fffu, packed_max >> 16 & 0x7fffu);
+  return max(min((int)(m >> 7) - 126, 127), least);
+}
+
 // ------------------------------------------------------------------ a segment's own state
 
 // U = sum of weighted x y^T over a segment, to fp32 accuracy: y's rows times their powers of the decay
@@ -87,7 +108,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
                        const __grid_constant__ CUtensorMap my) {
   extern __shared__ uint8_t raw_smem[];
   __shared__ uint32_t tmem_at;
-  __shared__ int failed_word;
+  __shared__ int failed_word, top[2];
   volatile int* failed = &failed_word;
   stream_order();
   if (!linear::usable(a.s)) return;
@@ -101,6 +122,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
   const int tid = threadIdx.x, warp = tid / 32;
   if (tid == 0) {
     failed_word = 0;
+    top[0] = top[1] = -126;
     for (int i = 0; i < 2; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(done + 8 * i, 1);
@@ -117,10 +139,10 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
   __syncthreads();
   fence_after_sync();
   const uint32_t tm = tmem_at;
-  const int tiles = (int)((t1 - t0 + kTile - 1) / kTile);
+  const int begin = (int)t0, length = (int)(t1 - t0), tiles = (length + kTile - 1) / kTile;
   // the i-th tile of the walk, its tokens
-  auto first_token = [&](int i) { return t0 + (int64_t)(a.reverse ? tiles - 1 - i : i) * kTile; };
-  auto tokens = [&](int i) { const int64_t m = t1 - first_token(i); return m < kTile ? (int)m : kTile; };
+  auto first_token = [&](int i) { return begin + (a.reverse ? tiles - 1 - i : i) * kTile; };
+  auto tokens = [&](int i) { return min(begin + length - first_token(i), kTile); };
 
   if (warp == 8) {
     // ---------------------------------------------------------------- loads and products
@@ -129,7 +151,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
       if (elected()) {
         const uint32_t bar = full + 8 * (i & 1), x = base + StateSmem::X + (i & 1) * kRaw,
                        y = base + StateSmem::Y + (i & 1) * kRaw;
-        const int t = (int)first_token(i);
+        const int t = first_token(i);
         mbar_expect_tx(bar, 2 * kRaw);
         for (int b = 0; b < 2; ++b) {
           tma_box(x + b * (kRaw / 2), &mx, 64 * b, head / a.x.share, t, bar);
@@ -176,66 +198,95 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
     // ---------------------------------------------------------------- weights, parts, the sum
     const float log2a = linear::log2_decay(a.s, head);
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, cols = (uint32_t)(warp >> 2) * 64;
-    float u[64];
+    float2 u[32];
+    uint32_t x_max = 0, y_max = 0;
 #pragma unroll
-    for (int i = 0; i < 64; ++i) u[i] = 0.f;
+    for (int i = 0; i < 32; ++i) u[i] = make_float2(0.f, 0.f);
+    const float whole = linear::power(log2a, kTile);
     auto add = [&](int i) {  // tile i into u
+      const int m = tokens(i);
+      const float w = m == kTile ? whole : linear::power(log2a, m);
       wait_bar(done + 8 * (i & 1), (i >> 1) & 1, failed);
       fence_after_sync();
-      const float w = linear::power(log2a, tokens(i));
 #pragma unroll
-      for (int c = 0; c < 64; c += 16) {
+      for (int c = 0; c < 32; c += 8) {
         uint32_t p[16];
-        tmem_ld16_nw(tm + lanes + 128 * (i & 1) + cols + c, p);
+        tmem_ld16_nw(tm + lanes + 128 * (i & 1) + cols + 2 * c, p);
         tmem_wait_ld16(p);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) u[c + k] = fmaf(w, u[c + k], __uint_as_float(p[k]));
+        for (int k = 0; k < 8; ++k)
+          u[c + k] = __ffma2_rn(make_float2(w, w), u[c + k],
+                                make_float2(__uint_as_float(p[2 * k]), __uint_as_float(p[2 * k + 1])));
       }
     };
-    for (int i = 0; i < tiles; ++i) {
-      const uint32_t x = base + StateSmem::X + (i & 1) * kRaw, y = base + StateSmem::Y + (i & 1) * kRaw;
-      const int m = tokens(i);
-      wait_bar(full + 8 * (i & 1), (i >> 1) & 1, failed);
-      if (i > 0) wait_bar(done + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, failed);  // the parts' tiles
+    // A thread's 16-byte pieces of a tile are 4096 bytes apart: of rows r0, r0 + 32 of either block.
+    const int r0 = tid / 8;
 #pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t at = 16 * (tid + kWorkers * k);  // a 16-byte piece of a row
-        const int r = at / 128 % kTile;
-        const float w = linear::power(log2a, a.reverse ? r + 1 : m - 1 - r);
-        uint4 v = lds16(y + at), mid, lo;
-        uint32_t* pv = &v.x;
-        uint32_t* pm = &mid.x;
-        uint32_t* pl = &lo.x;
+    for (int i = 0; i <= tiles; ++i) {
+      if (i < tiles) {
+        const uint32_t at = 16 * tid, x = base + StateSmem::X + (i & 1) * kRaw + at,
+                       y = base + StateSmem::Y + (i & 1) * kRaw + at;
+        const int m = tokens(i);
+        float w[2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float f0 = r < m ? low(pv[j]) * w : 0.f, f1 = r < m ? high(pv[j]) * w : 0.f;
-          pv[j] = pack_bf2(f0, f1);
-          f0 -= low(pv[j]);
-          f1 -= high(pv[j]);
-          pm[j] = pack_bf2(f0, f1);
-          pl[j] = pack_bf2(f0 - low(pm[j]), f1 - high(pm[j]));
+        for (int k = 0; k < 2; ++k) {
+          const int r = r0 + 32 * k;
+          w[k] = r < m ? linear::power(log2a, a.reverse ? r + 1 : m - 1 - r) : 0.f;
         }
-        sts16(y + at, v);
-        sts16(base + StateSmem::MID + at, mid);
-        sts16(base + StateSmem::LOW + at, lo);
-        if (r >= m) sts16(x + at, make_uint4(0, 0, 0, 0));  // (another sequence's rows, or none)
+        wait_bar(full + 8 * (i & 1), (i >> 1) & 1, failed);
+        if (i > 0) wait_bar(done + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, failed);  // the parts' tiles
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const bool live = r0 + 32 * (k & 1) < m;
+          const float2 ww = k & 1 ? make_float2(w[1], w[1]) : make_float2(w[0], w[0]);
+          uint4 v = make_uint4(0, 0, 0, 0), mid = v, lo = v;
+          if (live) {
+            v = lds16(y + 4096 * k);
+            const uint4 xv = lds16(x + 4096 * k);
+            x_max = larger(larger(larger(larger(x_max, xv.x), xv.y), xv.z), xv.w);
+            y_max = larger(larger(larger(larger(y_max, v.x), v.y), v.z), v.w);
+            uint32_t* pv = &v.x;
+            uint32_t* pm = &mid.x;
+            uint32_t* pl = &lo.x;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float2 f = mul2(make_float2(low(pv[j]), high(pv[j])), ww);
+              pv[j] = pack_bf2(f.x, f.y);
+              f = __fadd2_rn(f, make_float2(-low(pv[j]), -high(pv[j])));
+              pm[j] = pack_bf2(f.x, f.y);
+              f = __fadd2_rn(f, make_float2(-low(pm[j]), -high(pm[j])));
+              pl[j] = pack_bf2(f.x, f.y);
+            }
+          } else {  // (another sequence's rows, or none)
+            sts16(x + 4096 * k, v);
+          }
+          sts16(y + 4096 * k, v);
+          sts16(base + StateSmem::MID + at + 4096 * k, mid);
+          sts16(base + StateSmem::LOW + at + 4096 * k, lo);
+        }
+        fence_async_smem();
+        fence_before_sync();
+        mbar_arrive(ready);
       }
-      fence_async_smem();
-      fence_before_sync();
-      mbar_arrive(ready);
       if (i > 0) add(i - 1);
     }
-    add(tiles - 1);
+    const int e_x = __reduce_max_sync(0xffffffffu, exponent_of(x_max, -126));
+    const int e_y = __reduce_max_sync(0xffffffffu, exponent_of(y_max, -126));
+    if (tid % 32 == 0) {
+      atomicMax(top, e_x);
+      atomicMax(top + 1, e_y);
+    }
     float* out = a.states + (slot * a.s.hv + head) * D * D + (int64_t)(tid & 127) * D + cols;
     if (!*failed) {
 #pragma unroll
-      for (int c = 0; c < 64; c += 4)
-        *reinterpret_cast<float4*>(out + c) = make_float4(u[c], u[c + 1], u[c + 2], u[c + 3]);
+      for (int c = 0; c < 32; c += 2)
+        *reinterpret_cast<float4*>(out + 2 * c) = make_float4(u[c].x, u[c].y, u[c + 1].x, u[c + 1].y);
     }
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
+  if (tid < 2) a.tops[2 * (slot * a.s.hv + head) + tid] = top[tid];
   if (warp == 8) tmem_dealloc(tm, 256);
   if (tid == 0 && *failed) set_status(a.s.status, GDN_ERR_DEVICE_TIMEOUT);
 }
@@ -246,54 +297,127 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
 // Per chunk, with i, j counted in the walk's direction, p_i = a^i and n the chunk's tokens:
 //     P = z x^T                       bf16 as loaded, into Tensor Memory
 //     W = P a^{i - j}, j <= i         fp16, in P's place: an operand in Tensor Memory
-//     O = W y + (p_i z) S             fp16 operands, one fp32 sum
+//     O = W y + (p_i z) S             fp16 operands, one fp32 sum; z's beside W
 //     S <- a^n S + (a^{n - j} x)^T y  fp16 operands; S fp32 in registers, its fp16 copy in shared memory
 // fp16's range is not bf16's, so operands are scaled by powers of two, which come off again in fp32:
-// a row of y, x or z by that of its largest magnitude, e_y, e_x, e_z; with M = max_j(e_x + e_y) and 2^E
-// a bound of S and of 2^(M + 7):
+// with 2^e_x, 2^e_y above all of a head's x and y in the segment (the state kernel has seen them), 2^e_z
+// above a row of z, or all of it, M = e_x + e_y, and 2^E a bound of S and of 2^(M + 7):
 //     y~ = y 2^(14 - e_y)     x~ = a^{n - j} x 2^(15 + e_y - M)     S~ = S 2^(15 - E)
 //     z~ = p_i z 2^(14 - e_z)   W~ = W 2^(15 + e_y - e_z - E)         O = O~ 2^(e_z + E - 29)
 // so that nothing can overflow that does not in fp32, and each rounding is half a step of fp16 (2^-11) of
 // a term, or 2^-38 of what bounds the sum.
+//
+// What bounds it is shared memory: a chunk's tiles go through it to the tensor cores (768 cycles of its
+// 128 bytes a cycle to arrive, 1536 as operands), twice more for x and y, whose rows change type there, and
+// S's copy and the outputs make it about 4900 of the 4300 that HBM takes for a chunk.  So z's rows go to
+// the tensor core through Tensor Memory, the outputs leave by TMA from z's tile, and a sum over value heads
+// is kept in an order of rows that its threads read together.
 constexpr int C = 128;
 constexpr uint32_t kTileBytes = C * D * 2, kBlock = kTileBytes / 2;  // (a block: 64 columns)
 constexpr int kWeightWarps = 4, kStateWarps = 8, kOpenWarps = 4;
-constexpr int kPassThreads = 32 * (kWeightWarps + kStateWarps + kOpenWarps + 2);
+constexpr int kPassThreads = 32 * (kWeightWarps + kStateWarps + kOpenWarps + 4);  // (warpgroups)
 constexpr int kFirstState = kWeightWarps, kFirstOpen = kFirstState + kStateWarps,
               kLoadWarp = kFirstOpen + kOpenWarps, kMmaWarp = kLoadWarp + 1;
-struct PassTables {           // a chunk's, double-buffered
-  int8_t ey[C], ez[C];        // (e_y, e_z clamped to [-113, 127], [-60, 127])
-  int M, E;
-};
 struct PassSmem {             // offsets from a 1024-byte boundary
   static constexpr uint32_t Z = 0, X = kTileBytes, Y = 2 * kTileBytes, stage = 3 * kTileBytes;
-  static constexpr uint32_t S = 2 * stage, POWERS = S + kTileBytes, TABLES = POWERS + C * 4;
-  static constexpr uint32_t BARS = TABLES + 2 * sizeof(PassTables), MISC = BARS + 20 * 8;
-  static constexpr int bytes = MISC + 48 + 1024;
+  static constexpr uint32_t S = 2 * stage, POWERS = S + kTileBytes, TARGETS = POWERS + (C + 32) * 4;
+  static constexpr uint32_t BARS = TARGETS + 2 * C * 4, MISC = BARS + 28 * 8;
+  static constexpr int bytes = MISC + 16 + 1024;
 };
 static_assert(PassSmem::bytes <= 232448, "shared memory of a block");
+// Registers: 640 threads launch with 96 each, 480 for the five warpgroups' warps of an SM's quarter; the
+// state's two take 136, the weights keep 88, opening and the last one 56 each: 472.
 // barriers: those of a pair alternate from chunk to chunk
-enum { kFull = 0, kScores = 2, kTables = 4, kWeights = 6, kOpened = 8, kFree = 10, kStateIn = 12,
-       kGrown, kTaken, kSums, kSumsRead, kStart, kEnd };
+enum { kFull = 0, kScores = 2, kValues = 4, kWeights = 6, kFree = 10, kSumsRead = 12,
+       kTargets = 14, kOut = 16, kRows = 18, kFullY = 20, kStateIn = 22, kGrown, kTaken, kSums, kStart, kEnd };
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-// e with |v| < 2^e for the largest magnitude in packed bf16 bits; of zeros the least
-__device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
-  const uint32_t m = max(packed_max & 0xffffu, packed_max >> 16);
-  return max(min((int)(m >> 7) - 126, 127), least);
+// Rows of a tile, a thread each.  (A row's logical 16-byte piece p lies at p ^ (row & 7) of its block, so
+// that neighbouring rows' threads meet different banks.)
+__device__ __forceinline__ uint32_t piece(uint32_t tile, int row, int p) {
+  return tile + (p >> 3) * kBlock + row * 128 + ((p & 7 ^ row & 7) << 4);
 }
-// packed bf16 times f, as packed fp16
-__device__ __forceinline__ uint32_t to_half2(uint32_t bf2, float f) {
-  return pack_h2(low(bf2) * f, high(bf2) * f);
+// the largest magnitudes of a row of bf16, of even and odd elements
+__device__ __forceinline__ uint32_t row_max_of(uint32_t tile, int row) {
+  uint32_t m[4] = {};
+#pragma unroll 4
+  for (int p = 0; p < 16; ++p) {
+    const uint4 v = lds16(piece(tile, row, p));
+    m[0] = larger(m[0], v.x);
+    m[1] = larger(m[1], v.y);
+    m[2] = larger(m[2], v.z);
+    m[3] = larger(m[3], v.w);
+  }
+  return larger(larger(m[0], m[1]), larger(m[2], m[3]));
+}
+// Four pieces of a row of bf16 times f, as packed fp16.
+__device__ __forceinline__ void open_pieces(uint32_t tile, int row, int p0, float f, uint4 (&v)[4]) {
+  const float2 ff = make_float2(f, f);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) v[p] = lds16(piece(tile, row, p0 + p));
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    uint32_t* w = &v[p].x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = mul2(make_float2(low(w[j]), high(w[j])), ff);
+      w[j] = pack_h2(x.x, x.y);
+    }
+  }
+}
+// A row in its place; zeros where it is not live.
+__device__ __forceinline__ void open_row(uint32_t tile, int row, bool live, float f) {
+  if (live) {
+#pragma unroll 1
+    for (int p0 = 0; p0 < 16; p0 += 4) {
+      uint4 v[4];
+      open_pieces(tile, row, p0, f, v);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) sts16(piece(tile, row, p0 + p), v[p]);
+    }
+  } else {
+#pragma unroll 1
+    for (int p = 0; p < 16; ++p) sts16(piece(tile, row, p), make_uint4(0, 0, 0, 0));
+  }
+  __syncwarp();
+}
+// Exponents of a head's rows in a segment: 2^e above all of them.
+__device__ __forceinline__ int top_of(const int* tops, int64_t at, int least) {
+  return max(min(tops[2 * at], 127), least);
+}
+// |S| < 2^E for what S starts from and what the chunks have added (2^M bounds a product), kept as b 2^q.
+struct Bound {
+  float b, whole, grown;  // a^C and C 2^(M - q): what a whole chunk does
+  int q, M;
+  __device__ __forceinline__ void start(float max_s, int m, float log2a) {
+    M = m;
+    q = max((int)(__float_as_uint(max_s) >> 23) - 126, M + 7);
+    b = 1.f;
+    whole = linear::power(log2a, C);
+    grown = C * two_to(M - q);
+  }
+  __device__ __forceinline__ int E() const {
+    return max((int)(__float_as_uint(b) >> 23) - 126 + q, M + 7);
+  }
+  // (a chunk of fewer tokens is the walk's first or last: it may count as whole where it adds, and
+  // decays by what it has)
+  __device__ __forceinline__ void grow(float decay) { b = fmaxf(fmaf(decay, b, grown), 0x1p-120f); }
+};
+__device__ __forceinline__ void tma_out(const CUtensorMap* map, uint32_t src, int x, int head, int t0) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(map)), "r"(src), "r"(x), "r"(head), "r"(t0)
+               : "memory");
 }
 
+// REVERSE: the walk goes backward in time.  SUM: an output head has several value heads.
+template <bool REVERSE, bool SUM>
 __global__ void __launch_bounds__(kPassThreads, 1)
 linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz,
-                      const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my) {
+                      const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
+                      const __grid_constant__ CUtensorMap mo) {
   extern __shared__ uint8_t raw_smem[];
   stream_order();
   if (!linear::usable(a.s)) return;
-  const int heads = a.s.hv / a.out_share;
+  const int share = SUM ? a.out_share : 1, heads = a.s.hv / share;
   const int oh = blockIdx.x % heads;
   const int64_t slot = blockIdx.x / heads;
   int n;
@@ -301,11 +425,10 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
   if (!linear::slot_tokens(a.s, slot, n, t0, t1)) return;
   const uint32_t base = (saddr(raw_smem) + 1023u) & ~1023u;
   uint8_t* const gbase = raw_smem + (base - saddr(raw_smem));
-  float* const powers = reinterpret_cast<float*>(gbase + PassSmem::POWERS);
-  PassTables* const tables = reinterpret_cast<PassTables*>(gbase + PassSmem::TABLES);
+  float* const powers = reinterpret_cast<float*>(gbase + PassSmem::POWERS) + 32;  // [-32, C)
+  int* const targets = reinterpret_cast<int*>(gbase + PassSmem::TARGETS);  // e_z of two chunks' rows
   int* const misc = reinterpret_cast<int*>(gbase + PassSmem::MISC);
-  volatile int* const failed = misc;       // 0: failed, 1: Tensor Memory, 2-3: max |S| at a head's start,
-  int* const row_max = misc + 4;           // 4-11: a chunk's M by warp, twice
+  volatile int* const failed = misc;       // 0: failed, 1: Tensor Memory, 2-3: max |S| at a head's start
   const uint32_t bars = base + PassSmem::BARS;
   auto bar = [&](int which, int it) { return bars + 8 * (which + (it & 1)); };
   auto one = [&](int which) { return bars + 8 * which; };
@@ -315,17 +438,20 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
     misc[0] = misc[2] = misc[3] = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kFull, i), 1);
+      mbar_init(bar(kFullY, i), 1);
       mbar_init(bar(kScores, i), 1);
       mbar_init(bar(kFree, i), 1);
-      mbar_init(bar(kTables, i), 32 * kOpenWarps);
+      mbar_init(bar(kValues, i), 32 * kOpenWarps);
       mbar_init(bar(kWeights, i), 32 * kWeightWarps);
-      mbar_init(bar(kOpened, i), 32 * kOpenWarps);
+      mbar_init(bar(kRows, i), 32 * kOpenWarps);
+      mbar_init(bar(kTargets, i), 32 * kWeightWarps);
+      mbar_init(bar(kSumsRead, i), 32 * kStateWarps);
+      mbar_init(bar(kOut, i), 32 * kStateWarps);
     }
     mbar_init(one(kStateIn), 32 * kStateWarps);
     mbar_init(one(kGrown), 1);
     mbar_init(one(kTaken), 32 * kStateWarps);
     mbar_init(one(kSums), 1);
-    mbar_init(one(kSumsRead), 32 * kWeightWarps);
     mbar_init(one(kStart), 32 * kStateWarps);
     mbar_init(one(kEnd), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -337,96 +463,141 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tm = (uint32_t)misc[1], tm_o = tm + 256, tm_g = tm + 384;  // P twice, O, growth of S
-  const int chunks = (int)((t1 - t0 + C - 1) / C), total = chunks * a.out_share;
-  auto first_token = [&](int c) { return t0 + (int64_t)(a.reverse ? chunks - 1 - c : c) * C; };
-  auto tokens = [&](int c) { const int64_t m = t1 - first_token(c); return m < C ? (int)m : C; };
+  constexpr uint32_t tm = 0;  // (all of Tensor Memory: its first column)
+  const uint32_t tm_o = tm + 256, tm_g = tm + 384;  // P twice, O, growth of S
+  const int begin = (int)t0, length = (int)(t1 - t0);
+  const int chunks = (length + C - 1) / C, total = chunks * share;
+  auto first_token = [&](int c) { return begin + (REVERSE ? chunks - 1 - c : c) * C; };
+  auto tokens = [&](int c) { return min(begin + length - first_token(c), C); };
 
   if (warp == kLoadWarp) {
-    // ---------------------------------------------------------------- loads
-    int it = 0;
-    for (int g = 0; g < a.out_share && !*failed; ++g) {
-      const int head = oh * a.out_share + g;
-      for (int c = 0; c < chunks; ++c, ++it) {
-        if (it >= 2) wait_bar(bar(kFree, it), half(it - 2), failed);
-        if (*failed) break;
-        if (elected()) {
-          const uint32_t b = bar(kFull, it), st = base + (it & 1) * PassSmem::stage;
-          const int t = (int)first_token(c);
-          mbar_expect_tx(b, PassSmem::stage);
+    // ---------------------------------------------------------------- loads, and the outputs' stores
+    leave_registers<56>();
+    if (lane == 0) {
+      int loaded = 0, next_c = 0, head = oh * share;  // of the next loads
+#pragma unroll 1
+      for (int it = -2, c = -2, g = 0; it < total; ++it) {  // (chunk it is given out, it + 2 loaded)
+        const bool more = loaded < total;
+        const uint32_t st = base + (it & 1) * PassSmem::stage;
+        const int t = first_token(next_c);
+        if (more) {
+          if (it >= 0) wait_one(bar(kFree, it), half(it), failed);
+          if (*failed) break;
+          const uint32_t b = bar(kFull, it);
+          mbar_expect_tx(b, 2 * kTileBytes);
+          const int zh = head / a.z.share, xh = head / a.x.share;
+#pragma unroll 1
           for (int k = 0; k < 2; ++k) {
-            tma_box(st + PassSmem::Z + k * kBlock, &mz, 64 * k, head / a.z.share, t, b);
-            tma_box(st + PassSmem::X + k * kBlock, &mx, 64 * k, head / a.x.share, t, b);
+            tma_box(st + PassSmem::Z + k * kBlock, &mz, 64 * k, zh, t, b);
+            tma_box(st + PassSmem::X + k * kBlock, &mx, 64 * k, xh, t, b);
           }
-          for (int k = 0; k < 2; ++k)
-            tma_box(st + PassSmem::Y + k * kBlock, &my, 64 * k, head / a.y.share, t, b);
         }
-        __syncwarp();
+        if (it >= 0) {
+          wait_one(bar(kOut, it), half(it), failed);
+          if (*failed) break;
+          if (g + 1 == share && tokens(c) == C) {
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k)
+              tma_out(&mo, st + PassSmem::Y + k * kBlock, 64 * k, oh, first_token(c));
+            asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+            if (more) bulk_wait_read();
+          }
+        }
+        if (more) {
+          const uint32_t b = bar(kFullY, it);
+          mbar_expect_tx(b, kTileBytes);
+          const int yh = head / a.y.share;
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) tma_box(st + PassSmem::Y + k * kBlock, &my, 64 * k, yh, t, b);
+          ++loaded;
+          if (++next_c == chunks) {
+            next_c = 0;
+            ++head;
+          }
+        }
+        if (++c == chunks) {
+          c = 0;
+          ++g;
+        }
       }
+      bulk_wait_all();
+      if (*failed)
+        for (int i = loaded > 2 ? loaded - 2 : 0; i < loaded; ++i) {
+          drain(bar(kFull, i), half(i));
+          drain(bar(kFullY, i), half(i));
+        }
+      if (*failed && loaded < total) drain(bar(kFull, loaded), half(loaded));
     }
-    if (*failed && lane == 0)
-      for (int i = it > 2 ? it - 2 : 0; i < it; ++i) drain(bar(kFull, i), half(i));
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
+    leave_registers<56>();
     const uint32_t id_p = idesc_f16(128, 128, 0, 0, 1), id_o = idesc_f16(128, 128, 0, 1),
                    id_g = idesc_f16(128, 128, 1, 1);
-    auto scores = [&](int it) {
-      wait_bar(bar(kFull, it), half(it), failed);
-      fence_after_sync();
-      const uint32_t st = base + (it & 1) * PassSmem::stage;
-      if (elected()) {
+    // rows by features (the contraction's index contiguous), and features or columns by rows
+    const uint64_t of_rows = sdesc(base, 16, 1024), of_cols = sdesc(base, kBlock, 1024);
+    // A chunk takes two turns: the state's growth, the sums.  The next chunk's scores are made behind the
+    // one when its tiles are there already, else behind the other; the first chunk's before all.
+    int grown = 0, scored = 0;
+#pragma unroll 1
+    for (int turn = -1, c = 0; turn < 2 * total && !*failed; ++turn) {
+      const int it = turn >> 1;
+      const uint64_t x = of_cols + (((it & 1) * PassSmem::stage + PassSmem::X) >> 4),
+                     y = of_cols + (((it & 1) * PassSmem::stage + PassSmem::Y) >> 4);
+      if (turn >= 0 && !(turn & 1)) {
+        wait_bar(bar(kValues, it), half(it), failed);  // (and x)
+        if (c + 1 < chunks) {
+          if (grown > 0) wait_bar(one(kTaken), (grown - 1) & 1, failed);
+          fence_after_sync();
+          if (elected()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t at = (ks >> 2) * kBlock + (ks & 3) * 32;
-          mma_ss(tm + 128 * (it & 1), sdesc(st + PassSmem::Z + at, 16, 1024),
-                 sdesc(st + PassSmem::X + at, 16, 1024), id_p, ks > 0);
+            for (int ks = 0; ks < 8; ++ks) mma_ss(tm_g, x + ks * 128, y + ks * 128, id_g, ks > 0);
+            mma_commit(one(kGrown));
+          }
+          __syncwarp();
+          ++grown;
         }
-        mma_commit(bar(kScores, it));
-      }
-      __syncwarp();
-    };
-    scores(0);
-    int grown = 0;
-    for (int it = 0, c = 0; it < total && !*failed; ++it, c = c + 1 == chunks ? 0 : c + 1) {
-      const uint32_t st = base + (it & 1) * PassSmem::stage;
-      if (it + 1 < total) scores(it + 1);
-      wait_bar(bar(kTables, it), half(it), failed);
-      wait_bar(bar(kOpened, it), half(it), failed);
-      if (c + 1 < chunks) {
-        if (grown > 0) wait_bar(one(kTaken), (grown - 1) & 1, failed);
+      } else if (turn >= 0) {
+        const uint32_t w = tm + 128 * (it & 1);
+        wait_bar(bar(kWeights, it), half(it), failed);
+        if (it > 0) wait_bar(bar(kSumsRead, it - 1), half(it - 1), failed);
+        fence_after_sync();
+        if (elected()) {
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) mma_ts(tm_o, w + 8 * ks, y + ks * 128, id_o, ks > 0);
+        }
+        __syncwarp();
+        wait_bar(bar(kTargets, it), half(it), failed);
+        wait_bar(one(kStateIn), it & 1, failed);
         fence_after_sync();
         if (elected()) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ss(tm_g, sdesc(st + PassSmem::X + ks * 2048, kBlock, 1024),
-                   sdesc(st + PassSmem::Y + ks * 2048, kBlock, 1024), id_g, ks > 0);
-          mma_commit(one(kGrown));
+            mma_ts(tm_o, w + 64 + 8 * ks, of_cols + (PassSmem::S >> 4) + ks * 128, id_o, 1);
+          mma_commit(one(kSums));
+          mma_commit(bar(kFree, it));
         }
         __syncwarp();
-        ++grown;
+        c = c + 1 == chunks ? 0 : c + 1;
       }
-      wait_bar(bar(kWeights, it), half(it), failed);
-      if (it > 0) wait_bar(one(kSumsRead), (it - 1) & 1, failed);
-      fence_after_sync();
-      if (elected()) {
+      if (scored < total && scored <= it + 1 &&
+          ((turn & 1) ||
+           __shfl_sync(0xffffffffu, mbar_test(bar(kFull, scored), half(scored)), 0))) {
+        wait_bar(bar(kFull, scored), half(scored), failed);
+        fence_after_sync();
+        const uint64_t z = of_rows + (((scored & 1) * PassSmem::stage + PassSmem::Z) >> 4),
+                       xr = of_rows + (((scored & 1) * PassSmem::stage + PassSmem::X) >> 4);
+        if (elected()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ts(tm_o, tm + 128 * (it & 1) + 8 * ks, sdesc(st + PassSmem::Y + ks * 2048, kBlock, 1024),
-                 id_o, ks > 0);
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+            mma_ss(tm + 128 * (scored & 1), z + at, xr + at, id_p, ks > 0);
+          }
+          mma_commit(bar(kScores, scored));
+        }
+        __syncwarp();
+        ++scored;
       }
-      __syncwarp();
-      wait_bar(one(kStateIn), it & 1, failed);
-      fence_after_sync();
-      if (elected()) {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_ss(tm_o, sdesc(st + PassSmem::Z + (ks >> 2) * kBlock + (ks & 3) * 32, 16, 1024),
-                 sdesc(base + PassSmem::S + ks * 2048, kBlock, 1024), id_o, 1);
-        mma_commit(one(kSums));
-        mma_commit(bar(kFree, it));
-      }
-      __syncwarp();
     }
     if (*failed) {
       if (elected()) {
@@ -436,248 +607,317 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       __syncwarp();
     }
   } else if (warp < kWeightWarps) {
-    // ---------------------------------------------------------------- weights, and the outputs
-    const int row = tid;  // its lane of Tensor Memory
+    // ---------------------------------------------------------------- weights; z to Tensor Memory
+    leave_registers<88>();
+    const int row = tid;  // its lane of Tensor Memory, and row of z
     const uint32_t lanes = (uint32_t)warp * 32 << 16;
-    const int64_t ots = (int64_t)heads * D;
-    float log2a = 0.f;
-    auto give = [&](int it, int c, int g) {
-      const int m = tokens(c);
-      const int64_t at = (first_token(c) + row) * ots + (int64_t)oh * D;
-      wait_bar(one(kSums), it & 1, failed);
-      fence_after_sync();
-      const PassTables& tab = tables[it & 1];
-      const int e = tab.ez[row] + tab.E - 29;
-      const float s0 = two_to(e / 2), s1 = two_to(e - e / 2);
-      const bool live = row < m && !*failed;
-#pragma unroll
-      for (int k = 0; k < D; k += 32) {
-        uint32_t o[2][16];
-        tmem_ld16_nw(tm_o + lanes + k, o[0]);
-        tmem_ld16_nw(tm_o + lanes + k + 16, o[1]);
-        tmem_wait_ld16x2(o[0], o[1]);
-        if (live) {
-          float f[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i / 16][i % 16]) * s0 * s1;
-          if (g > 0) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 before = *reinterpret_cast<const float4*>(a.partial + at + k + i);
-              f[i] += before.x; f[i + 1] += before.y; f[i + 2] += before.z; f[i + 3] += before.w;
-            }
-          }
-          if (g + 1 < a.out_share) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<float4*>(a.partial + at + k + i) =
-                  make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at + k + i) =
-                  make_uint4(pack_bf2(f[i], f[i + 1]), pack_bf2(f[i + 2], f[i + 3]),
-                             pack_bf2(f[i + 4], f[i + 5]), pack_bf2(f[i + 6], f[i + 7]));
-          }
-        }
-        __syncwarp();
-      }
-      fence_before_sync();
-      mbar_arrive(one(kSumsRead));
-    };
-    int it = 0, c_before = 0, g_before = 0;  // (a chunk's outputs follow the next one's weights)
-    for (int g = 0; g < a.out_share; ++g) {
-      log2a = linear::log2_decay(a.s, oh * a.out_share + g);
-      named_bar(1, 32 * kWeightWarps);  // (the last head's powers have been read)
-      powers[row] = linear::power(log2a, row);
+    int it = 0;
+    for (int g = 0; g < share; ++g) {
+      const int64_t at = slot * a.s.hv + oh * share + g;
+      const float log2a = linear::log2_decay(a.s, oh * share + g);
+      const int ex = top_of(a.x_top, at, -110), ey = top_of(a.y_top, at, -110);
+      const int ez_all = a.z_top ? top_of(a.z_top, at, -60) : 0;
+      wait_bar(one(kStart), g & 1, failed);
+      Bound bound;
+      bound.start(__int_as_float(((volatile int*)misc)[2 + (g & 1)]), max(ex + ey, -97), log2a);
+      // W~'s factor 2^(15 + e_y - e_z - E) in two, each in fp32's range
+      const int h = max(0, -59 - bound.M);
+      named_bar(1, 32 * kWeightWarps);  // (the last head's powers have been read, this one's max |S|)
+      if (row == 0) misc[2 + (~g & 1)] = 0;  // for the next head (who used it has read it)
+      // a^i 2^(e_y + h), 0 for i < 0
+      powers[row] = linear::power(log2a, row) * two_to(ey + h);
+      if (row < 32) powers[row - 32] = 0.f;
       named_bar(1, 32 * kWeightWarps);
+      float2 step[8];  // those of |a 16-column piece's far end - column|
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        step[i] = REVERSE ? make_float2(powers[2 * i], powers[2 * i + 1])
+                            : make_float2(powers[15 - 2 * i], powers[14 - 2 * i]);
+      const float z_whole = linear::power(log2a, REVERSE ? C - 1 - row : row);
       for (int c = 0; c < chunks; ++c, ++it) {
-        const int m = tokens(c);
-        wait_bar(bar(kTables, it), half(it), failed);
+        const int m = tokens(c), E = bound.E();
+        bound.grow(m == C ? bound.whole : linear::power(log2a, m));
+        if (!a.z_top) wait_bar(bar(kRows, it), half(it), failed);
         wait_bar(bar(kScores, it), half(it), failed);
         fence_after_sync();
-        const PassTables& tab = tables[it & 1];
-        const int e = 15 - tab.ez[row] - tab.E;
-        const float s0 = two_to(e / 2), s1 = two_to(e - e / 2);
+        const int ez = a.z_top ? ez_all : targets[C * (it & 1) + row];
+        const float mine = two_to(15 - ez - E - h);
         const uint32_t p_at = tm + lanes + 128 * (it & 1);
 #pragma unroll 1
-        for (int k = 0; k < C; k += 16) {  // (whole pieces of the triangle that are zero are not read)
-          const bool none = a.reverse ? k + 15 < 32 * warp : k > 32 * warp + 31;
-          uint32_t w[8];
-          if (none) {
+        for (int k0 = 0; k0 < C; k0 += 32) {
+          // (32 x 32 pieces on the far side of the diagonal, or behind the last token, are not read)
+          const int first = 32 * warp;
+          uint32_t w[2][8] = {};
+          if ((REVERSE ? k0 >= first : k0 <= first) && k0 < m) {
+            uint32_t p[2][16];
+            tmem_ld16_nw(p_at + k0, p[0]);
+            tmem_ld16_nw(p_at + k0 + 16, p[1]);
+            tmem_wait_ld16x2(p[0], p[1]);
+            if (k0 != first) {  // a^|i - j| as a power of the row and one of the column
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 0u;
-          } else {
-            uint32_t p[16];
-            tmem_ld16_nw(p_at + k, p);
-            tmem_wait_ld16(p);
+              for (int q = 0; q < 2; ++q) {
+                const int k = k0 + 16 * q;
+                const float r = mine * linear::power(log2a, REVERSE ? k - row : row - k - 15);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              float f[2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const int s = k + i + j, gap = a.reverse ? s - row : row - s;
-                const float v = __uint_as_float(p[i + j]) * s0 * s1 * powers[gap & (C - 1)] *
-                                two_to(tab.ey[s]);
-                f[j] = gap >= 0 && s < m ? v : 0.f;
+                for (int j = 0; j < 8; ++j) {
+                  const float2 f = mul2(mul2(make_float2(__uint_as_float(p[q][2 * j]),
+                                                         __uint_as_float(p[q][2 * j + 1])),
+                                             make_float2(r, r)), step[j]);
+                  w[q][j] = pack_h2(f.x, f.y);
+                }
               }
-              w[i / 2] = pack_h2(f[0], f[1]);
+            } else {  // across the diagonal
+              const float* const at = powers + (REVERSE ? -lane : lane);
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const int t = 16 * q + 2 * j;
+                  const float2 f = mul2(mul2(make_float2(__uint_as_float(p[q][2 * j]),
+                                                         __uint_as_float(p[q][2 * j + 1])),
+                                             make_float2(mine, mine)),
+                                        REVERSE ? make_float2(at[t], at[t + 1])
+                                                  : make_float2(at[-t], at[-t - 1]));
+                  w[q][j] = pack_h2(f.x, f.y);
+                }
+            }
+            if (k0 + 32 > m) {  // (columns of another sequence's rows, or of none)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const int left = m - k0 - 16 * q - 2 * j;
+                  w[q][j] = left > 1 ? w[q][j] : left == 1 ? w[q][j] & 0xffffu : 0u;
+                }
             }
           }
-          tmem_st8_nw(p_at + k / 2, w);
+          tmem_st8_nw(p_at + k0 / 2, w[0]);
+          tmem_st8_nw(p_at + k0 / 2 + 8, w[1]);
         }
         tmem_wait_st();
         fence_before_sync();
         mbar_arrive(bar(kWeights, it));
-        if (it > 0) give(it - 1, c_before, g_before);
-        c_before = c;
-        g_before = g;
+        // z goes behind W, where P has been read.  (Rows behind the chunk's last token: whatever they
+        // hold ends in rows of O that nobody reads.)
+        const float z_scale =
+            two_to(14 - ez) *
+            (!REVERSE || m == C ? z_whole : row < m ? linear::power(log2a, m - 1 - row) : 0.f);
+#pragma unroll 1
+        for (int p0 = 0; p0 < 16; p0 += 4) {
+          uint4 v[4];
+          open_pieces(base + (it & 1) * PassSmem::stage + PassSmem::Z, row, p0, z_scale, v);
+#pragma unroll
+          for (int p = 0; p < 4; p += 2) {
+            const uint32_t w[8] = {v[p].x, v[p].y, v[p].z, v[p].w,
+                                   v[p + 1].x, v[p + 1].y, v[p + 1].z, v[p + 1].w};
+            tmem_st8_nw(p_at + 64 + 4 * (p0 + p), w);
+          }
+        }
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(bar(kTargets, it));
       }
     }
-    give(total - 1, c_before, g_before);
   } else if (warp < kFirstOpen) {
-    // ---------------------------------------------------------------- the state
+    // ---------------------------------------------------------------- the state, and the outputs
+    take_registers<136>();
     const int st = tid - 32 * kFirstState, row = st & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, cols = (uint32_t)(st >> 7) * 64;
     const uint32_t copy = base + PassSmem::S + (st >> 7) * kBlock + row * 128;
-    float S[64];
-    int it = 0, grown = 0;
-    for (int g = 0; g < a.out_share; ++g) {
-      const int head = oh * a.out_share + g;
-      const float log2a = linear::log2_decay(a.s, head);
-      const float* from = a.states + (slot * a.s.hv + head) * D * D;
-      const float enter = a.reverse ? 1.f : linear::power(log2a, 1);
-      uint32_t top = 0;
+    const uint32_t turn = (uint32_t)(row & 7);
+    float2 S[32];
+    auto give = [&](int it, int c, int g, int E, int ez_all) {  // (its sums are there)
+      const int m = tokens(c), e = (a.z_top ? ez_all : targets[C * (it & 1) + row]) + E - 29;
+      const int near = max(-126, min(e, 127));
+      const float s0 = two_to(near);
+      const bool far = __any_sync(0xffffffffu, near != e), live = row < m && !*failed;
+      const bool last = !SUM || g + 1 == share;
+      const uint32_t tile = base + (it & 1) * PassSmem::stage + PassSmem::Y + (st >> 7) * kBlock + row * 128;
+#pragma unroll 1
+      for (int k = 0; k < 64; k += 32) {
+        uint32_t o[2][16];
+        tmem_ld16_nw(tm_o + lanes + cols + k, o[0]);
+        tmem_ld16_nw(tm_o + lanes + cols + k + 16, o[1]);
+        tmem_wait_ld16x2(o[0], o[1]);
+        if (k == 32) {  // (the next chunk's sums may take their place)
+          fence_before_sync();
+          mbar_arrive(bar(kSumsRead, it));
+        }
+        float2 f[16];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) {
-        S[i] = enter * (a.transposed ? from[(cols + i) * D + row] : from[row * D + cols + i]);
-        top = max(top, __float_as_uint(S[i]) & 0x7fffffffu);
+        for (int i = 0; i < 16; ++i)
+          f[i] = mul2(make_float2(__uint_as_float(o[i / 8][2 * i % 16]),
+                                  __uint_as_float(o[i / 8][2 * i % 16 + 1])), make_float2(s0, s0));
+        if (far) {
+          const float s1 = two_to(e - near);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) f[i] = mul2(f[i], make_float2(s1, s1));
+        }
+        if (SUM) {  // the running sum of a chunk: row after row of each four columns
+          float4* const sum =
+              reinterpret_cast<float4*>(a.partial + ((int64_t)oh * a.s.T + first_token(c)) * D) +
+              (int64_t)((cols + k) / 4) * m + row;
+          if (g > 0 && live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 before = sum[i * m];
+              f[2 * i].x += before.x; f[2 * i].y += before.y;
+              f[2 * i + 1].x += before.z; f[2 * i + 1].y += before.w;
+            }
+          }
+          if (!last && live) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              sum[i * m] = make_float4(f[2 * i].x, f[2 * i].y, f[2 * i + 1].x, f[2 * i + 1].y);
+          }
+        }
+        if (last) {
+          uint4 b[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            b[i] = make_uint4(pack_bf2(f[4 * i].x, f[4 * i].y), pack_bf2(f[4 * i + 1].x, f[4 * i + 1].y),
+                              pack_bf2(f[4 * i + 2].x, f[4 * i + 2].y),
+                              pack_bf2(f[4 * i + 3].x, f[4 * i + 3].y));
+          if (m == C) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sts16(tile + (((k / 8 + i) ^ turn) << 4), b[i]);
+          } else if (live) {
+            uint4* const out = reinterpret_cast<uint4*>(
+                static_cast<__nv_bfloat16*>(a.out) + ((int64_t)(first_token(c) + row) * heads + oh) * D +
+                cols + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) out[i] = b[i];
+          }
+        }
+        __syncwarp();
       }
-      atomicMax(misc + 2 + (g & 1), (int)__reduce_max_sync(0xffffffffu, top));
-      mbar_arrive(one(kStart));
-      for (int c = 0; c < chunks; ++c, ++it) {
-        wait_bar(bar(kTables, it), half(it), failed);
-        const int M = tables[it & 1].M;
-        const float scale = two_to(15 - tables[it & 1].E);
-        if (it > 0) wait_bar(one(kSums), (it - 1) & 1, failed);  // (the last chunk's use of the copy)
+      fence_async_smem();
+      mbar_arrive(bar(kOut, it));
+    };
+    int grown = 0, c = 0, g = 0, c_before = 0, g_before = 0, E_before = 0, ez_before = 0, E = 0, ez = 0;
+    float log2a = 0.f;
+    Bound bound = {};
+#pragma unroll 1
+    for (int it = 0; it <= total; ++it) {
+      if (it < total && c == 0) {
+        const int64_t where = slot * a.s.hv + oh * share + g;
+        log2a = linear::log2_decay(a.s, oh * share + g);
+        const float* from = a.states + where * D * D;
+        const int M = max(top_of(a.x_top, where, -110) + top_of(a.y_top, where, -110), -97);
+        const float enter = REVERSE ? 1.f : linear::power(log2a, 1);
+        uint32_t top = 0;
+        if (a.transposed) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          sts16(copy + ((k ^ (row & 7)) << 4),
-                make_uint4(pack_h2(S[8 * k] * scale, S[8 * k + 1] * scale),
-                           pack_h2(S[8 * k + 2] * scale, S[8 * k + 3] * scale),
-                           pack_h2(S[8 * k + 4] * scale, S[8 * k + 5] * scale),
-                           pack_h2(S[8 * k + 6] * scale, S[8 * k + 7] * scale)));
+          for (int i = 0; i < 32; ++i)
+            S[i] = make_float2(from[(cols + 2 * i) * D + row], from[(cols + 2 * i + 1) * D + row]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float4 v = *reinterpret_cast<const float4*>(from + row * D + cols + 2 * i);
+            S[i] = make_float2(v.x, v.y);
+            S[i + 1] = make_float2(v.z, v.w);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          S[i] = mul2(S[i], make_float2(enter, enter));
+          top = max(top, max(__float_as_uint(S[i].x) & 0x7fffffffu, __float_as_uint(S[i].y) & 0x7fffffffu));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) atomicMax(misc + 2 + (g & 1), (int)top);
+        mbar_arrive(one(kStart));
+        wait_bar(one(kStart), g & 1, failed);
+        ez = a.z_top ? top_of(a.z_top, where, -60) : 0;
+        bound.start(__int_as_float(((volatile int*)misc)[2 + (g & 1)]), M, log2a);
+      }
+      if (it > 0) {  // (the last chunk's use of the copy)
+        wait_bar(one(kSums), (it - 1) & 1, failed);
+        fence_after_sync();
+        give(it - 1, c_before, g_before, E_before, ez_before);
+      }
+      if (it < total) {
+        E = bound.E();
+        const float s = two_to(15 - E);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float2 f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[i] = mul2(S[4 * k + i], make_float2(s, s));
+          sts16(copy + ((k ^ turn) << 4), make_uint4(pack_h2(f[0].x, f[0].y), pack_h2(f[1].x, f[1].y),
+                                                     pack_h2(f[2].x, f[2].y), pack_h2(f[3].x, f[3].y)));
+        }
         fence_async_smem();
         mbar_arrive(one(kStateIn));
+      }
+      if (it < total) {
+        const int m = tokens(c);
+        const float w = m == C ? bound.whole : linear::power(log2a, m);
+        bound.grow(w);
         if (c + 1 < chunks) {
-          const float w = linear::power(log2a, tokens(c)), add = two_to(M - 29);
+          const float add = two_to(bound.M - 29);
           wait_bar(one(kGrown), grown & 1, failed);
           fence_after_sync();
 #pragma unroll
-          for (int k = 0; k < 64; k += 16) {
+          for (int k = 0; k < 32; k += 8) {
             uint32_t p[16];
-            tmem_ld16_nw(tm_g + lanes + cols + k, p);
+            tmem_ld16_nw(tm_g + lanes + cols + 2 * k, p);
             tmem_wait_ld16(p);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              S[k + i] = fmaf(w, S[k + i], __uint_as_float(p[i]) * add);
+            for (int i = 0; i < 8; ++i)
+              S[k + i] = __ffma2_rn(S[k + i], make_float2(w, w),
+                                    mul2(make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1])),
+                                         make_float2(add, add)));
           }
           fence_before_sync();
           mbar_arrive(one(kTaken));
           ++grown;
         }
       }
+      c_before = c;
+      g_before = g;
+      E_before = E;
+      ez_before = ez;
+      if (++c == chunks) {
+        c = 0;
+        ++g;
+      }
     }
-  } else {
+  } else if (warp < kLoadWarp) {
     // ---------------------------------------------------------------- rows opened to fp16
-    // One thread a row.  (Its 16-byte pieces are read in an order by which eight neighbouring rows
-    // meet different banks: logical piece p of row r lies at p ^ (r & 7) anyway.)
-    const int row = tid - 32 * kFirstOpen, ow = row / 32;
-    const uint32_t turn = (uint32_t)(row & 7);
-    auto piece = [&](int p) { return (uint32_t)((p >> 3) * kBlock + row * 128) + ((p & 7 ^ turn) << 4); };
+    leave_registers<56>();
+    const int row = tid - 32 * kFirstOpen;  // one thread a row
     int it = 0;
-    for (int g = 0; g < a.out_share; ++g) {
-      const float log2a = linear::log2_decay(a.s, oh * a.out_share + g);
-      double bound = 0.;  // of |S|
+    for (int g = 0; g < share; ++g) {
+      const int64_t at = slot * a.s.hv + oh * share + g;
+      const float log2a = linear::log2_decay(a.s, oh * share + g);
+      const int ex = top_of(a.x_top, at, -110), ey = top_of(a.y_top, at, -110);
+      const float x_scale = two_to(15 + ey - max(ex + ey, -97));
+      int ez = a.z_top ? top_of(a.z_top, at, -60) : 0;
+      const float x_whole = linear::power(log2a, REVERSE ? row + 1 : C - row) * x_scale;
       for (int c = 0; c < chunks; ++c, ++it) {
-        const int m = tokens(c), i = a.reverse ? m - 1 - row : row;
+        const int m = tokens(c);
         const bool live = row < m;
         const uint32_t st = base + (it & 1) * PassSmem::stage;
         wait_bar(bar(kFull, it), half(it), failed);
-        uint32_t x_max = 0, y_max = 0, z_max = 0;
-#pragma unroll 4
-        for (int p = 0; p < 16; ++p) {
-          const uint4 x = lds16(st + PassSmem::X + piece(p)), y = lds16(st + PassSmem::Y + piece(p)),
-                      z = lds16(st + PassSmem::Z + piece(p));
-          const uint32_t* xv = &x.x;
-          const uint32_t* yv = &y.x;
-          const uint32_t* zv = &z.x;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x_max = max_u16x2(x_max, xv[j] & 0x7fff7fffu);
-            y_max = max_u16x2(y_max, yv[j] & 0x7fff7fffu);
-            z_max = max_u16x2(z_max, zv[j] & 0x7fff7fffu);
-          }
+        if (!a.z_top) {
+          ez = live ? exponent_of(row_max_of(st + PassSmem::Z, row), -60) : -60;
+          if (it >= 2) wait_bar(bar(kSumsRead, it - 2), half(it - 2), failed);  // (who reads it there)
+          targets[C * (it & 1) + row] = ez;
+          mbar_arrive(bar(kRows, it));
         }
-        const int ex = live ? exponent_of(x_max, -110) : -110, ey = live ? exponent_of(y_max, -113) : -113;
-        const int ez = live ? exponent_of(z_max, -60) : -60;
-        const int warp_max = __reduce_max_sync(0xffffffffu, ex + ey);
-        // (the chunk before the last has been given out: its table may be written again)
-        if (it >= 2) wait_bar(one(kSumsRead), (it - 2) & 1, failed);
-        if (lane == 0) row_max[4 * (it & 1) + ow] = warp_max;
-        PassTables& tab = tables[it & 1];
-        tab.ey[row] = (int8_t)ey;
-        tab.ez[row] = (int8_t)ez;
-        if (c == 0) wait_bar(one(kStart), g & 1, failed);
-        named_bar(2, 32 * kOpenWarps);
-        const int* rm = row_max + 4 * (it & 1);
-        const int M = max(max(max(rm[0], rm[1]), max(rm[2], rm[3])), -97);
-        if (c == 0) {
-          bound = __int_as_float(misc[2 + (g & 1)]);
-          named_bar(2, 32 * kOpenWarps);
-          if (row == 0) misc[2 + (g & 1)] = 0;  // for the head after the next
+        if (c + 1 < chunks) {
+          wait_bar(bar(kScores, it), half(it), failed);  // (x as it was has been read)
+          open_row(st + PassSmem::X, row, live,
+                   REVERSE || m == C ? x_whole : live ? linear::power(log2a, m - row) * x_scale : 0.f);
         }
-        const int E = max((__double2hiint(bound) >> 20) - 1022, M + 7);  // (|S| < 2^E)
-        if (row == 0) {
-          tab.M = M;
-          tab.E = E;
-        }
-        bound = linear::power(log2a, m) * bound + (double)m * two_to(min(M, 120));
-        const float y_scale = two_to(14 - ey);
-#pragma unroll 4
-        for (int p = 0; p < 16; ++p) {
-          const uint32_t at = st + PassSmem::Y + piece(p);
-          uint4 y = lds16(at);
-          y.x = to_half2(y.x, y_scale);
-          y.y = to_half2(y.y, y_scale);
-          y.z = to_half2(y.z, y_scale);
-          y.w = to_half2(y.w, y_scale);
-          sts16(at, live ? y : make_uint4(0, 0, 0, 0));
-        }
+        wait_bar(bar(kFullY, it), half(it), failed);
+        open_row(st + PassSmem::Y, row, live, two_to(14 - ey));
         fence_async_smem();
-        mbar_arrive(bar(kTables, it));
-        const float z_scale = linear::power(log2a, live ? i : 0) * two_to(14 - ez);
-        const float x_scale = linear::power(log2a, live ? m - i : 0) * two_to(15 + ey - M);
-        wait_bar(bar(kScores, it), half(it), failed);  // (x and z as they were have been read)
-#pragma unroll 2
-        for (int p = 0; p < 16; ++p) {
-          const uint32_t xa = st + PassSmem::X + piece(p), za = st + PassSmem::Z + piece(p);
-          uint4 x = lds16(xa), z = lds16(za);
-          x.x = to_half2(x.x, x_scale);
-          x.y = to_half2(x.y, x_scale);
-          x.z = to_half2(x.z, x_scale);
-          x.w = to_half2(x.w, x_scale);
-          z.x = to_half2(z.x, z_scale);
-          z.y = to_half2(z.y, z_scale);
-          z.z = to_half2(z.z, z_scale);
-          z.w = to_half2(z.w, z_scale);
-          sts16(xa, live ? x : make_uint4(0, 0, 0, 0));
-          sts16(za, live ? z : make_uint4(0, 0, 0, 0));
-        }
-        fence_async_smem();
-        mbar_arrive(bar(kOpened, it));
+        mbar_arrive(bar(kValues, it));
       }
     }
+  } else {  // (the rest of the last warpgroup)
+    leave_registers<56>();
   }
   fence_before_sync();
   __syncthreads();
@@ -701,6 +941,21 @@ cudaError_t rows_map(CUtensorMap* m, const LinearRows& r, int64_t T, int heads, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+template <bool REVERSE, bool SUM> cudaError_t launch_pass(const LinearPass& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(linear_pass_tc_kernel<REVERSE, SUM>, PassSmem::bytes, done);
+  const int heads = a.s.hv / a.out_share;
+  const LinearRows out = {a.out, (int64_t)heads * D, D, a.out_share};
+  CUtensorMap mz, mx, my, mo;
+  if (e == cudaSuccess) e = rows_map(&mz, a.z, a.s.T, a.s.hv / a.z.share, C);
+  if (e == cudaSuccess) e = rows_map(&mx, a.x, a.s.T, a.s.hv / a.x.share, C);
+  if (e == cudaSuccess) e = rows_map(&my, a.y, a.s.T, a.s.hv / a.y.share, C);
+  if (e == cudaSuccess) e = rows_map(&mo, out, a.s.T, heads, C);
+  if (e != cudaSuccess) return e;
+  return launch_ordered(linear_pass_tc_kernel<REVERSE, SUM>, dim3((unsigned)(a.s.slots * heads)),
+                        kPassThreads, PassSmem::bytes, s, a, mz, mx, my, mo);
+}
+
 }  // namespace
 
 cudaError_t linear_state_tc(const LinearState& a, cudaStream_t s) {
@@ -715,15 +970,8 @@ cudaError_t linear_state_tc(const LinearState& a, cudaStream_t s) {
 }
 
 cudaError_t linear_pass_tc(const LinearPass& a, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(linear_pass_tc_kernel, PassSmem::bytes, done);
-  CUtensorMap mz, mx, my;
-  if (e == cudaSuccess) e = rows_map(&mz, a.z, a.s.T, a.s.hv / a.z.share, C);
-  if (e == cudaSuccess) e = rows_map(&mx, a.x, a.s.T, a.s.hv / a.x.share, C);
-  if (e == cudaSuccess) e = rows_map(&my, a.y, a.s.T, a.s.hv / a.y.share, C);
-  if (e != cudaSuccess) return e;
-  return launch_ordered(linear_pass_tc_kernel, dim3((unsigned)(a.s.slots * (a.s.hv / a.out_share))),
-                        kPassThreads, PassSmem::bytes, s, a, mz, mx, my);
+  if (a.out_share > 1) return a.reverse ? launch_pass<true, true>(a, s) : launch_pass<false, true>(a, s);
+  return a.reverse ? launch_pass<true, false>(a, s) : launch_pass<false, false>(a, s);
 }
 
 }  // namespace gdn
