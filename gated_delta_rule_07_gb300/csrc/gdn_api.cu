@@ -858,23 +858,40 @@ bool linear_on_tc(const gdn_linear_problem* p) {
          mapped(p->v_token_stride, p->v_head_stride, p->hv);
 }
 
-// A segment's tokens: so many that the segments of all heads fill the SMs a few times over, in whole
-// chunks, within bounds that keep a segment's own state (K V values written and read twice) small
-// beside its rows at the top and its walk short at the bottom.
-int linear_segment(const gdn_linear_problem* p) {
-  const bool tc = linear_on_tc(p);
-  const int64_t chunk = tc ? 128 : 64, most = tc ? 2048 : 1024;
-  const int64_t even = (p->total_tokens * p->hv / (152 * (tc ? 1 : 2)) + chunk - 1) / chunk * chunk;
-  return (int)(even < chunk ? chunk : even > most ? most : even);
+// A segment's tokens, in whole chunks.  On the CUDA cores so many that the segments of all heads fill
+// the SMs a few times over.  On the tensor cores an SM holds one segment of one output head at a time (in
+// the backward pass of shared heads, of all the value heads that it sums), so what counts is how many
+// rounds of the 152 SMs there are and how long one takes: its tokens and about 640 more for its start and
+// end.  (65536 tokens of 32 heads: 4 segments, one round of 128 SMs, 613 us; 9, two rounds of 144, 555; 16,
+// 674; 19, four rounds of 152, 564; 32, 634.)  Only the sum of the sequences' lengths is known here: they are
+// taken as alike, give or take a seventh.
+int linear_segment(const gdn_linear_problem* p, bool backward) {
+  const int64_t T = p->total_tokens, N = p->num_seqs, hv = p->hv;
+  if (!linear_on_tc(p)) {
+    const int64_t even = (T * hv / (152 * 2) + 63) / 64 * 64;
+    return (int)(even < 64 ? 64 : even > 1024 ? 1024 : even);
+  }
+  const int64_t heads = backward ? p->hk : hv, share = hv / heads;
+  const int64_t each = N == 1 ? T : (T + N - 1) / N * 8 / 7 + 1;
+  int64_t best = 0, least = INT64_MAX;
+  for (int64_t k = 1; k <= 64 && (k == 1 || each > (k - 1) * 128); ++k) {
+    const int64_t length = ((each + k - 1) / k + 127) / 128 * 128;
+    const int64_t rounds = (N * k * heads + 151) / 152, cost = rounds * share * (length + 640);
+    if (cost < least) {
+      least = cost;
+      best = length;
+    }
+  }
+  return (int)(best < 128 ? 128 : best < (int64_t)1 << 30 ? best : (int64_t)1 << 30);
 }
 
-gdn::LinearShape linear_shape(const gdn_linear_problem* p, const float* log_decay,
+gdn::LinearShape linear_shape(const gdn_linear_problem* p, bool backward, const float* log_decay,
                               const int32_t* cu, int32_t* dev_status) {
   gdn::LinearShape s;
   memset(&s, 0, sizeof(s));
   s.T = p->total_tokens;
   s.N = p->num_seqs; s.hk = p->hk; s.hv = p->hv; s.K = p->k_dim; s.V = p->v_dim;
-  s.seg = linear_segment(p);
+  s.seg = linear_segment(p, backward);
   s.slots = s.T / s.seg + s.N;
   s.bf16 = p->io_dtype == GDN_BF16;
   s.log_decay = log_decay; s.cu = cu; s.status = dev_status;
@@ -954,7 +971,7 @@ gdn_status gdn_check_linear_problem(const gdn_linear_problem* p) { return check_
 
 size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p) {
   if (check_linear(p) != GDN_OK) return 0;
-  return linear_states_bytes(linear_shape(p, nullptr, nullptr, nullptr));
+  return linear_states_bytes(linear_shape(p, false, nullptr, nullptr, nullptr));
 }
 
 gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, const void* k,
@@ -969,7 +986,7 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(h0) ||
       !aligned16(h_final))
     return GDN_ERR_INVALID_ARGUMENT;
-  const gdn::LinearShape s = linear_shape(p, log_decay, cu_seqlens, dev_status);
+  const gdn::LinearShape s = linear_shape(p, false, log_decay, cu_seqlens, dev_status);
   if (!workspace || !aligned16(workspace) || ws_bytes < linear_states_bytes(s))
     return GDN_ERR_WORKSPACE;
   float* states = static_cast<float*>(workspace);
@@ -989,7 +1006,7 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
 size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p, int saved) {
   if (check_linear(p) != GDN_OK) return 0;
   const gdn_linear_problem o = saved ? linear_opened(p) : *p;
-  return linear_bwd_layout(linear_shape(&o, nullptr, nullptr, nullptr), saved != 0).total;
+  return linear_bwd_layout(linear_shape(&o, true, nullptr, nullptr, nullptr), saved != 0).total;
 }
 
 gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void* q,
@@ -1012,7 +1029,7 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
     return GDN_ERR_INVALID_ARGUMENT;
   const gdn_linear_problem opened = linear_opened(p);
   if (saved) p = &opened;
-  const gdn::LinearShape s = linear_shape(p, log_decay, cu_seqlens, dev_status);
+  const gdn::LinearShape s = linear_shape(p, true, log_decay, cu_seqlens, dev_status);
   const LinearBwdLayout L = linear_bwd_layout(s, saved != nullptr);
   if (!workspace || !aligned16(workspace) || ws_bytes < L.total) return GDN_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);

@@ -95,15 +95,38 @@ __device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
 // are split into three bf16 parts (24 bits), x is bf16 as it stands, products and their sums are exact
 // or fp32.  64 tokens at a time go through the tensor core into Tensor Memory and from there into a
 // register-held U, decayed on the way: the weights stay within a tile, and the tensor core's own sums,
-// whose roundings do not average out, stay short.
-constexpr int kTile = 64, kWorkers = 256, kStateThreads = kWorkers + 32;
+// whose roundings do not average out, stay short.  Where what a segment gathers has decayed by 2^-13 at
+// the end of its sequence, two parts do: 2^-17 of it there is 2^-30, and beside the fp16 copy that the
+// pass makes of the state (2^-11) nothing.
+//
+// HBM takes 1340 cycles for a tile of an SM's share, so little may go through shared memory beside the
+// tiles themselves (256 of its cycles): y comes out of it transposed (ldmatrix) and the parts go straight to
+// Tensor Memory, as the operand whose rows are y's columns; the tensor core reads x alone from shared memory.
+// So it makes U^T.  (Parts written back to shared memory: 270 us for 65536 tokens of 32 heads, whatever the
+// number of warps.)  Five tiles are on their way or at work; splitting (sixteen warps), the products and the
+// sums (eight warps, for Tensor Memory's lanes and their registers) each on another.  896 threads launch
+// with 72 registers, 504 for the seven warpgroups' warps of an SM's quarter: the sums' two take 96,
+// splitting's four keep 64, the last 56.
+constexpr int kTile = 64, kSplit = 512, kAdd = 256, kStateThreads = kSplit + kAdd + 128, kStages = 5;
 constexpr uint32_t kRaw = kTile * D * 2;          // bytes of a tile of one tensor
 struct StateSmem {                                // offsets from a 1024-byte boundary
-  static constexpr uint32_t X = 0, Y = 2 * kRaw, MID = 4 * kRaw, LOW = 5 * kRaw, BARS = 6 * kRaw;
-  static constexpr int bytes = BARS + 64 + 1024;
+  static constexpr uint32_t X = 0, Y = kRaw, stage = 2 * kRaw, BARS = kStages * stage;
+  static constexpr int bytes = BARS + 24 * 8 + 1024;
 };
 
-__global__ void __launch_bounds__(kStateThreads, 2)
+// Four 8 x 8 blocks of 16-bit elements, transposed: a lane gives a row of one (lane / 8) and gets of each
+// the elements [lane / 4] [2 (lane % 4)] and the next.
+__device__ __forceinline__ void load_transposed(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+// Such blocks to 16 lanes and 8 columns of Tensor Memory: rows 0-7 and 8-15 of four columns, of the next four.
+__device__ __forceinline__ void tmem_st_blocks(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+
+__global__ void __launch_bounds__(kStateThreads, 1)
 linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap mx,
                        const __grid_constant__ CUtensorMap my) {
   extern __shared__ uint8_t raw_smem[];
@@ -117,96 +140,221 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
   int n;
   int64_t t0, t1;
   if (!linear::slot_tokens(a.s, slot, n, t0, t1)) return;
-  const uint32_t base = (saddr(raw_smem) + 1023u) & ~1023u;
-  const uint32_t full = base + StateSmem::BARS, ready = full + 16, done = ready + 8, end = done + 16;
+  const uint32_t base = (saddr(raw_smem) + 1023u) & ~1023u, bars = base + StateSmem::BARS;
+  // (one of a stage, or of two in turn)
+  const uint32_t full = bars, free_ = full + 8 * kStages, ready = free_ + 8 * kStages, done = ready + 16, taken = done + 16,
+                 end = taken + 16;
+  auto half = [](int i) { return (uint32_t)(i >> 1) & 1; };
   const int tid = threadIdx.x, warp = tid / 32;
   if (tid == 0) {
     failed_word = 0;
     top[0] = top[1] = -126;
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(done + 8 * i, 1);
+      mbar_init(free_ + 8 * i, 1);
     }
-    mbar_init(ready, kWorkers);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(ready + 8 * i, kSplit);
+      mbar_init(done + 8 * i, 1);
+      mbar_init(taken + 8 * i, kAdd);
+    }
     mbar_init(end, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 8) {
-    tmem_alloc(saddr(&tmem_at), 256);
+  constexpr int kLoad = (kSplit + kAdd) / 32, kMma = kLoad + 1;
+  if (warp == kMma) {
+    tmem_alloc(saddr(&tmem_at), 512);
     tmem_relinquish();
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tm = tmem_at;
+  constexpr uint32_t tm = 0, tm_parts = 256;  // (all of Tensor Memory): two sums; three parts, twice
   const int begin = (int)t0, length = (int)(t1 - t0), tiles = (length + kTile - 1) / kTile;
   // the i-th tile of the walk, its tokens
   auto first_token = [&](int i) { return begin + (a.reverse ? tiles - 1 - i : i) * kTile; };
   auto tokens = [&](int i) { return min(begin + length - first_token(i), kTile); };
+  const float log2a = linear::log2_decay(a.s, head);
+  // tokens between the segment and where the walk of its sequence ends
+  const int64_t left = a.reverse ? t0 - (a.s.cu ? a.s.cu[n] : 0) : (a.s.cu ? a.s.cu[n + 1] : a.s.T) - t1;
+  const bool three = log2a * (float)left > -13.f;
 
-  if (warp == 8) {
-    // ---------------------------------------------------------------- loads and products
-    int loaded = 0;
-    auto load = [&](int i) {
-      if (elected()) {
-        const uint32_t bar = full + 8 * (i & 1), x = base + StateSmem::X + (i & 1) * kRaw,
-                       y = base + StateSmem::Y + (i & 1) * kRaw;
+  if (warp >= kMma + 1) {  // (the rest of the last warpgroup)
+    leave_registers<56>();
+  } else if (warp == kLoad) {
+    leave_registers<56>();
+    if (tid % 32 == 0) {
+      int loaded = 0;
+      for (int i = 0, st = 0, round = 0; i < tiles; ++i) {
+        if (round) wait_one(free_ + 8 * st, (round - 1) & 1, failed);
+        if (*failed) break;
+        const uint32_t x = base + st * StateSmem::stage + StateSmem::X,
+                       y = base + st * StateSmem::stage + StateSmem::Y;
         const int t = first_token(i);
-        mbar_expect_tx(bar, 2 * kRaw);
+        mbar_expect_tx(full + 8 * st, StateSmem::stage);
+#pragma unroll 1
         for (int b = 0; b < 2; ++b) {
-          tma_box(x + b * (kRaw / 2), &mx, 64 * b, head / a.x.share, t, bar);
-          tma_box(y + b * (kRaw / 2), &my, 64 * b, head / a.y.share, t, bar);
+          tma_box(x + b * (kRaw / 2), &mx, 64 * b, head / a.x.share, t, full + 8 * st);
+          tma_box(y + b * (kRaw / 2), &my, 64 * b, head / a.y.share, t, full + 8 * st);
+        }
+        loaded = i + 1;
+        if (++st == kStages) {
+          st = 0;
+          ++round;
         }
       }
-      __syncwarp();
-      loaded = i + 1;
-    };
-    for (int i = 0; i < 2 && i < tiles; ++i) load(i);
-    const uint32_t id = idesc_f16(128, 128, 1, 1, 1);
-    for (int i = 0; i < tiles; ++i) {
-      wait_bar(ready, i & 1, failed);
+      if (*failed)
+        for (int i = loaded > kStages ? loaded - kStages : 0; i < loaded; ++i)
+          drain(full + 8 * (i % kStages), (i / kStages) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kMma) {
+    leave_registers<56>();
+    const uint32_t id = idesc_f16(128, 128, 0, 1, 1);
+    const uint64_t at = sdesc(base, kRaw / 2, 1024);
+#pragma unroll 1
+    for (int i = 0, st = 0; i < tiles; ++i) {
+      wait_bar(ready + 8 * (i & 1), half(i), failed);
+      if (i >= 2) wait_bar(taken + 8 * (i & 1), half(i - 2), failed);
       if (*failed) break;
       fence_after_sync();
-      const uint32_t x = base + StateSmem::X + (i & 1) * kRaw;
-      const uint32_t parts[3] = {base + StateSmem::LOW, base + StateSmem::MID,
-                                 base + StateSmem::Y + (i & 1) * kRaw};
+      const uint64_t x = at + ((st * StateSmem::stage + StateSmem::X) >> 4);
+      const uint32_t d = tm + 128 * (i & 1), parts = tm_parts + 96 * (i & 1);
       if (elected()) {
+        if (three) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p)  // (the small parts first)
+          for (int ks = 0; ks < kTile / 16; ++ks)  // (the small parts first)
+            mma_ts(d, parts + 64 + 8 * ks, x + ks * 128, id, ks > 0);
+        }
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_ss(tm + 128 * (i & 1), sdesc(x + ks * 2048, kRaw / 2, 1024),
-                   sdesc(parts[p] + ks * 2048, kRaw / 2, 1024), id, p > 0 || ks > 0);
+        for (int ks = 0; ks < kTile / 16; ++ks)
+          mma_ts(d, parts + 32 + 8 * ks, x + ks * 128, id, three || ks > 0);
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(d, parts + 8 * ks, x + ks * 128, id, 1);
         mma_commit(done + 8 * (i & 1));
+        mma_commit(free_ + 8 * st);
       }
       __syncwarp();
-      if (i + 2 < tiles) {
-        wait_bar(done + 8 * (i & 1), (i >> 1) & 1, failed);
-        if (*failed) break;
-        load(i + 2);
-      }
+      st = st + 1 == kStages ? 0 : st + 1;
     }
     if (*failed) {
       if (elected()) {
         mma_commit(end);
         drain(end, 0);
-        for (int i = loaded > 2 ? loaded - 2 : 0; i < loaded; ++i) drain(full + 8 * (i & 1), (i >> 1) & 1);
       }
       __syncwarp();
     }
-  } else {
-    // ---------------------------------------------------------------- weights, parts, the sum
-    const float log2a = linear::log2_decay(a.s, head);
-    const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, cols = (uint32_t)(warp >> 2) * 64;
-    float2 u[32];
+  } else if (warp < kSplit / 32) {
+    // ---------------------------------------------------------------- weights and parts
+    // A warp has 16 tokens, and the 32 columns whose lanes of Tensor Memory it can write; a thread four of
+    // the tokens, and of x two 16-byte pieces of a row to look at.
+    leave_registers<64>();
+    const int lane = tid % 32, quarter = warp & 3, token0 = 16 * (warp >> 2), pair = token0 + 2 * (lane & 3);
+    const int r = tid / 8;
+    const int from = token0 + (lane >> 4) * 8 + (lane & 7);  // the row that this lane gives ldmatrix,
+    uint32_t source[2];                                      // and where its columns are
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int c = 32 * quarter + 16 * g + (lane >> 3 & 1) * 8;
+      source[g] = sw128_offset(kTile, from, c);
+    }
     uint32_t x_max = 0, y_max = 0;
+    float2 w_whole[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = pair + 8 * k;
+      w_whole[k] = make_float2(linear::power(log2a, a.reverse ? t + 1 : kTile - 1 - t),
+                               linear::power(log2a, a.reverse ? t + 2 : kTile - 2 - t));
+    }
+#pragma unroll 1
+    for (int i = 0, st = 0, round = 0; i < tiles; ++i) {
+      const uint32_t x = base + st * StateSmem::stage + StateSmem::X + 16 * tid,
+                     y = base + st * StateSmem::stage + StateSmem::Y;
+      const int m = tokens(i);
+      float2 w[2] = {w_whole[0], w_whole[1]};
+      uint32_t mask[2] = {0xffffffffu, 0xffffffffu};
+      if (m < kTile) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int t = pair + 8 * k;
+          mask[k] = (t < m ? 0xffffu : 0u) | (t + 1 < m ? 0xffff0000u : 0u);
+          if (!a.reverse)
+            w[k] = make_float2(linear::power(log2a, max(0, m - 1 - t)),
+                               linear::power(log2a, max(0, m - 2 - t)));
+        }
+      }
+      wait_bar(full + 8 * st, round & 1, failed);
+      if (i >= 2) wait_bar(done + 8 * (i & 1), half(i - 2), failed);  // (the parts' columns)
+      fence_after_sync();
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        uint32_t v[4], mid[4];
+        float2 f[4];
+        load_transposed(y + source[g], v);
+        if (m < kTile) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] &= mask[j >> 1];
+        }
+        const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          y_max = larger(y_max, v[j]);
+          f[j] = mul2(make_float2(low(v[j]), high(v[j])), w[j >> 1]);
+          v[j] = pack_bf2(f[j].x, f[j].y);
+          f[j] = __ffma2_rn(make_float2(low(v[j]), high(v[j])), minus, f[j]);
+          mid[j] = pack_bf2(f[j].x, f[j].y);
+        }
+        const uint32_t to = ((uint32_t)(32 * quarter + 16 * g) << 16) + tm_parts + 96 * (i & 1) + token0 / 2;
+        tmem_st_blocks(to, v);
+        tmem_st_blocks(to + 32, mid);
+        if (three) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            f[j] = __ffma2_rn(make_float2(low(mid[j]), high(mid[j])), minus, f[j]);
+            mid[j] = pack_bf2(f[j].x, f[j].y);
+          }
+          tmem_st_blocks(to + 64, mid);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (r < m) {
+          const uint4 v = lds16(x + 8192 * b);
+          x_max = larger(larger(larger(larger(x_max, v.x), v.y), v.z), v.w);
+        } else {  // (another sequence's rows, or none)
+          sts16(x + 8192 * b, make_uint4(0, 0, 0, 0));
+        }
+      }
+      __syncwarp();
+      if (m < kTile) fence_async_smem();
+      tmem_wait_st();
+      fence_before_sync();
+      mbar_arrive(ready + 8 * (i & 1));
+      if (++st == kStages) {
+        st = 0;
+        ++round;
+      }
+    }
+    const int e_x = __reduce_max_sync(0xffffffffu, exponent_of(x_max, -126));
+    const int e_y = __reduce_max_sync(0xffffffffu, exponent_of(y_max, -126));
+    if (tid % 32 == 0) {
+      atomicMax(top, e_x);
+      atomicMax(top + 1, e_y);
+    }
+  } else {
+    // ---------------------------------------------------------------- the sum
+    take_registers<96>();
+    const int at = tid - kSplit, row = at & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, cols = (uint32_t)(at >> 7) * 64;
+    const float whole = linear::power(log2a, kTile);
+    float2 u[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) u[i] = make_float2(0.f, 0.f);
-    const float whole = linear::power(log2a, kTile);
-    auto add = [&](int i) {  // tile i into u
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
       const int m = tokens(i);
       const float w = m == kTile ? whole : linear::power(log2a, m);
-      wait_bar(done + 8 * (i & 1), (i >> 1) & 1, failed);
+      wait_bar(done + 8 * (i & 1), half(i), failed);
       fence_after_sync();
 #pragma unroll
       for (int c = 0; c < 32; c += 8) {
@@ -218,76 +366,23 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
           u[c + k] = __ffma2_rn(make_float2(w, w), u[c + k],
                                 make_float2(__uint_as_float(p[2 * k]), __uint_as_float(p[2 * k + 1])));
       }
-    };
-    // A thread's 16-byte pieces of a tile are 4096 bytes apart: of rows r0, r0 + 32 of either block.
-    const int r0 = tid / 8;
-#pragma unroll 1
-    for (int i = 0; i <= tiles; ++i) {
-      if (i < tiles) {
-        const uint32_t at = 16 * tid, x = base + StateSmem::X + (i & 1) * kRaw + at,
-                       y = base + StateSmem::Y + (i & 1) * kRaw + at;
-        const int m = tokens(i);
-        float w[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int r = r0 + 32 * k;
-          w[k] = r < m ? linear::power(log2a, a.reverse ? r + 1 : m - 1 - r) : 0.f;
-        }
-        wait_bar(full + 8 * (i & 1), (i >> 1) & 1, failed);
-        if (i > 0) wait_bar(done + 8 * ((i - 1) & 1), ((i - 1) >> 1) & 1, failed);  // the parts' tiles
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          const bool live = r0 + 32 * (k & 1) < m;
-          const float2 ww = k & 1 ? make_float2(w[1], w[1]) : make_float2(w[0], w[0]);
-          uint4 v = make_uint4(0, 0, 0, 0), mid = v, lo = v;
-          if (live) {
-            v = lds16(y + 4096 * k);
-            const uint4 xv = lds16(x + 4096 * k);
-            x_max = larger(larger(larger(larger(x_max, xv.x), xv.y), xv.z), xv.w);
-            y_max = larger(larger(larger(larger(y_max, v.x), v.y), v.z), v.w);
-            uint32_t* pv = &v.x;
-            uint32_t* pm = &mid.x;
-            uint32_t* pl = &lo.x;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float2 f = mul2(make_float2(low(pv[j]), high(pv[j])), ww);
-              pv[j] = pack_bf2(f.x, f.y);
-              f = __fadd2_rn(f, make_float2(-low(pv[j]), -high(pv[j])));
-              pm[j] = pack_bf2(f.x, f.y);
-              f = __fadd2_rn(f, make_float2(-low(pm[j]), -high(pm[j])));
-              pl[j] = pack_bf2(f.x, f.y);
-            }
-          } else {  // (another sequence's rows, or none)
-            sts16(x + 4096 * k, v);
-          }
-          sts16(y + 4096 * k, v);
-          sts16(base + StateSmem::MID + at + 4096 * k, mid);
-          sts16(base + StateSmem::LOW + at + 4096 * k, lo);
-        }
-        fence_async_smem();
-        fence_before_sync();
-        mbar_arrive(ready);
-      }
-      if (i > 0) add(i - 1);
+      fence_before_sync();
+      mbar_arrive(taken + 8 * (i & 1));
     }
-    const int e_x = __reduce_max_sync(0xffffffffu, exponent_of(x_max, -126));
-    const int e_y = __reduce_max_sync(0xffffffffu, exponent_of(y_max, -126));
-    if (tid % 32 == 0) {
-      atomicMax(top, e_x);
-      atomicMax(top + 1, e_y);
-    }
-    float* out = a.states + (slot * a.s.hv + head) * D * D + (int64_t)(tid & 127) * D + cols;
+    float* out = a.states + (slot * a.s.hv + head) * D * D + (int64_t)cols * D + row;  // (U^T's row)
     if (!*failed) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 2)
-        *reinterpret_cast<float4*>(out + 2 * c) = make_float4(u[c].x, u[c].y, u[c + 1].x, u[c + 1].y);
+      for (int c = 0; c < 32; ++c) {
+        out[2 * c * D] = u[c].x;
+        out[(2 * c + 1) * D] = u[c].y;
+      }
     }
   }
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
   if (tid < 2) a.tops[2 * (slot * a.s.hv + head) + tid] = top[tid];
-  if (warp == 8) tmem_dealloc(tm, 256);
+  if (warp == kMma) tmem_dealloc(tm, 512);
   if (tid == 0 && *failed) set_status(a.s.status, GDN_ERR_DEVICE_TIMEOUT);
 }
 
