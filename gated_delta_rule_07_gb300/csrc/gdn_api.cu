@@ -852,7 +852,7 @@ bool linear_on_tc(const gdn_linear_problem* p) {
     return (T == 1 || (ts > 0 && ts < (int64_t)1 << 38)) &&
            (heads == 1 || (hs > 0 && hs < (int64_t)1 << 38));
   };
-  return p->io_dtype == GDN_BF16 && p->k_dim == 128 && p->v_dim == 128 &&
+  return p->io_dtype == GDN_BF16 &&
          mapped(p->q_token_stride, p->q_head_stride, p->hk) &&
          mapped(p->k_token_stride, p->k_head_stride, p->hk) &&
          mapped(p->v_token_stride, p->v_head_stride, p->hv);
@@ -996,7 +996,8 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
                         vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);
   int* tops = linear_tops(s, states);  // of k, and of v
   if (T > 0) GDN_TRY(linear_state(p, {s, kr, vr, false, states, tops}, stream));
-  GDN_TRY(gdn::linear_scan({s, false, states, h0, h_final}, stream));
+  const gdn::LinearScan scan = {s, false, states, h0, h_final};
+  GDN_TRY(gdn::linear_scan(&scan, 1, stream));
   if (T > 0)
     GDN_TRY(linear_pass(p, {s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr, tops,
                             tops + 1, nullptr}, stream));
@@ -1062,9 +1063,9 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
   if (T > 0) {
     GDN_TRY(linear_state(p, {s, kr, vr, false, h, linear_tops(s, h)}, stream));
     GDN_TRY(linear_state(p, {s, qr, gr, true, d, linear_tops(s, d)}, stream));
-    GDN_TRY(gdn::linear_scan({s, false, h, h0, nullptr}, stream));
   }
-  GDN_TRY(gdn::linear_scan({s, true, d, dh_final, dh0}, stream));
+  const gdn::LinearScan scans[2] = {{s, true, d, dh_final, dh0}, {s, false, h, h0, nullptr}};
+  GDN_TRY(gdn::linear_scan(scans, T > 0 ? 2 : 1, stream));
   if (T > 0) {
     float* partial = reinterpret_cast<float*>(ws + L.partial);
     const int *tk = linear_tops(s, h), *tv = tk + 1, *tq = linear_tops(s, d), *tg = tq + 1;

@@ -75,9 +75,9 @@ struct LinearPass {
 // fp32 arithmetic on the CUDA cores: every dtype and head size.
 cudaError_t linear_state_simt(const LinearState& a, cudaStream_t s);
 cudaError_t linear_pass_simt(const LinearPass& a, cudaStream_t s);
-cudaError_t linear_scan(const LinearScan& a, cudaStream_t s);
+cudaError_t linear_scan(const LinearScan* scans, int count, cudaStream_t s);  // one, or two of a shape
 
-// The same on the tensor cores: bf16, K = V = 128, segments of whole chunks of 128 tokens, T > 0, rows
+// The same on the tensor cores: bf16, segments of whole chunks of 128 tokens, T > 0, rows
 // that are strided by 16 bytes or more.
 cudaError_t linear_state_tc(const LinearState& a, cudaStream_t s);
 cudaError_t linear_pass_tc(const LinearPass& a, cudaStream_t s);

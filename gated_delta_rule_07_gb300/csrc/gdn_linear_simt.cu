@@ -96,14 +96,20 @@ __global__ void __launch_bounds__(kThreads) linear_state_kernel(LinearState a) {
 // ------------------------------------------------------------------ the scan over segments
 
 // One thread carries four elements of a state through its sequence's segments; the segments' sums are
-// read eight ahead, for each step waits for the one before only in registers.
-constexpr int kAhead = 8;
-__global__ void __launch_bounds__(kThreads) linear_scan_kernel(LinearScan a) {
+// read `kAhead` at a time, for each step waits for the one before only in registers.  A backward pass has
+// two scans, which run side by side.
+struct ScanPair {
+  LinearScan of[2];
+};
+template <int kAhead>
+__global__ void __launch_bounds__(kThreads) linear_scan_kernel(const __grid_constant__ ScanPair both,
+                                                               int blocks) {
   stream_order();
+  const LinearScan& a = both.of[blockIdx.z / blocks];
   if (!linear::usable(a.s)) return;
   const int n = blockIdx.x, head = blockIdx.y;
   const int64_t size = (int64_t)a.s.K * a.s.V;
-  const int64_t at = ((int64_t)blockIdx.z * kThreads + threadIdx.x) * 4;
+  const int64_t at = ((int64_t)(blockIdx.z % blocks) * kThreads + threadIdx.x) * 4;
   if (at >= size) return;
   const int64_t b = a.s.cu ? a.s.cu[n] : 0, e = a.s.cu ? a.s.cu[n + 1] : a.s.T;
   const int count = (int)((e - b + a.s.seg - 1) / a.s.seg);
@@ -314,10 +320,19 @@ cudaError_t linear_state_simt(const LinearState& a, cudaStream_t s) {
   return a.s.V == 128 ? launch_state<64, 128>(a, s) : launch_state<64, 64>(a, s);
 }
 
-cudaError_t linear_scan(const LinearScan& a, cudaStream_t s) {
-  const dim3 grid((unsigned)a.s.N, (unsigned)a.s.hv,
-                  (unsigned)((a.s.K * a.s.V / 4 + kThreads - 1) / kThreads));
-  return launch_ordered(linear_scan_kernel, grid, kThreads, 0, s, a);
+cudaError_t linear_scan(const LinearScan* scans, int count, cudaStream_t s) {
+  const LinearShape& shape = scans[0].s;
+  const int blocks = (shape.K * shape.V / 4 + kThreads - 1) / kThreads;
+  ScanPair both;
+  both.of[0] = scans[0];
+  both.of[1] = scans[count - 1];
+  const dim3 grid((unsigned)shape.N, (unsigned)shape.hv, (unsigned)(blocks * count));
+  // Sixteen ahead for sequences of many segments (16384 tokens of 32 heads, 9 segments: 22 us for the two
+  // scans of a backward pass, 38 four at a time), four for those of a few, where the registers cost more
+  // (eight ragged sequences: 16 us, 54).
+  if (shape.T / shape.seg >= 4 * (int64_t)shape.N)
+    return launch_ordered(linear_scan_kernel<16>, grid, kThreads, 0, s, both, blocks);
+  return launch_ordered(linear_scan_kernel<4>, grid, kThreads, 0, s, both, blocks);
 }
 
 cudaError_t linear_pass_simt(const LinearPass& a, cudaStream_t s) {

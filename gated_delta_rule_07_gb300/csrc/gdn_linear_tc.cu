@@ -1,5 +1,6 @@
 // gdn_linear_tc.cu -- linear attention with a decay for each head (gdn_linear.h) on the fifth-generation
-// tensor cores: bf16 I/O, K = V = 128.
+// tensor cores: bf16 I/O.  Tiles are 128 columns wide, two blocks of 64; rows of 64 have the first block
+// alone, and products take that many steps or columns fewer.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,7 +17,7 @@ namespace {
 using namespace sm100;
 using namespace tc5u;
 
-constexpr int D = 128;                            // K and V
+constexpr int D = 128;                            // K and V at most
 constexpr long long kWaitCycles = 2000000000LL;   // limit of a bounded wait: about a second
 
 // true in one thread of a converged warp
@@ -126,6 +127,7 @@ __device__ __forceinline__ void tmem_st_blocks(uint32_t taddr, const uint32_t (&
                "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
 
+template <bool WIDE>  // K = V = 128
 __global__ void __launch_bounds__(kStateThreads, 1)
 linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap mx,
                        const __grid_constant__ CUtensorMap my) {
@@ -135,6 +137,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
   volatile int* failed = &failed_word;
   stream_order();
   if (!linear::usable(a.s)) return;
+  const int K = WIDE ? D : a.s.K, V = WIDE ? D : a.s.V;
   const int head = blockIdx.x % a.s.hv;
   const int64_t slot = blockIdx.x / a.s.hv;
   int n;
@@ -191,12 +194,13 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
         const uint32_t x = base + st * StateSmem::stage + StateSmem::X,
                        y = base + st * StateSmem::stage + StateSmem::Y;
         const int t = first_token(i);
-        mbar_expect_tx(full + 8 * st, StateSmem::stage);
+        mbar_expect_tx(full + 8 * st, (uint32_t)(K + V) * kTile * 2);
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-          tma_box(x + b * (kRaw / 2), &mx, 64 * b, head / a.x.share, t, full + 8 * st);
-          tma_box(y + b * (kRaw / 2), &my, 64 * b, head / a.y.share, t, full + 8 * st);
-        }
+        for (int b = 0; b < K; b += 64)
+          tma_box(x + b * (kRaw / 128), &mx, b, head / a.x.share, t, full + 8 * st);
+#pragma unroll 1
+        for (int b = 0; b < V; b += 64)
+          tma_box(y + b * (kRaw / 128), &my, b, head / a.y.share, t, full + 8 * st);
         loaded = i + 1;
         if (++st == kStages) {
           st = 0;
@@ -210,7 +214,8 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
     __syncwarp();
   } else if (warp == kMma) {
     leave_registers<56>();
-    const uint32_t id = idesc_f16(128, 128, 0, 1, 1);
+    // (lanes behind V hold nothing that is read)
+    const uint32_t id = idesc_f16(128, K, 0, 1, 1);
     const uint64_t at = sdesc(base, kRaw / 2, 1024);
 #pragma unroll 1
     for (int i = 0, st = 0; i < tiles; ++i) {
@@ -288,6 +293,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
       fence_after_sync();
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
+        if (32 * quarter >= V) break;
         uint32_t v[4], mid[4];
         float2 f[4];
         load_transposed(y + source[g], v);
@@ -318,6 +324,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
+        if (64 * b >= K) break;
         if (r < m) {
           const uint4 v = lds16(x + 8192 * b);
           x_max = larger(larger(larger(larger(x_max, v.x), v.y), v.z), v.w);
@@ -369,12 +376,12 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
       fence_before_sync();
       mbar_arrive(taken + 8 * (i & 1));
     }
-    float* out = a.states + (slot * a.s.hv + head) * D * D + (int64_t)cols * D + row;  // (U^T's row)
-    if (!*failed) {
+    float* out = a.states + (slot * a.s.hv + head) * K * V + (int64_t)cols * V + row;  // (U^T's row)
+    if (!*failed && row < V && (int)cols < K) {
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
-        out[2 * c * D] = u[c].x;
-        out[(2 * c + 1) * D] = u[c].y;
+        out[2 * c * V] = u[c].x;
+        out[(2 * c + 1) * V] = u[c].y;
       }
     }
   }
@@ -432,10 +439,10 @@ __device__ __forceinline__ uint32_t piece(uint32_t tile, int row, int p) {
   return tile + (p >> 3) * kBlock + row * 128 + ((p & 7 ^ row & 7) << 4);
 }
 // the largest magnitudes of a row of bf16, of even and odd elements
-__device__ __forceinline__ uint32_t row_max_of(uint32_t tile, int row) {
+__device__ __forceinline__ uint32_t row_max_of(uint32_t tile, int row, int width) {
   uint32_t m[4] = {};
 #pragma unroll 4
-  for (int p = 0; p < 16; ++p) {
+  for (int p = 0; p < width / 8; ++p) {
     const uint4 v = lds16(piece(tile, row, p));
     m[0] = larger(m[0], v.x);
     m[1] = larger(m[1], v.y);
@@ -460,10 +467,10 @@ __device__ __forceinline__ void open_pieces(uint32_t tile, int row, int p0, floa
   }
 }
 // A row in its place; zeros where it is not live.
-__device__ __forceinline__ void open_row(uint32_t tile, int row, bool live, float f) {
+__device__ __forceinline__ void open_row(uint32_t tile, int row, int width, bool live, float f) {
   if (live) {
 #pragma unroll 1
-    for (int p0 = 0; p0 < 16; p0 += 4) {
+    for (int p0 = 0; p0 < width / 8; p0 += 4) {
       uint4 v[4];
       open_pieces(tile, row, p0, f, v);
 #pragma unroll
@@ -471,7 +478,7 @@ __device__ __forceinline__ void open_row(uint32_t tile, int row, bool live, floa
     }
   } else {
 #pragma unroll 1
-    for (int p = 0; p < 16; ++p) sts16(piece(tile, row, p), make_uint4(0, 0, 0, 0));
+    for (int p = 0; p < width / 8; ++p) sts16(piece(tile, row, p), make_uint4(0, 0, 0, 0));
   }
   __syncwarp();
 }
@@ -504,7 +511,8 @@ __device__ __forceinline__ void tma_out(const CUtensorMap* map, uint32_t src, in
 }
 
 // REVERSE: the walk goes backward in time.  SUM: an output head has several value heads.
-template <bool REVERSE, bool SUM>
+// WIDE: A = B = 128 (9% faster where that is known: 65536 tokens 554 us, 604).
+template <bool REVERSE, bool SUM, bool WIDE>
 __global__ void __launch_bounds__(kPassThreads, 1)
 linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz,
                       const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap my,
@@ -513,6 +521,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
   stream_order();
   if (!linear::usable(a.s)) return;
   const int share = SUM ? a.out_share : 1, heads = a.s.hv / share;
+  const int A = WIDE ? D : a.A, B = WIDE ? D : a.B;
   const int oh = blockIdx.x % heads;
   const int64_t slot = blockIdx.x / heads;
   int n;
@@ -579,10 +588,10 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
           if (it >= 0) wait_one(bar(kFree, it), half(it), failed);
           if (*failed) break;
           const uint32_t b = bar(kFull, it);
-          mbar_expect_tx(b, 2 * kTileBytes);
+          mbar_expect_tx(b, (uint32_t)A * C * 4);
           const int zh = head / a.z.share, xh = head / a.x.share;
 #pragma unroll 1
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; 64 * k < A; ++k) {
             tma_box(st + PassSmem::Z + k * kBlock, &mz, 64 * k, zh, t, b);
             tma_box(st + PassSmem::X + k * kBlock, &mx, 64 * k, xh, t, b);
           }
@@ -592,7 +601,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
           if (*failed) break;
           if (g + 1 == share && tokens(c) == C) {
 #pragma unroll 1
-            for (int k = 0; k < 2; ++k)
+            for (int k = 0; 64 * k < B; ++k)
               tma_out(&mo, st + PassSmem::Y + k * kBlock, 64 * k, oh, first_token(c));
             asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
             if (more) bulk_wait_read();
@@ -600,10 +609,10 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         }
         if (more) {
           const uint32_t b = bar(kFullY, it);
-          mbar_expect_tx(b, kTileBytes);
+          mbar_expect_tx(b, (uint32_t)B * C * 2);
           const int yh = head / a.y.share;
 #pragma unroll 1
-          for (int k = 0; k < 2; ++k) tma_box(st + PassSmem::Y + k * kBlock, &my, 64 * k, yh, t, b);
+          for (int k = 0; 64 * k < B; ++k) tma_box(st + PassSmem::Y + k * kBlock, &my, 64 * k, yh, t, b);
           ++loaded;
           if (++next_c == chunks) {
             next_c = 0;
@@ -627,8 +636,9 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
     leave_registers<56>();
-    const uint32_t id_p = idesc_f16(128, 128, 0, 0, 1), id_o = idesc_f16(128, 128, 0, 1),
-                   id_g = idesc_f16(128, 128, 1, 1);
+    // (growth: lanes behind A hold nothing that is read)
+    const uint32_t id_p = idesc_f16(128, 128, 0, 0, 1), id_o = idesc_f16(128, B, 0, 1),
+                   id_g = idesc_f16(128, B, 1, 1);
     // rows by features (the contraction's index contiguous), and features or columns by rows
     const uint64_t of_rows = sdesc(base, 16, 1024), of_cols = sdesc(base, kBlock, 1024);
     // A chunk takes two turns: the state's growth, the sums.  The next chunk's scores are made behind the
@@ -668,7 +678,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         if (elected()) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            mma_ts(tm_o, w + 64 + 8 * ks, of_cols + (PassSmem::S >> 4) + ks * 128, id_o, 1);
+            if (16 * ks < A) mma_ts(tm_o, w + 64 + 8 * ks, of_cols + (PassSmem::S >> 4) + ks * 128, id_o, 1);
           mma_commit(one(kSums));
           mma_commit(bar(kFree, it));
         }
@@ -686,7 +696,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
             const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
-            mma_ss(tm + 128 * (scored & 1), z + at, xr + at, id_p, ks > 0);
+            if (16 * ks < A) mma_ss(tm + 128 * (scored & 1), z + at, xr + at, id_p, ks > 0);
           }
           mma_commit(bar(kScores, scored));
         }
@@ -798,7 +808,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
             two_to(14 - ez) *
             (!REVERSE || m == C ? z_whole : row < m ? linear::power(log2a, m - 1 - row) : 0.f);
 #pragma unroll 1
-        for (int p0 = 0; p0 < 16; p0 += 4) {
+        for (int p0 = 0; p0 < A / 8; p0 += 4) {
           uint4 v[4];
           open_pieces(base + (it & 1) * PassSmem::stage + PassSmem::Z, row, p0, z_scale, v);
 #pragma unroll
@@ -820,6 +830,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
     const uint32_t lanes = (uint32_t)(warp & 3) * 32 << 16, cols = (uint32_t)(st >> 7) * 64;
     const uint32_t copy = base + PassSmem::S + (st >> 7) * kBlock + row * 128;
     const uint32_t turn = (uint32_t)(row & 7);
+    const bool mine = (int)cols < B, grows = mine && row < A;
     float2 S[32];
     auto give = [&](int it, int c, int g, int E, int ez_all) {  // (its sums are there)
       const int m = tokens(c), e = (a.z_top ? ez_all : targets[C * (it & 1) + row]) + E - 29;
@@ -827,6 +838,11 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       const float s0 = two_to(near);
       const bool far = __any_sync(0xffffffffu, near != e), live = row < m && !*failed;
       const bool last = !SUM || g + 1 == share;
+      if (!mine) {  // (half of the threads have no columns of 64)
+        mbar_arrive(bar(kSumsRead, it));
+        mbar_arrive(bar(kOut, it));
+        return;
+      }
       const uint32_t tile = base + (it & 1) * PassSmem::stage + PassSmem::Y + (st >> 7) * kBlock + row * 128;
 #pragma unroll 1
       for (int k = 0; k < 64; k += 32) {
@@ -850,7 +866,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         }
         if (SUM) {  // the running sum of a chunk: row after row of each four columns
           float4* const sum =
-              reinterpret_cast<float4*>(a.partial + ((int64_t)oh * a.s.T + first_token(c)) * D) +
+              reinterpret_cast<float4*>(a.partial + ((int64_t)oh * a.s.T + first_token(c)) * B) +
               (int64_t)((cols + k) / 4) * m + row;
           if (g > 0 && live) {
 #pragma unroll
@@ -878,7 +894,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
             for (int i = 0; i < 4; ++i) sts16(tile + (((k / 8 + i) ^ turn) << 4), b[i]);
           } else if (live) {
             uint4* const out = reinterpret_cast<uint4*>(
-                static_cast<__nv_bfloat16*>(a.out) + ((int64_t)(first_token(c) + row) * heads + oh) * D +
+                static_cast<__nv_bfloat16*>(a.out) + ((int64_t)(first_token(c) + row) * heads + oh) * B +
                 cols + k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) out[i] = b[i];
@@ -897,22 +913,26 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       if (it < total && c == 0) {
         const int64_t where = slot * a.s.hv + oh * share + g;
         log2a = linear::log2_decay(a.s, oh * share + g);
-        const float* from = a.states + where * D * D;
+        const float* from = a.states + where * A * B;
         const int M = max(top_of(a.x_top, where, -110) + top_of(a.y_top, where, -110), -97);
         const float enter = REVERSE ? 1.f : linear::power(log2a, 1);
         uint32_t top = 0;
-        if (a.transposed) {
+        if (!grows) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) S[i] = make_float2(0.f, 0.f);
+        } else if (a.transposed) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            S[i] = make_float2(from[(cols + 2 * i) * D + row], from[(cols + 2 * i + 1) * D + row]);
+            S[i] = make_float2(from[(cols + 2 * i) * A + row], from[(cols + 2 * i + 1) * A + row]);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float4 v = *reinterpret_cast<const float4*>(from + row * D + cols + 2 * i);
+            const float4 v = *reinterpret_cast<const float4*>(from + row * B + cols + 2 * i);
             S[i] = make_float2(v.x, v.y);
             S[i + 1] = make_float2(v.z, v.w);
           }
         }
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           S[i] = mul2(S[i], make_float2(enter, enter));
@@ -925,6 +945,15 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         ez = a.z_top ? top_of(a.z_top, where, -60) : 0;
         bound.start(__int_as_float(((volatile int*)misc)[2 + (g & 1)]), M, log2a);
       }
+      if (SUM && it > 0 && g_before > 0 && lane % 8 == 0) {  // (the running sum's lines, 8 rows each)
+        const int m = tokens(c_before);
+        const float4* sum =
+            reinterpret_cast<const float4*>(a.partial + ((int64_t)oh * a.s.T + first_token(c_before)) * B) +
+            (int64_t)(cols / 4) * m + row;
+        if (mine && row < m)
+          for (int i = 0; i < 16; ++i) asm volatile("prefetch.global.L1 [%0];" ::"l"(sum + i * m));
+      }
+      __syncwarp();
       if (it > 0) {  // (the last chunk's use of the copy)
         wait_bar(one(kSums), (it - 1) & 1, failed);
         fence_after_sync();
@@ -935,6 +964,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         const float s = two_to(15 - E);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
+          if (!mine) break;
           float2 f[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = mul2(S[4 * k + i], make_float2(s, s));
@@ -954,6 +984,8 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
           fence_after_sync();
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
+            // (a warp's rows are all before A, or all behind it)
+            if (!grows) break;
             uint32_t p[16];
             tmem_ld16_nw(tm_g + lanes + cols + 2 * k, p);
             tmem_wait_ld16(p);
@@ -995,18 +1027,18 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         const uint32_t st = base + (it & 1) * PassSmem::stage;
         wait_bar(bar(kFull, it), half(it), failed);
         if (!a.z_top) {
-          ez = live ? exponent_of(row_max_of(st + PassSmem::Z, row), -60) : -60;
+          ez = live ? exponent_of(row_max_of(st + PassSmem::Z, row, A), -60) : -60;
           if (it >= 2) wait_bar(bar(kSumsRead, it - 2), half(it - 2), failed);  // (who reads it there)
           targets[C * (it & 1) + row] = ez;
           mbar_arrive(bar(kRows, it));
         }
         if (c + 1 < chunks) {
           wait_bar(bar(kScores, it), half(it), failed);  // (x as it was has been read)
-          open_row(st + PassSmem::X, row, live,
+          open_row(st + PassSmem::X, row, A, live,
                    REVERSE || m == C ? x_whole : live ? linear::power(log2a, m - row) * x_scale : 0.f);
         }
         wait_bar(bar(kFullY, it), half(it), failed);
-        open_row(st + PassSmem::Y, row, live, two_to(14 - ey));
+        open_row(st + PassSmem::Y, row, B, live, two_to(14 - ey));
         fence_async_smem();
         mbar_arrive(bar(kValues, it));
       }
@@ -1021,52 +1053,61 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
   if (tid == 0 && *failed) set_status(a.s.status, GDN_ERR_DEVICE_TIMEOUT);
 }
 
-// Rows [T, heads, 128] bf16 read in boxes of 64 features of one head and `tokens` tokens (128-byte
+// Rows [T, heads, width] bf16 read in boxes of 64 features of one head and `tokens` tokens (128-byte
 // swizzle); tokens past T read as zeros.
-cudaError_t rows_map(CUtensorMap* m, const LinearRows& r, int64_t T, int heads, int tokens) {
+cudaError_t rows_map(CUtensorMap* m, const LinearRows& r, int64_t T, int heads, int width, int tokens) {
   EncodeTiled fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+  const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)T};
   // (the stride of a dimension of one row means nothing, but has to be one)
-  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? r.hs * 2 : D * 2),
-                                 (cuuint64_t)(T > 1 ? r.ts * 2 : (int64_t)heads * D * 2)};
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? r.hs * 2 : width * 2),
+                                 (cuuint64_t)(T > 1 ? r.ts * 2 : (int64_t)heads * width * 2)};
   const cuuint32_t box[3] = {64, 1, (cuuint32_t)tokens}, each[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(r.p), dims, strides, box, each,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <bool REVERSE, bool SUM> cudaError_t launch_pass(const LinearPass& a, cudaStream_t s) {
+template <bool WIDE> cudaError_t launch_state(const LinearState& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(linear_pass_tc_kernel<REVERSE, SUM>, PassSmem::bytes, done);
-  const int heads = a.s.hv / a.out_share;
-  const LinearRows out = {a.out, (int64_t)heads * D, D, a.out_share};
-  CUtensorMap mz, mx, my, mo;
-  if (e == cudaSuccess) e = rows_map(&mz, a.z, a.s.T, a.s.hv / a.z.share, C);
-  if (e == cudaSuccess) e = rows_map(&mx, a.x, a.s.T, a.s.hv / a.x.share, C);
-  if (e == cudaSuccess) e = rows_map(&my, a.y, a.s.T, a.s.hv / a.y.share, C);
-  if (e == cudaSuccess) e = rows_map(&mo, out, a.s.T, heads, C);
+  cudaError_t e = allow_smem(linear_state_tc_kernel<WIDE>, StateSmem::bytes, done);
+  CUtensorMap mx, my;
+  if (e == cudaSuccess) e = rows_map(&mx, a.x, a.s.T, a.s.hv / a.x.share, a.s.K, kTile);
+  if (e == cudaSuccess) e = rows_map(&my, a.y, a.s.T, a.s.hv / a.y.share, a.s.V, kTile);
   if (e != cudaSuccess) return e;
-  return launch_ordered(linear_pass_tc_kernel<REVERSE, SUM>, dim3((unsigned)(a.s.slots * heads)),
+  return launch_ordered(linear_state_tc_kernel<WIDE>, dim3((unsigned)(a.s.slots * a.s.hv)), kStateThreads,
+                        StateSmem::bytes, s, a, mx, my);
+}
+
+template <bool REVERSE, bool SUM, bool WIDE> cudaError_t launch_pass(const LinearPass& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(linear_pass_tc_kernel<REVERSE, SUM, WIDE>, PassSmem::bytes, done);
+  const int heads = a.s.hv / a.out_share;
+  const LinearRows out = {a.out, (int64_t)heads * a.B, a.B, a.out_share};
+  CUtensorMap mz, mx, my, mo;
+  if (e == cudaSuccess) e = rows_map(&mz, a.z, a.s.T, a.s.hv / a.z.share, a.A, C);
+  if (e == cudaSuccess) e = rows_map(&mx, a.x, a.s.T, a.s.hv / a.x.share, a.A, C);
+  if (e == cudaSuccess) e = rows_map(&my, a.y, a.s.T, a.s.hv / a.y.share, a.B, C);
+  if (e == cudaSuccess) e = rows_map(&mo, out, a.s.T, heads, a.B, C);
+  if (e != cudaSuccess) return e;
+  return launch_ordered(linear_pass_tc_kernel<REVERSE, SUM, WIDE>, dim3((unsigned)(a.s.slots * heads)),
                         kPassThreads, PassSmem::bytes, s, a, mz, mx, my, mo);
 }
 
 }  // namespace
 
 cudaError_t linear_state_tc(const LinearState& a, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(linear_state_tc_kernel, StateSmem::bytes, done);
-  CUtensorMap mx, my;
-  if (e == cudaSuccess) e = rows_map(&mx, a.x, a.s.T, a.s.hv / a.x.share, kTile);
-  if (e == cudaSuccess) e = rows_map(&my, a.y, a.s.T, a.s.hv / a.y.share, kTile);
-  if (e != cudaSuccess) return e;
-  return launch_ordered(linear_state_tc_kernel, dim3((unsigned)(a.s.slots * a.s.hv)), kStateThreads,
-                        StateSmem::bytes, s, a, mx, my);
+  return a.s.K == D && a.s.V == D ? launch_state<true>(a, s) : launch_state<false>(a, s);
 }
 
 cudaError_t linear_pass_tc(const LinearPass& a, cudaStream_t s) {
-  if (a.out_share > 1) return a.reverse ? launch_pass<true, true>(a, s) : launch_pass<false, true>(a, s);
-  return a.reverse ? launch_pass<true, false>(a, s) : launch_pass<false, false>(a, s);
+  const bool wide = a.A == D && a.B == D;
+  if (a.out_share > 1) {
+    if (a.reverse) return wide ? launch_pass<true, true, true>(a, s) : launch_pass<true, true, false>(a, s);
+    return wide ? launch_pass<false, true, true>(a, s) : launch_pass<false, true, false>(a, s);
+  }
+  if (a.reverse) return wide ? launch_pass<true, false, true>(a, s) : launch_pass<true, false, false>(a, s);
+  return wide ? launch_pass<false, false, true>(a, s) : launch_pass<false, false, false>(a, s);
 }
 
 }  // namespace gdn

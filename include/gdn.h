@@ -386,8 +386,10 @@ size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p);
  * recorded.  The same inputs give the same bits.  A value of a sequence that is not finite makes
  * that sequence's outputs and final state undefined from up to 127 tokens before it on (in the
  * head that reads it), and no other's.
- * Precision: states are carried and h_final is formed to fp32 accuracy.  bf16 I/O with K = V = 128
- * runs on the tensor cores, elsewhere everything is fp32 arithmetic. */
+ * Precision: states are carried and h_final is formed to fp32 accuracy.  fp32 I/O is fp32 arithmetic.  bf16
+ * I/O runs on the tensor cores: q . k of the inputs as they are; the weighted products, the weighted rows
+ * of q and k and the state enter the other products as fp16 (scaled by powers of two, so that no size of
+ * the inputs is out of range; 2^-11 of a term each), all sums are fp32. */
 gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, const void* k,
                                 const void* v, const float* log_decay, const float* h0,
                                 const int32_t* cu_seqlens, void* out, float* h_final,

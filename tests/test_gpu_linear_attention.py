@@ -52,7 +52,7 @@ class Case:
         s = scale[1] * scale[2]
         self.h0 = (rand(N, hv, K, V) * s).cuda() if carry else None
         self.dh = (rand(N, hv, K, V) * scale[0] * scale[3]).cuda() if carry else None
-        self.cores = io is BF16 and K == V == 128
+        self.cores = io is BF16
 
     def forward(self, gdn, **kw):
         return gdn.linear_attention(self.q, self.k, self.v, self.g, self.h0, self.cu,
@@ -84,7 +84,8 @@ SHAPES = [  # lengths, hk, hv
 
 
 @pytest.mark.parametrize("io,K,V", [(BF16, 128, 128), (F32, 128, 128), (BF16, 64, 128),
-                                    (F32, 128, 64), (BF16, 64, 64), (F32, 64, 64)])
+                                    (F32, 128, 64), (BF16, 64, 64), (F32, 64, 64),
+                                    (BF16, 128, 64)])
 @pytest.mark.parametrize("lens,hk,hv", SHAPES)
 def test_prompts(gdn, lens, hk, hv, io, K, V):
     c = Case(lens, hk, hv, K, V, io, carry=len(lens) != 1, seed=len(lens) + hv)
@@ -92,7 +93,8 @@ def test_prompts(gdn, lens, hk, hv, io, K, V):
 
 
 @pytest.mark.parametrize("io,K,V", [(BF16, 128, 128), (F32, 128, 128), (BF16, 64, 128),
-                                    (F32, 128, 64), (BF16, 64, 64), (F32, 64, 64)])
+                                    (F32, 128, 64), (BF16, 64, 64), (F32, 64, 64),
+                                    (BF16, 128, 64)])
 @pytest.mark.parametrize("lens,hk,hv", SHAPES)
 def test_gradients(gdn, lens, hk, hv, io, K, V):
     c = Case(lens, hk, hv, K, V, io, carry=len(lens) != 1, seed=10 + len(lens) + hv)
@@ -100,10 +102,11 @@ def test_gradients(gdn, lens, hk, hv, io, K, V):
 
 
 @pytest.mark.parametrize("hk,hv", [(4, 12), (12, 12)])
-@pytest.mark.parametrize("io", [BF16, F32])
-def test_walks_of_several_chunks(gdn, io, hk, hv):
+@pytest.mark.parametrize("io,K,V", [(BF16, 128, 128), (F32, 128, 128), (BF16, 64, 128),
+                                    (BF16, 128, 64), (BF16, 64, 64)])
+def test_walks_of_several_chunks(gdn, io, K, V, hk, hv):
     """So many tokens and heads that a segment is several chunks, and its last one a part of one."""
-    c = Case([4000, 33, 2111], hk, hv, 128, 128, io, seed=hk)
+    c = Case([4000, 33, 2111], hk, hv, K, V, io, seed=hk)
     c.check_forward(c.forward(gdn))
     c.check_backward(c.backward(gdn))
 
