@@ -858,31 +858,28 @@ bool linear_on_tc(const gdn_linear_problem* p) {
          mapped(p->v_token_stride, p->v_head_stride, p->hv);
 }
 
-// A segment's tokens, in whole chunks.  On the CUDA cores so many that the segments of all heads fill
-// the SMs a few times over.  On the tensor cores an SM holds one segment of one output head at a time (in
-// the backward pass of shared heads, of all the value heads that it sums), so what counts is how many
-// rounds of the 152 SMs there are and how long one takes: its tokens and about 640 more for its start and
-// end.  (65536 tokens of 32 heads: 4 segments, one round of 128 SMs, 613 us; 9, two rounds of 144, 555; 16,
-// 674; 19, four rounds of 152, 564; 32, 634.)  Only the sum of the sequences' lengths is known here: they are
-// taken as alike, give or take a seventh.
+// A segment's tokens, in whole chunks.  An SM holds one segment of one output head at a time (in the
+// backward pass of shared heads, of all the value heads that it sums), so what counts is how many rounds of
+// the 152 SMs there are and how long one takes: its tokens and some more for its start and end, 640 on the
+// tensor cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
+// 613 us; 9, two rounds of 144, 555; 16, 674; 19, four rounds of 152, 564; 32, 634.)  Only the sum of the
+// sequences' lengths is known here: they are taken as alike, give or take a seventh.
 int linear_segment(const gdn_linear_problem* p, bool backward) {
   const int64_t T = p->total_tokens, N = p->num_seqs, hv = p->hv;
-  if (!linear_on_tc(p)) {
-    const int64_t even = (T * hv / (152 * 2) + 63) / 64 * 64;
-    return (int)(even < 64 ? 64 : even > 1024 ? 1024 : even);
-  }
+  const bool tc = linear_on_tc(p);
+  const int64_t chunk = tc ? 128 : 64, more = tc ? 640 : 96;
   const int64_t heads = backward ? p->hk : hv, share = hv / heads;
   const int64_t each = N == 1 ? T : (T + N - 1) / N * 8 / 7 + 1;
   int64_t best = 0, least = INT64_MAX;
-  for (int64_t k = 1; k <= 64 && (k == 1 || each > (k - 1) * 128); ++k) {
-    const int64_t length = ((each + k - 1) / k + 127) / 128 * 128;
-    const int64_t rounds = (N * k * heads + 151) / 152, cost = rounds * share * (length + 640);
+  for (int64_t k = 1; k <= 128 && (k == 1 || each > (k - 1) * chunk); ++k) {
+    const int64_t length = ((each + k - 1) / k + chunk - 1) / chunk * chunk;
+    const int64_t rounds = (N * k * heads + 151) / 152, cost = rounds * share * (length + more);
     if (cost < least) {
       least = cost;
       best = length;
     }
   }
-  return (int)(best < 128 ? 128 : best < (int64_t)1 << 30 ? best : (int64_t)1 << 30);
+  return (int)(best < chunk ? chunk : best < (int64_t)1 << 30 ? best : (int64_t)1 << 30);
 }
 
 gdn::LinearShape linear_shape(const gdn_linear_problem* p, bool backward, const float* log_decay,

@@ -30,6 +30,52 @@ __device__ __forceinline__ int64_t offset_of(const CheckpointArgs::Rows& t, int6
   return (int64_t)token * t.ts + (int64_t)(r - token * (uint32_t)t.heads) * t.hs;
 }
 
+// The largest magnitude of a lane's eight elements; not finite where one of them is not.
+__device__ __forceinline__ float largest(const Quad<float> (&q)[2]) {
+  float f[8], m = 0.f;
+  q[0].open(f);
+  q[1].open(f + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = f[i] == f[i] ? fmaxf(m, fabsf(f[i])) : INFINITY;
+  return m;
+}
+__device__ __forceinline__ float largest(const Quad<__nv_bfloat16> (&q)[2]) {
+  const uint32_t w[4] = {q[0].v.x, q[0].v.y, q[1].v.x, q[1].v.y};
+  __nv_bfloat162 m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+  const __nv_bfloat162 r = __hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3]));
+  const float2 f = __bfloat1622float2(r);
+  return f.x == f.x && f.y == f.y ? fmaxf(f.x, f.y) : INFINITY;
+}
+// The codes of eight finite elements of a row, whose largest gives qmax: none is beyond it by more than
+// the rounding of fp32, and none is rounded beyond it.  int8: a value of magnitude up to 127, added to
+// 3 2^22, has its nearest integer (ties to even) in the sum's low bits, which are its code.
+template <bool E4M3> __device__ __forceinline__ uint2 codes_of(const float* f, float inv) {
+  // (the product is rounded by itself, as the definition has it: no packed or fused form)
+  float2 y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) y[i] = make_float2(__fmul_rn(f[2 * i], inv), __fmul_rn(f[2 * i + 1], inv));
+  uint32_t r[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (E4M3) {
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[2 * i].y), "f"(y[2 * i].x));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[2 * i + 1].y), "f"(y[2 * i + 1].x));
+      r[i] = (uint32_t)lo | (uint32_t)hi << 16;
+    } else {
+      const float big = 12582912.f;
+      const float2 a = make_float2(__fadd_rn(y[2 * i].x, big), __fadd_rn(y[2 * i].y, big));
+      const float2 b = make_float2(__fadd_rn(y[2 * i + 1].x, big), __fadd_rn(y[2 * i + 1].y, big));
+      const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+      const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+      r[i] = __byte_perm(lo, hi, 0x5410);
+    }
+  }
+  return make_uint2(r[0], r[1]);
+}
+
 template <int D, typename IO, bool E4M3>
 __device__ __forceinline__ void pack_rows(const CheckpointArgs::Rows& t, int64_t block,
                                           int32_t* status) {
@@ -53,32 +99,37 @@ __device__ __forceinline__ void pack_rows(const CheckpointArgs::Rows& t, int64_t
 #pragma unroll
   for (int k = 0; k < kGroups; ++k) {
     const int64_t row = row0 + k * RPG;
-    float f[8], amax = 0.f;
+    float f[8], amax = largest(q[k]);
     q[k][0].open(f);
     q[k][1].open(f + 4);
-    bool bad = false;
+    const bool bad = !is_finite(amax);
+    if (bad) {
+      amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool fine = is_finite(f[i]);
-      bad |= !fine;
-      amax = fmaxf(amax, fine ? fabsf(f[i]) : 0.f);
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, is_finite(f[i]) ? fabsf(f[i]) : 0.f);
     }
 #pragma unroll
     for (int m = LANES / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
     const float scale = amax >= kKvTiny ? amax * (float)(1.0 / kv_qmax<E4M3>()) : 0.f;
     const float inv = scale > 0.f ? 1.f / scale : 0.f;
-    uint32_t c[8];
+    uint2 codes;
+    if (!bad) {
+      codes = codes_of<E4M3>(f, inv);
+    } else {
+      uint32_t c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      c[i] = kv_code<E4M3>(is_finite(f[i]) ? f[i] * inv
-                           : f[i] == f[i]  ? copysignf(kv_qmax<E4M3>(), f[i]) : 0.f);
+      for (int i = 0; i < 8; ++i)
+        c[i] = kv_code<E4M3>(is_finite(f[i]) ? f[i] * inv
+                             : f[i] == f[i]  ? copysignf(kv_qmax<E4M3>(), f[i]) : 0.f);
+      codes = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
+                         c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+    }
     if (row < t.rows) {
       if (bad) set_status(status, GDN_ERR_DEVICE_RANGE);
-      *reinterpret_cast<uint2*>(t.codes + row * D + 8 * sub) =
-          make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-                     c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
+      *reinterpret_cast<uint2*>(t.codes + row * D + 8 * sub) = codes;
       if (sub == 0) t.scale[row] = scale;
     }
+    __syncwarp();
   }
 }
 

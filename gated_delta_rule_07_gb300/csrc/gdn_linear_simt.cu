@@ -146,117 +146,121 @@ __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const __grid_cons
 
 // ------------------------------------------------------------------ the pass
 
-// One block a (slot, output head, 64 output columns) walks the segment's chunks of 64 tokens with S in
-// shared memory.  Output heads that several value heads add to are walked once for each, the running
-// sum kept in fp32 (in the output where that is fp32): always in the same order.
-constexpr int BW = 64;
-template <int A> constexpr int pass_smem() {
-  return (2 * C * (A + 4) + C * (BW + 4) + A * (BW + 4) + C * (C + 4)) * 4;
+// One block a (slot, output head) walks the segment's chunks of 64 tokens with S in shared memory.  Output
+// heads that several value heads add to are walked once for each, the running sum kept in fp32 (in the
+// output where that is fp32): always in the same order.
+//
+// 49152 multiply-adds a token at A = B = 128 make it the CUDA cores' to bound, if their operands come
+// cheaply: a thread has four neighbouring columns of several rows (of P, two columns of eight), so that a
+// warp reads the rows' operand as broadcasts and four steps of it at once.  (Threads of 4 x 4 and 64
+// columns a block: 571 us for four sequences of 2048 tokens, 16 heads of 128; so 226.)
+template <int A, int B> constexpr int pass_smem() {
+  return (2 * C * (A + 4) + C * B + A * B + C * (C + 4) + C + 4) * 4;
 }
-template <int A, typename IO>
-__global__ void __launch_bounds__(kThreads) linear_pass_kernel(LinearPass a) {
+template <int A, int B, typename IO>
+__global__ void __launch_bounds__(kThreads, 1) linear_pass_kernel(LinearPass a) {
+  constexpr int CL = B / 4, RG = kThreads / CL;  // threads of a row, groups of rows
+  constexpr int MO = C / RG, MS = A / RG;        // rows a thread of the output, of S
   extern __shared__ __align__(16) float smem[];
   float* zs = smem;                    // [C][A + 4]
   float* xs = zs + C * (A + 4);        // [C][A + 4]
-  float* ys = xs + C * (A + 4);        // [C][BW + 4]
-  float* S = ys + C * (BW + 4);        // [A][BW + 4]
-  float* P = S + A * (BW + 4);         // [C][C + 4]
+  float* ys = xs + C * (A + 4);        // [C][B]
+  float* S = ys + C * B;               // [A][B]
+  float* P = S + A * B;                // [C][C + 4]
+  float* power = P + C * (C + 4);      // [C + 1]: a^i
   stream_order();
   if (!linear::usable(a.s)) return;
   int n;
   int64_t t0, t1;
   const int64_t slot = blockIdx.x;
   if (!linear::slot_tokens(a.s, slot, n, t0, t1)) return;
-  const int oh = blockIdx.y, c0 = blockIdx.z * BW;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int oh = blockIdx.y;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int rg = threadIdx.x / CL, col = threadIdx.x % CL * 4;
   const int chunks = (int)((t1 - t0 + C - 1) / C);
-  const int64_t ots = (int64_t)(a.s.hv / a.out_share) * a.B;
-  IO* out = static_cast<IO*>(a.out) + (int64_t)oh * a.B + c0 + 4 * tx;
-  float* sum = sizeof(IO) == 4 ? reinterpret_cast<float*>(out)
-                               : a.partial + (int64_t)oh * a.B + c0 + 4 * tx;
+  const int64_t ots = (int64_t)(a.s.hv / a.out_share) * B;
+  IO* out = static_cast<IO*>(a.out) + (int64_t)oh * B + col;
+  float* sum = sizeof(IO) == 4 ? reinterpret_cast<float*>(out) : a.partial + (int64_t)oh * B + col;
 
   for (int g = 0; g < a.out_share; ++g) {
     const int head = oh * a.out_share + g;
     const float log2a = linear::log2_decay(a.s, head);
     const IO* z = head_rows<IO>(a.z, head);
     const IO* x = head_rows<IO>(a.x, head);
-    const IO* y = head_rows<IO>(a.y, head) + c0;
-    const float* st = a.states + (slot * a.s.hv + head) * a.A * a.B;
+    const IO* y = head_rows<IO>(a.y, head);
+    const float* st = a.states + (slot * a.s.hv + head) * A * B;
     const float enter = a.reverse ? 1.f : linear::power(log2a, 1);
-    for (int i = threadIdx.x; i < A * BW; i += kThreads) {
+    for (int i = threadIdx.x; i < A * B; i += kThreads) {
       // (the faster index along the stored rows)
-      const int r = a.transposed ? i % A : i / BW, c = a.transposed ? i / A : i % BW;
-      const float v = a.transposed ? st[(int64_t)(c0 + c) * a.A + r] : st[(int64_t)r * a.B + c0 + c];
-      S[r * (BW + 4) + c] = v * enter;
+      const int r = a.transposed ? i % A : i / B, c = a.transposed ? i / A : i % B;
+      S[r * B + c] = (a.transposed ? st[c * A + r] : st[i]) * enter;
     }
+    if (threadIdx.x <= C) power[threadIdx.x] = linear::power(log2a, threadIdx.x);
     for (int ci = 0; ci < chunks; ++ci) {
       const int64_t t = t0 + (int64_t)(a.reverse ? chunks - 1 - ci : ci) * C;
       const int m = (int)(t1 - t < C ? t1 - t : C);
       stage<C, A, IO, false>(zs, A + 4, z, a.z.ts, t, m, 0.f, 0, 0);
       stage<C, A, IO, false>(xs, A + 4, x, a.x.ts, t, m, 0.f, 0, 0);
-      stage<C, BW, IO, false>(ys, BW + 4, y, a.y.ts, t, m, 0.f, 0, 0);
+      stage<C, B, IO, false>(ys, B, y, a.y.ts, t, m, 0.f, 0, 0);
       __syncthreads();
-      {  // P[i][j] = a^{|i - j|} z_i . x_j where j is at or before i
-        float p[4][4] = {};
-#pragma unroll 4
+      {  // P[i][j] = a^{|i - j|} z_i . x_j where j is at or before i; a warp has eight rows
+        float p[8][2] = {};
+#pragma unroll 2
         for (int k = 0; k < A; k += 4) {
-          float4 u[4], w[4];
+          float4 w[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            u[i] = *reinterpret_cast<const float4*>(zs + (4 * ty + i) * (A + 4) + k);
-            w[i] = *reinterpret_cast<const float4*>(xs + (tx + 16 * i) * (A + 4) + k);
+          for (int j = 0; j < 2; ++j)
+            w[j] = *reinterpret_cast<const float4*>(xs + (lane + 32 * j) * (A + 4) + k);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 u = *reinterpret_cast<const float4*>(zs + (8 * warp + i) * (A + 4) + k);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              p[i][j] = fmaf(u.x, w[j].x, fmaf(u.y, w[j].y, fmaf(u.z, w[j].z, fmaf(u.w, w[j].w, p[i][j]))));
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              p[i][j] = fmaf(u[i].x, w[j].x, fmaf(u[i].y, w[j].y,
-                        fmaf(u[i].z, w[j].z, fmaf(u[i].w, w[j].w, p[i][j]))));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = 4 * ty + i, c = tx + 16 * j, gap = a.reverse ? c - r : r - c;
-            P[r * (C + 4) + c] = gap >= 0 && c < m ? p[i][j] * linear::power(log2a, gap) : 0.f;
+          for (int j = 0; j < 2; ++j) {
+            const int r = 8 * warp + i, c = lane + 32 * j, gap = a.reverse ? c - r : r - c;
+            P[r * (C + 4) + c] = gap >= 0 && c < m ? p[i][j] * power[gap] : 0.f;
           }
       }
       __syncthreads();
-      float o[4][4] = {};
-#pragma unroll 4
-      for (int k = 0; k < A; ++k) {
-        const float4 w = *reinterpret_cast<const float4*>(S + k * (BW + 4) + 4 * tx);
+      float o[MO][4] = {};
+      auto times = [&](const float* u, int stride, const float* w, int steps) {  // o += rows of u by w
+#pragma unroll 2
+        for (int k = 0; k < steps; k += 4) {
+          float4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = zs[(4 * ty + i) * (A + 4) + k];
-          o[i][0] = fmaf(u, w.x, o[i][0]);
-          o[i][1] = fmaf(u, w.y, o[i][1]);
-          o[i][2] = fmaf(u, w.z, o[i][2]);
-          o[i][3] = fmaf(u, w.w, o[i][3]);
+          for (int l = 0; l < 4; ++l) v[l] = *reinterpret_cast<const float4*>(w + (k + l) * B + col);
+#pragma unroll
+          for (int i = 0; i < MO; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(u + (rg * MO + i) * stride + k);
+            const float e[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+              o[i][0] = fmaf(e[l], v[l].x, o[i][0]);
+              o[i][1] = fmaf(e[l], v[l].y, o[i][1]);
+              o[i][2] = fmaf(e[l], v[l].z, o[i][2]);
+              o[i][3] = fmaf(e[l], v[l].w, o[i][3]);
+            }
+          }
         }
-      }
+      };
+      times(zs, A + 4, S, A);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
-        const float w = linear::power(log2a, a.reverse ? (r < m ? m - 1 - r : 0) : r);
+      for (int i = 0; i < MO; ++i) {
+        const int r = rg * MO + i;
+        const float w = power[a.reverse ? (r < m ? m - 1 - r : 0) : r];
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[i][j] *= w;
       }
-#pragma unroll 4
-      for (int k = 0; k < C; ++k) {
-        const float4 w = *reinterpret_cast<const float4*>(ys + k * (BW + 4) + 4 * tx);
+      times(P, C + 4, ys, C);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = P[(4 * ty + i) * (C + 4) + k];
-          o[i][0] = fmaf(u, w.x, o[i][0]);
-          o[i][1] = fmaf(u, w.y, o[i][1]);
-          o[i][2] = fmaf(u, w.z, o[i][2]);
-          o[i][3] = fmaf(u, w.w, o[i][3]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i;
+      for (int i = 0; i < MO; ++i) {
+        const int r = rg * MO + i;
         if (r >= m) continue;
         const int64_t row = (t + r) * ots;
         if (g > 0) {
@@ -269,32 +273,39 @@ __global__ void __launch_bounds__(kThreads) linear_pass_kernel(LinearPass a) {
           put4(out + row, o[i]);
       }
       __syncthreads();
-      {  // S <- a^m S + sum_j a^{steps to the chunk's end} x_j y_j^T
-        constexpr int MA = A / 16;
-        const float w = linear::power(log2a, m);
-        float acc[MA][4];
+      if (ci + 1 < chunks) {  // S <- a^m S + sum_j a^{steps to the chunk's end} x_j y_j^T
+        const float w = power[m];
+        float* const mine = S + rg * MS * B + col;
+        float acc[MS][4];
 #pragma unroll
-        for (int i = 0; i < MA; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = w * S[(ty * MA + i) * (BW + 4) + 4 * tx + j];
+        for (int i = 0; i < MS; ++i) {
+          const float4 v = *reinterpret_cast<const float4*>(mine + i * B);
+          acc[i][0] = w * v.x; acc[i][1] = w * v.y; acc[i][2] = w * v.z; acc[i][3] = w * v.w;
+        }
 #pragma unroll 2
         for (int k = 0; k < m; ++k) {
-          const float wk = linear::power(log2a, a.reverse ? k + 1 : m - k);
-          const float4 yk = *reinterpret_cast<const float4*>(ys + k * (BW + 4) + 4 * tx);
+          const float wk = power[a.reverse ? k + 1 : m - k];
+          float4 v = *reinterpret_cast<const float4*>(ys + k * B + col);
+          v.x *= wk; v.y *= wk; v.z *= wk; v.w *= wk;
 #pragma unroll
-          for (int i = 0; i < MA; ++i) {
-            const float u = wk * xs[k * (A + 4) + ty * MA + i];
-            acc[i][0] = fmaf(u, yk.x, acc[i][0]);
-            acc[i][1] = fmaf(u, yk.y, acc[i][1]);
-            acc[i][2] = fmaf(u, yk.z, acc[i][2]);
-            acc[i][3] = fmaf(u, yk.w, acc[i][3]);
+          for (int i = 0; i < MS; i += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(xs + k * (A + 4) + rg * MS + i);
+            const float e[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int l = 0; l < 4; ++l) {
+              acc[i + l][0] = fmaf(e[l], v.x, acc[i + l][0]);
+              acc[i + l][1] = fmaf(e[l], v.y, acc[i + l][1]);
+              acc[i + l][2] = fmaf(e[l], v.z, acc[i + l][2]);
+              acc[i + l][3] = fmaf(e[l], v.w, acc[i + l][3]);
+            }
           }
         }
 #pragma unroll
-        for (int i = 0; i < MA; ++i) put4(S + (ty * MA + i) * (BW + 4) + 4 * tx, acc[i]);
+        for (int i = 0; i < MS; ++i) put4(mine + i * B, acc[i]);
+        __syncthreads();
       }
-      __syncthreads();
     }
+    __syncthreads();
   }
 }
 
@@ -305,12 +316,16 @@ cudaError_t launch_state(const LinearState& a, cudaStream_t s) {
                   : launch_ordered(linear_state_kernel<K, V, float>, grid, kThreads, 0, s, a);
 }
 
-template <int A, typename IO> cudaError_t launch_pass(const LinearPass& a, cudaStream_t s) {
+template <int A, int B, typename IO> cudaError_t launch_pass(const LinearPass& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(linear_pass_kernel<A, IO>, pass_smem<A>(), done);
+  const cudaError_t e = allow_smem(linear_pass_kernel<A, B, IO>, pass_smem<A, B>(), done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)a.s.slots, (unsigned)(a.s.hv / a.out_share), (unsigned)(a.B / BW));
-  return launch_ordered(linear_pass_kernel<A, IO>, grid, kThreads, pass_smem<A>(), s, a);
+  const dim3 grid((unsigned)a.s.slots, (unsigned)(a.s.hv / a.out_share));
+  return launch_ordered(linear_pass_kernel<A, B, IO>, grid, kThreads, pass_smem<A, B>(), s, a);
+}
+template <typename IO> cudaError_t launch_pass_of(const LinearPass& a, cudaStream_t s) {
+  if (a.A == 128) return a.B == 128 ? launch_pass<128, 128, IO>(a, s) : launch_pass<128, 64, IO>(a, s);
+  return a.B == 128 ? launch_pass<64, 128, IO>(a, s) : launch_pass<64, 64, IO>(a, s);
 }
 
 }  // namespace
@@ -336,9 +351,7 @@ cudaError_t linear_scan(const LinearScan* scans, int count, cudaStream_t s) {
 }
 
 cudaError_t linear_pass_simt(const LinearPass& a, cudaStream_t s) {
-  if (a.A == 128)
-    return a.s.bf16 ? launch_pass<128, __nv_bfloat16>(a, s) : launch_pass<128, float>(a, s);
-  return a.s.bf16 ? launch_pass<64, __nv_bfloat16>(a, s) : launch_pass<64, float>(a, s);
+  return a.s.bf16 ? launch_pass_of<__nv_bfloat16>(a, s) : launch_pass_of<float>(a, s);
 }
 
 }  // namespace gdn
