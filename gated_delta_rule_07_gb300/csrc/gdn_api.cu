@@ -956,7 +956,9 @@ gdn_status checkpoint_args(const gdn_checkpoint* t, int count, int format,
       return GDN_ERR_INVALID_ARGUMENT;
     a.t[i] = {c.x, static_cast<uint8_t*>(c.codes), c.scale, c.total_tokens * c.heads,
               stride_of(c.token_stride, c.total_tokens), stride_of(c.head_stride, c.heads),
-              c.heads, c.head_dim, c.io_dtype == GDN_BF16};
+              c.heads, c.head_dim, c.io_dtype == GDN_BF16, false};
+    a.t[i].packed = (c.heads == 1 || a.t[i].hs == c.head_dim) &&
+                    (c.total_tokens == 1 || a.t[i].ts == (int64_t)c.heads * c.head_dim);
     blocks += a.t[i].rows / 32 + 1;  // (a block has 32 rows at least)
   }
   return blocks > (int64_t)INT32_MAX ? GDN_ERR_UNSUPPORTED : GDN_OK;

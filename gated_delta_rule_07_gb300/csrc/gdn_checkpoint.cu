@@ -26,6 +26,7 @@ __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823
 
 // Offset in x of row `row` (its heads are neighbours in the packed tensors, strided in x).
 __device__ __forceinline__ int64_t offset_of(const CheckpointArgs::Rows& t, int64_t row) {
+  if (t.packed) return row * t.D;
   const uint32_t r = (uint32_t)row, token = r / (uint32_t)t.heads;
   return (int64_t)token * t.ts + (int64_t)(r - token * (uint32_t)t.heads) * t.hs;
 }

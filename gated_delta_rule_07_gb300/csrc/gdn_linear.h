@@ -104,7 +104,7 @@ struct CheckpointArgs {
     float* scale;           // [T, heads]
     int64_t rows, ts, hs;   // T heads rows
     int heads, D;
-    bool bf16;
+    bool bf16, packed;      // packed: x's rows follow one another
   } t[kCheckpoints];
   int64_t first[kCheckpoints + 1];  // blocks before each tensor's
   int32_t* status;

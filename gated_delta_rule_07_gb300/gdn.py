@@ -861,8 +861,7 @@ def checkpoint_pack(*tensors, dtype=torch.int8, check_status=False, stream=None)
     each row of D elements, int8 or float8_e4m3fn.  With check_status, raises where a value was not
     finite."""
     if stream is not None:
-        side = _side_stream(stream, tensors)
-        made = _on(side, lambda: tuple(x for c in checkpoint_pack(
+        made = _on(stream, lambda: tuple(x for c in checkpoint_pack(
             *tensors, dtype=dtype, check_status=check_status) for x in (c.codes, c.scale)), *tensors)
     else:
         fmt = _KV_FORMATS.get(dtype)
@@ -870,9 +869,13 @@ def checkpoint_pack(*tensors, dtype=torch.int8, check_status=False, stream=None)
             _refuse("checkpoint_pack", f"dtype {dtype}", 2)
         if not tensors:
             _refuse("checkpoint_pack", "nothing to hold")
-        made = _checked(check_status, tensors[0].device, "checkpoint_pack",
-                        lambda st: _native.checkpoint_pack(st, fmt, *tensors))
-    return tuple(_checkpoint(made[2 * i], made[2 * i + 1], x.dtype) for i, x in enumerate(tensors))
+        if not check_status:
+            made = _native.checkpoint_pack(None, fmt, *tensors)
+        else:
+            made = _checked(True, tensors[0].device, "checkpoint_pack",
+                            lambda st: _native.checkpoint_pack(st, fmt, *tensors))
+    parts = iter(made)
+    return tuple([_checkpoint(codes, scale, x.dtype) for x, codes, scale in zip(tensors, parts, parts)])
 
 
 def _checkpoint(codes, scale, dtype):
@@ -893,8 +896,8 @@ def checkpoint_open(*checkpoints, stream=None):
                    *(t for c in checkpoints for t in (c.codes, c.scale)))
     if not checkpoints:
         _refuse("checkpoint_open", "nothing to open")
-    return _native.checkpoint_open(*(x for c in checkpoints
-                                     for x in (c.codes, c.scale, _IO[c.dtype])))
+    return _native.checkpoint_open(*[x for c in checkpoints
+                                     for x in (c.codes, c.scale, _IO[c.dtype])])
 
 
 # ------------------------------------------------------------------ convenience API
