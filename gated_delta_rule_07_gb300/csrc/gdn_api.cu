@@ -859,7 +859,7 @@ bool linear_on_tc(const gdn_linear_problem* p) {
 }
 
 // A segment's tokens, in whole chunks.  An SM holds one segment of one output head at a time (in the
-// backward pass of shared heads, of all the value heads that it sums), so what counts is how many rounds of
+// tensor cores' backward pass of shared heads, of all the value heads that it sums), so what counts is how many rounds of
 // the 152 SMs there are and how long one takes: its tokens and some more for its start and end, 640 on the
 // tensor cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
 // 613 us; 9, two rounds of 144, 555; 16, 674; 19, four rounds of 152, 564; 32, 634.)  Only the sum of the
@@ -868,7 +868,7 @@ int linear_segment(const gdn_linear_problem* p, bool backward) {
   const int64_t T = p->total_tokens, N = p->num_seqs, hv = p->hv;
   const bool tc = linear_on_tc(p);
   const int64_t chunk = tc ? 128 : 64, more = tc ? 640 : 96;
-  const int64_t heads = backward ? p->hk : hv, share = hv / heads;
+  const int64_t heads = backward && tc ? p->hk : hv, share = hv / heads;
   const int64_t each = N == 1 ? T : (T + N - 1) / N * 8 / 7 + 1;
   int64_t best = 0, least = INT64_MAX;
   for (int64_t k = 1; k <= 128 && (k == 1 || each > (k - 1) * chunk); ++k) {
@@ -920,13 +920,13 @@ cudaError_t linear_pass(const gdn_linear_problem* p, const gdn::LinearPass& a, c
 struct LinearBwdLayout {
   size_t h, d, partial, q, k, v, total;
 };
-LinearBwdLayout linear_bwd_layout(const gdn::LinearShape& s, bool saved) {
+LinearBwdLayout linear_bwd_layout(const gdn::LinearShape& s, bool tc, bool saved) {
   LinearBwdLayout L;
   const size_t e = s.bf16 ? 2 : 4, keys = (size_t)s.T * s.hk * s.K, values = (size_t)s.T * s.hv * s.V;
   L.h = 0;
   L.d = L.h + linear_states_bytes(s);
   L.partial = L.d + linear_states_bytes(s);
-  L.q = L.partial + (s.bf16 && s.hv > s.hk ? align_up(keys * sizeof(float)) : 0);
+  L.q = L.partial + (s.hv == s.hk ? 0 : align_up(keys * (tc ? 1 : s.hv / s.hk) * sizeof(float)));
   L.k = L.q + (saved ? align_up(keys * e) : 0);
   L.v = L.k + (saved ? align_up(keys * e) : 0);
   L.total = L.v + (saved ? align_up(values * e) : 0);
@@ -1006,7 +1006,7 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
 size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p, int saved) {
   if (check_linear(p) != GDN_OK) return 0;
   const gdn_linear_problem o = saved ? linear_opened(p) : *p;
-  return linear_bwd_layout(linear_shape(&o, true, nullptr, nullptr, nullptr), saved != 0).total;
+  return linear_bwd_layout(linear_shape(&o, true, nullptr, nullptr, nullptr), linear_on_tc(&o), saved != 0).total;
 }
 
 gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void* q,
@@ -1030,7 +1030,7 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
   const gdn_linear_problem opened = linear_opened(p);
   if (saved) p = &opened;
   const gdn::LinearShape s = linear_shape(p, true, log_decay, cu_seqlens, dev_status);
-  const LinearBwdLayout L = linear_bwd_layout(s, saved != nullptr);
+  const LinearBwdLayout L = linear_bwd_layout(s, linear_on_tc(p), saved != nullptr);
   if (!workspace || !aligned16(workspace) || ws_bytes < L.total) return GDN_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
   float* h = reinterpret_cast<float*>(ws + L.h);

@@ -26,7 +26,9 @@ __device__ __forceinline__ const IO* head_rows(const LinearRows& r, int head) {
 template <int ROWS, int D, typename IO, bool WEIGHTED>
 __device__ __forceinline__ void stage(float* dst, int stride, const IO* src, int64_t ts, int64_t t0,
                                       int n, float log2a, int w0, int w1) {
-  for (int i = threadIdx.x; i < ROWS * (D / 4); i += kThreads) {
+#pragma unroll 8
+  for (int i0 = 0; i0 < ROWS * (D / 4); i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
     const int r = i / (D / 4), c = i % (D / 4) * 4;
     Quad<IO> q;
     float f[4];
@@ -46,7 +48,8 @@ __device__ __forceinline__ void stage(float* dst, int stride, const IO* src, int
 
 // ------------------------------------------------------------------ a segment's own state
 
-// One block a (slot, value head): the K x V sums in registers, 32 tokens staged at a time.
+// One block a (slot, value head): the K x V sums in registers, 32 tokens staged at a time.  (Half of K a
+// block: 195 us for four sequences of 2048 tokens, 16 heads of 128, against 167.)
 template <int K, int V, typename IO>
 __global__ void __launch_bounds__(kThreads) linear_state_kernel(LinearState a) {
   constexpr int MK = K / 16, MV = V / 16;
@@ -146,14 +149,15 @@ __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const __grid_cons
 
 // ------------------------------------------------------------------ the pass
 
-// One block a (slot, output head) walks the segment's chunks of 64 tokens with S in shared memory.  Output
-// heads that several value heads add to are walked once for each, the running sum kept in fp32 (in the
-// output where that is fp32): always in the same order.
+// One block a (slot, value head) walks the segment's chunks of 64 tokens with S in shared memory.  What
+// several value heads add to one output head goes to fp32 rows of their own, which a kernel behind sums in
+// the heads' order.  (Walked one after another by one block: 104 us for the two such passes of four ragged
+// sequences of up to 500 tokens, three value heads to each of two key heads, instead of 39.)
 //
 // 49152 multiply-adds a token at A = B = 128 make it the CUDA cores' to bound, if their operands come
 // cheaply: a thread has four neighbouring columns of several rows (of P, two columns of eight), so that a
 // warp reads the rows' operand as broadcasts and four steps of it at once.  (Threads of 4 x 4 and 64
-// columns a block: 571 us for four sequences of 2048 tokens, 16 heads of 128; so 226.)
+// columns a block: 571 us for four sequences of 2048 tokens, 16 heads of 128; so 407, where the segments fill fewer SMs.)
 template <int A, int B> constexpr int pass_smem() {
   return (2 * C * (A + 4) + C * B + A * B + C * (C + 4) + C + 4) * 4;
 }
@@ -174,139 +178,148 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pass_kernel(LinearPass a) 
   int64_t t0, t1;
   const int64_t slot = blockIdx.x;
   if (!linear::slot_tokens(a.s, slot, n, t0, t1)) return;
-  const int oh = blockIdx.y;
+  const int head = blockIdx.y;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rg = threadIdx.x / CL, col = threadIdx.x % CL * 4;
   const int chunks = (int)((t1 - t0 + C - 1) / C);
-  const int64_t ots = (int64_t)(a.s.hv / a.out_share) * B;
-  IO* out = static_cast<IO*>(a.out) + (int64_t)oh * B + col;
-  float* sum = sizeof(IO) == 4 ? reinterpret_cast<float*>(out) : a.partial + (int64_t)oh * B + col;
-
-  for (int g = 0; g < a.out_share; ++g) {
-    const int head = oh * a.out_share + g;
-    const float log2a = linear::log2_decay(a.s, head);
-    const IO* z = head_rows<IO>(a.z, head);
-    const IO* x = head_rows<IO>(a.x, head);
-    const IO* y = head_rows<IO>(a.y, head);
-    const float* st = a.states + (slot * a.s.hv + head) * A * B;
-    const float enter = a.reverse ? 1.f : linear::power(log2a, 1);
-    for (int i = threadIdx.x; i < A * B; i += kThreads) {
-      // (the faster index along the stored rows)
-      const int r = a.transposed ? i % A : i / B, c = a.transposed ? i / A : i % B;
-      S[r * B + c] = (a.transposed ? st[c * A + r] : st[i]) * enter;
-    }
-    if (threadIdx.x <= C) power[threadIdx.x] = linear::power(log2a, threadIdx.x);
-    for (int ci = 0; ci < chunks; ++ci) {
-      const int64_t t = t0 + (int64_t)(a.reverse ? chunks - 1 - ci : ci) * C;
-      const int m = (int)(t1 - t < C ? t1 - t : C);
-      stage<C, A, IO, false>(zs, A + 4, z, a.z.ts, t, m, 0.f, 0, 0);
-      stage<C, A, IO, false>(xs, A + 4, x, a.x.ts, t, m, 0.f, 0, 0);
-      stage<C, B, IO, false>(ys, B, y, a.y.ts, t, m, 0.f, 0, 0);
-      __syncthreads();
-      {  // P[i][j] = a^{|i - j|} z_i . x_j where j is at or before i; a warp has eight rows
-        float p[8][2] = {};
+  const int64_t ots = (int64_t)a.s.hv * B;
+  IO* out = static_cast<IO*>(a.out) + (int64_t)head * B + col;
+  float* apart = a.out_share > 1 ? a.partial + (int64_t)head * B + col : nullptr;
+  const float log2a = linear::log2_decay(a.s, head);
+  const IO* z = head_rows<IO>(a.z, head);
+  const IO* x = head_rows<IO>(a.x, head);
+  const IO* y = head_rows<IO>(a.y, head);
+  const float* st = a.states + (slot * a.s.hv + head) * A * B;
+  const float enter = a.reverse ? 1.f : linear::power(log2a, 1);
+  for (int i = threadIdx.x; i < A * B; i += kThreads) {
+    // (the faster index along the stored rows)
+    const int r = a.transposed ? i % A : i / B, c = a.transposed ? i / A : i % B;
+    S[r * B + c] = (a.transposed ? st[c * A + r] : st[i]) * enter;
+  }
+  if (threadIdx.x <= C) power[threadIdx.x] = linear::power(log2a, threadIdx.x);
+  for (int ci = 0; ci < chunks; ++ci) {
+    const int64_t t = t0 + (int64_t)(a.reverse ? chunks - 1 - ci : ci) * C;
+    const int m = (int)(t1 - t < C ? t1 - t : C);
+    stage<C, A, IO, false>(zs, A + 4, z, a.z.ts, t, m, 0.f, 0, 0);
+    stage<C, A, IO, false>(xs, A + 4, x, a.x.ts, t, m, 0.f, 0, 0);
+    stage<C, B, IO, false>(ys, B, y, a.y.ts, t, m, 0.f, 0, 0);
+    __syncthreads();
+    {  // P[i][j] = a^{|i - j|} z_i . x_j where j is at or before i; a warp has eight rows
+      float p[8][2] = {};
 #pragma unroll 2
-        for (int k = 0; k < A; k += 4) {
-          float4 w[2];
+      for (int k = 0; k < A; k += 4) {
+        float4 w[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          w[j] = *reinterpret_cast<const float4*>(xs + (lane + 32 * j) * (A + 4) + k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 u = *reinterpret_cast<const float4*>(zs + (8 * warp + i) * (A + 4) + k);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            w[j] = *reinterpret_cast<const float4*>(xs + (lane + 32 * j) * (A + 4) + k);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 u = *reinterpret_cast<const float4*>(zs + (8 * warp + i) * (A + 4) + k);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-              p[i][j] = fmaf(u.x, w[j].x, fmaf(u.y, w[j].y, fmaf(u.z, w[j].z, fmaf(u.w, w[j].w, p[i][j]))));
-          }
+            p[i][j] = fmaf(u.x, w[j].x, fmaf(u.y, w[j].y, fmaf(u.z, w[j].z, fmaf(u.w, w[j].w, p[i][j]))));
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int r = 8 * warp + i, c = lane + 32 * j, gap = a.reverse ? c - r : r - c;
-            P[r * (C + 4) + c] = gap >= 0 && c < m ? p[i][j] * power[gap] : 0.f;
-          }
       }
-      __syncthreads();
-      float o[MO][4] = {};
-      auto times = [&](const float* u, int stride, const float* w, int steps) {  // o += rows of u by w
-#pragma unroll 2
-        for (int k = 0; k < steps; k += 4) {
-          float4 v[4];
 #pragma unroll
-          for (int l = 0; l < 4; ++l) v[l] = *reinterpret_cast<const float4*>(w + (k + l) * B + col);
+      for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int i = 0; i < MO; ++i) {
-            const float4 f = *reinterpret_cast<const float4*>(u + (rg * MO + i) * stride + k);
-            const float e[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int l = 0; l < 4; ++l) {
-              o[i][0] = fmaf(e[l], v[l].x, o[i][0]);
-              o[i][1] = fmaf(e[l], v[l].y, o[i][1]);
-              o[i][2] = fmaf(e[l], v[l].z, o[i][2]);
-              o[i][3] = fmaf(e[l], v[l].w, o[i][3]);
-            }
-          }
+        for (int j = 0; j < 2; ++j) {
+          const int r = 8 * warp + i, c = lane + 32 * j, gap = a.reverse ? c - r : r - c;
+          P[r * (C + 4) + c] = gap >= 0 && c < m ? p[i][j] * power[gap] : 0.f;
         }
-      };
-      times(zs, A + 4, S, A);
-#pragma unroll
-      for (int i = 0; i < MO; ++i) {
-        const int r = rg * MO + i;
-        const float w = power[a.reverse ? (r < m ? m - 1 - r : 0) : r];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] *= w;
-      }
-      times(P, C + 4, ys, C);
-#pragma unroll
-      for (int i = 0; i < MO; ++i) {
-        const int r = rg * MO + i;
-        if (r >= m) continue;
-        const int64_t row = (t + r) * ots;
-        if (g > 0) {
-          const float4 before = *reinterpret_cast<const float4*>(sum + row);
-          o[i][0] += before.x; o[i][1] += before.y; o[i][2] += before.z; o[i][3] += before.w;
-        }
-        if (g + 1 < a.out_share)
-          put4(sum + row, o[i]);
-        else
-          put4(out + row, o[i]);
-      }
-      __syncthreads();
-      if (ci + 1 < chunks) {  // S <- a^m S + sum_j a^{steps to the chunk's end} x_j y_j^T
-        const float w = power[m];
-        float* const mine = S + rg * MS * B + col;
-        float acc[MS][4];
-#pragma unroll
-        for (int i = 0; i < MS; ++i) {
-          const float4 v = *reinterpret_cast<const float4*>(mine + i * B);
-          acc[i][0] = w * v.x; acc[i][1] = w * v.y; acc[i][2] = w * v.z; acc[i][3] = w * v.w;
-        }
-#pragma unroll 2
-        for (int k = 0; k < m; ++k) {
-          const float wk = power[a.reverse ? k + 1 : m - k];
-          float4 v = *reinterpret_cast<const float4*>(ys + k * B + col);
-          v.x *= wk; v.y *= wk; v.z *= wk; v.w *= wk;
-#pragma unroll
-          for (int i = 0; i < MS; i += 4) {
-            const float4 f = *reinterpret_cast<const float4*>(xs + k * (A + 4) + rg * MS + i);
-            const float e[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-            for (int l = 0; l < 4; ++l) {
-              acc[i + l][0] = fmaf(e[l], v.x, acc[i + l][0]);
-              acc[i + l][1] = fmaf(e[l], v.y, acc[i + l][1]);
-              acc[i + l][2] = fmaf(e[l], v.z, acc[i + l][2]);
-              acc[i + l][3] = fmaf(e[l], v.w, acc[i + l][3]);
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < MS; ++i) put4(mine + i * B, acc[i]);
-        __syncthreads();
-      }
     }
     __syncthreads();
+    float o[MO][4] = {};
+    auto times = [&](const float* u, int stride, const float* w, int steps) {  // o += rows of u by w
+#pragma unroll 2
+      for (int k = 0; k < steps; k += 4) {
+        float4 v[4];
+#pragma unroll
+        for (int l = 0; l < 4; ++l) v[l] = *reinterpret_cast<const float4*>(w + (k + l) * B + col);
+#pragma unroll
+        for (int i = 0; i < MO; ++i) {
+          const float4 f = *reinterpret_cast<const float4*>(u + (rg * MO + i) * stride + k);
+          const float e[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int l = 0; l < 4; ++l) {
+            o[i][0] = fmaf(e[l], v[l].x, o[i][0]);
+            o[i][1] = fmaf(e[l], v[l].y, o[i][1]);
+            o[i][2] = fmaf(e[l], v[l].z, o[i][2]);
+            o[i][3] = fmaf(e[l], v[l].w, o[i][3]);
+          }
+        }
+      }
+    };
+    times(zs, A + 4, S, A);
+#pragma unroll
+    for (int i = 0; i < MO; ++i) {
+      const int r = rg * MO + i;
+      const float w = power[a.reverse ? (r < m ? m - 1 - r : 0) : r];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] *= w;
+    }
+    times(P, C + 4, ys, C);
+#pragma unroll
+    for (int i = 0; i < MO; ++i) {
+      const int r = rg * MO + i;
+      if (r >= m) continue;
+      const int64_t row = (t + r) * ots;
+      if (apart)
+        put4(apart + row, o[i]);
+      else
+        put4(out + row, o[i]);
+    }
+    __syncthreads();
+    if (ci + 1 < chunks) {  // S <- a^m S + sum_j a^{steps to the chunk's end} x_j y_j^T
+      const float w = power[m];
+      float* const mine = S + rg * MS * B + col;
+      float acc[MS][4];
+#pragma unroll
+      for (int i = 0; i < MS; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(mine + i * B);
+        acc[i][0] = w * v.x; acc[i][1] = w * v.y; acc[i][2] = w * v.z; acc[i][3] = w * v.w;
+      }
+#pragma unroll 2
+      for (int k = 0; k < m; ++k) {
+        const float wk = power[a.reverse ? k + 1 : m - k];
+        float4 v = *reinterpret_cast<const float4*>(ys + k * B + col);
+        v.x *= wk; v.y *= wk; v.z *= wk; v.w *= wk;
+#pragma unroll
+        for (int i = 0; i < MS; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(xs + k * (A + 4) + rg * MS + i);
+          const float e[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+          for (int l = 0; l < 4; ++l) {
+            acc[i + l][0] = fmaf(e[l], v.x, acc[i + l][0]);
+            acc[i + l][1] = fmaf(e[l], v.y, acc[i + l][1]);
+            acc[i + l][2] = fmaf(e[l], v.z, acc[i + l][2]);
+            acc[i + l][3] = fmaf(e[l], v.w, acc[i + l][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < MS; ++i) put4(mine + i * B, acc[i]);
+      __syncthreads();
+    }
   }
+}
+
+// out [T, heads, B] = the sum of the share's fp32 rows, in the heads' order; four elements a thread.  Rows
+// behind the last sequence are left as they are.
+template <typename IO>
+__global__ void __launch_bounds__(kThreads) linear_sum_kernel(LinearPass a) {
+  stream_order();
+  if (!linear::usable(a.s)) return;
+  const int64_t rows = (a.s.cu ? a.s.cu[a.s.N] : a.s.T) * (a.s.hv / a.out_share);
+  const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x, row = at / (a.B / 4);
+  const int c = (int)(at - row * (a.B / 4)) * 4;
+  if (row >= rows) return;
+  float f[4] = {};
+  for (int g = 0; g < a.out_share; ++g) {
+    const float4 v = *reinterpret_cast<const float4*>(a.partial + (row * a.out_share + g) * a.B + c);
+    f[0] += v.x; f[1] += v.y; f[2] += v.z; f[3] += v.w;
+  }
+  put4(static_cast<IO*>(a.out) + row * a.B + c, f);
 }
 
 template <int K, int V>
@@ -320,8 +333,13 @@ template <int A, int B, typename IO> cudaError_t launch_pass(const LinearPass& a
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(linear_pass_kernel<A, B, IO>, pass_smem<A, B>(), done);
   if (e != cudaSuccess) return e;
-  const dim3 grid((unsigned)a.s.slots, (unsigned)(a.s.hv / a.out_share));
-  return launch_ordered(linear_pass_kernel<A, B, IO>, grid, kThreads, pass_smem<A, B>(), s, a);
+  const dim3 grid((unsigned)a.s.slots, (unsigned)a.s.hv);
+  const cudaError_t done_pass =
+      launch_ordered(linear_pass_kernel<A, B, IO>, grid, kThreads, pass_smem<A, B>(), s, a);
+  if (done_pass != cudaSuccess || a.out_share == 1) return done_pass;
+  const int64_t threads = a.s.T * (a.s.hv / a.out_share) * (B / 4);
+  return launch_ordered(linear_sum_kernel<IO>, dim3((unsigned)((threads + kThreads - 1) / kThreads)),
+                        kThreads, 0, s, a);
 }
 template <typename IO> cudaError_t launch_pass_of(const LinearPass& a, cudaStream_t s) {
   if (a.A == 128) return a.B == 128 ? launch_pass<128, 128, IO>(a, s) : launch_pass<128, 64, IO>(a, s);
