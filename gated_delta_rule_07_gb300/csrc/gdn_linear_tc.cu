@@ -1058,6 +1058,16 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
 cudaError_t rows_map(CUtensorMap* m, const LinearRows& r, int64_t T, int heads, int width, int tokens) {
   EncodeTiled fn = encode_fn();
   if (!fn) return cudaErrorNotSupported;
+  // (The driver's call wants a context on the thread, which a thread's first runtime call alone may not have
+  // made: an autograd engine's thread comes here with none.)
+  thread_local int bound = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev != bound) {
+    e = cudaSetDevice(dev);
+    if (e == cudaSuccess) bound = dev;
+  }
+  if (e != cudaSuccess) return e;
   const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)T};
   // (the stride of a dimension of one row means nothing, but has to be one)
   const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? r.hs * 2 : width * 2),
