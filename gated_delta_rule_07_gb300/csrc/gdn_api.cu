@@ -825,8 +825,8 @@ gdn_status check_linear(const gdn_linear_problem* p) {
   if ((p->k_dim != 64 && p->k_dim != 128) || (p->v_dim != 64 && p->v_dim != 128))
     return GDN_ERR_UNSUPPORTED;
   if (p->hv > 65535) return GDN_ERR_UNSUPPORTED;  // grid.y
-  // segments are grid.x, of at least 64 tokens each but the last of a sequence
-  if (p->total_tokens / 64 + p->num_seqs > (int64_t)INT32_MAX) return GDN_ERR_UNSUPPORTED;
+  // segments (times heads) are grid.x, of at least 64 tokens each but the last of a sequence
+  if ((p->total_tokens / 64 + p->num_seqs) * p->hv > (int64_t)INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (!strides_ok(p->q_token_stride, p->total_tokens, p->q_head_stride, p->hk, p->io_dtype) ||
       !strides_ok(p->k_token_stride, p->total_tokens, p->k_head_stride, p->hk, p->io_dtype) ||
       !strides_ok(p->v_token_stride, p->total_tokens, p->v_head_stride, p->hv, p->io_dtype))
@@ -904,7 +904,13 @@ size_t linear_tops_at(const gdn::LinearShape& s) {
   return align_up((size_t)s.slots * s.hv * s.K * s.V * sizeof(float));
 }
 size_t linear_states_bytes(const gdn::LinearShape& s) {
-  return linear_tops_at(s) + align_up((size_t)s.slots * s.hv * 2 * sizeof(int));
+  return linear_tops_at(s) + align_up((size_t)s.slots * s.hv * 2 * sizeof(int)) + kAlign;
+}
+// (and the word of a call that looks its table over once)
+cudaError_t linear_look(gdn::LinearShape& s, void* states, cudaStream_t stream) {
+  if (s.N <= gdn::kLinearLooked) return cudaSuccess;
+  s.refused = reinterpret_cast<int32_t*>(static_cast<char*>(states) + linear_states_bytes(s) - kAlign);
+  return gdn::linear_check(s, stream);
 }
 int* linear_tops(const gdn::LinearShape& s, float* states) {
   return reinterpret_cast<int*>(reinterpret_cast<char*>(states) + linear_tops_at(s));
@@ -985,10 +991,11 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(h0) ||
       !aligned16(h_final))
     return GDN_ERR_INVALID_ARGUMENT;
-  const gdn::LinearShape s = linear_shape(p, false, log_decay, cu_seqlens, dev_status);
+  gdn::LinearShape s = linear_shape(p, false, log_decay, cu_seqlens, dev_status);
   if (!workspace || !aligned16(workspace) || ws_bytes < linear_states_bytes(s))
     return GDN_ERR_WORKSPACE;
   float* states = static_cast<float*>(workspace);
+  GDN_TRY(linear_look(s, states, stream));
   const int64_t T = s.T;
   const gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
                         kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
@@ -1029,7 +1036,7 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
     return GDN_ERR_INVALID_ARGUMENT;
   const gdn_linear_problem opened = linear_opened(p);
   if (saved) p = &opened;
-  const gdn::LinearShape s = linear_shape(p, true, log_decay, cu_seqlens, dev_status);
+  gdn::LinearShape s = linear_shape(p, true, log_decay, cu_seqlens, dev_status);
   const LinearBwdLayout L = linear_bwd_layout(s, linear_on_tc(p), saved != nullptr);
   if (!workspace || !aligned16(workspace) || ws_bytes < L.total) return GDN_ERR_WORKSPACE;
   char* ws = static_cast<char*>(workspace);
@@ -1054,6 +1061,7 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
     if (cs != GDN_OK) return cs;
     GDN_TRY(gdn::checkpoint_open(ca, stream));
   }
+  GDN_TRY(linear_look(s, h, stream));
   const gdn::LinearRows qr = linear_rows(q, p->q_token_stride, p->q_head_stride, T, s.hk, s.hv),
                         kr = linear_rows(k, p->k_token_stride, p->k_head_stride, T, s.hk, s.hv),
                         vr = linear_rows(v, p->v_token_stride, p->v_head_stride, T, s.hv, s.hv);

@@ -11,6 +11,7 @@ namespace linear {
 // Whether the call's table and decays can be used, decided alike by every block of every kernel of a
 // call (so that outputs are written whole or not at all).  Contains a block barrier.
 __device__ __forceinline__ bool usable(const LinearShape& s) {
+  if (s.refused != nullptr) return *s.refused == 0;
   bool bad = false;
   if (s.cu != nullptr) {
     for (int i = threadIdx.x; i < s.N; i += blockDim.x) {

@@ -46,6 +46,14 @@ __device__ __forceinline__ void stage(float* dst, int stride, const IO* src, int
   }
 }
 
+__global__ void __launch_bounds__(1024) linear_check_kernel(LinearShape s) {
+  stream_order();
+  int32_t* const word = s.refused;
+  s.refused = nullptr;
+  const bool fine = linear::usable(s);
+  if (threadIdx.x == 0) *word = fine ? 0 : 1;
+}
+
 // ------------------------------------------------------------------ a segment's own state
 
 // One block a (slot, value head): the K x V sums in registers, 32 tokens staged at a time.  (Half of K a
@@ -347,6 +355,10 @@ template <typename IO> cudaError_t launch_pass_of(const LinearPass& a, cudaStrea
 }
 
 }  // namespace
+
+cudaError_t linear_check(const LinearShape& a, cudaStream_t s) {
+  return launch_ordered(linear_check_kernel, dim3(1), 1024, 0, s, a);
+}
 
 cudaError_t linear_state_simt(const LinearState& a, cudaStream_t s) {
   if (a.s.K == 128) return a.s.V == 128 ? launch_state<128, 128>(a, s) : launch_state<128, 64>(a, s);

@@ -246,6 +246,24 @@ def test_bad_tables_and_decays_write_nothing(gdn, bad, io):
         c.forward(gdn)
 
 
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_many_sequences(gdn, io):
+    """More than the blocks look at themselves; and a bad table among so many."""
+    gen = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 5, (700,), generator=gen).tolist()
+    lens[350] = 300
+    c = Case(lens, 1, 2, 64, 64, io, seed=4)
+    c.check_forward(c.forward(gdn))
+    c.check_backward(c.backward(gdn))
+    c.cu[600] = c.cu[-1] + 1
+    p, st = _problem(gdn, c, 700), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, last = torch.full_like(c.v, 7.0), torch.full_like(c.h0, 7.0)
+    ws = torch.full((gdn.gdn_linear_attention_workspace_size(p),), 255, dtype=torch.uint8, device="cuda")
+    gdn.gdn_linear_attention(p, c.q, c.k, c.v, c.g, c.h0, c.cu, out, last, ws, dev_status=st)
+    assert gdn.gdn_device_status(st) == 6
+    assert (out == 7).all() and (last == 7).all()
+
+
 def test_no_tokens(gdn):
     for io in (BF16, F32):
         c = Case([0, 0], 1, 2, 128, 64, io, seed=1)
