@@ -3,7 +3,9 @@
 //     h <- a h + k v^T,     o = h^T q.
 //
 // The step reads and writes each K x V fp32 state once (128 KiB a row and head at K = V = 128) and does
-// four operations an element: it is bound by HBM.  One block of 256 threads a (row, value head): a
+// four operations an element: it is bound by HBM.  (256 requests of 32 heads of 128, 1.08 GB:
+// 159.5 us, the measured copy's rate; five fp32 requests of 6 heads: 2.7 us.)  One block of 256 threads
+// a (row, value head): a
 // thread holds K V / 1024 rows of four columns, so that a warp's accesses are whole 512- or 256-byte
 // runs; the new state is stored before the sums of o are joined, which only need it in registers.
 #include <cuda_bf16.h>

@@ -103,8 +103,8 @@ __device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
 // HBM takes 1340 cycles for a tile of an SM's share, so little may go through shared memory beside the
 // tiles themselves (256 of its cycles): y comes out of it transposed (ldmatrix) and the parts go straight to
 // Tensor Memory, as the operand whose rows are y's columns; the tensor core reads x alone from shared memory.
-// So it makes U^T.  (Parts written back to shared memory: 270 us for 65536 tokens of 32 heads, whatever the
-// number of warps.)  Five tiles are on their way or at work; splitting (sixteen warps), the products and the
+// So it makes U^T.  (65536 tokens of 32 heads: 188 us, of HBM's 119, with 69% of the issue slots used, by
+// the splitting above all; with parts written back to shared memory 270, whatever the number of warps.)  Five tiles are on their way or at work; splitting (sixteen warps), the products and the
 // sums (eight warps, for Tensor Memory's lanes and their registers) each on another.  896 threads launch
 // with 72 registers, 504 for the seven warpgroups' warps of an SM's quarter: the sums' two take 96,
 // splitting's four keep 64, the last 56.
@@ -409,11 +409,11 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
 // so that nothing can overflow that does not in fp32, and each rounding is half a step of fp16 (2^-11) of
 // a term, or 2^-38 of what bounds the sum.
 //
-// What bounds it is shared memory: a chunk's tiles go through it to the tensor cores (768 cycles of its
-// 128 bytes a cycle to arrive, 1536 as operands), twice more for x and y, whose rows change type there, and
-// S's copy and the outputs make it about 4900 of the 4300 that HBM takes for a chunk.  So z's rows go to
-// the tensor core through Tensor Memory, the outputs leave by TMA from z's tile, and a sum over value heads
-// is kept in an order of rows that its threads read together.
+// What bounds it is shared memory and the hand-offs between its roles: a chunk takes 6300 cycles (65536
+// tokens of 32 heads: 360 to 373 us), where HBM takes 4300 (238 us).  Its threads read and write shared
+// memory in 3250 of them, its tiles arrive in 768 (128 bytes a cycle) and go to the tensor cores in 1536.
+// So z's rows go to the tensor core through Tensor Memory, the outputs leave by TMA from y's tile, and a
+// sum over value heads is kept in an order of rows that its threads read together.
 constexpr int C = 128;
 constexpr uint32_t kTileBytes = C * D * 2, kBlock = kTileBytes / 2;  // (a block: 64 columns)
 constexpr int kWeightWarps = 4, kStateWarps = 8, kOpenWarps = 4;
@@ -511,7 +511,7 @@ __device__ __forceinline__ void tma_out(const CUtensorMap* map, uint32_t src, in
 }
 
 // REVERSE: the walk goes backward in time.  SUM: an output head has several value heads.
-// WIDE: A = B = 128 (9% faster where that is known: 65536 tokens 554 us, 604).
+// WIDE: A = B = 128 (9% faster where that is known: a call of 65536 tokens 554 us, 604).
 template <bool REVERSE, bool SUM, bool WIDE>
 __global__ void __launch_bounds__(kPassThreads, 1)
 linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz,
