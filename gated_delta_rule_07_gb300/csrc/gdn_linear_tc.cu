@@ -84,6 +84,8 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
                                    __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// such magnitudes, or zeros where one is infinite
+__device__ __forceinline__ uint32_t finite(uint32_t m) { return (m + 0x00800080u) & 0x80008000u ? 0u : m; }
 // e with |v| < 2^e for these magnitudes; of zeros the least
 __device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
   const uint32_t m = max(packed_max & 0x7fffu, packed_max >> 16 & 0x7fffu);
@@ -103,7 +105,7 @@ __device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
 // HBM takes 1340 cycles for a tile of an SM's share, so little may go through shared memory beside the
 // tiles themselves (256 of its cycles): y comes out of it transposed (ldmatrix) and the parts go straight to
 // Tensor Memory, as the operand whose rows are y's columns; the tensor core reads x alone from shared memory.
-// So it makes U^T.  (65536 tokens of 32 heads: 188 us, of HBM's 119, with 69% of the issue slots used, by
+// So it makes U^T.  (65536 tokens of 32 heads: 192 us, of HBM's 119, with 69% of the issue slots used, by
 // the splitting above all; with parts written back to shared memory 270, whatever the number of warps.)  Five tiles are on their way or at work; splitting (sixteen warps), the products and the
 // sums (eight warps, for Tensor Memory's lanes and their registers) each on another.  896 threads launch
 // with 72 registers, 504 for the seven warpgroups' warps of an SM's quarter: the sums' two take 96,
@@ -341,6 +343,33 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
         st = 0;
         ++round;
       }
+    }
+    // An infinity does not reach the outputs of the chunks before its own, so it is not to scale their rows:
+    // a warp that has met one looks at its rows once more, without it.  (Left out tile by tile: 196 us
+    // for 65536 tokens of 32 heads, not 192.)
+    if (__any_sync(0xffffffffu, finite(x_max) != x_max || finite(y_max) != y_max)) {
+      const __nv_bfloat16* const xp = static_cast<const __nv_bfloat16*>(a.x.p) +
+                                      (int64_t)(head / a.x.share) * a.x.hs + 8 * (tid % 8);
+      const __nv_bfloat16* const yp = static_cast<const __nv_bfloat16*>(a.y.p) +
+                                      (int64_t)(head / a.y.share) * a.y.hs + 32 * quarter + 16 * (lane & 1);
+      auto look = [](uint32_t most, const __nv_bfloat16* p) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int j = 0; j < 4; ++j) most = larger(most, finite(larger(0u, w[j])));
+        return most;
+      };
+      x_max = y_max = 0;
+#pragma unroll 1
+      for (int i = 0; i < tiles; ++i) {
+        const int64_t t = first_token(i);
+        const int m = tokens(i), other = token0 + lane / 2;
+#pragma unroll 1
+        for (int b = 0; b < K && r < m; b += 64) x_max = look(x_max, xp + (t + r) * a.x.ts + b);
+#pragma unroll 1
+        for (int c = 0; c < 16 && other < m && 32 * quarter < V; c += 8)
+          y_max = look(y_max, yp + (t + other) * a.y.ts + c);
+      }
+      __syncwarp();
     }
     const int e_x = __reduce_max_sync(0xffffffffu, exponent_of(x_max, -126));
     const int e_y = __reduce_max_sync(0xffffffffu, exponent_of(y_max, -126));

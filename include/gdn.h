@@ -389,7 +389,8 @@ size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p);
  * Precision: states are carried and h_final is formed to fp32 accuracy.  fp32 I/O is fp32 arithmetic.  bf16
  * I/O runs on the tensor cores: q . k of the inputs as they are; the weighted products, the weighted rows
  * of q and k and the state enter the other products as fp16 (scaled by powers of two, so that no size of
- * the inputs is out of range; 2^-11 of a term each), all sums are fp32. */
+ * the inputs is out of range; 2^-11 of a term each, or 2^-38 of what the largest k and v of its
+ * sequence would make a term), all sums are fp32. */
 gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, const void* k,
                                 const void* v, const float* log_decay, const float* h0,
                                 const int32_t* cu_seqlens, void* out, float* h_final,
@@ -415,7 +416,8 @@ size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p,
  *               fp32 and in a fixed order),  dv [T, hv, V] io dtype, contiguous
  *   dh0         [N, hv, K, V] fp32, or NULL to skip; may be dh_final itself
  * The decays are constants of the layer: they get no gradient.  Checks, unwritten rows, workspace,
- * precision and errors as in the forward; dh0 is formed to fp32 accuracy. */
+ * precision and errors as in the forward; dh0 is formed to fp32 accuracy.  A value of a sequence that is
+ * not finite makes that sequence's gradients undefined (in the heads that read it), and no other's. */
 gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void* q,
                                          const void* k, const void* v,
                                          const gdn_linear_saved* saved, const float* log_decay,

@@ -201,6 +201,22 @@ def test_a_neighbours_infinities_stay_its_own(gdn, io):
             lt.assert_close(x, want[i], size[i], lt.inner_error(50, c.cores and i < 3), str(i))
 
 
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("which,bad", [("k", INF), ("v", -INF), ("v", float("nan")), ("q", INF)])
+def test_what_is_not_finite_stays_behind(gdn, io, which, bad):
+    """A value that is not finite leaves the outputs alone that lie 128 tokens before it or more.  (As many
+    heads as SMs, so that a segment has several chunks.)"""
+    c = Case([1000], 1, 152, 128, 128, io, seed=13)
+    x = getattr(c, which)
+    x[700, -1, 5] = bad
+    out, _ = c.forward(gdn)
+    cut = 700 - 127
+    args = (c.q[:cut], c.k[:cut], c.v[:cut], c.g, c.h0, [cut])
+    want, size = lt.forward(*args), lt.magnitudes(lt.forward, *args)
+    lt.assert_close(out[:cut], want[0], size[0], lt.inner_error(cut, c.cores), "out")
+    assert not torch.isfinite(out[700, -1]).all()
+
+
 @pytest.mark.parametrize("io,K,V", [(BF16, 128, 128), (F32, 64, 128)])
 def test_pieces_continue(gdn, io, K, V):
     """A sequence in one call, and in pieces that carry its state (which may be updated in place)."""
