@@ -775,7 +775,9 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         wait_bar(bar(kScores, it), half(it), failed);
         fence_after_sync();
         const int ez = a.z_top ? ez_all : targets[C * (it & 1) + row];
-        const float mine = two_to(15 - ez - E - h);
+        // (where z, x and y together pass fp32's range, what would be lost is made NaN)
+        const int top = 15 - ez - E - h;
+        const float mine = top < -126 ? __int_as_float(0x7fffffff) : two_to(top);
         const uint32_t p_at = tm + lanes + 128 * (it & 1);
 #pragma unroll 1
         for (int k0 = 0; k0 < C; k0 += 32) {

@@ -390,7 +390,8 @@ size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p);
  * I/O runs on the tensor cores: q . k of the inputs as they are; the weighted products, the weighted rows
  * of q and k and the state enter the other products as fp16 (scaled by powers of two, so that no size of
  * the inputs is out of range; 2^-11 of a term each, or 2^-38 of what the largest k and v of its
- * sequence would make a term), all sums are fp32. */
+ * sequence would make a term; rows of q whose product with these passes fp32's range may be NaN), all
+ * sums are fp32. */
 gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, const void* k,
                                 const void* v, const float* log_decay, const float* h0,
                                 const int32_t* cu_seqlens, void* out, float* h_final,

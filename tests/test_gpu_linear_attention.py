@@ -217,6 +217,18 @@ def test_what_is_not_finite_stays_behind(gdn, io, which, bad):
     assert not torch.isfinite(out[700, -1]).all()
 
 
+@pytest.mark.parametrize("io", [BF16, F32])
+def test_what_passes_the_range_is_not_finite(gdn, io):
+    """Products beyond fp32's range are not lost without a sign of it (each output here is 2^150 or more)."""
+    q, v = torch.full((300, 1, 128), 2.0 ** 50, dtype=io, device="cuda"), None
+    v = q.repeat(1, 2, 1)
+    g = torch.tensor([0.0, -0.1], device="cuda")
+    out, _ = gdn.linear_attention(q, q, v, g, check_status=True)
+    assert not torch.isfinite(out).any()
+    for x in gdn.linear_attention_backward(q, q, v, g, v, check_status=True)[:3]:
+        assert not torch.isfinite(x).any()
+
+
 @pytest.mark.parametrize("io,K,V", [(BF16, 128, 128), (F32, 64, 128)])
 def test_pieces_continue(gdn, io, K, V):
     """A sequence in one call, and in pieces that carry its state (which may be updated in place)."""
