@@ -45,6 +45,20 @@ def test_codes_and_values(gdn, T, H, D, dtype, io):
             back.double().abs() * lt.HALF_STEP[io] + 2.0 ** -22 * x.double().abs()).all()
 
 
+def test_offsets_past_32_bits(gdn):
+    """More than 2^31 elements, in a slice of rows as long again: the last rows."""
+    x = torch.empty(530000, 2, 32, 128, dtype=BF16, device="cuda")[:, 1]
+    assert x.numel() > 2 ** 31
+    x[-100:].normal_()
+    x[:-100] = 1.0
+    held, = gdn.checkpoint_pack(x, check_status=True)
+    codes, scale = lt.checkpoint(x[-100:], torch.int8)
+    assert torch.equal(held.scale[-100:], scale) and torch.equal(held.codes[-100:].double(), codes)
+    assert torch.equal(held.scale[:-100], torch.full_like(held.scale[:-100], 1 / torch.tensor(127.)))
+    back, = gdn.checkpoint_open(held)
+    assert torch.equal(back[-100:], (codes.float() * scale[..., None]).to(BF16))
+
+
 @pytest.mark.parametrize("dtype", FORMATS)
 def test_several_tensors_and_slices(gdn, dtype):
     gen = torch.Generator().manual_seed(1)

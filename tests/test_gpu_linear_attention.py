@@ -434,6 +434,30 @@ def test_offsets_past_32_bits(gdn):
     lt.assert_close(state[-1:], want[1], size[1], 4 * 2.0 ** -24)
 
 
+@pytest.mark.parametrize("io,T", [(BF16, 530000), (F32, 530000)])
+def test_rows_past_32_bits(gdn, io, T):
+    """Values and outputs of more than 2^31 elements: the last sequence's rows and gradients."""
+    hv, L = 32, 500
+    gen = torch.Generator("cuda").manual_seed(5)
+    rand = lambda *n: torch.randn(*n, device="cuda", generator=gen, dtype=io)  # noqa: E731
+    q, k, v, do = rand(T, 2, 128), rand(T, 2, 128), rand(T, hv, 128), rand(T, hv, 128)
+    assert v.numel() > 2 ** 31
+    g = decays(hv, torch.Generator().manual_seed(1))
+    cu = torch.tensor([0, T - L, T], dtype=torch.int32, device="cuda")
+    cut = [x[T - L:] for x in (q, k, v, do)]
+    out, last = gdn.linear_attention(q, k, v, g, None, cu, check_status=True)
+    args = (*cut[:3], g, None, [L])
+    want, size = lt.forward(*args), lt.magnitudes(lt.forward, *args)
+    lt.assert_close(out[T - L:], want[0], size[0], lt.inner_error(L, io is BF16), "out")
+    lt.assert_close(last[1:], want[1], size[1], lt.inner_error(L, False), "h_final")
+    del out
+    grads = gdn.linear_attention_backward(q, k, v, g, do, None, None, cu, check_status=True)
+    args = (*cut[:3], g, cut[3], None, None, [L])
+    want, size = lt.backward(*args), lt.magnitudes(lt.backward, *args)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        lt.assert_close(grads[i][T - L:], want[i], size[i], lt.inner_error(L, io is BF16), name)
+
+
 # ------------------------------------------------------------------------------- what is refused
 
 def test_refusals_of_gpu_tensors(gdn):
