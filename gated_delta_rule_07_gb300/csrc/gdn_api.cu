@@ -906,11 +906,14 @@ size_t linear_tops_at(const gdn::LinearShape& s) {
 size_t linear_states_bytes(const gdn::LinearShape& s) {
   return linear_tops_at(s) + align_up((size_t)s.slots * s.hv * 2 * sizeof(int)) + kAlign;
 }
-// (and the word of a call that looks its table over once)
+// (and a word for whether the table and the decays can be used: a kernel of its own looks at those of many
+// sequences, else the call's first kernels do)
 cudaError_t linear_look(gdn::LinearShape& s, void* states, cudaStream_t stream) {
-  if (s.N <= gdn::kLinearLooked) return cudaSuccess;
   s.refused = reinterpret_cast<int32_t*>(static_cast<char*>(states) + linear_states_bytes(s) - kAlign);
-  return gdn::linear_check(s, stream);
+  if (s.N <= gdn::kLinearLooked) return cudaSuccess;
+  const cudaError_t e = gdn::linear_check(s, stream);
+  s.looked = true;
+  return e;
 }
 int* linear_tops(const gdn::LinearShape& s, float* states) {
   return reinterpret_cast<int*>(reinterpret_cast<char*>(states) + linear_tops_at(s));
@@ -1003,6 +1006,7 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
   int* tops = linear_tops(s, states);  // of k, and of v
   if (T > 0) GDN_TRY(linear_state(p, {s, kr, vr, false, states, tops}, stream));
   const gdn::LinearScan scan = {s, false, states, h0, h_final};
+  s.looked = true;
   GDN_TRY(gdn::linear_scan(&scan, 1, stream));
   if (T > 0)
     GDN_TRY(linear_pass(p, {s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr, tops,
@@ -1072,6 +1076,7 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
     GDN_TRY(linear_state(p, {s, qr, gr, true, d, linear_tops(s, d)}, stream));
   }
   const gdn::LinearScan scans[2] = {{s, true, d, dh_final, dh0}, {s, false, h, h0, nullptr}};
+  s.looked = true;
   GDN_TRY(gdn::linear_scan(scans, T > 0 ? 2 : 1, stream));
   if (T > 0) {
     float* partial = reinterpret_cast<float*>(ws + L.partial);

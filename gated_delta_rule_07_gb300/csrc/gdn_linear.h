@@ -40,10 +40,11 @@ struct LinearShape {
   const float* log_decay;   // [hv]
   const int32_t* cu;        // [N + 1], or null: one sequence
   int32_t* status;
-  int32_t* refused;         // for many sequences: 1 where the call's table or decays cannot be used, else 0
+  int32_t* refused;         // 1 where the call's table or decays cannot be used, else 0
+  bool looked;              // a kernel ahead has written it
 };
-// Beyond so many sequences the table is looked at once, ahead of the call's kernels, and not by their
-// every block (10000 sequences of 32 heads: 320000 blocks, 40 KB each).
+// Beyond so many sequences the table is looked at once, ahead of the call's kernels, and not by the first
+// one's every block (10000 sequences of 32 heads: 320000 blocks, 40 KB each).
 constexpr int kLinearLooked = 512;
 cudaError_t linear_check(const LinearShape& a, cudaStream_t s);
 

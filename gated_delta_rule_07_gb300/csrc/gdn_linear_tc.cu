@@ -438,8 +438,8 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
 // so that nothing can overflow that does not in fp32, and each rounding is half a step of fp16 (2^-11) of
 // a term, or 2^-38 of what bounds the sum.
 //
-// What bounds it is shared memory and the hand-offs between its roles: a chunk takes 6300 cycles (65536
-// tokens of 32 heads: 360 to 373 us), where HBM takes 4300 (238 us).  Its threads read and write shared
+// What bounds it is shared memory and the hand-offs between its roles: a chunk takes 6000 cycles (65536
+// tokens of 32 heads: 349 us), where HBM takes 4300 (238 us).  Its threads read and write shared
 // memory in 3250 of them, its tiles arrive in 768 (128 bytes a cycle) and go to the tensor cores in 1536.
 // So z's rows go to the tensor core through Tensor Memory, the outputs leave by TMA from y's tile, and a
 // sum over value heads is kept in an order of rows that its threads read together.
@@ -548,7 +548,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
                       const __grid_constant__ CUtensorMap mo) {
   extern __shared__ uint8_t raw_smem[];
   stream_order();
-  if (!linear::usable(a.s)) return;
+  if (!linear::accepted(a.s)) return;
   const int share = SUM ? a.out_share : 1, heads = a.s.hv / share;
   const int A = WIDE ? D : a.A, B = WIDE ? D : a.B;
   const int oh = blockIdx.x % heads;
