@@ -862,7 +862,7 @@ bool linear_on_tc(const gdn_linear_problem* p) {
 // tensor cores' backward pass of shared heads, of all the value heads that it sums), so what counts is how many rounds of
 // the 152 SMs there are and how long one takes: its tokens and some more for its start and end, 640 on the
 // tensor cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
-// 613 us; 9, two rounds of 144, 555; 16, 674; 19, four rounds of 152, 564; 32, 634.)  Only the sum of the
+// 609 us; 9, two rounds of 144, 552; 16, 634; 19, four rounds of 152, 557; 32, 620.)  Only the sum of the
 // sequences' lengths is known here: they are taken as alike, give or take a seventh.
 int linear_segment(const gdn_linear_problem* p, bool backward) {
   const int64_t T = p->total_tokens, N = p->num_seqs, hv = p->hv;
