@@ -859,9 +859,9 @@ bool linear_on_tc(const gdn_linear_problem* p) {
 }
 
 // A segment's tokens, in whole chunks.  An SM holds one segment of one output head at a time (in the
-// tensor cores' backward pass of shared heads, of all the value heads that it sums), so what counts is how many rounds of
-// the 152 SMs there are and how long one takes: its tokens and some more for its start and end, 640 on the
-// tensor cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
+// tensor cores' backward pass of shared heads, of all the value heads that it sums), so what counts is how
+// many rounds of the 152 SMs there are and how long one takes: its tokens and some more for its start and
+// end, 640 on the tensor cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
 // 609 us; 9, two rounds of 144, 552; 16, 634; 19, four rounds of 152, 557; 32, 620.)  Only the sum of the
 // sequences' lengths is known here: they are taken as alike, give or take a seventh.
 int linear_segment(const gdn_linear_problem* p, bool backward) {

@@ -1,6 +1,6 @@
 // gdn_linear_simt.cu -- linear attention with a decay for each head (gdn_linear.h) in fp32 on the CUDA
-// cores, for fp32 I/O and the head sizes that the tensor-core kernels do not take; and the scan over a
-// sequence's segments, which both families use.
+// cores, for fp32 I/O and for bf16 rows that tensor maps cannot describe (broadcast ones); and the scan
+// over a sequence's segments, which both families use.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -173,7 +173,8 @@ __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const __grid_cons
 // 49152 multiply-adds a token at A = B = 128 make it the CUDA cores' to bound, if their operands come
 // cheaply: a thread has four neighbouring columns of several rows (of P, two columns of eight), so that a
 // warp reads the rows' operand as broadcasts and four steps of it at once.  (Threads of 4 x 4 and 64
-// columns a block: 571 us for four sequences of 2048 tokens, 16 heads of 128; so 407, where the segments fill fewer SMs.)
+// columns a block: 571 us for four sequences of 2048 tokens, 16 heads of 128; so 407, where the segments
+// fill fewer SMs.)
 template <int A, int B> constexpr int pass_smem() {
   return (2 * C * (A + 4) + C * B + A * B + C * (C + 4) + C + 4) * 4;
 }
