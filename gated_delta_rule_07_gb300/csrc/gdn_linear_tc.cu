@@ -452,7 +452,7 @@ constexpr int kFirstState = kWeightWarps, kFirstOpen = kFirstState + kStateWarps
 struct PassSmem {             // offsets from a 1024-byte boundary
   static constexpr uint32_t Z = 0, X = kTileBytes, Y = 2 * kTileBytes, stage = 3 * kTileBytes;
   static constexpr uint32_t S = 2 * stage, POWERS = S + kTileBytes, TARGETS = POWERS + (C + 32) * 4;
-  static constexpr uint32_t BARS = TARGETS + 2 * C * 4, MISC = BARS + 28 * 8;
+  static constexpr uint32_t BARS = TARGETS + 2 * C * 4, MISC = BARS + 30 * 8;
   static constexpr int bytes = MISC + 16 + 1024;
 };
 static_assert(PassSmem::bytes <= 232448, "shared memory of a block");
@@ -460,7 +460,7 @@ static_assert(PassSmem::bytes <= 232448, "shared memory of a block");
 // state's two take 136, the weights keep 88, opening and the last one 56 each: 472.
 // barriers: those of a pair alternate from chunk to chunk
 enum { kFull = 0, kScores = 2, kValues = 4, kWeights = 6, kFree = 10, kSumsRead = 12,
-       kTargets = 14, kOut = 16, kRows = 18, kFullY = 20, kStateIn = 22, kGrown, kTaken, kSums, kStart, kEnd };
+       kTargets = 14, kOut = 16, kRows = 18, kFullY = 20, kStateIn = 22, kGrown, kTaken, kSums, kStart, kBegun, kEnd };
 
 // Rows of a tile, a thread each.  (A row's logical 16-byte piece p lies at p ^ (row & 7) of its block, so
 // that neighbouring rows' threads meet different banks.)
@@ -586,6 +586,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
     mbar_init(one(kTaken), 32 * kStateWarps);
     mbar_init(one(kSums), 1);
     mbar_init(one(kStart), 32 * kStateWarps);
+    mbar_init(one(kBegun), 32 * kWeightWarps);
     mbar_init(one(kEnd), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -762,6 +763,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       powers[row] = linear::power(log2a, row) * two_to(ey + h);
       if (row < 32) powers[row - 32] = 0.f;
       named_bar(1, 32 * kWeightWarps);
+      mbar_arrive(one(kBegun));
       float2 step[8];  // those of |a 16-column piece's far end - column|
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -970,6 +972,9 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
           top = max(top, max(__float_as_uint(S[i].x) & 0x7fffffffu, __float_as_uint(S[i].y) & 0x7fffffffu));
         }
         top = __reduce_max_sync(0xffffffffu, top);
+        // (the weights have passed the last head's start, and cleared this one's max: with one chunk a
+        // head nothing else says so)
+        if (g > 0) wait_bar(one(kBegun), (g - 1) & 1, failed);
         if (lane == 0) atomicMax(misc + 2 + (g & 1), (int)top);
         mbar_arrive(one(kStart));
         wait_bar(one(kStart), g & 1, failed);

@@ -1,0 +1,46 @@
+"""GPU: linear attention where its tensor-core kernels hand over between heads and scale their operands:
+many short sequences of shared key heads, rows of very different sizes, values at the ends of bf16's
+range, and states that have to keep every bit."""
+import pytest
+import torch
+
+import linear_testutil as lt
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    from gated_delta_rule_07_gb300 import build
+    build.build()
+    from gated_delta_rule_07_gb300 import gdn as mod
+    assert torch.cuda.is_available()
+    return mod
+
+
+def rand(gen, *shape, io=BF16):
+    return torch.randn(*shape, generator=gen).to(io).cuda()
+
+
+@pytest.mark.parametrize("hk,hv", [(1, 4), (2, 6), (4, 8)])
+@pytest.mark.parametrize("K,V", [(128, 128), (64, 128)])
+def test_many_sequences_of_one_chunk_with_shared_key_heads(gdn, hk, hv, K, V):
+    """Every segment is one chunk, walked for a key head's value heads one after another; the states
+    that they start from differ by powers of two up to 2^20 from head to head."""
+    gen = torch.Generator().manual_seed(hv + K)
+    lens = torch.randint(0, 129, (120,), generator=gen).tolist()
+    lens[7], lens[8] = 128, 1
+    T, N, cu = sum(lens), len(lens), lt.cumulative(lens)
+    q, k, v, do = rand(gen, T, hk, K), rand(gen, T, hk, K), rand(gen, T, hv, V), rand(gen, T, hv, V)
+    g = -torch.rand(hv, generator=gen).cuda() * 0.2
+    sizes = torch.exp2(torch.randint(0, 21, (N, hv, 1, 1), generator=gen).float())
+    h0, dh = ((torch.randn(N, hv, K, V, generator=gen) * sizes).cuda() for _ in range(2))
+    first = gdn.linear_attention_backward(q, k, v, g, do, h0, dh, cu, check_status=True)
+    args = q, k, v, g, do, h0, dh, lens
+    want, size = lt.backward(*args), lt.magnitudes(lt.backward, *args)
+    for i, name in enumerate(("dq", "dk", "dv", "dh0")):
+        lt.assert_close(first[i], want[i], size[i], lt.inner_error(128, i < 3), name)
+    for _ in range(20):
+        again = gdn.linear_attention_backward(q, k, v, g, do, h0, dh, cu)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
