@@ -39,7 +39,8 @@ __device__ __forceinline__ void wait_bar(uint32_t bar, uint32_t parity, volatile
   wait_one(bar, parity, failed);
   __syncwarp();
 }
-// A warpgroup's registers a thread, from now on (of the block's, which the groups share).
+// A warpgroup's registers a thread, from now on (of the block's, which the groups share).  All warps of
+// a group are to come to the same one of these, so roles branch by warpgroups first.
 template <int N> __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
 }
@@ -111,6 +112,7 @@ __device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
 // with 72 registers, 504 for the seven warpgroups' warps of an SM's quarter: the sums' two take 96,
 // splitting's four keep 64, the last 56.
 constexpr int kTile = 64, kSplit = 512, kAdd = 256, kStateThreads = kSplit + kAdd + 128, kStages = 5;
+static_assert(kSplit % 128 == 0 && kAdd % 128 == 0, "roles that set registers are whole warpgroups");
 constexpr uint32_t kRaw = kTile * D * 2;          // bytes of a tile of one tensor
 struct StateSmem {                                // offsets from a 1024-byte boundary
   static constexpr uint32_t X = 0, Y = kRaw, stage = 2 * kRaw, BARS = kStages * stage;
@@ -184,72 +186,71 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
   const int64_t left = a.reverse ? t0 - (a.s.cu ? a.s.cu[n] : 0) : (a.s.cu ? a.s.cu[n + 1] : a.s.T) - t1;
   const bool three = log2a * (float)left > -13.f;
 
-  if (warp >= kMma + 1) {  // (the rest of the last warpgroup)
+  if (warp >= kLoad) {  // (the last warpgroup; the rest of its warps have nothing to do)
     leave_registers<56>();
-  } else if (warp == kLoad) {
-    leave_registers<56>();
-    if (tid % 32 == 0) {
-      int loaded = 0;
-      for (int i = 0, st = 0, round = 0; i < tiles; ++i) {
-        if (round) wait_one(free_ + 8 * st, (round - 1) & 1, failed);
+    if (warp == kLoad) {
+      if (tid % 32 == 0) {
+        int loaded = 0;
+        for (int i = 0, st = 0, round = 0; i < tiles; ++i) {
+          if (round) wait_one(free_ + 8 * st, (round - 1) & 1, failed);
+          if (*failed) break;
+          const uint32_t x = base + st * StateSmem::stage + StateSmem::X,
+                         y = base + st * StateSmem::stage + StateSmem::Y;
+          const int t = first_token(i);
+          mbar_expect_tx(full + 8 * st, (uint32_t)(K + V) * kTile * 2);
+#pragma unroll 1
+          for (int b = 0; b < K; b += 64)
+            tma_box(x + b * (kRaw / 128), &mx, b, head / a.x.share, t, full + 8 * st);
+#pragma unroll 1
+          for (int b = 0; b < V; b += 64)
+            tma_box(y + b * (kRaw / 128), &my, b, head / a.y.share, t, full + 8 * st);
+          loaded = i + 1;
+          if (++st == kStages) {
+            st = 0;
+            ++round;
+          }
+        }
+        if (*failed)
+          for (int i = loaded > kStages ? loaded - kStages : 0; i < loaded; ++i)
+            drain(full + 8 * (i % kStages), (i / kStages) & 1);
+      }
+      __syncwarp();
+    } else if (warp == kMma) {
+      // (lanes behind V hold nothing that is read)
+      const uint32_t id = idesc_f16(128, K, 0, 1, 1);
+      const uint64_t at = sdesc(base, kRaw / 2, 1024);
+#pragma unroll 1
+      for (int i = 0, st = 0; i < tiles; ++i) {
+        wait_bar(ready + 8 * (i & 1), half(i), failed);
+        if (i >= 2) wait_bar(taken + 8 * (i & 1), half(i - 2), failed);
         if (*failed) break;
-        const uint32_t x = base + st * StateSmem::stage + StateSmem::X,
-                       y = base + st * StateSmem::stage + StateSmem::Y;
-        const int t = first_token(i);
-        mbar_expect_tx(full + 8 * st, (uint32_t)(K + V) * kTile * 2);
-#pragma unroll 1
-        for (int b = 0; b < K; b += 64)
-          tma_box(x + b * (kRaw / 128), &mx, b, head / a.x.share, t, full + 8 * st);
-#pragma unroll 1
-        for (int b = 0; b < V; b += 64)
-          tma_box(y + b * (kRaw / 128), &my, b, head / a.y.share, t, full + 8 * st);
-        loaded = i + 1;
-        if (++st == kStages) {
-          st = 0;
-          ++round;
+        fence_after_sync();
+        const uint64_t x = at + ((st * StateSmem::stage + StateSmem::X) >> 4);
+        const uint32_t d = tm + 128 * (i & 1), parts = tm_parts + 96 * (i & 1);
+        if (elected()) {
+          if (three) {
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)  // (the small parts first)
+              mma_ts(d, parts + 64 + 8 * ks, x + ks * 128, id, ks > 0);
+          }
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_ts(d, parts + 32 + 8 * ks, x + ks * 128, id, three || ks > 0);
+#pragma unroll
+          for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(d, parts + 8 * ks, x + ks * 128, id, 1);
+          mma_commit(done + 8 * (i & 1));
+          mma_commit(free_ + 8 * st);
         }
+        __syncwarp();
+        st = st + 1 == kStages ? 0 : st + 1;
       }
-      if (*failed)
-        for (int i = loaded > kStages ? loaded - kStages : 0; i < loaded; ++i)
-          drain(full + 8 * (i % kStages), (i / kStages) & 1);
-    }
-    __syncwarp();
-  } else if (warp == kMma) {
-    leave_registers<56>();
-    // (lanes behind V hold nothing that is read)
-    const uint32_t id = idesc_f16(128, K, 0, 1, 1);
-    const uint64_t at = sdesc(base, kRaw / 2, 1024);
-#pragma unroll 1
-    for (int i = 0, st = 0; i < tiles; ++i) {
-      wait_bar(ready + 8 * (i & 1), half(i), failed);
-      if (i >= 2) wait_bar(taken + 8 * (i & 1), half(i - 2), failed);
-      if (*failed) break;
-      fence_after_sync();
-      const uint64_t x = at + ((st * StateSmem::stage + StateSmem::X) >> 4);
-      const uint32_t d = tm + 128 * (i & 1), parts = tm_parts + 96 * (i & 1);
-      if (elected()) {
-        if (three) {
-#pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)  // (the small parts first)
-            mma_ts(d, parts + 64 + 8 * ks, x + ks * 128, id, ks > 0);
+      if (*failed) {
+        if (elected()) {
+          mma_commit(end);
+          drain(end, 0);
         }
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
-          mma_ts(d, parts + 32 + 8 * ks, x + ks * 128, id, three || ks > 0);
-#pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(d, parts + 8 * ks, x + ks * 128, id, 1);
-        mma_commit(done + 8 * (i & 1));
-        mma_commit(free_ + 8 * st);
+        __syncwarp();
       }
-      __syncwarp();
-      st = st + 1 == kStages ? 0 : st + 1;
-    }
-    if (*failed) {
-      if (elected()) {
-        mma_commit(end);
-        drain(end, 0);
-      }
-      __syncwarp();
     }
   } else if (warp < kSplit / 32) {
     // ---------------------------------------------------------------- weights and parts
@@ -449,6 +450,8 @@ constexpr int kWeightWarps = 4, kStateWarps = 8, kOpenWarps = 4;
 constexpr int kPassThreads = 32 * (kWeightWarps + kStateWarps + kOpenWarps + 4);  // (warpgroups)
 constexpr int kFirstState = kWeightWarps, kFirstOpen = kFirstState + kStateWarps,
               kLoadWarp = kFirstOpen + kOpenWarps, kMmaWarp = kLoadWarp + 1;
+static_assert(kWeightWarps % 4 == 0 && kStateWarps % 4 == 0 && kOpenWarps % 4 == 0,
+              "roles that set registers are whole warpgroups");
 struct PassSmem {             // offsets from a 1024-byte boundary
   static constexpr uint32_t Z = 0, X = kTileBytes, Y = 2 * kTileBytes, stage = 3 * kTileBytes;
   static constexpr uint32_t S = 2 * stage, POWERS = S + kTileBytes, TARGETS = POWERS + (C + 32) * 4;
@@ -604,142 +607,143 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
   auto first_token = [&](int c) { return begin + (REVERSE ? chunks - 1 - c : c) * C; };
   auto tokens = [&](int c) { return min(begin + length - first_token(c), C); };
 
-  if (warp == kLoadWarp) {
-    // ---------------------------------------------------------------- loads, and the outputs' stores
+  if (warp >= kLoadWarp) {  // (the last warpgroup; the rest of its warps have nothing to do)
     leave_registers<56>();
-    if (lane == 0) {
-      int loaded = 0, next_c = 0, head = oh * share;  // of the next loads
+    if (warp == kLoadWarp) {
+      // ---------------------------------------------------------------- loads, and the outputs' stores
+      if (lane == 0) {
+        int loaded = 0, next_c = 0, head = oh * share;  // of the next loads
 #pragma unroll 1
-      for (int it = -2, c = -2, g = 0; it < total; ++it) {  // (chunk it is given out, it + 2 loaded)
-        const bool more = loaded < total;
-        const uint32_t st = base + (it & 1) * PassSmem::stage;
-        const int t = first_token(next_c);
-        if (more) {
-          if (it >= 0) wait_one(bar(kFree, it), half(it), failed);
-          if (*failed) break;
-          const uint32_t b = bar(kFull, it);
-          mbar_expect_tx(b, (uint32_t)A * C * 4);
-          const int zh = head / a.z.share, xh = head / a.x.share;
+        for (int it = -2, c = -2, g = 0; it < total; ++it) {  // (chunk it is given out, it + 2 loaded)
+          const bool more = loaded < total;
+          const uint32_t st = base + (it & 1) * PassSmem::stage;
+          const int t = first_token(next_c);
+          if (more) {
+            if (it >= 0) wait_one(bar(kFree, it), half(it), failed);
+            if (*failed) break;
+            const uint32_t b = bar(kFull, it);
+            mbar_expect_tx(b, (uint32_t)A * C * 4);
+            const int zh = head / a.z.share, xh = head / a.x.share;
 #pragma unroll 1
-          for (int k = 0; 64 * k < A; ++k) {
-            tma_box(st + PassSmem::Z + k * kBlock, &mz, 64 * k, zh, t, b);
-            tma_box(st + PassSmem::X + k * kBlock, &mx, 64 * k, xh, t, b);
+            for (int k = 0; 64 * k < A; ++k) {
+              tma_box(st + PassSmem::Z + k * kBlock, &mz, 64 * k, zh, t, b);
+              tma_box(st + PassSmem::X + k * kBlock, &mx, 64 * k, xh, t, b);
+            }
+          }
+          if (it >= 0) {
+            wait_one(bar(kOut, it), half(it), failed);
+            if (*failed) break;
+            if (g + 1 == share && tokens(c) == C) {
+#pragma unroll 1
+              for (int k = 0; 64 * k < B; ++k)
+                tma_out(&mo, st + PassSmem::Y + k * kBlock, 64 * k, oh, first_token(c));
+              asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+              if (more) bulk_wait_read();
+            }
+          }
+          if (more) {
+            const uint32_t b = bar(kFullY, it);
+            mbar_expect_tx(b, (uint32_t)B * C * 2);
+            const int yh = head / a.y.share;
+#pragma unroll 1
+            for (int k = 0; 64 * k < B; ++k) tma_box(st + PassSmem::Y + k * kBlock, &my, 64 * k, yh, t, b);
+            ++loaded;
+            if (++next_c == chunks) {
+              next_c = 0;
+              ++head;
+            }
+          }
+          if (++c == chunks) {
+            c = 0;
+            ++g;
           }
         }
-        if (it >= 0) {
-          wait_one(bar(kOut, it), half(it), failed);
-          if (*failed) break;
-          if (g + 1 == share && tokens(c) == C) {
-#pragma unroll 1
-            for (int k = 0; 64 * k < B; ++k)
-              tma_out(&mo, st + PassSmem::Y + k * kBlock, 64 * k, oh, first_token(c));
-            asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
-            if (more) bulk_wait_read();
+        bulk_wait_all();
+        if (*failed)
+          for (int i = loaded > 2 ? loaded - 2 : 0; i < loaded; ++i) {
+            drain(bar(kFull, i), half(i));
+            drain(bar(kFullY, i), half(i));
           }
-        }
-        if (more) {
-          const uint32_t b = bar(kFullY, it);
-          mbar_expect_tx(b, (uint32_t)B * C * 2);
-          const int yh = head / a.y.share;
-#pragma unroll 1
-          for (int k = 0; 64 * k < B; ++k) tma_box(st + PassSmem::Y + k * kBlock, &my, 64 * k, yh, t, b);
-          ++loaded;
-          if (++next_c == chunks) {
-            next_c = 0;
-            ++head;
-          }
-        }
-        if (++c == chunks) {
-          c = 0;
-          ++g;
-        }
+        if (*failed && loaded < total) drain(bar(kFull, loaded), half(loaded));
       }
-      bulk_wait_all();
-      if (*failed)
-        for (int i = loaded > 2 ? loaded - 2 : 0; i < loaded; ++i) {
-          drain(bar(kFull, i), half(i));
-          drain(bar(kFullY, i), half(i));
-        }
-      if (*failed && loaded < total) drain(bar(kFull, loaded), half(loaded));
-    }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ---------------------------------------------------------------- products
-    leave_registers<56>();
-    // (growth: lanes behind A hold nothing that is read)
-    const uint32_t id_p = idesc_f16(128, 128, 0, 0, 1), id_o = idesc_f16(128, B, 0, 1),
-                   id_g = idesc_f16(128, B, 1, 1);
-    // rows by features (the contraction's index contiguous), and features or columns by rows
-    const uint64_t of_rows = sdesc(base, 16, 1024), of_cols = sdesc(base, kBlock, 1024);
-    // A chunk takes two turns: the state's growth, the sums.  The next chunk's scores are made behind the
-    // one when its tiles are there already, else behind the other; the first chunk's before all.
-    int grown = 0, scored = 0;
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------- products
+      // (growth: lanes behind A hold nothing that is read)
+      const uint32_t id_p = idesc_f16(128, 128, 0, 0, 1), id_o = idesc_f16(128, B, 0, 1),
+                     id_g = idesc_f16(128, B, 1, 1);
+      // rows by features (the contraction's index contiguous), and features or columns by rows
+      const uint64_t of_rows = sdesc(base, 16, 1024), of_cols = sdesc(base, kBlock, 1024);
+      // A chunk takes two turns: the state's growth, the sums.  The next chunk's scores are made behind the
+      // one when its tiles are there already, else behind the other; the first chunk's before all.
+      int grown = 0, scored = 0;
 #pragma unroll 1
-    for (int turn = -1, c = 0; turn < 2 * total && !*failed; ++turn) {
-      const int it = turn >> 1;
-      const uint64_t x = of_cols + (((it & 1) * PassSmem::stage + PassSmem::X) >> 4),
-                     y = of_cols + (((it & 1) * PassSmem::stage + PassSmem::Y) >> 4);
-      if (turn >= 0 && !(turn & 1)) {
-        wait_bar(bar(kValues, it), half(it), failed);  // (and x)
-        if (c + 1 < chunks) {
-          if (grown > 0) wait_bar(one(kTaken), (grown - 1) & 1, failed);
+      for (int turn = -1, c = 0; turn < 2 * total && !*failed; ++turn) {
+        const int it = turn >> 1;
+        const uint64_t x = of_cols + (((it & 1) * PassSmem::stage + PassSmem::X) >> 4),
+                       y = of_cols + (((it & 1) * PassSmem::stage + PassSmem::Y) >> 4);
+        if (turn >= 0 && !(turn & 1)) {
+          wait_bar(bar(kValues, it), half(it), failed);  // (and x)
+          if (c + 1 < chunks) {
+            if (grown > 0) wait_bar(one(kTaken), (grown - 1) & 1, failed);
+            fence_after_sync();
+            if (elected()) {
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks) mma_ss(tm_g, x + ks * 128, y + ks * 128, id_g, ks > 0);
+              mma_commit(one(kGrown));
+            }
+            __syncwarp();
+            ++grown;
+          }
+        } else if (turn >= 0) {
+          const uint32_t w = tm + 128 * (it & 1);
+          wait_bar(bar(kWeights, it), half(it), failed);
+          if (it > 0) wait_bar(bar(kSumsRead, it - 1), half(it - 1), failed);
           fence_after_sync();
           if (elected()) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks) mma_ss(tm_g, x + ks * 128, y + ks * 128, id_g, ks > 0);
-            mma_commit(one(kGrown));
+            for (int ks = 0; ks < 8; ++ks) mma_ts(tm_o, w + 8 * ks, y + ks * 128, id_o, ks > 0);
           }
           __syncwarp();
-          ++grown;
-        }
-      } else if (turn >= 0) {
-        const uint32_t w = tm + 128 * (it & 1);
-        wait_bar(bar(kWeights, it), half(it), failed);
-        if (it > 0) wait_bar(bar(kSumsRead, it - 1), half(it - 1), failed);
-        fence_after_sync();
-        if (elected()) {
+          wait_bar(bar(kTargets, it), half(it), failed);
+          wait_bar(one(kStateIn), it & 1, failed);
+          fence_after_sync();
+          if (elected()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) mma_ts(tm_o, w + 8 * ks, y + ks * 128, id_o, ks > 0);
-        }
-        __syncwarp();
-        wait_bar(bar(kTargets, it), half(it), failed);
-        wait_bar(one(kStateIn), it & 1, failed);
-        fence_after_sync();
-        if (elected()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            if (16 * ks < A) mma_ts(tm_o, w + 64 + 8 * ks, of_cols + (PassSmem::S >> 4) + ks * 128, id_o, 1);
-          mma_commit(one(kSums));
-          mma_commit(bar(kFree, it));
-        }
-        __syncwarp();
-        c = c + 1 == chunks ? 0 : c + 1;
-      }
-      if (scored < total && scored <= it + 1 &&
-          ((turn & 1) ||
-           __shfl_sync(0xffffffffu, mbar_test(bar(kFull, scored), half(scored)), 0))) {
-        wait_bar(bar(kFull, scored), half(scored), failed);
-        fence_after_sync();
-        const uint64_t z = of_rows + (((scored & 1) * PassSmem::stage + PassSmem::Z) >> 4),
-                       xr = of_rows + (((scored & 1) * PassSmem::stage + PassSmem::X) >> 4);
-        if (elected()) {
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
-            if (16 * ks < A) mma_ss(tm + 128 * (scored & 1), z + at, xr + at, id_p, ks > 0);
+            for (int ks = 0; ks < 8; ++ks)
+              if (16 * ks < A) mma_ts(tm_o, w + 64 + 8 * ks, of_cols + (PassSmem::S >> 4) + ks * 128, id_o, 1);
+            mma_commit(one(kSums));
+            mma_commit(bar(kFree, it));
           }
-          mma_commit(bar(kScores, scored));
+          __syncwarp();
+          c = c + 1 == chunks ? 0 : c + 1;
+        }
+        if (scored < total && scored <= it + 1 &&
+            ((turn & 1) ||
+             __shfl_sync(0xffffffffu, mbar_test(bar(kFull, scored), half(scored)), 0))) {
+          wait_bar(bar(kFull, scored), half(scored), failed);
+          fence_after_sync();
+          const uint64_t z = of_rows + (((scored & 1) * PassSmem::stage + PassSmem::Z) >> 4),
+                         xr = of_rows + (((scored & 1) * PassSmem::stage + PassSmem::X) >> 4);
+          if (elected()) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t at = ((ks >> 2) * kBlock + (ks & 3) * 32) >> 4;
+              if (16 * ks < A) mma_ss(tm + 128 * (scored & 1), z + at, xr + at, id_p, ks > 0);
+            }
+            mma_commit(bar(kScores, scored));
+          }
+          __syncwarp();
+          ++scored;
+        }
+      }
+      if (*failed) {
+        if (elected()) {
+          mma_commit(one(kEnd));
+          drain(one(kEnd), 0);
         }
         __syncwarp();
-        ++scored;
       }
-    }
-    if (*failed) {
-      if (elected()) {
-        mma_commit(one(kEnd));
-        drain(one(kEnd), 0);
-      }
-      __syncwarp();
     }
   } else if (warp < kWeightWarps) {
     // ---------------------------------------------------------------- weights; z to Tensor Memory
@@ -1045,7 +1049,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         ++g;
       }
     }
-  } else if (warp < kLoadWarp) {
+  } else {
     // ---------------------------------------------------------------- rows opened to fp16
     leave_registers<56>();
     const int row = tid - 32 * kFirstOpen;  // one thread a row
@@ -1079,8 +1083,6 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         mbar_arrive(bar(kValues, it));
       }
     }
-  } else {  // (the rest of the last warpgroup)
-    leave_registers<56>();
   }
   fence_before_sync();
   __syncthreads();

@@ -10,8 +10,11 @@ block walks.  Random schedules, with copies and products that complete at random
 
 The models mirror gated_delta_rule_07_gb300/csrc/gdn_linear_tc.cu and must be kept in step with it.
 Planted bugs have to be found, among them a head's start that does not wait for the weights' warps.
+That a warpgroup's warps set their registers together is read from the kernels' source.
 """
+import os
 import random
+import re
 
 import pytest
 
@@ -415,3 +418,50 @@ def test_other_planted_bugs_are_found():
     assert wrong and "RACE" in wrong and " e" in wrong
     wrong = check(lambda: linear_state(4, parts_kept=False), 400)
     assert wrong and "RACE" in wrong and "parts" in wrong
+
+
+# ----------------------------------------------------------------------------- registers
+SOURCE = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                      "gated_delta_rule_07_gb300", "csrc", "gdn_linear_tc.cu")
+
+
+@pytest.mark.parametrize("kernel,threads", [("linear_state_tc_kernel", "kStateThreads"),
+                                            ("linear_pass_tc_kernel", "kPassThreads")])
+def test_a_warpgroup_sets_its_registers_at_one_place(kernel, threads):
+    """setmaxnreg is for all warps of a warpgroup together: each of them has to come to the same one,
+    which stands first under the branches of the roles, and the registers have to add up."""
+    with open(SOURCE) as f:
+        text = f.read()
+    known = {}
+    for line in re.findall(r"constexpr int ([^;]*);", text):
+        for name, value in re.findall(r"(k\w+) = ([^,]+)", line):
+            try:
+                known[name] = int(eval(value.replace("/", "//"), {}, known))
+            except (NameError, SyntaxError):
+                pass
+    body = text[text.index(f"\n{kernel}("):]
+    body = body[:body.index("\n}\n")].split("\n")
+    branches = []   # [condition, registers of the call under it] of the first `if (warp ...)` chain
+    for i, line in enumerate(body):
+        role = re.match(r"  (?:} else )?if \((warp [<>=].*)\) {", line)
+        if role:
+            condition = role.group(1)
+        elif line.startswith("  } else {") and branches:
+            condition = "True"
+        else:
+            continue
+        after = next(x for x in body[i + 1:] if x.strip() and not x.strip().startswith("//"))
+        call = re.match(r"    (?:take|leave)_registers<(\d+)>\(\);", after)
+        if call:
+            branches.append((condition.replace("/", "//"), int(call.group(1))))
+    calls = sum(len(re.findall(r"(?:take|leave)_registers<", line)) for line in body)
+    assert len(branches) >= 3 and calls == len(branches)
+
+    def place(warp):
+        return next(i for i, (c, _) in enumerate(branches) if eval(c, {}, {**known, "warp": warp}))
+
+    warps = known[threads] // 32
+    groups = [{place(w) for w in range(g, g + 4)} for g in range(0, warps, 4)]
+    assert warps % 4 == 0 and all(len(g) == 1 for g in groups), groups
+    at_launch = 65536 // known[threads] // 8 * 8
+    assert sum(branches[p][1] for g in groups for p in g) <= at_launch * warps // 4
