@@ -1010,7 +1010,7 @@ gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, cons
   GDN_TRY(gdn::linear_scan(&scan, 1, stream));
   if (T > 0)
     GDN_TRY(linear_pass(p, {s, qr, kr, vr, s.K, s.V, false, false, states, out, 1, nullptr, tops,
-                            tops + 1, nullptr}, stream));
+                            tops + 1}, stream));
   return GDN_OK;
 }
 
@@ -1081,11 +1081,11 @@ gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void
   if (T > 0) {
     float* partial = reinterpret_cast<float*>(ws + L.partial);
     const int *tk = linear_tops(s, h), *tv = tk + 1, *tq = linear_tops(s, d), *tg = tq + 1;
-    GDN_TRY(linear_pass(p, {s, gr, vr, kr, s.V, s.K, false, true, h, dq, share, partial, tv, tk, tg},
+    GDN_TRY(linear_pass(p, {s, gr, vr, kr, s.V, s.K, false, true, h, dq, share, partial, tv, tk},
                         stream));
-    GDN_TRY(linear_pass(p, {s, vr, gr, qr, s.V, s.K, true, true, d, dk, share, partial, tg, tq, tv},
+    GDN_TRY(linear_pass(p, {s, vr, gr, qr, s.V, s.K, true, true, d, dk, share, partial, tg, tq},
                         stream));
-    GDN_TRY(linear_pass(p, {s, kr, qr, gr, s.K, s.V, true, false, d, dv, 1, nullptr, tq, tg, tk},
+    GDN_TRY(linear_pass(p, {s, kr, qr, gr, s.K, s.V, true, false, d, dv, 1, nullptr, tq, tg},
                         stream));
   }
   return GDN_OK;

@@ -75,8 +75,8 @@ struct LinearPass {
   int out_share;            // value heads summed into one output head
   float* partial;           // with out_share > 1: their running sum, T hv / out_share B values (tensor
                             // cores), or each's rows, T hv B values (CUDA cores)
-  // tensor cores: entry 2 (slot hv + head) bounds these rows (see LinearState); z_top may be null
-  const int *x_top, *y_top, *z_top;
+  // tensor cores: entry 2 (slot hv + head) bounds these rows (see LinearState)
+  const int *x_top, *y_top;
 };
 
 // fp32 arithmetic on the CUDA cores: every dtype and head size.

@@ -433,7 +433,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
 //     S <- a^n S + (a^{n - j} x)^T y  fp16 operands; S fp32 in registers, its fp16 copy in shared memory
 // fp16's range is not bf16's, so operands are scaled by powers of two, which come off again in fp32:
 // with 2^e_x, 2^e_y above all of a head's x and y in the segment (the state kernel has seen them), 2^e_z
-// above a row of z, or all of it, M = e_x + e_y, and 2^E a bound of S and of 2^(M + 7):
+// above a row of z, M = e_x + e_y, and 2^E a bound of S and of 2^(M + 7):
 //     y~ = y 2^(14 - e_y)     x~ = a^{n - j} x 2^(15 + e_y - M)     S~ = S 2^(15 - E)
 //     z~ = p_i z 2^(14 - e_z)   W~ = W 2^(15 + e_y - e_z - E)         O = O~ 2^(e_z + E - 29)
 // so that nothing can overflow that does not in fp32, and each rounding is half a step of fp16 (2^-11) of
@@ -755,7 +755,6 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       const int64_t at = slot * a.s.hv + oh * share + g;
       const float log2a = linear::log2_decay(a.s, oh * share + g);
       const int ex = top_of(a.x_top, at, -110), ey = top_of(a.y_top, at, -110);
-      const int ez_all = a.z_top ? top_of(a.z_top, at, -60) : 0;
       wait_bar(one(kStart), g & 1, failed);
       Bound bound;
       bound.start(__int_as_float(((volatile int*)misc)[2 + (g & 1)]), max(ex + ey, -97), log2a);
@@ -777,10 +776,10 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       for (int c = 0; c < chunks; ++c, ++it) {
         const int m = tokens(c), E = bound.E();
         bound.grow(m == C ? bound.whole : linear::power(log2a, m));
-        if (!a.z_top) wait_bar(bar(kRows, it), half(it), failed);
+        wait_bar(bar(kRows, it), half(it), failed);
         wait_bar(bar(kScores, it), half(it), failed);
         fence_after_sync();
-        const int ez = a.z_top ? ez_all : targets[C * (it & 1) + row];
+        const int ez = targets[C * (it & 1) + row];
         // (where z, x and y together pass fp32's range, what would be lost is made NaN)
         const int top = 15 - ez - E - h;
         const float mine = top < -126 ? __int_as_float(0x7fffffff) : two_to(top);
@@ -869,8 +868,8 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
     const uint32_t turn = (uint32_t)(row & 7);
     const bool mine = (int)cols < B, grows = mine && row < A;
     float2 S[32];
-    auto give = [&](int it, int c, int g, int E, int ez_all) {  // (its sums are there)
-      const int m = tokens(c), e = (a.z_top ? ez_all : targets[C * (it & 1) + row]) + E - 29;
+    auto give = [&](int it, int c, int g, int E) {  // (its sums are there)
+      const int m = tokens(c), e = targets[C * (it & 1) + row] + E - 29;
       const int near = max(-126, min(e, 127));
       const float s0 = two_to(near);
       const bool far = __any_sync(0xffffffffu, near != e), live = row < m && !*failed;
@@ -942,7 +941,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       fence_async_smem();
       mbar_arrive(bar(kOut, it));
     };
-    int grown = 0, c = 0, g = 0, c_before = 0, g_before = 0, E_before = 0, ez_before = 0, E = 0, ez = 0;
+    int grown = 0, c = 0, g = 0, c_before = 0, g_before = 0, E_before = 0, E = 0;
     float log2a = 0.f;
     Bound bound = {};
 #pragma unroll 1
@@ -982,7 +981,6 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         if (lane == 0) atomicMax(misc + 2 + (g & 1), (int)top);
         mbar_arrive(one(kStart));
         wait_bar(one(kStart), g & 1, failed);
-        ez = a.z_top ? top_of(a.z_top, where, -60) : 0;
         bound.start(__int_as_float(((volatile int*)misc)[2 + (g & 1)]), M, log2a);
       }
       if (SUM && it > 0 && g_before > 0 && lane % 8 == 0) {  // (the running sum's lines, 8 rows each)
@@ -997,7 +995,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       if (it > 0) {  // (the last chunk's use of the copy)
         wait_bar(one(kSums), (it - 1) & 1, failed);
         fence_after_sync();
-        give(it - 1, c_before, g_before, E_before, ez_before);
+        give(it - 1, c_before, g_before, E_before);
       }
       if (it < total) {
         E = bound.E();
@@ -1043,7 +1041,6 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       c_before = c;
       g_before = g;
       E_before = E;
-      ez_before = ez;
       if (++c == chunks) {
         c = 0;
         ++g;
@@ -1059,19 +1056,16 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       const float log2a = linear::log2_decay(a.s, oh * share + g);
       const int ex = top_of(a.x_top, at, -110), ey = top_of(a.y_top, at, -110);
       const float x_scale = two_to(15 + ey - max(ex + ey, -97));
-      int ez = a.z_top ? top_of(a.z_top, at, -60) : 0;
       const float x_whole = linear::power(log2a, REVERSE ? row + 1 : C - row) * x_scale;
       for (int c = 0; c < chunks; ++c, ++it) {
         const int m = tokens(c);
         const bool live = row < m;
         const uint32_t st = base + (it & 1) * PassSmem::stage;
         wait_bar(bar(kFull, it), half(it), failed);
-        if (!a.z_top) {
-          ez = live ? exponent_of(row_max_of(st + PassSmem::Z, row, A), -60) : -60;
-          if (it >= 2) wait_bar(bar(kSumsRead, it - 2), half(it - 2), failed);  // (who reads it there)
-          targets[C * (it & 1) + row] = ez;
-          mbar_arrive(bar(kRows, it));
-        }
+        const int ez = live ? exponent_of(row_max_of(st + PassSmem::Z, row, A), -60) : -60;
+        if (it >= 2) wait_bar(bar(kSumsRead, it - 2), half(it - 2), failed);  // (who reads it there)
+        targets[C * (it & 1) + row] = ez;
+        mbar_arrive(bar(kRows, it));
         if (c + 1 < chunks) {
           wait_bar(bar(kScores, it), half(it), failed);  // (x as it was has been read)
           open_row(st + PassSmem::X, row, A, live,

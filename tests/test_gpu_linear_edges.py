@@ -44,3 +44,28 @@ def test_many_sequences_of_one_chunk_with_shared_key_heads(gdn, hk, hv, K, V):
     for _ in range(20):
         again = gdn.linear_attention_backward(q, k, v, g, do, h0, dh, cu)
         assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+# ------------------------------------------------------------------------------- sizes of the operands
+
+def close(got, want, size, tokens, what=""):
+    lt.assert_close(got, want, size, lt.inner_error(tokens, True), what)
+
+
+@pytest.mark.parametrize("times", [2.0 ** 30, 2.0 ** 60])
+@pytest.mark.parametrize("hk,hv", [(2, 2), (1, 3)])
+def test_gradients_of_a_token_keep_their_own_accuracy(gdn, hk, hv, times):
+    """One token's dout (v, k) far above the others': dq (dk, dv) of the others have the accuracy that
+    they have without it, for each is made of its own token's dout (v, k) and of the other tensors."""
+    gen = torch.Generator().manual_seed(hv)
+    T, lens, cu = 300, [300], lt.cumulative([300])
+    q, k, v, do = (rand(gen, T, h, 128) for h in (hk, hk, hv, hv))
+    g = -torch.rand(hv, generator=gen).cuda() * 0.1
+    h0, dh = (torch.randn(1, hv, 128, 128, generator=gen).cuda() for _ in range(2))
+    for i, name in enumerate(("do", "v", "k")):
+        x = dict(q=q, k=k, v=v, do=do)
+        x[name] = x[name].clone()
+        x[name][100] *= times
+        args = x["q"], x["k"], x["v"], g, x["do"], h0, dh
+        got = gdn.linear_attention_backward(*args, cu, check_status=True)
+        close(got[i], lt.backward(*args, lens)[i], lt.magnitudes(lt.backward, *args, lens)[i], 300, name)
