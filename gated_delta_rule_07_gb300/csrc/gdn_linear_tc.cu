@@ -514,6 +514,9 @@ __device__ __forceinline__ void open_row(uint32_t tile, int row, int width, bool
   }
   __syncwarp();
 }
+// Exponents of rows of z: the least one that is told apart (times 2^126, bf16's least value is 2^-7 and has
+// all its bits in fp16), and that of a row of zeros.
+constexpr int kLeastRow = -112, kNoRow = -120;
 // Exponents of a head's rows in a segment: 2^e above all of them.
 __device__ __forceinline__ int top_of(const int* tops, int64_t at, int least) {
   return max(min(tops[2 * at], 127), least);
@@ -781,8 +784,10 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         fence_after_sync();
         const int ez = targets[C * (it & 1) + row];
         // (where z, x and y together pass fp32's range, what would be lost is made NaN)
+        // (and where they are small, the factor takes another power of two)
         const int top = 15 - ez - E - h;
         const float mine = top < -126 ? __int_as_float(0x7fffffff) : two_to(top);
+        const bool far = __any_sync(0xffffffffu, ez != kNoRow && top > 127);
         const uint32_t p_at = tm + lanes + 128 * (it & 1);
 #pragma unroll 1
         for (int k0 = 0; k0 < C; k0 += 32) {
@@ -794,6 +799,13 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
             tmem_ld16_nw(p_at + k0, p[0]);
             tmem_ld16_nw(p_at + k0 + 16, p[1]);
             tmem_wait_ld16x2(p[0], p[1]);
+            if (far) {
+              const float more = two_to(max(0, top - 127));
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) p[q][j] = __float_as_uint(__uint_as_float(p[q][j]) * more);
+            }
             if (k0 != first) {  // a^|i - j| as a power of the row and one of the column
 #pragma unroll
               for (int q = 0; q < 2; ++q) {
@@ -869,7 +881,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
     const bool mine = (int)cols < B, grows = mine && row < A;
     float2 S[32];
     auto give = [&](int it, int c, int g, int E) {  // (its sums are there)
-      const int m = tokens(c), e = targets[C * (it & 1) + row] + E - 29;
+      const int m = tokens(c), ez = targets[C * (it & 1) + row], e = ez == kNoRow ? 0 : ez + E - 29;
       const int near = max(-126, min(e, 127));
       const float s0 = two_to(near);
       const bool far = __any_sync(0xffffffffu, near != e), live = row < m && !*failed;
@@ -1062,7 +1074,8 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         const bool live = row < m;
         const uint32_t st = base + (it & 1) * PassSmem::stage;
         wait_bar(bar(kFull, it), half(it), failed);
-        const int ez = live ? exponent_of(row_max_of(st + PassSmem::Z, row, A), -60) : -60;
+        const uint32_t most = live ? row_max_of(st + PassSmem::Z, row, A) : 0u;
+        const int ez = most ? exponent_of(most, kLeastRow) : kNoRow;
         if (it >= 2) wait_bar(bar(kSumsRead, it - 2), half(it - 2), failed);  // (who reads it there)
         targets[C * (it & 1) + row] = ez;
         mbar_arrive(bar(kRows, it));

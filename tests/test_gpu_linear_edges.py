@@ -69,3 +69,23 @@ def test_gradients_of_a_token_keep_their_own_accuracy(gdn, hk, hv, times):
         args = x["q"], x["k"], x["v"], g, x["do"], h0, dh
         got = gdn.linear_attention_backward(*args, cu, check_status=True)
         close(got[i], lt.backward(*args, lens)[i], lt.magnitudes(lt.backward, *args, lens)[i], 300, name)
+
+
+@pytest.mark.parametrize("small,large", [(2.0 ** -100, 2.0 ** 40), (2.0 ** -120, 2.0 ** 50)])
+def test_small_rows_against_large_ones(gdn, small, large):
+    """q (dout) so small that its fp16 form needs more than a power of two that fp32 holds beside the
+    others'; what comes out is of ordinary size."""
+    gen = torch.Generator().manual_seed(3)
+    T, lens, cu = 300, [170, 130], lt.cumulative([170, 130])
+    q, k, v, do = (rand(gen, T, h, 128) for h in (1, 1, 2, 2))
+    g = torch.tensor([-0.3, -0.01], device="cuda")
+    h0, dh = (torch.randn(2, 2, 128, 128, generator=gen).cuda() for _ in range(2))
+    args = q * small, k * large, v * large, g, h0 * large ** 2
+    out, last = gdn.linear_attention(*args, cu, check_status=True)
+    want, size = lt.forward(*args, lens), lt.magnitudes(lt.forward, *args, lens)
+    close(out, want[0], size[0], 170, "out")
+    args = q * large, k * large, v * large, g, do * small, h0 * large ** 2, dh * large * small
+    got = gdn.linear_attention_backward(*args, cu, check_status=True)
+    want, size = lt.backward(*args, lens), lt.magnitudes(lt.backward, *args, lens)
+    for i, name in enumerate(("dq", "dk", "dv")):
+        close(got[i], want[i], size[i], 170, name)
