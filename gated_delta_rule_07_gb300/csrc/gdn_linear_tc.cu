@@ -530,7 +530,7 @@ struct Bound {
     q = max((int)(__float_as_uint(max_s) >> 23) - 126, M + 7);
     b = 1.f;
     whole = linear::power(log2a, C);
-    grown = C * two_to(M - q);
+    grown = C * two_to(max(M - q, -126));  // (not nothing: it may outlive what S starts from)
   }
   __device__ __forceinline__ int E() const {
     return max((int)(__float_as_uint(b) >> 23) - 126 + q, M + 7);

@@ -89,3 +89,23 @@ def test_small_rows_against_large_ones(gdn, small, large):
     want, size = lt.backward(*args, lens), lt.magnitudes(lt.backward, *args, lens)
     for i, name in enumerate(("dq", "dk", "dv")):
         close(got[i], want[i], size[i], 170, name)
+
+
+def test_a_state_that_forgets_its_start(gdn):
+    """A start of 2^100, and keys times values of 2^-27: by the time that the start has decayed below them,
+    the state is what thousands of tokens have gathered, and its bound has to be too.  Every element is
+    the same, so the definition is a geometric sum."""
+    T, hv, d = 70000, 152, 0.85 ** (1 / 128)
+    x = (2 - 2.0 ** -7) * 2.0 ** -14
+    q = torch.ones(T, 1, 128, device="cuda", dtype=BF16)
+    k = torch.full_like(q, x)
+    v = torch.full((T, hv, 64), x / 2, device="cuda", dtype=BF16)
+    g = torch.full((hv,), d, device="cuda").log()
+    h0 = torch.full((1, hv, 128, 64), 2.0 ** 100, device="cuda")
+    out, last = gdn.linear_attention(q, k, v, g, h0, check_status=True)
+    t = torch.arange(T, device="cuda", dtype=torch.float64) + 1
+    a = g[0].double()
+    want = 128 * (torch.exp(a * t) * 2.0 ** 100 + x * x / 2 * torch.expm1(a * t) / torch.expm1(a))
+    off = (out[:, [0, 76, 151]].double() / want[:, None, None] - 1).abs().amax((1, 2))
+    # (a bf16 rounding, three fp16 ones, and the powers: t log2(a) of up to 130 is off by 2^-24 of it, twice)
+    assert off.max() <= 2.0 ** -8 + 3 * 2.0 ** -11 + 130 * 2.0 ** -23
