@@ -54,7 +54,7 @@ struct LinearState {
   LinearRows x, y;
   bool reverse;
   float* states;            // [slots, hv, K, V]
-  int* tops;                // tensor cores: [slots, hv, 2], 2^e above all of x's magnitudes, and y's
+  int* tops;                // tensor cores: [slots, hv, 2], the largest finite |x| and |y|, as fp32's bits
 };
 // The states that the segments start from, in place of U; the walk starts from `first` (null: 0) and
 // its end goes to `last` (null: nowhere), [N, hv, K, V] each.

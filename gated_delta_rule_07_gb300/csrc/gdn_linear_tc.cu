@@ -87,11 +87,12 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
 }
 // such magnitudes, or zeros where one is infinite
 __device__ __forceinline__ uint32_t finite(uint32_t m) { return (m + 0x00800080u) & 0x80008000u ? 0u : m; }
-// e with |v| < 2^e for these magnitudes; of zeros the least
-__device__ __forceinline__ int exponent_of(uint32_t packed_max, int least) {
-  const uint32_t m = max(packed_max & 0x7fffu, packed_max >> 16 & 0x7fffu);
-  return max(min((int)(m >> 7) - 126, 127), least);
+// the larger of such a pair, as bits of fp32 (which have magnitudes' order)
+__device__ __forceinline__ int larger_of_two(uint32_t m) {
+  return (int)(max(m & 0x7fffu, m >> 16 & 0x7fffu) << 16);
 }
+// e with |v| < 2^e for the bits of a magnitude of fp32's normal range
+__device__ __forceinline__ int exponent_of(int bits) { return (bits >> 23) - 126; }
 
 // ------------------------------------------------------------------ a segment's own state
 
@@ -155,7 +156,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
   const int tid = threadIdx.x, warp = tid / 32;
   if (tid == 0) {
     failed_word = 0;
-    top[0] = top[1] = -126;
+    top[0] = top[1] = 0;
     for (int i = 0; i < kStages; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(free_ + 8 * i, 1);
@@ -372,11 +373,11 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
       }
       __syncwarp();
     }
-    const int e_x = __reduce_max_sync(0xffffffffu, exponent_of(x_max, -126));
-    const int e_y = __reduce_max_sync(0xffffffffu, exponent_of(y_max, -126));
+    const int most_x = __reduce_max_sync(0xffffffffu, larger_of_two(x_max));
+    const int most_y = __reduce_max_sync(0xffffffffu, larger_of_two(y_max));
     if (tid % 32 == 0) {
-      atomicMax(top, e_x);
-      atomicMax(top + 1, e_y);
+      atomicMax(top, most_x);
+      atomicMax(top + 1, most_y);
     }
   } else {
     // ---------------------------------------------------------------- the sum
@@ -433,7 +434,7 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
 //     S <- a^n S + (a^{n - j} x)^T y  fp16 operands; S fp32 in registers, its fp16 copy in shared memory
 // fp16's range is not bf16's, so operands are scaled by powers of two, which come off again in fp32:
 // with 2^e_x, 2^e_y above all of a head's x and y in the segment (the state kernel has seen them), 2^e_z
-// above a row of z, M = e_x + e_y, and 2^E a bound of S and of 2^(M + 7):
+// above a row of z, M = e_x + e_y, and 2^(E + 1) a bound of S and of 128 |x| |y|:
 //     y~ = y 2^(14 - e_y)     x~ = a^{n - j} x 2^(15 + e_y - M)     S~ = S 2^(15 - E)
 //     z~ = p_i z 2^(14 - e_z)   W~ = W 2^(15 + e_y - e_z - E)         O = O~ 2^(e_z + E - 29)
 // so that nothing can overflow that does not in fp32, and each rounding is half a step of fp16 (2^-11) of
@@ -517,27 +518,44 @@ __device__ __forceinline__ void open_row(uint32_t tile, int row, int width, bool
 // Exponents of rows of z: the least one that is told apart (times 2^126, bf16's least value is 2^-7 and has
 // all its bits in fp16), and that of a row of zeros.
 constexpr int kLeastRow = -112, kNoRow = -120;
-// Exponents of a head's rows in a segment: 2^e above all of them.
-__device__ __forceinline__ int top_of(const int* tops, int64_t at, int least) {
-  return max(min(tops[2 * at], 127), least);
+// A head's x and y in a segment: 2^ex and 2^ey above their largest magnitudes (of at least 2^-101, and products
+// of at least 2^-97: what is left out is below fp32's states), p 2^M above a product of the two, with a
+// thousandth more for the roundings of what is bounded by it.
+struct Tops {
+  int ex, ey, M;
+  float p;
+};
+constexpr float kMore = 1.002f;
+// the fraction of a magnitude that exponent_of leaves, in [1/2, 1)
+__device__ __forceinline__ float fraction_of(int bits) {
+  return __int_as_float((bits & 0x7fffff) | 126 << 23);
 }
-// |S| < 2^E for what S starts from and what the chunks have added (2^M bounds a product), kept as b 2^q.
+__device__ __forceinline__ Tops tops_of(const LinearPass& a, int64_t at) {
+  const int x = max(a.x_top[2 * at], 26 << 23), y = max(a.y_top[2 * at], 26 << 23);
+  Tops t;
+  t.ex = exponent_of(x);
+  t.ey = exponent_of(y);
+  t.M = max(t.ex + t.ey, -97);
+  t.p = t.ex + t.ey < -97 ? 1.f : kMore * fraction_of(x) * fraction_of(y);
+  return t;
+}
+// |S| <= b 2^q for what S starts from and what the chunks have added.
 struct Bound {
-  float b, whole, grown;  // a^C and C 2^(M - q): what a whole chunk does
-  int q, M;
-  __device__ __forceinline__ void start(float max_s, int m, float log2a) {
-    M = m;
-    q = max((int)(__float_as_uint(max_s) >> 23) - 126, M + 7);
-    b = 1.f;
+  float b, whole, grown;  // a^C and C p 2^(M - q): what a whole chunk does
+  int q, M, least;
+  __device__ __forceinline__ void start(int max_s, const Tops& t, float log2a) {
+    M = t.M;
+    q = max(exponent_of(max_s), M + 7);
+    b = kMore * fraction_of(max_s) * two_to(exponent_of(max_s) - q);
     whole = linear::power(log2a, C);
-    grown = C * two_to(max(M - q, -126));  // (not nothing: it may outlive what S starts from)
+    grown = C * t.p * two_to(max(M - q, -126));  // (not nothing: it may outlive what S starts from)
+    least = exponent_of(__float_as_int(C * t.p)) - 1 + M;
   }
-  __device__ __forceinline__ int E() const {
-    return max((int)(__float_as_uint(b) >> 23) - 126 + q, M + 7);
-  }
+  // E: |S| 2^(15 - E) and |W| 2^(15 + e_y - e_z - E) <= 65536 / kMore, which fp16 holds
+  __device__ __forceinline__ int E() const { return max(exponent_of(__float_as_int(b)) - 1 + q, least); }
   // (a chunk of fewer tokens is the walk's first or last: it may count as whole where it adds, and
   // decays by what it has)
-  __device__ __forceinline__ void grow(float decay) { b = fmaxf(fmaf(decay, b, grown), 0x1p-120f); }
+  __device__ __forceinline__ void grow(float decay) { b = fmaf(decay, b, grown); }
 };
 __device__ __forceinline__ void tma_out(const CUtensorMap* map, uint32_t src, int x, int head, int t0) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(
@@ -757,16 +775,16 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
     for (int g = 0; g < share; ++g) {
       const int64_t at = slot * a.s.hv + oh * share + g;
       const float log2a = linear::log2_decay(a.s, oh * share + g);
-      const int ex = top_of(a.x_top, at, -110), ey = top_of(a.y_top, at, -110);
+      const Tops tops = tops_of(a, at);
       wait_bar(one(kStart), g & 1, failed);
       Bound bound;
-      bound.start(__int_as_float(((volatile int*)misc)[2 + (g & 1)]), max(ex + ey, -97), log2a);
-      // W~'s factor 2^(15 + e_y - e_z - E) in two, each in fp32's range
-      const int h = max(0, -59 - bound.M);
+      bound.start(((volatile int*)misc)[2 + (g & 1)], tops, log2a);
+      // W~'s factor 2^(15 + e_y - e_z - E) in two, the columns' in fp32's range: 2^h, and the rest
+      const int h = max(-1, -60 - bound.M);
       named_bar(1, 32 * kWeightWarps);  // (the last head's powers have been read, this one's max |S|)
       if (row == 0) misc[2 + (~g & 1)] = 0;  // for the next head (who used it has read it)
       // a^i 2^(e_y + h), 0 for i < 0
-      powers[row] = linear::power(log2a, row) * two_to(ey + h);
+      powers[row] = linear::power(log2a, row) * two_to(tops.ey + h);
       if (row < 32) powers[row - 32] = 0.f;
       named_bar(1, 32 * kWeightWarps);
       mbar_arrive(one(kBegun));
@@ -786,7 +804,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         // (where z, x and y together pass fp32's range, what would be lost is made NaN)
         // (and where they are small, the factor takes another power of two)
         const int top = 15 - ez - E - h;
-        const float mine = top < -126 ? __int_as_float(0x7fffffff) : two_to(top);
+        const float mine = top < -126 && ez != kNoRow ? __int_as_float(0x7fffffff) : two_to(top);
         const bool far = __any_sync(0xffffffffu, ez != kNoRow && top > 127);
         const uint32_t p_at = tm + lanes + 128 * (it & 1);
 #pragma unroll 1
@@ -962,7 +980,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         const int64_t where = slot * a.s.hv + oh * share + g;
         log2a = linear::log2_decay(a.s, oh * share + g);
         const float* from = a.states + where * A * B;
-        const int M = max(top_of(a.x_top, where, -110) + top_of(a.y_top, where, -110), -97);
+        const Tops tops = tops_of(a, where);
         const float enter = REVERSE ? 1.f : linear::power(log2a, 1);
         uint32_t top = 0;
         if (!grows) {
@@ -993,7 +1011,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         if (lane == 0) atomicMax(misc + 2 + (g & 1), (int)top);
         mbar_arrive(one(kStart));
         wait_bar(one(kStart), g & 1, failed);
-        bound.start(__int_as_float(((volatile int*)misc)[2 + (g & 1)]), M, log2a);
+        bound.start(((volatile int*)misc)[2 + (g & 1)], tops, log2a);
       }
       if (SUM && it > 0 && g_before > 0 && lane % 8 == 0) {  // (the running sum's lines, 8 rows each)
         const int m = tokens(c_before);
@@ -1011,13 +1029,18 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
       }
       if (it < total) {
         E = bound.E();
-        const float s = two_to(15 - E);
+        const float s = two_to(max(15 - E, -126));
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (!mine) break;
           float2 f[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) f[i] = mul2(S[4 * k + i], make_float2(s, s));
+          if (E > 141) {  // (the factor is below fp32's range, what it makes is not)
+            const float s1 = two_to(141 - E);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = mul2(f[i], make_float2(s1, s1));
+          }
           sts16(copy + ((k ^ turn) << 4), make_uint4(pack_h2(f[0].x, f[0].y), pack_h2(f[1].x, f[1].y),
                                                      pack_h2(f[2].x, f[2].y), pack_h2(f[3].x, f[3].y)));
         }
@@ -1029,7 +1052,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         const float w = m == C ? bound.whole : linear::power(log2a, m);
         bound.grow(w);
         if (c + 1 < chunks) {
-          const float add = two_to(bound.M - 29);
+          const float add = two_to(min(bound.M - 29, 127));
           wait_bar(one(kGrown), grown & 1, failed);
           fence_after_sync();
 #pragma unroll
@@ -1039,6 +1062,11 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
             uint32_t p[16];
             tmem_ld16_nw(tm_g + lanes + cols + 2 * k, p);
             tmem_wait_ld16(p);
+            if (bound.M > 156) {  // (beyond it, likewise)
+              const float more = two_to(bound.M - 156);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) p[i] = __float_as_uint(__uint_as_float(p[i]) * more);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               S[k + i] = __ffma2_rn(S[k + i], make_float2(w, w),
@@ -1066,8 +1094,8 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
     for (int g = 0; g < share; ++g) {
       const int64_t at = slot * a.s.hv + oh * share + g;
       const float log2a = linear::log2_decay(a.s, oh * share + g);
-      const int ex = top_of(a.x_top, at, -110), ey = top_of(a.y_top, at, -110);
-      const float x_scale = two_to(15 + ey - max(ex + ey, -97));
+      const Tops tops = tops_of(a, at);
+      const float x_scale = two_to(15 + tops.ey - tops.M);
       const float x_whole = linear::power(log2a, REVERSE ? row + 1 : C - row) * x_scale;
       for (int c = 0; c < chunks; ++c, ++it) {
         const int m = tokens(c);
@@ -1075,7 +1103,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
         const uint32_t st = base + (it & 1) * PassSmem::stage;
         wait_bar(bar(kFull, it), half(it), failed);
         const uint32_t most = live ? row_max_of(st + PassSmem::Z, row, A) : 0u;
-        const int ez = most ? exponent_of(most, kLeastRow) : kNoRow;
+        const int ez = most ? max(exponent_of(larger_of_two(most)), kLeastRow) : kNoRow;
         if (it >= 2) wait_bar(bar(kSumsRead, it - 2), half(it - 2), failed);  // (who reads it there)
         targets[C * (it & 1) + row] = ez;
         mbar_arrive(bar(kRows, it));
@@ -1085,7 +1113,7 @@ linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz
                    REVERSE || m == C ? x_whole : live ? linear::power(log2a, m - row) * x_scale : 0.f);
         }
         wait_bar(bar(kFullY, it), half(it), failed);
-        open_row(st + PassSmem::Y, row, B, live, two_to(14 - ey));
+        open_row(st + PassSmem::Y, row, B, live, two_to(14 - tops.ey));
         fence_async_smem();
         mbar_arrive(bar(kValues, it));
       }

@@ -754,7 +754,8 @@ def linear_attention(q, k, v, log_decay, h0=None, cu_seqlens=None, workspace=Non
                      check_status=False, stream=None):
     """out [T, hv, V] and the final states [N, hv, K, V] of h_t = exp(log_decay) h_{t-1} + k_t v_t^T,
     out_t = h_t^T q_t over packed sequences (see include/gdn.h): q, k [T, hk, K] and v [T, hv, V]
-    may be slices of one projection, log_decay [hv] <= 0 belongs to the layer."""
+    may be slices of one projection, log_decay [hv] <= 0 belongs to the layer.  bf16 tensors go through
+    fp16 operands, float32 ones (.float() of them too) are computed in fp32 throughout."""
     if stream is not None:
         return _on(stream, lambda: linear_attention(q, k, v, log_decay, h0, cu_seqlens, workspace,
                                                     check_status),

@@ -386,12 +386,14 @@ size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p);
  * recorded.  The same inputs give the same bits.  A value of a sequence that is not finite makes
  * that sequence's outputs and final state undefined from up to 127 tokens before it on (in the
  * head that reads it), and no other's.
- * Precision: states are carried and h_final is formed to fp32 accuracy.  fp32 I/O is fp32 arithmetic.  bf16
- * I/O runs on the tensor cores: q . k of the inputs as they are; the weighted products, the weighted rows
- * of q and k and the state enter the other products as fp16 (scaled by powers of two, so that no size of
- * the inputs is out of range; 2^-11 of a term each, or 2^-38 of what the largest k and v of its
- * sequence would make a term; rows of q whose product with these passes fp32's range may be NaN), all
- * sums are fp32. */
+ * Precision: states are carried and h_final is formed to fp32 accuracy.  fp32 I/O is fp32 arithmetic
+ * throughout, for bf16 tensors too where they are converted first.  bf16 I/O runs on the tensor cores:
+ * q . k of the inputs as they are; the weighted products, the weighted rows of q and k and the state enter
+ * the other products as fp16, scaled by powers of two, and all sums are fp32.  Each such operand is off
+ * by 2^-11 of itself, or makes a term off by 2^-38 of the row's largest |q| times B, where B is what the
+ * state could be: what its segment of the sequence starts from, decayed, and 128 times the segment's
+ * largest |k| times its largest |v| for every 128 tokens since (|k| and |v| counting as 2^-101 at least,
+ * 4 |k| |v| as 2^-97).  Rows for which |q| B passes fp32's range may be NaN. */
 gdn_status gdn_linear_attention(const gdn_linear_problem* p, const void* q, const void* k,
                                 const void* v, const float* log_decay, const float* h0,
                                 const int32_t* cu_seqlens, void* out, float* h_final,
@@ -417,7 +419,8 @@ size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p,
  *               fp32 and in a fixed order),  dv [T, hv, V] io dtype, contiguous
  *   dh0         [N, hv, K, V] fp32, or NULL to skip; may be dh_final itself
  * The decays are constants of the layer: they get no gradient.  Checks, unwritten rows, workspace,
- * precision and errors as in the forward; dh0 is formed to fp32 accuracy.  A value of a sequence that is
+ * precision and errors as in the forward, with (dout, v, k) for dq, (v, dout, q) for dk and (k, q, dout) for
+ * dv in the place of (q, k, v); dh0 is formed to fp32 accuracy.  A value of a sequence that is
  * not finite makes that sequence's gradients undefined (in the heads that read it), and no other's. */
 gdn_status gdn_linear_attention_backward(const gdn_linear_problem* p, const void* q,
                                          const void* k, const void* v,

@@ -91,6 +91,46 @@ def test_small_rows_against_large_ones(gdn, small, large):
         close(got[i], want[i], size[i], 170, name)
 
 
+@pytest.mark.parametrize("start", ["token", "h0"])
+def test_states_beside_the_largest_keys_and_values(gdn, start):
+    """A state of 2^110 beside a key of 2^70 and a value of 2^70 of different tokens: what would be their
+    product is beyond fp32, but nothing is that is computed.  152 heads, so that the chunks are of one
+    segment; one has values."""
+    T, hv = 400, 152
+    q, k = (torch.zeros(T, 1, 128, device="cuda", dtype=BF16) for _ in range(2))
+    v = torch.zeros(T, hv, 128, device="cuda", dtype=BF16)
+    h0 = torch.zeros(1, hv, 128, 128, device="cuda")
+    if start == "token":
+        k[10, 0, 0], v[10, -1, 0] = 2.0 ** 70, 2.0 ** 40
+    else:
+        k[10, 0, 1], v[10, -1, 1] = 2.0 ** 70, 2.0 ** -40
+        h0[0, -1, 0, 0] = 2.0 ** 110
+    k[11, 0, 2], v[11, -1, 2] = 1.0, 2.0 ** 70
+    q[128:, 0, 0] = 2.0 ** -25
+    out, last = gdn.linear_attention(q, k, v, torch.zeros(hv, device="cuda"), h0, check_status=True)
+    assert last[0, -1, 0, 0] == 2.0 ** 110
+    want = torch.zeros_like(out)
+    want[128:, -1, 0] = 2.0 ** 85
+    # (powers of two: nothing is rounded that is not below what the range allows, 2^79 here)
+    assert ((out.double() - want.double()).abs() <= 2.0 ** 79).all()
+
+
+def test_sums_beside_the_largest_keys_and_values(gdn):
+    """The same where what is beyond the range is the scale of the chunks' growth: a key of 2^78 and a value
+    of 2^77 of different tokens, and products of no more than 2^125."""
+    T, hv = 400, 152
+    q, k = (torch.zeros(T, 1, 128, device="cuda", dtype=BF16) for _ in range(2))
+    v = torch.zeros(T, hv, 128, device="cuda", dtype=BF16)
+    k[10, 0, 0], v[10, -1, 0] = 2.0 ** 78, 2.0 ** 47
+    k[11, 0, 2], v[11, -1, 2] = 2.0 ** -20, 2.0 ** 77
+    q[128:, 0, 0] = 2.0 ** -40
+    out, last = gdn.linear_attention(q, k, v, torch.zeros(hv, device="cuda"), check_status=True)
+    assert last[0, -1, 0, 0] == 2.0 ** 125
+    want = torch.zeros_like(out)
+    want[128:, -1, 0] = 2.0 ** 85
+    assert ((out.double() - want.double()).abs() <= 2.0 ** 79).all()
+
+
 def test_a_state_that_forgets_its_start(gdn):
     """A start of 2^100, and keys times values of 2^-27: by the time that the start has decayed below them,
     the state is what thousands of tokens have gathered, and its bound has to be too.  Every element is
