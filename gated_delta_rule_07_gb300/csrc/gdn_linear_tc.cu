@@ -100,9 +100,8 @@ __device__ __forceinline__ int exponent_of(int bits) { return (bits >> 23) - 126
 // are split into three bf16 parts (24 bits), x is bf16 as it stands, products and their sums are exact
 // or fp32.  64 tokens at a time go through the tensor core into Tensor Memory and from there into a
 // register-held U, decayed on the way: the weights stay within a tile, and the tensor core's own sums,
-// whose roundings do not average out, stay short.  Where what a segment gathers has decayed by 2^-13 at
-// the end of its sequence, two parts do: 2^-17 of it there is 2^-30, and beside the fp16 copy that the
-// pass makes of the state (2^-11) nothing.
+// whose roundings do not average out, stay short.  (However far the share has decayed at the end of its
+// sequence: what is behind it may be zeros, and then it is all that there is.)
 //
 // HBM takes 1340 cycles for a tile of an SM's share, so little may go through shared memory beside the
 // tiles themselves (256 of its cycles): y comes out of it transposed (ldmatrix) and the parts go straight to
@@ -183,9 +182,6 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
   auto first_token = [&](int i) { return begin + (a.reverse ? tiles - 1 - i : i) * kTile; };
   auto tokens = [&](int i) { return min(begin + length - first_token(i), kTile); };
   const float log2a = linear::log2_decay(a.s, head);
-  // tokens between the segment and where the walk of its sequence ends
-  const int64_t left = a.reverse ? t0 - (a.s.cu ? a.s.cu[n] : 0) : (a.s.cu ? a.s.cu[n + 1] : a.s.T) - t1;
-  const bool three = log2a * (float)left > -13.f;
 
   if (warp >= kLoad) {  // (the last warpgroup; the rest of its warps have nothing to do)
     leave_registers<56>();
@@ -229,14 +225,11 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
         const uint64_t x = at + ((st * StateSmem::stage + StateSmem::X) >> 4);
         const uint32_t d = tm + 128 * (i & 1), parts = tm_parts + 96 * (i & 1);
         if (elected()) {
-          if (three) {
 #pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)  // (the small parts first)
-              mma_ts(d, parts + 64 + 8 * ks, x + ks * 128, id, ks > 0);
-          }
+          for (int ks = 0; ks < kTile / 16; ++ks)  // (the small parts first)
+            mma_ts(d, parts + 64 + 8 * ks, x + ks * 128, id, ks > 0);
 #pragma unroll
-          for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_ts(d, parts + 32 + 8 * ks, x + ks * 128, id, three || ks > 0);
+          for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(d, parts + 32 + 8 * ks, x + ks * 128, id, 1);
 #pragma unroll
           for (int ks = 0; ks < kTile / 16; ++ks) mma_ts(d, parts + 8 * ks, x + ks * 128, id, 1);
           mma_commit(done + 8 * (i & 1));
@@ -317,14 +310,12 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
         const uint32_t to = ((uint32_t)(32 * quarter + 16 * g) << 16) + tm_parts + 96 * (i & 1) + token0 / 2;
         tmem_st_blocks(to, v);
         tmem_st_blocks(to + 32, mid);
-        if (three) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            f[j] = __ffma2_rn(make_float2(low(mid[j]), high(mid[j])), minus, f[j]);
-            mid[j] = pack_bf2(f[j].x, f[j].y);
-          }
-          tmem_st_blocks(to + 64, mid);
+        for (int j = 0; j < 4; ++j) {
+          f[j] = __ffma2_rn(make_float2(low(mid[j]), high(mid[j])), minus, f[j]);
+          mid[j] = pack_bf2(f[j].x, f[j].y);
         }
+        tmem_st_blocks(to + 64, mid);
       }
 #pragma unroll
       for (int b = 0; b < 2; ++b) {

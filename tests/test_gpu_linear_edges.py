@@ -149,3 +149,31 @@ def test_a_state_that_forgets_its_start(gdn):
     off = (out[:, [0, 76, 151]].double() / want[:, None, None] - 1).abs().amax((1, 2))
     # (a bf16 rounding, three fp16 ones, and the powers: t log2(a) of up to 130 is off by 2^-24 of it, twice)
     assert off.max() <= 2.0 ** -8 + 3 * 2.0 ** -11 + 130 * 2.0 ** -23
+
+
+# ------------------------------------------------------------------------------- states to the last bit
+
+@pytest.mark.parametrize("where", ["h_final", "dh0"])
+def test_states_keep_every_bit_of_their_terms(gdn, where):
+    """Each element of the state is one product, of a token whose key is one feature, and the tokens
+    behind it (before it, for dh0) have none, however far the state decays on its way.  Whatever its
+    weight is, all elements of a row share it, so their ratios to v (dout) agree to the roundings of one
+    weighting, a decay a tile of 64 tokens, and a decay a segment: 12 of 2^-24 at most, each way, with
+    the row's own scale.  (A part of the weighted rows left out is up to 2^-18.)"""
+    gen = torch.Generator().manual_seed(1)
+    T, hv = 384, 4
+    g = torch.tensor([-0.01, -0.07, -0.1, -0.13], device="cuda")   # 2^-3 to 2^-48 over 256 tokens
+    one, x = torch.zeros(T, 1, 128, device="cuda", dtype=BF16), rand(gen, T, hv, 128)
+    rows = slice(0, 128) if where == "h_final" else slice(256, 384)
+    one[rows, 0] = torch.eye(128, device="cuda", dtype=BF16)
+    x[x == 0] = 1.0
+    if where == "h_final":
+        got = gdn.linear_attention(one, one, x, g, check_status=True)[1][0]
+        steps = 383.0 - torch.arange(128, device="cuda", dtype=torch.float64)
+    else:
+        got = gdn.linear_attention_backward(one, one, x, g, x, check_status=True)[3][0]
+        steps = 257.0 + torch.arange(128, device="cuda", dtype=torch.float64)
+    ratio = got.double() / x[rows].double().transpose(0, 1)              # [hv, K, V]
+    want = torch.exp(g.double()[:, None] * steps)
+    assert ((ratio.mean(-1) / want - 1).abs() <= 60 * 2.0 ** -22).all()  # (the powers' own error)
+    assert ((ratio / ratio.mean(-1, keepdim=True) - 1).abs() <= 24 * 2.0 ** -24).all()
