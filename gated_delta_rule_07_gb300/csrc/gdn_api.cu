@@ -860,10 +860,12 @@ bool linear_on_tc(const gdn_linear_problem* p) {
 
 // A segment's tokens, in whole chunks.  An SM holds one segment of one output head at a time (in the
 // tensor cores' backward pass of shared heads, of all the value heads that it sums), so what counts is how
-// many rounds of the 152 SMs there are and how long one takes: its tokens and some more for its start and
-// end, 640 on the tensor cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
+// many rounds of the part's SMs there are (a constant: a workspace's size is asked for on the host, without
+// a device) and how long one takes: its tokens and some more for its start and end, 640 on the tensor
+// cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
 // 609 us; 9, two rounds of 144, 552; 16, 634; 19, four rounds of 152, 557; 32, 620.)  Only the sum of the
 // sequences' lengths is known here: they are taken as alike, give or take a seventh.
+constexpr int kSms = 152;
 int linear_segment(const gdn_linear_problem* p, bool backward) {
   const int64_t T = p->total_tokens, N = p->num_seqs, hv = p->hv;
   const bool tc = linear_on_tc(p);
@@ -873,7 +875,7 @@ int linear_segment(const gdn_linear_problem* p, bool backward) {
   int64_t best = 0, least = INT64_MAX;
   for (int64_t k = 1; k <= 128 && (k == 1 || each > (k - 1) * chunk); ++k) {
     const int64_t length = ((each + k - 1) / k + chunk - 1) / chunk * chunk;
-    const int64_t rounds = (N * k * heads + 151) / 152, cost = rounds * share * (length + more);
+    const int64_t rounds = (N * k * heads + kSms - 1) / kSms, cost = rounds * share * (length + more);
     if (cost < least) {
       least = cost;
       best = length;

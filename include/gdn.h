@@ -364,7 +364,9 @@ typedef struct gdn_linear_problem {
 gdn_status gdn_check_linear_problem(const gdn_linear_problem* p);
 
 /* Bytes of device workspace gdn_linear_attention needs for problem p (0 when p is invalid): one
- * K x V fp32 state for each value head of each segment of the sequences. */
+ * K x V fp32 state for each value head of each segment of the sequences.  How many segments are best goes by
+ * the tokens, sequences, heads, type and strides, so a size is that problem's alone: one with fewer tokens
+ * may need more.  A workspace kept for several problems has the largest of their sizes. */
 size_t gdn_linear_attention_workspace_size(const gdn_linear_problem* p);
 
 /* Linear attention over packed sequences.  Per value head j (key head j / (hv / hk)), with
@@ -407,8 +409,8 @@ typedef struct gdn_linear_saved {
     int32_t format;           /* gdn_kv_format of all three                                  */
 } gdn_linear_saved;
 
-/* Bytes of device workspace gdn_linear_attention_backward needs (0 when p is invalid); `saved`
- * != 0 for a call that is given 8-bit activations. */
+/* Bytes of device workspace gdn_linear_attention_backward needs (0 when p is invalid), for this problem
+ * alone as above; `saved` != 0 for a call that is given 8-bit activations. */
 size_t gdn_linear_attention_backward_workspace_size(const gdn_linear_problem* p, int saved);
 
 /* Gradients of <dout, out> + <dh_final, h_final> through gdn_linear_attention on the same inputs.

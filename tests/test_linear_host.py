@@ -182,3 +182,19 @@ def test_fp64_form_is_the_recurrence():
             h = torch.exp(g[0]) * h + torch.outer(k[t, 0], v[t, 0])
             assert torch.allclose(out[t, 0], h.T @ q[t, 0], atol=1e-13, rtol=0)
         assert torch.allclose(last[0, 0], h, atol=1e-13, rtol=0)
+
+
+@pytest.mark.parametrize("saved", [False, True])
+def test_a_workspace_size_is_one_problems(gdn, saved):
+    """Over lengths at which the number of segments goes up and down: a call wants the size that it was
+    asked for, and one byte less is refused."""
+    held = gdn.LinearSaved(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0) if saved else None
+    rows = dict(q=None, k=None, v=None) if saved else {}
+    for tokens in (1, 127, 129, 1000, 4991, 4992, 4993, 20000, 70001):
+        for kw in (dict(), dict(num_seqs=3), dict(q_head_stride=0), dict(io_dtype=1)):
+            p = problem(gdn, total_tokens=tokens, **kw)
+            cu = FAKE if p.num_seqs > 1 else None
+            need = gdn.gdn_linear_attention_workspace_size(p)
+            assert need >= p.num_seqs * 4 * 128 * 128 * 4 and forward(gdn, p, ws=need - 1, cu=cu) == 3
+            need = gdn.gdn_linear_attention_backward_workspace_size(p, saved)
+            assert backward(gdn, p, ws=need - 1, saved=held, cu=cu, **rows) == 3
