@@ -963,7 +963,8 @@ gdn_status checkpoint_args(const gdn_checkpoint* t, int count, int format,
     if (!strides_ok(c.token_stride, c.total_tokens, c.head_stride, c.heads, c.io_dtype))
       return GDN_ERR_INVALID_ARGUMENT;
     if (c.total_tokens > 0 && (!c.x || !c.codes || !c.scale)) return GDN_ERR_INVALID_ARGUMENT;
-    if (!aligned16(c.x) || !aligned16(c.codes) || !aligned16(c.scale))
+    // (a scale is read by itself: those of a part of the tokens may start at any of them)
+    if (!aligned16(c.x) || !aligned16(c.codes) || reinterpret_cast<uintptr_t>(c.scale) % sizeof(float))
       return GDN_ERR_INVALID_ARGUMENT;
     a.t[i] = {c.x, static_cast<uint8_t*>(c.codes), c.scale, c.total_tokens * c.heads,
               stride_of(c.token_stride, c.total_tokens), stride_of(c.head_stride, c.heads),

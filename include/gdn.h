@@ -448,7 +448,8 @@ gdn_status gdn_linear_attention_decode(const gdn_linear_problem* p, int32_t slot
                                        int32_t* dev_status, cudaStream_t stream);
 
 /* A tensor of a checkpoint call: rows x [T, heads, D] of io dtype, strided; codes [T, heads, D] one
- * byte each and scale [T, heads] fp32, contiguous. */
+ * byte each and scale [T, heads] fp32, contiguous.  x and codes are 16-byte aligned; codes and scales of
+ * a part of the tokens are a checkpoint too. */
 typedef struct gdn_checkpoint {
     void* x;
     void* codes;

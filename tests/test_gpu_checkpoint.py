@@ -165,3 +165,20 @@ def test_refusals(gdn):
             gdn.Checkpoint(codes, scale)
     with pytest.raises(gdn.GdnError):
         gdn.checkpoint_open(c, e)
+
+
+@pytest.mark.parametrize("dtype", FORMATS)
+def test_a_part_of_the_tokens(gdn, dtype):
+    """Codes and scales of some tokens are a checkpoint of these, wherever they start."""
+    gen = torch.Generator().manual_seed(9)
+    q, k, v, do = (torch.randn(200, 3, 128, generator=gen).to(BF16).cuda() for _ in range(4))
+    g = -torch.rand(3, generator=gen).cuda()
+    held = gdn.checkpoint_pack(q, k, v, dtype=dtype)
+    for b, e in ((1, 200), (50, 133), (199, 200)):
+        part = [gdn.Checkpoint(c.codes[b:e], c.scale[b:e], c.dtype) for c in held]
+        opened = gdn.checkpoint_open(*part)
+        for x, y in zip(opened, gdn.checkpoint_open(*held)):
+            assert torch.equal(x, y[b:e])
+        got = gdn.linear_attention_backward(*part, g, do[b:e].contiguous(), check_status=True)
+        want = gdn.linear_attention_backward(*opened, g, do[b:e].contiguous())
+        assert all(torch.equal(x, y) for x, y in zip(got, want))

@@ -198,3 +198,11 @@ def test_a_workspace_size_is_one_problems(gdn, saved):
             assert need >= p.num_seqs * 4 * 128 * 128 * 4 and forward(gdn, p, ws=need - 1, cu=cu) == 3
             need = gdn.gdn_linear_attention_backward_workspace_size(p, saved)
             assert backward(gdn, p, ws=need - 1, saved=held, cu=cu, **rows) == 3
+
+
+def test_checkpoint_scales_are_aligned_as_floats(gdn):
+    c = gdn.CheckpointDesc(x=FAKE, codes=FAKE, scale=FAKE + 2, total_tokens=5, token_stride=256,
+                           head_stride=128, heads=2, head_dim=128, io_dtype=0)
+    one = (gdn.CheckpointDesc * 1)(c)
+    assert gdn._lib.gdn_checkpoint_pack(one, 1, 0, None, None) == 1
+    assert gdn._lib.gdn_checkpoint_open(one, 1, 0, None) == 1
