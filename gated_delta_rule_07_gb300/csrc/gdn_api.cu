@@ -863,7 +863,7 @@ bool linear_on_tc(const gdn_linear_problem* p) {
 // many rounds of the part's SMs there are (a constant: a workspace's size is asked for on the host, without
 // a device) and how long one takes: its tokens and some more for its start and end, 640 on the tensor
 // cores, 96 on the CUDA cores.  (bf16, 65536 tokens of 32 heads: 4 segments, one round of 128 SMs,
-// 609 us; 9, two rounds of 144, 552; 16, 634; 19, four rounds of 152, 557; 32, 620.)  Only the sum of the
+// 599 us; 9, two rounds of 144, 552; 16, 638; 19, four rounds of 152, 562; 32, 625.)  Only the sum of the
 // sequences' lengths is known here: they are taken as alike, give or take a seventh.
 constexpr int kSms = 152;
 int linear_segment(const gdn_linear_problem* p, bool backward) {

@@ -106,11 +106,12 @@ __device__ __forceinline__ int exponent_of(int bits) { return (bits >> 23) - 126
 // HBM takes 1340 cycles for a tile of an SM's share, so little may go through shared memory beside the
 // tiles themselves (256 of its cycles): y comes out of it transposed (ldmatrix) and the parts go straight to
 // Tensor Memory, as the operand whose rows are y's columns; the tensor core reads x alone from shared memory.
-// So it makes U^T.  (65536 tokens of 32 heads: 192 us, of HBM's 119, with 69% of the issue slots used, by
-// the splitting above all; with parts written back to shared memory 270, whatever the number of warps.)  Five tiles are on their way or at work; splitting (sixteen warps), the products and the
-// sums (eight warps, for Tensor Memory's lanes and their registers) each on another.  896 threads launch
-// with 72 registers, 504 for the seven warpgroups' warps of an SM's quarter: the sums' two take 96,
-// splitting's four keep 64, the last 56.
+// So it makes U^T.  (65536 tokens of 32 heads: 198 us, of HBM's 119, with 69% of the issue slots used, by
+// the splitting above all; with parts written back to shared memory 270, whatever the number of warps.)
+// Five tiles are on their way or at work; splitting (sixteen warps), the products and the sums (eight
+// warps, for Tensor Memory's lanes and their registers) each on another.  896 threads launch with 72
+// registers, 504 for the seven warpgroups' warps of an SM's quarter: the sums' two take 96, splitting's
+// four keep 64, the last 56.
 constexpr int kTile = 64, kSplit = 512, kAdd = 256, kStateThreads = kSplit + kAdd + 128, kStages = 5;
 static_assert(kSplit % 128 == 0 && kAdd % 128 == 0, "roles that set registers are whole warpgroups");
 constexpr uint32_t kRaw = kTile * D * 2;          // bytes of a tile of one tensor
@@ -338,8 +339,8 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
       }
     }
     // An infinity does not reach the outputs of the chunks before its own, so it is not to scale their rows:
-    // a warp that has met one looks at its rows once more, without it.  (Left out tile by tile: 196 us
-    // for 65536 tokens of 32 heads, not 192.)
+    // a warp that has met one looks at its rows once more, without it.  (Left out tile by tile it took
+    // 2% more: 196 us for 65536 tokens of 32 heads, 192 so.)
     if (__any_sync(0xffffffffu, finite(x_max) != x_max || finite(y_max) != y_max)) {
       const __nv_bfloat16* const xp = static_cast<const __nv_bfloat16*>(a.x.p) +
                                       (int64_t)(head / a.x.share) * a.x.hs + 8 * (tid % 8);
@@ -429,11 +430,12 @@ linear_state_tc_kernel(const LinearState a, const __grid_constant__ CUtensorMap 
 //     y~ = y 2^(14 - e_y)     x~ = a^{n - j} x 2^(15 + e_y - M)     S~ = S 2^(15 - E)
 //     z~ = p_i z 2^(14 - e_z)   W~ = W 2^(15 + e_y - e_z - E)         O = O~ 2^(e_z + E - 29)
 // so that nothing can overflow that does not in fp32, and each rounding is half a step of fp16 (2^-11) of
-// a term, or 2^-38 of what bounds the sum.
+// a term, or 2^-38 of what bounds the sum.  (E comes from bounds, not from S: every role has to know it, and
+// none is to wait for S.)
 //
 // What bounds it is shared memory and the hand-offs between its roles: a chunk takes 6000 cycles (65536
-// tokens of 32 heads: 349 us), where HBM takes 4300 (238 us).  Its threads read and write shared
-// memory in 3250 of them, its tiles arrive in 768 (128 bytes a cycle) and go to the tensor cores in 1536.
+// tokens of 32 heads: 345 us), where HBM takes 4300 (238 us).  Its threads read and write shared
+// memory in 3150 of them, its tiles arrive in 768 (128 bytes a cycle) and go to the tensor cores in 1536.
 // So z's rows go to the tensor core through Tensor Memory, the outputs leave by TMA from y's tile, and a
 // sum over value heads is kept in an order of rows that its threads read together.
 constexpr int C = 128;
@@ -555,7 +557,8 @@ __device__ __forceinline__ void tma_out(const CUtensorMap* map, uint32_t src, in
 }
 
 // REVERSE: the walk goes backward in time.  SUM: an output head has several value heads.
-// WIDE: A = B = 128 (9% faster where that is known: a call of 65536 tokens 554 us, 604).
+// WIDE: A = B = 128 (faster where that is known: a call of 65536 tokens 552 us, 585 otherwise; gradients of
+// 16384 502 and 558).
 template <bool REVERSE, bool SUM, bool WIDE>
 __global__ void __launch_bounds__(kPassThreads, 1)
 linear_pass_tc_kernel(const LinearPass a, const __grid_constant__ CUtensorMap mz,
