@@ -177,3 +177,27 @@ def test_states_keep_every_bit_of_their_terms(gdn, where):
     want = torch.exp(g.double()[:, None] * steps)
     assert ((ratio.mean(-1) / want - 1).abs() <= 60 * 2.0 ** -22).all()  # (the powers' own error)
     assert ((ratio / ratio.mean(-1, keepdim=True) - 1).abs() <= 24 * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** 60])
+@pytest.mark.parametrize("hk,hv", [(2, 2), (1, 3)])
+def test_rows_of_zeros(gdn, hk, hv, size):
+    """Masked tokens: their rows of q, or of dout, are zeros, and so are their outputs and their dq; the
+    tokens beside them are as they are, whatever the keys and values are."""
+    gen = torch.Generator().manual_seed(4)
+    T, lens, cu = 330, [200, 130], lt.cumulative([200, 130])
+    q, k, v, do = (rand(gen, T, h, 128) for h in (hk, hk, hv, hv))
+    masked = torch.rand(T, generator=gen).cuda() < 0.5
+    masked[:40] = True
+    q[masked], do[masked] = 0.0, 0.0
+    g = -torch.rand(hv, generator=gen).cuda() * 0.1
+    args = q / size, k * size, v * size, g, None
+    out, _ = gdn.linear_attention(*args, cu, check_status=True)
+    assert (out[masked] == 0).all()
+    close(out, lt.forward(*args, lens)[0], lt.magnitudes(lt.forward, *args, lens)[0], 200, "out")
+    args = q, k * size, v * size, g, do / size, None, None
+    got = gdn.linear_attention_backward(*args, cu, check_status=True)
+    want, sizes = lt.backward(*args, lens), lt.magnitudes(lt.backward, *args, lens)
+    assert (got[0][masked] == 0).all()
+    for i, name in enumerate(("dq", "dk", "dv")):
+        close(got[i], want[i], sizes[i], 200, name)
